@@ -1,6 +1,9 @@
 /*
  * mm.h -- C ABI of the GB300 (sm_103a) library for the ONNX matrix-product
- * operator family: MatMul, Gemm, QLinearMatMul and GroupedMatMul.
+ * operator family (MatMul, Gemm, QLinearMatMul and GroupedMatMul) and for the
+ * language-model operators whose products select their weights per row:
+ * top-k routing, the mixture-of-experts layer for a few tokens, and per-row
+ * low-rank adapters beside a shared projection.
  *
  * Every entry point takes plain pointers and sizes; no C++ or framework type
  * crosses this boundary.  All computation runs in this library's own CUDA
@@ -30,7 +33,8 @@
  *   complete (and its memory to be visible) before its first global-memory
  *   access, so stream order is kept for any work before or after a call.
  * Memory.  The library never allocates device memory.  Operators whose fast
- *   path needs scratch space (QLinearMatMul, GroupedMatMul) take a
+ *   path needs scratch space (QLinearMatMul, GroupedMatMul, the
+ *   mixture-of-experts layer and the low-rank adapters) take a
  *   caller-provided workspace whose size is given by the matching
  *   *_workspace_size function; the workspace must be 256-byte aligned.
  * Threads.  Entry points may be called from several host threads; calls that
@@ -57,7 +61,7 @@ typedef enum mm_status {
   MM_ERR_WORKSPACE = 5,    /* workspace NULL, too small or not 256-byte aligned */
   MM_ERR_CUDA = 6,         /* a CUDA runtime call or kernel launch failed */
   MM_ERR_TIMEOUT = 7,      /* device side: a pipeline wait exceeded its limit and the kernel gave up */
-  MM_ERR_INDEX_RANGE = 8   /* device side: a GroupedMatMul index outside [0, G) was seen */
+  MM_ERR_INDEX_RANGE = 8   /* device side: a group, expert or adapter index out of its range was seen */
 } mm_status;
 
 typedef enum mm_dtype {
@@ -278,6 +282,96 @@ size_t mm_grouped_matmul_noalloc_max_scratch(void);
 mm_status mm_grouped_matmul_noalloc(const mm_tensor* input, const mm_tensor* weights,
                                     const mm_tensor* group_indices, const mm_tensor* bias /* NULL = absent */,
                                     const mm_tensor* output, void* stream);
+
+/* ---------------------------------------------------------------- top-k routing
+ * The router of a mixture of experts: picks k experts per row of logits [T,G]
+ * (bf16, f16 or f32, any strides) and their weights.  With p = softmax of the
+ * row (fp32, the maximum subtracted), the picks are the k largest logits in
+ * decreasing order, ties to the lowest index; a pick's weight is its p
+ * (normalize == 0) or its p over the sum of the row's picked p (normalize !=
+ * 0).  A logit of -inf or NaN is an expert that cannot be picked and takes no
+ * part in the softmax; a row with fewer than k others gets index -1 and
+ * weight 0 in the remaining places.  A maximum of +inf takes the limit: the
+ * +inf logits share the row equally.
+ *   indices: dense [T,k] MM_I32 (as mm_grouped_matmul and mm_moe_layer take
+ *   them); weights: dense [T,k] MM_F32.  1 <= k <= min(G, 32) (else
+ *   MM_ERR_SHAPE) and G <= 1024 (else MM_ERR_UNSUPPORTED). */
+mm_status mm_route_topk(const mm_tensor* logits, int32_t normalize, const mm_tensor* indices,
+                        const mm_tensor* weights, void* stream);
+/* The gradient of mm_route_topk's weights with respect to the logits, which
+ * are given again (the weights are recomputed, not stored): indices [T,k]
+ * (MM_I32 or MM_I64, distinct within a row) and the weights' gradient
+ * grad_weights [T,k] (MM_F32) give, dense and in the logits' type,
+ *   normalize == 0: dl_i = p_i ([i picked] dw_i - sum_j p_j dw_j) over the picks j,
+ *   normalize != 0: dl_i = w_i (dw_i - sum_j w_j dw_j) on the picks, 0 elsewhere.
+ * An index of -1 is no pick; any other index outside [0,G) is treated as -1
+ * and recorded as MM_ERR_INDEX_RANGE. */
+mm_status mm_route_topk_grad(const mm_tensor* logits, const mm_tensor* indices, const mm_tensor* grad_weights,
+                             int32_t normalize, const mm_tensor* grad_logits, void* stream);
+
+/* ---------------------------------------------------------------- mixture-of-experts layer, few tokens
+ * The whole expert layer for the tokens of a decode step:
+ *   h[t,s,:] = act(x[t,:] @ w_gate[e]) * (x[t,:] @ w_up[e]),  e = expert_indices[t,s],
+ *   out[t,:] = sum_s expert_weights[t,s] * (h[t,s,:] @ w_down[e]).
+ * x [T,K], w_gate and w_up [G,K,F], w_down [G,F,N], out dense [T,N], all of
+ * type bf16, f16 or f32; w_up NULL leaves the second factor out (an ungated
+ * layer).  expert_indices [T,S] MM_I32 or MM_I64; expert_weights [T,S] MM_F32
+ * (NULL = 1).  activation is an mm_activation.  Inputs take any strides, so
+ * w_gate and w_up may be the two halves of one tensor.
+ * Every sum is fp32.  On the tensor cores (bf16/f16 operands whose rows are
+ * 16-byte aligned along a unit-stride matrix dimension) h is rounded once to
+ * T between the two products; the CUDA-core form keeps it fp32.  out is
+ * rounded once to T.
+ * An index of -1 is no pick (mm_route_topk writes it); a token without any
+ * pick gets zeros.  Any other index outside [0,G) counts as -1 and is
+ * recorded as MM_ERR_INDEX_RANGE.  A token's result depends on its own picks
+ * alone, whatever the other tokens or the unpicked experts hold.
+ * The layer reads each picked expert's weights once per 128 tokens: it is
+ * meant for few tokens; for many, mm_grouped_matmul is the better product.
+ * Workspace: mm_moe_layer_workspace_size() bytes. */
+typedef enum mm_activation {
+  MM_ACT_SILU = 0,   /* g / (1 + exp(-g)) */
+  MM_ACT_GELU = 1,   /* g/2 (1 + erf(g / sqrt 2)) */
+  MM_ACT_RELU = 2    /* max(g, 0) */
+} mm_activation;
+mm_status mm_moe_layer_workspace_size(const mm_tensor* x, const mm_tensor* w_gate, const mm_tensor* w_up,
+                                      const mm_tensor* w_down, const mm_tensor* expert_indices, size_t* bytes);
+mm_status mm_moe_layer(const mm_tensor* x, const mm_tensor* w_gate, const mm_tensor* w_up /* NULL = none */,
+                       const mm_tensor* w_down, const mm_tensor* expert_indices,
+                       const mm_tensor* expert_weights /* NULL = 1 */, int32_t activation, const mm_tensor* out,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- per-row low-rank adapters
+ * A shared projection with one low-rank adapter per row (the rows of many
+ * requests, each with its own adapter or none, in one call):
+ *   Y[m,:] = X[m,:] @ W + scales[g] * ((X[m,:] @ A[g]) @ B[g]),  g = adapter_indices[m].
+ * X [M,K], W [K,N], A [G,K,R], B [G,R,N], Y dense [M,N], all of type bf16, f16
+ * or f32; adapter_indices [M] MM_I32 or MM_I64; scales [G] MM_F32 (NULL = 1).
+ * Inputs take any strides (W, A and B may be transposed views).  An index of
+ * -1 is a row without adapter; any other index outside [0,G) counts as -1 and
+ * is recorded as MM_ERR_INDEX_RANGE.
+ * Every sum is fp32; Y is rounded to T.  On some paths the low-rank factor
+ * X A, or the low-rank part of Y, is rounded to T once before it is used.
+ * Workspace: mm_lowrank_matmul_workspace_size() bytes. */
+mm_status mm_lowrank_matmul_workspace_size(const mm_tensor* X, const mm_tensor* W, const mm_tensor* A,
+                                           const mm_tensor* B, size_t* bytes);
+mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_tensor* A, const mm_tensor* B,
+                            const mm_tensor* adapter_indices, const mm_tensor* scales /* NULL = 1 */,
+                            const mm_tensor* Y, void* workspace, size_t workspace_bytes, void* stream);
+/* The gradients of mm_lowrank_matmul for a frozen W, given dY [M,N]: with
+ * U[m] = scales[g] X[m] @ A[g] and V[m] = scales[g] dY[m] @ B[g]^T,
+ *   dX[m]  = dY[m] @ W^T + V[m] @ A[g]^T                       dense [M,K]
+ *   dA[g]  = sum over the rows m of adapter g of X[m]^T V[m]    dense [G,K,R]
+ *   dB[g]  = sum over the rows m of adapter g of U[m]^T dY[m]   dense [G,R,N]
+ * An adapter without rows gets zeros.  Each output may be NULL (not wanted).
+ * Results do not depend on the order of execution.
+ * Workspace: mm_lowrank_matmul_grad_workspace_size() bytes. */
+mm_status mm_lowrank_matmul_grad_workspace_size(const mm_tensor* X, const mm_tensor* W, const mm_tensor* A,
+                                                const mm_tensor* B, size_t* bytes);
+mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const mm_tensor* W, const mm_tensor* A,
+                                 const mm_tensor* B, const mm_tensor* adapter_indices,
+                                 const mm_tensor* scales /* NULL = 1 */, const mm_tensor* dX, const mm_tensor* dA,
+                                 const mm_tensor* dB, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- memory-stream measurement
  * Not an operator (the pages have no counterpart): the streaming kernels that

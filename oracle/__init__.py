@@ -24,6 +24,8 @@ Each module cites the page and section it follows:
 * ``grouped_matmul``  -- GroupedMatMul - 29 (onnx.ai)
 * ``dequantize_linear`` -- GroupedMatMul - 29, Summary: weight-only quantized
   experts (DequantizeLinear of the weights, then GroupedMatMul)
+* ``select``          -- top-k routing, the mixture-of-experts layer and per-row
+  low-rank adapters, with gradients (formulas in ``include/mm.h``)
 
 A second, independent oracle restates the same pages as plain C++ loops
 (``csrc/oracle.cpp``: double accumulation in k order without fused
@@ -32,11 +34,12 @@ multiply-adds, exact integers, the same float32 requantisation), bound by
 baseline times and what the full-size GPU parity tests use.  The two share no
 code.
 
-Parity status: every function of both oracles is pinned by tests in
+Parity status: every function of both oracles that follows a page is pinned by tests in
 ``tests/test_oracle_pins.py`` (printed worked examples, brute force on tiny
 inputs, closed forms, identities and hand-computed error-bound denominators),
 and ``tests/test_oracle_native.py`` checks that the two agree on random
-inputs; none is "parity unpinned".
+inputs; none is "parity unpinned".  ``select`` is pinned by hand values and
+differences in ``tests/test_oracle_select.py``.
 """
 
 from .matmul import matmul, matmul_output_shape, matmul_abs_scale

@@ -23,6 +23,9 @@ __all__ = [
     "mm_grouped_matmul_qweights", "mm_grouped_matmul_qweights_workspace_size",
     "MM_PATH_AUTO", "MM_PATH_SIMT", "MM_PATH_TENSOR", "MM_PATH_NONE", "MM_PATH_VECTOR", "mm_stream_probe",
     "mm_alu_probe", "MM_ALU_CHAINS",
+    "mm_route_topk", "mm_route_topk_grad", "mm_moe_layer", "mm_moe_layer_workspace_size",
+    "mm_lowrank_matmul", "mm_lowrank_matmul_workspace_size", "mm_lowrank_matmul_grad",
+    "mm_lowrank_matmul_grad_workspace_size",
 ]
 
 MM_MAX_DIMS = 8
@@ -90,6 +93,14 @@ def _lib():
             "mm_grouped_matmul_qweights": ([T, T, T, T, I64, T, T, T, P, SZ, P], I32),
             "mm_stream_probe": ([P, P, SZ, I32, P], I32),
             "mm_alu_probe": ([I32, P, I64, P, P], I32),
+            "mm_route_topk": ([T, I32, T, T, P], I32),
+            "mm_route_topk_grad": ([T, T, T, I32, T, P], I32),
+            "mm_moe_layer_workspace_size": ([T, T, T, T, T, ctypes.POINTER(SZ)], I32),
+            "mm_moe_layer": ([T, T, T, T, T, T, I32, T, P, SZ, P], I32),
+            "mm_lowrank_matmul_workspace_size": ([T, T, T, T, ctypes.POINTER(SZ)], I32),
+            "mm_lowrank_matmul": ([T, T, T, T, T, T, T, P, SZ, P], I32),
+            "mm_lowrank_matmul_grad_workspace_size": ([T, T, T, T, ctypes.POINTER(SZ)], I32),
+            "mm_lowrank_matmul_grad": ([T, T, T, T, T, T, T, T, T, T, P, SZ, P], I32),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(lib, name)
@@ -345,6 +356,101 @@ def mm_grouped_matmul_noalloc(input, weights, group_indices, bias=None, out=None
                                             _ref(_desc(bias)), _ref(_desc(y)), _stream(input, stream)),
            "mm_grouped_matmul_noalloc")
     return y
+
+
+def mm_route_topk(logits, k, normalize=1, indices=None, weights=None, stream=None):
+    """Top-k routing of logits [T, G]: (indices int32 [T, k], weights fp32 [T, k]), the largest logits first, ties to
+    the lowest index; weights are the softmax over all experts, divided by the picks' sum when ``normalize``."""
+    shape = (logits.shape[0], int(k))
+    idx = torch.empty(shape, dtype=torch.int32, device=logits.device) if indices is None else indices
+    w = torch.empty(shape, dtype=torch.float32, device=logits.device) if weights is None else weights
+    _check(_lib().mm_route_topk(_ref(_desc(logits)), int(normalize), _ref(_desc(idx)), _ref(_desc(w)),
+                                _stream(logits, stream)), "mm_route_topk")
+    return idx, w
+
+
+def mm_route_topk_grad(logits, indices, grad_weights, normalize=1, out=None, stream=None):
+    """Gradient of mm_route_topk's weights with respect to the logits (in the logits' type)."""
+    y = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if out is None else out
+    _check(_lib().mm_route_topk_grad(_ref(_desc(logits)), _ref(_desc(indices)), _ref(_desc(grad_weights)),
+                                     int(normalize), _ref(_desc(y)), _stream(logits, stream)), "mm_route_topk_grad")
+    return y
+
+
+_ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
+
+
+def _sized(fn, *descs):
+    nbytes = ctypes.c_size_t()
+    _check(fn(*[_ref(d) for d in descs], ctypes.byref(nbytes)), fn.__name__)
+    return nbytes.value
+
+
+def _given_or_sized(workspace, device, fn, *descs):
+    """(tensor, size) of the workspace: the caller's (the library checks its size), or one of the size ``fn`` names."""
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    return _workspace(_sized(fn, *descs), device)
+
+
+def mm_moe_layer_workspace_size(x, w_gate, w_up, w_down, expert_indices):
+    return _sized(_lib().mm_moe_layer_workspace_size, _desc(x), _desc(w_gate), _desc(w_up), _desc(w_down),
+                  _desc(expert_indices))
+
+
+def mm_moe_layer(x, w_gate, w_up, w_down, expert_indices, expert_weights=None, activation="silu", out=None,
+                 stream=None, workspace=None):
+    """The mixture-of-experts layer for a few tokens: out[t] = sum_s expert_weights[t, s] * (act(x[t] @ w_gate[e]) *
+    (x[t] @ w_up[e])) @ w_down[e], e = expert_indices[t, s] (-1: no pick).  ``activation`` is 'silu', 'gelu' or
+    'relu'; w_up None leaves the second factor out."""
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(sorted(_ACTIVATIONS)))
+    lib = _lib()
+    d = [_desc(t) for t in (x, w_gate, w_up, w_down, expert_indices)]
+    y = torch.empty((x.shape[0], w_down.shape[2]), dtype=x.dtype, device=x.device) if out is None else out
+    ws, wsb = _given_or_sized(workspace, x.device, lib.mm_moe_layer_workspace_size, *d)
+    _check(lib.mm_moe_layer(*[_ref(t) for t in d], _ref(_desc(expert_weights)), _ACTIVATIONS[activation],
+                            _ref(_desc(y)), None if ws is None else ws.data_ptr(), wsb, _stream(x, stream)),
+           "mm_moe_layer")
+    return y
+
+
+def mm_lowrank_matmul_workspace_size(X, W, A, B):
+    return _sized(_lib().mm_lowrank_matmul_workspace_size, _desc(X), _desc(W), _desc(A), _desc(B))
+
+
+def mm_lowrank_matmul(X, W, A, B, adapter_indices, scales=None, out=None, stream=None, workspace=None):
+    """X @ W plus each row's low-rank adapter: Y[m] = X[m] @ W + scales[g] * (X[m] @ A[g]) @ B[g],
+    g = adapter_indices[m] (-1: no adapter)."""
+    lib = _lib()
+    d = [_desc(t) for t in (X, W, A, B)]
+    y = torch.empty((X.shape[0], W.shape[1]), dtype=X.dtype, device=X.device) if out is None else out
+    ws, wsb = _given_or_sized(workspace, X.device, lib.mm_lowrank_matmul_workspace_size, *d)
+    _check(lib.mm_lowrank_matmul(*[_ref(t) for t in d], _ref(_desc(adapter_indices)), _ref(_desc(scales)),
+                                 _ref(_desc(y)), None if ws is None else ws.data_ptr(), wsb, _stream(X, stream)),
+           "mm_lowrank_matmul")
+    return y
+
+
+def mm_lowrank_matmul_grad_workspace_size(X, W, A, B):
+    return _sized(_lib().mm_lowrank_matmul_grad_workspace_size, _desc(X), _desc(W), _desc(A), _desc(B))
+
+
+def mm_lowrank_matmul_grad(dY, X, W, A, B, adapter_indices, scales=None, need=(True, True, True), stream=None,
+                           workspace=None):
+    """Gradients (dX, dA, dB) of mm_lowrank_matmul for a frozen W; ``need`` says which are wanted (None in the
+    others' place)."""
+    lib = _lib()
+    d = [_desc(t) for t in (X, W, A, B)]
+    dX = torch.empty(X.shape, dtype=X.dtype, device=X.device) if need[0] else None
+    dA = torch.empty(A.shape, dtype=A.dtype, device=X.device) if need[1] else None
+    dB = torch.empty(B.shape, dtype=B.dtype, device=X.device) if need[2] else None
+    ws, wsb = _given_or_sized(workspace, X.device, lib.mm_lowrank_matmul_grad_workspace_size, *d)
+    _check(lib.mm_lowrank_matmul_grad(_ref(_desc(dY)), *[_ref(t) for t in d], _ref(_desc(adapter_indices)),
+                                      _ref(_desc(scales)), _ref(_desc(dX)), _ref(_desc(dA)), _ref(_desc(dB)),
+                                      None if ws is None else ws.data_ptr(), wsb, _stream(X, stream)),
+           "mm_lowrank_matmul_grad")
+    return dX, dA, dB
 
 
 def mm_get_device_status(stream=None, device=None):

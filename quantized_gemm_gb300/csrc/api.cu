@@ -6,6 +6,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "api_internal.h"
 #include "kernels.h"
 #include "tc.h"
 
@@ -19,6 +20,10 @@ thread_local int g_last_path = MM_PATH_NONE;
 // Device-side status word (one instance per device); kernels receive its
 // address as a parameter, so no relocatable device code is needed.
 __device__ unsigned g_device_status;
+
+}  // namespace
+
+namespace qg {
 
 unsigned* device_status_ptr() {
   static std::mutex mu;
@@ -88,6 +93,10 @@ mm_status check_output(const mm_tensor* y, int dtype, int ndim, const int64_t* s
   return MM_OK;
 }
 
+}  // namespace qg
+
+namespace {
+
 // numpy.matmul shape inference (MatMul page summary and Examples): 1-D
 // promotion, right-aligned batch broadcast.  Produces the broadcast batch map
 // and the matrix views of both operands.
@@ -154,7 +163,13 @@ MatView output_view(const mm_tensor* Y, const MatmulPlan& p, int a_is_1d, int b_
   return v;
 }
 
+}  // namespace
+
+namespace qg {
+
 // Chosen path for a call, honouring the process-wide policy.
+int path_policy() { return g_policy.load(); }
+
 int choose(bool tensor_ok, bool tensor_pays) {
   const int pol = g_policy.load();
   if (pol == MM_PATH_SIMT) return MM_PATH_SIMT;
@@ -185,7 +200,7 @@ mm_status finish(mm_status s, int path) {
 // The few-row kernels pay when they stream at least 2^17 elements of B'
 // (their k split and cross-CTA reduction cost a few microseconds); smaller
 // products take one pass of the CUDA-core tiles.
-bool few_row_pays(const GemmArgs& g) { return (double)g.N * (double)g.K * (double)g.bm.count >= 131072.0; }
+static bool few_row_pays(const GemmArgs& g) { return (double)g.N * (double)g.K * (double)g.bm.count >= 131072.0; }
 
 mm_status run_dense(const GemmArgs& g, bool pays, cudaStream_t st) {
   const int pol = g_policy.load();
@@ -199,7 +214,7 @@ mm_status run_dense(const GemmArgs& g, bool pays, cudaStream_t st) {
   return finish(launch_simt_gemm(g, st), MM_PATH_SIMT);
 }
 
-}  // namespace
+}  // namespace qg
 
 extern "C" {
 
@@ -213,7 +228,7 @@ const char* mm_status_string(mm_status s) {
     case MM_ERR_WORKSPACE: return "MM_ERR_WORKSPACE: workspace missing, too small or misaligned";
     case MM_ERR_CUDA: return "MM_ERR_CUDA: a CUDA call or kernel launch failed";
     case MM_ERR_TIMEOUT: return "MM_ERR_TIMEOUT: a device pipeline wait exceeded its limit";
-    case MM_ERR_INDEX_RANGE: return "MM_ERR_INDEX_RANGE: a group index outside [0, G) was seen";
+    case MM_ERR_INDEX_RANGE: return "MM_ERR_INDEX_RANGE: a group, expert or adapter index out of its range was seen";
   }
   return "unknown mm_status";
 }

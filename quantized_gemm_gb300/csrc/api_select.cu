@@ -1,0 +1,321 @@
+// C-ABI entry points of the operators whose products select their weights per
+// row: top-k routing, the mixture-of-experts layer and the low-rank adapters
+// (include/mm.h).  Validation, workspace layout and dispatch only.
+#include <cstring>
+
+#include "api_internal.h"
+#include "kernels.h"
+#include "tc.h"
+
+using namespace qg;
+
+namespace {
+
+bool is_float16_32(int dt) { return dt == MM_BF16 || dt == MM_F16 || dt == MM_F32; }
+bool is_index(int dt) { return dt == MM_I32 || dt == MM_I64; }
+
+bool has_shape(const mm_tensor* t, std::initializer_list<int64_t> shape) {
+  if (t->ndim != (int)shape.size()) return false;
+  int d = 0;
+  for (int64_t n : shape)
+    if (t->shape[d++] != n) return false;
+  return true;
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+bool workspace_ok(const void* ws, size_t have, size_t need) {
+  return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & 255) == 0);
+}
+
+}  // namespace
+
+extern "C" {
+
+// ------------------------------------------------------------------ top-k routing
+
+mm_status mm_route_topk(const mm_tensor* logits, int32_t normalize, const mm_tensor* indices,
+                        const mm_tensor* weights, void* stream) {
+  mm_status s;
+  if ((s = check_tensor(logits)) != MM_OK || (s = check_tensor(indices)) != MM_OK ||
+      (s = check_tensor(weights)) != MM_OK)
+    return s;
+  if (!is_float16_32(logits->dtype)) return MM_ERR_DTYPE;
+  if (logits->ndim != 2 || indices->ndim != 2) return MM_ERR_SHAPE;
+  RouteArgs a;
+  memset(&a, 0, sizeof(a));
+  a.dtype = logits->dtype;
+  a.rows = logits->shape[0]; a.G = logits->shape[1]; a.k = indices->shape[1];
+  const int64_t oshape[2] = {a.rows, a.k};
+  if ((s = check_output(indices, MM_I32, 2, oshape)) != MM_OK || (s = check_output(weights, MM_F32, 2, oshape)) != MM_OK)
+    return s;
+  if (a.k < 1 || a.k > a.G || a.k > kRouteMaxPicks) return MM_ERR_SHAPE;
+  if (a.G > kRouteMaxExperts) return MM_ERR_UNSUPPORTED;
+  if (a.rows == 0) return finish(MM_OK, MM_PATH_NONE);
+  a.normalize = normalize != 0;
+  a.logits = logits->data; a.l_rs = logits->strides[0]; a.l_cs = logits->strides[1];
+  a.indices = indices->data;
+  a.weights = weights->data;
+  return finish(launch_route_topk(a, static_cast<cudaStream_t>(stream)), MM_PATH_SIMT);
+}
+
+mm_status mm_route_topk_grad(const mm_tensor* logits, const mm_tensor* indices, const mm_tensor* grad_weights,
+                             int32_t normalize, const mm_tensor* grad_logits, void* stream) {
+  mm_status s;
+  if ((s = check_tensor(logits)) != MM_OK || (s = check_tensor(indices)) != MM_OK ||
+      (s = check_tensor(grad_weights)) != MM_OK)
+    return s;
+  if (!is_float16_32(logits->dtype) || !is_index(indices->dtype) || grad_weights->dtype != MM_F32) return MM_ERR_DTYPE;
+  if (logits->ndim != 2 || indices->ndim != 2) return MM_ERR_SHAPE;
+  RouteArgs a;
+  memset(&a, 0, sizeof(a));
+  a.dtype = logits->dtype;
+  a.rows = logits->shape[0]; a.G = logits->shape[1]; a.k = indices->shape[1];
+  if (indices->shape[0] != a.rows || !has_shape(grad_weights, {a.rows, a.k})) return MM_ERR_SHAPE;
+  if ((s = check_output(grad_logits, a.dtype, 2, logits->shape)) != MM_OK) return s;
+  if (a.k < 1 || a.k > a.G || a.k > kRouteMaxPicks) return MM_ERR_SHAPE;
+  if (a.G > kRouteMaxExperts) return MM_ERR_UNSUPPORTED;
+  if (a.rows == 0) return finish(MM_OK, MM_PATH_NONE);
+  a.normalize = normalize != 0;
+  a.logits = logits->data; a.l_rs = logits->strides[0]; a.l_cs = logits->strides[1];
+  a.indices = indices->data; a.ind64 = indices->dtype == MM_I64;
+  a.i_rs = indices->strides[0]; a.i_cs = indices->strides[1];
+  a.gw = grad_weights->data; a.gw_rs = grad_weights->strides[0]; a.gw_cs = grad_weights->strides[1];
+  a.out = grad_logits->data;
+  unsigned* status = device_status_ptr();
+  if (!status) return MM_ERR_CUDA;
+  return finish(launch_route_topk_grad(a, status, static_cast<cudaStream_t>(stream)), MM_PATH_SIMT);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ mixture-of-experts layer
+
+namespace {
+
+mm_status plan_moe(const mm_tensor* x, const mm_tensor* w_gate, const mm_tensor* w_up, const mm_tensor* w_down,
+                   const mm_tensor* gi, MoeArgs* a) {
+  mm_status s;
+  if ((s = check_tensor(x)) != MM_OK || (s = check_tensor(w_gate)) != MM_OK || (s = check_tensor(w_down)) != MM_OK ||
+      (s = check_tensor(gi)) != MM_OK)
+    return s;
+  if (w_up && (s = check_tensor(w_up)) != MM_OK) return s;
+  if (!is_float16_32(x->dtype) || w_gate->dtype != x->dtype || w_down->dtype != x->dtype ||
+      (w_up && w_up->dtype != x->dtype) || !is_index(gi->dtype))
+    return MM_ERR_DTYPE;
+  if (x->ndim != 2 || w_gate->ndim != 3 || w_down->ndim != 3 || gi->ndim != 2) return MM_ERR_SHAPE;
+  memset(a, 0, sizeof(*a));
+  a->dtype = x->dtype;
+  a->ind64 = gi->dtype == MM_I64;
+  a->tokens = x->shape[0]; a->K = x->shape[1];
+  a->G = w_gate->shape[0]; a->F = w_gate->shape[2];
+  a->N = w_down->shape[2]; a->S = gi->shape[1];
+  if (w_gate->shape[1] != a->K || gi->shape[0] != a->tokens || w_down->shape[0] != a->G || w_down->shape[1] != a->F ||
+      (w_up && !has_shape(w_up, {a->G, a->K, a->F})))
+    return MM_ERR_SHAPE;
+  a->x = x->data; a->x_rs = x->strides[0]; a->x_cs = x->strides[1];
+  a->wg = w_gate->data; a->wg_gs = w_gate->strides[0]; a->wg_ks = w_gate->strides[1]; a->wg_fs = w_gate->strides[2];
+  if (w_up) {
+    a->wu = w_up->data; a->wu_gs = w_up->strides[0]; a->wu_ks = w_up->strides[1]; a->wu_fs = w_up->strides[2];
+  }
+  a->wd = w_down->data; a->wd_gs = w_down->strides[0]; a->wd_fs = w_down->strides[1]; a->wd_ns = w_down->strides[2];
+  a->gi = gi->data; a->gi_ts = gi->strides[0]; a->gi_ss = gi->strides[1];
+  return MM_OK;
+}
+
+size_t moe_simt_bytes(const MoeArgs& a) { return align256((size_t)(a.tokens * a.S) * (size_t)a.F * sizeof(float)); }
+
+}  // namespace
+
+extern "C" {
+
+mm_status mm_moe_layer_workspace_size(const mm_tensor* x, const mm_tensor* w_gate, const mm_tensor* w_up,
+                                      const mm_tensor* w_down, const mm_tensor* expert_indices, size_t* bytes) {
+  if (!bytes) return MM_ERR_INVALID_ARG;
+  MoeArgs a;
+  const mm_status s = plan_moe(x, w_gate, w_up, w_down, expert_indices, &a);
+  if (s != MM_OK) return s;
+  *bytes = moe_simt_bytes(a);
+  return MM_OK;
+}
+
+mm_status mm_moe_layer(const mm_tensor* x, const mm_tensor* w_gate, const mm_tensor* w_up, const mm_tensor* w_down,
+                       const mm_tensor* expert_indices, const mm_tensor* expert_weights, int32_t activation,
+                       const mm_tensor* out, void* workspace, size_t workspace_bytes, void* stream) {
+  MoeArgs a;
+  mm_status s = plan_moe(x, w_gate, w_up, w_down, expert_indices, &a);
+  if (s != MM_OK) return s;
+  if (activation != MM_ACT_SILU && activation != MM_ACT_GELU && activation != MM_ACT_RELU) return MM_ERR_INVALID_ARG;
+  if (expert_weights) {
+    if ((s = check_tensor(expert_weights)) != MM_OK) return s;
+    if (expert_weights->dtype != MM_F32) return MM_ERR_DTYPE;
+    if (!has_shape(expert_weights, {a.tokens, a.S})) return MM_ERR_SHAPE;
+    a.ew = expert_weights->data; a.ew_ts = expert_weights->strides[0]; a.ew_ss = expert_weights->strides[1];
+  }
+  const int64_t oshape[2] = {a.tokens, a.N};
+  if ((s = check_output(out, a.dtype, 2, oshape)) != MM_OK) return s;
+  a.act = activation;
+  a.out = out->data;
+  if (a.tokens == 0 || a.N == 0) return finish(MM_OK, MM_PATH_NONE);
+  unsigned* status = device_status_ptr();
+  if (!status) return MM_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!workspace_ok(workspace, workspace_bytes, moe_simt_bytes(a))) return MM_ERR_WORKSPACE;
+  return finish(launch_simt_moe(a, static_cast<float*>(workspace), status, st), MM_PATH_SIMT);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ low-rank adapters
+
+namespace {
+
+struct LowRankPlan {
+  LowRankArgs l;
+  int64_t K, N;
+};
+
+// idx may be NULL (workspace queries).
+mm_status plan_lowrank(const mm_tensor* X, const mm_tensor* W, const mm_tensor* A, const mm_tensor* B,
+                       const mm_tensor* idx, const mm_tensor* scales, LowRankPlan* p) {
+  mm_status s;
+  for (const mm_tensor* t : {X, W, A, B})
+    if ((s = check_tensor(t)) != MM_OK) return s;
+  if (!is_float16_32(X->dtype) || W->dtype != X->dtype || A->dtype != X->dtype || B->dtype != X->dtype)
+    return MM_ERR_DTYPE;
+  if (X->ndim != 2 || W->ndim != 2 || A->ndim != 3 || B->ndim != 3) return MM_ERR_SHAPE;
+  memset(p, 0, sizeof(*p));
+  p->K = X->shape[1];
+  p->N = W->shape[1];
+  LowRankArgs& l = p->l;
+  l.dtype = X->dtype;
+  l.M = X->shape[0]; l.G = A->shape[0]; l.R = A->shape[2];
+  if (W->shape[0] != p->K || A->shape[1] != p->K || !has_shape(B, {l.G, l.R, p->N})) return MM_ERR_SHAPE;
+  if (l.R > 65535 * 16) return MM_ERR_UNSUPPORTED;
+  if (idx) {
+    if ((s = check_tensor(idx)) != MM_OK) return s;
+    if (!is_index(idx->dtype)) return MM_ERR_DTYPE;
+    if (!has_shape(idx, {l.M})) return MM_ERR_SHAPE;
+    l.idx = idx->data; l.idx_s = idx->strides[0]; l.ind64 = idx->dtype == MM_I64;
+  }
+  if (scales) {
+    if ((s = check_tensor(scales)) != MM_OK) return s;
+    if (scales->dtype != MM_F32) return MM_ERR_DTYPE;
+    if (!has_shape(scales, {l.G})) return MM_ERR_SHAPE;
+    l.scales = static_cast<const float*>(scales->data); l.scales_s = scales->strides[0];
+  }
+  return MM_OK;
+}
+
+size_t factor_bytes(const LowRankArgs& l) { return align256((size_t)l.M * (size_t)l.R * sizeof(float)); }
+
+// Y = X W + Y for dense Y [M, N] that already holds the low-rank part.
+mm_status add_projection(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t K, const void* w,
+                         int64_t w_rs, int64_t w_cs, int64_t N, void* y, cudaStream_t st) {
+  GemmArgs g;
+  memset(&g, 0, sizeof(g));
+  g.dtype = l.dtype; g.M = l.M; g.N = N; g.K = K;
+  g.bm.nb = 0; g.bm.count = 1;
+  for (int d = 0; d < kMaxBatchDims; ++d) g.bm.shape[d] = 1;
+  g.a.ptr = x; g.a.rs = x_rs; g.a.cs = x_cs;
+  g.b.ptr = w; g.b.rs = w_rs; g.b.cs = w_cs;
+  g.y.ptr = y; g.y.rs = N; g.y.cs = 1;
+  // Every kernel of the dense product reads an element of C in the thread
+  // that then writes that element of Y (or before its tile's store).
+  g.c = g.y;
+  g.alpha = 1.f; g.beta = 1.f; g.alpha_d = 1.0; g.beta_d = 1.0; g.alpha_i = 1; g.beta_i = 1;
+  return run_dense(g, tensor_pays_dense(g.dtype, l.M, N, K, 1), st);
+}
+
+}  // namespace
+
+extern "C" {
+
+mm_status mm_lowrank_matmul_workspace_size(const mm_tensor* X, const mm_tensor* W, const mm_tensor* A,
+                                           const mm_tensor* B, size_t* bytes) {
+  if (!bytes) return MM_ERR_INVALID_ARG;
+  LowRankPlan p;
+  const mm_status s = plan_lowrank(X, W, A, B, nullptr, nullptr, &p);
+  if (s != MM_OK) return s;
+  *bytes = factor_bytes(p.l);
+  return MM_OK;
+}
+
+mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_tensor* A, const mm_tensor* B,
+                            const mm_tensor* adapter_indices, const mm_tensor* scales, const mm_tensor* Y,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  if (!adapter_indices) return MM_ERR_INVALID_ARG;
+  LowRankPlan p;
+  mm_status s = plan_lowrank(X, W, A, B, adapter_indices, scales, &p);
+  if (s != MM_OK) return s;
+  LowRankArgs& l = p.l;
+  const int64_t yshape[2] = {l.M, p.N};
+  if ((s = check_output(Y, l.dtype, 2, yshape)) != MM_OK) return s;
+  if (l.M == 0 || p.N == 0) return finish(MM_OK, MM_PATH_NONE);
+  if (!workspace_ok(workspace, workspace_bytes, factor_bytes(l))) return MM_ERR_WORKSPACE;
+  if (!(l.status = device_status_ptr())) return MM_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float* z = static_cast<float*>(workspace);
+  if ((s = launch_lowrank_shrink(l, X->data, X->strides[0], X->strides[1], p.K, A->data, A->strides[0], A->strides[1],
+                                 A->strides[2], z, st)) != MM_OK)
+    return s;
+  if ((s = launch_lowrank_expand(l, z, B->data, B->strides[0], B->strides[1], B->strides[2], p.N, Y->data, st)) !=
+      MM_OK)
+    return s;
+  return add_projection(l, X->data, X->strides[0], X->strides[1], p.K, W->data, W->strides[0], W->strides[1], p.N,
+                        Y->data, st);
+}
+
+mm_status mm_lowrank_matmul_grad_workspace_size(const mm_tensor* X, const mm_tensor* W, const mm_tensor* A,
+                                                const mm_tensor* B, size_t* bytes) {
+  if (!bytes) return MM_ERR_INVALID_ARG;
+  LowRankPlan p;
+  const mm_status s = plan_lowrank(X, W, A, B, nullptr, nullptr, &p);
+  if (s != MM_OK) return s;
+  *bytes = 2 * factor_bytes(p.l);
+  return MM_OK;
+}
+
+mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const mm_tensor* W, const mm_tensor* A,
+                                 const mm_tensor* B, const mm_tensor* adapter_indices, const mm_tensor* scales,
+                                 const mm_tensor* dX, const mm_tensor* dA, const mm_tensor* dB, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (!adapter_indices) return MM_ERR_INVALID_ARG;
+  LowRankPlan p;
+  mm_status s = plan_lowrank(X, W, A, B, adapter_indices, scales, &p);
+  if (s != MM_OK) return s;
+  LowRankArgs& l = p.l;
+  const int64_t K = p.K, N = p.N;
+  if ((s = check_tensor(dY)) != MM_OK) return s;
+  if (dY->dtype != l.dtype) return MM_ERR_DTYPE;
+  if (!has_shape(dY, {l.M, N})) return MM_ERR_SHAPE;
+  const int64_t xshape[2] = {l.M, K}, ashape[3] = {l.G, K, l.R}, bshape[3] = {l.G, l.R, N};
+  if (dX && (s = check_output(dX, l.dtype, 2, xshape)) != MM_OK) return s;
+  if (dA && (s = check_output(dA, l.dtype, 3, ashape)) != MM_OK) return s;
+  if (dB && (s = check_output(dB, l.dtype, 3, bshape)) != MM_OK) return s;
+  if (!workspace_ok(workspace, workspace_bytes, 2 * factor_bytes(l))) return MM_ERR_WORKSPACE;
+  if (!(l.status = device_status_ptr())) return MM_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float* v = static_cast<float*>(workspace);
+  float* u = reinterpret_cast<float*>(static_cast<char*>(workspace) + factor_bytes(l));
+  s = finish(MM_OK, MM_PATH_NONE);
+  if (dX || dA)
+    s = launch_lowrank_shrink(l, dY->data, dY->strides[0], dY->strides[1], N, B->data, B->strides[0], B->strides[2],
+                              B->strides[1], v, st);
+  if (s == MM_OK && dB)
+    s = launch_lowrank_shrink(l, X->data, X->strides[0], X->strides[1], K, A->data, A->strides[0], A->strides[1],
+                              A->strides[2], u, st);
+  if (s == MM_OK && dA)
+    s = launch_lowrank_outer(l, X->data, X->strides[0], X->strides[1], K, v, dA->data, K * l.R, l.R, 1, st);
+  if (s == MM_OK && dB)
+    s = launch_lowrank_outer(l, dY->data, dY->strides[0], dY->strides[1], N, u, dB->data, l.R * N, 1, N, st);
+  if (s == MM_OK && dX && l.M > 0 && K > 0) {
+    s = launch_lowrank_expand(l, v, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
+    if (s == MM_OK)
+      s = add_projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1], W->strides[0], K,
+                         dX->data, st);
+  }
+  return s;
+}
+
+}  // extern "C"

@@ -89,6 +89,20 @@ __device__ __forceinline__ float requant_f32(int32_t acc, float sa, float sb, fl
   return fminf(fmaxf(t, qmin), qmax);
 }
 
+// Element `off` of a tensor of type T as fp32, and fp32 rounded to T.
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Element `off` of an index tensor (int32 or int64).
+__device__ __forceinline__ int64_t load_index(const void* gi, int64_t off, int ind64) {
+  return ind64 ? static_cast<const int64_t*>(gi)[off] : (int64_t) static_cast<const int32_t*>(gi)[off];
+}
+
 // Programmatic dependent launch.  Every kernel of the library is launched
 // with programmatic stream serialization (launch_pdl) and calls pdl_wait()
 // before its first access to global memory: it waits there until the kernels

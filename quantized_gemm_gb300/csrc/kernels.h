@@ -60,6 +60,62 @@ struct GroupedArgs {
   int64_t qblock;
 };
 
+// Top-k routing (mm_route_topk) and its gradient.
+struct RouteArgs {
+  int dtype;                 // T of logits (and grad_logits)
+  int64_t rows, G, k;
+  int normalize;
+  const void* logits; int64_t l_rs, l_cs;
+  void* indices; int64_t i_rs, i_cs;           // forward: out, dense int32; gradient: in, int32 or int64
+  int ind64;
+  void* weights;                               // forward: out, dense f32
+  const void* gw; int64_t gw_rs, gw_cs;        // gradient: of the weights, f32
+  void* out;                                   // gradient: of the logits, dense T
+};
+constexpr int64_t kRouteMaxExperts = 1024, kRouteMaxPicks = 32;
+
+// Mixture-of-experts layer (mm_moe_layer).
+struct MoeArgs {
+  int dtype;                 // T
+  int ind64, act;
+  int64_t tokens, S, G, K, F, N;
+  const void* x;    int64_t x_rs, x_cs;
+  const void* wg;   int64_t wg_gs, wg_ks, wg_fs;
+  const void* wu;   int64_t wu_gs, wu_ks, wu_fs;   // null = no up projection
+  const void* wd;   int64_t wd_gs, wd_fs, wd_ns;
+  const void* gi;   int64_t gi_ts, gi_ss;
+  const void* ew;   int64_t ew_ts, ew_ss;          // f32 (null = 1)
+  void* out;                 // dense [tokens, N]
+};
+
+// Per-row low-rank adapters (mm_lowrank_matmul and its gradient).
+struct LowRankArgs {
+  int dtype;                 // T
+  int ind64;
+  int64_t M, G, R;
+  const void* idx;  int64_t idx_s;
+  const float* scales; int64_t scales_s;           // null = 1
+  unsigned* status;
+};
+
+mm_status launch_route_topk(const RouteArgs& args, cudaStream_t stream);
+mm_status launch_route_topk_grad(const RouteArgs& args, unsigned* status, cudaStream_t stream);
+
+// h[t * S + s, f] (f32) and then the weighted sum over s, on the CUDA cores.
+mm_status launch_simt_moe(const MoeArgs& args, float* h, unsigned* status, cudaStream_t stream);
+
+// z[m, r] = scale_g * sum_c x[m, c] a[g, c, r], g the adapter of row m (0 without one).
+mm_status launch_lowrank_shrink(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
+                                const void* a, int64_t a_gs, int64_t a_cs, int64_t a_rs, float* z,
+                                cudaStream_t stream);
+// y[m, n] = sum_r z[m, r] b[g, r, n], rounded to T (dense rows of N).
+mm_status launch_lowrank_expand(const LowRankArgs& l, const float* z, const void* b, int64_t b_gs, int64_t b_rs,
+                                int64_t b_ns, int64_t N, void* y, cudaStream_t stream);
+// out[g, c, r] = sum over the rows m of adapter g of x[m, c] z[m, r] (element strides of out given).
+mm_status launch_lowrank_outer(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
+                               const float* z, void* out, int64_t o_gs, int64_t o_cs, int64_t o_rs,
+                               cudaStream_t stream);
+
 mm_status launch_simt_gemm(const GemmArgs& args, cudaStream_t stream);
 // Multiprocessors of the current device (cached per device).
 int sm_count_public();

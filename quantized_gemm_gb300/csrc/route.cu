@@ -1,0 +1,247 @@
+// Top-k routing of tokens to experts (mm_route_topk) and its gradient.
+//
+// For a row of logits l over G experts, p_i = exp(l_i - max) / sum_j exp(l_j -
+// max); the k largest logits are picked (ties to the lowest index) with weight
+// p_i, or p_i over the picked p's sum.  A NaN or -inf logit is an expert that
+// cannot be picked; it takes no part in the sums.  A +inf maximum takes the
+// limit: equal shares among the +inf logits.
+//
+// A row belongs to LPR neighbouring lanes of a warp, lane i holding logits
+// [i*V, (i+1)*V) in registers, so a row is read once.  Logits become unsigned
+// keys in the same order (0: cannot be picked); each of the k rounds takes the
+// group's largest key, and among the lanes holding it the lowest lane and
+// within it the lowest position, which is the lowest index.
+#include "kernels.h"
+
+namespace qg {
+
+namespace {
+
+constexpr int kRouteThreads = 128;
+
+// Unsigned keys in the order of the floats, 0 for NaN and -inf.  Adding +0
+// makes -0 a +0, so that the two tie.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(__fadd_rn(x, 0.f));
+  if (!(x > -INFINITY)) return 0u;
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+// exp(l - top) for l <= top, with the limit for an infinite top.
+__device__ __forceinline__ float share(float l, float top) { return l == top ? 1.f : expf(l - top); }
+
+template <int LPR>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Logits [lane*V, lane*V + V) of a row as floats (-inf past the end).
+template <typename T, int V>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t row, int lane, int vec, float (&l)[V]) {
+  const T* src = static_cast<const T*>(a.logits) + row * a.l_rs;
+  constexpr int kPer = 16 / sizeof(T);
+  if constexpr (V % kPer == 0) {
+    if (vec && (int64_t)(lane + 1) * V <= a.G) {
+#pragma unroll
+      for (int q = 0; q < V / kPer; ++q) {
+        const uint4 u = *reinterpret_cast<const uint4*>(src + lane * V + q * kPer);
+        const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) l[q * kPer + j] = to_f32(e[j]);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int64_t i = (int64_t)lane * V + j;
+    l[j] = i < a.G ? to_f32(src[i * a.l_cs]) : -INFINITY;
+  }
+}
+
+template <typename T, int LPR, int V>
+__global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const RouteArgs a, const int vec) {
+  pdl_begin();
+  constexpr int kRows = kRouteThreads / LPR;
+  const int lane = threadIdx.x % LPR, shift = (threadIdx.x & 31) / LPR * LPR;
+  const unsigned gmask = (LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u)) << shift;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / LPR;
+  const bool live = row < a.rows;
+  float l[V];
+  uint32_t key[V];
+  load_logits<T, V>(a, live ? row : 0, lane, vec, l);
+#pragma unroll
+  for (int j = 0; j < V; ++j) key[j] = order_key(l[j]);
+  float top = 0.f, sum = 0.f, mine = 0.f;
+  int pick = -1;
+#pragma unroll 1
+  for (int r = 0; r < (int)a.k; ++r) {
+    uint32_t best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int j = 1; j < V; ++j)
+      if (key[j] > best) { best = key[j]; at = j; }
+    const uint32_t m = group_max<LPR>(best);
+    const int win = __ffs(__ballot_sync(0xffffffffu, best == m) & gmask) - 1 - shift;   // lowest lane of the group
+    const int wat = __shfl_sync(0xffffffffu, at, win, LPR);
+    if (r == 0) {
+      top = m ? key_value(m) : 0.f;
+      if (!a.normalize) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum += key[j] ? share(l[j], top) : 0.f;
+        sum = group_sum<LPR>(sum);
+      }
+    }
+    if (lane == win) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (j == wat) key[j] = 0u;
+    }
+    const float e = m ? share(key_value(m), top) : 0.f;
+    if (a.normalize) sum += e;
+    if (lane == r) {
+      pick = m ? win * V + wat : -1;
+      mine = e;
+    }
+  }
+  if (live && lane < a.k) {
+    static_cast<int32_t*>(a.indices)[row * a.k + lane] = pick;
+    static_cast<float*>(a.weights)[row * a.k + lane] = pick >= 0 ? mine / sum : 0.f;
+  }
+}
+
+// Gradient of the weights with respect to the logits, the weights recomputed
+// from the logits.  With q the weights scattered over the experts (normalised)
+// or the softmax (not), d the given gradient scattered likewise:
+// dl_i = q_i (d_i - sum_j q_j d_j), for the normalised form only on the picks
+// (q is 0 elsewhere).
+template <typename T, int LPR, int V>
+__global__ void __launch_bounds__(kRouteThreads)
+    route_topk_grad_kernel(const RouteArgs a, const int vec, const int ovec, unsigned* status) {
+  pdl_begin();
+  constexpr int kRows = kRouteThreads / LPR;
+  const int lane = threadIdx.x % LPR;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / LPR;
+  const bool live = row < a.rows;
+  const int64_t rr = live ? row : 0;
+  float l[V], d[V];
+  load_logits<T, V>(a, rr, lane, vec, l);
+  int64_t my_i = -1;
+  float my_d = 0.f;
+  if (lane < a.k) {
+    my_i = load_index(a.indices, rr * a.i_rs + lane * a.i_cs, a.ind64);
+    if (my_i < -1 || my_i >= a.G) {
+      if (live) atomicOr(status, kStatusIndexRange);
+      my_i = -1;
+    }
+    if (my_i >= 0) my_d = static_cast<const float*>(a.gw)[rr * a.gw_rs + lane * a.gw_cs];
+  }
+  uint32_t best = 0u, picked = 0u;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    best = max(best, order_key(l[j]));
+    d[j] = 0.f;
+  }
+  static_assert(V <= 32, "one bit per logit of a lane");
+#pragma unroll 1
+  for (int r = 0; r < (int)a.k; ++r) {
+    const int i = __shfl_sync(0xffffffffu, (int)my_i, r, LPR);
+    const float g = __shfl_sync(0xffffffffu, my_d, r, LPR);
+    const int at = i - lane * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (i >= 0 && j == at) { d[j] += g; picked |= 1u << j; }
+  }
+  const uint32_t m = group_max<LPR>(best);
+  const float top = m ? key_value(m) : 0.f;
+  float sum = 0.f, dot = 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const bool in = order_key(l[j]) != 0u && (!a.normalize || ((picked >> j) & 1u));
+    l[j] = in ? share(l[j], top) : 0.f;
+    sum += l[j];
+  }
+  sum = group_sum<LPR>(sum);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    l[j] *= inv;
+    dot += l[j] > 0.f ? l[j] * d[j] : 0.f;
+  }
+  dot = group_sum<LPR>(dot);
+#pragma unroll
+  for (int j = 0; j < V; ++j) l[j] = l[j] > 0.f ? l[j] * (d[j] - dot) : 0.f;
+  if (!live) return;
+  T* dst = static_cast<T*>(a.out) + row * a.G;
+  constexpr int kPer = 16 / sizeof(T);
+  if constexpr (V % kPer == 0) {
+    if (ovec && (int64_t)(lane + 1) * V <= a.G) {
+#pragma unroll
+      for (int q = 0; q < V / kPer; ++q) {
+        uint4 u;
+        T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) e[j] = from_f32<T>(l[q * kPer + j]);
+        *reinterpret_cast<uint4*>(dst + lane * V + q * kPer) = u;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if ((int64_t)lane * V + j < a.G) dst[(int64_t)lane * V + j] = from_f32<T>(l[j]);
+}
+
+template <typename T, int LPR, int V>
+mm_status launch_one(const RouteArgs& a, bool grad, unsigned* status, cudaStream_t stream) {
+  const int64_t rows_per_block = kRouteThreads / LPR, blocks = (a.rows + rows_per_block - 1) / rows_per_block;
+  if (blocks > 0x7fffffffLL) return MM_ERR_UNSUPPORTED;
+  const int per = 16 / (int)sizeof(T);
+  const int vec = a.l_cs == 1 && a.l_rs % per == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+  if (!grad)
+    return launch_pdl(route_topk_kernel<T, LPR, V>, dim3((unsigned)blocks), dim3(kRouteThreads), 0, stream, a, vec) ==
+                   cudaSuccess ? MM_OK : MM_ERR_CUDA;
+  const int ovec = a.G % per == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+  return launch_pdl(route_topk_grad_kernel<T, LPR, V>, dim3((unsigned)blocks), dim3(kRouteThreads), 0, stream, a, vec,
+                    ovec, status) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+}
+
+// Lanes per row and logits per lane: the fewest lanes that keep a row within
+// 8 logits a lane (fewer lanes per row mean fewer shuffle steps per round),
+// at least one lane per pick.
+template <typename T>
+mm_status launch_typed(const RouteArgs& a, bool grad, unsigned* status, cudaStream_t stream) {
+  if (a.G <= 64 && a.k <= 8) return launch_one<T, 8, 8>(a, grad, status, stream);
+  if (a.G <= 128 && a.k <= 16) return launch_one<T, 16, 8>(a, grad, status, stream);
+  if (a.G <= 256) return launch_one<T, 32, 8>(a, grad, status, stream);
+  if (a.G <= 512) return launch_one<T, 32, 16>(a, grad, status, stream);
+  return launch_one<T, 32, 32>(a, grad, status, stream);
+}
+
+mm_status launch_any(const RouteArgs& a, bool grad, unsigned* status, cudaStream_t stream) {
+  switch (a.dtype) {
+    case MM_BF16: return launch_typed<__nv_bfloat16>(a, grad, status, stream);
+    case MM_F16: return launch_typed<__half>(a, grad, status, stream);
+    default: return launch_typed<float>(a, grad, status, stream);
+  }
+}
+
+}  // namespace
+
+mm_status launch_route_topk(const RouteArgs& a, cudaStream_t stream) { return launch_any(a, false, nullptr, stream); }
+
+mm_status launch_route_topk_grad(const RouteArgs& a, unsigned* status, cudaStream_t stream) {
+  return launch_any(a, true, status, stream);
+}
+
+}  // namespace qg

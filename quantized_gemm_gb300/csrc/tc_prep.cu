@@ -381,10 +381,6 @@ GLayout glayout(int64_t M, int64_t S, int64_t G, int64_t K, int elem) {
   return l;
 }
 
-__device__ __forceinline__ int64_t load_index(const void* gi, int64_t off, int ind64) {
-  return ind64 ? static_cast<const int64_t*>(gi)[off] : (int64_t) static_cast<const int32_t*>(gi)[off];
-}
-
 // Up to kHistGroups groups are counted in a shared-memory histogram per block
 // (lanes of a warp that pick the same group add once, by popcount), then added
 // to the global counts; more groups count with global atomics directly.
