@@ -6,7 +6,7 @@
 //
 // One pass computes h (fp32, in the workspace), one the weighted sum, every
 // sum in fp32 in a fixed order.  Each pick reads its expert's weights anew.
-#include "kernels.h"
+#include "moe.cuh"
 
 namespace qg {
 
@@ -14,14 +14,6 @@ namespace {
 
 constexpr int kMoeThreads = 128;
 constexpr int kMoeChunk = 512;     // x or h values staged at a time
-
-__device__ __forceinline__ float activate(float g, int act) {
-  switch (act) {
-    case MM_ACT_SILU: return g / (1.f + expf(-g));
-    case MM_ACT_GELU: return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
-    default: return g < 0.f ? 0.f : g;   // keeps NaN
-  }
-}
 
 // Expert of pick (t, s): -1 for none; an index past [-1, G) counts as none and is recorded.
 __device__ __forceinline__ int64_t pick_of(const MoeArgs& a, int64_t t, int64_t s, unsigned* status) {

@@ -1,0 +1,672 @@
+// Mixture-of-experts layer for a few tokens (mm_moe_layer) on the tensor
+// cores: three launches, the last two of which do all the work.
+//
+//   plan    one block: which experts are picked, by which tokens
+//   hidden  h[row] = act(x Wg[e]) * (x Wu[e])    one row per (expert, token) pick
+//   down    out[t] = sum over t's rows of weight * (h[row] Wd[e])
+//
+// A few tokens make the layer a stream of the picked experts' weights, each
+// read once: the bound is memory.  So the weights take the MMA's 128-row side
+// (a tile of 128 output columns, whatever the number of tokens) and the tokens
+// its narrow side (N = 16 .. 128): D[column, token] += W[k, column] x[token, k].
+// Every expert's tile multiplies all tokens at once; a column of D belongs to
+// one token, and only the columns of tokens that picked the expert are used,
+// so no token sees another's values or an unpicked expert's.
+//
+// The work is one sequence of k-blocks of 64 (all tiles of all picked experts
+// for `hidden`; for `down` each output tile's experts in turn), cut into equal
+// contiguous shares, one per SM: every SM streams the same number of bytes
+// however many experts are picked.  A tile whose blocks fall into several
+// shares is finished by the last of its CTAs to arrive, which adds the shares'
+// partial sums (fp32, in the workspace) in share order, so results do not
+// depend on timing.
+//
+// A CTA has 6 warps: warp 0 streams weight and token tiles by TMA into a ring,
+// warp 1 issues the MMAs into one of two TMEM accumulators, warps 2-5 (one
+// TMEM lane quadrant each) run the epilogue.
+#include <cuda.h>
+
+#include <cstring>
+
+#include "moe.cuh"
+#include "tc.h"
+#include "tc_internal.h"
+#include "tc_ptx.cuh"
+
+namespace qg {
+
+using namespace ptx;
+
+namespace {
+
+constexpr int kTok = 128;                    // tokens per launch: one bit each in an expert's mask
+constexpr int kMaskWords = kTok / 32;
+constexpr int kTileBytes = 128 * 64 * 2;     // a weight tile: 128 columns x 64 k
+constexpr int kMaxStages = 12;
+constexpr int kThreads = 192;
+constexpr int kCtrl = 512;                   // barriers, TMEM slot, flags
+constexpr uint32_t kTmem = 512;
+constexpr int kPlanThreads = 512;
+constexpr int kPlanExperts = 2048;           // experts the plan's tables hold (shared memory)
+// A share of fewer k-blocks than this is not worth its partial sums.
+constexpr int kMinShare = 4;
+constexpr int kSmemMax = 227 * 1024;
+
+// Tables written by the plan, in the workspace (read through L2: the kernels
+// that read them may have started before they were written).
+struct MoeTables {
+  int32_t* head;          // [0] picked experts, [1] rows
+  int32_t* expert;        // [picked] expert id, ascending
+  int32_t* offset;        // [picked + 1] first row
+  uint32_t* mask;         // [picked][kMaskWords] tokens that picked it
+  int32_t* row_token;     // [rows]
+  float* row_weight;      // [rows]
+  int32_t* count;         // [hidden tiles + down tiles] arrivals, zeroed
+  int64_t count_n;
+};
+
+struct MoeTcParams {
+  MoeTables tb;
+  int64_t F, N;
+  int tokens, nt;         // tokens of this launch; rounded up to 16
+  int col_tiles;          // tiles of 128 columns (of F, of N)
+  int kblocks;            // k-blocks of 64 (of K, of F)
+  int gated, act, f16;
+  int a_mn;               // the weights are MN-major (unit stride along the columns)
+  int64_t g_bc, u_bc;     // TMA batch coordinate per expert
+  int stages, stage_bytes;
+  uint32_t idesc0;        // instruction descriptor without N
+  void* out;              // hidden: h [rows, h_ld]; down: out [tokens, N]
+  int64_t ld;
+  float* part;            // partial sums, two slots per CTA
+  int32_t* count;         // this phase's arrival counters
+  unsigned* status;
+  unsigned long long timeout_ns, teardown_ns;
+};
+
+// ------------------------------------------------------------------ plan
+
+// T <= kTok tokens.  A token that names an expert twice is one row with the
+// sum of the two weights.  An expert's tokens are bits of its mask, so a row's
+// place (offset + number of lower tokens) needs no order of arrival.
+__global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(const MoeArgs a, const int64_t t0, const int T,
+                                                                const MoeTables tb, unsigned* status) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ uint32_t sm[];
+  uint32_t* mask = sm;                                     // [G][kMaskWords]
+  int* base = reinterpret_cast<int*>(sm + a.G * kMaskWords);   // [G] first row
+  __shared__ int wsum[kPlanThreads / 32][2];
+  const int G = (int)a.G, S = (int)a.S, n = T * S, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < G * kMaskWords; i += kPlanThreads) mask[i] = 0u;
+  for (int64_t i = tid; i < tb.count_n; i += kPlanThreads) tb.count[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const int t = i / S, s = i - t * S;
+    const int64_t e = load_index(a.gi, (t0 + t) * a.gi_ts + s * a.gi_ss, a.ind64);
+    if (e >= 0 && e < G) atomicOr(mask + e * kMaskWords + (t >> 5), 1u << (t & 31));
+    else if (e != -1) atomicOr(status, kStatusIndexRange);
+  }
+  __syncthreads();
+  // Exclusive sums, in expert order, of (picked, rows): a contiguous range per thread.
+  const int per = (G + kPlanThreads - 1) / kPlanThreads, lo = min(G, tid * per), hi = min(G, lo + per);
+  int act = 0, rows = 0;
+  for (int g = lo; g < hi; ++g) {
+    int c = 0;
+#pragma unroll
+    for (int w = 0; w < kMaskWords; ++w) c += __popc(mask[g * kMaskWords + w]);
+    act += c > 0;
+    rows += c;
+  }
+  int ia = act, ir = rows;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int ua = __shfl_up_sync(0xffffffffu, ia, o), ur = __shfl_up_sync(0xffffffffu, ir, o);
+    if (lane >= o) { ia += ua; ir += ur; }
+  }
+  if (lane == 31) { wsum[warp][0] = ia; wsum[warp][1] = ir; }
+  __syncthreads();
+  int pa = ia - act, pr = ir - rows;
+  for (int w = 0; w < warp; ++w) { pa += wsum[w][0]; pr += wsum[w][1]; }
+  for (int g = lo; g < hi; ++g) {
+    int c = 0;
+#pragma unroll
+    for (int w = 0; w < kMaskWords; ++w) c += __popc(mask[g * kMaskWords + w]);
+    base[g] = pr;
+    if (c > 0) {
+      tb.expert[pa] = g;
+      tb.offset[pa] = pr;
+#pragma unroll
+      for (int w = 0; w < kMaskWords; ++w) tb.mask[pa * kMaskWords + w] = mask[g * kMaskWords + w];
+      ++pa;
+      pr += c;
+    }
+  }
+  if (tid == kPlanThreads - 1) {
+    tb.head[0] = pa;
+    tb.head[1] = pr;
+    tb.offset[pa] = pr;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const int t = i / S, s = i - t * S;
+    const int64_t row0 = (t0 + t) * a.gi_ts;
+    const int64_t e = load_index(a.gi, row0 + s * a.gi_ss, a.ind64);
+    if (e < 0 || e >= G) continue;
+    bool first = true;
+    float w = 0.f;
+    for (int q = 0; q < S; ++q) {
+      if (load_index(a.gi, row0 + q * a.gi_ss, a.ind64) != e) continue;
+      if (q < s) { first = false; break; }
+      w += a.ew ? static_cast<const float*>(a.ew)[(t0 + t) * a.ew_ts + q * a.ew_ss] : 1.f;
+    }
+    if (!first) continue;
+    int r = base[e];
+    for (int v = 0; v < (t >> 5); ++v) r += __popc(mask[e * kMaskWords + v]);
+    r += __popc(mask[e * kMaskWords + (t >> 5)] & ((1u << (t & 31)) - 1u));
+    tb.row_token[r] = t;
+    tb.row_weight[r] = w;
+  }
+}
+
+// ------------------------------------------------------------------ shares
+
+// CTA c of P owns k-blocks [U c / P, U (c + 1) / P).
+struct Share {
+  uint32_t U, P;
+  __device__ __forceinline__ uint32_t begin(uint32_t c) const { return (uint32_t)((uint64_t)U * c / P); }
+  __device__ __forceinline__ uint32_t owner(uint32_t u) const { return (uint32_t)(((uint64_t)(u + 1) * P - 1) / U); }
+};
+
+// A run of k-blocks of one tile and one expert within a share.
+struct Seg {
+  uint32_t item;          // tile (hidden: expert-major; down: column tile), indexes the counters
+  uint32_t a, col;        // picked expert, column tile
+  uint32_t kb0, kb1;
+};
+
+// The segment that begins at block u of a share that ends at `end`.
+template <bool DOWN>
+__device__ __forceinline__ Seg seg_at(const MoeTcParams& p, uint32_t picked, uint32_t u, uint32_t end) {
+  Seg s;
+  const uint32_t kb = (uint32_t)p.kblocks;
+  const uint32_t q = u / kb;               // (tile, expert) pair
+  s.kb0 = u - q * kb;
+  s.kb1 = min(kb, s.kb0 + (end - u));
+  if (DOWN) {
+    s.item = s.col = q / picked;
+    s.a = q - s.col * picked;
+  } else {
+    s.item = q;
+    s.a = q / (uint32_t)p.col_tiles;
+    s.col = q - s.a * (uint32_t)p.col_tiles;
+  }
+  return s;
+}
+
+__device__ __forceinline__ int seg_rows(const MoeTcParams& p, uint32_t a) {
+  return __ldcg(p.tb.offset + a + 1) - __ldcg(p.tb.offset + a);
+}
+
+// ------------------------------------------------------------------ kernel
+
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+// One decision for the four epilogue warps, which meet at barriers later on.
+__device__ __forceinline__ bool epi_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
+// Arrival of this CTA's share of a tile; true in every epilogue thread of the
+// CTA that arrives last, which then sees all the shares' partial sums.
+__device__ __forceinline__ bool last_to_arrive(int32_t* counter, int expected, volatile int* flag) {
+  __threadfence();
+  epi_sync();
+  if (threadIdx.x == 64) {
+    const int last = atomicAdd(counter, 1) == expected - 1;
+    __threadfence();
+    *flag = last;
+  }
+  epi_sync();
+  const bool last = *flag != 0;
+  if (last) __threadfence();
+  return last;
+}
+
+__device__ __forceinline__ void store16(void* dst, int64_t i, float v, int f16) {
+  if (f16) static_cast<__half*>(dst)[i] = __float2half_rn(v);
+  else static_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(v);
+}
+
+template <bool DOWN>
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmU,
+                  const __grid_constant__ CUtensorMap tmX, const MoeTcParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t ring = (raw + 1023u) & ~1023u;
+  uint8_t* ctrl = smem_raw + (ring - raw) + p.stages * p.stage_bytes;
+  const uint32_t cbase = ring + (uint32_t)(p.stages * p.stage_bytes);
+  const uint32_t full0 = cbase, empty0 = cbase + 8 * kMaxStages, accf0 = empty0 + 8 * kMaxStages;
+  const uint32_t acce0 = accf0 + 16, drain = acce0 + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 16 * kMaxStages + 40);
+  volatile int* abort = reinterpret_cast<volatile int*>(ctrl + 16 * kMaxStages + 44);
+  volatile int* flag = reinterpret_cast<volatile int*>(ctrl + 16 * kMaxStages + 48);
+  float* acc = reinterpret_cast<float*>(ctrl + kCtrl);       // down: [tokens][128]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf0 + 8 * b, 1);
+      mbar_init(acce0 + 8 * b, 4);
+    }
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // `hidden` lets `down` be scheduled as its CTAs leave the SMs.  By then every
+  // CTA of `hidden` has passed its wait, so the plan (and all work before it)
+  // is complete: `down` streams weights before `hidden` has finished and waits
+  // for it only before it touches h, the partial sums or the output.
+  if (!DOWN) pdl_begin();
+
+  const uint32_t picked = (uint32_t)__ldcg(p.tb.head);
+  Share sh;
+  sh.U = picked * (uint32_t)p.col_tiles * (uint32_t)p.kblocks;
+  sh.P = max(1u, min(gridDim.x, sh.U / kMinShare));
+  const uint32_t cta = blockIdx.x;
+  const uint32_t ub = cta < sh.P ? sh.begin(cta) : 0u, ue = cta < sh.P ? sh.begin(cta + 1) : 0u;
+  constexpr int kW = DOWN ? 1 : 2;                // weight tiles per k-block
+  const int wtiles = DOWN ? 1 : (p.gated ? 2 : 1);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tmap(&tmW);
+      if (!DOWN && p.gated) prefetch_tmap(&tmU);
+      prefetch_tmap(&tmX);
+      uint32_t stage = 0, phase = 0, issued = 0, iparity = 0;
+      uint32_t early_a[kMaxStages], early_kb[kMaxStages];     // down: stages whose h tile waits for `hidden`
+      int early = DOWN ? p.stages : 0, nearly = 0;
+      auto load_weights = [&](uint32_t dst, const CUtensorMap* tm, uint32_t col, uint32_t kb, int32_t b, uint32_t bar) {
+        const int32_t c0 = (int32_t)col * 128, k0 = (int32_t)kb * 64;
+        if (p.a_mn) {
+          tma_load_3d(dst, tm, c0, k0, b, bar);
+          tma_load_3d(dst + 8192, tm, c0 + 64, k0, b, bar);
+        } else {
+          tma_load_3d(dst, tm, k0, c0, b, bar);
+        }
+      };
+      auto load_tokens = [&](uint32_t st, uint32_t a, uint32_t kb) {
+        const uint32_t dst = ring + st * p.stage_bytes + kW * kTileBytes, bar = full0 + 8 * st;
+        if (DOWN) {
+          const int rows = seg_rows(p, a), r0 = __ldcg(p.tb.offset + a);
+          for (int r = 0; r < rows; r += 16) tma_load_3d(dst + r * 128, &tmX, (int32_t)kb * 64, r0 + r, 0, bar);
+        } else {
+          tma_load_3d(dst, &tmX, (int32_t)kb * 64, 0, 0, bar);
+        }
+      };
+      auto release_early = [&]() {
+        pdl_wait();
+        asm volatile("fence.proxy.async;" ::: "memory");      // h was written through the generic proxy
+        for (int i = 0; i < nearly; ++i) load_tokens((uint32_t)i, early_a[i], early_kb[i]);
+        early = 0;
+      };
+      bool ok = true;
+      for (uint32_t u = ub; u < ue && ok;) {
+        const Seg s = seg_at<DOWN>(p, picked, u, ue);
+        const int32_t e = __ldcg(p.tb.expert + s.a);
+        const uint32_t tok_bytes = DOWN ? (uint32_t)((seg_rows(p, s.a) + 15) & ~15) * 128u : (uint32_t)p.nt * 128u;
+        for (uint32_t kb = s.kb0; kb < s.kb1; ++kb) {
+          if (DOWN && early && nearly == early) release_early();
+          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort, p.status, p.timeout_ns)) { ok = false; break; }
+          const uint32_t full = full0 + 8 * stage, dst = ring + stage * p.stage_bytes;
+          mbar_arrive_expect_tx(full, (uint32_t)wtiles * kTileBytes + tok_bytes);
+          load_weights(dst, &tmW, s.col, kb, (int32_t)(e * p.g_bc), full);
+          if (!DOWN && p.gated) load_weights(dst + kTileBytes, &tmU, s.col, kb, (int32_t)(e * p.u_bc), full);
+          if (DOWN && early) {
+            early_a[nearly] = s.a;
+            early_kb[nearly++] = kb;
+          } else {
+            load_tokens(stage, s.a, kb);
+          }
+          issued |= 1u << stage;
+          iparity = (iparity & ~(1u << stage)) | (phase << stage);
+          if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
+        }
+        u += s.kb1 - s.kb0;
+      }
+      if (DOWN && early) release_early();
+      // Let every issued copy land before the CTA can exit.
+      for (int s = 0; s < p.stages; ++s)
+        if (issued & (1u << s)) mbar_wait_teardown(full0 + 8 * s, (iparity >> s) & 1u, p.teardown_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, seg = 0;
+      bool ok = true;
+      for (uint32_t u = ub; u < ue && ok; ++seg) {
+        const Seg s = seg_at<DOWN>(p, picked, u, ue);
+        const uint32_t buf = seg & 1, aph = (seg >> 1) & 1;
+        if (!mbar_wait(acce0 + 8 * buf, aph ^ 1, abort, p.status, p.timeout_ns)) break;
+        tc_fence_after();
+        const uint32_t n = DOWN ? (uint32_t)((seg_rows(p, s.a) + 15) & ~15) : (uint32_t)p.nt;
+        const uint32_t idesc = p.idesc0 | ((n >> 3) << 17), d = tmem + buf * 256;
+        for (uint32_t kb = s.kb0; kb < s.kb1; ++kb) {
+          if (!mbar_wait(full0 + 8 * stage, phase, abort, p.status, p.timeout_ns)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sw = ring + stage * p.stage_bytes, sx = sw + kW * kTileBytes;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t bd = smem_desc_sw128(sx + k * 32, 16, 1024);
+            const uint32_t accum = (kb > s.kb0 || k > 0) ? 1u : 0u;
+            const uint64_t ad = p.a_mn ? smem_desc_sw128(sw + k * 2048, 8192, 1024) : smem_desc_sw128(sw + k * 32, 16, 1024);
+            tc_mma_f16(d, ad, bd, idesc, accum);
+            if (!DOWN && p.gated) {
+              const uint32_t su = sw + kTileBytes;
+              const uint64_t ud = p.a_mn ? smem_desc_sw128(su + k * 2048, 8192, 1024) : smem_desc_sw128(su + k * 32, 16, 1024);
+              tc_mma_f16(d + 128, ud, bd, idesc, accum);
+            }
+          }
+          tc_commit(empty0 + 8 * stage);
+          if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
+        }
+        if (ok) tc_commit(accf0 + 8 * buf);
+        u += s.kb1 - s.kb0;
+      }
+      tc_commit(drain);
+      mbar_wait_teardown(drain, 0, p.teardown_ns);
+    }
+  } else {
+    const int quad = warp & 3, l = quad * 32 + lane;          // column of the tile
+    const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
+    if (DOWN) pdl_wait();
+    uint32_t seg = 0;
+    auto release = [&](uint32_t buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acce0 + 8 * buf);
+    };
+    if (!DOWN) {
+      for (uint32_t u = ub; u < ue; ++seg) {
+        const Seg s = seg_at<false>(p, picked, u, ue);
+        const uint32_t buf = seg & 1, aph = (seg >> 1) & 1;
+        const int64_t f = (int64_t)s.col * 128 + l;
+        const int r0 = __ldcg(p.tb.offset + s.a), rows = __ldcg(p.tb.offset + s.a + 1) - r0;
+        const uint4 mk = __ldcg(reinterpret_cast<const uint4*>(p.tb.mask) + s.a);
+        const bool whole = s.kb0 == 0 && s.kb1 == (uint32_t)p.kblocks;
+        // the share's first tile unless the share begins before the tile
+        const uint32_t slot = 2 * cta + (u == ub ? 0u : 1u);
+        float* part = p.part + (int64_t)slot * p.tokens * 256 + l;
+        if (!epi_all(mbar_wait(accf0 + 8 * buf, aph, abort, p.status, p.timeout_ns))) break;
+        tc_fence_after();
+        int r = 0;
+        for (int g = 0; g < p.nt / 16; ++g) {
+          const uint32_t word = g < 2 ? mk.x : g < 4 ? mk.y : g < 6 ? mk.z : mk.w;
+          const uint32_t bits = (word >> (16 * (g & 1))) & 0xffffu;
+          if (!bits) continue;
+          uint32_t vg[16], vu[16];
+          tmem_ld16(tl + buf * 256 + g * 16, vg);
+          if (p.gated) tmem_ld16(tl + buf * 256 + 128 + g * 16, vu);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (!((bits >> j) & 1u)) continue;
+            const float gv = __uint_as_float(vg[j]), uv = p.gated ? __uint_as_float(vu[j]) : 1.f;
+            if (whole) {
+              const float h = p.gated ? activate(gv, p.act) * uv : activate(gv, p.act);
+              if (f < p.F) store16(p.out, (int64_t)(r0 + r) * p.ld + f, h, p.f16);
+            } else {
+              part[(int64_t)r * 256] = gv;
+              part[(int64_t)r * 256 + 128] = uv;
+            }
+            ++r;
+          }
+        }
+        release(buf);
+        if (!whole) {
+          const uint32_t t0 = s.item * (uint32_t)p.kblocks;
+          const uint32_t c0 = sh.owner(t0), c1 = sh.owner(t0 + (uint32_t)p.kblocks - 1);
+          if (last_to_arrive(p.count + s.item, (int)(c1 - c0 + 1), flag) && f < p.F) {
+            for (int j = 0; j < rows; ++j) {
+              float gv = 0.f, uv = 0.f;
+              for (uint32_t c = c0; c <= c1; ++c) {
+                const float* q = p.part + ((int64_t)(2 * c + (sh.begin(c) < t0 ? 1u : 0u)) * p.tokens + j) * 256 + l;
+                gv += __ldcg(q);
+                uv += __ldcg(q + 128);
+              }
+              const float h = p.gated ? activate(gv, p.act) * uv : activate(gv, p.act);
+              store16(p.out, (int64_t)(r0 + j) * p.ld + f, h, p.f16);
+            }
+          }
+        }
+        u += s.kb1 - s.kb0;
+      }
+    } else {
+      const uint32_t per_tile = picked * (uint32_t)p.kblocks;
+      if (picked == 0)                                         // no pick at all: zeros
+        for (uint32_t col = cta; col < (uint32_t)p.col_tiles; col += gridDim.x) {
+          const int64_t n = (int64_t)col * 128 + l;
+          for (int t = 0; t < p.tokens && n < p.N; ++t) store16(p.out, t * p.ld + n, 0.f, p.f16);
+        }
+      for (uint32_t u = ub; u < ue; ++seg) {
+        const Seg s = seg_at<true>(p, picked, u, ue);
+        const uint32_t buf = seg & 1, aph = (seg >> 1) & 1;
+        const uint32_t t0 = s.item * per_tile, t1 = t0 + per_tile;
+        if (u == ub || u == t0)
+          for (int t = 0; t < p.tokens; ++t) acc[t * 128 + l] = 0.f;
+        const int r0 = __ldcg(p.tb.offset + s.a), rows = __ldcg(p.tb.offset + s.a + 1) - r0;
+        if (!epi_all(mbar_wait(accf0 + 8 * buf, aph, abort, p.status, p.timeout_ns))) break;
+        tc_fence_after();
+        for (int j0 = 0; j0 < rows; j0 += 16) {
+          const int mine = min(j0 + (lane & 15), rows - 1);
+          const int tok = __ldcg(p.tb.row_token + r0 + mine);
+          const float wt = __ldcg(p.tb.row_weight + r0 + mine);
+          uint32_t v[16];
+          tmem_ld16(tl + buf * 256 + j0, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int t = __shfl_sync(0xffffffffu, tok, j);
+            const float w = __shfl_sync(0xffffffffu, wt, j);
+            if (j0 + j < rows) acc[t * 128 + l] = __fmaf_rn(w, __uint_as_float(v[j]), acc[t * 128 + l]);
+          }
+        }
+        release(buf);
+        const uint32_t next = u + (s.kb1 - s.kb0);
+        if (next == ue || next == t1) {                        // the share's last block of this tile
+          const int64_t n = (int64_t)s.col * 128 + l;
+          if (ub <= t0 && ue >= t1) {
+            for (int t = 0; t < p.tokens && n < p.N; ++t) store16(p.out, t * p.ld + n, acc[t * 128 + l], p.f16);
+          } else {
+            const uint32_t slot = 2 * cta + (ub < t0 ? 1u : 0u);
+            float* part = p.part + (int64_t)slot * p.tokens * 128 + l;
+            for (int t = 0; t < p.tokens; ++t) part[t * 128] = acc[t * 128 + l];
+            const uint32_t c0 = sh.owner(t0), c1 = sh.owner(t1 - 1);
+            if (last_to_arrive(p.count + s.item, (int)(c1 - c0 + 1), flag) && n < p.N) {
+              for (int t = 0; t < p.tokens; ++t) {
+                float v = 0.f;
+                for (uint32_t c = c0; c <= c1; ++c)
+                  v += __ldcg(p.part + ((int64_t)(2 * c + (sh.begin(c) < t0 ? 1u : 0u)) * p.tokens + t) * 128 + l);
+                store16(p.out, t * p.ld + n, v, p.f16);
+              }
+            }
+          }
+        }
+        u = next;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+struct MoeLayout {
+  int64_t tok, rows, picked, f_tiles, n_tiles, h_ld;
+  size_t off_head, off_expert, off_offset, off_mask, off_token, off_weight, off_count, off_h, off_part, total;
+};
+
+MoeLayout moe_layout(const MoeArgs& a) {
+  MoeLayout l;
+  l.tok = a.tokens < kTok ? a.tokens : kTok;
+  l.rows = l.tok * a.S;
+  l.picked = a.G < l.rows ? a.G : l.rows;
+  l.f_tiles = (a.F + 127) / 128;
+  l.n_tiles = (a.N + 127) / 128;
+  l.h_ld = (a.F + 7) / 8 * 8;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o = round256(o + bytes); return at; };
+  l.off_head = take(8);
+  l.off_expert = take((size_t)l.picked * 4);
+  l.off_offset = take((size_t)(l.picked + 1) * 4);
+  l.off_mask = take((size_t)l.picked * kMaskWords * 4);
+  l.off_token = take((size_t)l.rows * 4);
+  l.off_weight = take((size_t)l.rows * 4);
+  l.off_count = take((size_t)(l.picked * l.f_tiles + l.n_tiles) * 4);
+  l.off_h = take((size_t)l.rows * (size_t)l.h_ld * 2);
+  l.off_part = take((size_t)2 * (size_t)sm_count_public() * (size_t)l.tok * 256 * 4);
+  l.total = o;
+  return l;
+}
+
+bool plan_weights(const void* w, int dtype, int64_t G, int64_t cols, int64_t k, int64_t gs, int64_t cs, int64_t ks,
+                  OperandPlan* out) {
+  BatchMap bm;
+  memset(&bm, 0, sizeof(bm));
+  bm.nb = 1;
+  bm.shape[0] = bm.count = G;
+  for (int d = 1; d < kMaxBatchDims; ++d) bm.shape[d] = 1;
+  int64_t bs[kMaxBatchDims] = {gs, 0, 0, 0, 0, 0};
+  return plan_operand(w, dtype, cols, k, cs, ks, bm, bs, 128, out);
+}
+
+bool plan_rows(const void* x, int dtype, int64_t rows, int64_t k, int64_t rs, int64_t cs, int box, OperandPlan* out) {
+  BatchMap bm;
+  memset(&bm, 0, sizeof(bm));
+  bm.count = 1;
+  for (int d = 0; d < kMaxBatchDims; ++d) bm.shape[d] = 1;
+  int64_t bs[kMaxBatchDims] = {};
+  if (cs != 1 && k > 1) return false;
+  if (rows == 1) rs = (k + 7) / 8 * 8;      // one row: its stride is never used
+  return plan_operand(x, dtype, rows, k, rs, 1, bm, bs, box, out) && !out->mn_major;
+}
+
+}  // namespace
+
+bool tc_moe_supported(const MoeArgs& a) {
+  if (a.dtype != MM_BF16 && a.dtype != MM_F16) return false;
+  if (a.tokens < 1 || a.S < 1 || a.G < 1 || a.K < 1 || a.F < 1 || a.N < 1) return false;
+  if (a.G > kPlanExperts || a.S > 64) return false;
+  const MoeLayout l = moe_layout(a);
+  // block indices are 32-bit, with room for the shares' products
+  const double blocks = (double)l.picked * (double)l.f_tiles * (double)((a.K + 63) / 64);
+  const double blocks2 = (double)l.picked * (double)l.n_tiles * (double)((a.F + 63) / 64);
+  if (blocks >= 2147483648.0 || blocks2 >= 2147483648.0) return false;
+  OperandPlan w, u, d, x;
+  if (!plan_weights(a.wg, a.dtype, a.G, a.F, a.K, a.wg_gs, a.wg_fs, a.wg_ks, &w)) return false;
+  if (a.wu && (!plan_weights(a.wu, a.dtype, a.G, a.F, a.K, a.wu_gs, a.wu_fs, a.wu_ks, &u) || u.mn_major != w.mn_major))
+    return false;
+  if (!plan_weights(a.wd, a.dtype, a.G, a.N, a.F, a.wd_gs, a.wd_ns, a.wd_fs, &d)) return false;
+  if (!plan_rows(a.x, a.dtype, l.tok, a.K, a.x_rs, a.x_cs, 16, &x)) return false;
+  // Tokens past the first launch's start at other rows: 16-byte aligned too
+  // (x_rs is a multiple of 8 for more than one row).
+  return true;
+}
+
+size_t tc_moe_workspace_bytes(const MoeArgs& a) { return moe_layout(a).total; }
+
+mm_status launch_tc_moe(const MoeArgs& a, void* workspace, unsigned* status, cudaStream_t stream) {
+  const MoeLayout l = moe_layout(a);
+  char* ws = static_cast<char*>(workspace);
+  TcParams limits;                        // the pipelines' wait limits
+  init_params(&limits);
+  MoeTcParams p;
+  memset(&p, 0, sizeof(p));
+  p.tb.head = reinterpret_cast<int32_t*>(ws + l.off_head);
+  p.tb.expert = reinterpret_cast<int32_t*>(ws + l.off_expert);
+  p.tb.offset = reinterpret_cast<int32_t*>(ws + l.off_offset);
+  p.tb.mask = reinterpret_cast<uint32_t*>(ws + l.off_mask);
+  p.tb.row_token = reinterpret_cast<int32_t*>(ws + l.off_token);
+  p.tb.row_weight = reinterpret_cast<float*>(ws + l.off_weight);
+  p.tb.count = reinterpret_cast<int32_t*>(ws + l.off_count);
+  p.tb.count_n = l.picked * l.f_tiles + l.n_tiles;
+  p.F = a.F; p.N = a.N;
+  p.gated = a.wu != nullptr; p.act = a.act; p.f16 = a.dtype == MM_F16;
+  p.part = reinterpret_cast<float*>(ws + l.off_part);
+  p.status = status;
+  p.timeout_ns = limits.timeout_ns; p.teardown_ns = limits.teardown_ns;
+
+  OperandPlan wg, wu, wd, h, x;
+  if (!plan_weights(a.wg, a.dtype, a.G, a.F, a.K, a.wg_gs, a.wg_fs, a.wg_ks, &wg) ||
+      (a.wu && !plan_weights(a.wu, a.dtype, a.G, a.F, a.K, a.wu_gs, a.wu_fs, a.wu_ks, &wu)) ||
+      !plan_weights(a.wd, a.dtype, a.G, a.N, a.F, a.wd_gs, a.wd_ns, a.wd_fs, &wd) ||
+      !plan_rows(ws + l.off_h, a.dtype, l.rows, a.F, l.h_ld, 1, 16, &h))
+    return MM_ERR_UNSUPPORTED;
+  const int plan_smem = (int)(a.G * (kMaskWords + 1) * 4);
+  const int sms = sm_count_public();
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += kTok) {
+    const int T = (int)(a.tokens - t0 < kTok ? a.tokens - t0 : kTok);
+    p.tokens = T;
+    p.nt = (T + 15) / 16 * 16;
+    if (launch_pdl(moe_plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)plan_smem, stream, a, t0, T, p.tb, status) !=
+        cudaSuccess)
+      return MM_ERR_CUDA;
+    for (int down = 0; down < 2; ++down) {
+      MoeTcParams q = p;
+      const OperandPlan& w = down ? wd : wg;
+      if (!down && !plan_rows(static_cast<const uint16_t*>(a.x) + t0 * a.x_rs, a.dtype, T, a.K, a.x_rs, a.x_cs, p.nt, &x))
+        return MM_ERR_UNSUPPORTED;
+      q.col_tiles = (int)(down ? l.n_tiles : l.f_tiles);
+      q.kblocks = (int)(((down ? a.F : a.K) + 63) / 64);
+      q.a_mn = w.mn_major;
+      q.g_bc = w.bc[0];
+      q.u_bc = !down && a.wu ? wu.bc[0] : 0;
+      q.idesc0 = make_idesc_mn(q.f16, q.a_mn, 0, 128, 0);
+      q.out = down ? a.out : ws + l.off_h;
+      if (down) q.out = static_cast<uint16_t*>(a.out) + t0 * a.N;
+      q.ld = down ? a.N : l.h_ld;
+      q.count = p.tb.count + (down ? l.picked * l.f_tiles : 0);
+      q.stage_bytes = (down ? 1 : 2) * kTileBytes + p.nt * 128;
+      const int acc_bytes = down ? T * 128 * 4 : 0;
+      q.stages = (kSmemMax - 1024 - kCtrl - acc_bytes) / q.stage_bytes;
+      if (q.stages > kMaxStages) q.stages = kMaxStages;
+      const int smem = 1024 + q.stages * q.stage_bytes + kCtrl + acc_bytes;
+      const auto kernel = down ? moe_tc_kernel<true> : moe_tc_kernel<false>;
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
+        return MM_ERR_CUDA;
+      if (launch_pdl(kernel, dim3((unsigned)sms), dim3(kThreads), (size_t)smem, stream, w.map,
+                     !down && a.wu ? wu.map : w.map, down ? h.map : x.map, q) != cudaSuccess)
+        return MM_ERR_CUDA;
+    }
+  }
+  return MM_OK;
+}
+
+}  // namespace qg

@@ -23,4 +23,11 @@ size_t tc_grouped_workspace_bytes(const GroupedArgs& g);
 // the weights stay int8/uint8 in memory and are dequantised in shared memory.
 mm_status launch_tc_grouped(const GroupedArgs& g, void* workspace, unsigned* status, cudaStream_t stream);
 
+// The mixture-of-experts layer for a few tokens (moe_tc.cu): every matrix with
+// 16-byte aligned rows along a unit-stride matrix dimension, w_gate and w_up
+// with the same one.
+bool tc_moe_supported(const MoeArgs& a);
+size_t tc_moe_workspace_bytes(const MoeArgs& a);
+mm_status launch_tc_moe(const MoeArgs& a, void* workspace, unsigned* status, cudaStream_t stream);
+
 }  // namespace qg

@@ -152,6 +152,38 @@ def test_moe_layer(T, G, S, K, F, N, dtype):
     _check_moe(*_moe_inputs(T, G, S, K, F, N, dtype, T + K))
 
 
+@pytest.fixture
+def tensor_path():
+    qg.mm_set_path_policy(qg.MM_PATH_TENSOR)
+    yield
+    qg.mm_set_path_policy(qg.MM_PATH_AUTO)
+
+
+# sizes at the tiles' edges (128 columns, 64 k, 16 tokens, 128 tokens a pass) and shares of a few blocks
+MOE_TC = [(1, 1, 1, 8, 8, 8), (1, 3, 1, 64, 128, 128), (2, 2, 2, 72, 136, 8), (15, 9, 4, 128, 120, 248),
+          (16, 200, 8, 64, 64, 64), (17, 2, 1, 520, 264, 136), (33, 300, 3, 128, 72, 264), (127, 5, 2, 256, 128, 72),
+          (128, 4, 4, 192, 136, 128), (129, 4, 2, 64, 64, 64), (300, 7, 3, 128, 192, 200), (4, 2, 2, 2048, 1536, 1024)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,G,S,K,F,N", MOE_TC)
+def test_moe_layer_on_the_tensor_cores(T, G, S, K, F, N, dtype, tensor_path):
+    args = _moe_inputs(T, G, S, K, F, N, dtype, T + K + G)
+    out = _check_moe(*args)
+    assert qg.mm_last_path() == qg.MM_PATH_TENSOR
+    for _ in range(2):
+        assert torch.equal(out, qg.mm_moe_layer(*args))
+
+
+def test_moe_layer_uneven_experts_on_the_tensor_cores(tensor_path):
+    x, wg, wu, wd, idx, w = _moe_inputs(100, 8, 2, 256, 320, 256, BF16, 23)
+    idx[:, 0] = 1                     # one expert with every token, one with a single one, some with none
+    idx[:, 1] = torch.where(torch.arange(100, device=DEV) == 77, 6, -1)
+    _check_moe(x, wg, wu, wd, idx, w)
+    idx[:] = -1
+    assert not qg.mm_moe_layer(x, wg, wu, wd, idx, w).any()
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
 @pytest.mark.parametrize("up", [True, False])
 @pytest.mark.parametrize("dtype", [BF16, F32])
