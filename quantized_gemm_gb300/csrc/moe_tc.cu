@@ -75,6 +75,7 @@ struct MoeTcParams {
   int a_mn;               // the weights are MN-major (unit stride along the columns)
   int64_t g_bc, u_bc;     // TMA batch coordinate per expert
   int stages, stage_bytes;
+  int max_picked, table_bytes;
   uint32_t idesc0;        // instruction descriptor without N
   void* out;              // hidden: h [rows, h_ld]; down: out [tokens, N]
   int64_t ld;
@@ -204,10 +205,6 @@ __device__ __forceinline__ Seg seg_at(const MoeTcParams& p, uint32_t picked, uin
   return s;
 }
 
-__device__ __forceinline__ int seg_rows(const MoeTcParams& p, uint32_t a) {
-  return __ldcg(p.tb.offset + a + 1) - __ldcg(p.tb.offset + a);
-}
-
 // ------------------------------------------------------------------ kernel
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
@@ -241,6 +238,21 @@ __device__ __forceinline__ bool last_to_arrive(int32_t* counter, int expected, v
   return last;
 }
 
+// The partial sums at `at` of shares c0..c1 of the tile that starts at block
+// t0, added in share order; slots are `stride` floats apart, and a share that
+// began before the tile holds it in its second slot.
+__device__ __forceinline__ float4 sum_shares(const float* at, int64_t stride, const Share& sh, uint32_t c0, uint32_t c1,
+                                             uint32_t t0) {
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (uint32_t c = c0; c <= c1; ++c) {
+    // only the first share can have begun before the tile
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(at + (int64_t)(2 * c + (c == c0 && sh.begin(c) < t0)) * stride));
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  return s;
+}
+
 __device__ __forceinline__ void store16(void* dst, int64_t i, float v, int f16) {
   if (f16) static_cast<__half*>(dst)[i] = __float2half_rn(v);
   else static_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(v);
@@ -260,7 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 16 * kMaxStages + 40);
   volatile int* abort = reinterpret_cast<volatile int*>(ctrl + 16 * kMaxStages + 44);
   volatile int* flag = reinterpret_cast<volatile int*>(ctrl + 16 * kMaxStages + 48);
-  float* acc = reinterpret_cast<float*>(ctrl + kCtrl);       // down: [tokens][128]
+  int32_t* t_expert = reinterpret_cast<int32_t*>(ctrl + kCtrl);        // the plan's tables: a copy, [picked] and
+  int32_t* t_offset = t_expert + p.max_picked;                         // [picked + 1]
+  float* acc = reinterpret_cast<float*>(ctrl + kCtrl + p.table_bytes);   // down: [tokens][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -291,6 +305,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!DOWN) pdl_begin();
 
   const uint32_t picked = (uint32_t)__ldcg(p.tb.head);
+  for (uint32_t i = threadIdx.x; i < picked; i += kThreads) t_expert[i] = __ldcg(p.tb.expert + i);
+  for (uint32_t i = threadIdx.x; i <= picked; i += kThreads) t_offset[i] = __ldcg(p.tb.offset + i);
+  __syncthreads();
+  auto seg_rows = [&](uint32_t a) { return t_offset[a + 1] - t_offset[a]; };
   Share sh;
   sh.U = picked * (uint32_t)p.col_tiles * (uint32_t)p.kblocks;
   sh.P = max(1u, min(gridDim.x, sh.U / kMinShare));
@@ -319,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load_tokens = [&](uint32_t st, uint32_t a, uint32_t kb) {
         const uint32_t dst = ring + st * p.stage_bytes + kW * kTileBytes, bar = full0 + 8 * st;
         if (DOWN) {
-          const int rows = seg_rows(p, a), r0 = __ldcg(p.tb.offset + a);
+          const int rows = seg_rows(a), r0 = t_offset[a];
           for (int r = 0; r < rows; r += 16) tma_load_3d(dst + r * 128, &tmX, (int32_t)kb * 64, r0 + r, 0, bar);
         } else {
           tma_load_3d(dst, &tmX, (int32_t)kb * 64, 0, 0, bar);
@@ -334,8 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (uint32_t u = ub; u < ue && ok;) {
         const Seg s = seg_at<DOWN>(p, picked, u, ue);
-        const int32_t e = __ldcg(p.tb.expert + s.a);
-        const uint32_t tok_bytes = DOWN ? (uint32_t)((seg_rows(p, s.a) + 15) & ~15) * 128u : (uint32_t)p.nt * 128u;
+        const int32_t e = t_expert[s.a];
+        const uint32_t tok_bytes = DOWN ? (uint32_t)((seg_rows(s.a) + 15) & ~15) * 128u : (uint32_t)p.nt * 128u;
         for (uint32_t kb = s.kb0; kb < s.kb1; ++kb) {
           if (DOWN && early && nearly == early) release_early();
           if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort, p.status, p.timeout_ns)) { ok = false; break; }
@@ -369,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t buf = seg & 1, aph = (seg >> 1) & 1;
         if (!mbar_wait(acce0 + 8 * buf, aph ^ 1, abort, p.status, p.timeout_ns)) break;
         tc_fence_after();
-        const uint32_t n = DOWN ? (uint32_t)((seg_rows(p, s.a) + 15) & ~15) : (uint32_t)p.nt;
+        const uint32_t n = DOWN ? (uint32_t)((seg_rows(s.a) + 15) & ~15) : (uint32_t)p.nt;
         const uint32_t idesc = p.idesc0 | ((n >> 3) << 17), d = tmem + buf * 256;
         for (uint32_t kb = s.kb0; kb < s.kb1; ++kb) {
           if (!mbar_wait(full0 + 8 * stage, phase, abort, p.status, p.timeout_ns)) { ok = false; break; }
@@ -411,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Seg s = seg_at<false>(p, picked, u, ue);
         const uint32_t buf = seg & 1, aph = (seg >> 1) & 1;
         const int64_t f = (int64_t)s.col * 128 + l;
-        const int r0 = __ldcg(p.tb.offset + s.a), rows = __ldcg(p.tb.offset + s.a + 1) - r0;
+        const int r0 = t_offset[s.a], rows = seg_rows(s.a);
         const uint4 mk = __ldcg(reinterpret_cast<const uint4*>(p.tb.mask) + s.a);
         const bool whole = s.kb0 == 0 && s.kb1 == (uint32_t)p.kblocks;
         // the share's first tile unless the share begins before the tile
@@ -446,16 +464,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!whole) {
           const uint32_t t0 = s.item * (uint32_t)p.kblocks;
           const uint32_t c0 = sh.owner(t0), c1 = sh.owner(t0 + (uint32_t)p.kblocks - 1);
-          if (last_to_arrive(p.count + s.item, (int)(c1 - c0 + 1), flag) && f < p.F) {
-            for (int j = 0; j < rows; ++j) {
-              float gv = 0.f, uv = 0.f;
-              for (uint32_t c = c0; c <= c1; ++c) {
-                const float* q = p.part + ((int64_t)(2 * c + (sh.begin(c) < t0 ? 1u : 0u)) * p.tokens + j) * 256 + l;
-                gv += __ldcg(q);
-                uv += __ldcg(q + 128);
-              }
-              const float h = p.gated ? activate(gv, p.act) * uv : activate(gv, p.act);
-              store16(p.out, (int64_t)(r0 + j) * p.ld + f, h, p.f16);
+          if (last_to_arrive(p.count + s.item, (int)(c1 - c0 + 1), flag)) {
+            const int64_t f4 = (int64_t)s.col * 128 + lane * 4;
+            for (int j = quad; j < rows; j += 4) {
+              const float4 gv = sum_shares(p.part + j * 256 + lane * 4, (int64_t)p.tokens * 256, sh, c0, c1, t0);
+              const float4 uv = sum_shares(p.part + j * 256 + 128 + lane * 4, (int64_t)p.tokens * 256, sh, c0, c1, t0);
+              const float g[4] = {gv.x, gv.y, gv.z, gv.w}, v[4] = {uv.x, uv.y, uv.z, uv.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (f4 + e < p.F)
+                  store16(p.out, (int64_t)(r0 + j) * p.ld + f4 + e, p.gated ? activate(g[e], p.act) * v[e] : activate(g[e], p.act),
+                          p.f16);
             }
           }
         }
@@ -474,13 +493,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t0 = s.item * per_tile, t1 = t0 + per_tile;
         if (u == ub || u == t0)
           for (int t = 0; t < p.tokens; ++t) acc[t * 128 + l] = 0.f;
-        const int r0 = __ldcg(p.tb.offset + s.a), rows = __ldcg(p.tb.offset + s.a + 1) - r0;
+        const int r0 = t_offset[s.a], rows = seg_rows(s.a);
+        int tok_n;                                             // lane j: token and weight of row j0 + j % 16
+        float wt_n;
+        auto load_rows = [&](int j0) {
+          const int mine = r0 + min(j0 + (lane & 15), rows - 1);
+          tok_n = __ldcg(p.tb.row_token + mine);
+          wt_n = __ldcg(p.tb.row_weight + mine);
+        };
+        load_rows(0);
         if (!epi_all(mbar_wait(accf0 + 8 * buf, aph, abort, p.status, p.timeout_ns))) break;
         tc_fence_after();
         for (int j0 = 0; j0 < rows; j0 += 16) {
-          const int mine = min(j0 + (lane & 15), rows - 1);
-          const int tok = __ldcg(p.tb.row_token + r0 + mine);
-          const float wt = __ldcg(p.tb.row_weight + r0 + mine);
+          const int tok = tok_n;
+          const float wt = wt_n;
+          if (j0 + 16 < rows) load_rows(j0 + 16);
           uint32_t v[16];
           tmem_ld16(tl + buf * 256 + j0, v);
           tmem_ld_wait();
@@ -502,12 +529,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* part = p.part + (int64_t)slot * p.tokens * 128 + l;
             for (int t = 0; t < p.tokens; ++t) part[t * 128] = acc[t * 128 + l];
             const uint32_t c0 = sh.owner(t0), c1 = sh.owner(t1 - 1);
-            if (last_to_arrive(p.count + s.item, (int)(c1 - c0 + 1), flag) && n < p.N) {
-              for (int t = 0; t < p.tokens; ++t) {
-                float v = 0.f;
-                for (uint32_t c = c0; c <= c1; ++c)
-                  v += __ldcg(p.part + ((int64_t)(2 * c + (sh.begin(c) < t0 ? 1u : 0u)) * p.tokens + t) * 128 + l);
-                store16(p.out, t * p.ld + n, v, p.f16);
+            if (last_to_arrive(p.count + s.item, (int)(c1 - c0 + 1), flag)) {
+              const int64_t n4 = (int64_t)s.col * 128 + lane * 4;
+              for (int t = quad; t < p.tokens; t += 4) {
+                const float4 o = sum_shares(p.part + t * 128 + lane * 4, (int64_t)p.tokens * 128, sh, c0, c1, t0);
+                const float v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (n4 + e < p.N) store16(p.out, t * p.ld + n4 + e, v[e], p.f16);
               }
             }
           }
@@ -654,7 +683,9 @@ mm_status launch_tc_moe(const MoeArgs& a, void* workspace, unsigned* status, cud
       q.ld = down ? a.N : l.h_ld;
       q.count = p.tb.count + (down ? l.picked * l.f_tiles : 0);
       q.stage_bytes = (down ? 1 : 2) * kTileBytes + p.nt * 128;
-      const int acc_bytes = down ? T * 128 * 4 : 0;
+      q.max_picked = (int)l.picked;
+      q.table_bytes = (int)((2 * l.picked + 1) * 4 + 15) / 16 * 16;
+      const int acc_bytes = q.table_bytes + (down ? T * 128 * 4 : 0);
       q.stages = (kSmemMax - 1024 - kCtrl - acc_bytes) / q.stage_bytes;
       if (q.stages > kMaxStages) q.stages = kMaxStages;
       const int smem = 1024 + q.stages * q.stage_bytes + kCtrl + acc_bytes;
