@@ -218,7 +218,11 @@ mm_status plan_lowrank(const mm_tensor* X, const mm_tensor* W, const mm_tensor* 
   return MM_OK;
 }
 
-size_t factor_bytes(const LowRankArgs& l) { return align256((size_t)l.M * (size_t)l.R * sizeof(float)); }
+// One factor's z [M, R] (or its shares, for few rows).
+size_t factor_bytes(const LowRankArgs& l) {
+  const size_t z = (size_t)l.M * (size_t)l.R * sizeof(float);
+  return align256(l.M <= kFewRows && l.dtype != MM_F32 ? lowrank_few_bytes(l) : z);
+}
 
 // Y = X W + Y for dense Y [M, N] that already holds the low-rank part.
 mm_status add_projection(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t K, const void* w,
@@ -267,6 +271,13 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
   if (!(l.status = device_status_ptr())) return MM_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* z = static_cast<float*>(workspace);
+  const LowRankFew f = {X->data, X->strides[0], X->strides[1], p.K, A->data, A->strides[0], A->strides[1], A->strides[2],
+                        B->data, B->strides[0], B->strides[1], B->strides[2], p.N, Y->data};
+  if (path_policy() != MM_PATH_SIMT && lowrank_few_supported(l, f)) {
+    if ((s = launch_lowrank_few(l, f, z, st)) != MM_OK) return s;
+    return add_projection(l, X->data, X->strides[0], X->strides[1], p.K, W->data, W->strides[0], W->strides[1], p.N,
+                          Y->data, st);
+  }
   if ((s = launch_lowrank_shrink(l, X->data, X->strides[0], X->strides[1], p.K, A->data, A->strides[0], A->strides[1],
                                  A->strides[2], z, st)) != MM_OK)
     return s;

@@ -116,6 +116,19 @@ mm_status launch_lowrank_outer(const LowRankArgs& l, const void* x, int64_t x_rs
                                const float* z, void* out, int64_t o_gs, int64_t o_cs, int64_t o_rs,
                                cudaStream_t stream);
 
+// Few rows of 16-bit types: both steps with vector reads, z's shares in zp.
+constexpr int64_t kFewRows = 256;
+struct LowRankFew {
+  const void* x; int64_t x_rs, x_cs, C;
+  const void* a; int64_t a_gs, a_cs, a_rs;     // [G, C, R]
+  const void* b; int64_t b_gs, b_rs, b_ns;     // [G, R, N]
+  int64_t N;
+  void* y;                                     // dense [M, N]
+};
+bool lowrank_few_supported(const LowRankArgs& l, const LowRankFew& f);
+size_t lowrank_few_bytes(const LowRankArgs& l);
+mm_status launch_lowrank_few(const LowRankArgs& l, const LowRankFew& f, float* zp, cudaStream_t stream);
+
 mm_status launch_simt_gemm(const GemmArgs& args, cudaStream_t stream);
 // Multiprocessors of the current device (cached per device).
 int sm_count_public();

@@ -82,6 +82,205 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// ------------------------------------------------------------------ few rows (16-bit types)
+//
+// A decode batch: each row has its own adapter, so the bound is reading the
+// adapters once.  Every row is cut into kSplit shares of c, one block each,
+// so that one row's adapter streams through kSplit SMs; a share's sums stay
+// apart in zp[share][m][r] and the expansion adds them in share order.
+// Rows of one adapter read it from L2 again, which costs less than sorting
+// rows while there are few of them (kFewRows).
+
+constexpr int kSplit = 8;
+constexpr int kFewThreads = 128;
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = to_f32(e[j]);
+}
+
+// a with r contiguous: a thread takes 8 ranks of every (128 / octets)-th c.
+template <typename T>
+__device__ __forceinline__ void shrink_share_r(const T* x, int64_t x_cs, const T* a, int64_t a_cs, int64_t c0,
+                                               int64_t c1, int oct, float (&acc)[8]) {
+  // lanes of an octet column: threads oct_id + i * oct
+  const int o = threadIdx.x % oct, step = kFewThreads / oct;
+  const int first = threadIdx.x / oct;
+  if (first >= step) return;
+  constexpr int kAhead = 8;
+  for (int64_t c = c0 + first; c < c1; c += (int64_t)step * kAhead) {
+    uint4 u[kAhead];
+    float xv[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t ci = c + (int64_t)i * step;
+      u[i] = make_uint4(0u, 0u, 0u, 0u);
+      xv[i] = 0.f;
+      if (ci < c1) {
+        u[i] = *reinterpret_cast<const uint4*>(a + ci * a_cs + o * 8);
+        xv[i] = to_f32(x[ci * x_cs]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (c + (int64_t)i * step >= c1) break;     // nothing was read: 0 * x must not make a NaN
+      float f[8];
+      unpack8<T>(u[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = __fmaf_rn(xv[i], f[j], acc[j]);
+    }
+  }
+}
+
+// Block (share, row): ranks in passes of 64 (a with r contiguous) or one rank
+// per warp at a time (a with c contiguous).
+template <typename T, bool CC>
+__global__ void __launch_bounds__(kFewThreads)
+    shrink_rows_kernel(const LowRankArgs l, const T* x, int64_t x_rs, int64_t x_cs, int64_t C, const T* a, int64_t a_gs,
+                       int64_t a_ld, float* zp) {
+  pdl_begin();
+  __shared__ float part[kFewThreads][9];
+  const int64_t m = blockIdx.y;
+  const int share = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t g = adapter_of(l, m);
+  float* z = zp + ((int64_t)share * l.M + m) * l.R;
+  if (g < 0) {
+    for (int64_t r = threadIdx.x; r < l.R; r += kFewThreads) z[r] = 0.f;
+    return;
+  }
+  const int64_t per = ((C + kSplit - 1) / kSplit + 7) / 8 * 8;
+  const int64_t c0 = min(C, share * per), c1 = min(C, c0 + per);
+  const float scale = l.scales ? l.scales[g * l.scales_s] : 1.f;
+  const T* xr = x + m * x_rs;
+  const T* ag = a + g * a_gs;
+  if constexpr (!CC) {
+    for (int64_t r0 = 0; r0 < l.R; r0 += 64) {
+      const int oct = (int)min((int64_t)8, (l.R - r0) / 8);     // R is a multiple of 8
+      float acc[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+      shrink_share_r<T>(xr, x_cs, ag + r0, a_ld, c0, c1, oct, acc);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) part[threadIdx.x][j] = acc[j];
+      __syncthreads();
+      const int step = kFewThreads / oct;
+      if (threadIdx.x < oct * 8) {
+        const int o = threadIdx.x / 8, j = threadIdx.x % 8;
+        float v = 0.f;
+        for (int i = 0; i < step; ++i) v += part[o + i * oct][j];
+        z[r0 + threadIdx.x] = v * scale;
+      }
+    }
+  } else {
+    // four ranks at a time share the reads of x
+    for (int64_t r0 = warp * 4; r0 < l.R; r0 += 16) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int64_t c = c0 + lane * 8; c < c1; c += 256) {
+        uint4 u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = *reinterpret_cast<const uint4*>(ag + min(r0 + j, l.R - 1) * a_ld + c);
+        float xv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xv[i] = to_f32(xr[(c + i) * x_cs]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float f[8];
+          unpack8<T>(u[j], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[j] = __fmaf_rn(xv[i], f[i], acc[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+        if (lane == j && r0 + j < l.R) z[r0 + j] = acc[j] * scale;
+      }
+    }
+  }
+}
+
+// Block (1024 columns, row): a thread takes 8 columns (b with n contiguous) or
+// walks columns with r contiguous; the row's z is the sum of its shares.
+constexpr int kExpandMaxR = 1024;
+
+template <typename T, bool NC>
+__global__ void __launch_bounds__(kFewThreads)
+    expand_rows_kernel(const LowRankArgs l, const float* zp, const T* b, int64_t b_gs, int64_t b_ld, int64_t N, T* y,
+                       int yvec) {
+  pdl_begin();
+  __shared__ float zs[kExpandMaxR];
+  const int64_t m = blockIdx.y;
+  const int64_t g = adapter_of(l, m);
+  const int R = (int)l.R;
+  for (int r = threadIdx.x; r < R; r += kFewThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int s = 0; s < kSplit; ++s) v += zp[((int64_t)s * l.M + m) * R + r];
+    zs[r] = v;
+  }
+  __syncthreads();
+  const T* bg = b + (g < 0 ? 0 : g) * b_gs;
+  T* yr = y + m * N;
+  if constexpr (NC) {
+    const int64_t n = ((int64_t)blockIdx.x * kFewThreads + threadIdx.x) * 8;
+    if (n >= N) return;
+    float acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    if (g >= 0) {
+      constexpr int kAhead = 8;
+      for (int r0 = 0; r0 < R; r0 += kAhead) {
+        uint4 u[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) u[i] = *reinterpret_cast<const uint4*>(bg + (int64_t)min(r0 + i, R - 1) * b_ld + n);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (r0 + i >= R) break;
+          float f[8];
+          unpack8<T>(u[i], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = __fmaf_rn(zs[r0 + i], f[j], acc[j]);
+        }
+      }
+    }
+    uint4 o;
+    T* e = reinterpret_cast<T*>(&o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = from_f32<T>(acc[j]);
+    if (yvec) {
+      *reinterpret_cast<uint4*>(yr + n) = o;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n + j < N) yr[n + j] = e[j];
+    }
+  } else {
+    for (int64_t n = (int64_t)blockIdx.x * kFewThreads * 8 + threadIdx.x;
+         n < min(N, ((int64_t)blockIdx.x + 1) * kFewThreads * 8); n += kFewThreads) {
+      float acc = 0.f;
+      if (g >= 0) {
+        const T* bn = bg + n * b_ld;
+#pragma unroll 4
+        for (int r0 = 0; r0 < R; r0 += 8) {                    // R is a multiple of 8
+          float f[8];
+          unpack8<T>(*reinterpret_cast<const uint4*>(bn + r0), f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc = __fmaf_rn(zs[r0 + j], f[j], acc);
+        }
+      }
+      yr[n] = from_f32<T>(acc);
+    }
+  }
+}
+
+bool vec8(const void* p, int64_t gs, int64_t ld) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && gs % 8 == 0 && ld % 8 == 0;
+}
+
 constexpr int kOuterR = 16;
 
 template <typename T>
@@ -137,7 +336,52 @@ mm_status outer_typed(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t
                     static_cast<T*>(out), o_gs, o_cs, o_rs) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
+template <typename T>
+mm_status few_typed(const LowRankArgs& l, const LowRankFew& f, float* zp, cudaStream_t stream) {
+  const T* x = static_cast<const T*>(f.x);
+  const T* a = static_cast<const T*>(f.a);
+  const T* b = static_cast<const T*>(f.b);
+  const dim3 gs(kSplit, (unsigned)l.M);
+  cudaError_t e;
+  if (f.a_rs == 1)
+    e = launch_pdl(shrink_rows_kernel<T, false>, gs, dim3(kFewThreads), 0, stream, l, x, f.x_rs, f.x_cs, f.C, a, f.a_gs,
+                   f.a_cs, zp);
+  else
+    e = launch_pdl(shrink_rows_kernel<T, true>, gs, dim3(kFewThreads), 0, stream, l, x, f.x_rs, f.x_cs, f.C, a, f.a_gs,
+                   f.a_rs, zp);
+  if (e != cudaSuccess) return MM_ERR_CUDA;
+  const dim3 ge((unsigned)((f.N + kFewThreads * 8 - 1) / (kFewThreads * 8)), (unsigned)l.M);
+  T* y = static_cast<T*>(f.y);
+  const int yvec = f.N % 8 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
+  if (f.b_ns == 1)
+    e = launch_pdl(expand_rows_kernel<T, true>, ge, dim3(kFewThreads), 0, stream, l, (const float*)zp, b, f.b_gs, f.b_rs,
+                   f.N, y, yvec);
+  else
+    e = launch_pdl(expand_rows_kernel<T, false>, ge, dim3(kFewThreads), 0, stream, l, (const float*)zp, b, f.b_gs, f.b_ns,
+                   f.N, y, yvec);
+  return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+}
+
 }  // namespace
+
+// 16-byte reads of a along whichever of its dimensions has unit stride, and of
+// b likewise; whole octets of that dimension (c and n rows are read past their
+// end by no one: C and N are multiples of 8).
+bool lowrank_few_supported(const LowRankArgs& l, const LowRankFew& f) {
+  if (l.dtype != MM_BF16 && l.dtype != MM_F16) return false;
+  if (l.M < 1 || l.M > kFewRows || l.R < 1 || l.R > kExpandMaxR || l.G < 1 || f.C < 1 || f.N < 1) return false;
+  const bool a_r = f.a_rs == 1 && l.R % 8 == 0 && vec8(f.a, f.a_gs, f.a_cs);
+  const bool a_c = f.a_rs != 1 && f.a_cs == 1 && f.C % 8 == 0 && vec8(f.a, f.a_gs, f.a_rs);
+  const bool b_n = f.b_ns == 1 && f.N % 8 == 0 && vec8(f.b, f.b_gs, f.b_rs);
+  const bool b_r = f.b_ns != 1 && f.b_rs == 1 && l.R % 8 == 0 && vec8(f.b, f.b_gs, f.b_ns);
+  return (a_r || a_c) && (b_n || b_r);
+}
+
+size_t lowrank_few_bytes(const LowRankArgs& l) { return (size_t)kSplit * (size_t)l.M * (size_t)l.R * sizeof(float); }
+
+mm_status launch_lowrank_few(const LowRankArgs& l, const LowRankFew& f, float* zp, cudaStream_t stream) {
+  return l.dtype == MM_F16 ? few_typed<__half>(l, f, zp, stream) : few_typed<__nv_bfloat16>(l, f, zp, stream);
+}
 
 #define QG_BY_TYPE(fn, ...)                                      \
   switch (l.dtype) {                                             \
