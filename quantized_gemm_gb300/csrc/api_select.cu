@@ -5,6 +5,7 @@
 
 #include "api_internal.h"
 #include "kernels.h"
+#include "lowrank.cuh"
 #include "tc.h"
 
 using namespace qg;
@@ -224,6 +225,33 @@ size_t factor_bytes(const LowRankArgs& l) {
   return align256(l.M <= kFewRows && l.dtype != MM_F32 ? lowrank_few_bytes(l) : z);
 }
 
+// Workspace of the many-row gradient kernels.
+struct GradLayout {
+  int64_t zt_ld;
+  size_t v, u, vt, ut, row, offset, chunk, part, sums, total;
+};
+GradLayout grad_layout(const LowRankPlan& p) {
+  const LowRankArgs& l = p.l;
+  GradLayout w;
+  w.zt_ld = (l.R + 7) / 8 * 8;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o = align256(o + bytes); return at; };
+  const size_t z = (size_t)l.M * (size_t)l.R * 4, zt = (size_t)l.M * (size_t)w.zt_ld * 2;
+  w.v = take(z); w.u = take(z); w.vt = take(zt); w.ut = take(zt);
+  w.row = take((size_t)l.M * 4);
+  w.offset = take((size_t)(l.G + 1) * 4);
+  w.chunk = take((size_t)(l.G + 1) * 4);
+  w.part = take((size_t)l.G * 4);
+  w.sums = take((size_t)lowrank_max_parts(l) * (size_t)(p.K > p.N ? p.K : p.N) * (size_t)l.R * 4);
+  w.total = o;
+  return w;
+}
+// Independent of the operands' layout, so that the workspace query needs none of it.
+bool many_rows(const LowRankArgs& l) {
+  return path_policy() != MM_PATH_SIMT && (l.dtype == MM_BF16 || l.dtype == MM_F16) && l.M >= 1 && l.R >= 1 &&
+         lowrank_sort_supported(l);
+}
+
 // Y = X W + Y for dense Y [M, N] that already holds the low-rank part.
 mm_status add_projection(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t K, const void* w,
                          int64_t w_rs, int64_t w_cs, int64_t N, void* y, cudaStream_t st) {
@@ -295,6 +323,10 @@ mm_status mm_lowrank_matmul_grad_workspace_size(const mm_tensor* X, const mm_ten
   const mm_status s = plan_lowrank(X, W, A, B, nullptr, nullptr, &p);
   if (s != MM_OK) return s;
   *bytes = 2 * factor_bytes(p.l);
+  if (many_rows(p.l)) {
+    const size_t need = grad_layout(p).total;
+    if (need > *bytes) *bytes = need;
+  }
   return MM_OK;
 }
 
@@ -321,6 +353,37 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
   float* v = static_cast<float*>(workspace);
   float* u = reinterpret_cast<float*>(static_cast<char*>(workspace) + factor_bytes(l));
   s = finish(MM_OK, MM_PATH_NONE);
+  if (many_rows(l) && K >= 1 && N >= 1 &&
+      lowrank_shrink_tiles_supported(l, dY->data, dY->strides[0], dY->strides[1], N, B->strides[2], B->strides[1]) &&
+      lowrank_shrink_tiles_supported(l, X->data, X->strides[0], X->strides[1], K, A->strides[1], A->strides[2])) {
+    const GradLayout w = grad_layout(p);
+    if (!workspace_ok(workspace, workspace_bytes, w.total)) return MM_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    float* zv = reinterpret_cast<float*>(ws + w.v);
+    const AdapterRows t = {reinterpret_cast<int32_t*>(ws + w.row), reinterpret_cast<int32_t*>(ws + w.offset),
+                           reinterpret_cast<int32_t*>(ws + w.chunk), reinterpret_cast<int32_t*>(ws + w.part)};
+    float* sums = reinterpret_cast<float*>(ws + w.sums);
+    if (dX || dA)
+      s = launch_lowrank_shrink_tiles(l, dY->data, dY->strides[0], N, B->data, B->strides[0], B->strides[2],
+                                      B->strides[1], zv, ws + w.vt, w.zt_ld, st);
+    if (s == MM_OK && dB)
+      s = launch_lowrank_shrink_tiles(l, X->data, X->strides[0], K, A->data, A->strides[0], A->strides[1],
+                                      A->strides[2], reinterpret_cast<float*>(ws + w.u), ws + w.ut, w.zt_ld, st);
+    if (s == MM_OK && (dA || dB)) s = launch_lowrank_sort(l, t, st);
+    if (s == MM_OK && dA)
+      s = launch_lowrank_outer_tiles(l, t, X->data, X->strides[0], K, ws + w.vt, w.zt_ld, dA->data, K * l.R, l.R, 1,
+                                     sums, st);
+    if (s == MM_OK && dB)
+      s = launch_lowrank_outer_tiles(l, t, dY->data, dY->strides[0], N, ws + w.ut, w.zt_ld, dB->data, l.R * N, 1, N,
+                                     sums, st);
+    if (s == MM_OK && dX) {
+      s = launch_lowrank_expand(l, zv, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
+      if (s == MM_OK)
+        s = add_projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1], W->strides[0], K,
+                           dX->data, st);
+    }
+    return s;
+  }
   if (dX || dA)
     s = launch_lowrank_shrink(l, dY->data, dY->strides[0], dY->strides[1], N, B->data, B->strides[0], B->strides[2],
                               B->strides[1], v, st);

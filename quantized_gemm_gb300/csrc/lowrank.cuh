@@ -1,0 +1,41 @@
+// Launchers of the many-row kernels of the low-rank adapters (lowrank_tc.cu).
+#pragma once
+
+#include <type_traits>
+
+#include "kernels.h"
+
+namespace qg {
+
+constexpr int kChunkRows = 512;            // rows of one adapter that one block sums
+constexpr int64_t kSortAdapters = 1024;    // adapters that the sort's counters hold (shared memory)
+
+// Rows in adapter order (device tables in the workspace).
+struct AdapterRows {
+  int32_t* row;       // [M] rows that have an adapter
+  int32_t* offset;    // [G + 1]
+  int32_t* chunk;     // [G + 1] first chunk of kChunkRows rows
+  int32_t* part;      // [G] first partial sum, counting the adapters of several chunks only
+};
+// More chunks than this cannot occur.
+inline int64_t lowrank_max_chunks(const LowRankArgs& l) {
+  return l.M / kChunkRows + (l.G < l.M ? l.G : l.M);
+}
+// Chunks of adapters with several: each such adapter has more than kChunkRows rows.
+inline int64_t lowrank_max_parts(const LowRankArgs& l) { return 2 * (l.M / kChunkRows); }
+
+// z [M, R] (fp32) and zt [M, zt_ld] (T, zeros past R), both scaled.
+bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
+                                    int64_t a_cs, int64_t a_rs);
+mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a,
+                                      int64_t a_gs, int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld,
+                                      cudaStream_t stream);
+bool lowrank_sort_supported(const LowRankArgs& l);
+mm_status launch_lowrank_sort(const LowRankArgs& l, const AdapterRows& t, cudaStream_t stream);
+// out[g, c, r] from x (16-byte aligned rows) and zt; part holds
+// lowrank_max_parts * C * R floats.
+mm_status launch_lowrank_outer_tiles(const LowRankArgs& l, const AdapterRows& t, const void* x, int64_t x_rs, int64_t C,
+                                     const void* zt, int64_t zt_ld, void* out, int64_t o_gs, int64_t o_cs, int64_t o_rs,
+                                     float* part, cudaStream_t stream);
+
+}  // namespace qg

@@ -1,0 +1,481 @@
+// Per-row low-rank adapters for many rows (16-bit types): the narrow products
+// on mma.sync tensor instructions.
+//
+// These products are N = R wide (a rank, 4 to 128 or so) and read one large
+// matrix once: their bound is memory, at 2 R operations per 2 bytes read, so
+// the warp-level instructions are enough and their register operands take any
+// row pattern.
+//
+//   shrink   z[m, r]      = s_g sum_c x[m, c] a[g, c, r]
+//   outer    out[g, c, r] = sum over the rows m of adapter g of x[m, c] z[m, r]
+#include <cstring>
+
+#include "lowrank.cuh"
+
+namespace qg {
+
+namespace {
+
+// ------------------------------------------------------------------ building blocks
+
+__device__ __forceinline__ uint32_t shared_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x2(uint32_t (&r)[2], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x2_t(uint32_t (&r)[2], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// Asynchronous copy of 16, 8 or 4 bytes, of which the first `valid` come from
+// src and the rest are zeros.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int valid) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// `rows` rows of `len` elements (zeros past `rows_ok` rows and `len_ok`
+// elements) into shared memory with `pitch` bytes a row, `per` elements a
+// copy (8, 4 or 2; 1: plain loads).  len_ok may end inside a copy.
+template <typename T>
+__device__ __forceinline__ void load_block(uint32_t dst, int pitch, const T* src, int64_t ld, int rows, int rows_ok,
+                                           int len, int len_ok, int per, int tid, int threads) {
+  const int n = (len + per - 1) / per;
+  for (int i = tid; i < rows * n; i += threads) {
+    const int r = i / n, c = (i - r * n) * per;
+    const int ok = r < rows_ok ? max(0, min(per, len_ok - c)) : 0;
+    const T* s = ok ? src + (int64_t)r * ld + c : src;
+    const uint32_t d = dst + (uint32_t)(r * pitch + c * 2);
+    if (per == 8) cp_async<16>(d, s, ok * 2);
+    else if (per == 4) cp_async<8>(d, s, ok * 2);
+    else if (per == 2) cp_async<4>(d, s, ok * 2);
+    else {
+      const uint16_t v = ok ? *reinterpret_cast<const uint16_t*>(s) : (uint16_t)0;
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(d), "h"(v) : "memory");
+    }
+  }
+}
+
+// ------------------------------------------------------------------ shrink
+
+// A block takes 32 rows x 64 ranks.  Four pairs of warps split c (64 at a
+// time, in turn), each pair with its own 3-stage ring, so that a block keeps
+// four loads streams in flight; the pairs' sums meet in shared memory.  The
+// tile is multiplied once per adapter that its rows name (rows of a request
+// are neighbours, so one or two); each pass keeps its own adapter's rows.
+constexpr int kShRows = 32, kShK = 64, kShStages = 3, kShPairs = 4, kShThreads = 256;
+constexpr int kShXPitch = kShK * 2 + 16;
+constexpr int kShXBytes = kShRows * kShXPitch;
+
+__host__ __device__ constexpr int shrink_a_bytes(bool ck, int rc) {
+  return ck ? (rc + 7) / 8 * 8 * kShXPitch : kShK * ((rc + 7) / 8 * 16 + 16);
+}
+
+template <typename T, bool CK>
+__global__ void __launch_bounds__(kShThreads)
+    shrink_tiles_kernel(const LowRankArgs l, const T* x, int64_t x_rs, int64_t C, const T* a, int64_t a_gs, int64_t a_ld,
+                        int per, float* z, T* zt, int64_t zt_ld) {
+  pdl_begin();
+  extern __shared__ __align__(16) uint8_t sm[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pair = warp >> 1, rg = warp & 1;
+  const int64_t m0 = (int64_t)blockIdx.x * kShRows;
+  const int r0 = blockIdx.y * 64, rc = (int)min((int64_t)64, l.R - r0), nt = (rc + 7) / 8;
+  const int rows = (int)min((int64_t)kShRows, l.M - m0);
+  const int a_bytes = shrink_a_bytes(CK, rc), stage = kShXBytes + a_bytes;
+  const int a_pitch = CK ? kShXPitch : nt * 16 + 16;
+  const uint32_t ring = shared_u32(sm) + (uint32_t)(pair * kShStages * stage);
+  float* red = reinterpret_cast<float*>(sm);             // [pairs][32][68], after the sums
+  constexpr int kRedPitch = 68;
+  const int ptid = tid & 63;
+  const int nk = (int)((C + kShK - 1) / kShK);
+  const int mine = nk > pair ? (nk - pair + kShPairs - 1) / kShPairs : 0;   // this pair's k-blocks
+  auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory"); };
+
+  int g_lane = -1;
+  if (lane < rows) {
+    const int64_t g = load_index(l.idx, (m0 + lane) * l.idx_s, l.ind64);
+    if (g >= 0 && g < l.G) g_lane = (int)g;
+    else if (g != -1) atomicOr(l.status, kStatusIndexRange);
+  }
+  unsigned left = __ballot_sync(0xffffffffu, g_lane >= 0);
+  const unsigned none = ~left;
+  // rows without adapter
+  for (int i = tid; i < rows * rc; i += kShThreads) {
+    const int r = i / rc, c = i - r * rc;
+    if ((none >> r) & 1u) z[(m0 + r) * l.R + r0 + c] = 0.f;
+  }
+  for (int i = tid; i < rows * nt * 8; i += kShThreads) {
+    const int r = i / (nt * 8), c = i - r * (nt * 8);
+    if (((none >> r) & 1u) && r0 + c < zt_ld) zt[(m0 + r) * zt_ld + r0 + c] = from_f32<T>(0.f);
+  }
+  while (left) {
+    const int g = __shfl_sync(0xffffffffu, g_lane, __ffs(left) - 1);
+    const unsigned sel = __ballot_sync(0xffffffffu, g_lane == g);
+    left &= ~sel;
+    const T* ag = a + (int64_t)g * a_gs;
+    auto load = [&](int i) {
+      const int64_t c0 = ((int64_t)i * kShPairs + pair) * kShK;
+      const int cn = (int)min((int64_t)kShK, C - c0);
+      const uint32_t s = ring + (uint32_t)((i % kShStages) * stage);
+      load_block<T>(s, kShXPitch, x + m0 * x_rs + c0, x_rs, kShRows, rows, kShK, cn, 8, ptid, 64);
+      if constexpr (CK)
+        load_block<T>(s + kShXBytes, a_pitch, ag + (int64_t)r0 * a_ld + c0, a_ld, rc, rc, kShK, cn, per, ptid, 64);
+      else
+        load_block<T>(s + kShXBytes, a_pitch, ag + c0 * a_ld + r0, a_ld, kShK, cn, rc, rc, per, ptid, 64);
+    };
+    float acc[8][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kShStages - 1; ++i) {
+      if (i < mine) load(i);
+      cp_commit();
+    }
+    for (int i = 0; i < mine; ++i) {
+      cp_wait<kShStages - 2>();
+      pair_sync();                       // block i has landed, and block i - 1 has been used
+      if (i + kShStages - 1 < mine) load(i + kShStages - 1);
+      cp_commit();
+      const uint32_t s = ring + (uint32_t)((i % kShStages) * stage);
+#pragma unroll
+      for (int k = 0; k < kShK / 16; ++k) {
+        uint32_t fa[4];
+        ldsm_x4(fa, s + (uint32_t)((rg * 16 + (lane & 15)) * kShXPitch + k * 32 + (lane >> 4) * 16));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j >= nt) break;
+          uint32_t fb[2];
+          if constexpr (CK)
+            ldsm_x2(fb, s + kShXBytes + (uint32_t)((j * 8 + (lane & 7)) * a_pitch + k * 32 + ((lane >> 3) & 1) * 16));
+          else
+            ldsm_x2_t(fb, s + kShXBytes + (uint32_t)((k * 16 + (lane & 15)) * a_pitch + j * 16));
+          mma16816<T>(acc[j], fa, fb);
+        }
+      }
+    }
+    cp_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= nt) break;
+      float* q = red + (pair * kShRows + rg * 16 + (lane >> 2)) * kRedPitch + j * 8 + (lane & 3) * 2;
+      q[0] = acc[j][0]; q[1] = acc[j][1];
+      q[8 * kRedPitch] = acc[j][2]; q[8 * kRedPitch + 1] = acc[j][3];
+    }
+    __syncthreads();
+    const float scale = l.scales ? l.scales[g * l.scales_s] : 1.f;
+    for (int i = tid; i < rows * nt * 8; i += kShThreads) {
+      const int r = i / (nt * 8), c = i - r * (nt * 8);
+      if (!((sel >> r) & 1u)) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int q = 0; q < kShPairs; ++q) v += red[(q * kShRows + r) * kRedPitch + c];
+      v = c < rc ? v * scale : 0.f;
+      if (c < rc) z[(m0 + r) * l.R + r0 + c] = v;
+      if (r0 + c < zt_ld) zt[(m0 + r) * zt_ld + r0 + c] = from_f32<T>(v);
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ rows in adapter order
+
+// One block, a stable counting sort: warp w counts and then places the w-th
+// 32nd of the rows, in order, so rows keep their order within an adapter and
+// sums over them do not depend on timing.
+constexpr int kSortThreads = 1024;
+
+__global__ void __launch_bounds__(kSortThreads) adapter_sort_kernel(const LowRankArgs l, const AdapterRows t) {
+  pdl_begin();
+  extern __shared__ int32_t cnt[];                  // [32 warps][G]
+  __shared__ int32_t wtot[32][3];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = (int)l.G;
+  for (int i = tid; i < 32 * G; i += kSortThreads) cnt[i] = 0;
+  __syncthreads();
+  const int64_t per = ((l.M + 31) / 32 + 31) / 32 * 32, lo = warp * per, hi = min(l.M, lo + per);
+  int32_t* mine = cnt + warp * G;
+  auto adapter = [&](int64_t m) {
+    if (m >= hi) return -1;
+    const int64_t g = load_index(l.idx, m * l.idx_s, l.ind64);
+    return g >= 0 && g < l.G ? (int)g : -1;
+  };
+  for (int64_t b = lo; b < hi; b += 32) {
+    const int g = adapter(b + lane);
+    const unsigned same = __match_any_sync(0xffffffffu, g);
+    if (g >= 0 && lane == __ffs(same) - 1) mine[g] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  // Exclusive sums over (adapter, warp), adapter-major, a range of adapters per thread.
+  const int gp = (G + kSortThreads - 1) / kSortThreads, g0 = min(G, tid * gp), g1 = min(G, g0 + gp);
+  int rows = 0, chunks = 0, parts = 0;
+  for (int g = g0; g < g1; ++g) {
+    int c = 0;
+    for (int w = 0; w < 32; ++w) c += cnt[w * G + g];
+    const int k = (c + kChunkRows - 1) / kChunkRows;
+    rows += c;
+    chunks += k;
+    parts += k > 1 ? k : 0;
+  }
+  int ir = rows, ic = chunks, ip = parts;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int ur = __shfl_up_sync(0xffffffffu, ir, o), uc = __shfl_up_sync(0xffffffffu, ic, o);
+    const int up = __shfl_up_sync(0xffffffffu, ip, o);
+    if (lane >= o) { ir += ur; ic += uc; ip += up; }
+  }
+  if (lane == 31) { wtot[warp][0] = ir; wtot[warp][1] = ic; wtot[warp][2] = ip; }
+  __syncthreads();
+  int pr = ir - rows, pc = ic - chunks, pp = ip - parts;
+  for (int w = 0; w < warp; ++w) { pr += wtot[w][0]; pc += wtot[w][1]; pp += wtot[w][2]; }
+  for (int g = g0; g < g1; ++g) {
+    t.offset[g] = pr;
+    t.chunk[g] = pc;
+    t.part[g] = pp;
+    const int first = pr;
+    for (int w = 0; w < 32; ++w) {
+      const int c = cnt[w * G + g];
+      cnt[w * G + g] = pr;
+      pr += c;
+    }
+    const int k = (pr - first + kChunkRows - 1) / kChunkRows;
+    pc += k;
+    pp += k > 1 ? k : 0;
+  }
+  if (tid == kSortThreads - 1) { t.offset[G] = pr; t.chunk[G] = pc; }
+  __syncthreads();
+  for (int64_t b = lo; b < hi; b += 32) {
+    const int g = adapter(b + lane);
+    const unsigned same = __match_any_sync(0xffffffffu, g);
+    const int at = g >= 0 ? mine[g] + __popc(same & ((1u << lane) - 1u)) : 0;
+    __syncwarp();
+    if (g >= 0) {
+      t.row[at] = (int32_t)(b + lane);
+      if (lane == __ffs(same) - 1) mine[g] += __popc(same);
+    }
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------------ outer
+
+// A block sums one chunk (kChunkRows rows of one adapter) for 128 columns of x
+// and 64 ranks: out[c, r] += x[m, c] z[m, r], 32 rows a step in a 3-stage
+// ring.  An adapter of one chunk is written at once; the others' chunks are
+// added, in order, by outer_sum_kernel.
+constexpr int kOutC = 128, kOutRows = 32, kOutStages = 3, kOutThreads = 256;
+constexpr int kOutXPitch = kOutC * 2 + 16, kOutZPitch = 64 * 2 + 16;
+constexpr int kOutStage = kOutRows * (kOutXPitch + kOutZPitch);
+
+template <typename T>
+__global__ void __launch_bounds__(kOutThreads)
+    outer_tiles_kernel(const LowRankArgs l, const AdapterRows t, const T* x, int64_t x_rs, int64_t C, const T* zt,
+                       int64_t zt_ld, T* out, int64_t o_gs, int64_t o_cs, int64_t o_rs, float* part) {
+  pdl_begin();
+  extern __shared__ __align__(16) uint8_t sm[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = (int)l.G;
+  const int chunk = blockIdx.y;
+  if (chunk >= __ldcg(t.chunk + G)) return;
+  int lo = 0, hi = G;                               // the adapter with chunk[g] <= chunk < chunk[g + 1]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldcg(t.chunk + mid) <= chunk) lo = mid;
+    else hi = mid;
+  }
+  const int g = lo, ch0 = __ldcg(t.chunk + g);
+  const int first = __ldcg(t.offset + g) + (chunk - ch0) * kChunkRows;
+  const int n = min(kChunkRows, __ldcg(t.offset + g + 1) - first);
+  const int64_t c0 = (int64_t)blockIdx.x * kOutC;
+  const int cn = (int)min((int64_t)kOutC, C - c0);
+  const int r0 = blockIdx.z * 64, rc = (int)min((int64_t)64, l.R - r0), nt = (rc + 7) / 8;
+  const uint32_t ring = shared_u32(sm);
+  const int steps = (n + kOutRows - 1) / kOutRows;
+  auto load = [&](int i) {
+    const uint32_t s = ring + (uint32_t)((i % kOutStages) * kOutStage);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {                   // 32 rows x 16 pieces of x
+      const int e = tid + q * kOutThreads, r = e >> 4, c = (e & 15) * 8;
+      const int at = i * kOutRows + r;
+      const int ok = at < n ? max(0, min(8, cn - c)) : 0;
+      const T* src = ok ? x + (int64_t)__ldcg(t.row + first + at) * x_rs + c0 + c : x;
+      cp_async<16>(s + (uint32_t)(r * kOutXPitch + c * 2), src, ok * 2);
+    }
+    const int r = tid >> 3, c = (tid & 7) * 8;      // 32 rows x 8 pieces of z
+    const int at = i * kOutRows + r;
+    if (c < nt * 8) {
+      const bool ok = at < n;
+      const T* src = ok ? zt + (int64_t)__ldcg(t.row + first + at) * zt_ld + r0 + c : zt;
+      cp_async<16>(s + (uint32_t)(kOutRows * kOutXPitch + r * kOutZPitch + c * 2), src, ok ? 16 : 0);
+    }
+  };
+  float acc[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kOutStages - 1; ++i) {
+    if (i < steps) load(i);
+    cp_commit();
+  }
+  for (int i = 0; i < steps; ++i) {
+    cp_wait<kOutStages - 2>();
+    __syncthreads();
+    if (i + kOutStages - 1 < steps) load(i + kOutStages - 1);
+    cp_commit();
+    const uint32_t s = ring + (uint32_t)((i % kOutStages) * kOutStage);
+#pragma unroll
+    for (int k = 0; k < kOutRows / 16; ++k) {
+      uint32_t fa[4];
+      ldsm_x4_t(fa, s + (uint32_t)((k * 16 + (lane & 7) + ((lane >> 4) & 1) * 8) * kOutXPitch + warp * 32 +
+                                   ((lane >> 3) & 1) * 16));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j >= nt) break;
+        uint32_t fb[2];
+        ldsm_x2_t(fb, s + (uint32_t)(kOutRows * kOutXPitch + (k * 16 + (lane & 15)) * kOutZPitch + j * 16));
+        mma16816<T>(acc[j], fa, fb);
+      }
+    }
+  }
+  const bool whole = __ldcg(t.chunk + g + 1) - ch0 == 1;
+  float* mine = part + (int64_t)(__ldcg(t.part + g) + chunk - ch0) * C * l.R;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j >= nt) break;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t c = c0 + warp * 16 + (lane >> 2) + (e >> 1) * 8;
+      const int r = r0 + j * 8 + (lane & 3) * 2 + (e & 1);
+      if (c >= C || r >= l.R) continue;
+      if (whole) out[g * o_gs + c * o_cs + r * o_rs] = from_f32<T>(acc[j][e]);
+      else mine[c * o_cs + r * o_rs] = acc[j][e];
+    }
+  }
+}
+
+// The adapters with several chunks (their sum) or none (zeros); element e of
+// an adapter's [C, R] in the output's own order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    outer_sum_kernel(const LowRankArgs l, const AdapterRows t, int64_t C, T* out, const float* part) {
+  pdl_begin();
+  const int64_t n = C * l.R;
+  for (int g = blockIdx.y; g < l.G; g += gridDim.y) {
+    const int k = __ldcg(t.chunk + g + 1) - __ldcg(t.chunk + g);
+    if (k == 1) continue;
+    const float* src = part + (int64_t)__ldcg(t.part + g) * n;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+      float v = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < k; ++c) v += __ldcg(src + (int64_t)c * n + e);
+      out[(int64_t)g * n + e] = from_f32<T>(v);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+bool rows16(const void* x, int64_t rs, int64_t cs, int64_t rows) {
+  return cs == 1 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && (rs % 8 == 0 || rows == 1);
+}
+
+template <typename T>
+mm_status shrink_launch(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a, int64_t a_gs,
+                        int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld, cudaStream_t stream) {
+  const bool ck = a_rs != 1;            // c is a's unit-stride dimension
+  const int64_t ld = ck ? a_rs : a_cs;
+  int per = 8;                          // elements per copy of a, by its alignment
+  while (per > 1 && (reinterpret_cast<uintptr_t>(a) % (per * 2) || (l.G > 1 && a_gs % per) || ld % per)) per >>= 1;
+  const int rc = (int)(l.R < 64 ? l.R : 64);
+  int smem = kShPairs * kShStages * (kShXBytes + shrink_a_bytes(ck, rc));
+  const int red = kShPairs * kShRows * 68 * 4;
+  if (smem < red) smem = red;
+  const dim3 grid((unsigned)((l.M + kShRows - 1) / kShRows), (unsigned)((l.R + 63) / 64));
+  const auto kernel = ck ? shrink_tiles_kernel<T, true> : shrink_tiles_kernel<T, false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
+    return MM_ERR_CUDA;
+  return launch_pdl(kernel, grid, dim3(kShThreads), (size_t)smem, stream, l, static_cast<const T*>(x), x_rs, C,
+                    static_cast<const T*>(a), a_gs, ld, per, z, static_cast<T*>(zt), zt_ld) == cudaSuccess ? MM_OK
+                                                                                                          : MM_ERR_CUDA;
+}
+
+template <typename T>
+mm_status outer_launch(const LowRankArgs& l, const AdapterRows& t, const void* x, int64_t x_rs, int64_t C, const void* zt,
+                       int64_t zt_ld, void* out, int64_t o_gs, int64_t o_cs, int64_t o_rs, float* part,
+                       cudaStream_t stream) {
+  const int64_t chunks = lowrank_max_chunks(l);
+  const dim3 grid((unsigned)((C + kOutC - 1) / kOutC), (unsigned)chunks, (unsigned)((l.R + 63) / 64));
+  const int smem = kOutStages * kOutStage;
+  if (chunks > 0 &&
+      launch_pdl(outer_tiles_kernel<T>, grid, dim3(kOutThreads), (size_t)smem, stream, l, t, static_cast<const T*>(x), x_rs,
+                 C, static_cast<const T*>(zt), zt_ld, static_cast<T*>(out), o_gs, o_cs, o_rs, part) != cudaSuccess)
+    return MM_ERR_CUDA;
+  const int64_t n = C * l.R;
+  const dim3 gs((unsigned)((n + 1023) / 1024 < 64 ? (n + 1023) / 1024 : 64), (unsigned)l.G);
+  return launch_pdl(outer_sum_kernel<T>, gs, dim3(256), 0, stream, l, t, C, static_cast<T*>(out), (const float*)part) ==
+                 cudaSuccess ? MM_OK : MM_ERR_CUDA;
+}
+
+}  // namespace
+
+bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
+                                    int64_t a_cs, int64_t a_rs) {
+  return (l.dtype == MM_BF16 || l.dtype == MM_F16) && l.M >= 1 && l.R >= 1 && l.G >= 1 && l.G <= 0x7fffffffLL && C >= 1 &&
+         l.M <= 0x7fffffffLL && l.R <= 64 * 65535LL && rows16(x, x_rs, x_cs, l.M) && (a_rs == 1 || a_cs == 1);
+}
+
+mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a,
+                                      int64_t a_gs, int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld,
+                                      cudaStream_t stream) {
+  return l.dtype == MM_F16 ? shrink_launch<__half>(l, x, x_rs, C, a, a_gs, a_cs, a_rs, z, zt, zt_ld, stream)
+                           : shrink_launch<__nv_bfloat16>(l, x, x_rs, C, a, a_gs, a_cs, a_rs, z, zt, zt_ld, stream);
+}
+
+bool lowrank_sort_supported(const LowRankArgs& l) { return l.G >= 1 && l.G <= kSortAdapters && l.M <= 0x7fffffffLL; }
+
+mm_status launch_lowrank_sort(const LowRankArgs& l, const AdapterRows& t, cudaStream_t stream) {
+  const int smem = (int)(32 * l.G * 4);
+  if (cudaFuncSetAttribute(adapter_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * (int)kSortAdapters * 4) !=
+      cudaSuccess)
+    return MM_ERR_CUDA;
+  return launch_pdl(adapter_sort_kernel, dim3(1), dim3(kSortThreads), (size_t)smem, stream, l, t) == cudaSuccess
+             ? MM_OK : MM_ERR_CUDA;
+}
+
+mm_status launch_lowrank_outer_tiles(const LowRankArgs& l, const AdapterRows& t, const void* x, int64_t x_rs, int64_t C,
+                                     const void* zt, int64_t zt_ld, void* out, int64_t o_gs, int64_t o_cs, int64_t o_rs,
+                                     float* part, cudaStream_t stream) {
+  return l.dtype == MM_F16
+             ? outer_launch<__half>(l, t, x, x_rs, C, zt, zt_ld, out, o_gs, o_cs, o_rs, part, stream)
+             : outer_launch<__nv_bfloat16>(l, t, x, x_rs, C, zt, zt_ld, out, o_gs, o_cs, o_rs, part, stream);
+}
+
+}  // namespace qg
