@@ -228,16 +228,18 @@ size_t factor_bytes(const LowRankArgs& l) {
 // Workspace of the many-row gradient kernels.
 struct GradLayout {
   int64_t zt_ld;
-  size_t v, u, vt, ut, row, offset, chunk, part, sums, total;
+  FusedLayout fused;     // dX's product; its z and zt are V's
+  size_t u, ut, row, offset, chunk, part, sums, total;
 };
 GradLayout grad_layout(const LowRankPlan& p) {
   const LowRankArgs& l = p.l;
   GradLayout w;
-  w.zt_ld = (l.R + 7) / 8 * 8;
-  size_t o = 0;
+  w.fused = lowrank_fused_layout(l, p.K);
+  w.zt_ld = w.fused.zt_ld;
+  size_t o = w.fused.total;
   auto take = [&](size_t bytes) { const size_t at = o; o = align256(o + bytes); return at; };
-  const size_t z = (size_t)l.M * (size_t)l.R * 4, zt = (size_t)l.M * (size_t)w.zt_ld * 2;
-  w.v = take(z); w.u = take(z); w.vt = take(zt); w.ut = take(zt);
+  w.u = take((size_t)l.M * (size_t)l.R * 4);
+  w.ut = take((size_t)l.M * (size_t)w.zt_ld * 2);
   w.row = take((size_t)l.M * 4);
   w.offset = take((size_t)(l.G + 1) * 4);
   w.chunk = take((size_t)(l.G + 1) * 4);
@@ -252,9 +254,19 @@ bool many_rows(const LowRankArgs& l) {
          lowrank_sort_supported(l);
 }
 
-// Y = X W + Y for dense Y [M, N] that already holds the low-rank part.
-mm_status add_projection(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t K, const void* w,
-                         int64_t w_rs, int64_t w_cs, int64_t N, void* y, cudaStream_t st) {
+// What a call asks for, whichever of its kernels then runs.
+size_t lowrank_bytes(const LowRankPlan& p) {
+  const size_t few = factor_bytes(p.l), many = many_rows(p.l) ? lowrank_fused_layout(p.l, p.N).total : 0;
+  return few > many ? few : many;
+}
+size_t lowrank_grad_bytes(const LowRankPlan& p) {
+  const size_t few = 2 * factor_bytes(p.l), many = many_rows(p.l) ? grad_layout(p).total : 0;
+  return few > many ? few : many;
+}
+
+// Y = x w for dense Y [M, N].
+GemmArgs projection(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t K, const void* w,
+                    int64_t w_rs, int64_t w_cs, int64_t N, void* y) {
   GemmArgs g;
   memset(&g, 0, sizeof(g));
   g.dtype = l.dtype; g.M = l.M; g.N = N; g.K = K;
@@ -263,11 +275,21 @@ mm_status add_projection(const LowRankArgs& l, const void* x, int64_t x_rs, int6
   g.a.ptr = x; g.a.rs = x_rs; g.a.cs = x_cs;
   g.b.ptr = w; g.b.rs = w_rs; g.b.cs = w_cs;
   g.y.ptr = y; g.y.rs = N; g.y.cs = 1;
+  g.alpha = 1.f; g.beta = 1.f; g.alpha_d = 1.0; g.beta_d = 1.0; g.alpha_i = 1; g.beta_i = 1;
+  return g;
+}
+
+// Y += x w where Y already holds the low-rank part.
+mm_status add_projection(GemmArgs g, cudaStream_t st) {
   // Every kernel of the dense product reads an element of C in the thread
   // that then writes that element of Y (or before its tile's store).
   g.c = g.y;
-  g.alpha = 1.f; g.beta = 1.f; g.alpha_d = 1.0; g.beta_d = 1.0; g.alpha_i = 1; g.beta_i = 1;
-  return run_dense(g, tensor_pays_dense(g.dtype, l.M, N, K, 1), st);
+  return run_dense(g, tensor_pays_dense(g.dtype, g.M, g.N, g.K, 1), st);
+}
+
+// Whether a 16-bit product may take the fused kernel (the dense products' rules).
+bool fused_pays(const LowRankArgs& l, const GemmArgs& g) {
+  return choose(true, tensor_pays_dense(g.dtype, g.M, g.N, g.K, 1)) == MM_PATH_TENSOR && lowrank_fused_supported(l, g);
 }
 
 }  // namespace
@@ -280,7 +302,7 @@ mm_status mm_lowrank_matmul_workspace_size(const mm_tensor* X, const mm_tensor* 
   LowRankPlan p;
   const mm_status s = plan_lowrank(X, W, A, B, nullptr, nullptr, &p);
   if (s != MM_OK) return s;
-  *bytes = factor_bytes(p.l);
+  *bytes = lowrank_bytes(p);
   return MM_OK;
 }
 
@@ -295,16 +317,29 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
   const int64_t yshape[2] = {l.M, p.N};
   if ((s = check_output(Y, l.dtype, 2, yshape)) != MM_OK) return s;
   if (l.M == 0 || p.N == 0) return finish(MM_OK, MM_PATH_NONE);
-  if (!workspace_ok(workspace, workspace_bytes, factor_bytes(l))) return MM_ERR_WORKSPACE;
+  if (!workspace_ok(workspace, workspace_bytes, lowrank_bytes(p))) return MM_ERR_WORKSPACE;
   if (!(l.status = device_status_ptr())) return MM_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* z = static_cast<float*>(workspace);
+  const GemmArgs g = projection(l, X->data, X->strides[0], X->strides[1], p.K, W->data, W->strides[0], W->strides[1], p.N,
+                                Y->data);
   const LowRankFew f = {X->data, X->strides[0], X->strides[1], p.K, A->data, A->strides[0], A->strides[1], A->strides[2],
                         B->data, B->strides[0], B->strides[1], B->strides[2], p.N, Y->data};
   if (path_policy() != MM_PATH_SIMT && lowrank_few_supported(l, f)) {
     if ((s = launch_lowrank_few(l, f, z, st)) != MM_OK) return s;
-    return add_projection(l, X->data, X->strides[0], X->strides[1], p.K, W->data, W->strides[0], W->strides[1], p.N,
-                          Y->data, st);
+    return add_projection(g, st);
+  }
+  if (many_rows(l) && p.K >= 1 &&
+      lowrank_shrink_tiles_supported(l, X->data, X->strides[0], X->strides[1], p.K, A->strides[1], A->strides[2]) &&
+      fused_pays(l, g)) {
+    const FusedLayout w = lowrank_fused_layout(l, p.N);
+    char* ws = static_cast<char*>(workspace);
+    z = reinterpret_cast<float*>(ws + w.z);
+    s = launch_lowrank_shrink_tiles(l, X->data, X->strides[0], p.K, A->data, A->strides[0], A->strides[1], A->strides[2],
+                                    z, ws + w.zt, w.zt_ld, st);
+    if (s == MM_OK)
+      s = launch_lowrank_fused(l, g, w, ws, z, ws + w.zt, B->data, B->strides[0], B->strides[1], B->strides[2], st);
+    return finish(s, MM_PATH_TENSOR);
   }
   if ((s = launch_lowrank_shrink(l, X->data, X->strides[0], X->strides[1], p.K, A->data, A->strides[0], A->strides[1],
                                  A->strides[2], z, st)) != MM_OK)
@@ -312,8 +347,7 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
   if ((s = launch_lowrank_expand(l, z, B->data, B->strides[0], B->strides[1], B->strides[2], p.N, Y->data, st)) !=
       MM_OK)
     return s;
-  return add_projection(l, X->data, X->strides[0], X->strides[1], p.K, W->data, W->strides[0], W->strides[1], p.N,
-                        Y->data, st);
+  return add_projection(g, st);
 }
 
 mm_status mm_lowrank_matmul_grad_workspace_size(const mm_tensor* X, const mm_tensor* W, const mm_tensor* A,
@@ -322,11 +356,7 @@ mm_status mm_lowrank_matmul_grad_workspace_size(const mm_tensor* X, const mm_ten
   LowRankPlan p;
   const mm_status s = plan_lowrank(X, W, A, B, nullptr, nullptr, &p);
   if (s != MM_OK) return s;
-  *bytes = 2 * factor_bytes(p.l);
-  if (many_rows(p.l)) {
-    const size_t need = grad_layout(p).total;
-    if (need > *bytes) *bytes = need;
-  }
+  *bytes = lowrank_grad_bytes(p);
   return MM_OK;
 }
 
@@ -347,7 +377,7 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
   if (dX && (s = check_output(dX, l.dtype, 2, xshape)) != MM_OK) return s;
   if (dA && (s = check_output(dA, l.dtype, 3, ashape)) != MM_OK) return s;
   if (dB && (s = check_output(dB, l.dtype, 3, bshape)) != MM_OK) return s;
-  if (!workspace_ok(workspace, workspace_bytes, 2 * factor_bytes(l))) return MM_ERR_WORKSPACE;
+  if (!workspace_ok(workspace, workspace_bytes, lowrank_grad_bytes(p))) return MM_ERR_WORKSPACE;
   if (!(l.status = device_status_ptr())) return MM_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* v = static_cast<float*>(workspace);
@@ -357,30 +387,35 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
       lowrank_shrink_tiles_supported(l, dY->data, dY->strides[0], dY->strides[1], N, B->strides[2], B->strides[1]) &&
       lowrank_shrink_tiles_supported(l, X->data, X->strides[0], X->strides[1], K, A->strides[1], A->strides[2])) {
     const GradLayout w = grad_layout(p);
-    if (!workspace_ok(workspace, workspace_bytes, w.total)) return MM_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
-    float* zv = reinterpret_cast<float*>(ws + w.v);
+    float* zv = reinterpret_cast<float*>(ws + w.fused.z);
+    void* vt = ws + w.fused.zt;
     const AdapterRows t = {reinterpret_cast<int32_t*>(ws + w.row), reinterpret_cast<int32_t*>(ws + w.offset),
                            reinterpret_cast<int32_t*>(ws + w.chunk), reinterpret_cast<int32_t*>(ws + w.part)};
     float* sums = reinterpret_cast<float*>(ws + w.sums);
     if (dX || dA)
       s = launch_lowrank_shrink_tiles(l, dY->data, dY->strides[0], N, B->data, B->strides[0], B->strides[2],
-                                      B->strides[1], zv, ws + w.vt, w.zt_ld, st);
+                                      B->strides[1], zv, vt, w.zt_ld, st);
     if (s == MM_OK && dB)
       s = launch_lowrank_shrink_tiles(l, X->data, X->strides[0], K, A->data, A->strides[0], A->strides[1],
                                       A->strides[2], reinterpret_cast<float*>(ws + w.u), ws + w.ut, w.zt_ld, st);
     if (s == MM_OK && (dA || dB)) s = launch_lowrank_sort(l, t, st);
     if (s == MM_OK && dA)
-      s = launch_lowrank_outer_tiles(l, t, X->data, X->strides[0], K, ws + w.vt, w.zt_ld, dA->data, K * l.R, l.R, 1,
+      s = launch_lowrank_outer_tiles(l, t, X->data, X->strides[0], K, vt, w.zt_ld, dA->data, K * l.R, l.R, 1,
                                      sums, st);
     if (s == MM_OK && dB)
       s = launch_lowrank_outer_tiles(l, t, dY->data, dY->strides[0], N, ws + w.ut, w.zt_ld, dB->data, l.R * N, 1, N,
                                      sums, st);
     if (s == MM_OK && dX) {
-      s = launch_lowrank_expand(l, zv, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
-      if (s == MM_OK)
-        s = add_projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1], W->strides[0], K,
-                           dX->data, st);
+      const GemmArgs g = projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1],
+                                    W->strides[0], K, dX->data);
+      if (fused_pays(l, g)) {
+        s = finish(launch_lowrank_fused(l, g, w.fused, ws, zv, vt, A->data, A->strides[0], A->strides[2], A->strides[1],
+                                        st), MM_PATH_TENSOR);
+      } else {
+        s = launch_lowrank_expand(l, zv, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
+        if (s == MM_OK) s = add_projection(g, st);
+      }
     }
     return s;
   }
@@ -397,8 +432,8 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
   if (s == MM_OK && dX && l.M > 0 && K > 0) {
     s = launch_lowrank_expand(l, v, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
     if (s == MM_OK)
-      s = add_projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1], W->strides[0], K,
-                         dX->data, st);
+      s = add_projection(projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1],
+                                    W->strides[0], K, dX->data), st);
   }
   return s;
 }

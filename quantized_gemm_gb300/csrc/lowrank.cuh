@@ -4,6 +4,8 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "tc.h"
+#include "tc_internal.h"
 
 namespace qg {
 
@@ -30,6 +32,27 @@ bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t
 mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a,
                                       int64_t a_gs, int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld,
                                       cudaStream_t stream);
+// The fused product Y = g (A B, 16-bit, no batch) + z b.
+constexpr int kSlots = 128;                // adapters of one call that have a copy
+struct FusedTables {
+  int32_t* head;         // [0] slots in use, [1] whether the fix has work
+  int32_t* slot_of;      // [G] of the adapters in use
+  int32_t* adapter_of;   // [kSlots]
+  int32_t* bad;          // [kSlots] the adapter holds a non-finite value
+  int32_t* row_entry;    // [M] place in the row tile's list, -1: not in it
+  int32_t* ext_count;    // [row tiles]
+  int32_t* ext_slot;     // [row tiles][kExtPerTile]
+};
+struct FusedLayout {
+  int64_t slots, zt_ld, f_ld, c_ld;
+  size_t z, zt, head, slot_of, adapter_of, bad, row_entry, ext_count, ext_slot, factors, copy, total;
+};
+FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N);
+bool lowrank_fused_supported(const LowRankArgs& l, const GemmArgs& g);
+mm_status launch_lowrank_fused(const LowRankArgs& l, const GemmArgs& g, const FusedLayout& w, char* ws, const float* z,
+                               const void* zt, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
+                               cudaStream_t stream);
+
 bool lowrank_sort_supported(const LowRankArgs& l);
 mm_status launch_lowrank_sort(const LowRankArgs& l, const AdapterRows& t, cudaStream_t stream);
 // out[g, c, r] from x (16-byte aligned rows) and zt; part holds

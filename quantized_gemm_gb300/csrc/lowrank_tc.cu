@@ -8,6 +8,17 @@
 //
 //   shrink   z[m, r]      = s_g sum_c x[m, c] a[g, c, r]
 //   outer    out[g, c, r] = sum over the rows m of adapter g of x[m, c] z[m, r]
+//
+// and the preparation of the fused product Y[m] = X[m] W + z[m] b[g], in which
+// the tcgen05 kernel (tc_gemm.cu, kLowRank) lets each row tile go on, after
+// the k-blocks of X W, with one set of k-blocks per adapter that the tile's
+// rows name: the rows' z (zeros for the other adapters' rows) times that
+// adapter.  The low-rank part then costs ceil(R / 64) k-blocks per adapter and
+// tile on top of K / 64, and Y is written once.  A zero times an infinity or
+// a NaN is not zero, so the adapters that the kernel reads are copies with
+// their non-finite values set to 0; what those values add to their own rows
+// comes last (lowrank_fix_kernel), with the rows of any adapter past
+// kExtPerTile of one tile or kSlots in all.
 #include <cstring>
 
 #include "lowrank.cuh"
@@ -401,6 +412,163 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// ------------------------------------------------------------------ the fused product's operands
+
+constexpr int kSlotThreads = 1024;
+
+// One block: the adapters in use, ascending, get slots 0, 1, .. (-1 past kSlots).
+__global__ void __launch_bounds__(kSlotThreads) adapter_slots_kernel(const LowRankArgs l, const FusedTables t) {
+  pdl_begin();
+  extern __shared__ uint32_t used[];               // one bit per adapter
+  __shared__ int wsum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, words = (int)((l.G + 31) / 32);
+  for (int i = tid; i < words; i += kSlotThreads) used[i] = 0u;
+  __syncthreads();
+  for (int64_t m = tid; m < l.M; m += kSlotThreads) {
+    const int64_t g = load_index(l.idx, m * l.idx_s, l.ind64);
+    if (g >= 0 && g < l.G) {
+      const uint32_t bit = 1u << (g & 31);
+      if (!(used[g >> 5] & bit)) atomicOr(used + (g >> 5), bit);
+    }
+  }
+  __syncthreads();
+  const int per = (words + kSlotThreads - 1) / kSlotThreads, lo = min(words, tid * per), hi = min(words, lo + per);
+  int n = 0;
+  for (int i = lo; i < hi; ++i) n += __popc(used[i]);
+  int s = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 31) wsum[warp] = s;
+  __syncthreads();
+  s -= n;
+  for (int w = 0; w < warp; ++w) s += wsum[w];
+  for (int i = lo; i < hi; ++i)
+    for (uint32_t b = used[i]; b; b &= b - 1, ++s) {
+      const int g = i * 32 + __ffs(b) - 1;
+      t.slot_of[g] = s < kSlots ? s : -1;
+      if (s < kSlots) t.adapter_of[s] = g;
+    }
+  if (tid == kSlotThreads - 1) {
+    t.head[0] = min(s, kSlots);
+    t.head[1] = 0;                                  // rows or adapters left for the fix
+  }
+  if (tid < kSlots) t.bad[tid] = 0;
+}
+
+// Blocks [0, tiles): a row tile's adapters (the first kExtPerTile in order of
+// appearance) and its blocks of factor rows.  The others: the adapters'
+// copies, 1024 columns of one slot a block.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    lowrank_place_kernel(const LowRankArgs l, const FusedTables t, const int tile_rows, const int tiles, const T* zt,
+                         const int64_t zt_ld, T* factors, const int64_t f_ld, const T* b, const int64_t b_gs,
+                         const int64_t b_rs, const int64_t b_ns, const int64_t N, T* copy, const int64_t c_ld,
+                         const int pieces, const int vec) {
+  pdl_begin();
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x < tiles) {
+    __shared__ int first, list[kExtPerTile];
+    __shared__ signed char entry[256];
+    const int tile = blockIdx.x;
+    const int64_t m = (int64_t)tile * tile_rows + tid;
+    int slot = -1;
+    bool has = false;
+    if (tid < tile_rows && m < l.M) {
+      const int64_t g = load_index(l.idx, m * l.idx_s, l.ind64);
+      has = g >= 0 && g < l.G;
+      if (has) slot = __ldcg(t.slot_of + g);
+    }
+    int mine = -1, n = 0;
+    for (; n < kExtPerTile; ++n) {
+      if (tid == 0) first = 256;
+      __syncthreads();
+      if (slot >= 0 && mine < 0) atomicMin(&first, tid);
+      __syncthreads();
+      const int f = first;
+      if (f == 256) break;
+      if (tid == f) list[n] = slot;
+      __syncthreads();
+      if (slot >= 0 && slot == list[n]) mine = n;
+    }
+    entry[tid] = (signed char)mine;
+    if (tid < n) t.ext_slot[tile * kExtPerTile + tid] = list[tid];
+    if (tid == 0) t.ext_count[tile] = n;
+    if (tid < tile_rows && m < l.M) {
+      t.row_entry[m] = mine;
+      if (has && mine < 0) atomicOr(t.head + 1, 1);
+    }
+    __syncthreads();
+    const int pieces_row = (int)(f_ld / 8), total = n * tile_rows * pieces_row;
+    for (int i = tid; i < total; i += 256) {
+      const int row = i / pieces_row, c = (i - row * pieces_row) * 8;     // row of the tile's n blocks
+      const int r = row % tile_rows, j = row / tile_rows;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (entry[r] == j && c < zt_ld)
+        v = __ldcg(reinterpret_cast<const uint4*>(zt + ((int64_t)tile * tile_rows + r) * zt_ld + c));
+      *reinterpret_cast<uint4*>(factors + ((int64_t)tile * kExtPerTile * tile_rows + row) * f_ld + c) = v;
+    }
+    return;
+  }
+  const int piece = ((int)blockIdx.x - tiles) % pieces, slot = ((int)blockIdx.x - tiles) / pieces;
+  if (slot >= __ldcg(t.head)) return;
+  const int64_t n = ((int64_t)piece * 128 + (tid & 127)) * 8;
+  if (n >= c_ld) return;
+  constexpr uint16_t kExp = std::is_same<T, __half>::value ? 0x7C00 : 0x7F80;
+  const uint16_t* src = reinterpret_cast<const uint16_t*>(b) + (int64_t)__ldcg(t.adapter_of + slot) * b_gs + n * b_ns;
+  bool bad = false;
+#pragma unroll 4
+  for (int64_t r = tid >> 7; r < l.R; r += 2) {
+    uint4 u;
+    uint16_t* e = reinterpret_cast<uint16_t*>(&u);
+    if (vec && n + 8 <= N) {
+      u = *reinterpret_cast<const uint4*>(src + r * b_rs);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = n + j < N ? src[r * b_rs + j * b_ns] : (uint16_t)0;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if ((e[j] & kExp) == kExp) { e[j] = 0; bad = true; }
+    *reinterpret_cast<uint4*>(copy + ((int64_t)slot * l.R + r) * c_ld + n) = u;
+  }
+  if (bad) {
+    atomicOr(t.bad + slot, 1);
+    atomicOr(t.head + 1, 1);
+  }
+}
+
+// What the fused product left out: Y[m] += z[m] b[g] for rows outside their
+// tile's list, and the terms of non-finite adapter values.  Usually nothing.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    lowrank_fix_kernel(const LowRankArgs l, const FusedTables t, const float* z, const T* b, const int64_t b_gs,
+                       const int64_t b_rs, const int64_t b_ns, const int64_t N, T* y) {
+  pdl_begin();
+  if (__ldcg(t.head + 1) == 0) return;
+  constexpr uint16_t kExp = std::is_same<T, __half>::value ? 0x7C00 : 0x7F80;
+  for (int64_t m = blockIdx.y; m < l.M; m += gridDim.y) {
+    const int64_t g = load_index(l.idx, m * l.idx_s, l.ind64);
+    if (g < 0 || g >= l.G) continue;
+    const bool all = __ldcg(t.row_entry + m) < 0;
+    if (!all && !__ldcg(t.bad + __ldcg(t.slot_of + g))) continue;
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < N; n += (int64_t)gridDim.x * 256) {
+      const T* bn = b + g * b_gs + n * b_ns;
+      float v = 0.f;
+      bool any = all;
+      for (int64_t r = 0; r < l.R; ++r) {
+        const T q = bn[r * b_rs];
+        const bool bad = (*reinterpret_cast<const uint16_t*>(&q) & kExp) == kExp;
+        if (all || bad) v = __fmaf_rn(z[m * l.R + r], to_f32(q), v);
+        any |= bad;
+      }
+      if (any) y[m * N + n] = from_f32<T>(to_f32(y[m * N + n]) + v);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ host side
 
 bool rows16(const void* x, int64_t rs, int64_t cs, int64_t rows) {
@@ -457,6 +625,96 @@ mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const void* x, int64
                                       cudaStream_t stream) {
   return l.dtype == MM_F16 ? shrink_launch<__half>(l, x, x_rs, C, a, a_gs, a_cs, a_rs, z, zt, zt_ld, stream)
                            : shrink_launch<__nv_bfloat16>(l, x, x_rs, C, a, a_gs, a_cs, a_rs, z, zt, zt_ld, stream);
+}
+
+namespace {
+
+template <typename T>
+mm_status place_launch(const LowRankArgs& l, const FusedTables& t, int tile_rows, const void* zt, int64_t zt_ld,
+                       void* factors, int64_t f_ld, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns, int64_t N,
+                       void* copy, int64_t c_ld, int64_t slots, cudaStream_t stream) {
+  const int64_t tiles = (l.M + tile_rows - 1) / tile_rows, pieces = (c_ld + 1023) / 1024;
+  const int64_t blocks = tiles + slots * pieces;
+  if (blocks > 0x7fffffffLL) return MM_ERR_UNSUPPORTED;
+  const int vec = b_ns == 1 && b_rs % 8 == 0 && (l.G == 1 || b_gs % 8 == 0) && reinterpret_cast<uintptr_t>(b) % 16 == 0;
+  return launch_pdl(lowrank_place_kernel<T>, dim3((unsigned)blocks), dim3(256), 0, stream, l, t, tile_rows, (int)tiles,
+                    static_cast<const T*>(zt), zt_ld, static_cast<T*>(factors), f_ld, static_cast<const T*>(b), b_gs, b_rs,
+                    b_ns, N, static_cast<T*>(copy), c_ld, (int)pieces, vec) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+}
+
+template <typename T>
+mm_status fix_launch(const LowRankArgs& l, const FusedTables& t, const float* z, const void* b, int64_t b_gs, int64_t b_rs,
+                     int64_t b_ns, int64_t N, void* y, cudaStream_t stream) {
+  const int64_t gx = (N + 255) / 256 < 8 ? (N + 255) / 256 : 8, gy = l.M < 64 ? l.M : 64;
+  return launch_pdl(lowrank_fix_kernel<T>, dim3((unsigned)gx, (unsigned)gy), dim3(256), 0, stream, l, t, z,
+                    static_cast<const T*>(b), b_gs, b_rs, b_ns, N, static_cast<T*>(y)) == cudaSuccess ? MM_OK
+                                                                                                     : MM_ERR_CUDA;
+}
+
+}  // namespace
+
+FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N) {
+  FusedLayout w;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o = (o + bytes + 255) & ~(size_t)255; return at; };
+  const int64_t rows = (l.M + 255) / 256 * 256, tiles = rows / 128;
+  w.slots = l.G < l.M ? l.G : l.M;
+  if (w.slots > kSlots) w.slots = kSlots;
+  w.zt_ld = (l.R + 7) / 8 * 8;
+  w.f_ld = (l.R + 63) / 64 * 64;
+  w.c_ld = (N + 7) / 8 * 8;
+  w.z = take((size_t)l.M * (size_t)l.R * 4);
+  w.zt = take((size_t)l.M * (size_t)w.zt_ld * 2);
+  w.head = take(8);
+  w.slot_of = take((size_t)l.G * 4);
+  w.adapter_of = take(kSlots * 4);
+  w.bad = take(kSlots * 4);
+  w.row_entry = take((size_t)l.M * 4);
+  w.ext_count = take((size_t)tiles * 4);
+  w.ext_slot = take((size_t)tiles * kExtPerTile * 4);
+  w.factors = take((size_t)rows * kExtPerTile * (size_t)w.f_ld * 2);
+  w.copy = take((size_t)w.slots * (size_t)l.R * (size_t)w.c_ld * 2);
+  w.total = o;
+  return w;
+}
+
+bool lowrank_fused_supported(const LowRankArgs& l, const GemmArgs& g) {
+  return (l.dtype == MM_BF16 || l.dtype == MM_F16) && l.M >= 1 && l.R >= 1 && l.R <= 4096 && l.G >= 1 && l.G <= 65536 &&
+         l.M * kExtPerTile < (1ll << 30) && tc_lowrank_tile_rows(g) != 0;
+}
+
+// slots, then (z and zt by the caller's shrink) place, product, fix.
+mm_status launch_lowrank_fused(const LowRankArgs& l, const GemmArgs& g, const FusedLayout& w, char* ws, const float* z,
+                               const void* zt, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
+                               cudaStream_t stream) {
+  FusedTables t;
+  t.head = reinterpret_cast<int32_t*>(ws + w.head);
+  t.slot_of = reinterpret_cast<int32_t*>(ws + w.slot_of);
+  t.adapter_of = reinterpret_cast<int32_t*>(ws + w.adapter_of);
+  t.bad = reinterpret_cast<int32_t*>(ws + w.bad);
+  t.row_entry = reinterpret_cast<int32_t*>(ws + w.row_entry);
+  t.ext_count = reinterpret_cast<int32_t*>(ws + w.ext_count);
+  t.ext_slot = reinterpret_cast<int32_t*>(ws + w.ext_slot);
+  void* factors = ws + w.factors;
+  void* copy = ws + w.copy;
+  void* y = const_cast<void*>(g.y.ptr);
+  LowRankExt e;
+  e.tile_rows = tc_lowrank_tile_rows(g);
+  e.factors = factors; e.factor_ld = w.f_ld;
+  e.adapters = copy; e.slots = w.slots; e.R = l.R; e.adapter_ld = w.c_ld;
+  e.count = t.ext_count; e.slot = t.ext_slot;
+  const int smem = (int)((l.G + 31) / 32 * 4);
+  if (launch_pdl(adapter_slots_kernel, dim3(1), dim3(kSlotThreads), (size_t)smem, stream, l, t) != cudaSuccess)
+    return MM_ERR_CUDA;
+  const bool f16 = l.dtype == MM_F16;
+  mm_status s = f16 ? place_launch<__half>(l, t, e.tile_rows, zt, w.zt_ld, factors, w.f_ld, b, b_gs, b_rs, b_ns, g.N, copy,
+                                           w.c_ld, w.slots, stream)
+                    : place_launch<__nv_bfloat16>(l, t, e.tile_rows, zt, w.zt_ld, factors, w.f_ld, b, b_gs, b_rs, b_ns,
+                                                  g.N, copy, w.c_ld, w.slots, stream);
+  if (s != MM_OK) return s;
+  if ((s = launch_tc_lowrank(g, e, l.status, stream)) != MM_OK) return s;
+  return f16 ? fix_launch<__half>(l, t, z, b, b_gs, b_rs, b_ns, g.N, y, stream)
+             : fix_launch<__nv_bfloat16>(l, t, z, b, b_gs, b_rs, b_ns, g.N, y, stream);
 }
 
 bool lowrank_sort_supported(const LowRankArgs& l) { return l.G >= 1 && l.G <= kSortAdapters && l.M <= 0x7fffffffLL; }

@@ -23,6 +23,20 @@ size_t tc_grouped_workspace_bytes(const GroupedArgs& g);
 // the weights stay int8/uint8 in memory and are dequantised in shared memory.
 mm_status launch_tc_grouped(const GroupedArgs& g, void* workspace, unsigned* status, cudaStream_t stream);
 
+// Y = A B (16-bit, no batch) plus, per row tile, the products of the rows'
+// factors with their adapters (device tables as TcParams describes them).
+struct LowRankExt {
+  int tile_rows;                 // tc_lowrank_tile_rows
+  const void* factors;           // [row tiles * kExtPerTile * tile_rows, factor_ld], factor_ld a multiple of 64
+  int64_t factor_ld;
+  const void* adapters;          // [slots, R, adapter_ld], finite, adapter_ld a multiple of 8
+  int64_t slots, R, adapter_ld;
+  const int32_t* count;
+  const int32_t* slot;
+};
+int tc_lowrank_tile_rows(const GemmArgs& g);
+mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* status, cudaStream_t stream);
+
 // The mixture-of-experts layer for a few tokens (moe_tc.cu): every matrix with
 // 16-byte aligned rows along a unit-stride matrix dimension, w_gate and w_up
 // with the same one.

@@ -46,6 +46,8 @@
 //   kGroupedQ GroupedMatMul with int8/uint8 weights: converter warps form
 //             T((q - zp) * scale) in shared memory (CTA pairs).
 //   kTF32     fp32 MatMul / Gemm as three tf32 products of split operands.
+//   kLowRank  kDense whose tiles go on with the k-blocks of their rows'
+//             low-rank adapters (see lowrank_tc.cu).
 //   kSkinny   kDense for at most 64 rows of A': 256-column tiles whose
 //             k-blocks are split over the CTAs of a cluster (non-persistent,
 //             one tile per cluster), so that B' streams through every SM with
@@ -264,6 +266,10 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
     prefetch_tmap(tmS);
     if (p.wzp_present) prefetch_tmap(tmZ);
   }
+  if (MODE == kLowRank) {
+    prefetch_tmap(tmS);
+    prefetch_tmap(tmZ);
+  }
   const int64_t total = total_tiles<MODE>(p);
   // In a pair each CTA loads its own 128 rows of A and 128 columns of B; every
   // copy completes on the leader CTA's full barrier, which expects both CTAs' bytes.
@@ -282,7 +288,9 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
   int kb_b, kb_e;
   kb_range<MODE>(p, kb_b, kb_e);
   for (int64_t t = first_tile<MODE, PAIR>(p); get_tile<MODE, PAIR>(p, t, total, ti, gh); t += tile_step<MODE, PAIR>(p)) {
-    for (int kb = kb_b; kb < kb_e; ++kb) {
+    int kb_x = kb_e;   // kLowRank: the row tile's adapters follow
+    if (MODE == kLowRank) kb_x += __ldcg(p.ext_count + ti.m0 / G::kTileRows) * p.ext_kb;
+    for (int kb = kb_b; kb < kb_x; ++kb) {
       if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort, p.status, p.timeout_ns)) goto done;
       const uint32_t full = full0 + 8 * stage;
       const uint32_t sa = sbase + stage * G::kStageBytes, sb = sa + G::kABytes;
@@ -328,6 +336,22 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
         qpending |= 1u << qstage;
         qpend_parity = (qpend_parity & ~(1u << qstage)) | (qphase << qstage);
         if (++qstage == kQStages) { qstage = 0; qphase ^= 1; }
+      } else if (MODE == kLowRank && kb >= kb_e) {
+        const int32_t ent = (int32_t)(ti.m0 / G::kTileRows) * kExtPerTile + (kb - kb_e) / p.ext_kb;
+        const int32_t r0 = (kb - kb_e) % p.ext_kb * BK, slot = __ldcg(p.ext_slot + ent);
+        const int32_t zr = ent * G::kTileRows + arow_off;
+        if (PAIR) {
+          const uint32_t bar = mapa_shared(full, 0);
+          if (rank == 0) mbar_arrive_expect_tx(full, 2 * G::kStageBytes);
+          tma_load_3d_pair(sa, tmS, r0, zr, 0, bar);
+#pragma unroll
+          for (int j = 0; j < G::kBRows / 64; ++j) tma_load_3d_pair(sb + j * 8192, tmZ, bc + 64 * j, r0, slot, bar);
+        } else {
+          mbar_arrive_expect_tx(full, G::kStageBytes);
+          tma_load_3d(sa, tmS, r0, zr, 0, full);
+#pragma unroll
+          for (int j = 0; j < G::kBRows / 64; ++j) tma_load_3d(sb + j * 8192, tmZ, bc + 64 * j, r0, slot, full);
+        }
       } else if (PAIR) {
         const uint32_t bar = mapa_shared(full, 0);
         // A tail tile (at most 128 rows) takes 64 rows of A per CTA.
@@ -411,9 +435,12 @@ __device__ void run_mma(const TcParams& p, uint32_t sbase, uint32_t tmem, uint32
       if (!ok) goto done;
       tc_fence_after();
       const uint32_t d = tmem + buf * BN;
-      const int kb1 = min(kb0 + p.kb_per_seg, kb_e);
-      const uint32_t idesc = (PAIR && p.pair_tail && ti.rows <= BM) ? p.idesc_tail : p.idesc;
+      int kb1 = min(kb0 + p.kb_per_seg, kb_e);
+      if (MODE == kLowRank) kb1 += __ldcg(p.ext_count + ti.m0 / G::kTileRows) * p.ext_kb;   // one segment
+      uint32_t idesc = (PAIR && p.pair_tail && ti.rows <= BM) ? p.idesc_tail : p.idesc;
       for (int kb = kb0; kb < kb1; ++kb) {
+        const bool ext = MODE == kLowRank && kb >= kb_e;
+        if (ext) idesc = p.idesc_ext;
         const bool got = PAIR ? mbar_wait_cluster(full0 + 8 * stage, phase, abort, p.status, p.timeout_ns)
                               : mbar_wait(full0 + 8 * stage, phase, abort, p.status, p.timeout_ns);
         if (!got) goto done;
@@ -424,7 +451,7 @@ __device__ void run_mma(const TcParams& p, uint32_t sbase, uint32_t tmem, uint32
           // K-major: advance 32 bytes inside the 128-byte swizzle row.
           // MN-major: advance two 8-row (1024-byte) swizzle atoms.
           // (kTF32 operands are K-major in shared memory whatever their layout in memory.)
-          const bool amn = MODE != kTF32 && p.a_mn, bmn = MODE != kTF32 && p.b_mn;
+          const bool amn = MODE != kTF32 && p.a_mn && !ext, bmn = MODE != kTF32 && (p.b_mn || ext);
           const uint64_t ad = amn ? smem_desc_sw128(sa + k * 2048, 8192, 1024) : smem_desc_sw128(sa + k * 32, 16, 1024);
           const uint64_t bd = bmn ? smem_desc_sw128(sb + k * 2048, 8192, 1024) : smem_desc_sw128(sb + k * 32, 16, 1024);
           const uint32_t acc = (kb > kb0 || k > 0) ? 1u : 0u;
@@ -445,7 +472,7 @@ __device__ void run_mma(const TcParams& p, uint32_t sbase, uint32_t tmem, uint32
           } else if (PAIR) {
             tc_mma_f16_pair(d, ad, bd, idesc, acc);
           } else {
-            tc_mma_f16(d, ad, bd, p.idesc, acc);
+            tc_mma_f16(d, ad, bd, idesc, acc);
           }
         }
         if (PAIR) tc_commit_pair(empty0 + 8 * stage, 0x3);
@@ -1649,6 +1676,10 @@ mm_status launch_tc(int mode, bool pair, const OperandPlan& a, const OperandPlan
                   : launch_kernel<kDense, false>(a, b, ms, mz, p, work, stream);
     case kSkinny:   // single CTAs only
       return pair ? MM_ERR_UNSUPPORTED : launch_kernel<kSkinny, false>(a, b, ms, mz, p, work, stream);
+    case kLowRank:
+      if (!s || !z) return MM_ERR_UNSUPPORTED;
+      return pair ? launch_kernel<kLowRank, true>(a, b, ms, mz, p, work, stream)
+                  : launch_kernel<kLowRank, false>(a, b, ms, mz, p, work, stream);
     case kGrouped:
       return pair ? launch_kernel<kGrouped, true>(a, b, ms, mz, p, work, stream)
                   : launch_kernel<kGrouped, false>(a, b, ms, mz, p, work, stream);
@@ -1808,6 +1839,52 @@ mm_status launch_tc_gemm(const GemmArgs& g, unsigned* status, cudaStream_t strea
     if (st != MM_ERR_UNSUPPORTED || !pair) return st;
   }
   return MM_ERR_UNSUPPORTED;
+}
+
+// ------------------------------------------------------------------ dense product with per-row adapters
+
+// Rows of the row tiles (256: CTA pairs, 128: single CTAs), 0 where the
+// product does not fit the kernel.
+int tc_lowrank_tile_rows(const GemmArgs& g) {
+  OperandPlan a, b;
+  if (g.dtype == MM_F32 || g.bm.nb != 0) return 0;
+  const bool pair = use_pair(g.M, g.K) && max_pair_clusters<kLowRank>() > 0;
+  if (!plan_dense(g, pair, &a, &b)) return 0;
+  return pair ? 2 * BM : BM;
+}
+
+mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* status, cudaStream_t stream) {
+  if (!status) return MM_ERR_CUDA;
+  const bool pair = e.tile_rows == 2 * BM;
+  TcParams p;
+  init_params(&p);
+  p.M = g.M; p.N = g.N; p.K = g.K;
+  p.bm = g.bm;
+  p.out_f16 = g.dtype == MM_F16;
+  p.y = const_cast<void*>(g.y.ptr);
+  p.y_rs = g.y.rs;
+  p.y_vec = (reinterpret_cast<uintptr_t>(g.y.ptr) % 16 == 0) && (g.y.rs % 8 == 0);
+  p.status = status;
+  OperandPlan a, b, z, w;
+  if (!plan_dense(g, pair, &a, &b)) return MM_ERR_UNSUPPORTED;
+  BatchMap one = g.bm;
+  const int64_t none[kMaxBatchDims] = {};
+  const int64_t tiles = (g.M + e.tile_rows - 1) / e.tile_rows;
+  if (!plan_operand(e.factors, g.dtype, tiles * kExtPerTile * e.tile_rows, e.factor_ld, e.factor_ld, 1, one, none, BM, &z) ||
+      z.mn_major)
+    return MM_ERR_UNSUPPORTED;
+  BatchMap slots = g.bm;
+  slots.nb = 1;
+  slots.shape[0] = slots.count = e.slots;
+  const int64_t ss[kMaxBatchDims] = {e.R * e.adapter_ld, 0, 0, 0, 0, 0};
+  if (!plan_operand(e.adapters, g.dtype, g.N, e.R, 1, e.adapter_ld, slots, ss, BN, &w) || !w.mn_major)
+    return MM_ERR_UNSUPPORTED;
+  p.idesc = make_idesc(p.out_f16, a.mn_major, b.mn_major, pair);
+  p.idesc_ext = make_idesc(p.out_f16, 0, 1, pair);
+  p.ext_count = e.count;
+  p.ext_slot = e.slot;
+  p.ext_kb = (int)((e.R + BK - 1) / BK);
+  return launch_tc(kLowRank, pair, a, b, p, stream, &z, &w);
 }
 
 }  // namespace qg

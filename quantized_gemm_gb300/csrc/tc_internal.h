@@ -22,7 +22,11 @@ constexpr int kTileK = 64;    // one 128-byte swizzle row of 16-bit elements
 // are split across the `split` CTAs of a cluster; each CTA keeps its fp32
 // partial sums in shared memory and reduces a slice of the columns over
 // distributed shared memory, so that every SM streams its own share of B'.
-enum TcMode { kDense = 0, kGrouped = 1, kQLinear = 2, kGroupedQ = 3, kTF32 = 4, kSkinny = 5 };
+// kLowRank: a dense product whose row tiles go on, after the k-blocks of A B,
+// with k-blocks of other operands (the rows' low-rank factors times their
+// adapters), accumulated on top.
+enum TcMode { kDense = 0, kGrouped = 1, kQLinear = 2, kGroupedQ = 3, kTF32 = 4, kSkinny = 5, kLowRank = 6 };
+constexpr int kExtPerTile = 16;   // kLowRank: adapters per row tile
 
 struct TcParams {
   int64_t M, N, K;
@@ -74,6 +78,14 @@ struct TcParams {
   const int32_t* g_tile_start;
   const int32_t* g_rowlist;
   int G;
+  // kLowRank: row tile i goes on with ext_count[i] adapters, the j-th
+  // (ext_slot[i * kExtPerTile + j]) in ext_kb k-blocks: the tile's rows of the
+  // factor matrix (rows (i * kExtPerTile + j) * tile rows .., K-major) times
+  // the staged adapter (MN-major).
+  const int32_t* ext_count;
+  const int32_t* ext_slot;
+  int ext_kb;
+  uint32_t idesc_ext;
   // kGroupedQ: weights are int8 (w_signed) or uint8, or with w4 int4
   // (w_signed) or uint4 packed two per byte (the even column in the low
   // nibble); a scale row (and, when wzp_present, a zero-point row of the
