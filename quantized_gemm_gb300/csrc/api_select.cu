@@ -229,7 +229,7 @@ size_t factor_bytes(const LowRankArgs& l) {
 struct GradLayout {
   int64_t zt_ld;
   FusedLayout fused;     // dX's product; its z and zt are V's
-  size_t u, ut, row, offset, chunk, part, sums, total;
+  size_t u, ut, row, offset, chunk, part, sums_a, sums_b, total;
 };
 GradLayout grad_layout(const LowRankPlan& p) {
   const LowRankArgs& l = p.l;
@@ -244,7 +244,8 @@ GradLayout grad_layout(const LowRankPlan& p) {
   w.offset = take((size_t)(l.G + 1) * 4);
   w.chunk = take((size_t)(l.G + 1) * 4);
   w.part = take((size_t)l.G * 4);
-  w.sums = take((size_t)lowrank_max_parts(l) * (size_t)(p.K > p.N ? p.K : p.N) * (size_t)l.R * 4);
+  w.sums_a = take((size_t)lowrank_max_parts(l) * (size_t)p.K * (size_t)l.R * 4);
+  w.sums_b = take((size_t)lowrank_max_parts(l) * (size_t)p.N * (size_t)l.R * 4);
   w.total = o;
   return w;
 }
@@ -335,8 +336,9 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
     const FusedLayout w = lowrank_fused_layout(l, p.N);
     char* ws = static_cast<char*>(workspace);
     z = reinterpret_cast<float*>(ws + w.z);
+    const FusedTables slots = lowrank_fused_tables(w, ws);
     s = launch_lowrank_shrink_tiles(l, X->data, X->strides[0], p.K, A->data, A->strides[0], A->strides[1], A->strides[2],
-                                    z, ws + w.zt, w.zt_ld, st);
+                                    z, ws + w.zt, w.zt_ld, &slots, nullptr, st);
     if (s == MM_OK)
       s = launch_lowrank_fused(l, g, w, ws, z, ws + w.zt, B->data, B->strides[0], B->strides[1], B->strides[2], st);
     return finish(s, MM_PATH_TENSOR);
@@ -392,20 +394,23 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
     void* vt = ws + w.fused.zt;
     const AdapterRows t = {reinterpret_cast<int32_t*>(ws + w.row), reinterpret_cast<int32_t*>(ws + w.offset),
                            reinterpret_cast<int32_t*>(ws + w.chunk), reinterpret_cast<int32_t*>(ws + w.part)};
-    float* sums = reinterpret_cast<float*>(ws + w.sums);
+    const FusedTables slots = lowrank_fused_tables(w.fused, ws);
+    const bool sort_with_u = dB != nullptr;
     if (dX || dA)
       s = launch_lowrank_shrink_tiles(l, dY->data, dY->strides[0], N, B->data, B->strides[0], B->strides[2],
-                                      B->strides[1], zv, vt, w.zt_ld, st);
+                                      B->strides[1], zv, vt, w.zt_ld, dX ? &slots : nullptr,
+                                      dA && !sort_with_u ? &t : nullptr, st);
     if (s == MM_OK && dB)
       s = launch_lowrank_shrink_tiles(l, X->data, X->strides[0], K, A->data, A->strides[0], A->strides[1],
-                                      A->strides[2], reinterpret_cast<float*>(ws + w.u), ws + w.ut, w.zt_ld, st);
-    if (s == MM_OK && (dA || dB)) s = launch_lowrank_sort(l, t, st);
-    if (s == MM_OK && dA)
-      s = launch_lowrank_outer_tiles(l, t, X->data, X->strides[0], K, vt, w.zt_ld, dA->data, K * l.R, l.R, 1,
-                                     sums, st);
-    if (s == MM_OK && dB)
-      s = launch_lowrank_outer_tiles(l, t, dY->data, dY->strides[0], N, ws + w.ut, w.zt_ld, dB->data, l.R * N, 1, N,
-                                     sums, st);
+                                      A->strides[2], reinterpret_cast<float*>(ws + w.u), ws + w.ut, w.zt_ld, nullptr, &t,
+                                      st);
+    LowRankOuter o[2];
+    int problems = 0;
+    if (dA)
+      o[problems++] = {X->data, X->strides[0], K, vt, dA->data, l.R, 1, reinterpret_cast<float*>(ws + w.sums_a)};
+    if (dB)
+      o[problems++] = {dY->data, dY->strides[0], N, ws + w.ut, dB->data, 1, N, reinterpret_cast<float*>(ws + w.sums_b)};
+    if (s == MM_OK && problems) s = launch_lowrank_outer_tiles(l, t, o, problems, w.zt_ld, st);
     if (s == MM_OK && dX) {
       const GemmArgs g = projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1],
                                     W->strides[0], K, dX->data);

@@ -11,6 +11,7 @@ namespace qg {
 
 constexpr int kChunkRows = 512;            // rows of one adapter that one block sums
 constexpr int64_t kSortAdapters = 1024;    // adapters that the sort's counters hold (shared memory)
+constexpr int kSlots = 128;                // adapters of one call that the fused product holds copies of
 
 // Rows in adapter order (device tables in the workspace).
 struct AdapterRows {
@@ -25,15 +26,11 @@ inline int64_t lowrank_max_chunks(const LowRankArgs& l) {
 }
 // Chunks of adapters with several: each such adapter has more than kChunkRows rows.
 inline int64_t lowrank_max_parts(const LowRankArgs& l) { return 2 * (l.M / kChunkRows); }
+inline bool lowrank_sort_supported(const LowRankArgs& l) {
+  return l.G >= 1 && l.G <= kSortAdapters && l.M <= 0x7fffffffLL;
+}
 
-// z [M, R] (fp32) and zt [M, zt_ld] (T, zeros past R), both scaled.
-bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
-                                    int64_t a_cs, int64_t a_rs);
-mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a,
-                                      int64_t a_gs, int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld,
-                                      cudaStream_t stream);
-// The fused product Y = g (A B, 16-bit, no batch) + z b.
-constexpr int kSlots = 128;                // adapters of one call that have a copy
+// Tables of the fused product Y = A B + z b (device, in the workspace).
 struct FusedTables {
   int32_t* head;         // [0] slots in use, [1] whether the fix has work
   int32_t* slot_of;      // [G] of the adapters in use
@@ -48,17 +45,29 @@ struct FusedLayout {
   size_t z, zt, head, slot_of, adapter_of, bad, row_entry, ext_count, ext_slot, factors, copy, total;
 };
 FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N);
+FusedTables lowrank_fused_tables(const FusedLayout& w, char* ws);
 bool lowrank_fused_supported(const LowRankArgs& l, const GemmArgs& g);
+
+// z [M, R] (fp32) and zt [M, zt_ld] (T, zeros past R), both scaled; the same
+// launch makes the fused product's slots and the sorted rows where asked for.
+bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
+                                    int64_t a_cs, int64_t a_rs);
+mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a,
+                                      int64_t a_gs, int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld,
+                                      const FusedTables* slots, const AdapterRows* sort, cudaStream_t stream);
+// Y = g (A B, 16-bit, no batch) + z b, z, zt and the slots made before.
 mm_status launch_lowrank_fused(const LowRankArgs& l, const GemmArgs& g, const FusedLayout& w, char* ws, const float* z,
                                const void* zt, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
                                cudaStream_t stream);
-
-bool lowrank_sort_supported(const LowRankArgs& l);
-mm_status launch_lowrank_sort(const LowRankArgs& l, const AdapterRows& t, cudaStream_t stream);
-// out[g, c, r] from x (16-byte aligned rows) and zt; part holds
-// lowrank_max_parts * C * R floats.
-mm_status launch_lowrank_outer_tiles(const LowRankArgs& l, const AdapterRows& t, const void* x, int64_t x_rs, int64_t C,
-                                     const void* zt, int64_t zt_ld, void* out, int64_t o_gs, int64_t o_cs, int64_t o_rs,
-                                     float* part, cudaStream_t stream);
+// One or two gradients out[g, c, r] from x (16-byte aligned rows) and zt; part
+// holds lowrank_max_parts * C * R floats.
+struct LowRankOuter {
+  const void* x; int64_t x_rs, C;
+  const void* zt;
+  void* out; int64_t o_cs, o_rs;
+  float* part;
+};
+mm_status launch_lowrank_outer_tiles(const LowRankArgs& l, const AdapterRows& t, const LowRankOuter* o, int problems,
+                                     int64_t zt_ld, cudaStream_t stream);
 
 }  // namespace qg

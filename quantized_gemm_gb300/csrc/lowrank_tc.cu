@@ -22,6 +22,7 @@
 #include <cstring>
 
 #include "lowrank.cuh"
+#include "tc_ptx.cuh"
 
 namespace qg {
 
@@ -36,12 +37,12 @@ __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
+__device__ __forceinline__ void ldsm_x2(uint32_t (&r)[2], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
 __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x2(uint32_t (&r)[2], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
 }
 __device__ __forceinline__ void ldsm_x2_t(uint32_t (&r)[2], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
@@ -70,62 +71,92 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// `rows` rows of `len` elements (zeros past `rows_ok` rows and `len_ok`
-// elements) into shared memory with `pitch` bytes a row, `per` elements a
-// copy (8, 4 or 2; 1: plain loads).  len_ok may end inside a copy.
+// One warp's copy of `rows` rows of `len` elements into shared memory with
+// `pitch` bytes a row, `per` elements a copy (8, 4 or 2; 1: plain loads);
+// zeros past rows_ok rows and len_ok elements (which may end inside a copy).
+// A row takes 2^lpr lanes.
 template <typename T>
 __device__ __forceinline__ void load_block(uint32_t dst, int pitch, const T* src, int64_t ld, int rows, int rows_ok,
-                                           int len, int len_ok, int per, int tid, int threads) {
-  const int n = (len + per - 1) / per;
-  for (int i = tid; i < rows * n; i += threads) {
-    const int r = i / n, c = (i - r * n) * per;
-    const int ok = r < rows_ok ? max(0, min(per, len_ok - c)) : 0;
-    const T* s = ok ? src + (int64_t)r * ld + c : src;
-    const uint32_t d = dst + (uint32_t)(r * pitch + c * 2);
-    if (per == 8) cp_async<16>(d, s, ok * 2);
-    else if (per == 4) cp_async<8>(d, s, ok * 2);
-    else if (per == 2) cp_async<4>(d, s, ok * 2);
-    else {
-      const uint16_t v = ok ? *reinterpret_cast<const uint16_t*>(s) : (uint16_t)0;
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(d), "h"(v) : "memory");
+                                           int len, int len_ok, int per, int lpr, int lane) {
+  const int step = 32 >> lpr, width = 1 << lpr;
+  for (int c = (lane & (width - 1)) * per; c < len; c += width * per)
+    for (int r = lane >> lpr; r < rows; r += step) {
+      const int ok = r < rows_ok ? max(0, min(per, len_ok - c)) : 0;
+      const T* s = ok ? src + (int64_t)r * ld + c : src;
+      const uint32_t d = dst + (uint32_t)(r * pitch + c * 2);
+      if (per == 8) cp_async<16>(d, s, ok * 2);
+      else if (per == 4) cp_async<8>(d, s, ok * 2);
+      else if (per == 2) cp_async<4>(d, s, ok * 2);
+      else {
+        const uint16_t v = ok ? *reinterpret_cast<const uint16_t*>(s) : (uint16_t)0;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(d), "h"(v) : "memory");
+      }
     }
-  }
 }
 
 // ------------------------------------------------------------------ shrink
 
-// A block takes 32 rows x 64 ranks.  Four pairs of warps split c (64 at a
-// time, in turn), each pair with its own 3-stage ring, so that a block keeps
-// four loads streams in flight; the pairs' sums meet in shared memory.  The
+// A block takes 32 rows x 64 ranks; its 4 warps split c, 64 at a time in
+// turn, each with its own ring (no block barrier until the warps' sums meet in
+// shared memory): one lane streams 32 x 64 tiles of x by TMA (128-byte
+// swizzle), the adapter arrives by asynchronous copies of whatever width its
+// alignment allows.  Two blocks per SM keep some 96 KB of x in flight.  The
 // tile is multiplied once per adapter that its rows name (rows of a request
 // are neighbours, so one or two); each pass keeps its own adapter's rows.
-constexpr int kShRows = 32, kShK = 64, kShStages = 3, kShPairs = 4, kShThreads = 256;
-constexpr int kShXPitch = kShK * 2 + 16;
-constexpr int kShXBytes = kShRows * kShXPitch;
+constexpr int kShRows = 32, kShK = 64, kShWarps = 4, kShThreads = 32 * kShWarps;
+constexpr int kShXBytes = kShRows * kShK * 2;
+constexpr int kShKPitch = kShK * 2 + 16;
+constexpr int kShCtrl = 256;                   // barriers, abort flag
 
 __host__ __device__ constexpr int shrink_a_bytes(bool ck, int rc) {
-  return ck ? (rc + 7) / 8 * 8 * kShXPitch : kShK * ((rc + 7) / 8 * 16 + 16);
+  return ck ? (rc + 7) / 8 * 8 * kShKPitch : kShK * ((rc + 7) / 8 * 16 + 16);
+}
+__host__ __device__ constexpr int shrink_stages(int rc) { return rc <= 32 ? 4 : 3; }
+__host__ __device__ constexpr int shrink_red_pitch(int rc) { return (rc + 7) / 8 * 8 + 4; }
+// [x rings][control][adapter rings][sums]
+__host__ __device__ constexpr int shrink_smem(bool ck, int rc) {
+  return 1024 + kShWarps * shrink_stages(rc) * (kShXBytes + shrink_a_bytes(ck, rc)) + kShCtrl +
+         kShWarps * kShRows * shrink_red_pitch(rc) * 4;
 }
 
-template <typename T, bool CK>
-__global__ void __launch_bounds__(kShThreads)
-    shrink_tiles_kernel(const LowRankArgs l, const T* x, int64_t x_rs, int64_t C, const T* a, int64_t a_gs, int64_t a_ld,
-                        int per, float* z, T* zt, int64_t zt_ld) {
-  pdl_begin();
-  extern __shared__ __align__(16) uint8_t sm[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pair = warp >> 1, rg = warp & 1;
-  const int64_t m0 = (int64_t)blockIdx.x * kShRows;
+struct ShrinkArgs {
+  int64_t C;
+  const void* a; int64_t a_gs, a_ld;
+  int per;                                     // elements per copy of the adapter
+  float* z;
+  void* zt; int64_t zt_ld;
+  int tiles;
+  unsigned long long timeout_ns, teardown_ns;
+};
+
+// NT: 8-rank tiles that the accumulators hold.
+template <typename T, bool CK, int NT>
+__device__ void shrink_tile(const CUtensorMap* tmX, const LowRankArgs& l, const ShrinkArgs& p, int tile, uint8_t* sm_raw) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t m0 = (int64_t)tile * kShRows, C = p.C;
   const int r0 = blockIdx.y * 64, rc = (int)min((int64_t)64, l.R - r0), nt = (rc + 7) / 8;
   const int rows = (int)min((int64_t)kShRows, l.M - m0);
-  const int a_bytes = shrink_a_bytes(CK, rc), stage = kShXBytes + a_bytes;
-  const int a_pitch = CK ? kShXPitch : nt * 16 + 16;
-  const uint32_t ring = shared_u32(sm) + (uint32_t)(pair * kShStages * stage);
-  float* red = reinterpret_cast<float*>(sm);             // [pairs][32][68], after the sums
-  constexpr int kRedPitch = 68;
-  const int ptid = tid & 63;
+  const int stages = shrink_stages((int)min((int64_t)64, l.R)), a_bytes = shrink_a_bytes(CK, rc);
+  const int a_pitch = CK ? kShKPitch : nt * 16 + 16;
+  const uint32_t raw = shared_u32(sm_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = sm_raw + (base - raw);
+  const uint32_t xring = base + (uint32_t)(warp * stages * kShXBytes);
+  const uint32_t ctrl = base + (uint32_t)(kShWarps * stages * kShXBytes);
+  const uint32_t bar0 = ctrl + (uint32_t)(warp * 32);
+  const uint32_t aring = ctrl + kShCtrl + (uint32_t)(warp * stages * a_bytes);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + (ctrl - base) + 240);
+  float* red = reinterpret_cast<float*>(sm + (ctrl - base) + kShCtrl + kShWarps * stages * a_bytes);
+  const int red_pitch = shrink_red_pitch(rc);
   const int nk = (int)((C + kShK - 1) / kShK);
-  const int mine = nk > pair ? (nk - pair + kShPairs - 1) / kShPairs : 0;   // this pair's k-blocks
-  auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory"); };
+  const int mine = nk > warp ? (nk - warp + kShWarps - 1) / kShWarps : 0;   // this warp's k-blocks
+  int lpr = 0;                                            // 2^lpr lanes per adapter row
+  while (lpr < 5 && (p.per << lpr) < (CK ? kShK : rc)) ++lpr;
+
+  if (lane == 0)
+    for (int i = 0; i < stages; ++i) ptx::mbar_init(bar0 + 8 * i, 1);
+  if (tid == 0) *abort = 0;
+  ptx::fence_mbar_init();
+  __syncthreads();
 
   int g_lane = -1;
   if (lane < rows) {
@@ -135,121 +166,160 @@ __global__ void __launch_bounds__(kShThreads)
   }
   unsigned left = __ballot_sync(0xffffffffu, g_lane >= 0);
   const unsigned none = ~left;
-  // rows without adapter
-  for (int i = tid; i < rows * rc; i += kShThreads) {
-    const int r = i / rc, c = i - r * rc;
-    if ((none >> r) & 1u) z[(m0 + r) * l.R + r0 + c] = 0.f;
-  }
-  for (int i = tid; i < rows * nt * 8; i += kShThreads) {
+  T* zt = static_cast<T*>(p.zt);
+  for (int i = tid; i < rows * nt * 8; i += kShThreads) {   // rows without adapter
     const int r = i / (nt * 8), c = i - r * (nt * 8);
-    if (((none >> r) & 1u) && r0 + c < zt_ld) zt[(m0 + r) * zt_ld + r0 + c] = from_f32<T>(0.f);
+    if (!((none >> r) & 1u)) continue;
+    if (c < rc) p.z[(m0 + r) * l.R + r0 + c] = 0.f;
+    if (r0 + c < p.zt_ld) zt[(m0 + r) * p.zt_ld + r0 + c] = from_f32<T>(0.f);
   }
-  while (left) {
+  uint32_t done = 0, issued = 0;       // this warp's k-blocks over all passes: stage = count % stages
+  uint32_t istage = 0, dstage = 0, dphase = 0;
+  bool ok = true;
+  while (left && ok) {
     const int g = __shfl_sync(0xffffffffu, g_lane, __ffs(left) - 1);
     const unsigned sel = __ballot_sync(0xffffffffu, g_lane == g);
     left &= ~sel;
-    const T* ag = a + (int64_t)g * a_gs;
+    const T* ag = static_cast<const T*>(p.a) + (int64_t)g * p.a_gs;
     auto load = [&](int i) {
-      const int64_t c0 = ((int64_t)i * kShPairs + pair) * kShK;
+      const int64_t c0 = ((int64_t)i * kShWarps + warp) * kShK;
+      if (lane == 0) {
+        const uint32_t bar = bar0 + 8 * istage;
+        ptx::mbar_arrive_expect_tx(bar, kShXBytes);
+        ptx::tma_load_3d(xring + istage * kShXBytes, tmX, (int32_t)c0, (int32_t)m0, 0, bar);
+      }
       const int cn = (int)min((int64_t)kShK, C - c0);
-      const uint32_t s = ring + (uint32_t)((i % kShStages) * stage);
-      load_block<T>(s, kShXPitch, x + m0 * x_rs + c0, x_rs, kShRows, rows, kShK, cn, 8, ptid, 64);
-      if constexpr (CK)
-        load_block<T>(s + kShXBytes, a_pitch, ag + (int64_t)r0 * a_ld + c0, a_ld, rc, rc, kShK, cn, per, ptid, 64);
-      else
-        load_block<T>(s + kShXBytes, a_pitch, ag + c0 * a_ld + r0, a_ld, kShK, cn, rc, rc, per, ptid, 64);
+      const uint32_t s = aring + istage * (uint32_t)a_bytes;
+      const T* src = CK ? ag + (int64_t)r0 * p.a_ld + c0 : ag + c0 * p.a_ld + r0;
+      const int arows = CK ? rc : kShK, alen = CK ? kShK : rc;
+      if (p.per == 8 && cn == kShK && (alen & 7) == 0) {     // whole 16-byte copies
+        const int r = lane >> lpr, c = (lane & ((1 << lpr) - 1)) * 8, step = 32 >> lpr;
+        const T* q = src + (int64_t)r * p.a_ld + c;
+        uint32_t d = s + (uint32_t)(r * a_pitch + c * 2);
+        if (c < alen)
+          for (int e = r; e < arows; e += step, q += (int64_t)step * p.a_ld, d += (uint32_t)(step * a_pitch))
+            cp_async<16>(d, q, 16);
+      } else if constexpr (CK) {
+        load_block<T>(s, a_pitch, src, p.a_ld, rc, rc, kShK, cn, p.per, lpr, lane);
+      } else {
+        load_block<T>(s, a_pitch, src, p.a_ld, kShK, cn, rc, rc, p.per, lpr, lane);
+      }
+      ++issued;
+      if (++istage == (uint32_t)stages) istage = 0;
     };
-    float acc[8][4];
+    float acc[2][NT][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < kShStages - 1; ++i) {
+        for (int e = 0; e < 4; ++e) acc[h][j][e] = 0.f;
+    // stages - 1 blocks ahead: one group of copies per block, empty past the end
+    for (int i = 0; i < stages - 1; ++i) {
       if (i < mine) load(i);
       cp_commit();
     }
     for (int i = 0; i < mine; ++i) {
-      cp_wait<kShStages - 2>();
-      pair_sync();                       // block i has landed, and block i - 1 has been used
-      if (i + kShStages - 1 < mine) load(i + kShStages - 1);
+      if (stages == 4) cp_wait<2>();
+      else cp_wait<1>();
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar0 + 8 * dstage, dphase, abort, l.status, p.timeout_ns));
+      if (!ok) break;
+      __syncwarp();                      // block i has landed for every lane, and block i - 1 has been used
+      if (i + stages - 1 < mine) load(i + stages - 1);
       cp_commit();
-      const uint32_t s = ring + (uint32_t)((i % kShStages) * stage);
+      const uint32_t xs = xring + dstage * kShXBytes, as = aring + dstage * (uint32_t)a_bytes;
 #pragma unroll
       for (int k = 0; k < kShK / 16; ++k) {
-        uint32_t fa[4];
-        ldsm_x4(fa, s + (uint32_t)((rg * 16 + (lane & 15)) * kShXPitch + k * 32 + (lane >> 4) * 16));
+        uint32_t fa[2][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int h = 0; h < 2; ++h) {
+          const int row = h * 16 + (lane & 15);
+          ldsm_x4(fa[h], xs + (uint32_t)(row * 128 + (((k * 2 + (lane >> 4)) ^ (row & 7)) << 4)));
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
           if (j >= nt) break;
           uint32_t fb[2];
           if constexpr (CK)
-            ldsm_x2(fb, s + kShXBytes + (uint32_t)((j * 8 + (lane & 7)) * a_pitch + k * 32 + ((lane >> 3) & 1) * 16));
+            ldsm_x2(fb, as + (uint32_t)((j * 8 + (lane & 7)) * a_pitch + k * 32 + ((lane >> 3) & 1) * 16));
           else
-            ldsm_x2_t(fb, s + kShXBytes + (uint32_t)((k * 16 + (lane & 15)) * a_pitch + j * 16));
-          mma16816<T>(acc[j], fa, fb);
+            ldsm_x2_t(fb, as + (uint32_t)((k * 16 + (lane & 15)) * a_pitch + j * 16));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) mma16816<T>(acc[h][j], fa[h], fb);
         }
       }
+      ++done;
+      if (++dstage == (uint32_t)stages) { dstage = 0; dphase ^= 1; }
     }
     cp_wait<0>();
-    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j >= nt) break;
-      float* q = red + (pair * kShRows + rg * 16 + (lane >> 2)) * kRedPitch + j * 8 + (lane & 3) * 2;
-      q[0] = acc[j][0]; q[1] = acc[j][1];
-      q[8 * kRedPitch] = acc[j][2]; q[8 * kRedPitch + 1] = acc[j][3];
-    }
-    __syncthreads();
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (j >= nt) break;
+        float* q = red + (warp * kShRows + h * 16 + (lane >> 2)) * red_pitch + j * 8 + (lane & 3) * 2;
+        q[0] = acc[h][j][0]; q[1] = acc[h][j][1];
+        q[8 * red_pitch] = acc[h][j][2]; q[8 * red_pitch + 1] = acc[h][j][3];
+      }
+    ok = __syncthreads_and(ok);
     const float scale = l.scales ? l.scales[g * l.scales_s] : 1.f;
     for (int i = tid; i < rows * nt * 8; i += kShThreads) {
       const int r = i / (nt * 8), c = i - r * (nt * 8);
       if (!((sel >> r) & 1u)) continue;
       float v = 0.f;
 #pragma unroll
-      for (int q = 0; q < kShPairs; ++q) v += red[(q * kShRows + r) * kRedPitch + c];
+      for (int w = 0; w < kShWarps; ++w) v += red[(w * kShRows + r) * red_pitch + c];
       v = c < rc ? v * scale : 0.f;
-      if (c < rc) z[(m0 + r) * l.R + r0 + c] = v;
-      if (r0 + c < zt_ld) zt[(m0 + r) * zt_ld + r0 + c] = from_f32<T>(v);
+      if (c < rc) p.z[(m0 + r) * l.R + r0 + c] = v;
+      if (r0 + c < p.zt_ld) zt[(m0 + r) * p.zt_ld + r0 + c] = from_f32<T>(v);
     }
     __syncthreads();
+  }
+  // After a wait that ran out: let the copies still in flight land.
+  for (; done != issued; ++done) {
+    if (lane == 0) ptx::mbar_wait_teardown(bar0 + 8 * dstage, dphase, p.teardown_ns);
+    if (++dstage == (uint32_t)stages) { dstage = 0; dphase ^= 1; }
   }
 }
 
 // ------------------------------------------------------------------ rows in adapter order
 
 // One block, a stable counting sort: warp w counts and then places the w-th
-// 32nd of the rows, in order, so rows keep their order within an adapter and
+// 8th of the rows, in order, so rows keep their order within an adapter and
 // sums over them do not depend on timing.
-constexpr int kSortThreads = 1024;
-
-__global__ void __launch_bounds__(kSortThreads) adapter_sort_kernel(const LowRankArgs l, const AdapterRows t) {
-  pdl_begin();
-  extern __shared__ int32_t cnt[];                  // [32 warps][G]
-  __shared__ int32_t wtot[32][3];
+__device__ void adapter_sort(const LowRankArgs& l, const AdapterRows& t, uint8_t* sm) {
+  int32_t* cnt = reinterpret_cast<int32_t*>(sm);    // [warps][G]
+  __shared__ int32_t wtot[kShWarps][3];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = (int)l.G;
-  for (int i = tid; i < 32 * G; i += kSortThreads) cnt[i] = 0;
+  for (int i = tid; i < kShWarps * G; i += kShThreads) cnt[i] = 0;
   __syncthreads();
-  const int64_t per = ((l.M + 31) / 32 + 31) / 32 * 32, lo = warp * per, hi = min(l.M, lo + per);
+  const int64_t per = ((l.M + kShWarps - 1) / kShWarps + 31) / 32 * 32, lo = warp * per, hi = min(l.M, lo + per);
   int32_t* mine = cnt + warp * G;
+  constexpr int kAhead = 8;                         // index reads in flight
   auto adapter = [&](int64_t m) {
     if (m >= hi) return -1;
     const int64_t g = load_index(l.idx, m * l.idx_s, l.ind64);
     return g >= 0 && g < l.G ? (int)g : -1;
   };
-  for (int64_t b = lo; b < hi; b += 32) {
-    const int g = adapter(b + lane);
-    const unsigned same = __match_any_sync(0xffffffffu, g);
-    if (g >= 0 && lane == __ffs(same) - 1) mine[g] += __popc(same);
-    __syncwarp();
+  for (int64_t b = lo; b < hi; b += 32 * kAhead) {
+    int gs[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) gs[i] = adapter(b + 32 * i + lane);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int g = gs[i];
+      const unsigned same = __match_any_sync(0xffffffffu, g);
+      if (g >= 0 && lane == __ffs(same) - 1) mine[g] += __popc(same);
+      __syncwarp();
+    }
   }
   __syncthreads();
   // Exclusive sums over (adapter, warp), adapter-major, a range of adapters per thread.
-  const int gp = (G + kSortThreads - 1) / kSortThreads, g0 = min(G, tid * gp), g1 = min(G, g0 + gp);
+  const int gp = (G + kShThreads - 1) / kShThreads, g0 = min(G, tid * gp), g1 = min(G, g0 + gp);
   int rows = 0, chunks = 0, parts = 0;
   for (int g = g0; g < g1; ++g) {
     int c = 0;
-    for (int w = 0; w < 32; ++w) c += cnt[w * G + g];
+    for (int w = 0; w < kShWarps; ++w) c += cnt[w * G + g];
     const int k = (c + kChunkRows - 1) / kChunkRows;
     rows += c;
     chunks += k;
@@ -271,7 +341,7 @@ __global__ void __launch_bounds__(kSortThreads) adapter_sort_kernel(const LowRan
     t.chunk[g] = pc;
     t.part[g] = pp;
     const int first = pr;
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < kShWarps; ++w) {
       const int c = cnt[w * G + g];
       cnt[w * G + g] = pr;
       pr += c;
@@ -280,18 +350,82 @@ __global__ void __launch_bounds__(kSortThreads) adapter_sort_kernel(const LowRan
     pc += k;
     pp += k > 1 ? k : 0;
   }
-  if (tid == kSortThreads - 1) { t.offset[G] = pr; t.chunk[G] = pc; }
+  if (tid == kShThreads - 1) { t.offset[G] = pr; t.chunk[G] = pc; }
   __syncthreads();
-  for (int64_t b = lo; b < hi; b += 32) {
-    const int g = adapter(b + lane);
-    const unsigned same = __match_any_sync(0xffffffffu, g);
-    const int at = g >= 0 ? mine[g] + __popc(same & ((1u << lane) - 1u)) : 0;
-    __syncwarp();
-    if (g >= 0) {
-      t.row[at] = (int32_t)(b + lane);
-      if (lane == __ffs(same) - 1) mine[g] += __popc(same);
+  for (int64_t b = lo; b < hi; b += 32 * kAhead) {
+    int gs[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) gs[i] = adapter(b + 32 * i + lane);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int g = gs[i];
+      const unsigned same = __match_any_sync(0xffffffffu, g);
+      const int at = g >= 0 ? mine[g] + __popc(same & ((1u << lane) - 1u)) : 0;
+      __syncwarp();
+      if (g >= 0) {
+        t.row[at] = (int32_t)(b + 32 * i + lane);
+        if (lane == __ffs(same) - 1) mine[g] += __popc(same);
+      }
+      __syncwarp();
     }
-    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------------ adapters in use
+
+// One block: the adapters in use, ascending, get slots 0, 1, .. (-1 past kSlots).
+__device__ void adapter_slots(const LowRankArgs& l, const FusedTables& t, uint8_t* sm) {
+  uint32_t* used = reinterpret_cast<uint32_t*>(sm);      // one bit per adapter
+  __shared__ int wsum[kShWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, words = (int)((l.G + 31) / 32);
+  for (int i = tid; i < words; i += kShThreads) used[i] = 0u;
+  __syncthreads();
+#pragma unroll 8
+  for (int64_t m = tid; m < l.M; m += kShThreads) {
+    const int64_t g = load_index(l.idx, m * l.idx_s, l.ind64);
+    if (g >= 0 && g < l.G) atomicOr(used + (g >> 5), 1u << (g & 31));
+  }
+  __syncthreads();
+  const int per = (words + kShThreads - 1) / kShThreads, lo = min(words, tid * per), hi = min(words, lo + per);
+  int n = 0;
+  for (int i = lo; i < hi; ++i) n += __popc(used[i]);
+  int s = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 31) wsum[warp] = s;
+  __syncthreads();
+  s -= n;
+  for (int w = 0; w < warp; ++w) s += wsum[w];
+  for (int i = lo; i < hi; ++i)
+    for (uint32_t b = used[i]; b; b &= b - 1, ++s) {
+      const int g = i * 32 + __ffs(b) - 1;
+      t.slot_of[g] = s < kSlots ? s : -1;
+      if (s < kSlots) t.adapter_of[s] = g;
+    }
+  if (tid == kShThreads - 1) {
+    t.head[0] = min(s, kSlots);
+    t.head[1] = 0;                                  // rows or adapters left for the fix
+  }
+  if (tid < kSlots) t.bad[tid] = 0;
+}
+
+// The first blocks make the tables that later launches want (they depend on
+// the indices alone): slots, then the sort; the others shrink one tile each.
+template <typename T, bool CK, int NT>
+__global__ void __launch_bounds__(kShThreads, NT <= 4 ? 2 : 1)
+    shrink_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const LowRankArgs l, const ShrinkArgs p,
+                        const FusedTables slots, const AdapterRows sort) {
+  pdl_begin();
+  extern __shared__ __align__(16) uint8_t sm[];
+  const int tile = (int)blockIdx.x - ((int)gridDim.x - p.tiles);
+  if (tile >= 0) {
+    shrink_tile<T, CK, NT>(&tmX, l, p, tile, sm);
+  } else if (blockIdx.y == 0) {
+    if (blockIdx.x == 0 && slots.head) adapter_slots(l, slots, sm);
+    else adapter_sort(l, sort, sm);
   }
 }
 
@@ -306,14 +440,26 @@ constexpr int kOutXPitch = kOutC * 2 + 16, kOutZPitch = 64 * 2 + 16;
 constexpr int kOutStage = kOutRows * (kOutXPitch + kOutZPitch);
 
 template <typename T>
+struct OuterProblem {
+  const T* x; int64_t x_rs, C;
+  const T* zt;
+  T* out; int64_t o_cs, o_rs;      // out [G, C, R] in the order of these strides
+  float* part;
+};
+
+// grid: (columns of both problems' x, chunks, ranks)
+template <typename T>
 __global__ void __launch_bounds__(kOutThreads)
-    outer_tiles_kernel(const LowRankArgs l, const AdapterRows t, const T* x, int64_t x_rs, int64_t C, const T* zt,
-                       int64_t zt_ld, T* out, int64_t o_gs, int64_t o_cs, int64_t o_rs, float* part) {
+    outer_tiles_kernel(const LowRankArgs l, const AdapterRows t, const OuterProblem<T> p0, const OuterProblem<T> p1,
+                       const int blocks0, const int64_t zt_ld) {
   pdl_begin();
   extern __shared__ __align__(16) uint8_t sm[];
+  __shared__ int32_t rows[kChunkRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = (int)l.G;
   const int chunk = blockIdx.y;
   if (chunk >= __ldcg(t.chunk + G)) return;
+  const OuterProblem<T>& p = (int)blockIdx.x < blocks0 ? p0 : p1;
+  const int64_t C = p.C;
   int lo = 0, hi = G;                               // the adapter with chunk[g] <= chunk < chunk[g + 1]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -323,7 +469,9 @@ __global__ void __launch_bounds__(kOutThreads)
   const int g = lo, ch0 = __ldcg(t.chunk + g);
   const int first = __ldcg(t.offset + g) + (chunk - ch0) * kChunkRows;
   const int n = min(kChunkRows, __ldcg(t.offset + g + 1) - first);
-  const int64_t c0 = (int64_t)blockIdx.x * kOutC;
+  for (int i = tid; i < n; i += kOutThreads) rows[i] = __ldcg(t.row + first + i);
+  __syncthreads();
+  const int64_t c0 = (int64_t)((int)blockIdx.x < blocks0 ? blockIdx.x : blockIdx.x - blocks0) * kOutC;
   const int cn = (int)min((int64_t)kOutC, C - c0);
   const int r0 = blockIdx.z * 64, rc = (int)min((int64_t)64, l.R - r0), nt = (rc + 7) / 8;
   const uint32_t ring = shared_u32(sm);
@@ -335,14 +483,14 @@ __global__ void __launch_bounds__(kOutThreads)
       const int e = tid + q * kOutThreads, r = e >> 4, c = (e & 15) * 8;
       const int at = i * kOutRows + r;
       const int ok = at < n ? max(0, min(8, cn - c)) : 0;
-      const T* src = ok ? x + (int64_t)__ldcg(t.row + first + at) * x_rs + c0 + c : x;
+      const T* src = ok ? p.x + (int64_t)rows[at] * p.x_rs + c0 + c : p.x;
       cp_async<16>(s + (uint32_t)(r * kOutXPitch + c * 2), src, ok * 2);
     }
     const int r = tid >> 3, c = (tid & 7) * 8;      // 32 rows x 8 pieces of z
     const int at = i * kOutRows + r;
     if (c < nt * 8) {
       const bool ok = at < n;
-      const T* src = ok ? zt + (int64_t)__ldcg(t.row + first + at) * zt_ld + r0 + c : zt;
+      const T* src = ok ? p.zt + (int64_t)rows[at] * zt_ld + r0 + c : p.zt;
       cp_async<16>(s + (uint32_t)(kOutRows * kOutXPitch + r * kOutZPitch + c * 2), src, ok ? 16 : 0);
     }
   };
@@ -377,7 +525,8 @@ __global__ void __launch_bounds__(kOutThreads)
     }
   }
   const bool whole = __ldcg(t.chunk + g + 1) - ch0 == 1;
-  float* mine = part + (int64_t)(__ldcg(t.part + g) + chunk - ch0) * C * l.R;
+  float* mine = p.part + (int64_t)(__ldcg(t.part + g) + chunk - ch0) * C * l.R;
+  T* out = p.out + (int64_t)g * C * l.R;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (j >= nt) break;
@@ -386,81 +535,52 @@ __global__ void __launch_bounds__(kOutThreads)
       const int64_t c = c0 + warp * 16 + (lane >> 2) + (e >> 1) * 8;
       const int r = r0 + j * 8 + (lane & 3) * 2 + (e & 1);
       if (c >= C || r >= l.R) continue;
-      if (whole) out[g * o_gs + c * o_cs + r * o_rs] = from_f32<T>(acc[j][e]);
-      else mine[c * o_cs + r * o_rs] = acc[j][e];
+      if (whole) out[c * p.o_cs + r * p.o_rs] = from_f32<T>(acc[j][e]);
+      else mine[c * p.o_cs + r * p.o_rs] = acc[j][e];
     }
   }
 }
 
 // The adapters with several chunks (their sum) or none (zeros); element e of
-// an adapter's [C, R] in the output's own order.
+// an adapter's [C, R] in the output's own order.  grid.z: the problems.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    outer_sum_kernel(const LowRankArgs l, const AdapterRows t, int64_t C, T* out, const float* part) {
+    outer_sum_kernel(const LowRankArgs l, const AdapterRows t, const OuterProblem<T> p0, const OuterProblem<T> p1) {
   pdl_begin();
-  const int64_t n = C * l.R;
+  const OuterProblem<T>& p = blockIdx.z == 0 ? p0 : p1;
+  const int64_t n = p.C * l.R;
   for (int g = blockIdx.y; g < l.G; g += gridDim.y) {
     const int k = __ldcg(t.chunk + g + 1) - __ldcg(t.chunk + g);
     if (k == 1) continue;
-    const float* src = part + (int64_t)__ldcg(t.part + g) * n;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
-      float v = 0.f;
+    const float* src = p.part + (int64_t)__ldcg(t.part + g) * n;
+    if (n % 4 == 0) {
+      for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; e < n; e += (int64_t)gridDim.x * 1024) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int c = 0; c < k; ++c) v += __ldcg(src + (int64_t)c * n + e);
-      out[(int64_t)g * n + e] = from_f32<T>(v);
+        for (int c = 0; c < k; ++c) {
+          const float4 u = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)c * n + e));
+          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+        T o[4] = {from_f32<T>(v.x), from_f32<T>(v.y), from_f32<T>(v.z), from_f32<T>(v.w)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p.out[(int64_t)g * n + e + j] = o[j];
+      }
+    } else {
+      for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+        float v = 0.f;
+        for (int c = 0; c < k; ++c) v += __ldcg(src + (int64_t)c * n + e);
+        p.out[(int64_t)g * n + e] = from_f32<T>(v);
+      }
     }
   }
 }
 
 // ------------------------------------------------------------------ the fused product's operands
 
-constexpr int kSlotThreads = 1024;
-
-// One block: the adapters in use, ascending, get slots 0, 1, .. (-1 past kSlots).
-__global__ void __launch_bounds__(kSlotThreads) adapter_slots_kernel(const LowRankArgs l, const FusedTables t) {
-  pdl_begin();
-  extern __shared__ uint32_t used[];               // one bit per adapter
-  __shared__ int wsum[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, words = (int)((l.G + 31) / 32);
-  for (int i = tid; i < words; i += kSlotThreads) used[i] = 0u;
-  __syncthreads();
-  for (int64_t m = tid; m < l.M; m += kSlotThreads) {
-    const int64_t g = load_index(l.idx, m * l.idx_s, l.ind64);
-    if (g >= 0 && g < l.G) {
-      const uint32_t bit = 1u << (g & 31);
-      if (!(used[g >> 5] & bit)) atomicOr(used + (g >> 5), bit);
-    }
-  }
-  __syncthreads();
-  const int per = (words + kSlotThreads - 1) / kSlotThreads, lo = min(words, tid * per), hi = min(words, lo + per);
-  int n = 0;
-  for (int i = lo; i < hi; ++i) n += __popc(used[i]);
-  int s = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += u;
-  }
-  if (lane == 31) wsum[warp] = s;
-  __syncthreads();
-  s -= n;
-  for (int w = 0; w < warp; ++w) s += wsum[w];
-  for (int i = lo; i < hi; ++i)
-    for (uint32_t b = used[i]; b; b &= b - 1, ++s) {
-      const int g = i * 32 + __ffs(b) - 1;
-      t.slot_of[g] = s < kSlots ? s : -1;
-      if (s < kSlots) t.adapter_of[s] = g;
-    }
-  if (tid == kSlotThreads - 1) {
-    t.head[0] = min(s, kSlots);
-    t.head[1] = 0;                                  // rows or adapters left for the fix
-  }
-  if (tid < kSlots) t.bad[tid] = 0;
-}
-
-// Blocks [0, tiles): a row tile's adapters (the first kExtPerTile in order of
-// appearance) and its blocks of factor rows.  The others: the adapters'
-// copies, 1024 columns of one slot a block.
+// Blocks [0, kPlaceParts * tiles): a row tile's adapters (the first
+// kExtPerTile in order of appearance) and a part of its blocks of factor rows.
+// The others: the adapters' copies, 1024 columns of one slot a block.
+constexpr int kPlaceParts = 4;
 template <typename T>
 __global__ void __launch_bounds__(256)
     lowrank_place_kernel(const LowRankArgs l, const FusedTables t, const int tile_rows, const int tiles, const T* zt,
@@ -469,10 +589,10 @@ __global__ void __launch_bounds__(256)
                          const int pieces, const int vec) {
   pdl_begin();
   const int tid = threadIdx.x;
-  if ((int)blockIdx.x < tiles) {
+  if ((int)blockIdx.x < tiles * kPlaceParts) {
     __shared__ int first, list[kExtPerTile];
     __shared__ signed char entry[256];
-    const int tile = blockIdx.x;
+    const int tile = blockIdx.x / kPlaceParts, part = blockIdx.x % kPlaceParts;
     const int64_t m = (int64_t)tile * tile_rows + tid;
     int slot = -1;
     bool has = false;
@@ -494,45 +614,89 @@ __global__ void __launch_bounds__(256)
       if (slot >= 0 && slot == list[n]) mine = n;
     }
     entry[tid] = (signed char)mine;
-    if (tid < n) t.ext_slot[tile * kExtPerTile + tid] = list[tid];
-    if (tid == 0) t.ext_count[tile] = n;
-    if (tid < tile_rows && m < l.M) {
+    if (part == 0 && tid < n) t.ext_slot[tile * kExtPerTile + tid] = list[tid];
+    if (part == 0 && tid == 0) t.ext_count[tile] = n;
+    if (part == 0 && tid < tile_rows && m < l.M) {
       t.row_entry[m] = mine;
       if (has && mine < 0) atomicOr(t.head + 1, 1);
     }
     __syncthreads();
     const int pieces_row = (int)(f_ld / 8), total = n * tile_rows * pieces_row;
-    for (int i = tid; i < total; i += 256) {
-      const int row = i / pieces_row, c = (i - row * pieces_row) * 8;     // row of the tile's n blocks
-      const int r = row % tile_rows, j = row / tile_rows;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (entry[r] == j && c < zt_ld)
-        v = __ldcg(reinterpret_cast<const uint4*>(zt + ((int64_t)tile * tile_rows + r) * zt_ld + c));
-      *reinterpret_cast<uint4*>(factors + ((int64_t)tile * kExtPerTile * tile_rows + row) * f_ld + c) = v;
+    constexpr int kAhead = 4;                             // reads in flight before the first write
+    for (int i0 = part * 256 + tid; i0 < total; i0 += 256 * kPlaceParts * kAhead) {
+      uint4 v[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int i = i0 + q * 256 * kPlaceParts;
+        const int row = i / pieces_row, c = (i - row * pieces_row) * 8;     // row of the tile's n blocks
+        const int r = row % tile_rows, j = row / tile_rows;
+        v[q] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < total && entry[r] == j && c < zt_ld)
+          v[q] = __ldcg(reinterpret_cast<const uint4*>(zt + ((int64_t)tile * tile_rows + r) * zt_ld + c));
+      }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int i = i0 + q * 256 * kPlaceParts;
+        if (i < total)
+          *reinterpret_cast<uint4*>(factors + (int64_t)tile * kExtPerTile * tile_rows * f_ld + (int64_t)i * 8) = v[q];
+      }
     }
     return;
   }
-  const int piece = ((int)blockIdx.x - tiles) % pieces, slot = ((int)blockIdx.x - tiles) / pieces;
+  const int rest = (int)blockIdx.x - tiles * kPlaceParts;
+  const int piece = rest % pieces, slot = rest / pieces;
   if (slot >= __ldcg(t.head)) return;
-  const int64_t n = ((int64_t)piece * 128 + (tid & 127)) * 8;
-  if (n >= c_ld) return;
   constexpr uint16_t kExp = std::is_same<T, __half>::value ? 0x7C00 : 0x7F80;
-  const uint16_t* src = reinterpret_cast<const uint16_t*>(b) + (int64_t)__ldcg(t.adapter_of + slot) * b_gs + n * b_ns;
+  const uint16_t* src = reinterpret_cast<const uint16_t*>(b) + (int64_t)__ldcg(t.adapter_of + slot) * b_gs;
+  uint16_t* dst = reinterpret_cast<uint16_t*>(copy) + (int64_t)slot * l.R * c_ld;
   bool bad = false;
-#pragma unroll 4
-  for (int64_t r = tid >> 7; r < l.R; r += 2) {
-    uint4 u;
-    uint16_t* e = reinterpret_cast<uint16_t*>(&u);
-    if (vec && n + 8 <= N) {
-      u = *reinterpret_cast<const uint4*>(src + r * b_rs);
-    } else {
+  auto finite = [&](uint16_t v) {
+    const bool f = (v & kExp) != kExp;
+    bad |= !f;
+    return f ? v : (uint16_t)0;
+  };
+  constexpr int kAhead = 8;
+  if (vec == 1) {                                          // n contiguous: 8 columns of every other rank
+    const int64_t n = ((int64_t)piece * 128 + (tid & 127)) * 8;
+    for (int64_t r0 = tid >> 7; n < N && r0 < l.R; r0 += 2 * kAhead) {
+      uint4 u[kAhead];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = n + j < N ? src[r * b_rs + j * b_ns] : (uint16_t)0;
+      for (int q = 0; q < kAhead; ++q) u[q] = *reinterpret_cast<const uint4*>(src + min(r0 + 2 * q, l.R - 1) * b_rs + n);
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        uint16_t* e = reinterpret_cast<uint16_t*>(&u[q]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = finite(e[j]);
+        if (r0 + 2 * q < l.R) *reinterpret_cast<uint4*>(dst + (r0 + 2 * q) * c_ld + n) = u[q];
+      }
     }
+  } else {                                                 // 4 columns, 8 ranks of each at a time
+    for (int64_t r0 = 0; r0 < l.R; r0 += 8) {
+      uint4 u[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if ((e[j] & kExp) == kExp) { e[j] = 0; bad = true; }
-    *reinterpret_cast<uint4*>(copy + ((int64_t)slot * l.R + r) * c_ld + n) = u;
+      for (int q = 0; q < 4; ++q) {
+        const int64_t n = (int64_t)piece * 1024 + q * 256 + tid;
+        u[q] = make_uint4(0u, 0u, 0u, 0u);
+        if (n >= N) continue;
+        const uint16_t* col = src + n * b_ns + r0 * b_rs;
+        if (vec == 2) {
+          u[q] = *reinterpret_cast<const uint4*>(col);
+        } else {
+          uint16_t* e = reinterpret_cast<uint16_t*>(&u[q]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (r0 + j < l.R) e[j] = col[j * b_rs];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t n = (int64_t)piece * 1024 + q * 256 + tid;
+        const uint16_t* e = reinterpret_cast<const uint16_t*>(&u[q]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (n < c_ld && r0 + j < l.R) dst[(r0 + j) * c_ld + n] = finite(e[j]);
+      }
+    }
   }
   if (bad) {
     atomicOr(t.bad + slot, 1);
@@ -575,56 +739,90 @@ bool rows16(const void* x, int64_t rs, int64_t cs, int64_t rows) {
   return cs == 1 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && (rs % 8 == 0 || rows == 1);
 }
 
-template <typename T>
-mm_status shrink_launch(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a, int64_t a_gs,
-                        int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld, cudaStream_t stream) {
-  const bool ck = a_rs != 1;            // c is a's unit-stride dimension
-  const int64_t ld = ck ? a_rs : a_cs;
-  int per = 8;                          // elements per copy of a, by its alignment
-  while (per > 1 && (reinterpret_cast<uintptr_t>(a) % (per * 2) || (l.G > 1 && a_gs % per) || ld % per)) per >>= 1;
-  const int rc = (int)(l.R < 64 ? l.R : 64);
-  int smem = kShPairs * kShStages * (kShXBytes + shrink_a_bytes(ck, rc));
-  const int red = kShPairs * kShRows * 68 * 4;
-  if (smem < red) smem = red;
-  const dim3 grid((unsigned)((l.M + kShRows - 1) / kShRows), (unsigned)((l.R + 63) / 64));
-  const auto kernel = ck ? shrink_tiles_kernel<T, true> : shrink_tiles_kernel<T, false>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
-    return MM_ERR_CUDA;
-  return launch_pdl(kernel, grid, dim3(kShThreads), (size_t)smem, stream, l, static_cast<const T*>(x), x_rs, C,
-                    static_cast<const T*>(a), a_gs, ld, per, z, static_cast<T*>(zt), zt_ld) == cudaSuccess ? MM_OK
-                                                                                                          : MM_ERR_CUDA;
+// x [M, C] as a tensor map of 32-row, 64-column tiles.
+bool shrink_map(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, OperandPlan* out) {
+  BatchMap one;
+  memset(&one, 0, sizeof(one));
+  one.count = 1;
+  for (int d = 0; d < kMaxBatchDims; ++d) one.shape[d] = 1;
+  const int64_t none[kMaxBatchDims] = {};
+  const int64_t rs = l.M == 1 ? (C + 7) / 8 * 8 : x_rs;     // one row: its stride is never used
+  return plan_operand(x, l.dtype, l.M, C, rs, 1, one, none, kShRows, out) && !out->mn_major;
 }
 
 template <typename T>
-mm_status outer_launch(const LowRankArgs& l, const AdapterRows& t, const void* x, int64_t x_rs, int64_t C, const void* zt,
-                       int64_t zt_ld, void* out, int64_t o_gs, int64_t o_cs, int64_t o_rs, float* part,
-                       cudaStream_t stream) {
-  const int64_t chunks = lowrank_max_chunks(l);
-  const dim3 grid((unsigned)((C + kOutC - 1) / kOutC), (unsigned)chunks, (unsigned)((l.R + 63) / 64));
-  const int smem = kOutStages * kOutStage;
-  if (chunks > 0 &&
-      launch_pdl(outer_tiles_kernel<T>, grid, dim3(kOutThreads), (size_t)smem, stream, l, t, static_cast<const T*>(x), x_rs,
-                 C, static_cast<const T*>(zt), zt_ld, static_cast<T*>(out), o_gs, o_cs, o_rs, part) != cudaSuccess)
+mm_status shrink_launch(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a, int64_t a_gs,
+                        int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld, const FusedTables* slots,
+                        const AdapterRows* sort, cudaStream_t stream) {
+  const bool ck = a_rs != 1;            // c is a's unit-stride dimension
+  ShrinkArgs p;
+  memset(&p, 0, sizeof(p));
+  p.C = C;
+  p.a = a; p.a_gs = a_gs; p.a_ld = ck ? a_rs : a_cs;
+  p.per = 8;
+  while (p.per > 1 && (reinterpret_cast<uintptr_t>(a) % (p.per * 2) || (l.G > 1 && a_gs % p.per) || p.a_ld % p.per))
+    p.per >>= 1;
+  p.z = z; p.zt = zt; p.zt_ld = zt_ld;
+  TcParams limits;                      // the pipelines' wait limits
+  init_params(&limits);
+  p.timeout_ns = limits.timeout_ns; p.teardown_ns = limits.teardown_ns;
+  OperandPlan map;
+  if (!shrink_map(l, x, x_rs, C, &map)) return MM_ERR_UNSUPPORTED;
+  const int rc = (int)(l.R < 64 ? l.R : 64);
+  int smem = shrink_smem(ck, rc);
+  const int tables = (int)(sort ? kShWarps * l.G * 4 : 0), bits = (int)(slots ? (l.G + 31) / 32 * 4 : 0);
+  for (int need : {tables, bits})
+    if (smem < need) smem = need;
+  p.tiles = (int)((l.M + kShRows - 1) / kShRows);
+  const dim3 grid((unsigned)(p.tiles + (slots ? 1 : 0) + (sort ? 1 : 0)), (unsigned)((l.R + 63) / 64));
+  const auto kernel = ck ? (rc <= 16 ? shrink_tiles_kernel<T, true, 2> : rc <= 32 ? shrink_tiles_kernel<T, true, 4>
+                                                                               : shrink_tiles_kernel<T, true, 8>)
+                         : (rc <= 16 ? shrink_tiles_kernel<T, false, 2> : rc <= 32 ? shrink_tiles_kernel<T, false, 4>
+                                                                                : shrink_tiles_kernel<T, false, 8>);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024) != cudaSuccess)
     return MM_ERR_CUDA;
-  const int64_t n = C * l.R;
-  const dim3 gs((unsigned)((n + 1023) / 1024 < 64 ? (n + 1023) / 1024 : 64), (unsigned)l.G);
-  return launch_pdl(outer_sum_kernel<T>, gs, dim3(256), 0, stream, l, t, C, static_cast<T*>(out), (const float*)part) ==
-                 cudaSuccess ? MM_OK : MM_ERR_CUDA;
+  return launch_pdl(kernel, grid, dim3(kShThreads), (size_t)smem, stream, map.map, l, p, slots ? *slots : FusedTables{},
+                    sort ? *sort : AdapterRows{}) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+}
+
+template <typename T>
+mm_status outer_launch(const LowRankArgs& l, const AdapterRows& t, const LowRankOuter* o, int problems, int64_t zt_ld,
+                       cudaStream_t stream) {
+  OuterProblem<T> p[2];
+  int64_t blocks[2] = {0, 0}, most = 0;
+  for (int i = 0; i < 2; ++i) {
+    const LowRankOuter& q = o[i < problems ? i : 0];
+    p[i] = {static_cast<const T*>(q.x), q.x_rs, q.C, static_cast<const T*>(q.zt), static_cast<T*>(q.out), q.o_cs, q.o_rs,
+            q.part};
+    if (i < problems) blocks[i] = (q.C + kOutC - 1) / kOutC;
+    if (q.C > most) most = q.C;
+  }
+  const int64_t chunks = lowrank_max_chunks(l);
+  const dim3 grid((unsigned)(blocks[0] + blocks[1]), (unsigned)chunks, (unsigned)((l.R + 63) / 64));
+  if (chunks > 0 && launch_pdl(outer_tiles_kernel<T>, grid, dim3(kOutThreads), (size_t)(kOutStages * kOutStage), stream, l,
+                               t, p[0], p[1], (int)blocks[0], zt_ld) != cudaSuccess)
+    return MM_ERR_CUDA;
+  const int64_t gx = (most * l.R + 1023) / 1024;
+  const dim3 gs((unsigned)(gx < 64 ? gx : 64), (unsigned)l.G, (unsigned)problems);
+  return launch_pdl(outer_sum_kernel<T>, gs, dim3(256), 0, stream, l, t, p[0], p[1]) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
 }  // namespace
 
 bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
                                     int64_t a_cs, int64_t a_rs) {
+  OperandPlan map;
   return (l.dtype == MM_BF16 || l.dtype == MM_F16) && l.M >= 1 && l.R >= 1 && l.G >= 1 && l.G <= 0x7fffffffLL && C >= 1 &&
-         l.M <= 0x7fffffffLL && l.R <= 64 * 65535LL && rows16(x, x_rs, x_cs, l.M) && (a_rs == 1 || a_cs == 1);
+         l.M <= 0x7fffffffLL && l.R <= 64 * 65535LL && rows16(x, x_rs, x_cs, l.M) && (a_rs == 1 || a_cs == 1) &&
+         shrink_map(l, x, x_rs, C, &map);
 }
 
 mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a,
                                       int64_t a_gs, int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld,
-                                      cudaStream_t stream) {
-  return l.dtype == MM_F16 ? shrink_launch<__half>(l, x, x_rs, C, a, a_gs, a_cs, a_rs, z, zt, zt_ld, stream)
-                           : shrink_launch<__nv_bfloat16>(l, x, x_rs, C, a, a_gs, a_cs, a_rs, z, zt, zt_ld, stream);
+                                      const FusedTables* slots, const AdapterRows* sort, cudaStream_t stream) {
+  return l.dtype == MM_F16
+             ? shrink_launch<__half>(l, x, x_rs, C, a, a_gs, a_cs, a_rs, z, zt, zt_ld, slots, sort, stream)
+             : shrink_launch<__nv_bfloat16>(l, x, x_rs, C, a, a_gs, a_cs, a_rs, z, zt, zt_ld, slots, sort, stream);
 }
 
 namespace {
@@ -634,9 +832,12 @@ mm_status place_launch(const LowRankArgs& l, const FusedTables& t, int tile_rows
                        void* factors, int64_t f_ld, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns, int64_t N,
                        void* copy, int64_t c_ld, int64_t slots, cudaStream_t stream) {
   const int64_t tiles = (l.M + tile_rows - 1) / tile_rows, pieces = (c_ld + 1023) / 1024;
-  const int64_t blocks = tiles + slots * pieces;
+  const int64_t blocks = tiles * kPlaceParts + slots * pieces;
   if (blocks > 0x7fffffffLL) return MM_ERR_UNSUPPORTED;
-  const int vec = b_ns == 1 && b_rs % 8 == 0 && (l.G == 1 || b_gs % 8 == 0) && reinterpret_cast<uintptr_t>(b) % 16 == 0;
+  // 16-byte reads along n (1) or along the ranks (2)
+  const bool base = (l.G == 1 || b_gs % 8 == 0) && reinterpret_cast<uintptr_t>(b) % 16 == 0;
+  const int vec = base && b_ns == 1 && b_rs % 8 == 0 && N % 8 == 0   ? 1
+                  : base && b_rs == 1 && b_ns % 8 == 0 && l.R % 8 == 0 ? 2 : 0;
   return launch_pdl(lowrank_place_kernel<T>, dim3((unsigned)blocks), dim3(256), 0, stream, l, t, tile_rows, (int)tiles,
                     static_cast<const T*>(zt), zt_ld, static_cast<T*>(factors), f_ld, static_cast<const T*>(b), b_gs, b_rs,
                     b_ns, N, static_cast<T*>(copy), c_ld, (int)pieces, vec) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
@@ -683,10 +884,7 @@ bool lowrank_fused_supported(const LowRankArgs& l, const GemmArgs& g) {
          l.M * kExtPerTile < (1ll << 30) && tc_lowrank_tile_rows(g) != 0;
 }
 
-// slots, then (z and zt by the caller's shrink) place, product, fix.
-mm_status launch_lowrank_fused(const LowRankArgs& l, const GemmArgs& g, const FusedLayout& w, char* ws, const float* z,
-                               const void* zt, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
-                               cudaStream_t stream) {
+FusedTables lowrank_fused_tables(const FusedLayout& w, char* ws) {
   FusedTables t;
   t.head = reinterpret_cast<int32_t*>(ws + w.head);
   t.slot_of = reinterpret_cast<int32_t*>(ws + w.slot_of);
@@ -695,6 +893,14 @@ mm_status launch_lowrank_fused(const LowRankArgs& l, const GemmArgs& g, const Fu
   t.row_entry = reinterpret_cast<int32_t*>(ws + w.row_entry);
   t.ext_count = reinterpret_cast<int32_t*>(ws + w.ext_count);
   t.ext_slot = reinterpret_cast<int32_t*>(ws + w.ext_slot);
+  return t;
+}
+
+// After the shrink that made z, zt and the slots: place, product, fix.
+mm_status launch_lowrank_fused(const LowRankArgs& l, const GemmArgs& g, const FusedLayout& w, char* ws, const float* z,
+                               const void* zt, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
+                               cudaStream_t stream) {
+  const FusedTables t = lowrank_fused_tables(w, ws);
   void* factors = ws + w.factors;
   void* copy = ws + w.copy;
   void* y = const_cast<void*>(g.y.ptr);
@@ -703,9 +909,6 @@ mm_status launch_lowrank_fused(const LowRankArgs& l, const GemmArgs& g, const Fu
   e.factors = factors; e.factor_ld = w.f_ld;
   e.adapters = copy; e.slots = w.slots; e.R = l.R; e.adapter_ld = w.c_ld;
   e.count = t.ext_count; e.slot = t.ext_slot;
-  const int smem = (int)((l.G + 31) / 32 * 4);
-  if (launch_pdl(adapter_slots_kernel, dim3(1), dim3(kSlotThreads), (size_t)smem, stream, l, t) != cudaSuccess)
-    return MM_ERR_CUDA;
   const bool f16 = l.dtype == MM_F16;
   mm_status s = f16 ? place_launch<__half>(l, t, e.tile_rows, zt, w.zt_ld, factors, w.f_ld, b, b_gs, b_rs, b_ns, g.N, copy,
                                            w.c_ld, w.slots, stream)
@@ -717,23 +920,10 @@ mm_status launch_lowrank_fused(const LowRankArgs& l, const GemmArgs& g, const Fu
              : fix_launch<__nv_bfloat16>(l, t, z, b, b_gs, b_rs, b_ns, g.N, y, stream);
 }
 
-bool lowrank_sort_supported(const LowRankArgs& l) { return l.G >= 1 && l.G <= kSortAdapters && l.M <= 0x7fffffffLL; }
-
-mm_status launch_lowrank_sort(const LowRankArgs& l, const AdapterRows& t, cudaStream_t stream) {
-  const int smem = (int)(32 * l.G * 4);
-  if (cudaFuncSetAttribute(adapter_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * (int)kSortAdapters * 4) !=
-      cudaSuccess)
-    return MM_ERR_CUDA;
-  return launch_pdl(adapter_sort_kernel, dim3(1), dim3(kSortThreads), (size_t)smem, stream, l, t) == cudaSuccess
-             ? MM_OK : MM_ERR_CUDA;
-}
-
-mm_status launch_lowrank_outer_tiles(const LowRankArgs& l, const AdapterRows& t, const void* x, int64_t x_rs, int64_t C,
-                                     const void* zt, int64_t zt_ld, void* out, int64_t o_gs, int64_t o_cs, int64_t o_rs,
-                                     float* part, cudaStream_t stream) {
-  return l.dtype == MM_F16
-             ? outer_launch<__half>(l, t, x, x_rs, C, zt, zt_ld, out, o_gs, o_cs, o_rs, part, stream)
-             : outer_launch<__nv_bfloat16>(l, t, x, x_rs, C, zt, zt_ld, out, o_gs, o_cs, o_rs, part, stream);
+mm_status launch_lowrank_outer_tiles(const LowRankArgs& l, const AdapterRows& t, const LowRankOuter* o, int problems,
+                                     int64_t zt_ld, cudaStream_t stream) {
+  return l.dtype == MM_F16 ? outer_launch<__half>(l, t, o, problems, zt_ld, stream)
+                           : outer_launch<__nv_bfloat16>(l, t, o, problems, zt_ld, stream);
 }
 
 }  // namespace qg
