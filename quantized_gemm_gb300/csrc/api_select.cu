@@ -229,7 +229,7 @@ size_t factor_bytes(const LowRankArgs& l) {
 struct GradLayout {
   int64_t zt_ld;
   FusedLayout fused;     // dX's product; its z and zt are V's
-  size_t u, ut, row, offset, chunk, part, sums_a, sums_b, total;
+  size_t u, ut, row, offset, sums_a, sums_b, total;
 };
 GradLayout grad_layout(const LowRankPlan& p) {
   const LowRankArgs& l = p.l;
@@ -242,8 +242,6 @@ GradLayout grad_layout(const LowRankPlan& p) {
   w.ut = take((size_t)l.M * (size_t)w.zt_ld * 2);
   w.row = take((size_t)l.M * 4);
   w.offset = take((size_t)(l.G + 1) * 4);
-  w.chunk = take((size_t)(l.G + 1) * 4);
-  w.part = take((size_t)l.G * 4);
   w.sums_a = take((size_t)lowrank_max_parts(l) * (size_t)p.K * (size_t)l.R * 4);
   w.sums_b = take((size_t)lowrank_max_parts(l) * (size_t)p.N * (size_t)l.R * 4);
   w.total = o;
@@ -392,8 +390,7 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
     char* ws = static_cast<char*>(workspace);
     float* zv = reinterpret_cast<float*>(ws + w.fused.z);
     void* vt = ws + w.fused.zt;
-    const AdapterRows t = {reinterpret_cast<int32_t*>(ws + w.row), reinterpret_cast<int32_t*>(ws + w.offset),
-                           reinterpret_cast<int32_t*>(ws + w.chunk), reinterpret_cast<int32_t*>(ws + w.part)};
+    const AdapterRows t = {reinterpret_cast<int32_t*>(ws + w.row), reinterpret_cast<int32_t*>(ws + w.offset)};
     const FusedTables slots = lowrank_fused_tables(w.fused, ws);
     const bool sort_with_u = dB != nullptr;
     if (dX || dA)

@@ -10,24 +10,25 @@
 namespace qg {
 
 constexpr int kChunkRows = 512;            // rows of one adapter that one block sums
-constexpr int64_t kSortAdapters = 1024;    // adapters that the sort's counters hold (shared memory)
+constexpr int64_t kSortAdapters = 4096;    // adapters that get a block each in the sort
 constexpr int kSlots = 128;                // adapters of one call that the fused product holds copies of
 
 // Rows in adapter order (device tables in the workspace).
 struct AdapterRows {
   int32_t* row;       // [M] rows that have an adapter
   int32_t* offset;    // [G + 1]
-  int32_t* chunk;     // [G + 1] first chunk of kChunkRows rows
-  int32_t* part;      // [G] first partial sum, counting the adapters of several chunks only
 };
-// More chunks than this cannot occur.
-inline int64_t lowrank_max_chunks(const LowRankArgs& l) {
-  return l.M / kChunkRows + (l.G < l.M ? l.G : l.M);
-}
-// Chunks of adapters with several: each such adapter has more than kChunkRows rows.
-inline int64_t lowrank_max_parts(const LowRankArgs& l) { return 2 * (l.M / kChunkRows); }
+// Adapter g's chunks of kChunkRows rows have the numbers from first_chunk(g)
+// on: at least as many numbers as chunks, since ceil(n / c) <= floor((o + n) /
+// c) - floor(o / c) + 1.  The partial sums of an adapter of several chunks (n
+// > c rows, so that ceil(n / c) <= floor(n / (c / 2))) start at first_part.
+__host__ __device__ __forceinline__ int first_chunk(int offset, int g) { return offset / kChunkRows + g; }
+__host__ __device__ __forceinline__ int first_part(int offset) { return offset / (kChunkRows / 2); }
+inline int64_t lowrank_max_chunks(const LowRankArgs& l) { return l.M / kChunkRows + l.G; }
+inline int64_t lowrank_max_parts(const LowRankArgs& l) { return l.M / (kChunkRows / 2) + 1; }
+// The sort's bitmap of the rows lives in shared memory.
 inline bool lowrank_sort_supported(const LowRankArgs& l) {
-  return l.G >= 1 && l.G <= kSortAdapters && l.M <= 0x7fffffffLL;
+  return l.G >= 1 && l.G <= kSortAdapters && l.M <= (1 << 20);
 }
 
 // Tables of the fused product Y = A B + z b (device, in the workspace).

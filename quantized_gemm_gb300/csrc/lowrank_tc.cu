@@ -100,7 +100,7 @@ __device__ __forceinline__ void load_block(uint32_t dst, int pitch, const T* src
 // turn, each with its own ring (no block barrier until the warps' sums meet in
 // shared memory): one lane streams 32 x 64 tiles of x by TMA (128-byte
 // swizzle), the adapter arrives by asynchronous copies of whatever width its
-// alignment allows.  Two blocks per SM keep some 96 KB of x in flight.  The
+// alignment allows.  Two blocks per SM (up to 16 ranks) keep 64 KB of x in flight.  The
 // tile is multiplied once per adapter that its rows name (rows of a request
 // are neighbours, so one or two); each pass keeps its own adapter's rows.
 constexpr int kShRows = 32, kShK = 64, kShWarps = 4, kShThreads = 32 * kShWarps;
@@ -111,11 +111,11 @@ constexpr int kShCtrl = 256;                   // barriers, abort flag
 __host__ __device__ constexpr int shrink_a_bytes(bool ck, int rc) {
   return ck ? (rc + 7) / 8 * 8 * kShKPitch : kShK * ((rc + 7) / 8 * 16 + 16);
 }
-__host__ __device__ constexpr int shrink_stages(int rc) { return rc <= 32 ? 4 : 3; }
+constexpr int kShStages = 3;
 __host__ __device__ constexpr int shrink_red_pitch(int rc) { return (rc + 7) / 8 * 8 + 4; }
 // [x rings][control][adapter rings][sums]
 __host__ __device__ constexpr int shrink_smem(bool ck, int rc) {
-  return 1024 + kShWarps * shrink_stages(rc) * (kShXBytes + shrink_a_bytes(ck, rc)) + kShCtrl +
+  return 1024 + kShWarps * kShStages * (kShXBytes + shrink_a_bytes(ck, rc)) + kShCtrl +
          kShWarps * kShRows * shrink_red_pitch(rc) * 4;
 }
 
@@ -136,7 +136,8 @@ __device__ void shrink_tile(const CUtensorMap* tmX, const LowRankArgs& l, const 
   const int64_t m0 = (int64_t)tile * kShRows, C = p.C;
   const int r0 = blockIdx.y * 64, rc = (int)min((int64_t)64, l.R - r0), nt = (rc + 7) / 8;
   const int rows = (int)min((int64_t)kShRows, l.M - m0);
-  const int stages = shrink_stages((int)min((int64_t)64, l.R)), a_bytes = shrink_a_bytes(CK, rc);
+  constexpr int stages = kShStages;
+  const int a_bytes = shrink_a_bytes(CK, rc);
   const int a_pitch = CK ? kShKPitch : nt * 16 + 16;
   const uint32_t raw = shared_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* sm = sm_raw + (base - raw);
@@ -220,8 +221,7 @@ __device__ void shrink_tile(const CUtensorMap* tmX, const LowRankArgs& l, const 
       cp_commit();
     }
     for (int i = 0; i < mine; ++i) {
-      if (stages == 4) cp_wait<2>();
-      else cp_wait<1>();
+      cp_wait<kShStages - 2>();
       ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar0 + 8 * dstage, dphase, abort, l.status, p.timeout_ns));
       if (!ok) break;
       __syncwarp();                      // block i has landed for every lane, and block i - 1 has been used
@@ -284,90 +284,50 @@ __device__ void shrink_tile(const CUtensorMap* tmX, const LowRankArgs& l, const 
 
 // ------------------------------------------------------------------ rows in adapter order
 
-// One block, a stable counting sort: warp w counts and then places the w-th
-// 8th of the rows, in order, so rows keep their order within an adapter and
-// sums over them do not depend on timing.
-__device__ void adapter_sort(const LowRankArgs& l, const AdapterRows& t, uint8_t* sm) {
-  int32_t* cnt = reinterpret_cast<int32_t*>(sm);    // [warps][G]
-  __shared__ int32_t wtot[kShWarps][3];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = (int)l.G;
-  for (int i = tid; i < kShWarps * G; i += kShThreads) cnt[i] = 0;
-  __syncthreads();
-  const int64_t per = ((l.M + kShWarps - 1) / kShWarps + 31) / 32 * 32, lo = warp * per, hi = min(l.M, lo + per);
-  int32_t* mine = cnt + warp * G;
-  constexpr int kAhead = 8;                         // index reads in flight
-  auto adapter = [&](int64_t m) {
-    if (m >= hi) return -1;
-    const int64_t g = load_index(l.idx, m * l.idx_s, l.ind64);
-    return g >= 0 && g < l.G ? (int)g : -1;
-  };
-  for (int64_t b = lo; b < hi; b += 32 * kAhead) {
-    int gs[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) gs[i] = adapter(b + 32 * i + lane);
+// Rows in adapter order, a block per adapter: it reads all the indices, marks
+// its own rows in a bitmap (a word per 32 rows, in shared memory) and counts
+// them and those of lower adapters; then it writes its rows, ascending, at
+// their place.  Sums over an adapter's rows therefore have a fixed order.
+__device__ void adapter_sort(const LowRankArgs& l, const AdapterRows& t, int g, uint8_t* sm) {
+  uint32_t* bits = reinterpret_cast<uint32_t*>(sm);
+  __shared__ int own[kShWarps], low[kShWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int words = (int)((l.M + 31) / 32), per = (words + kShWarps - 1) / kShWarps;
+  const int w0 = min(words, warp * per), w1 = min(words, w0 + per);
+  constexpr int kAhead = 16;                        // index reads in flight
+  int n = 0, below = 0;
+  for (int w = w0; w < w1; w += kAhead) {
+    int64_t v[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int g = gs[i];
-      const unsigned same = __match_any_sync(0xffffffffu, g);
-      if (g >= 0 && lane == __ffs(same) - 1) mine[g] += __popc(same);
-      __syncwarp();
+      const int64_t m = (int64_t)(w + i) * 32 + lane;
+      v[i] = w + i < w1 && m < l.M ? load_index(l.idx, m * l.idx_s, l.ind64) : -1;
     }
-  }
-  __syncthreads();
-  // Exclusive sums over (adapter, warp), adapter-major, a range of adapters per thread.
-  const int gp = (G + kShThreads - 1) / kShThreads, g0 = min(G, tid * gp), g1 = min(G, g0 + gp);
-  int rows = 0, chunks = 0, parts = 0;
-  for (int g = g0; g < g1; ++g) {
-    int c = 0;
-    for (int w = 0; w < kShWarps; ++w) c += cnt[w * G + g];
-    const int k = (c + kChunkRows - 1) / kChunkRows;
-    rows += c;
-    chunks += k;
-    parts += k > 1 ? k : 0;
-  }
-  int ir = rows, ic = chunks, ip = parts;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int ur = __shfl_up_sync(0xffffffffu, ir, o), uc = __shfl_up_sync(0xffffffffu, ic, o);
-    const int up = __shfl_up_sync(0xffffffffu, ip, o);
-    if (lane >= o) { ir += ur; ic += uc; ip += up; }
-  }
-  if (lane == 31) { wtot[warp][0] = ir; wtot[warp][1] = ic; wtot[warp][2] = ip; }
-  __syncthreads();
-  int pr = ir - rows, pc = ic - chunks, pp = ip - parts;
-  for (int w = 0; w < warp; ++w) { pr += wtot[w][0]; pc += wtot[w][1]; pp += wtot[w][2]; }
-  for (int g = g0; g < g1; ++g) {
-    t.offset[g] = pr;
-    t.chunk[g] = pc;
-    t.part[g] = pp;
-    const int first = pr;
-    for (int w = 0; w < kShWarps; ++w) {
-      const int c = cnt[w * G + g];
-      cnt[w * G + g] = pr;
-      pr += c;
-    }
-    const int k = (pr - first + kChunkRows - 1) / kChunkRows;
-    pc += k;
-    pp += k > 1 ? k : 0;
-  }
-  if (tid == kShThreads - 1) { t.offset[G] = pr; t.chunk[G] = pc; }
-  __syncthreads();
-  for (int64_t b = lo; b < hi; b += 32 * kAhead) {
-    int gs[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) gs[i] = adapter(b + 32 * i + lane);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int g = gs[i];
-      const unsigned same = __match_any_sync(0xffffffffu, g);
-      const int at = g >= 0 ? mine[g] + __popc(same & ((1u << lane) - 1u)) : 0;
-      __syncwarp();
-      if (g >= 0) {
-        t.row[at] = (int32_t)(b + 32 * i + lane);
-        if (lane == __ffs(same) - 1) mine[g] += __popc(same);
-      }
-      __syncwarp();
+      const unsigned eq = __ballot_sync(0xffffffffu, v[i] == g);
+      below += __popc(__ballot_sync(0xffffffffu, v[i] >= 0 && v[i] < g));
+      n += __popc(eq);
+      if (lane == 0 && w + i < w1) bits[w + i] = eq;
     }
+  }
+  if (lane == 0) { own[warp] = n; low[warp] = below; }
+  __syncthreads();
+  int first = 0, at = 0, all = 0;
+  for (int w = 0; w < kShWarps; ++w) {
+    first += low[w];
+    all += own[w];
+    if (w < warp) at += own[w];
+  }
+  at += first;
+  if (tid == 0) {
+    t.offset[g] = first;
+    if (g == l.G - 1) t.offset[g + 1] = first + all;
+  }
+  for (int w = w0; w < w1; ++w) {
+    const uint32_t b = bits[w];
+    if ((b >> lane) & 1u) t.row[at + __popc(b & ((1u << lane) - 1u))] = w * 32 + lane;
+    at += __popc(b);
   }
 }
 
@@ -413,7 +373,7 @@ __device__ void adapter_slots(const LowRankArgs& l, const FusedTables& t, uint8_
 }
 
 // The first blocks make the tables that later launches want (they depend on
-// the indices alone): slots, then the sort; the others shrink one tile each.
+// the indices alone): slots, then the sorted rows; the others shrink one tile each.
 template <typename T, bool CK, int NT>
 __global__ void __launch_bounds__(kShThreads, NT <= 4 ? 2 : 1)
     shrink_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const LowRankArgs l, const ShrinkArgs p,
@@ -424,8 +384,9 @@ __global__ void __launch_bounds__(kShThreads, NT <= 4 ? 2 : 1)
   if (tile >= 0) {
     shrink_tile<T, CK, NT>(&tmX, l, p, tile, sm);
   } else if (blockIdx.y == 0) {
-    if (blockIdx.x == 0 && slots.head) adapter_slots(l, slots, sm);
-    else adapter_sort(l, sort, sm);
+    const int b = (int)blockIdx.x - (slots.head ? 1 : 0);
+    if (b < 0) adapter_slots(l, slots, sm);
+    else adapter_sort(l, sort, b, sm);
   }
 }
 
@@ -456,19 +417,19 @@ __global__ void __launch_bounds__(kOutThreads)
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ int32_t rows[kChunkRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = (int)l.G;
-  const int chunk = blockIdx.y;
-  if (chunk >= __ldcg(t.chunk + G)) return;
   const OuterProblem<T>& p = (int)blockIdx.x < blocks0 ? p0 : p1;
   const int64_t C = p.C;
-  int lo = 0, hi = G;                               // the adapter with chunk[g] <= chunk < chunk[g + 1]
+  int lo = 0, hi = G;                               // the adapter with first_chunk(g) <= chunk < first_chunk(g + 1)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldcg(t.chunk + mid) <= chunk) lo = mid;
+    if (first_chunk(__ldcg(t.offset + mid), mid) <= (int)blockIdx.y) lo = mid;
     else hi = mid;
   }
-  const int g = lo, ch0 = __ldcg(t.chunk + g);
-  const int first = __ldcg(t.offset + g) + (chunk - ch0) * kChunkRows;
-  const int n = min(kChunkRows, __ldcg(t.offset + g + 1) - first);
+  const int g = lo, begin = __ldcg(t.offset + g), end = __ldcg(t.offset + g + 1);
+  const int chunk = (int)blockIdx.y - first_chunk(begin, g);          // of this adapter
+  const int first = begin + chunk * kChunkRows;
+  const int n = min(kChunkRows, end - first);
+  if (n <= 0) return;
   for (int i = tid; i < n; i += kOutThreads) rows[i] = __ldcg(t.row + first + i);
   __syncthreads();
   const int64_t c0 = (int64_t)((int)blockIdx.x < blocks0 ? blockIdx.x : blockIdx.x - blocks0) * kOutC;
@@ -476,22 +437,25 @@ __global__ void __launch_bounds__(kOutThreads)
   const int r0 = blockIdx.z * 64, rc = (int)min((int64_t)64, l.R - r0), nt = (rc + 7) / 8;
   const uint32_t ring = shared_u32(sm);
   const int steps = (n + kOutRows - 1) / kOutRows;
-  auto load = [&](int i) {
-    const uint32_t s = ring + (uint32_t)((i % kOutStages) * kOutStage);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {                   // 32 rows x 16 pieces of x
-      const int e = tid + q * kOutThreads, r = e >> 4, c = (e & 15) * 8;
-      const int at = i * kOutRows + r;
-      const int ok = at < n ? max(0, min(8, cn - c)) : 0;
-      const T* src = ok ? p.x + (int64_t)rows[at] * p.x_rs + c0 + c : p.x;
-      cp_async<16>(s + (uint32_t)(r * kOutXPitch + c * 2), src, ok * 2);
-    }
-    const int r = tid >> 3, c = (tid & 7) * 8;      // 32 rows x 8 pieces of z
-    const int at = i * kOutRows + r;
-    if (c < nt * 8) {
-      const bool ok = at < n;
-      const T* src = ok ? p.zt + (int64_t)rows[at] * zt_ld + r0 + c : p.zt;
-      cp_async<16>(s + (uint32_t)(kOutRows * kOutXPitch + r * kOutZPitch + c * 2), src, ok ? 16 : 0);
+  // A thread's pieces: 16 bytes of x in rows tid / 16 and 16 more, 16 bytes of z in row tid / 8.
+  const int xr = tid >> 4, zr = tid >> 3;
+  const int x_ok = max(0, min(8, cn - (tid & 15) * 8)) * 2;
+  const bool z_in = (tid & 7) < nt;
+  const T* xc = p.x + c0 + (x_ok ? (tid & 15) * 8 : 0);
+  const T* zc = p.zt + r0 + (z_in ? (tid & 7) * 8 : 0);
+  const uint32_t xd = ring + (uint32_t)(xr * kOutXPitch + (tid & 15) * 16);
+  const uint32_t zd = ring + (uint32_t)(kOutRows * kOutXPitch + zr * kOutZPitch + (tid & 7) * 16);
+  auto load = [&](int i, uint32_t st) {
+    const int at = i * kOutRows;
+    if (at + kOutRows <= n) {
+      cp_async<16>(xd + st, xc + (int64_t)rows[at + xr] * p.x_rs, x_ok);
+      cp_async<16>(xd + st + 16 * kOutXPitch, xc + (int64_t)rows[at + xr + 16] * p.x_rs, x_ok);
+      if (z_in) cp_async<16>(zd + st, zc + (int64_t)rows[at + zr] * zt_ld, 16);
+    } else {                                        // rows past the end: zeros
+      const int a = at + xr, b = a + 16, z = at + zr;
+      cp_async<16>(xd + st, xc + (int64_t)rows[min(a, n - 1)] * p.x_rs, a < n ? x_ok : 0);
+      cp_async<16>(xd + st + 16 * kOutXPitch, xc + (int64_t)rows[min(b, n - 1)] * p.x_rs, b < n ? x_ok : 0);
+      if (z_in) cp_async<16>(zd + st, zc + (int64_t)rows[min(z, n - 1)] * zt_ld, z < n ? 16 : 0);
     }
   };
   float acc[8][4];
@@ -501,15 +465,18 @@ __global__ void __launch_bounds__(kOutThreads)
     for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 #pragma unroll
   for (int i = 0; i < kOutStages - 1; ++i) {
-    if (i < steps) load(i);
+    if (i < steps) load(i, (uint32_t)(i * kOutStage));
     cp_commit();
   }
+  uint32_t cur = 0, nxt = (kOutStages - 1) * kOutStage;      // byte offsets of stages i and i + kOutStages - 1
   for (int i = 0; i < steps; ++i) {
     cp_wait<kOutStages - 2>();
     __syncthreads();
-    if (i + kOutStages - 1 < steps) load(i + kOutStages - 1);
+    if (i + kOutStages - 1 < steps) load(i + kOutStages - 1, nxt);
     cp_commit();
-    const uint32_t s = ring + (uint32_t)((i % kOutStages) * kOutStage);
+    const uint32_t s = ring + cur;
+    cur = cur == (kOutStages - 1) * kOutStage ? 0u : cur + kOutStage;
+    nxt = nxt == (kOutStages - 1) * kOutStage ? 0u : nxt + kOutStage;
 #pragma unroll
     for (int k = 0; k < kOutRows / 16; ++k) {
       uint32_t fa[4];
@@ -524,8 +491,8 @@ __global__ void __launch_bounds__(kOutThreads)
       }
     }
   }
-  const bool whole = __ldcg(t.chunk + g + 1) - ch0 == 1;
-  float* mine = p.part + (int64_t)(__ldcg(t.part + g) + chunk - ch0) * C * l.R;
+  const bool whole = end - begin <= kChunkRows;
+  float* mine = p.part + (int64_t)(first_part(begin) + chunk) * C * l.R;
   T* out = p.out + (int64_t)g * C * l.R;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -550,9 +517,10 @@ __global__ void __launch_bounds__(256)
   const OuterProblem<T>& p = blockIdx.z == 0 ? p0 : p1;
   const int64_t n = p.C * l.R;
   for (int g = blockIdx.y; g < l.G; g += gridDim.y) {
-    const int k = __ldcg(t.chunk + g + 1) - __ldcg(t.chunk + g);
+    const int begin = __ldcg(t.offset + g);
+    const int k = (__ldcg(t.offset + g + 1) - begin + kChunkRows - 1) / kChunkRows;
     if (k == 1) continue;
-    const float* src = p.part + (int64_t)__ldcg(t.part + g) * n;
+    const float* src = p.part + (int64_t)first_part(begin) * n;
     if (n % 4 == 0) {
       for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; e < n; e += (int64_t)gridDim.x * 1024) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -770,11 +738,11 @@ mm_status shrink_launch(const LowRankArgs& l, const void* x, int64_t x_rs, int64
   if (!shrink_map(l, x, x_rs, C, &map)) return MM_ERR_UNSUPPORTED;
   const int rc = (int)(l.R < 64 ? l.R : 64);
   int smem = shrink_smem(ck, rc);
-  const int tables = (int)(sort ? kShWarps * l.G * 4 : 0), bits = (int)(slots ? (l.G + 31) / 32 * 4 : 0);
+  const int tables = (int)(sort ? (l.M + 31) / 32 * 4 : 0), bits = (int)(slots ? (l.G + 31) / 32 * 4 : 0);
   for (int need : {tables, bits})
     if (smem < need) smem = need;
   p.tiles = (int)((l.M + kShRows - 1) / kShRows);
-  const dim3 grid((unsigned)(p.tiles + (slots ? 1 : 0) + (sort ? 1 : 0)), (unsigned)((l.R + 63) / 64));
+  const dim3 grid((unsigned)(p.tiles + (slots ? 1 : 0) + (sort ? l.G : 0)), (unsigned)((l.R + 63) / 64));
   const auto kernel = ck ? (rc <= 16 ? shrink_tiles_kernel<T, true, 2> : rc <= 32 ? shrink_tiles_kernel<T, true, 4>
                                                                                : shrink_tiles_kernel<T, true, 8>)
                          : (rc <= 16 ? shrink_tiles_kernel<T, false, 2> : rc <= 32 ? shrink_tiles_kernel<T, false, 4>
