@@ -326,7 +326,11 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
                         B->data, B->strides[0], B->strides[1], B->strides[2], p.N, Y->data};
   if (path_policy() != MM_PATH_SIMT && lowrank_few_supported(l, f)) {
     if ((s = launch_lowrank_few(l, f, z, st)) != MM_OK) return s;
-    return add_projection(g, st);
+    // The expansion lets the product start while it runs; the first of the two
+    // launches waited for all earlier work, X and W included.
+    GemmArgs late = g;
+    late.c_late = 1;
+    return add_projection(late, st);
   }
   if (many_rows(l) && p.K >= 1 &&
       lowrank_shrink_tiles_supported(l, X->data, X->strides[0], X->strides[1], p.K, A->strides[1], A->strides[2]) &&

@@ -19,6 +19,10 @@ struct GemmArgs {
   float alpha, beta;         // float types
   double alpha_d, beta_d;    // f64
   uint64_t alpha_i, beta_i;  // integer types: two's complement of the integral values
+  // C and Y are touched by the previous launch on the stream, while A and B
+  // were complete before that launch began: a few-row kernel may then read A
+  // and B at once and wait for the previous launch only before its epilogue.
+  int c_late;
   // Integer types with a non-integral alpha or beta: y = trunc(alpha*acc + beta*c)
   // evaluated in fp64 (each product, then the sum, rounded once), saturated to T.
   int int_float;

@@ -205,46 +205,53 @@ __global__ void __launch_bounds__(kFewThreads)
 
 // Block (1024 columns, row): a thread takes 8 columns (b with n contiguous) or
 // walks columns with r contiguous; the row's z is the sum of its shares.
+// Only z depends on the launch before: the adapter's first rows are read, and
+// the next launch let in, ahead of the wait for it (that launch began after
+// all earlier work was complete).
 constexpr int kExpandMaxR = 1024;
 
 template <typename T, bool NC>
 __global__ void __launch_bounds__(kFewThreads)
     expand_rows_kernel(const LowRankArgs l, const float* zp, const T* b, int64_t b_gs, int64_t b_ld, int64_t N, T* y,
                        int yvec) {
-  pdl_begin();
+  pdl_trigger();
   __shared__ float zs[kExpandMaxR];
   const int64_t m = blockIdx.y;
   const int64_t g = adapter_of(l, m);
   const int R = (int)l.R;
+  const T* bg = b + (g < 0 ? 0 : g) * b_gs;
+  T* yr = y + m * N;
+  const int64_t n8 = ((int64_t)blockIdx.x * kFewThreads + threadIdx.x) * 8;
+  constexpr int kAhead = 8;
+  uint4 u[kAhead];
+  auto read = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) u[i] = *reinterpret_cast<const uint4*>(bg + (int64_t)min(r0 + i, R - 1) * b_ld + n8);
+  };
+  const bool live = NC && n8 < N && g >= 0;
+  if (live) read(0);
+  pdl_wait();
   for (int r = threadIdx.x; r < R; r += kFewThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int s = 0; s < kSplit; ++s) v += zp[((int64_t)s * l.M + m) * R + r];
+    for (int s = 0; s < kSplit; ++s) v += __ldcg(zp + ((int64_t)s * l.M + m) * R + r);
     zs[r] = v;
   }
   __syncthreads();
-  const T* bg = b + (g < 0 ? 0 : g) * b_gs;
-  T* yr = y + m * N;
   if constexpr (NC) {
-    const int64_t n = ((int64_t)blockIdx.x * kFewThreads + threadIdx.x) * 8;
-    if (n >= N) return;
+    if (n8 >= N) return;
     float acc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-    if (g >= 0) {
-      constexpr int kAhead = 8;
-      for (int r0 = 0; r0 < R; r0 += kAhead) {
-        uint4 u[kAhead];
+    for (int r0 = 0; live && r0 < R; r0 += kAhead) {
+      if (r0) read(r0);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) u[i] = *reinterpret_cast<const uint4*>(bg + (int64_t)min(r0 + i, R - 1) * b_ld + n);
+      for (int i = 0; i < kAhead; ++i) {
+        if (r0 + i >= R) break;
+        float f[8];
+        unpack8<T>(u[i], f);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          if (r0 + i >= R) break;
-          float f[8];
-          unpack8<T>(u[i], f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] = __fmaf_rn(zs[r0 + i], f[j], acc[j]);
-        }
+        for (int j = 0; j < 8; ++j) acc[j] = __fmaf_rn(zs[r0 + i], f[j], acc[j]);
       }
     }
     uint4 o;
@@ -252,11 +259,11 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll
     for (int j = 0; j < 8; ++j) e[j] = from_f32<T>(acc[j]);
     if (yvec) {
-      *reinterpret_cast<uint4*>(yr + n) = o;
+      *reinterpret_cast<uint4*>(yr + n8) = o;
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (n + j < N) yr[n + j] = e[j];
+        if (n8 + j < N) yr[n8 + j] = e[j];
     }
   } else {
     for (int64_t n = (int64_t)blockIdx.x * kFewThreads * 8 + threadIdx.x;

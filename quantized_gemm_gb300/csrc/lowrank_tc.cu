@@ -419,13 +419,13 @@ __global__ void __launch_bounds__(kOutThreads)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = (int)l.G;
   const OuterProblem<T>& p = (int)blockIdx.x < blocks0 ? p0 : p1;
   const int64_t C = p.C;
-  int lo = 0, hi = G;                               // the adapter with first_chunk(g) <= chunk < first_chunk(g + 1)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first_chunk(__ldcg(t.offset + mid), mid) <= (int)blockIdx.y) lo = mid;
-    else hi = mid;
-  }
-  const int g = lo, begin = __ldcg(t.offset + g), end = __ldcg(t.offset + g + 1);
+  __shared__ int found;                             // the adapter with first_chunk(g) <= chunk < first_chunk(g + 1)
+  for (int h = tid; h < G; h += kOutThreads)
+    if (first_chunk(__ldcg(t.offset + h), h) <= (int)blockIdx.y && (int)blockIdx.y < first_chunk(__ldcg(t.offset + h + 1), h + 1))
+      found = h;
+  __syncthreads();
+  if ((int)blockIdx.y >= first_chunk(__ldcg(t.offset + G), G)) return;
+  const int g = found, begin = __ldcg(t.offset + g), end = __ldcg(t.offset + g + 1);
   const int chunk = (int)blockIdx.y - first_chunk(begin, g);          // of this adapter
   const int first = begin + chunk * kChunkRows;
   const int n = min(kChunkRows, end - first);

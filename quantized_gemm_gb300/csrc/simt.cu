@@ -445,7 +445,7 @@ template <> __device__ __forceinline__ float dot16<float>(float acc, uint4 a, ui
 template <typename T, int MT>
 __global__ void __launch_bounds__(kVecWarps * 32) vec_gemm_kernel(const GemmArgs p, int64_t groups, int64_t tasks,
                                                                   int64_t warps) {
-  pdl_begin();
+  if (!p.c_late) pdl_begin();
   constexpr int kVecCols = VecShape<MT>::cols;
   constexpr int U = VecShape<MT>::steps;
   constexpr int kPiece = 16 / (int)sizeof(T);   // values of k in a 16-byte piece
@@ -528,6 +528,7 @@ __global__ void __launch_bounds__(kVecWarps * 32) vec_gemm_kernel(const GemmArgs
       for (int r = 0; r < kVecCols; ++r)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) acc[m][r] += __shfl_xor_sync(0xffffffffu, acc[m][r], o);
+    if (p.c_late) pdl_begin();
     // Lane kVecCols * m + r stores output (m, n0 + r).
     const T* Cb = C ? C + batch_offset(p.bm, p.c.bstride, bt) : nullptr;
     T* Yb = Y + batch_offset(p.bm, p.y.bstride, bt);
@@ -560,7 +561,7 @@ constexpr int kMnRounds = 8;   // rows of B' per warp in flight
 template <typename T, int MT>
 __global__ void __cluster_dims__(kMnSplit, 1, 1) __launch_bounds__(kMnWarps * 32)
     vec_mn_kernel(const GemmArgs p) {
-  pdl_begin();
+  if (!p.c_late) pdl_begin();
   constexpr int kPiece = 16 / (int)sizeof(T);
   constexpr int kSpan = 32 * kPiece;   // columns of a cluster
   __shared__ __align__(16) float part[kMnWarps][MT][kSpan];
@@ -620,6 +621,7 @@ __global__ void __cluster_dims__(kMnSplit, 1, 1) __launch_bounds__(kMnWarps * 32
 #pragma unroll
       for (int j = 0; j < kPiece; ++j) part[warp][m][lane * kPiece + j] = acc[m][j];
     cluster.sync();   // every CTA's partial sums visible to the leader
+    if (p.c_late) pdl_begin();
     if (crank == 0) {
       const T* Cb = C ? C + batch_offset(p.bm, p.c.bstride, bt) : nullptr;
       T* Yb = Y + batch_offset(p.bm, p.y.bstride, bt);

@@ -1325,7 +1325,7 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
   // Launched with programmatic stream serialization, this grid may start while
   // the previous kernel on the stream is finishing: the set-up above overlaps
   // its tail, and nothing below touches global memory before it completes.
-  pdl_wait();
+  if (MODE != kSkinny || !p.c_late) pdl_wait();
   if constexpr (MODE == kDense || MODE == kTF32) pdl_trigger();
   const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
 
@@ -1357,6 +1357,7 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
     // cluster's partials for its share of the columns, and no CTA leaves
     // (taking its shared memory with it) until all have read them.
     cluster_sync();
+    if (p.c_late) pdl_wait();
     if (warp >= kEpiWarp0) run_skinny_reduce<MODE, PAIR>(p, sbase);
     cluster_sync();
   }
@@ -1817,6 +1818,7 @@ mm_status launch_tc_gemm(const GemmArgs& g, unsigned* status, cudaStream_t strea
         plan_operand(g.a.ptr, g.dtype, g.M, g.K, a_rs, g.a.cs, g.bm, g.a.bstride, BM / 2, &a) && !a.mn_major &&
         plan_operand(g.b.ptr, g.dtype, g.N, g.K, g.b.cs, g.b.rs, g.bm, g.b.bstride, BN, &b)) {
       p.idesc = make_idesc_mn(p.out_f16, 0, b.mn_major, BM, BN);
+      p.c_late = g.c_late;
       return launch_tc(kSkinny, false, a, b, p, stream);
     }
   }

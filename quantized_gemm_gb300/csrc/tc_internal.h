@@ -64,6 +64,7 @@ struct TcParams {
   int64_t c_bstride[kMaxBatchDims];
   int64_t c_rs, c_cs, c_gs;                    // c_gs: grouped bias row stride per group
   int c_vec;
+  int c_late;                                  // kSkinny: GemmArgs::c_late
   // QLinear epilogue: zero-point correction from the operand sums, then requantisation
   VecView sa, sb, za, zb;
   const void* ys;
