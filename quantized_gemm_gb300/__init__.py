@@ -111,8 +111,12 @@ def _lib():
 
 
 # MMTensor's bytes: pointer, dtype, ndim, shape[8], strides[8] (packed in one
-# call, which is cheaper than filling the ctypes arrays element by element).
+# call, which is cheaper than filling the ctypes arrays element by element; one
+# format per rank, whose pad bytes are the unused entries' zeros).
 _MM_TENSOR_BYTES = struct.Struct("<Qii%dq%dq" % (MM_MAX_DIMS, MM_MAX_DIMS))
+_PACK = [struct.Struct("<Qii%dq%dx%dq%dx" % (n, 8 * (MM_MAX_DIMS - n), n, 8 * (MM_MAX_DIMS - n))).pack
+         for n in range(MM_MAX_DIMS + 1)]
+_TENSOR_OF = MMTensor.from_buffer_copy
 _ZEROS = (0,) * MM_MAX_DIMS
 
 
@@ -126,8 +130,7 @@ def _desc(t):
     nd = t.dim()
     if nd > MM_MAX_DIMS:
         raise ValueError("at most %d dimensions" % MM_MAX_DIMS)
-    return MMTensor.from_buffer_copy(_MM_TENSOR_BYTES.pack(
-        t.data_ptr() if t.numel() > 0 else 0, dt, nd, *(tuple(t.shape) + _ZEROS[nd:]), *(t.stride() + _ZEROS[nd:])))
+    return _TENSOR_OF(_PACK[nd](t.data_ptr() if t.numel() > 0 else 0, dt, nd, *t.shape, *t.stride()))
 
 
 def _desc4(t, kind):

@@ -6,6 +6,7 @@
 #include "api_internal.h"
 #include "kernels.h"
 #include "lowrank.cuh"
+#include "moe.cuh"
 #include "tc.h"
 
 using namespace qg;
@@ -125,8 +126,8 @@ mm_status plan_moe(const mm_tensor* x, const mm_tensor* w_gate, const mm_tensor*
 }
 
 // Products of at least 2^21 multiply-adds (the dense products' rule) over all picks.
-int moe_path(const MoeArgs& a) {
-  return choose(tc_moe_supported(a), tensor_pays(a.tokens * a.S, a.F, a.K + a.N, 1));
+int moe_path(const MoeArgs& a, MoeMaps* maps) {
+  return choose(tc_moe_supported(a, maps), tensor_pays(a.tokens * a.S, a.F, a.K + a.N, 1));
 }
 
 size_t moe_simt_bytes(const MoeArgs& a) { return align256((size_t)(a.tokens * a.S) * (size_t)a.F * sizeof(float)); }
@@ -141,7 +142,8 @@ mm_status mm_moe_layer_workspace_size(const mm_tensor* x, const mm_tensor* w_gat
   MoeArgs a;
   const mm_status s = plan_moe(x, w_gate, w_up, w_down, expert_indices, &a);
   if (s != MM_OK) return s;
-  *bytes = moe_path(a) == MM_PATH_TENSOR ? tc_moe_workspace_bytes(a) : moe_simt_bytes(a);
+  MoeMaps maps;
+  *bytes = moe_path(a, &maps) == MM_PATH_TENSOR ? tc_moe_workspace_bytes(a) : moe_simt_bytes(a);
   return MM_OK;
 }
 
@@ -166,11 +168,12 @@ mm_status mm_moe_layer(const mm_tensor* x, const mm_tensor* w_gate, const mm_ten
   unsigned* status = device_status_ptr();
   if (!status) return MM_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int path = moe_path(a);
+  MoeMaps maps;
+  const int path = moe_path(a, &maps);
   if (path < 0) return MM_ERR_UNSUPPORTED;
   if (path == MM_PATH_TENSOR) {
     if (!workspace_ok(workspace, workspace_bytes, tc_moe_workspace_bytes(a))) return MM_ERR_WORKSPACE;
-    return finish(launch_tc_moe(a, workspace, status, st), MM_PATH_TENSOR);
+    return finish(launch_tc_moe(a, maps, workspace, status, st), MM_PATH_TENSOR);
   }
   if (!workspace_ok(workspace, workspace_bytes, moe_simt_bytes(a))) return MM_ERR_WORKSPACE;
   return finish(launch_simt_moe(a, static_cast<float*>(workspace), status, st), MM_PATH_SIMT);

@@ -2,8 +2,13 @@
 #pragma once
 
 #include "kernels.h"
+#include "tc_internal.h"
 
 namespace qg {
+
+struct MoeMaps {
+  OperandPlan gate, up, down;
+};
 
 __device__ __forceinline__ float activate(float g, int act) {
   switch (act) {

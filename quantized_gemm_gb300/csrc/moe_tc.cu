@@ -609,7 +609,7 @@ bool plan_rows(const void* x, int dtype, int64_t rows, int64_t k, int64_t rs, in
 
 }  // namespace
 
-bool tc_moe_supported(const MoeArgs& a) {
+bool tc_moe_supported(const MoeArgs& a, MoeMaps* maps) {
   if (a.dtype != MM_BF16 && a.dtype != MM_F16) return false;
   if (a.tokens < 1 || a.S < 1 || a.G < 1 || a.K < 1 || a.F < 1 || a.N < 1) return false;
   if (a.G > kPlanExperts || a.S > 64) return false;
@@ -618,20 +618,20 @@ bool tc_moe_supported(const MoeArgs& a) {
   const double blocks = (double)l.picked * (double)l.f_tiles * (double)((a.K + 63) / 64);
   const double blocks2 = (double)l.picked * (double)l.n_tiles * (double)((a.F + 63) / 64);
   if (blocks >= 2147483648.0 || blocks2 >= 2147483648.0) return false;
-  OperandPlan w, u, d, x;
-  if (!plan_weights(a.wg, a.dtype, a.G, a.F, a.K, a.wg_gs, a.wg_fs, a.wg_ks, &w)) return false;
-  if (a.wu && (!plan_weights(a.wu, a.dtype, a.G, a.F, a.K, a.wu_gs, a.wu_fs, a.wu_ks, &u) || u.mn_major != w.mn_major))
+  OperandPlan x;
+  if (!plan_weights(a.wg, a.dtype, a.G, a.F, a.K, a.wg_gs, a.wg_fs, a.wg_ks, &maps->gate)) return false;
+  if (a.wu && (!plan_weights(a.wu, a.dtype, a.G, a.F, a.K, a.wu_gs, a.wu_fs, a.wu_ks, &maps->up) ||
+               maps->up.mn_major != maps->gate.mn_major))
     return false;
-  if (!plan_weights(a.wd, a.dtype, a.G, a.N, a.F, a.wd_gs, a.wd_ns, a.wd_fs, &d)) return false;
-  if (!plan_rows(a.x, a.dtype, l.tok, a.K, a.x_rs, a.x_cs, 16, &x)) return false;
-  // Tokens past the first launch's start at other rows: 16-byte aligned too
-  // (x_rs is a multiple of 8 for more than one row).
-  return true;
+  if (!plan_weights(a.wd, a.dtype, a.G, a.N, a.F, a.wd_gs, a.wd_ns, a.wd_fs, &maps->down)) return false;
+  // The rows of x that later launches start at are 16-byte aligned too (more
+  // than one row: the stride is a multiple of 8).
+  return plan_rows(a.x, a.dtype, l.tok, a.K, a.x_rs, a.x_cs, 16, &x);
 }
 
 size_t tc_moe_workspace_bytes(const MoeArgs& a) { return moe_layout(a).total; }
 
-mm_status launch_tc_moe(const MoeArgs& a, void* workspace, unsigned* status, cudaStream_t stream) {
+mm_status launch_tc_moe(const MoeArgs& a, const MoeMaps& maps, void* workspace, unsigned* status, cudaStream_t stream) {
   const MoeLayout l = moe_layout(a);
   char* ws = static_cast<char*>(workspace);
   TcParams limits;                        // the pipelines' wait limits
@@ -652,12 +652,9 @@ mm_status launch_tc_moe(const MoeArgs& a, void* workspace, unsigned* status, cud
   p.status = status;
   p.timeout_ns = limits.timeout_ns; p.teardown_ns = limits.teardown_ns;
 
-  OperandPlan wg, wu, wd, h, x;
-  if (!plan_weights(a.wg, a.dtype, a.G, a.F, a.K, a.wg_gs, a.wg_fs, a.wg_ks, &wg) ||
-      (a.wu && !plan_weights(a.wu, a.dtype, a.G, a.F, a.K, a.wu_gs, a.wu_fs, a.wu_ks, &wu)) ||
-      !plan_weights(a.wd, a.dtype, a.G, a.N, a.F, a.wd_gs, a.wd_ns, a.wd_fs, &wd) ||
-      !plan_rows(ws + l.off_h, a.dtype, l.rows, a.F, l.h_ld, 1, 16, &h))
-    return MM_ERR_UNSUPPORTED;
+  const OperandPlan &wg = maps.gate, &wu = maps.up, &wd = maps.down;
+  OperandPlan h, x;
+  if (!plan_rows(ws + l.off_h, a.dtype, l.rows, a.F, l.h_ld, 1, 16, &h)) return MM_ERR_UNSUPPORTED;
   const int plan_smem = (int)(a.G * (kMaskWords + 1) * 4);
   const int sms = sm_count_public();
   for (int64_t t0 = 0; t0 < a.tokens; t0 += kTok) {

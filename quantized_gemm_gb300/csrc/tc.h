@@ -39,9 +39,10 @@ mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* st
 
 // The mixture-of-experts layer for a few tokens (moe_tc.cu): every matrix with
 // 16-byte aligned rows along a unit-stride matrix dimension, w_gate and w_up
-// with the same one.
-bool tc_moe_supported(const MoeArgs& a);
+// with the same one.  `maps` receives the weights' tensor maps for the launch.
+struct MoeMaps;
+bool tc_moe_supported(const MoeArgs& a, MoeMaps* maps);
 size_t tc_moe_workspace_bytes(const MoeArgs& a);
-mm_status launch_tc_moe(const MoeArgs& a, void* workspace, unsigned* status, cudaStream_t stream);
+mm_status launch_tc_moe(const MoeArgs& a, const MoeMaps& maps, void* workspace, unsigned* status, cudaStream_t stream);
 
 }  // namespace qg
