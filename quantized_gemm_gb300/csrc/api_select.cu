@@ -342,8 +342,9 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
     char* ws = static_cast<char*>(workspace);
     z = reinterpret_cast<float*>(ws + w.z);
     const FusedTables slots = lowrank_fused_tables(w, ws);
-    s = launch_lowrank_shrink_tiles(l, X->data, X->strides[0], p.K, A->data, A->strides[0], A->strides[1], A->strides[2],
-                                    z, ws + w.zt, w.zt_ld, &slots, nullptr, st);
+    const LowRankShrink q = {X->data, X->strides[0], p.K, A->data, A->strides[0], A->strides[1], A->strides[2], z,
+                             ws + w.zt};
+    s = launch_lowrank_shrink_tiles(l, &q, 1, w.zt_ld, &slots, nullptr, st);
     if (s == MM_OK)
       s = launch_lowrank_fused(l, g, w, ws, z, ws + w.zt, B->data, B->strides[0], B->strides[1], B->strides[2], st);
     return finish(s, MM_PATH_TENSOR);
@@ -399,15 +400,14 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
     void* vt = ws + w.fused.zt;
     const AdapterRows t = {reinterpret_cast<int32_t*>(ws + w.row), reinterpret_cast<int32_t*>(ws + w.offset)};
     const FusedTables slots = lowrank_fused_tables(w.fused, ws);
-    const bool sort_with_u = dB != nullptr;
+    LowRankShrink q[2];
+    int factors = 0;
     if (dX || dA)
-      s = launch_lowrank_shrink_tiles(l, dY->data, dY->strides[0], N, B->data, B->strides[0], B->strides[2],
-                                      B->strides[1], zv, vt, w.zt_ld, dX ? &slots : nullptr,
-                                      dA && !sort_with_u ? &t : nullptr, st);
-    if (s == MM_OK && dB)
-      s = launch_lowrank_shrink_tiles(l, X->data, X->strides[0], K, A->data, A->strides[0], A->strides[1],
-                                      A->strides[2], reinterpret_cast<float*>(ws + w.u), ws + w.ut, w.zt_ld, nullptr, &t,
-                                      st);
+      q[factors++] = {dY->data, dY->strides[0], N, B->data, B->strides[0], B->strides[2], B->strides[1], zv, vt};
+    if (dB)
+      q[factors++] = {X->data, X->strides[0], K, A->data, A->strides[0], A->strides[1], A->strides[2],
+                      reinterpret_cast<float*>(ws + w.u), ws + w.ut};
+    if (factors) s = launch_lowrank_shrink_tiles(l, q, factors, w.zt_ld, dX ? &slots : nullptr, dA || dB ? &t : nullptr, st);
     LowRankOuter o[2];
     int problems = 0;
     if (dA)

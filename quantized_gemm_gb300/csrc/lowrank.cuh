@@ -49,12 +49,17 @@ FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N);
 FusedTables lowrank_fused_tables(const FusedLayout& w, char* ws);
 bool lowrank_fused_supported(const LowRankArgs& l, const GemmArgs& g);
 
-// z [M, R] (fp32) and zt [M, zt_ld] (T, zeros past R), both scaled; the same
+// One or two factors z [M, R] (fp32) and zt [M, zt_ld] (T, zeros past R), both scaled; the same
 // launch makes the fused product's slots and the sorted rows where asked for.
 bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
                                     int64_t a_cs, int64_t a_rs);
-mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a,
-                                      int64_t a_gs, int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld,
+struct LowRankShrink {
+  const void* x; int64_t x_rs, C;
+  const void* a; int64_t a_gs, a_cs, a_rs;
+  float* z;
+  void* zt;
+};
+mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const LowRankShrink* p, int problems, int64_t zt_ld,
                                       const FusedTables* slots, const AdapterRows* sort, cudaStream_t stream);
 // Y = g (A B, 16-bit, no batch) + z b, z, zt and the slots made before.
 mm_status launch_lowrank_fused(const LowRankArgs& l, const GemmArgs& g, const FusedLayout& w, char* ws, const float* z,

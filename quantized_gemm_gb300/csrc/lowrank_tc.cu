@@ -120,12 +120,12 @@ __host__ __device__ constexpr int shrink_smem(bool ck, int rc) {
 }
 
 struct ShrinkArgs {
+  int ck;                                      // c is a's unit-stride dimension
   int64_t C;
   const void* a; int64_t a_gs, a_ld;
   int per;                                     // elements per copy of the adapter
   float* z;
   void* zt; int64_t zt_ld;
-  int tiles;
   unsigned long long timeout_ns, teardown_ns;
 };
 
@@ -373,16 +373,23 @@ __device__ void adapter_slots(const LowRankArgs& l, const FusedTables& t, uint8_
 }
 
 // The first blocks make the tables that later launches want (they depend on
-// the indices alone): slots, then the sorted rows; the others shrink one tile each.
-template <typename T, bool CK, int NT>
+// the indices alone): slots, then the sorted rows; the others shrink one tile
+// each, of the first or the second problem (a gradient's V and U).
+template <typename T, int NT>
 __global__ void __launch_bounds__(kShThreads, NT <= 4 ? 2 : 1)
-    shrink_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const LowRankArgs l, const ShrinkArgs p,
-                        const FusedTables slots, const AdapterRows sort) {
+    shrink_tiles_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
+                        const LowRankArgs l, const ShrinkArgs p0, const ShrinkArgs p1, const int tiles,
+                        const int problems, const FusedTables slots, const AdapterRows sort) {
   pdl_begin();
   extern __shared__ __align__(16) uint8_t sm[];
-  const int tile = (int)blockIdx.x - ((int)gridDim.x - p.tiles);
+  const int tile = (int)blockIdx.x - ((int)gridDim.x - tiles * problems);
   if (tile >= 0) {
-    shrink_tile<T, CK, NT>(&tmX, l, p, tile, sm);
+    const bool second = tile >= tiles;
+    const ShrinkArgs& p = second ? p1 : p0;
+    const CUtensorMap* tm = second ? &tm1 : &tm0;
+    const int t = second ? tile - tiles : tile;
+    if (p.ck) shrink_tile<T, true, NT>(tm, l, p, t, sm);
+    else shrink_tile<T, false, NT>(tm, l, p, t, sm);
   } else if (blockIdx.y == 0) {
     const int b = (int)blockIdx.x - (slots.head ? 1 : 0);
     if (b < 0) adapter_slots(l, slots, sm);
@@ -719,37 +726,41 @@ bool shrink_map(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, Op
 }
 
 template <typename T>
-mm_status shrink_launch(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a, int64_t a_gs,
-                        int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld, const FusedTables* slots,
-                        const AdapterRows* sort, cudaStream_t stream) {
-  const bool ck = a_rs != 1;            // c is a's unit-stride dimension
-  ShrinkArgs p;
-  memset(&p, 0, sizeof(p));
-  p.C = C;
-  p.a = a; p.a_gs = a_gs; p.a_ld = ck ? a_rs : a_cs;
-  p.per = 8;
-  while (p.per > 1 && (reinterpret_cast<uintptr_t>(a) % (p.per * 2) || (l.G > 1 && a_gs % p.per) || p.a_ld % p.per))
-    p.per >>= 1;
-  p.z = z; p.zt = zt; p.zt_ld = zt_ld;
+mm_status shrink_launch(const LowRankArgs& l, const LowRankShrink* q, int problems, int64_t zt_ld,
+                        const FusedTables* slots, const AdapterRows* sort, cudaStream_t stream) {
   TcParams limits;                      // the pipelines' wait limits
   init_params(&limits);
-  p.timeout_ns = limits.timeout_ns; p.teardown_ns = limits.teardown_ns;
-  OperandPlan map;
-  if (!shrink_map(l, x, x_rs, C, &map)) return MM_ERR_UNSUPPORTED;
+  ShrinkArgs p[2];
+  OperandPlan map[2];
   const int rc = (int)(l.R < 64 ? l.R : 64);
-  int smem = shrink_smem(ck, rc);
+  int smem = 0;
+  for (int i = 0; i < 2; ++i) {
+    const LowRankShrink& s = q[i < problems ? i : 0];
+    ShrinkArgs& a = p[i];
+    memset(&a, 0, sizeof(a));
+    a.ck = s.a_rs != 1;
+    a.C = s.C;
+    a.a = s.a; a.a_gs = s.a_gs; a.a_ld = a.ck ? s.a_rs : s.a_cs;
+    a.per = 8;
+    while (a.per > 1 && (reinterpret_cast<uintptr_t>(a.a) % (a.per * 2) || (l.G > 1 && a.a_gs % a.per) || a.a_ld % a.per))
+      a.per >>= 1;
+    a.z = s.z; a.zt = s.zt; a.zt_ld = zt_ld;
+    a.timeout_ns = limits.timeout_ns; a.teardown_ns = limits.teardown_ns;
+    if (!shrink_map(l, s.x, s.x_rs, s.C, &map[i])) return MM_ERR_UNSUPPORTED;
+    const int need = shrink_smem(a.ck, rc);
+    if (smem < need) smem = need;
+  }
   const int tables = (int)(sort ? (l.M + 31) / 32 * 4 : 0), bits = (int)(slots ? (l.G + 31) / 32 * 4 : 0);
   for (int need : {tables, bits})
     if (smem < need) smem = need;
-  p.tiles = (int)((l.M + kShRows - 1) / kShRows);
-  const dim3 grid((unsigned)(p.tiles + (slots ? 1 : 0) + (sort ? l.G : 0)), (unsigned)((l.R + 63) / 64));
-  const auto kernel = ck ? (rc <= 16 ? shrink_tiles_kernel<T, true, 2> : rc <= 32 ? shrink_tiles_kernel<T, true, 4>
-                                                                               : shrink_tiles_kernel<T, true, 8>)
-                         : (rc <= 16 ? shrink_tiles_kernel<T, false, 2> : rc <= 32 ? shrink_tiles_kernel<T, false, 4>
-                                                                                : shrink_tiles_kernel<T, false, 8>);
+  const int64_t tiles = (l.M + kShRows - 1) / kShRows;
+  const int64_t blocks = tiles * problems + (slots ? 1 : 0) + (sort ? l.G : 0);
+  if (blocks > 0x7fffffffLL) return MM_ERR_UNSUPPORTED;
+  const auto kernel = rc <= 16 ? shrink_tiles_kernel<T, 2> : rc <= 32 ? shrink_tiles_kernel<T, 4> : shrink_tiles_kernel<T, 8>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024) != cudaSuccess)
     return MM_ERR_CUDA;
-  return launch_pdl(kernel, grid, dim3(kShThreads), (size_t)smem, stream, map.map, l, p, slots ? *slots : FusedTables{},
+  return launch_pdl(kernel, dim3((unsigned)blocks, (unsigned)((l.R + 63) / 64)), dim3(kShThreads), (size_t)smem, stream,
+                    map[0].map, map[1].map, l, p[0], p[1], (int)tiles, problems, slots ? *slots : FusedTables{},
                     sort ? *sort : AdapterRows{}) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
@@ -785,12 +796,10 @@ bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t
          shrink_map(l, x, x_rs, C, &map);
 }
 
-mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, const void* a,
-                                      int64_t a_gs, int64_t a_cs, int64_t a_rs, float* z, void* zt, int64_t zt_ld,
+mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const LowRankShrink* p, int problems, int64_t zt_ld,
                                       const FusedTables* slots, const AdapterRows* sort, cudaStream_t stream) {
-  return l.dtype == MM_F16
-             ? shrink_launch<__half>(l, x, x_rs, C, a, a_gs, a_cs, a_rs, z, zt, zt_ld, slots, sort, stream)
-             : shrink_launch<__nv_bfloat16>(l, x, x_rs, C, a, a_gs, a_cs, a_rs, z, zt, zt_ld, slots, sort, stream);
+  return l.dtype == MM_F16 ? shrink_launch<__half>(l, p, problems, zt_ld, slots, sort, stream)
+                           : shrink_launch<__nv_bfloat16>(l, p, problems, zt_ld, slots, sort, stream);
 }
 
 namespace {

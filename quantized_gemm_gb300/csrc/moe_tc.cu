@@ -45,11 +45,12 @@ constexpr int kTileBytes = 128 * 64 * 2;     // a weight tile: 128 columns x 64 
 constexpr int kMaxStages = 12;
 constexpr int kThreads = 192;
 constexpr int kCtrl = 512;                   // barriers, TMEM slot, flags
-constexpr uint32_t kTmem = 512;
 constexpr int kPlanThreads = 512;
 constexpr int kPlanExperts = 2048;           // experts the plan's tables hold (shared memory)
-// A share of fewer k-blocks than this is not worth its partial sums.
-constexpr int kMinShare = 4;
+// A share of fewer k-blocks than this is not worth its partial sums (three
+// tokens, 12 picks of K = 1000, F = 712: 32 us with 4, 27 us with 16, 35 us
+// with 24).
+constexpr uint32_t kMinShare = 12;
 constexpr int kSmemMax = 227 * 1024;
 
 // Tables written by the plan, in the workspace (read through L2: the kernels
@@ -76,6 +77,7 @@ struct MoeTcParams {
   int64_t g_bc, u_bc;     // TMA batch coordinate per expert
   int stages, stage_bytes;
   int max_picked, table_bytes;
+  uint32_t tmem_cols, up_off, buf_off;   // TMEM columns: allocated, of the up product, of the second buffer
   uint32_t idesc0;        // instruction descriptor without N
   void* out;              // hidden: h [rows, h_ld]; down: out [tokens, N]
   int64_t ld;
@@ -225,32 +227,35 @@ __device__ __forceinline__ bool epi_all(bool ok) {
 // Arrival of this CTA's share of a tile; true in every epilogue thread of the
 // CTA that arrives last, which then sees all the shares' partial sums.
 __device__ __forceinline__ bool last_to_arrive(int32_t* counter, int expected, volatile int* flag) {
-  __threadfence();
   epi_sync();
   if (threadIdx.x == 64) {
+    __threadfence();        // releases what the other threads wrote before the barrier, too
     const int last = atomicAdd(counter, 1) == expected - 1;
     __threadfence();
     *flag = last;
   }
   epi_sync();
-  const bool last = *flag != 0;
-  if (last) __threadfence();
-  return last;
+  return *flag != 0;
 }
 
-// The partial sums at `at` of shares c0..c1 of the tile that starts at block
-// t0, added in share order; slots are `stride` floats apart, and a share that
-// began before the tile holds it in its second slot.
-__device__ __forceinline__ float4 sum_shares(const float* at, int64_t stride, const Share& sh, uint32_t c0, uint32_t c1,
-                                             uint32_t t0) {
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+// The partial sums of shares c0..c1 of the tile that starts at block t0, added
+// in share order, for n <= N places `step` floats apart (the others read the
+// last one's); slots are `stride` floats apart.  Only the first share can have
+// begun before the tile; it then holds the tile in its second slot.
+template <int N>
+__device__ __forceinline__ void sum_shares(const float* at, int step, int n, int64_t stride, const Share& sh, uint32_t c0,
+                                           uint32_t c1, uint32_t t0, float4 (&s)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
   for (uint32_t c = c0; c <= c1; ++c) {
-    // only the first share can have begun before the tile
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(at + (int64_t)(2 * c + (c == c0 && sh.begin(c) < t0)) * stride));
-    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    const float* q = at + (int64_t)(2 * c + (c == c0 && sh.begin(c) < t0)) * stride;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(q + min(i, n - 1) * step));
+      s[i].x += v.x; s[i].y += v.y; s[i].z += v.z; s[i].w += v.w;
+    }
   }
-  return s;
 }
 
 __device__ __forceinline__ void store16(void* dst, int64_t i, float v, int f16) {
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), kTmem);
+    tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -303,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // is complete: `down` streams weights before `hidden` has finished and waits
   // for it only before it touches h, the partial sums or the output.
   if (!DOWN) pdl_begin();
+  else pdl_trigger();       // the next launch waits for this one before it touches anything
 
   const uint32_t picked = (uint32_t)__ldcg(p.tb.head);
   for (uint32_t i = threadIdx.x; i < picked; i += kThreads) t_expert[i] = __ldcg(p.tb.expert + i);
@@ -388,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(acce0 + 8 * buf, aph ^ 1, abort, p.status, p.timeout_ns)) break;
         tc_fence_after();
         const uint32_t n = DOWN ? (uint32_t)((seg_rows(s.a) + 15) & ~15) : (uint32_t)p.nt;
-        const uint32_t idesc = p.idesc0 | ((n >> 3) << 17), d = tmem + buf * 256;
+        const uint32_t idesc = p.idesc0 | ((n >> 3) << 17), d = tmem + buf * p.buf_off;
         for (uint32_t kb = s.kb0; kb < s.kb1; ++kb) {
           if (!mbar_wait(full0 + 8 * stage, phase, abort, p.status, p.timeout_ns)) { ok = false; break; }
           tc_fence_after();
@@ -402,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!DOWN && p.gated) {
               const uint32_t su = sw + kTileBytes;
               const uint64_t ud = p.a_mn ? smem_desc_sw128(su + k * 2048, 8192, 1024) : smem_desc_sw128(su + k * 32, 16, 1024);
-              tc_mma_f16(d + 128, ud, bd, idesc, accum);
+              tc_mma_f16(d + p.up_off, ud, bd, idesc, accum);
             }
           }
           tc_commit(empty0 + 8 * stage);
@@ -443,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bits = (word >> (16 * (g & 1))) & 0xffffu;
           if (!bits) continue;
           uint32_t vg[16], vu[16];
-          tmem_ld16(tl + buf * 256 + g * 16, vg);
-          if (p.gated) tmem_ld16(tl + buf * 256 + 128 + g * 16, vu);
+          tmem_ld16(tl + buf * p.buf_off + g * 16, vg);
+          if (p.gated) tmem_ld16(tl + buf * p.buf_off + p.up_off + g * 16, vu);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -467,8 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (last_to_arrive(p.count + s.item, (int)(c1 - c0 + 1), flag)) {
             const int64_t f4 = (int64_t)s.col * 128 + lane * 4;
             for (int j = quad; j < rows; j += 4) {
-              const float4 gv = sum_shares(p.part + j * 256 + lane * 4, (int64_t)p.tokens * 256, sh, c0, c1, t0);
-              const float4 uv = sum_shares(p.part + j * 256 + 128 + lane * 4, (int64_t)p.tokens * 256, sh, c0, c1, t0);
+              float4 o[2];
+              sum_shares<2>(p.part + j * 256 + lane * 4, 128, 2, (int64_t)p.tokens * 256, sh, c0, c1, t0, o);
+              const float4 gv = o[0], uv = o[1];
               const float g[4] = {gv.x, gv.y, gv.z, gv.w}, v[4] = {uv.x, uv.y, uv.z, uv.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -509,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float wt = wt_n;
           if (j0 + 16 < rows) load_rows(j0 + 16);
           uint32_t v[16];
-          tmem_ld16(tl + buf * 256 + j0, v);
+          tmem_ld16(tl + buf * p.buf_off + j0, v);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -531,12 +538,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t c0 = sh.owner(t0), c1 = sh.owner(t1 - 1);
             if (last_to_arrive(p.count + s.item, (int)(c1 - c0 + 1), flag)) {
               const int64_t n4 = (int64_t)s.col * 128 + lane * 4;
-              for (int t = quad; t < p.tokens; t += 4) {
-                const float4 o = sum_shares(p.part + t * 128 + lane * 4, (int64_t)p.tokens * 128, sh, c0, c1, t0);
-                const float v[4] = {o.x, o.y, o.z, o.w};
+              for (int t = quad; t < p.tokens; t += 16) {
+                float4 o[4];
+                sum_shares<4>(p.part + t * 128 + lane * 4, 4 * 128, (p.tokens - t + 3) / 4, (int64_t)p.tokens * 128, sh, c0, c1,
+                              t0, o);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (n4 + e < p.N) store16(p.out, t * p.ld + n4 + e, v[e], p.f16);
+                for (int i = 0; i < 4; ++i) {
+                  const float v[4] = {o[i].x, o[i].y, o[i].z, o[i].w};
+                  if (t + 4 * i < p.tokens)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      if (n4 + e < p.N) store16(p.out, (t + 4 * i) * p.ld + n4 + e, v[e], p.f16);
+                }
               }
             }
           }
@@ -549,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmem);
+    tmem_dealloc(tmem, p.tmem_cols);
   }
 }
 
@@ -683,6 +696,13 @@ mm_status launch_tc_moe(const MoeArgs& a, const MoeMaps& maps, void* workspace, 
       q.max_picked = (int)l.picked;
       q.table_bytes = (int)((2 * l.picked + 1) * 4 + 15) / 16 * 16;
       const int acc_bytes = q.table_bytes + (down ? T * 128 * 4 : 0);
+      const uint32_t ntp = p.nt <= 32 ? 32u : p.nt <= 64 ? 64u : 128u;
+      q.up_off = ntp;
+      q.buf_off = down || !a.wu ? ntp : 2 * ntp;
+      q.tmem_cols = 2 * q.buf_off;
+      // The whole SM's shared memory: halving the rings, so that the CTAs of
+      // both kernels fit an SM side by side, was slower (29 tokens over 128
+      // experts: 161 -> 166 us).
       q.stages = (kSmemMax - 1024 - kCtrl - acc_bytes) / q.stage_bytes;
       if (q.stages > kMaxStages) q.stages = kMaxStages;
       const int smem = 1024 + q.stages * q.stage_bytes + kCtrl + acc_bytes;
