@@ -345,8 +345,8 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
     const LowRankShrink q = {X->data, X->strides[0], p.K, A->data, A->strides[0], A->strides[1], A->strides[2], z,
                              ws + w.zt};
     s = launch_lowrank_shrink_tiles(l, &q, 1, w.zt_ld, &slots, nullptr, st);
-    if (s == MM_OK)
-      s = launch_lowrank_fused(l, g, w, ws, z, ws + w.zt, B->data, B->strides[0], B->strides[1], B->strides[2], st);
+    const LowRankFused u = {g, &w, ws, z, ws + w.zt, B->data, B->strides[0], B->strides[1], B->strides[2]};
+    if (s == MM_OK) s = launch_lowrank_finish(l, &u, nullptr, nullptr, 0, w.zt_ld, st);
     return finish(s, MM_PATH_TENSOR);
   }
   if ((s = launch_lowrank_shrink(l, X->data, X->strides[0], X->strides[1], p.K, A->data, A->strides[0], A->strides[1],
@@ -414,17 +414,16 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
       o[problems++] = {X->data, X->strides[0], K, vt, dA->data, l.R, 1, reinterpret_cast<float*>(ws + w.sums_a)};
     if (dB)
       o[problems++] = {dY->data, dY->strides[0], N, ws + w.ut, dB->data, 1, N, reinterpret_cast<float*>(ws + w.sums_b)};
-    if (s == MM_OK && problems) s = launch_lowrank_outer_tiles(l, t, o, problems, w.zt_ld, st);
-    if (s == MM_OK && dX) {
-      const GemmArgs g = projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1],
-                                    W->strides[0], K, dX->data);
-      if (fused_pays(l, g)) {
-        s = finish(launch_lowrank_fused(l, g, w.fused, ws, zv, vt, A->data, A->strides[0], A->strides[2], A->strides[1],
-                                        st), MM_PATH_TENSOR);
-      } else {
-        s = launch_lowrank_expand(l, zv, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
-        if (s == MM_OK) s = add_projection(g, st);
-      }
+    const GemmArgs g = projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1], W->strides[0], K,
+                                  dX ? dX->data : nullptr);
+    const bool fuse = dX && fused_pays(l, g);
+    const LowRankFused u = {g, &w.fused, ws, zv, vt, A->data, A->strides[0], A->strides[2], A->strides[1]};
+    if (s == MM_OK && (problems || fuse))
+      s = finish(launch_lowrank_finish(l, fuse ? &u : nullptr, &t, o, problems, w.zt_ld, st),
+                 fuse ? MM_PATH_TENSOR : MM_PATH_SIMT);
+    if (s == MM_OK && dX && !fuse) {
+      s = launch_lowrank_expand(l, zv, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
+      if (s == MM_OK) s = add_projection(g, st);
     }
     return s;
   }

@@ -61,19 +61,25 @@ struct LowRankShrink {
 };
 mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const LowRankShrink* p, int problems, int64_t zt_ld,
                                       const FusedTables* slots, const AdapterRows* sort, cudaStream_t stream);
-// Y = g (A B, 16-bit, no batch) + z b, z, zt and the slots made before.
-mm_status launch_lowrank_fused(const LowRankArgs& l, const GemmArgs& g, const FusedLayout& w, char* ws, const float* z,
-                               const void* zt, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
-                               cudaStream_t stream);
-// One or two gradients out[g, c, r] from x (16-byte aligned rows) and zt; part
-// holds lowrank_max_parts * C * R floats.
+// What follows the factors: the fused product Y = product (A B, 16-bit, no
+// batch) + z b (NULL: none), whose z, zt and slots were made before, and one
+// or two gradients (`rows` sorted before), each out[g, c, r] from x (16-byte
+// aligned rows) and zt; part holds lowrank_max_parts * C * R floats.
+struct LowRankFused {
+  GemmArgs product;
+  const FusedLayout* layout;
+  char* ws;
+  const float* z;
+  const void* zt;
+  const void* b; int64_t b_gs, b_rs, b_ns;
+};
 struct LowRankOuter {
   const void* x; int64_t x_rs, C;
   const void* zt;
   void* out; int64_t o_cs, o_rs;
   float* part;
 };
-mm_status launch_lowrank_outer_tiles(const LowRankArgs& l, const AdapterRows& t, const LowRankOuter* o, int problems,
-                                     int64_t zt_ld, cudaStream_t stream);
+mm_status launch_lowrank_finish(const LowRankArgs& l, const LowRankFused* fused, const AdapterRows* rows,
+                                const LowRankOuter* outer, int problems, int64_t zt_ld, cudaStream_t stream);
 
 }  // namespace qg

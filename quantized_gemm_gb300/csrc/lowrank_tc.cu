@@ -17,7 +17,7 @@
 // tile on top of K / 64, and Y is written once.  A zero times an infinity or
 // a NaN is not zero, so the adapters that the kernel reads are copies with
 // their non-finite values set to 0; what those values add to their own rows
-// comes last (lowrank_fix_kernel), with the rows of any adapter past
+// comes last (lowrank_fix), with the rows of any adapter past
 // kExtPerTile of one tile or kSlots in all.
 #include <cstring>
 
@@ -378,7 +378,8 @@ __device__ void adapter_slots(const LowRankArgs& l, const FusedTables& t, uint8_
 template <typename T, int NT>
 __global__ void __launch_bounds__(kShThreads, NT <= 4 ? 2 : 1)
     shrink_tiles_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
-                        const LowRankArgs l, const ShrinkArgs p0, const ShrinkArgs p1, const int tiles,
+                        const LowRankArgs l, const __grid_constant__ ShrinkArgs p0,
+                        const __grid_constant__ ShrinkArgs p1, const int tiles,
                         const int problems, const FusedTables slots, const AdapterRows sort) {
   pdl_begin();
   extern __shared__ __align__(16) uint8_t sm[];
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kShThreads, NT <= 4 ? 2 : 1)
 // A block sums one chunk (kChunkRows rows of one adapter) for 128 columns of x
 // and 64 ranks: out[c, r] += x[m, c] z[m, r], 32 rows a step in a 3-stage
 // ring.  An adapter of one chunk is written at once; the others' chunks are
-// added, in order, by outer_sum_kernel.
+// added, in order, by outer_sum.
 constexpr int kOutC = 128, kOutRows = 32, kOutStages = 3, kOutThreads = 256;
 constexpr int kOutXPitch = kOutC * 2 + 16, kOutZPitch = 64 * 2 + 16;
 constexpr int kOutStage = kOutRows * (kOutXPitch + kOutZPitch);
@@ -415,16 +416,13 @@ struct OuterProblem {
   float* part;
 };
 
-// grid: (columns of both problems' x, chunks, ranks)
+// Block bx: 128 columns of the first problem's x (below blocks0) or the second's.
 template <typename T>
-__global__ void __launch_bounds__(kOutThreads)
-    outer_tiles_kernel(const LowRankArgs l, const AdapterRows t, const OuterProblem<T> p0, const OuterProblem<T> p1,
-                       const int blocks0, const int64_t zt_ld) {
-  pdl_begin();
-  extern __shared__ __align__(16) uint8_t sm[];
+__device__ void outer_tile(const LowRankArgs& l, const AdapterRows& t, const OuterProblem<T>& p0, const OuterProblem<T>& p1,
+                           const int blocks0, const int64_t zt_ld, const int bx, uint8_t* sm) {
   __shared__ int32_t rows[kChunkRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = (int)l.G;
-  const OuterProblem<T>& p = (int)blockIdx.x < blocks0 ? p0 : p1;
+  const OuterProblem<T>& p = bx < blocks0 ? p0 : p1;
   const int64_t C = p.C;
   __shared__ int found;                             // the adapter with first_chunk(g) <= chunk < first_chunk(g + 1)
   for (int h = tid; h < G; h += kOutThreads)
@@ -439,7 +437,7 @@ __global__ void __launch_bounds__(kOutThreads)
   if (n <= 0) return;
   for (int i = tid; i < n; i += kOutThreads) rows[i] = __ldcg(t.row + first + i);
   __syncthreads();
-  const int64_t c0 = (int64_t)((int)blockIdx.x < blocks0 ? blockIdx.x : blockIdx.x - blocks0) * kOutC;
+  const int64_t c0 = (int64_t)(bx < blocks0 ? bx : bx - blocks0) * kOutC;
   const int cn = (int)min((int64_t)kOutC, C - c0);
   const int r0 = blockIdx.z * 64, rc = (int)min((int64_t)64, l.R - r0), nt = (rc + 7) / 8;
   const uint32_t ring = shared_u32(sm);
@@ -516,36 +514,32 @@ __global__ void __launch_bounds__(kOutThreads)
 }
 
 // The adapters with several chunks (their sum) or none (zeros); element e of
-// an adapter's [C, R] in the output's own order.  grid.z: the problems.
+// an adapter's [C, R] in the output's own order; block bx of nbx.
 template <typename T>
-__global__ void __launch_bounds__(256)
-    outer_sum_kernel(const LowRankArgs l, const AdapterRows t, const OuterProblem<T> p0, const OuterProblem<T> p1) {
-  pdl_begin();
-  const OuterProblem<T>& p = blockIdx.z == 0 ? p0 : p1;
+__device__ void outer_sum(const LowRankArgs& l, const AdapterRows& t, const OuterProblem<T>& p, const int g, const int bx,
+                          const int nbx) {
   const int64_t n = p.C * l.R;
-  for (int g = blockIdx.y; g < l.G; g += gridDim.y) {
-    const int begin = __ldcg(t.offset + g);
-    const int k = (__ldcg(t.offset + g + 1) - begin + kChunkRows - 1) / kChunkRows;
-    if (k == 1) continue;
-    const float* src = p.part + (int64_t)first_part(begin) * n;
-    if (n % 4 == 0) {
-      for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; e < n; e += (int64_t)gridDim.x * 1024) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int begin = __ldcg(t.offset + g);
+  const int k = (__ldcg(t.offset + g + 1) - begin + kChunkRows - 1) / kChunkRows;
+  if (k == 1) return;
+  const float* src = p.part + (int64_t)first_part(begin) * n;
+  if (n % 4 == 0) {
+    for (int64_t e = ((int64_t)bx * 256 + threadIdx.x) * 4; e < n; e += (int64_t)nbx * 1024) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int c = 0; c < k; ++c) {
-          const float4 u = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)c * n + e));
-          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-        }
-        T o[4] = {from_f32<T>(v.x), from_f32<T>(v.y), from_f32<T>(v.z), from_f32<T>(v.w)};
+      for (int c = 0; c < k; ++c) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)c * n + e));
+        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+      }
+      T o[4] = {from_f32<T>(v.x), from_f32<T>(v.y), from_f32<T>(v.z), from_f32<T>(v.w)};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p.out[(int64_t)g * n + e + j] = o[j];
-      }
-    } else {
-      for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
-        float v = 0.f;
-        for (int c = 0; c < k; ++c) v += __ldcg(src + (int64_t)c * n + e);
-        p.out[(int64_t)g * n + e] = from_f32<T>(v);
-      }
+      for (int j = 0; j < 4; ++j) p.out[(int64_t)g * n + e + j] = o[j];
+    }
+  } else {
+    for (int64_t e = (int64_t)bx * 256 + threadIdx.x; e < n; e += (int64_t)nbx * 256) {
+      float v = 0.f;
+      for (int c = 0; c < k; ++c) v += __ldcg(src + (int64_t)c * n + e);
+      p.out[(int64_t)g * n + e] = from_f32<T>(v);
     }
   }
 }
@@ -557,17 +551,27 @@ __global__ void __launch_bounds__(256)
 // The others: the adapters' copies, 1024 columns of one slot a block.
 constexpr int kPlaceParts = 4;
 template <typename T>
-__global__ void __launch_bounds__(256)
-    lowrank_place_kernel(const LowRankArgs l, const FusedTables t, const int tile_rows, const int tiles, const T* zt,
-                         const int64_t zt_ld, T* factors, const int64_t f_ld, const T* b, const int64_t b_gs,
-                         const int64_t b_rs, const int64_t b_ns, const int64_t N, T* copy, const int64_t c_ld,
-                         const int pieces, const int vec) {
-  pdl_begin();
+struct PlaceArgs {
+  int blocks;                    // 0: nothing to place
+  int tile_rows, tiles;
+  const T* zt; int64_t zt_ld;
+  T* factors; int64_t f_ld;
+  const T* b; int64_t b_gs, b_rs, b_ns, N;
+  T* copy; int64_t c_ld;
+  int pieces, vec;
+};
+
+template <typename T>
+__device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const PlaceArgs<T>& p, const int bx) {
+  const int tile_rows = p.tile_rows, tiles = p.tiles, pieces = p.pieces, vec = p.vec;
+  const T *zt = p.zt, *b = p.b;
+  T *factors = p.factors, *copy = p.copy;
+  const int64_t zt_ld = p.zt_ld, f_ld = p.f_ld, b_gs = p.b_gs, b_rs = p.b_rs, b_ns = p.b_ns, N = p.N, c_ld = p.c_ld;
   const int tid = threadIdx.x;
-  if ((int)blockIdx.x < tiles * kPlaceParts) {
+  if (bx < tiles * kPlaceParts) {
     __shared__ int first, list[kExtPerTile];
     __shared__ signed char entry[256];
-    const int tile = blockIdx.x / kPlaceParts, part = blockIdx.x % kPlaceParts;
+    const int tile = bx / kPlaceParts, part = bx % kPlaceParts;
     const int64_t m = (int64_t)tile * tile_rows + tid;
     int slot = -1;
     bool has = false;
@@ -618,7 +622,7 @@ __global__ void __launch_bounds__(256)
     }
     return;
   }
-  const int rest = (int)blockIdx.x - tiles * kPlaceParts;
+  const int rest = bx - tiles * kPlaceParts;
   const int piece = rest % pieces, slot = rest / pieces;
   if (slot >= __ldcg(t.head)) return;
   constexpr uint16_t kExp = std::is_same<T, __half>::value ? 0x7C00 : 0x7F80;
@@ -681,31 +685,70 @@ __global__ void __launch_bounds__(256)
 
 // What the fused product left out: Y[m] += z[m] b[g] for rows outside their
 // tile's list, and the terms of non-finite adapter values.  Usually nothing.
+constexpr int kFixColumns = 8, kFixRows = 64;   // its blocks: 256 columns at a time, rows in turn
+
 template <typename T>
-__global__ void __launch_bounds__(256)
-    lowrank_fix_kernel(const LowRankArgs l, const FusedTables t, const float* z, const T* b, const int64_t b_gs,
-                       const int64_t b_rs, const int64_t b_ns, const int64_t N, T* y) {
-  pdl_begin();
+struct FixArgs {
+  int blocks;                    // 0: nothing to fix
+  const float* z;
+  const T* b; int64_t b_gs, b_rs, b_ns, N;
+  T* y;
+};
+
+template <typename T>
+__device__ void lowrank_fix(const LowRankArgs& l, const FusedTables& t, const FixArgs<T>& p, const int bx) {
   if (__ldcg(t.head + 1) == 0) return;
   constexpr uint16_t kExp = std::is_same<T, __half>::value ? 0x7C00 : 0x7F80;
-  for (int64_t m = blockIdx.y; m < l.M; m += gridDim.y) {
+  for (int64_t m = bx / kFixColumns; m < l.M; m += kFixRows) {
     const int64_t g = load_index(l.idx, m * l.idx_s, l.ind64);
     if (g < 0 || g >= l.G) continue;
     const bool all = __ldcg(t.row_entry + m) < 0;
     if (!all && !__ldcg(t.bad + __ldcg(t.slot_of + g))) continue;
-    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < N; n += (int64_t)gridDim.x * 256) {
-      const T* bn = b + g * b_gs + n * b_ns;
+    for (int64_t n = (int64_t)(bx % kFixColumns) * 256 + threadIdx.x; n < p.N; n += kFixColumns * 256) {
+      const T* bn = p.b + g * p.b_gs + n * p.b_ns;
       float v = 0.f;
       bool any = all;
       for (int64_t r = 0; r < l.R; ++r) {
-        const T q = bn[r * b_rs];
+        const T q = bn[r * p.b_rs];
         const bool bad = (*reinterpret_cast<const uint16_t*>(&q) & kExp) == kExp;
-        if (all || bad) v = __fmaf_rn(z[m * l.R + r], to_f32(q), v);
+        if (all || bad) v = __fmaf_rn(p.z[m * l.R + r], to_f32(q), v);
         any |= bad;
       }
-      if (any) y[m * N + n] = from_f32<T>(to_f32(y[m * N + n]) + v);
+      if (any) p.y[m * p.N + n] = from_f32<T>(to_f32(p.y[m * p.N + n]) + v);
     }
   }
+}
+
+// ------------------------------------------------------------------ kernels of several steps
+
+// After the factors: the fused product's operands (first blocks) and the
+// adapters' gradients, which do not depend on each other.
+template <typename T>
+__global__ void __launch_bounds__(256, 3)
+    lowrank_middle_kernel(const LowRankArgs l, const FusedTables f, const __grid_constant__ PlaceArgs<T> place,
+                          const AdapterRows t, const __grid_constant__ OuterProblem<T> p0,
+                          const __grid_constant__ OuterProblem<T> p1, const int blocks0, const int64_t zt_ld) {
+  pdl_begin();
+  extern __shared__ __align__(16) uint8_t sm[];
+  if ((int)blockIdx.x < place.blocks) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) lowrank_place<T>(l, f, place, blockIdx.x);
+  } else {
+    outer_tile<T>(l, t, p0, p1, blocks0, zt_ld, (int)blockIdx.x - place.blocks, sm);
+  }
+}
+
+// After those and the fused product: the fix (first blocks) and the chunks' sums.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    lowrank_last_kernel(const LowRankArgs l, const FusedTables f, const __grid_constant__ FixArgs<T> fix,
+                        const AdapterRows t, const __grid_constant__ OuterProblem<T> p0,
+                        const __grid_constant__ OuterProblem<T> p1, const int sum_blocks) {
+  pdl_begin();
+  int bx = (int)blockIdx.x;
+  if (bx < fix.blocks) return lowrank_fix<T>(l, f, fix, bx);
+  bx -= fix.blocks;
+  const int per = (int)l.G * sum_blocks;
+  outer_sum<T>(l, t, bx < per ? p0 : p1, bx % per / sum_blocks, bx % sum_blocks, sum_blocks);
 }
 
 // ------------------------------------------------------------------ host side
@@ -764,28 +807,6 @@ mm_status shrink_launch(const LowRankArgs& l, const LowRankShrink* q, int proble
                     sort ? *sort : AdapterRows{}) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
-template <typename T>
-mm_status outer_launch(const LowRankArgs& l, const AdapterRows& t, const LowRankOuter* o, int problems, int64_t zt_ld,
-                       cudaStream_t stream) {
-  OuterProblem<T> p[2];
-  int64_t blocks[2] = {0, 0}, most = 0;
-  for (int i = 0; i < 2; ++i) {
-    const LowRankOuter& q = o[i < problems ? i : 0];
-    p[i] = {static_cast<const T*>(q.x), q.x_rs, q.C, static_cast<const T*>(q.zt), static_cast<T*>(q.out), q.o_cs, q.o_rs,
-            q.part};
-    if (i < problems) blocks[i] = (q.C + kOutC - 1) / kOutC;
-    if (q.C > most) most = q.C;
-  }
-  const int64_t chunks = lowrank_max_chunks(l);
-  const dim3 grid((unsigned)(blocks[0] + blocks[1]), (unsigned)chunks, (unsigned)((l.R + 63) / 64));
-  if (chunks > 0 && launch_pdl(outer_tiles_kernel<T>, grid, dim3(kOutThreads), (size_t)(kOutStages * kOutStage), stream, l,
-                               t, p[0], p[1], (int)blocks[0], zt_ld) != cudaSuccess)
-    return MM_ERR_CUDA;
-  const int64_t gx = (most * l.R + 1023) / 1024;
-  const dim3 gs((unsigned)(gx < 64 ? gx : 64), (unsigned)l.G, (unsigned)problems);
-  return launch_pdl(outer_sum_kernel<T>, gs, dim3(256), 0, stream, l, t, p[0], p[1]) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
-}
-
 }  // namespace
 
 bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
@@ -801,35 +822,6 @@ mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const LowRankShrink*
   return l.dtype == MM_F16 ? shrink_launch<__half>(l, p, problems, zt_ld, slots, sort, stream)
                            : shrink_launch<__nv_bfloat16>(l, p, problems, zt_ld, slots, sort, stream);
 }
-
-namespace {
-
-template <typename T>
-mm_status place_launch(const LowRankArgs& l, const FusedTables& t, int tile_rows, const void* zt, int64_t zt_ld,
-                       void* factors, int64_t f_ld, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns, int64_t N,
-                       void* copy, int64_t c_ld, int64_t slots, cudaStream_t stream) {
-  const int64_t tiles = (l.M + tile_rows - 1) / tile_rows, pieces = (c_ld + 1023) / 1024;
-  const int64_t blocks = tiles * kPlaceParts + slots * pieces;
-  if (blocks > 0x7fffffffLL) return MM_ERR_UNSUPPORTED;
-  // 16-byte reads along n (1) or along the ranks (2)
-  const bool base = (l.G == 1 || b_gs % 8 == 0) && reinterpret_cast<uintptr_t>(b) % 16 == 0;
-  const int vec = base && b_ns == 1 && b_rs % 8 == 0 && N % 8 == 0   ? 1
-                  : base && b_rs == 1 && b_ns % 8 == 0 && l.R % 8 == 0 ? 2 : 0;
-  return launch_pdl(lowrank_place_kernel<T>, dim3((unsigned)blocks), dim3(256), 0, stream, l, t, tile_rows, (int)tiles,
-                    static_cast<const T*>(zt), zt_ld, static_cast<T*>(factors), f_ld, static_cast<const T*>(b), b_gs, b_rs,
-                    b_ns, N, static_cast<T*>(copy), c_ld, (int)pieces, vec) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
-}
-
-template <typename T>
-mm_status fix_launch(const LowRankArgs& l, const FusedTables& t, const float* z, const void* b, int64_t b_gs, int64_t b_rs,
-                     int64_t b_ns, int64_t N, void* y, cudaStream_t stream) {
-  const int64_t gx = (N + 255) / 256 < 8 ? (N + 255) / 256 : 8, gy = l.M < 64 ? l.M : 64;
-  return launch_pdl(lowrank_fix_kernel<T>, dim3((unsigned)gx, (unsigned)gy), dim3(256), 0, stream, l, t, z,
-                    static_cast<const T*>(b), b_gs, b_rs, b_ns, N, static_cast<T*>(y)) == cudaSuccess ? MM_OK
-                                                                                                     : MM_ERR_CUDA;
-}
-
-}  // namespace
 
 FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N) {
   FusedLayout w;
@@ -873,34 +865,72 @@ FusedTables lowrank_fused_tables(const FusedLayout& w, char* ws) {
   return t;
 }
 
-// After the shrink that made z, zt and the slots: place, product, fix.
-mm_status launch_lowrank_fused(const LowRankArgs& l, const GemmArgs& g, const FusedLayout& w, char* ws, const float* z,
-                               const void* zt, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
-                               cudaStream_t stream) {
-  const FusedTables t = lowrank_fused_tables(w, ws);
-  void* factors = ws + w.factors;
-  void* copy = ws + w.copy;
-  void* y = const_cast<void*>(g.y.ptr);
-  LowRankExt e;
-  e.tile_rows = tc_lowrank_tile_rows(g);
-  e.factors = factors; e.factor_ld = w.f_ld;
-  e.adapters = copy; e.slots = w.slots; e.R = l.R; e.adapter_ld = w.c_ld;
-  e.count = t.ext_count; e.slot = t.ext_slot;
-  const bool f16 = l.dtype == MM_F16;
-  mm_status s = f16 ? place_launch<__half>(l, t, e.tile_rows, zt, w.zt_ld, factors, w.f_ld, b, b_gs, b_rs, b_ns, g.N, copy,
-                                           w.c_ld, w.slots, stream)
-                    : place_launch<__nv_bfloat16>(l, t, e.tile_rows, zt, w.zt_ld, factors, w.f_ld, b, b_gs, b_rs, b_ns,
-                                                  g.N, copy, w.c_ld, w.slots, stream);
-  if (s != MM_OK) return s;
-  if ((s = launch_tc_lowrank(g, e, l.status, stream)) != MM_OK) return s;
-  return f16 ? fix_launch<__half>(l, t, z, b, b_gs, b_rs, b_ns, g.N, y, stream)
-             : fix_launch<__nv_bfloat16>(l, t, z, b, b_gs, b_rs, b_ns, g.N, y, stream);
+namespace {
+
+template <typename T>
+mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const AdapterRows* t, const LowRankOuter* o,
+                       int problems, int64_t zt_ld, cudaStream_t stream) {
+  FusedTables f = {};
+  PlaceArgs<T> place = {};
+  FixArgs<T> fix = {};
+  LowRankExt e = {};
+  if (u) {
+    const FusedLayout& w = *u->layout;
+    f = lowrank_fused_tables(w, u->ws);
+    e.tile_rows = tc_lowrank_tile_rows(u->product);
+    e.factors = u->ws + w.factors; e.factor_ld = w.f_ld;
+    e.adapters = u->ws + w.copy; e.slots = w.slots; e.R = l.R; e.adapter_ld = w.c_ld;
+    e.count = f.ext_count; e.slot = f.ext_slot;
+    const int64_t N = u->product.N, tiles = (l.M + e.tile_rows - 1) / e.tile_rows, pieces = (w.c_ld + 1023) / 1024;
+    const int64_t blocks = tiles * kPlaceParts + w.slots * pieces;
+    if (blocks > (1 << 30)) return MM_ERR_UNSUPPORTED;
+    // 16-byte reads of b along n (1) or along the ranks (2)
+    const bool base = (l.G == 1 || u->b_gs % 8 == 0) && reinterpret_cast<uintptr_t>(u->b) % 16 == 0;
+    place.blocks = (int)blocks;
+    place.tile_rows = e.tile_rows; place.tiles = (int)tiles;
+    place.zt = static_cast<const T*>(u->zt); place.zt_ld = w.zt_ld;
+    place.factors = reinterpret_cast<T*>(u->ws + w.factors); place.f_ld = w.f_ld;
+    place.b = static_cast<const T*>(u->b);
+    place.b_gs = u->b_gs; place.b_rs = u->b_rs; place.b_ns = u->b_ns; place.N = N;
+    place.copy = reinterpret_cast<T*>(u->ws + w.copy); place.c_ld = w.c_ld;
+    place.pieces = (int)pieces;
+    place.vec = base && u->b_ns == 1 && u->b_rs % 8 == 0 && N % 8 == 0     ? 1
+                : base && u->b_rs == 1 && u->b_ns % 8 == 0 && l.R % 8 == 0 ? 2 : 0;
+    fix.blocks = kFixColumns * kFixRows;
+    fix.z = u->z;
+    fix.b = place.b; fix.b_gs = u->b_gs; fix.b_rs = u->b_rs; fix.b_ns = u->b_ns; fix.N = N;
+    fix.y = static_cast<T*>(const_cast<void*>(u->product.y.ptr));
+  }
+  OuterProblem<T> p[2] = {};
+  int64_t blocks[2] = {0, 0}, most = 0;
+  for (int i = 0; i < problems; ++i) {
+    p[i] = {static_cast<const T*>(o[i].x), o[i].x_rs, o[i].C, static_cast<const T*>(o[i].zt), static_cast<T*>(o[i].out),
+            o[i].o_cs, o[i].o_rs, o[i].part};
+    blocks[i] = (o[i].C + kOutC - 1) / kOutC;
+    if (o[i].C > most) most = o[i].C;
+  }
+  const AdapterRows rows = t ? *t : AdapterRows{};
+  const dim3 middle((unsigned)(place.blocks + blocks[0] + blocks[1]), problems ? (unsigned)lowrank_max_chunks(l) : 1u,
+                    problems ? (unsigned)((l.R + 63) / 64) : 1u);
+  if (launch_pdl(lowrank_middle_kernel<T>, middle, dim3(256), problems ? (size_t)(kOutStages * kOutStage) : 0, stream, l, f,
+                 place, rows, p[0], p[1], (int)blocks[0], zt_ld) != cudaSuccess)
+    return MM_ERR_CUDA;
+  if (u) {
+    const mm_status s = launch_tc_lowrank(u->product, e, l.status, stream);
+    if (s != MM_OK) return s;
+  }
+  const int64_t per = (most * l.R + 1023) / 1024, sum_blocks = per < 64 ? per : 64;
+  const int64_t last = fix.blocks + problems * l.G * sum_blocks;
+  return launch_pdl(lowrank_last_kernel<T>, dim3((unsigned)last), dim3(256), 0, stream, l, f, fix, rows, p[0], p[1],
+                    (int)(sum_blocks > 0 ? sum_blocks : 1)) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
-mm_status launch_lowrank_outer_tiles(const LowRankArgs& l, const AdapterRows& t, const LowRankOuter* o, int problems,
-                                     int64_t zt_ld, cudaStream_t stream) {
-  return l.dtype == MM_F16 ? outer_launch<__half>(l, t, o, problems, zt_ld, stream)
-                           : outer_launch<__nv_bfloat16>(l, t, o, problems, zt_ld, stream);
+}  // namespace
+
+mm_status launch_lowrank_finish(const LowRankArgs& l, const LowRankFused* fused, const AdapterRows* rows,
+                                const LowRankOuter* outer, int problems, int64_t zt_ld, cudaStream_t stream) {
+  return l.dtype == MM_F16 ? finish_typed<__half>(l, fused, rows, outer, problems, zt_ld, stream)
+                           : finish_typed<__nv_bfloat16>(l, fused, rows, outer, problems, zt_ld, stream);
 }
 
 }  // namespace qg
