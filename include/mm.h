@@ -319,9 +319,10 @@ mm_status mm_route_topk_grad(const mm_tensor* logits, const mm_tensor* indices, 
  * (NULL = 1).  activation is an mm_activation.  Inputs take any strides, so
  * w_gate and w_up may be the two halves of one tensor.
  * Every sum is fp32.  On the tensor cores (bf16/f16 operands whose rows are
- * 16-byte aligned along a unit-stride matrix dimension) h is rounded once to
- * T between the two products; the CUDA-core form keeps it fp32.  out is
- * rounded once to T.
+ * 16-byte aligned along a unit-stride matrix dimension) h is held as the sum
+ * of two T values between the two products (its first part is infinite where
+ * h exceeds T's range); the CUDA-core form keeps it fp32.  out is rounded
+ * once to T.
  * An index of -1 is no pick (mm_route_topk writes it); a token without any
  * pick gets zeros.  Any other index outside [0,G) counts as -1 and is
  * recorded as MM_ERR_INDEX_RANGE.  A token's result depends on its own picks

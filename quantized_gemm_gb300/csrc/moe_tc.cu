@@ -13,6 +13,13 @@
 // one token, and only the columns of tokens that picked the expert are used,
 // so no token sees another's values or an unpicked expert's.
 //
+// h is held as the sum of two T values (hi = T(h), lo = T(h - hi): 16 bits for
+// bf16, 22 for f16), which the second product takes as separate tokens side by
+// side (N doubled) and adds in its epilogue: no rounding of h worth speaking of
+// next to the output's, for 2 KB more per 16 KB of weights out of the L2.  (As
+// two MMAs per step instead, one token's layer took 134 us against 125: an MMA
+// this narrow takes as long as a wider one.)
+//
 // The work is one sequence of k-blocks of 64 (all tiles of all picked experts
 // for `hidden`; for `down` each output tile's experts in turn), cut into equal
 // contiguous shares, one per SM: every SM streams the same number of bytes
@@ -79,8 +86,9 @@ struct MoeTcParams {
   int max_picked, table_bytes;
   uint32_t tmem_cols, up_off, buf_off;   // TMEM columns: allocated, of the up product, of the second buffer
   uint32_t idesc0;        // instruction descriptor without N
-  void* out;              // hidden: h [rows, h_ld]; down: out [tokens, N]
+  void* out;              // hidden: h, hi rows then lo rows [2 * h_rows, ld]; down: out [tokens, N]
   int64_t ld;
+  int h_rows;
   float* part;            // partial sums, two slots per CTA
   int32_t* count;         // this phase's arrival counters
   unsigned* status;
@@ -263,6 +271,13 @@ __device__ __forceinline__ void store16(void* dst, int64_t i, float v, int f16) 
   else static_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(v);
 }
 
+// h[row, f] as its two parts; an infinite or NaN h is hi alone.
+__device__ __forceinline__ void store_h(const MoeTcParams& p, int row, int64_t f, float h) {
+  const float hi = p.f16 ? __half2float(__float2half_rn(h)) : __bfloat162float(__float2bfloat16_rn(h));
+  store16(p.out, (int64_t)row * p.ld + f, hi, p.f16);
+  store16(p.out, (int64_t)(p.h_rows + row) * p.ld + f, fabsf(hi) < INFINITY ? h - hi : 0.f, p.f16);
+}
+
 template <bool DOWN>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmU,
@@ -344,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dst = ring + st * p.stage_bytes + kW * kTileBytes, bar = full0 + 8 * st;
         if (DOWN) {
           const int rows = seg_rows(a), r0 = t_offset[a];
-          for (int r = 0; r < rows; r += 16) tma_load_3d(dst + r * 128, &tmX, (int32_t)kb * 64, r0 + r, 0, bar);
+          for (int r = 0; r < rows; r += 16)      // 16 rows' hi, then their lo
+            tma_load_3d(dst + 2 * r * 128, &tmX, (int32_t)kb * 64, r0 + r, 0, bar);
         } else {
           tma_load_3d(dst, &tmX, (int32_t)kb * 64, 0, 0, bar);
         }
@@ -359,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t u = ub; u < ue && ok;) {
         const Seg s = seg_at<DOWN>(p, picked, u, ue);
         const int32_t e = t_expert[s.a];
-        const uint32_t tok_bytes = DOWN ? (uint32_t)((seg_rows(s.a) + 15) & ~15) * 128u : (uint32_t)p.nt * 128u;
+        const uint32_t tok_bytes = DOWN ? (uint32_t)((seg_rows(s.a) + 15) & ~15) * 256u : (uint32_t)p.nt * 128u;
         for (uint32_t kb = s.kb0; kb < s.kb1; ++kb) {
           if (DOWN && early && nearly == early) release_early();
           if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort, p.status, p.timeout_ns)) { ok = false; break; }
@@ -393,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t buf = seg & 1, aph = (seg >> 1) & 1;
         if (!mbar_wait(acce0 + 8 * buf, aph ^ 1, abort, p.status, p.timeout_ns)) break;
         tc_fence_after();
-        const uint32_t n = DOWN ? (uint32_t)((seg_rows(s.a) + 15) & ~15) : (uint32_t)p.nt;
+        const uint32_t n = DOWN ? (uint32_t)((seg_rows(s.a) + 15) & ~15) * 2u : (uint32_t)p.nt;
         const uint32_t idesc = p.idesc0 | ((n >> 3) << 17), d = tmem + buf * p.buf_off;
         for (uint32_t kb = s.kb0; kb < s.kb1; ++kb) {
           if (!mbar_wait(full0 + 8 * stage, phase, abort, p.status, p.timeout_ns)) { ok = false; break; }
@@ -458,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float gv = __uint_as_float(vg[j]), uv = p.gated ? __uint_as_float(vu[j]) : 1.f;
             if (whole) {
               const float h = p.gated ? activate(gv, p.act) * uv : activate(gv, p.act);
-              if (f < p.F) store16(p.out, (int64_t)(r0 + r) * p.ld + f, h, p.f16);
+              if (f < p.F) store_h(p, r0 + r, f, h);
             } else {
               part[(int64_t)r * 256] = gv;
               part[(int64_t)r * 256 + 128] = uv;
@@ -479,9 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float g[4] = {gv.x, gv.y, gv.z, gv.w}, v[4] = {uv.x, uv.y, uv.z, uv.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (f4 + e < p.F)
-                  store16(p.out, (int64_t)(r0 + j) * p.ld + f4 + e, p.gated ? activate(g[e], p.act) * v[e] : activate(g[e], p.act),
-                          p.f16);
+                if (f4 + e < p.F) store_h(p, r0 + j, f4 + e, p.gated ? activate(g[e], p.act) * v[e] : activate(g[e], p.act));
             }
           }
         }
@@ -515,14 +529,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tok = tok_n;
           const float wt = wt_n;
           if (j0 + 16 < rows) load_rows(j0 + 16);
-          uint32_t v[16];
-          tmem_ld16(tl + buf * p.buf_off + j0, v);
+          uint32_t v[16], lo[16];
+          tmem_ld16(tl + buf * p.buf_off + 2 * j0, v);
+          tmem_ld16(tl + buf * p.buf_off + 2 * j0 + 16, lo);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const int t = __shfl_sync(0xffffffffu, tok, j);
             const float w = __shfl_sync(0xffffffffu, wt, j);
-            if (j0 + j < rows) acc[t * 128 + l] = __fmaf_rn(w, __uint_as_float(v[j]), acc[t * 128 + l]);
+            if (j0 + j < rows)
+              acc[t * 128 + l] = __fmaf_rn(w, __uint_as_float(v[j]) + __uint_as_float(lo[j]), acc[t * 128 + l]);
           }
         }
         release(buf);
@@ -592,7 +608,7 @@ MoeLayout moe_layout(const MoeArgs& a) {
   l.off_token = take((size_t)l.rows * 4);
   l.off_weight = take((size_t)l.rows * 4);
   l.off_count = take((size_t)(l.picked * l.f_tiles + l.n_tiles) * 4);
-  l.off_h = take((size_t)l.rows * (size_t)l.h_ld * 2);
+  l.off_h = take((size_t)2 * (size_t)l.rows * (size_t)l.h_ld * 2);
   l.off_part = take((size_t)2 * (size_t)sm_count_public() * (size_t)l.tok * 256 * 4);
   l.total = o;
   return l;
@@ -660,6 +676,7 @@ mm_status launch_tc_moe(const MoeArgs& a, const MoeMaps& maps, void* workspace, 
   p.tb.count = reinterpret_cast<int32_t*>(ws + l.off_count);
   p.tb.count_n = l.picked * l.f_tiles + l.n_tiles;
   p.F = a.F; p.N = a.N;
+  p.h_rows = (int)l.rows;
   p.gated = a.wu != nullptr; p.act = a.act; p.f16 = a.dtype == MM_F16;
   p.part = reinterpret_cast<float*>(ws + l.off_part);
   p.status = status;
@@ -667,7 +684,13 @@ mm_status launch_tc_moe(const MoeArgs& a, const MoeMaps& maps, void* workspace, 
 
   const OperandPlan &wg = maps.gate, &wu = maps.up, &wd = maps.down;
   OperandPlan h, x;
-  if (!plan_rows(ws + l.off_h, a.dtype, l.rows, a.F, l.h_ld, 1, 16, &h)) return MM_ERR_UNSUPPORTED;
+  BatchMap parts;                          // h's hi and lo rows, 16 of each in one box
+  memset(&parts, 0, sizeof(parts));
+  parts.nb = 1;
+  parts.shape[0] = parts.count = 2;
+  const int64_t part_stride[kMaxBatchDims] = {l.rows * l.h_ld, 0, 0, 0, 0, 0};
+  if (!plan_operand(ws + l.off_h, a.dtype, l.rows, a.F, l.h_ld, 1, parts, part_stride, 16, &h, 2) || h.mn_major)
+    return MM_ERR_UNSUPPORTED;
   const int plan_smem = (int)(a.G * (kMaskWords + 1) * 4);
   const int sms = sm_count_public();
   for (int64_t t0 = 0; t0 < a.tokens; t0 += kTok) {
@@ -692,13 +715,13 @@ mm_status launch_tc_moe(const MoeArgs& a, const MoeMaps& maps, void* workspace, 
       if (down) q.out = static_cast<uint16_t*>(a.out) + t0 * a.N;
       q.ld = down ? a.N : l.h_ld;
       q.count = p.tb.count + (down ? l.picked * l.f_tiles : 0);
-      q.stage_bytes = (down ? 1 : 2) * kTileBytes + p.nt * 128;
+      q.stage_bytes = (down ? 1 : 2) * kTileBytes + (down ? 2 : 1) * p.nt * 128;
       q.max_picked = (int)l.picked;
       q.table_bytes = (int)((2 * l.picked + 1) * 4 + 15) / 16 * 16;
       const int acc_bytes = q.table_bytes + (down ? T * 128 * 4 : 0);
       const uint32_t ntp = p.nt <= 32 ? 32u : p.nt <= 64 ? 64u : 128u;
       q.up_off = ntp;
-      q.buf_off = down || !a.wu ? ntp : 2 * ntp;
+      q.buf_off = down || a.wu ? 2 * ntp : ntp;
       q.tmem_cols = 2 * q.buf_off;
       // The whole SM's shared memory: halving the rings, so that the CTAs of
       // both kernels fit an SM side by side, was slower (29 tokens over 128

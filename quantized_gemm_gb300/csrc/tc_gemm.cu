@@ -1415,9 +1415,10 @@ int sm_count() {
 // element strides `mn_stride` / `k_stride` and batch strides `bstride` over the
 // broadcast batch `bm`, described as a 3-D tensor map (contiguous dimension,
 // other matrix dimension, batch).  The batch coordinate of batch index b is
-// sum_d i_d * bc[d]; false when the layout does not fit TMA.
+// sum_d i_d * bc[d]; false when the layout does not fit TMA.  A box of a 16-bit
+// K-major operand may span box_batch batch coordinates.
 bool plan_operand(const void* ptr, int dtype, int64_t mn_len, int64_t k_len, int64_t mn_stride, int64_t k_stride,
-                  const BatchMap& bm, const int64_t* bstride, int box_mn, OperandPlan* out) {
+                  const BatchMap& bm, const int64_t* bstride, int box_mn, OperandPlan* out, int box_batch) {
   auto encode = encode_fn();
   if (!encode || !ptr || (reinterpret_cast<uintptr_t>(ptr) & 15)) return false;
   if (mn_len < 1 || k_len < 1 || mn_len > 0x7fffffffLL || k_len > 0x7fffffffLL) return false;
@@ -1472,7 +1473,7 @@ bool plan_operand(const void* ptr, int dtype, int64_t mn_len, int64_t k_len, int
     out->mn_major = 0;
     dims[0] = (cuuint64_t)k_len; dims[1] = (cuuint64_t)mn_len; dims[2] = (cuuint64_t)nbat;
     strides[0] = (cuuint64_t)mn_stride * 2;
-    box[0] = 64; box[1] = (cuuint32_t)box_mn; box[2] = 1;
+    box[0] = 64; box[1] = (cuuint32_t)box_mn; box[2] = (cuuint32_t)box_batch;
   } else if (mn_stride == 1 && k_stride > 0 && k_stride % 8 == 0) {
     out->mn_major = 1;
     dims[0] = (cuuint64_t)mn_len; dims[1] = (cuuint64_t)k_len; dims[2] = (cuuint64_t)nbat;

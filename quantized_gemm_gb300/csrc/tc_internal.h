@@ -104,7 +104,7 @@ struct OperandPlan {
 };
 
 bool plan_operand(const void* ptr, int dtype, int64_t mn_len, int64_t k_len, int64_t mn_stride, int64_t k_stride,
-                  const BatchMap& bm, const int64_t* bstride, int box_mn, OperandPlan* out);
+                  const BatchMap& bm, const int64_t* bstride, int box_mn, OperandPlan* out, int box_batch = 1);
 // A plain (unswizzled) 3-D tensor map over elements of elem_bytes bytes:
 // dims d0 (contiguous) x d1 x d2, byte strides s1 and s2, box box0 x box1 x 1.
 bool plan_plain_3d(const void* ptr, int elem_bytes, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2,
