@@ -54,10 +54,11 @@ constexpr int kThreads = 192;
 constexpr int kCtrl = 512;                   // barriers, TMEM slot, flags
 constexpr int kPlanThreads = 512;
 constexpr int kPlanExperts = 2048;           // experts the plan's tables hold (shared memory)
-// A share of fewer k-blocks than this is not worth its partial sums (three
+// A share of fewer k-blocks than kMinShare is not worth its partial sums (three
 // tokens, 12 picks of K = 1000, F = 712: 32 us with 4, 27 us with 16, 35 us
-// with 24).
-constexpr uint32_t kMinShare = 12;
+// with 24).  Where a tile (hidden) or an expert's part of one (down) has fewer
+// blocks, whole ones are shares, in `down` from kMinDown blocks on.
+constexpr uint32_t kMinShare = 12, kMinDown = 4;
 constexpr int kSmemMax = 227 * 1024;
 
 // Tables written by the plan, in the workspace (read through L2: the kernels
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto seg_rows = [&](uint32_t a) { return t_offset[a + 1] - t_offset[a]; };
   Share sh;
   sh.U = picked * (uint32_t)p.col_tiles * (uint32_t)p.kblocks;
-  sh.P = max(1u, min(gridDim.x, sh.U / kMinShare));
+  sh.P = max(1u, min(gridDim.x, sh.U / max(min(kMinShare, (uint32_t)p.kblocks), DOWN ? kMinDown : 1u)));
   const uint32_t cta = blockIdx.x;
   const uint32_t ub = cta < sh.P ? sh.begin(cta) : 0u, ue = cta < sh.P ? sh.begin(cta + 1) : 0u;
   constexpr int kW = DOWN ? 1 : 2;                // weight tiles per k-block

@@ -273,6 +273,37 @@ def test_moe_layer_follows_the_router():
     assert (out.float() - ref).abs().max() < 0.05 * ref.abs().max()
 
 
+def test_the_example_runs_the_operators_together():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, os.path.join(root, "examples"))
+    import expert_step
+
+    block = expert_step.ExpertBlock(hidden=256, ffn=136, experts=12, picks=3, adapters=4, rank=8)
+    x = rand_tensor((21, 256), BF16, 77, DEV)
+    adapter = torch.arange(21, device=DEV) % 5 - 1
+    y, idx, w, out = block.step(x, adapter)
+    n = {k: to_np(getattr(block, k)) for k in ("W", "A", "B", "scales", "gate", "up", "down")}
+    a = to_np(adapter)
+    args = (to_np(x), n["W"], n["A"], n["B"], a, n["scales"])
+    assert_within(y, select.lowrank_matmul(*args), select.lowrank_matmul_bound(*args, u=U[BF16]), "y")
+    logits = to_np(qg.mm_matmul(y, block.router))            # each later step on the values it was given
+    assert np.array_equal(idx.cpu().numpy(), select.route_topk(logits, 3, 1)[0])
+    args = (to_np(y), n["gate"], n["up"], n["down"], idx.cpu().numpy(), to_np(w))
+    assert_within(out, select.moe_layer(*args), select.moe_layer_bound(*args, u=U[BF16]) + 1e-30, "out")
+    dy = rand_tensor((21, 256), BF16, 78, DEV)
+    args = (to_np(dy), to_np(x), n["W"], n["A"], n["B"], a, n["scales"])
+    for g, want, bound in zip(block.adapter_gradients(dy, x, adapter), select.lowrank_matmul_grad(*args),
+                              select.lowrank_matmul_grad_bound(*args, u=U[BF16])):
+        assert_within(g, want, bound)
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "expert_step.py"), "--steps", "3"],
+                       capture_output=True, text=True)
+    assert r.returncode == 0 and "us a step" in r.stdout, r.stderr
+
+
 # ------------------------------------------------------------------ low-rank adapters
 
 
