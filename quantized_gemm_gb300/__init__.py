@@ -361,6 +361,15 @@ def mm_grouped_matmul_noalloc(input, weights, group_indices, bias=None, out=None
     return y
 
 
+def _used_on(stream, *tensors):
+    """Tells torch's allocator that ``stream`` (None: the current one, whose memory it is) uses the tensors, which may
+    be freed before the work on it has run."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def mm_route_topk(logits, k, normalize=1, indices=None, weights=None, stream=None):
     """Top-k routing of logits [T, G]: (indices int32 [T, k], weights fp32 [T, k]), the largest logits first, ties to
     the lowest index; weights are the softmax over all experts, divided by the picks' sum when ``normalize``."""
@@ -369,6 +378,7 @@ def mm_route_topk(logits, k, normalize=1, indices=None, weights=None, stream=Non
     w = torch.empty(shape, dtype=torch.float32, device=logits.device) if weights is None else weights
     _check(_lib().mm_route_topk(_ref(_desc(logits)), int(normalize), _ref(_desc(idx)), _ref(_desc(w)),
                                 _stream(logits, stream)), "mm_route_topk")
+    _used_on(stream, idx, w)
     return idx, w
 
 
@@ -377,6 +387,7 @@ def mm_route_topk_grad(logits, indices, grad_weights, normalize=1, out=None, str
     y = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if out is None else out
     _check(_lib().mm_route_topk_grad(_ref(_desc(logits)), _ref(_desc(indices)), _ref(_desc(grad_weights)),
                                      int(normalize), _ref(_desc(y)), _stream(logits, stream)), "mm_route_topk_grad")
+    _used_on(stream, y)
     return y
 
 
@@ -415,6 +426,7 @@ def mm_moe_layer(x, w_gate, w_up, w_down, expert_indices, expert_weights=None, a
     _check(lib.mm_moe_layer(*[_ref(t) for t in d], _ref(_desc(expert_weights)), _ACTIVATIONS[activation],
                             _ref(_desc(y)), None if ws is None else ws.data_ptr(), wsb, _stream(x, stream)),
            "mm_moe_layer")
+    _used_on(stream, y, ws)
     return y
 
 
@@ -432,6 +444,7 @@ def mm_lowrank_matmul(X, W, A, B, adapter_indices, scales=None, out=None, stream
     _check(lib.mm_lowrank_matmul(*[_ref(t) for t in d], _ref(_desc(adapter_indices)), _ref(_desc(scales)),
                                  _ref(_desc(y)), None if ws is None else ws.data_ptr(), wsb, _stream(X, stream)),
            "mm_lowrank_matmul")
+    _used_on(stream, y, ws)
     return y
 
 
@@ -453,6 +466,7 @@ def mm_lowrank_matmul_grad(dY, X, W, A, B, adapter_indices, scales=None, need=(T
                                       _ref(_desc(scales)), _ref(_desc(dX)), _ref(_desc(dA)), _ref(_desc(dB)),
                                       None if ws is None else ws.data_ptr(), wsb, _stream(X, stream)),
            "mm_lowrank_matmul_grad")
+    _used_on(stream, dX, dA, dB, ws)
     return dX, dA, dB
 
 

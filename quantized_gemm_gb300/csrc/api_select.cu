@@ -288,7 +288,10 @@ mm_status add_projection(GemmArgs g, cudaStream_t st) {
   // Every kernel of the dense product reads an element of C in the thread
   // that then writes that element of Y (or before its tile's store).
   g.c = g.y;
-  return run_dense(g, tensor_pays_dense(g.dtype, g.M, g.N, g.K, 1), st);
+  // A long sum over k leaves the CUDA-core tiles waiting even where the work is
+  // small: 4 rows of 512 x 512 take 17 us there and 8 us on the tensor cores.
+  const bool long_k = g.dtype != MM_F32 && g.K >= 256;
+  return run_dense(g, long_k || tensor_pays_dense(g.dtype, g.M, g.N, g.K, 1), st);
 }
 
 // Whether a 16-bit product may take the fused kernel (the dense products' rules).

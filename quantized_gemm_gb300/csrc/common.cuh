@@ -113,7 +113,11 @@ __device__ __forceinline__ int64_t load_index(const void* gi, int64_t off, int i
 // kernels and the large dense tensor-core products trigger right after their
 // wait; the operand preparation kernels and the few-row, QLinear and grouped
 // products do not, since the next kernel's blocks, resident early, measured
-// slower there.
+// slower there.  A kernel may put its wait off past reads of data that was
+// complete before the previous launch began (the expert layer's second
+// product, the projection beside adapters): that holds where the previous
+// launch triggers only after its own wait, or itself started under such a
+// launch.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_begin() {

@@ -503,6 +503,25 @@ def test_streams_graphs_and_repeats_give_the_same_bits(M):
         assert torch.equal(a, b)
 
 
+def test_memory_of_a_call_on_another_stream_is_not_reused_early():
+    """Outputs and workspaces belong to the current stream's pool; a call given another stream must keep them from it."""
+    moe = _moe_inputs(20, 6, 2, 256, 320, 256, BF16, 161)
+    *lr, dY = _lowrank_inputs(300, 1024, 520, 16, 4, BF16, 162)
+    want = [t.clone() for t in _all_ops(*moe, lr, dY)]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)                    # the calls' work waits here
+        got = _all_ops(*moe, lr, dY, stream=side)
+        # whatever the calls let go of is written over on the current stream
+        junk = [torch.full((1 << n,), 0xFF, dtype=torch.uint8, device=DEV) for n in range(9, 27) for _ in range(2)]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+        del junk
+
+
 def test_given_workspace_and_outputs():
     x, wg, wu, wd, idx, w = _moe_inputs(5, 4, 2, 128, 128, 128, BF16, 151)
     n = qg.mm_moe_layer_workspace_size(x, wg, wu, wd, idx)
