@@ -326,9 +326,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!DOWN) pdl_begin();
   else pdl_trigger();       // the next launch waits for this one before it touches anything
 
+  // Places past the picked experts are read too, and not used: one latency.
   const uint32_t picked = (uint32_t)__ldcg(p.tb.head);
-  for (uint32_t i = threadIdx.x; i < picked; i += kThreads) t_expert[i] = __ldcg(p.tb.expert + i);
-  for (uint32_t i = threadIdx.x; i <= picked; i += kThreads) t_offset[i] = __ldcg(p.tb.offset + i);
+  for (int i = threadIdx.x; i < p.max_picked; i += kThreads) t_expert[i] = __ldcg(p.tb.expert + i);
+  for (int i = threadIdx.x; i <= p.max_picked; i += kThreads) t_offset[i] = __ldcg(p.tb.offset + i);
   __syncthreads();
   auto seg_rows = [&](uint32_t a) { return t_offset[a + 1] - t_offset[a]; };
   Share sh;
