@@ -227,7 +227,7 @@ mm_status plan_lowrank(const mm_tensor* X, const mm_tensor* W, const mm_tensor* 
 // One factor's z [M, R] (or its shares, for few rows).
 size_t factor_bytes(const LowRankArgs& l) {
   const size_t z = (size_t)l.M * (size_t)l.R * sizeof(float);
-  return align256(l.M <= kFewRows && l.dtype != MM_F32 ? lowrank_few_bytes(l) : z);
+  return align256(lowrank_few_rows(l.M, l.G) && l.dtype != MM_F32 ? lowrank_few_bytes(l) : z);
 }
 
 // Workspace of the many-row gradient kernels.

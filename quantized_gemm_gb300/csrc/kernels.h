@@ -121,7 +121,14 @@ mm_status launch_lowrank_outer(const LowRankArgs& l, const void* x, int64_t x_rs
                                cudaStream_t stream);
 
 // Few rows of 16-bit types: both steps with vector reads, z's shares in zp.
-constexpr int64_t kFewRows = 256;
+// The host does not know whether rows of one adapter are neighbours.  Where
+// they are, the many-row kernels (lowrank_tc.cu) win from 128 (wide products)
+// to 512 rows on; where every row names another adapter, they take one pass
+// per adapter and lose: 512 rows of 4096 x 4096, rank 16, 16 adapters: runs of
+// 64 rows 46 against 48 us here, rows in random order 226 against 48 us.  More
+// than kFewAdapters adapters make up to kManyRows rows count as few.
+constexpr int64_t kFewRows = 256, kManyRows = 512, kFewAdapters = 8;
+inline bool lowrank_few_rows(int64_t M, int64_t G) { return M <= (G > kFewAdapters ? kManyRows : kFewRows); }
 struct LowRankFew {
   const void* x; int64_t x_rs, x_cs, C;
   const void* a; int64_t a_gs, a_cs, a_rs;     // [G, C, R]

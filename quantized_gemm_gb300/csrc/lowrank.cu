@@ -89,7 +89,14 @@ __global__ void __launch_bounds__(256)
 // so that one row's adapter streams through kSplit SMs; a share's sums stay
 // apart in zp[share][m][r] and the expansion adds them in share order.
 // Rows of one adapter read it from L2 again, which costs less than sorting
-// rows while there are few of them (kFewRows).
+// rows while there are few of them (lowrank_few_rows).  (Reading an adapter
+// once for four neighbouring rows was slower below 512 rows, and above for
+// rows of different adapters.)
+//
+// 61 rows of 4096 x 14336, rank 32, 48 adapters: 43 us for the three launches,
+// 159 MB (3.7 TB/s): shrink about 10, the expansion 10 under the projection's
+// 29.  One row of 4096 x 4096, rank 16: 11 us (3.0 TB/s), most of it the three
+// launches' latency.
 
 constexpr int kSplit = 8;
 constexpr int kFewThreads = 128;
@@ -376,7 +383,7 @@ mm_status few_typed(const LowRankArgs& l, const LowRankFew& f, float* zp, cudaSt
 // end by no one: C and N are multiples of 8).
 bool lowrank_few_supported(const LowRankArgs& l, const LowRankFew& f) {
   if (l.dtype != MM_BF16 && l.dtype != MM_F16) return false;
-  if (l.M < 1 || l.M > kFewRows || l.R < 1 || l.R > kExpandMaxR || l.G < 1 || f.C < 1 || f.N < 1) return false;
+  if (l.M < 1 || !lowrank_few_rows(l.M, l.G) || l.R < 1 || l.R > kExpandMaxR || l.G < 1 || f.C < 1 || f.N < 1) return false;
   const bool a_r = f.a_rs == 1 && l.R % 8 == 0 && vec8(f.a, f.a_gs, f.a_cs);
   const bool a_c = f.a_rs != 1 && f.a_cs == 1 && f.C % 8 == 0 && vec8(f.a, f.a_gs, f.a_rs);
   const bool b_n = f.b_ns == 1 && f.N % 8 == 0 && vec8(f.b, f.b_gs, f.b_rs);

@@ -339,7 +339,8 @@ def _check_lowrank_grad(dY, X, W, A, B, idx, scales, **kw):
 
 LOWRANK = [(1, 256, 264, 16, 4, 0), (1, 1, 1, 1, 1, 0), (5, 200, 136, 8, 3, 0), (61, 512, 520, 32, 20, 0),
            (64, 264, 256, 12, 2, 1), (129, 256, 300, 5, 6, 1), (300, 512, 256, 16, 5, 1), (777, 128, 264, 64, 3, 1),
-           (515, 1024, 512, 16, 40, 0), (33, 77, 35, 3, 4, 0), (257, 1032, 648, 24, 300, 0), (600, 1024, 272, 128, 2, 1)]
+           (515, 1024, 512, 16, 40, 0), (33, 77, 35, 3, 4, 0), (257, 1032, 648, 24, 300, 0), (600, 1024, 272, 128, 2, 1),
+           (1030, 264, 520, 8, 300, 0), (530, 200, 200, 12, 9, 1)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
