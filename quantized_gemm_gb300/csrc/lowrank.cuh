@@ -40,10 +40,11 @@ struct FusedTables {
   int32_t* row_entry;    // [M] place in the row tile's list, -1: not in it
   int32_t* ext_count;    // [row tiles]
   int32_t* ext_slot;     // [row tiles][kExtPerTile]
+  int32_t* row_c;        // [M] the product adds what Y holds (written where head[1] is set)
 };
 struct FusedLayout {
   int64_t slots, zt_ld, f_ld, c_ld;
-  size_t z, zt, head, slot_of, adapter_of, bad, row_entry, ext_count, ext_slot, factors, copy, total;
+  size_t z, zt, head, slot_of, adapter_of, bad, row_entry, ext_count, ext_slot, row_c, factors, copy, total;
 };
 FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N);
 FusedTables lowrank_fused_tables(const FusedLayout& w, char* ws);

@@ -16,9 +16,10 @@
 // adapter.  The low-rank part then costs ceil(R / 64) k-blocks per adapter and
 // tile on top of K / 64, and Y is written once.  A zero times an infinity or
 // a NaN is not zero, so the adapters that the kernel reads are copies with
-// their non-finite values set to 0; what those values add to their own rows
-// comes last (lowrank_fix), with the rows of any adapter past
-// kExtPerTile of one tile or kSlots in all.
+// their non-finite values set to 0.  What those values add to their own rows,
+// and the whole low-rank part of the rows of any adapter past kExtPerTile of
+// one tile or kSlots in all, is written to Y before (lowrank_fix), rounded
+// once, and added by the product.
 //
 // 8192 x 4096 x 14336 with 12 adapters of rank 16 in runs: the product takes
 // 540 us (1.79 PFLOP/s; 40 to 50 adapters over its 32 row tiles of 64 k-blocks
@@ -702,8 +703,9 @@ __device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const 
   }
 }
 
-// What the fused product left out: Y[m] += z[m] b[g] for rows outside their
-// tile's list, and the terms of non-finite adapter values.  Usually nothing.
+// What the fused product's extra blocks leave out: Y[m] = z[m] b[g] for rows
+// outside their tile's list, or the terms of non-finite adapter values alone;
+// the product adds Y for these rows.  Usually nothing.
 constexpr int kFixColumns = 8, kFixRows = 152;   // its blocks: 256 columns at a time, rows in turn
 
 template <typename T>
@@ -720,21 +722,21 @@ __device__ void lowrank_fix(const LowRankArgs& l, const FusedTables& t, const Fi
   constexpr uint16_t kExp = std::is_same<T, __half>::value ? 0x7C00 : 0x7F80;
   for (int64_t m = bx / kFixColumns; m < l.M; m += kFixRows) {
     const int64_t g = load_index(l.idx, m * l.idx_s, l.ind64);
-    if (g < 0 || g >= l.G) continue;
-    const bool all = __ldcg(t.row_entry + m) < 0;
-    if (!all && !__ldcg(t.bad + __ldcg(t.slot_of + g))) continue;
+    const bool in = g >= 0 && g < l.G;
+    const bool all = in && __ldcg(t.row_entry + m) < 0;
+    const bool add = all || (in && __ldcg(t.bad + __ldcg(t.slot_of + g)));
+    if (bx % kFixColumns == 0 && threadIdx.x == 0) t.row_c[m] = add;
+    if (!add) continue;
     for (int64_t n = (int64_t)(bx % kFixColumns) * 256 + threadIdx.x; n < p.N; n += kFixColumns * 256) {
       const T* bn = p.b + g * p.b_gs + n * p.b_ns;
       float v = 0.f;
-      bool any = all;
 #pragma unroll 8
       for (int64_t r = 0; r < l.R; ++r) {
         const T q = bn[r * p.b_rs];
         const bool bad = (*reinterpret_cast<const uint16_t*>(&q) & kExp) == kExp;
         if (all || bad) v = __fmaf_rn(p.z[m * l.R + r], to_f32(q), v);
-        any |= bad;
       }
-      if (any) p.y[m * p.N + n] = from_f32<T>(to_f32(p.y[m * p.N + n]) + v);
+      p.y[m * p.N + n] = from_f32<T>(v);
     }
   }
 }
@@ -757,11 +759,11 @@ __global__ void __launch_bounds__(256, 3)
   }
 }
 
-// After those and the fused product: the fix (first blocks; 4 us, its launch,
-// when there is nothing to fix) and the chunks' sums (9 us).
+// After those, and before the fused product: the fix (first blocks; 4 us, its
+// launch, when there is nothing to fix) and the chunks' sums (9 us).
 template <typename T>
 __global__ void __launch_bounds__(256)
-    lowrank_last_kernel(const LowRankArgs l, const FusedTables f, const __grid_constant__ FixArgs<T> fix,
+    lowrank_sums_kernel(const LowRankArgs l, const FusedTables f, const __grid_constant__ FixArgs<T> fix,
                         const AdapterRows t, const __grid_constant__ OuterProblem<T> p0,
                         const __grid_constant__ OuterProblem<T> p1, const int sum_blocks) {
   pdl_begin();
@@ -863,6 +865,7 @@ FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N) {
   w.row_entry = take((size_t)l.M * 4);
   w.ext_count = take((size_t)tiles * 4);
   w.ext_slot = take((size_t)tiles * kExtPerTile * 4);
+  w.row_c = take((size_t)l.M * 4);
   w.factors = take((size_t)rows * kExtPerTile * (size_t)w.f_ld * 2);
   w.copy = take((size_t)w.slots * (size_t)l.R * (size_t)w.c_ld * 2);
   w.total = o;
@@ -883,6 +886,7 @@ FusedTables lowrank_fused_tables(const FusedLayout& w, char* ws) {
   t.row_entry = reinterpret_cast<int32_t*>(ws + w.row_entry);
   t.ext_count = reinterpret_cast<int32_t*>(ws + w.ext_count);
   t.ext_slot = reinterpret_cast<int32_t*>(ws + w.ext_slot);
+  t.row_c = reinterpret_cast<int32_t*>(ws + w.row_c);
   return t;
 }
 
@@ -902,6 +906,7 @@ mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const Adapte
     e.factors = u->ws + w.factors; e.factor_ld = w.f_ld;
     e.adapters = u->ws + w.copy; e.slots = w.slots; e.R = l.R; e.adapter_ld = w.c_ld;
     e.count = f.ext_count; e.slot = f.ext_slot;
+    e.head = f.head; e.row_c = f.row_c;
     const int64_t N = u->product.N, tiles = (l.M + e.tile_rows - 1) / e.tile_rows, pieces = (w.c_ld + 1023) / 1024;
     const int64_t blocks = tiles * kPlaceParts + w.slots * pieces;
     if (blocks > (1 << 30)) return MM_ERR_UNSUPPORTED;
@@ -936,14 +941,12 @@ mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const Adapte
   if (launch_pdl(lowrank_middle_kernel<T>, middle, dim3(256), problems ? (size_t)(kOutStages * kOutStage) : 0, stream, l, f,
                  place, rows, p[0], p[1], (int)blocks[0], zt_ld) != cudaSuccess)
     return MM_ERR_CUDA;
-  if (u) {
-    const mm_status s = launch_tc_lowrank(u->product, e, l.status, stream);
-    if (s != MM_OK) return s;
-  }
   const int64_t per = (most * l.R + 1023) / 1024, sum_blocks = per < 64 ? per : 64;
   const int64_t last = fix.blocks + problems * l.G * sum_blocks;
-  return launch_pdl(lowrank_last_kernel<T>, dim3((unsigned)last), dim3(256), 0, stream, l, f, fix, rows, p[0], p[1],
-                    (int)(sum_blocks > 0 ? sum_blocks : 1)) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+  if (launch_pdl(lowrank_sums_kernel<T>, dim3((unsigned)last), dim3(256), 0, stream, l, f, fix, rows, p[0], p[1],
+                 (int)(sum_blocks > 0 ? sum_blocks : 1)) != cudaSuccess)
+    return MM_ERR_CUDA;
+  return u ? launch_tc_lowrank(u->product, e, l.status, stream) : MM_OK;
 }
 
 }  // namespace

@@ -33,6 +33,8 @@ struct LowRankExt {
   int64_t slots, R, adapter_ld;
   const int32_t* count;
   const int32_t* slot;
+  const int32_t* head;           // [1]: whether any row's Y holds a part to add
+  const int32_t* row_c;          // [M] (read when it does): rows whose Y does
 };
 int tc_lowrank_tile_rows(const GemmArgs& g);
 mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* status, cudaStream_t stream);

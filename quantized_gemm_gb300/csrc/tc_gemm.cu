@@ -913,6 +913,7 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
     qmin = p.y_signed ? -128.f : 0.f;
     qmax = p.y_signed ? 127.f : 255.f;
   }
+  const bool ext_c = MODE == kLowRank && __ldcg(p.ext_head + 1) != 0;
   int gh = 0;
   for (int64_t t = first_tile<MODE, PAIR>(p); get_tile<MODE, PAIR>(p, t, total, ti, gh); t += tile_step<MODE, PAIR>(p)) {
     const int rows_cta = PAIR ? max(0, min(BM, ti.rows - (int)row_off)) : ti.rows;
@@ -1050,7 +1051,9 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
       } else {
         const int64_t m = ti.m0 + roff + rl;
         yrow = static_cast<uint16_t*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + m * p.y_rs;
-        if (p.c && rok)
+        if (MODE == kLowRank) {
+          if (ext_c && rok && __ldcg(p.ext_row_c + m)) crow = yrow;
+        } else if (p.c && rok)
           crow = static_cast<const uint16_t*>(p.c) + batch_off(p, p.c_bstride, ti.batch) + m * p.c_rs;
       }
       if constexpr (MODE == kDense || MODE == kSkinny) {
@@ -1886,6 +1889,11 @@ mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* st
   p.idesc_ext = make_idesc(p.out_f16, 0, 1, pair);
   p.ext_count = e.count;
   p.ext_slot = e.slot;
+  p.ext_head = e.head;
+  p.ext_row_c = e.row_c;
+  p.beta = 1.f;
+  p.c_cs = 1;
+  p.c_vec = p.y_vec;
   p.ext_kb = (int)((e.R + BK - 1) / BK);
   return launch_tc(kLowRank, pair, a, b, p, stream, &z, &w);
 }

@@ -86,6 +86,9 @@ struct TcParams {
   const int32_t* ext_count;
   const int32_t* ext_slot;
   int ext_kb;
+  // Where ext_head[1] is set, rows m with ext_row_c[m] add what Y holds.
+  const int32_t* ext_head;
+  const int32_t* ext_row_c;
   uint32_t idesc_ext;
   // kGroupedQ: weights are int8 (w_signed) or uint8, or with w4 int4
   // (w_signed) or uint4 packed two per byte (the even column in the low

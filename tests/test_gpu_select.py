@@ -420,6 +420,19 @@ def test_lowrank_index_out_of_range(M):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_lowrank_rows_past_their_tile_list_are_rounded_once(dtype):
+    """Rows of more adapters than a row tile lists: the projection's sum is not rounded before the low-rank part joins it."""
+    X, W, A, B, idx, scales, _ = _lowrank_inputs(700, 48, 520, 1, 71, dtype, 105)
+    args = [to_np(t) for t in (X, W, A, B, idx, scales)]
+    want = select.lowrank_matmul(*args)
+    base, zero = np.abs(args[0]) @ np.abs(args[1]), np.zeros_like(args[1])
+    low = select.lowrank_matmul(np.abs(args[0]), zero, np.abs(args[2]), np.abs(args[3]), args[4], args[5])
+    u = U[dtype]                     # Y's rounding, and one or two of the low-rank part
+    assert_within(qg.mm_lowrank_matmul(X, W, A, B, idx, scales), want,
+                  u * np.abs(want) + 2.01 * u * low + 2 * 48 * U[F32] * (base + low) + 2.0 ** -24)
+
+
 def test_lowrank_empty_dimensions():
     X, W, A, B, idx, scales, dY = _lowrank_inputs(6, 64, 72, 8, 3, BF16, 111)
     assert qg.mm_lowrank_matmul(X[:0], W, A, B, idx[:0], scales).shape == (0, 72)
