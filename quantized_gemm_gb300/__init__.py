@@ -362,32 +362,45 @@ def mm_grouped_matmul_noalloc(input, weights, group_indices, bias=None, out=None
 
 
 def _used_on(stream, *tensors):
-    """Tells torch's allocator that ``stream`` (None: the current one, whose memory it is) uses the tensors, which may
-    be freed before the work on it has run."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    """Tells torch's allocator that ``stream`` uses the tensors, which come from the current stream's memory and may be
+    freed before the work on ``stream`` has run."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
+# The calls below take a few microseconds on the device for small sizes, as
+# long as their marshalling: it is written out, without lists or helpers on
+# the way of a call that passes its workspace.
 
 
 def mm_route_topk(logits, k, normalize=1, indices=None, weights=None, stream=None):
     """Top-k routing of logits [T, G]: (indices int32 [T, k], weights fp32 [T, k]), the largest logits first, ties to
     the lowest index; weights are the softmax over all experts, divided by the picks' sum when ``normalize``."""
-    shape = (logits.shape[0], int(k))
-    idx = torch.empty(shape, dtype=torch.int32, device=logits.device) if indices is None else indices
-    w = torch.empty(shape, dtype=torch.float32, device=logits.device) if weights is None else weights
-    _check(_lib().mm_route_topk(_ref(_desc(logits)), int(normalize), _ref(_desc(idx)), _ref(_desc(w)),
-                                _stream(logits, stream)), "mm_route_topk")
-    _used_on(stream, idx, w)
-    return idx, w
+    lib = _LIB or _lib()
+    if indices is None:
+        indices = torch.empty((logits.shape[0], k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((logits.shape[0], k), dtype=torch.float32, device=logits.device)
+    status = lib.mm_route_topk(_ref(_desc(logits)), int(normalize), _ref(_desc(indices)), _ref(_desc(weights)),
+                               _stream(logits, stream))
+    if status:
+        raise MMError(status, "mm_route_topk")
+    if stream is not None:
+        _used_on(stream, indices, weights)
+    return indices, weights
 
 
 def mm_route_topk_grad(logits, indices, grad_weights, normalize=1, out=None, stream=None):
     """Gradient of mm_route_topk's weights with respect to the logits (in the logits' type)."""
+    lib = _LIB or _lib()
     y = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if out is None else out
-    _check(_lib().mm_route_topk_grad(_ref(_desc(logits)), _ref(_desc(indices)), _ref(_desc(grad_weights)),
-                                     int(normalize), _ref(_desc(y)), _stream(logits, stream)), "mm_route_topk_grad")
-    _used_on(stream, y)
+    status = lib.mm_route_topk_grad(_ref(_desc(logits)), _ref(_desc(indices)), _ref(_desc(grad_weights)),
+                                    int(normalize), _ref(_desc(y)), _stream(logits, stream))
+    if status:
+        raise MMError(status, "mm_route_topk_grad")
+    if stream is not None:
+        _used_on(stream, y)
     return y
 
 
@@ -417,16 +430,20 @@ def mm_moe_layer(x, w_gate, w_up, w_down, expert_indices, expert_weights=None, a
     """The mixture-of-experts layer for a few tokens: out[t] = sum_s expert_weights[t, s] * (act(x[t] @ w_gate[e]) *
     (x[t] @ w_up[e])) @ w_down[e], e = expert_indices[t, s] (-1: no pick).  ``activation`` is 'silu', 'gelu' or
     'relu'; w_up None leaves the second factor out."""
-    if activation not in _ACTIVATIONS:
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError("activation must be one of %s" % ", ".join(sorted(_ACTIVATIONS)))
-    lib = _lib()
-    d = [_desc(t) for t in (x, w_gate, w_up, w_down, expert_indices)]
+    lib = _LIB or _lib()
+    dx, dg, du, dd, di = _desc(x), _desc(w_gate), _desc(w_up), _desc(w_down), _desc(expert_indices)
     y = torch.empty((x.shape[0], w_down.shape[2]), dtype=x.dtype, device=x.device) if out is None else out
-    ws, wsb = _given_or_sized(workspace, x.device, lib.mm_moe_layer_workspace_size, *d)
-    _check(lib.mm_moe_layer(*[_ref(t) for t in d], _ref(_desc(expert_weights)), _ACTIVATIONS[activation],
-                            _ref(_desc(y)), None if ws is None else ws.data_ptr(), wsb, _stream(x, stream)),
-           "mm_moe_layer")
-    _used_on(stream, y, ws)
+    ws, wsb = _given_or_sized(workspace, x.device, lib.mm_moe_layer_workspace_size, dx, dg, du, dd, di)
+    status = lib.mm_moe_layer(_ref(dx), _ref(dg), _ref(du), _ref(dd), _ref(di),
+                              _ref(_desc(expert_weights)), act, _ref(_desc(y)),
+                              None if ws is None else ws.data_ptr(), wsb, _stream(x, stream))
+    if status:
+        raise MMError(status, "mm_moe_layer")
+    if stream is not None:
+        _used_on(stream, y, ws)
     return y
 
 
@@ -437,14 +454,17 @@ def mm_lowrank_matmul_workspace_size(X, W, A, B):
 def mm_lowrank_matmul(X, W, A, B, adapter_indices, scales=None, out=None, stream=None, workspace=None):
     """X @ W plus each row's low-rank adapter: Y[m] = X[m] @ W + scales[g] * (X[m] @ A[g]) @ B[g],
     g = adapter_indices[m] (-1: no adapter)."""
-    lib = _lib()
-    d = [_desc(t) for t in (X, W, A, B)]
+    lib = _LIB or _lib()
+    dX, dW, dA, dB = _desc(X), _desc(W), _desc(A), _desc(B)
     y = torch.empty((X.shape[0], W.shape[1]), dtype=X.dtype, device=X.device) if out is None else out
-    ws, wsb = _given_or_sized(workspace, X.device, lib.mm_lowrank_matmul_workspace_size, *d)
-    _check(lib.mm_lowrank_matmul(*[_ref(t) for t in d], _ref(_desc(adapter_indices)), _ref(_desc(scales)),
-                                 _ref(_desc(y)), None if ws is None else ws.data_ptr(), wsb, _stream(X, stream)),
-           "mm_lowrank_matmul")
-    _used_on(stream, y, ws)
+    ws, wsb = _given_or_sized(workspace, X.device, lib.mm_lowrank_matmul_workspace_size, dX, dW, dA, dB)
+    status = lib.mm_lowrank_matmul(_ref(dX), _ref(dW), _ref(dA), _ref(dB), _ref(_desc(adapter_indices)),
+                                   _ref(_desc(scales)), _ref(_desc(y)),
+                                   None if ws is None else ws.data_ptr(), wsb, _stream(X, stream))
+    if status:
+        raise MMError(status, "mm_lowrank_matmul")
+    if stream is not None:
+        _used_on(stream, y, ws)
     return y
 
 
@@ -456,17 +476,19 @@ def mm_lowrank_matmul_grad(dY, X, W, A, B, adapter_indices, scales=None, need=(T
                            workspace=None):
     """Gradients (dX, dA, dB) of mm_lowrank_matmul for a frozen W; ``need`` says which are wanted (None in the
     others' place)."""
-    lib = _lib()
+    lib = _LIB or _lib()
     d = [_desc(t) for t in (X, W, A, B)]
     dX = torch.empty(X.shape, dtype=X.dtype, device=X.device) if need[0] else None
     dA = torch.empty(A.shape, dtype=A.dtype, device=X.device) if need[1] else None
     dB = torch.empty(B.shape, dtype=B.dtype, device=X.device) if need[2] else None
     ws, wsb = _given_or_sized(workspace, X.device, lib.mm_lowrank_matmul_grad_workspace_size, *d)
-    _check(lib.mm_lowrank_matmul_grad(_ref(_desc(dY)), *[_ref(t) for t in d], _ref(_desc(adapter_indices)),
-                                      _ref(_desc(scales)), _ref(_desc(dX)), _ref(_desc(dA)), _ref(_desc(dB)),
-                                      None if ws is None else ws.data_ptr(), wsb, _stream(X, stream)),
-           "mm_lowrank_matmul_grad")
-    _used_on(stream, dX, dA, dB, ws)
+    status = lib.mm_lowrank_matmul_grad(_ref(_desc(dY)), *[_ref(t) for t in d], _ref(_desc(adapter_indices)),
+                                        _ref(_desc(scales)), _ref(_desc(dX)), _ref(_desc(dA)), _ref(_desc(dB)),
+                                        None if ws is None else ws.data_ptr(), wsb, _stream(X, stream))
+    if status:
+        raise MMError(status, "mm_lowrank_matmul_grad")
+    if stream is not None:
+        _used_on(stream, dX, dA, dB, ws)
     return dX, dA, dB
 
 
