@@ -121,14 +121,24 @@ mm_status launch_lowrank_outer(const LowRankArgs& l, const void* x, int64_t x_rs
                                cudaStream_t stream);
 
 // Few rows of 16-bit types: both steps with vector reads, z's shares in zp.
-// The host does not know whether rows of one adapter are neighbours.  Where
-// they are, the many-row kernels (lowrank_tc.cu) win from 128 (wide products)
-// to 512 rows on; where every row names another adapter, they take one pass
-// per adapter and lose: 512 rows of 4096 x 4096, rank 16, 16 adapters: runs of
-// 64 rows 46 against 48 us here, rows in random order 226 against 48 us.  More
-// than kFewAdapters adapters make up to kManyRows rows count as few.
-constexpr int64_t kFewRows = 256, kManyRows = 512, kFewAdapters = 8;
-inline bool lowrank_few_rows(int64_t M, int64_t G) { return M <= (G > kFewAdapters ? kManyRows : kFewRows); }
+// The host does not know whether rows of one adapter are neighbours, nor how
+// many of the G adapters are in use.  The many-row kernels (lowrank_tc.cu) make
+// one pass per adapter and row tile; these read each row's own adapter and do
+// not care.  us for rows in random order and in runs, N = K = 4096, rank 16:
+//      M     G    many-row         here
+//    256     8    48   47         42   42
+//    512     8    49   46         52   52
+//    512    32    76   54         52   52
+//   1024    16    73   48         73   73
+//   1024    64   124   57         74   75
+//   2048   128   267   91        142  147
+//   4096   256   566  254        314  310
+//  16384  1000  1996 1041       1304 1248
+// so these take up to kFewPerAdapter rows per adapter, or kFewRows in all.
+constexpr int64_t kFewRows = 256, kFewPerAdapter = 16, kFewMost = 16384;
+inline bool lowrank_few_rows(int64_t M, int64_t G) {
+  return M <= kFewRows || (M <= kFewMost && (M + kFewPerAdapter - 1) / kFewPerAdapter <= G);
+}
 struct LowRankFew {
   const void* x; int64_t x_rs, x_cs, C;
   const void* a; int64_t a_gs, a_cs, a_rs;     // [G, C, R]

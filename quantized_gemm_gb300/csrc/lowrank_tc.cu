@@ -17,9 +17,9 @@
 // tile on top of K / 64, and Y is written once.  A zero times an infinity or
 // a NaN is not zero, so the adapters that the kernel reads are copies with
 // their non-finite values set to 0.  What those values add to their own rows,
-// and the whole low-rank part of the rows of any adapter past kExtPerTile of
-// one tile or kSlots in all, is written to Y before (lowrank_fix), rounded
-// once, and added by the product.
+// and the whole low-rank part of the rows of any adapter past a tile's list
+// (per_tile) or past kSlots in all, is written to Y before (lowrank_fix),
+// rounded once, and added by the product.
 //
 // 8192 x 4096 x 14336 with 12 adapters of rank 16 in runs: the product takes
 // 540 us (1.79 PFLOP/s; 40 to 50 adapters over its 32 row tiles of 64 k-blocks
@@ -127,6 +127,12 @@ __host__ __device__ constexpr int shrink_a_bytes(bool ck, int rc) {
   return ck ? (rc + 7) / 8 * 8 * kShKPitch : kShK * ((rc + 7) / 8 * 16 + 16);
 }
 constexpr int kShStages = 3;
+// The adapters of a tile's rows are dealt out to 2 to kShParts blocks, so that
+// about kShBlocks start: rows in random order name up to 32 adapters a tile,
+// and blocks past the tile's adapters end at once.  1024 rows of 4096 x 4096,
+// rank 16, 32 adapters, the whole call: random order 89 us against 300 with
+// one block a tile, runs 50 against 69 us.
+constexpr int kShParts = 16, kShBlocks = 608;
 __host__ __device__ constexpr int shrink_red_pitch(int rc) { return (rc + 7) / 8 * 8 + 4; }
 // [x rings][control][adapter rings][sums]
 __host__ __device__ constexpr int shrink_smem(bool ck, int rc) {
@@ -146,7 +152,8 @@ struct ShrinkArgs {
 
 // NT: 8-rank tiles that the accumulators hold.
 template <typename T, bool CK, int NT>
-__device__ void shrink_tile(const CUtensorMap* tmX, const LowRankArgs& l, const ShrinkArgs& p, int tile, uint8_t* sm_raw) {
+__device__ void shrink_tile(const CUtensorMap* tmX, const LowRankArgs& l, const ShrinkArgs& p, int tile, int part, int parts,
+                            uint8_t* sm_raw) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t m0 = (int64_t)tile * kShRows, C = p.C;
   const int r0 = blockIdx.y * 64, rc = (int)min((int64_t)64, l.R - r0), nt = (rc + 7) / 8;
@@ -181,7 +188,7 @@ __device__ void shrink_tile(const CUtensorMap* tmX, const LowRankArgs& l, const 
     else if (g != -1) atomicOr(l.status, kStatusIndexRange);
   }
   unsigned left = __ballot_sync(0xffffffffu, g_lane >= 0);
-  const unsigned none = ~left;
+  const unsigned none = part == 0 ? ~left : 0u;
   T* zt = static_cast<T*>(p.zt);
   for (int i = tid; i < rows * nt * 8; i += kShThreads) {   // rows without adapter
     const int r = i / (nt * 8), c = i - r * (nt * 8);
@@ -192,10 +199,11 @@ __device__ void shrink_tile(const CUtensorMap* tmX, const LowRankArgs& l, const 
   uint32_t done = 0, issued = 0;       // this warp's k-blocks over all passes: stage = count % stages
   uint32_t istage = 0, dstage = 0, dphase = 0;
   bool ok = true;
-  while (left && ok) {
+  for (int pass = 0; left && ok; ++pass) {
     const int g = __shfl_sync(0xffffffffu, g_lane, __ffs(left) - 1);
     const unsigned sel = __ballot_sync(0xffffffffu, g_lane == g);
     left &= ~sel;
+    if (pass % parts != part) continue;
     const T* ag = static_cast<const T*>(p.a) + (int64_t)g * p.a_gs;
     auto load = [&](int i) {
       const int64_t c0 = ((int64_t)i * kShWarps + warp) * kShK;
@@ -395,17 +403,19 @@ __global__ void __launch_bounds__(kShThreads, NT <= 4 ? 2 : 1)
     shrink_tiles_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
                         const LowRankArgs l, const __grid_constant__ ShrinkArgs p0,
                         const __grid_constant__ ShrinkArgs p1, const int tiles,
-                        const int problems, const FusedTables slots, const AdapterRows sort) {
+                        const int problems, const int parts, const FusedTables slots, const AdapterRows sort) {
   pdl_begin();
   extern __shared__ __align__(16) uint8_t sm[];
-  const int tile = (int)blockIdx.x - ((int)gridDim.x - tiles * problems);
+  int tile = (int)blockIdx.x - ((int)gridDim.x - tiles * problems * parts);
   if (tile >= 0) {
+    const int part = tile / (tiles * problems);
+    tile -= part * tiles * problems;
     const bool second = tile >= tiles;
     const ShrinkArgs& p = second ? p1 : p0;
     const CUtensorMap* tm = second ? &tm1 : &tm0;
     const int t = second ? tile - tiles : tile;
-    if (p.ck) shrink_tile<T, true, NT>(tm, l, p, t, sm);
-    else shrink_tile<T, false, NT>(tm, l, p, t, sm);
+    if (p.ck) shrink_tile<T, true, NT>(tm, l, p, t, part, parts, sm);
+    else shrink_tile<T, false, NT>(tm, l, p, t, part, parts, sm);
   } else if (blockIdx.y == 0) {
     const int b = (int)blockIdx.x - (slots.head ? 1 : 0);
     if (b < 0) adapter_slots(l, slots, sm);
@@ -566,14 +576,13 @@ __device__ void outer_sum(const LowRankArgs& l, const AdapterRows& t, const Oute
 
 // ------------------------------------------------------------------ the fused product's operands
 
-// Blocks [0, kPlaceParts * tiles): a row tile's adapters (the first
-// kExtPerTile in order of appearance) and a part of its blocks of factor rows.
-// The others: the adapters' copies, 1024 columns of one slot a block.
-constexpr int kPlaceParts = 4;
+// Blocks [0, parts * tiles): a row tile's adapters (the first per_tile, by
+// slot) and a part of its blocks of factor rows.  The others: the adapters'
+// copies, 1024 columns of one slot a block.
 template <typename T>
 struct PlaceArgs {
   int blocks;                    // 0: nothing to place
-  int tile_rows, tiles;
+  int tile_rows, tiles, per_tile, parts;
   const T* zt; int64_t zt_ld;
   T* factors; int64_t f_ld;
   const T* b; int64_t b_gs, b_rs, b_ns, N;
@@ -583,15 +592,15 @@ struct PlaceArgs {
 
 template <typename T>
 __device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const PlaceArgs<T>& p, const int bx) {
-  const int tile_rows = p.tile_rows, tiles = p.tiles, pieces = p.pieces, vec = p.vec;
+  const int tile_rows = p.tile_rows, tiles = p.tiles, per_tile = p.per_tile, parts = p.parts, pieces = p.pieces, vec = p.vec;
   const T *zt = p.zt, *b = p.b;
   T *factors = p.factors, *copy = p.copy;
   const int64_t zt_ld = p.zt_ld, f_ld = p.f_ld, b_gs = p.b_gs, b_rs = p.b_rs, b_ns = p.b_ns, N = p.N, c_ld = p.c_ld;
   const int tid = threadIdx.x;
-  if (bx < tiles * kPlaceParts) {
-    __shared__ int first, list[kExtPerTile];
+  if (bx < tiles * parts) {
+    __shared__ uint32_t named[kSlots / 32];
     __shared__ signed char entry[256];
-    const int tile = bx / kPlaceParts, part = bx % kPlaceParts;
+    const int tile = bx / parts, part = bx % parts;
     const int64_t m = (int64_t)tile * tile_rows + tid;
     int slot = -1;
     bool has = false;
@@ -600,20 +609,25 @@ __device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const 
       has = g >= 0 && g < l.G;
       if (has) slot = __ldcg(t.slot_of + g);
     }
-    int mine = -1, n = 0;
-    for (; n < kExtPerTile; ++n) {
-      if (tid == 0) first = 256;
-      __syncthreads();
-      if (slot >= 0 && mine < 0) atomicMin(&first, tid);
-      __syncthreads();
-      const int f = first;
-      if (f == 256) break;
-      if (tid == f) list[n] = slot;
-      __syncthreads();
-      if (slot >= 0 && slot == list[n]) mine = n;
-    }
+    if (tid < kSlots / 32) named[tid] = 0u;
+    __syncthreads();
+    if (slot >= 0) atomicOr(named + (slot >> 5), 1u << (slot & 31));
+    __syncthreads();
+    // An adapter's place in the list: the named slots below its own.
+    auto place_of = [&](int s) {
+      int n = __popc(named[s >> 5] & ((1u << (s & 31)) - 1u));
+      for (int w = 0; w < s >> 5; ++w) n += __popc(named[w]);
+      return n;
+    };
+    int mine = slot >= 0 ? place_of(slot) : -1, n = 0;
+    if (mine >= per_tile) mine = -1;
+    for (int w = 0; w < kSlots / 32; ++w) n += __popc(named[w]);
+    n = min(n, per_tile);
     entry[tid] = (signed char)mine;
-    if (part == 0 && tid < n) t.ext_slot[tile * kExtPerTile + tid] = list[tid];
+    if (part == 0 && tid < kSlots && ((named[tid >> 5] >> (tid & 31)) & 1u)) {
+      const int at = place_of(tid);
+      if (at < per_tile) t.ext_slot[(int64_t)tile * per_tile + at] = tid;
+    }
     if (part == 0 && tid == 0) t.ext_count[tile] = n;
     if (part == 0 && tid < tile_rows && m < l.M) {
       t.row_entry[m] = mine;
@@ -622,11 +636,11 @@ __device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const 
     __syncthreads();
     const int pieces_row = (int)(f_ld / 8), total = n * tile_rows * pieces_row;
     constexpr int kAhead = 4;                             // reads in flight before the first write
-    for (int i0 = part * 256 + tid; i0 < total; i0 += 256 * kPlaceParts * kAhead) {
+    for (int i0 = part * 256 + tid; i0 < total; i0 += 256 * parts * kAhead) {
       uint4 v[kAhead];
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
-        const int i = i0 + q * 256 * kPlaceParts;
+        const int i = i0 + q * 256 * parts;
         const int row = i / pieces_row, c = (i - row * pieces_row) * 8;     // row of the tile's n blocks
         const int r = row % tile_rows, j = row / tile_rows;
         v[q] = make_uint4(0u, 0u, 0u, 0u);
@@ -635,14 +649,14 @@ __device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const 
       }
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
-        const int i = i0 + q * 256 * kPlaceParts;
+        const int i = i0 + q * 256 * parts;
         if (i < total)
-          *reinterpret_cast<uint4*>(factors + (int64_t)tile * kExtPerTile * tile_rows * f_ld + (int64_t)i * 8) = v[q];
+          *reinterpret_cast<uint4*>(factors + (int64_t)tile * per_tile * tile_rows * f_ld + (int64_t)i * 8) = v[q];
       }
     }
     return;
   }
-  const int rest = bx - tiles * kPlaceParts;
+  const int rest = bx - tiles * parts;
   const int piece = rest % pieces, slot = rest / pieces;
   if (slot >= __ldcg(t.head)) return;
   constexpr uint16_t kExp = std::is_same<T, __half>::value ? 0x7C00 : 0x7F80;
@@ -820,13 +834,16 @@ mm_status shrink_launch(const LowRankArgs& l, const LowRankShrink* q, int proble
   for (int need : {tables, bits})
     if (smem < need) smem = need;
   const int64_t tiles = (l.M + kShRows - 1) / kShRows;
-  const int64_t blocks = tiles * problems + (slots ? 1 : 0) + (sort ? l.G : 0);
+  const int64_t ranks = (l.R + 63) / 64;
+  int64_t parts = kShBlocks / (tiles * problems * ranks);
+  parts = parts < 2 ? 2 : parts > kShParts ? kShParts : parts;
+  const int64_t blocks = tiles * problems * parts + (slots ? 1 : 0) + (sort ? l.G : 0);
   if (blocks > 0x7fffffffLL) return MM_ERR_UNSUPPORTED;
   const auto kernel = rc <= 16 ? shrink_tiles_kernel<T, 2> : rc <= 32 ? shrink_tiles_kernel<T, 4> : shrink_tiles_kernel<T, 8>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024) != cudaSuccess)
     return MM_ERR_CUDA;
-  return launch_pdl(kernel, dim3((unsigned)blocks, (unsigned)((l.R + 63) / 64)), dim3(kShThreads), (size_t)smem, stream,
-                    map[0].map, map[1].map, l, p[0], p[1], (int)tiles, problems, slots ? *slots : FusedTables{},
+  return launch_pdl(kernel, dim3((unsigned)blocks, (unsigned)ranks), dim3(kShThreads), (size_t)smem, stream,
+                    map[0].map, map[1].map, l, p[0], p[1], (int)tiles, problems, (int)parts, slots ? *slots : FusedTables{},
                     sort ? *sort : AdapterRows{}) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
@@ -846,6 +863,20 @@ mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const LowRankShrink*
                            : shrink_launch<__nv_bfloat16>(l, p, problems, zt_ld, slots, sort, stream);
 }
 
+namespace {
+
+// Adapters that a row tile can list: all of them up to kExtPerTile, fewer
+// (16 at least) where the factors' blocks would take more than 256 MB.
+int64_t per_tile(const LowRankArgs& l) {
+  const int64_t bytes = (l.M + 255) / 256 * 256 * ((l.R + 63) / 64 * 64) * 2;
+  int64_t n = kExtPerTile;
+  while (n > 16 && n * bytes > (256ll << 20)) n /= 2;
+  const int64_t most = l.G < l.M ? l.G : l.M;
+  return n < most ? n : most;
+}
+
+}  // namespace
+
 FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N) {
   FusedLayout w;
   size_t o = 0;
@@ -855,6 +886,7 @@ FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N) {
   if (w.slots > kSlots) w.slots = kSlots;
   w.zt_ld = (l.R + 7) / 8 * 8;
   w.f_ld = (l.R + 63) / 64 * 64;
+  w.per_tile = per_tile(l);
   w.c_ld = (N + 7) / 8 * 8;
   w.z = take((size_t)l.M * (size_t)l.R * 4);
   w.zt = take((size_t)l.M * (size_t)w.zt_ld * 2);
@@ -864,9 +896,9 @@ FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N) {
   w.bad = take(kSlots * 4);
   w.row_entry = take((size_t)l.M * 4);
   w.ext_count = take((size_t)tiles * 4);
-  w.ext_slot = take((size_t)tiles * kExtPerTile * 4);
+  w.ext_slot = take((size_t)tiles * (size_t)w.per_tile * 4);
   w.row_c = take((size_t)l.M * 4);
-  w.factors = take((size_t)rows * kExtPerTile * (size_t)w.f_ld * 2);
+  w.factors = take((size_t)rows * (size_t)w.per_tile * (size_t)w.f_ld * 2);
   w.copy = take((size_t)w.slots * (size_t)l.R * (size_t)w.c_ld * 2);
   w.total = o;
   return w;
@@ -874,7 +906,7 @@ FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N) {
 
 bool lowrank_fused_supported(const LowRankArgs& l, const GemmArgs& g) {
   return (l.dtype == MM_BF16 || l.dtype == MM_F16) && l.M >= 1 && l.R >= 1 && l.R <= 4096 && l.G >= 1 && l.G <= 65536 &&
-         l.M * kExtPerTile < (1ll << 30) && tc_lowrank_tile_rows(g) != 0;
+         l.M * per_tile(l) < (1ll << 30) && tc_lowrank_tile_rows(g) != 0;
 }
 
 FusedTables lowrank_fused_tables(const FusedLayout& w, char* ws) {
@@ -903,17 +935,19 @@ mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const Adapte
     const FusedLayout& w = *u->layout;
     f = lowrank_fused_tables(w, u->ws);
     e.tile_rows = tc_lowrank_tile_rows(u->product);
-    e.factors = u->ws + w.factors; e.factor_ld = w.f_ld;
+    e.factors = u->ws + w.factors; e.factor_ld = w.f_ld; e.per_tile = w.per_tile;
     e.adapters = u->ws + w.copy; e.slots = w.slots; e.R = l.R; e.adapter_ld = w.c_ld;
     e.count = f.ext_count; e.slot = f.ext_slot;
     e.head = f.head; e.row_c = f.row_c;
     const int64_t N = u->product.N, tiles = (l.M + e.tile_rows - 1) / e.tile_rows, pieces = (w.c_ld + 1023) / 1024;
-    const int64_t blocks = tiles * kPlaceParts + w.slots * pieces;
+    int64_t parts = 152 / tiles;      // blocks that write one tile's factors: about one per SM in all
+    parts = parts < 4 ? 4 : parts > 32 ? 32 : parts;
+    const int64_t blocks = tiles * parts + w.slots * pieces;
     if (blocks > (1 << 30)) return MM_ERR_UNSUPPORTED;
     // 16-byte reads of b along n (1) or along the ranks (2)
     const bool base = (l.G == 1 || u->b_gs % 8 == 0) && reinterpret_cast<uintptr_t>(u->b) % 16 == 0;
     place.blocks = (int)blocks;
-    place.tile_rows = e.tile_rows; place.tiles = (int)tiles;
+    place.tile_rows = e.tile_rows; place.tiles = (int)tiles; place.per_tile = (int)w.per_tile; place.parts = (int)parts;
     place.zt = static_cast<const T*>(u->zt); place.zt_ld = w.zt_ld;
     place.factors = reinterpret_cast<T*>(u->ws + w.factors); place.f_ld = w.f_ld;
     place.b = static_cast<const T*>(u->b);

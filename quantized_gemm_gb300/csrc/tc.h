@@ -27,8 +27,8 @@ mm_status launch_tc_grouped(const GroupedArgs& g, void* workspace, unsigned* sta
 // factors with their adapters (device tables as TcParams describes them).
 struct LowRankExt {
   int tile_rows;                 // tc_lowrank_tile_rows
-  const void* factors;           // [row tiles * kExtPerTile * tile_rows, factor_ld], factor_ld a multiple of 64
-  int64_t factor_ld;
+  const void* factors;           // [row tiles * per_tile * tile_rows, factor_ld], factor_ld a multiple of 64
+  int64_t factor_ld, per_tile;   // per_tile: adapters that a tile can list
   const void* adapters;          // [slots, R, adapter_ld], finite, adapter_ld a multiple of 8
   int64_t slots, R, adapter_ld;
   const int32_t* count;

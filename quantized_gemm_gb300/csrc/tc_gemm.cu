@@ -337,7 +337,7 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
         qpend_parity = (qpend_parity & ~(1u << qstage)) | (qphase << qstage);
         if (++qstage == kQStages) { qstage = 0; qphase ^= 1; }
       } else if (MODE == kLowRank && kb >= kb_e) {
-        const int32_t ent = (int32_t)(ti.m0 / G::kTileRows) * kExtPerTile + (kb - kb_e) / p.ext_kb;
+        const int32_t ent = (int32_t)(ti.m0 / G::kTileRows) * p.ext_per_tile + (kb - kb_e) / p.ext_kb;
         const int32_t r0 = (kb - kb_e) % p.ext_kb * BK, slot = __ldcg(p.ext_slot + ent);
         const int32_t zr = ent * G::kTileRows + arow_off;
         if (PAIR) {
@@ -1876,7 +1876,7 @@ mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* st
   BatchMap one = g.bm;
   const int64_t none[kMaxBatchDims] = {};
   const int64_t tiles = (g.M + e.tile_rows - 1) / e.tile_rows;
-  if (!plan_operand(e.factors, g.dtype, tiles * kExtPerTile * e.tile_rows, e.factor_ld, e.factor_ld, 1, one, none, BM, &z) ||
+  if (!plan_operand(e.factors, g.dtype, tiles * e.per_tile * e.tile_rows, e.factor_ld, e.factor_ld, 1, one, none, BM, &z) ||
       z.mn_major)
     return MM_ERR_UNSUPPORTED;
   BatchMap slots = g.bm;
@@ -1888,6 +1888,7 @@ mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* st
   p.idesc = make_idesc(p.out_f16, a.mn_major, b.mn_major, pair);
   p.idesc_ext = make_idesc(p.out_f16, 0, 1, pair);
   p.ext_count = e.count;
+  p.ext_per_tile = (int)e.per_tile;
   p.ext_slot = e.slot;
   p.ext_head = e.head;
   p.ext_row_c = e.row_c;

@@ -26,7 +26,6 @@ constexpr int kTileK = 64;    // one 128-byte swizzle row of 16-bit elements
 // with k-blocks of other operands (the rows' low-rank factors times their
 // adapters), accumulated on top.
 enum TcMode { kDense = 0, kGrouped = 1, kQLinear = 2, kGroupedQ = 3, kTF32 = 4, kSkinny = 5, kLowRank = 6 };
-constexpr int kExtPerTile = 16;   // kLowRank: adapters per row tile
 
 struct TcParams {
   int64_t M, N, K;
@@ -80,12 +79,12 @@ struct TcParams {
   const int32_t* g_rowlist;
   int G;
   // kLowRank: row tile i goes on with ext_count[i] adapters, the j-th
-  // (ext_slot[i * kExtPerTile + j]) in ext_kb k-blocks: the tile's rows of the
-  // factor matrix (rows (i * kExtPerTile + j) * tile rows .., K-major) times
+  // (ext_slot[i * ext_per_tile + j]) in ext_kb k-blocks: the tile's rows of the
+  // factor matrix (rows (i * ext_per_tile + j) * tile rows .., K-major) times
   // the staged adapter (MN-major).
   const int32_t* ext_count;
   const int32_t* ext_slot;
-  int ext_kb;
+  int ext_kb, ext_per_tile;
   // Where ext_head[1] is set, rows m with ext_row_c[m] add what Y holds.
   const int32_t* ext_head;
   const int32_t* ext_row_c;

@@ -433,6 +433,18 @@ def test_lowrank_rows_past_their_tile_list_are_rounded_once(dtype):
                   u * np.abs(want) + 2.01 * u * low + 2 * 48 * U[F32] * (base + low) + 2.0 ** -24)
 
 
+# Rows in random order name most adapters in every row tile: more than a warp
+# of them, more than the product holds copies of, and (ranks this large) more
+# than a tile lists.
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("M,K,N,R,G", [(1040, 264, 520, 24, 40), (2100, 256, 264, 16, 131), (2600, 136, 272, 72, 160),
+                                       (1100, 64, 264, 2048, 68), (1200, 256, 264, 16, 80)])
+def test_lowrank_many_adapters_in_every_tile(M, K, N, R, G, dtype):
+    X, W, A, B, idx, scales, dY = _lowrank_inputs(M, K, N, R, G, dtype, M + G)
+    _check_lowrank(X, W, A, B, idx, scales)
+    _check_lowrank_grad(dY, X, W, A, B, idx, scales)
+
+
 def test_lowrank_empty_dimensions():
     X, W, A, B, idx, scales, dY = _lowrank_inputs(6, 64, 72, 8, 3, BF16, 111)
     assert qg.mm_lowrank_matmul(X[:0], W, A, B, idx[:0], scales).shape == (0, 72)
