@@ -112,12 +112,12 @@ __device__ __forceinline__ void load_block(uint32_t dst, int pitch, const T* src
 // rows.  zt is z rounded to T: it is the operand of the products that follow,
 // and the one rounding that they add to their sums.
 //
-// 8192 rows of 4096, rank 16: 27 us for one factor (67 MB), 41 us for a
-// gradient's two (134 MB, 3.3 TB/s); bound by latency: 256 or 512 blocks of
-// some 12 us on 304 places, the tiles that two adapters share taking twice as
-// long, and half as many bytes again of adapters out of the L2.  x staged
-// behind block barriers took 43 us for one, x straight into the MMA's
-// registers 43 to 54 us (one block per SM for want of registers).
+// 8192 rows of 4096, rank 16: 21 us for one factor (67 MB, 3.2 TB/s), 36 us for
+// a gradient's two (134 MB, 3.7 TB/s); bound by latency: 256 or 512 blocks of
+// some 12 us on 304 places, and half as many bytes again of adapters out of the
+// L2.  With one block for both adapters of a tile 27 and 41 us; x staged
+// behind block barriers 43 us for one, x straight into the MMA's registers 43
+// to 54 us (one block per SM for want of registers).
 constexpr int kShRows = 32, kShK = 64, kShWarps = 4, kShThreads = 32 * kShWarps;
 constexpr int kShXBytes = kShRows * kShK * 2;
 constexpr int kShKPitch = kShK * 2 + 16;
