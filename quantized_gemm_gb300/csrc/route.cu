@@ -298,10 +298,7 @@ __global__ void __launch_bounds__(kRouteThreads)
   }
   uint32_t best = 0u, picked = 0u;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    best = max(best, order_key(l[j]));
-    d[j] = 0.f;
-  }
+  for (int j = 0; j < V; ++j) d[j] = 0.f;
   static_assert(V <= 32, "one bit per logit of a lane");
 #pragma unroll 1
   for (int r = 0; r < (int)a.k; ++r) {
@@ -312,6 +309,11 @@ __global__ void __launch_bounds__(kRouteThreads)
     for (int j = 0; j < V; ++j)
       if (i >= 0 && j == at) { d[j] += g; picked |= 1u << j; }
   }
+  // The maximum of the logits that take part in the sum: the picks' own for the
+  // normalised form, since a larger logit need not be among the picks given.
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (!a.normalize || ((picked >> j) & 1u)) best = max(best, order_key(l[j]));
   const uint32_t m = group_max<LPR>(best);
   const float top = m ? key_value(m) : 0.f;
   float sum = 0.f, dot = 0.f;

@@ -1,0 +1,59 @@
+"""Routing, the expert layer and the adapters at values and layouts where a kernel's own arithmetic shows.
+
+Picks that are not the largest logits, infinite weights, factors and hidden
+values near the ends of f16's range, the error in the mean (not only at its
+worst), and calls on another stream.  Tolerances are the oracle's bounds, or
+derived beside the test.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_gemm_gb300 as qg
+from helpers import rand_tensor, to_np
+from oracle import select
+from test_gpu_select import (U, _check_route, _logits, _lowrank_inputs, _moe_inputs, assert_within,  # noqa: F401
+                             clean_status, tensor_path)
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+EPS32 = 2.0 ** -24
+
+
+# ------------------------------------------------------------------ routing
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("T,G,k", [(5, 8, 2), (9, 64, 4), (3, 256, 8), (2, 300, 20)])
+@pytest.mark.parametrize("gap", [5.0, 90.0, 104.0, 300.0])
+@pytest.mark.parametrize("normalize", [0, 1])
+def test_route_gradient_of_picks_below_the_largest_logit(T, G, k, gap, normalize, dtype):
+    """Picks of a biased or capacity-limited router: the row's largest logit, `gap` above the rest, is not among them."""
+    rng = np.random.default_rng(G + int(gap))
+    l = rng.normal(size=(T, G)) * 2
+    idx = np.argsort(rng.random((T, G)), axis=1)[:, :k + 1].astype(np.int32)
+    for t in range(T):
+        l[t, idx[t, k]] = l[t].max() + gap
+    idx = idx[:, :k].copy()
+    idx[0, 1:] = -1                                            # dropped picks; a row without any
+    idx[1] = -1
+    l = torch.from_numpy(l).to(dtype).to(DEV)
+    dw = rand_tensor((T, k), F32, 6, DEV)
+    got = qg.mm_route_topk_grad(l, torch.from_numpy(idx).to(DEV), dw, normalize)
+    want = select.route_topk_grad(to_np(l), idx, to_np(dw), normalize)
+    # the terms' sizes: exp's argument is within 40, or (normalize = 0) the share is below 1e-30 anyway
+    p, d = np.zeros((T, G)), np.zeros((T, G))
+    for t in range(T):
+        p[t] = select._softmax_row(to_np(l)[t])[0]
+        keep = np.isin(np.arange(G), idx[t])
+        if normalize:
+            p[t] = np.where(keep, p[t], 0)
+            p[t] /= max(p[t].sum(), 1e-300)
+        for r in range(k):
+            if idx[t, r] >= 0:
+                d[t, idx[t, r]] = abs(to_np(dw)[t, r])
+    mag = p * (d + (p * d).sum(axis=1, keepdims=True))
+    bound = U[dtype] * np.abs(want) + (2 * G + 140) * EPS32 * mag + 2.0 ** -24 * (dtype == F16) + 1e-30
+    assert_within(got, want, bound, "gradient")
