@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk16_kernel(const Route
     }
     if (live && lane < a.k) {
       static_cast<int32_t*>(a.indices)[row * a.k + lane] = ok ? (int32_t)(0xFFFFu - (mine & 0xFFFFu)) : -1;
-      static_cast<float*>(a.weights)[row * a.k + lane] = ok ? __fdividef(e, sum) : 0.f;
+      static_cast<float*>(a.weights)[row * a.k + lane] = ok ? e / sum : 0.f;
     }
   }
 }

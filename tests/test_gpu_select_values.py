@@ -57,3 +57,14 @@ def test_route_gradient_of_picks_below_the_largest_logit(T, G, k, gap, normalize
     mag = p * (d + (p * d).sum(axis=1, keepdims=True))
     bound = U[dtype] * np.abs(want) + (2 * G + 140) * EPS32 * mag + 2.0 ** -24 * (dtype == F16) + 1e-30
     assert_within(got, want, bound, "gradient")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_route_weights_are_rounded_quotients(dtype):
+    """Equal logits: shares of exactly 1, their sum exact, and the weight the fp32 number nearest to the quotient."""
+    for G in list(range(1, 130)) + [200, 256, 300, 511, 777, 1024]:
+        _, w = qg.mm_route_topk(torch.full((2, G), 0.75, dtype=dtype, device=DEV), 1, 0)
+        assert (w.cpu().numpy() == np.float32(1) / np.float32(G)).all(), G
+    for k in range(1, 33):
+        _, w = qg.mm_route_topk(torch.full((2, 40), -3.0, dtype=dtype, device=DEV), k, 1)
+        assert (w.cpu().numpy() == np.float32(1) / np.float32(k)).all(), k
