@@ -68,3 +68,35 @@ def test_route_weights_are_rounded_quotients(dtype):
     for k in range(1, 33):
         _, w = qg.mm_route_topk(torch.full((2, 40), -3.0, dtype=dtype, device=DEV), k, 1)
         assert (w.cpu().numpy() == np.float32(1) / np.float32(k)).all(), k
+
+
+@pytest.mark.parametrize("T,G,k", [(33, 64, 4), (21, 17, 9), (5, 256, 8), (3, 777, 11)])
+@pytest.mark.parametrize("normalize", [0, 1])
+def test_route_topk_masked_rows_f16(T, G, k, normalize):
+    _check_route(_logits(T, G, F16, T * G, masked=True), k, normalize)
+
+
+_LOWEST = {F32: -3.4028234663852886e38, BF16: -3.3895313892515355e38, F16: -65504.0}
+_SUBNORMAL = {F32: 2.0 ** -149, BF16: 2.0 ** -133, F16: 2.0 ** -24}
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("G,k", [(16, 6), (16, 12), (100, 12)])
+def test_route_topk_ties_zeros_subnormals_and_lowest_values(dtype, G, k):
+    """The order of equal logits, of the two zeros, of the smallest numbers and of the type's most negative ones."""
+    inf, tiny, low = float("inf"), _SUBNORMAL[dtype], _LOWEST[dtype]
+    rows = [[0.0, -0.0, 1.0, 1.0, 1.0, -0.0, 0.0, 0.5],
+            [tiny, 0.0, -tiny, 2 * tiny, -2 * tiny, -0.0, tiny, 3 * tiny],
+            [low, -inf, low, float("nan"), low, -1.0, -inf, low],
+            [inf, low, -low, inf, -inf, 0.0, float("nan"), -low]]
+    l = torch.full((len(rows), G), -inf)
+    l[:, G - 8:] = torch.tensor(rows)
+    l = l.to(dtype)
+    for normalize in (0, 1):
+        idx, w = qg.mm_route_topk(l.to(DEV), k, normalize)
+        ri, rw = select.route_topk(to_np(l), k, normalize)
+        assert idx.cpu().numpy().tolist() == ri.tolist()
+        assert_within(w, rw, (G + 60) * EPS32 * rw + 1e-30, "weights")
+    idx, w = qg.mm_route_topk(torch.full((4, 200), low, dtype=dtype, device=DEV), k, 0)
+    assert idx.cpu().tolist() == [list(range(k))] * 4
+    assert torch.allclose(w, torch.full_like(w, 1 / 200))
