@@ -286,6 +286,14 @@ __device__ __forceinline__ void store_h(const MoeTcParams& p, int row, int64_t f
   store16(p.out, (int64_t)(p.h_rows + row) * p.ld + f, fabsf(hi) < INFINITY ? h - hi : 0.f, p.f16);
 }
 
+// The product of h from those of its parts.  An infinite weight makes hi's
+// product infinite and lo's infinite of either sign or, where lo is 0, NaN: lo
+// only corrects a finite product.  (hi is 0 only where h is, or is too small
+// for T; a hi product that is NaN itself stays NaN.)
+__device__ __forceinline__ float join(float hi, float lo) {
+  return fabsf(hi) == INFINITY ? hi : hi + lo;
+}
+
 template <bool DOWN>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmU,
@@ -546,8 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 16; ++j) {
             const int t = __shfl_sync(0xffffffffu, tok, j);
             const float w = __shfl_sync(0xffffffffu, wt, j);
-            if (j0 + j < rows)
-              acc[t * 128 + l] = __fmaf_rn(w, __uint_as_float(v[j]) + __uint_as_float(lo[j]), acc[t * 128 + l]);
+            if (j0 + j < rows) acc[t * 128 + l] = __fmaf_rn(w, join(__uint_as_float(v[j]), __uint_as_float(lo[j])), acc[t * 128 + l]);
           }
         }
         release(buf);

@@ -100,3 +100,31 @@ def test_route_topk_ties_zeros_subnormals_and_lowest_values(dtype, G, k):
     idx, w = qg.mm_route_topk(torch.full((4, 200), low, dtype=dtype, device=DEV), k, 0)
     assert idx.cpu().tolist() == [list(range(k))] * 4
     assert torch.allclose(w, torch.full_like(w, 1 / 200))
+
+
+# ------------------------------------------------------------------ mixture-of-experts layer
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("act", ["relu", "silu"])
+@pytest.mark.parametrize("T,G,S,K,F,N", [(5, 4, 2, 128, 256, 136), (40, 3, 3, 192, 200, 128)])
+def test_moe_layer_infinite_weights_of_the_second_product(T, G, S, K, F, N, act, dtype, tensor_path):  # noqa: F811
+    """Infinite values of w_down give the infinity or NaN that the formula gives, whatever parts h is held in."""
+    x, wg, wu, wd, idx, w = _moe_inputs(T, G, S, K, F, N, dtype, T + F)
+    rng = np.random.default_rng(T)
+    for e in range(G):
+        f = rng.integers(0, F, size=6)
+        wd[e, f[0], 3], wd[e, f[1], 7], wd[e, f[2], N - 1] = float("inf"), float("-inf"), float("inf")
+        wd[e, f[3], 20], wd[e, f[4], 20] = float("inf"), float("-inf")    # may meet in one sum
+    out = to_np(qg.mm_moe_layer(x, wg, wu, wd, idx, w, act))
+    assert qg.mm_last_path() == qg.MM_PATH_TENSOR
+    args = [to_np(t) for t in (x, wg, wu, wd, idx, w)]
+    with np.errstate(invalid="ignore"):
+        want = select.moe_layer(*args, activation=act)
+    assert np.isinf(want).any()
+    assert (np.isnan(out) == np.isnan(want)).all()
+    assert (np.isposinf(out) == np.isposinf(want)).all() and (np.isneginf(out) == np.isneginf(want)).all()
+    ok = np.isfinite(want)
+    args[3] = np.where(np.isfinite(args[3]), args[3], 0.0)
+    bound = select.moe_layer_bound(*args, activation=act, u=U[dtype])
+    assert (np.abs(out - want)[ok] <= (bound + 1e-30)[ok]).all()
