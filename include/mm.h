@@ -320,10 +320,10 @@ mm_status mm_route_topk_grad(const mm_tensor* logits, const mm_tensor* indices, 
  * (NULL = 1).  activation is an mm_activation.  Inputs take any strides, so
  * w_gate and w_up may be the two halves of one tensor.
  * Every sum is fp32.  On the tensor cores (bf16/f16 operands whose rows are
- * 16-byte aligned along a unit-stride matrix dimension) h is held as the sum
- * of two T values between the two products (its first part is infinite where
- * h exceeds T's range); the CUDA-core form keeps it fp32.  out is rounded
- * once to T.
+ * 16-byte aligned along a unit-stride matrix dimension) h is held as two
+ * scaled T values between the two products: 16 bits of it for bf16; for f16 22
+ * bits, or an absolute 2^-32 where that is more, and an infinity from 2^20 on.
+ * The CUDA-core form keeps it fp32.  out is rounded once to T.
  * An index of -1 is no pick (mm_route_topk writes it); a token without any
  * pick gets zeros.  Any other index outside [0,G) counts as -1 and is
  * recorded as MM_ERR_INDEX_RANGE.  A token's result depends on its own picks

@@ -13,10 +13,10 @@
 // one token, and only the columns of tokens that picked the expert are used,
 // so no token sees another's values or an unpicked expert's.
 //
-// h is held as the sum of two T values (hi = T(h), lo = T(h - hi): 16 bits for
-// bf16, 22 for f16), which the second product takes as separate tokens side by
-// side (N doubled) and adds in its epilogue: no rounding of h worth speaking of
-// next to the output's, for 2 KB more per 16 KB of weights out of the L2.  (As
+// h is held as the sum of two T values (16 bits of it for bf16, 22 for f16:
+// store_h), which the second product takes as separate tokens side by side (N
+// doubled) and adds in its epilogue: no rounding of h worth speaking of next to
+// the output's, for 2 KB more per 16 KB of weights out of the L2.  (As
 // two MMAs per step instead, one token's layer took 134 us against 125: an MMA
 // this narrow takes as long as a wider one.)
 //
@@ -279,19 +279,34 @@ __device__ __forceinline__ void store16(void* dst, int64_t i, float v, int f16) 
   else static_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(v);
 }
 
-// h[row, f] as its two parts; an infinite or NaN h is hi alone.
+// h[row, f] as its two parts, h = hi kHi + lo kLo.  bf16 has fp32's range and
+// takes them as they are.  f16 does not: hi is scaled down, so that h may reach
+// 2^20 (an infinite or NaN h is hi alone), and lo up, so that what hi leaves is
+// a normal number of T however small h is: together 22 bits of h, and where
+// that would be less 2^-32.  hi is never 0 where h is not: its product then has
+// the infinity of an infinite weight.
+constexpr float kF16Hi = 16.f, kF16Lo = 1.f / 128.f;    // bf16: 1 and 1
+__device__ __forceinline__ uint16_t bits16(float v, int f16) {
+  return f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+__device__ __forceinline__ float value16(uint16_t b, int f16) {
+  return f16 ? __half2float(__ushort_as_half(b)) : __bfloat162float(__ushort_as_bfloat16(b));
+}
 __device__ __forceinline__ void store_h(const MoeTcParams& p, int row, int64_t f, float h) {
-  const float hi = p.f16 ? __half2float(__float2half_rn(h)) : __bfloat162float(__float2bfloat16_rn(h));
-  store16(p.out, (int64_t)row * p.ld + f, hi, p.f16);
-  store16(p.out, (int64_t)(p.h_rows + row) * p.ld + f, fabsf(hi) < INFINITY ? h - hi : 0.f, p.f16);
+  const float k_hi = p.f16 ? kF16Hi : 1.f, r_hi = p.f16 ? 1.f / kF16Hi : 1.f, r_lo = p.f16 ? 1.f / kF16Lo : 1.f;
+  uint16_t hi = bits16(h * r_hi, p.f16);
+  hi |= (hi & 0x7FFF) == 0 && h != 0.f;                     // the smallest number of h's sign
+  const float back = value16(hi, p.f16) * k_hi;
+  uint16_t* dst = static_cast<uint16_t*>(p.out) + (int64_t)row * p.ld + f;
+  dst[0] = hi;
+  dst[p.h_rows * p.ld] = bits16(fabsf(back) < INFINITY ? (h - back) * r_lo : 0.f, p.f16);
 }
 
 // The product of h from those of its parts.  An infinite weight makes hi's
 // product infinite and lo's infinite of either sign or, where lo is 0, NaN: lo
-// only corrects a finite product.  (hi is 0 only where h is, or is too small
-// for T; a hi product that is NaN itself stays NaN.)
-__device__ __forceinline__ float join(float hi, float lo) {
-  return fabsf(hi) == INFINITY ? hi : hi + lo;
+// only corrects a finite product (hi is 0 only where h is).
+__device__ __forceinline__ float join(float hi, float lo, float s_hi, float s_lo) {
+  return fabsf(hi) == INFINITY ? hi : __fmaf_rn(lo, s_lo, hi * s_hi);
 }
 
 template <bool DOWN>
@@ -520,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       const uint32_t per_tile = picked * (uint32_t)p.kblocks;
+      const float s_hi = p.f16 ? kF16Hi : 1.f, s_lo = p.f16 ? kF16Lo : 1.f;
       if (picked == 0)                                         // no pick at all: zeros
         for (uint32_t col = cta; col < (uint32_t)p.col_tiles; col += gridDim.x) {
           const int64_t n = (int64_t)col * 128 + l;
@@ -554,7 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 16; ++j) {
             const int t = __shfl_sync(0xffffffffu, tok, j);
             const float w = __shfl_sync(0xffffffffu, wt, j);
-            if (j0 + j < rows) acc[t * 128 + l] = __fmaf_rn(w, join(__uint_as_float(v[j]), __uint_as_float(lo[j])), acc[t * 128 + l]);
+            if (j0 + j < rows)
+              acc[t * 128 + l] = __fmaf_rn(w, join(__uint_as_float(v[j]), __uint_as_float(lo[j]), s_hi, s_lo), acc[t * 128 + l]);
           }
         }
         release(buf);

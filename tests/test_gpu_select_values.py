@@ -128,3 +128,35 @@ def test_moe_layer_infinite_weights_of_the_second_product(T, G, S, K, F, N, act,
     args[3] = np.where(np.isfinite(args[3]), args[3], 0.0)
     bound = select.moe_layer_bound(*args, activation=act, u=U[dtype])
     assert (np.abs(out - want)[ok] <= (bound + 1e-30)[ok]).all()
+
+
+def _rms(a):
+    return float(np.sqrt(np.mean(np.square(a))))
+
+
+def _rounded(want, dtype):
+    return torch.from_numpy(want).to(dtype).double().numpy()
+
+
+@pytest.mark.parametrize("scale", [4.0, 1.0, 2.0 ** -8, 2.0 ** -24])
+def test_moe_layer_hidden_values_over_f16s_range(scale, tensor_path):  # noqa: F811
+    """h (not x or the weights) far from 1 in f16: up to half a million, and down to where h itself is below 2^-17."""
+    T, G, S, K, F, N = 6, 4, 2, 128, 512, 128
+    x, wg, wu, wd, idx, w = _moe_inputs(T, G, S, K, F, N, F16, 17)
+    wg, wu = (wg * (180 * scale) ** 0.5).to(F16), (wu * (180 * scale) ** 0.5).to(F16)
+    if scale > 1:
+        wg, wu, wd = wg * 8, wu * 8, wd * 2.0 ** -10
+    elif scale < 1:
+        wd = (wd * (2.0 ** 6 if scale > 2.0 ** -10 else 2.0 ** 14)).to(F16)
+    out = qg.mm_moe_layer(x, wg, wu, wd, idx, w, "relu")
+    assert qg.mm_last_path() == qg.MM_PATH_TENSOR
+    args = [to_np(t) for t in (x, wg, wu, wd, idx, w)]
+    want = select.moe_layer(*args, activation="relu")
+    h = np.concatenate([np.abs(np.maximum(args[0] @ args[1][e], 0) * (args[0] @ args[2][e])).ravel() for e in range(G)])
+    assert (h.max() > 65504) == (scale > 1) and h.max() < 2.0 ** 20
+    assert (np.sqrt(np.mean(h ** 2)) < 2.0 ** -16) == (scale < 2.0 ** -10)
+    assert np.isfinite(to_np(out)).all()
+    # h in two parts: an error of at most 2^-22 of h, or 2^-32; the output's own rounding dominates.
+    once = _rms(_rounded(want, F16) - want)
+    floor = 2.0 ** -32 * _rms(args[3]) * F ** 0.5
+    assert _rms(to_np(out) - want) <= 1.05 * (once + floor) + 2.0 ** -19 * _rms(want)
