@@ -160,3 +160,27 @@ def test_moe_layer_hidden_values_over_f16s_range(scale, tensor_path):  # noqa: F
     once = _rms(_rounded(want, F16) - want)
     floor = 2.0 ** -32 * _rms(args[3]) * F ** 0.5
     assert _rms(to_np(out) - want) <= 1.05 * (once + floor) + 2.0 ** -19 * _rms(want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,G,S,K,F,N", [(7, 5, 2, 256, 512, 256), (33, 6, 3, 1024, 768, 520), (4, 2, 2, 2048, 1536, 1024)])
+def test_moe_layer_error_in_the_mean_is_one_rounding_of_the_output(T, G, S, K, F, N, dtype, tensor_path):  # noqa: F811
+    """h is not rounded to the tensors' type between the products: an h rounded once adds an error of the size of the
+    output's own rounding, sqrt(2) of it in the mean; two parts of h and fp32 sums add less than 1 % to it."""
+    args = _moe_inputs(T, G, S, K, F, N, dtype, T + F)
+    out = to_np(qg.mm_moe_layer(*args))
+    want = select.moe_layer(*[to_np(t) for t in args])
+    assert _rms(out - want) <= 1.05 * _rms(_rounded(want, dtype) - want)
+
+
+def test_a_hidden_value_rounded_once_would_be_seen():
+    """The check above on the formula with h rounded to the type: it must fail there."""
+    for dtype in (BF16, F16):
+        x, wg, wu, wd, idx, w = [to_np(t) for t in _moe_inputs(7, 5, 2, 256, 512, 256, dtype, 19)]
+        want, got = select.moe_layer(x, wg, wu, wd, idx, w), np.zeros((7, 256))
+        for t, s in np.ndindex(*idx.shape):
+            e = idx[t, s]
+            h = select.activate(x[t] @ wg[e], "silu") * (x[t] @ wu[e])
+            got[t] += w[t, s] * (_rounded(h, dtype) @ wd[e])
+        got = _rounded(got, dtype)
+        assert _rms(got - want) > 1.2 * _rms(_rounded(want, dtype) - want)
