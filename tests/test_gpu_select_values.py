@@ -184,3 +184,26 @@ def test_a_hidden_value_rounded_once_would_be_seen():
             got[t] += w[t, s] * (_rounded(h, dtype) @ wd[e])
         got = _rounded(got, dtype)
         assert _rms(got - want) > 1.2 * _rms(_rounded(want, dtype) - want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_moe_layer_gelu_of_negative_values(dtype):
+    """g/2 (1 + erf(g / sqrt 2)) where erf is close to -1: the value's own digits, not those left of 1 - 1."""
+    F = 64 if dtype == F32 else 256
+    K = 1 if dtype == F32 else 64
+    g = torch.linspace(-9.0, -2.5, F).to(dtype)
+    x = torch.zeros((1, K), dtype=dtype)
+    x[0, 0] = 1.0                                               # x w_gate is exact
+    wg = torch.zeros((1, K, F), dtype=dtype)
+    wg[0, 0] = g
+    wd = torch.ones((1, F, 8), dtype=dtype)
+    wd[0, :, 1:] = torch.nn.functional.one_hot(torch.arange(F) * 7 // F, 7).to(dtype)    # bands of g, small ones alone
+    idx = torch.zeros((1, 1), dtype=torch.int32)
+    out = qg.mm_moe_layer(x.to(DEV), wg.to(DEV), None, wd.to(DEV), idx.to(DEV), None, "gelu")
+    from math import erfc
+    h = np.array([0.5 * v * erfc(-v / np.sqrt(2.0)) for v in g.double().tolist()])
+    want = h @ to_np(wd)[0]
+    # the argument g / sqrt 2 carries two roundings, which erfc(z) takes 2 z^2 = g^2 times; erfc and the products 8
+    # more, h in two parts (bf16) 2^-17, the sum F, the output u
+    rel = (2 * 81 + 8 + F) * EPS32 + (2.0 ** -17 + U[BF16] if dtype == BF16 else 0)
+    assert_within(out, want[None], rel * np.abs(want)[None])
