@@ -505,13 +505,16 @@ __device__ __forceinline__ float unpack16(uint16_t x, int f16) {
   return f16 ? __half2float(__ushort_as_half(x)) : __bfloat162float(__ushort_as_bfloat16(x));
 }
 
-// v[j] += beta * C[n + j] for the 32 columns starting at n.
+// v[j] += beta * C[n + j] for the 32 columns starting at n.  Plain loads, not
+// those of the read-only cache: C may be Y, written by the launch before while
+// this grid waited for it, and then by this grid (kLowRank, and the product
+// beside adapters).
 __device__ __forceinline__ void add_c32(const TcParams& p, const uint16_t* crow, int64_t n, float (&v)[32]) {
   if (p.c_vec && n + 32 <= p.N) {
     const uint4* src = reinterpret_cast<const uint4*>(crow + n);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint4 u = __ldg(src + q);
+      const uint4 u = src[q];
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

@@ -207,3 +207,25 @@ def test_moe_layer_gelu_of_negative_values(dtype):
     # more, h in two parts (bf16) 2^-17, the sum F, the output u
     rel = (2 * 81 + 8 + F) * EPS32 + (2.0 ** -17 + U[BF16] if dtype == BF16 else 0)
     assert_within(out, want[None], rel * np.abs(want)[None])
+
+
+# ------------------------------------------------------------------ low-rank adapters
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("M,K,N", [(1, 512, 1024), (3, 1024, 520), (17, 512, 1024), (64, 1024, 2048), (130, 512, 520),
+                                   (256, 256, 1024)])
+def test_projection_adds_what_the_expansion_has_just_written(M, K, N, dtype):
+    """Y is written, read and written again within one call while its launches overlap: always with the same output
+    memory and other values in it before, the same bits as in fresh memory."""
+    X, W, A, B, idx, scales, _ = _lowrank_inputs(M, K, N, 16, 6, dtype, 231)
+    inputs = [X * s for s in (1.0, -0.5, 2.0, -4.0)]
+    fresh = [qg.mm_lowrank_matmul(x, W, A, B, idx, scales, out=torch.zeros((M, N), dtype=dtype, device=DEV)) for x in inputs]
+    out = torch.empty((M, N), dtype=dtype, device=DEV)
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for i in range(60):
+        qg.mm_lowrank_matmul(inputs[i % 4], W, A, B, idx, scales, out=out)
+        differ += (out != fresh[i % 4]).sum()
+    assert differ.item() == 0
+    args = [to_np(t) for t in (inputs[3], W, A, B, idx, scales)]
+    assert_within(fresh[3], select.lowrank_matmul(*args), select.lowrank_matmul_bound(*args, u=U[dtype]))
