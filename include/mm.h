@@ -352,8 +352,11 @@ mm_status mm_moe_layer(const mm_tensor* x, const mm_tensor* w_gate, const mm_ten
  * Inputs take any strides (W, A and B may be transposed views).  An index of
  * -1 is a row without adapter; any other index outside [0,G) counts as -1 and
  * is recorded as MM_ERR_INDEX_RANGE.
- * Every sum is fp32; Y is rounded to T.  On some paths the low-rank factor
- * X A, or the low-rank part of Y, is rounded to T once before it is used.
+ * Every sum is fp32; Y is rounded to T.  For few rows, and for a row whose
+ * factor scales[g] X A exceeds T's range, the low-rank part of Y is rounded to T
+ * once before the projection joins it.  For many rows on the tensor cores the
+ * factor is held as two T values instead (16 bits of it for bf16; for f16 22, or
+ * an absolute 2^-32 where that is more), or for bf16 above rank 32 as one.
  * Workspace: mm_lowrank_matmul_workspace_size() bytes. */
 mm_status mm_lowrank_matmul_workspace_size(const mm_tensor* X, const mm_tensor* W, const mm_tensor* A,
                                            const mm_tensor* B, size_t* bytes);
@@ -365,6 +368,8 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
  *   dX[m]  = dY[m] @ W^T + V[m] @ A[g]^T                       dense [M,K]
  *   dA[g]  = sum over the rows m of adapter g of X[m]^T V[m]    dense [G,K,R]
  *   dB[g]  = sum over the rows m of adapter g of U[m]^T dY[m]   dense [G,R,N]
+ * U and V are held like X A above; for dA and dB as two T values, which f16
+ * scales row by row to its range.
  * An adapter without rows gets zeros.  Each output may be NULL (not wanted).
  * Results do not depend on the order of execution.
  * Workspace: mm_lowrank_matmul_grad_workspace_size() bytes. */

@@ -232,19 +232,21 @@ size_t factor_bytes(const LowRankArgs& l) {
 
 // Workspace of the many-row gradient kernels.
 struct GradLayout {
-  int64_t zt_ld;
-  FusedLayout fused;     // dX's product; its z and zt are V's
-  size_t u, ut, row, offset, sums_a, sums_b, total;
+  FusedLayout fused;     // dX's product; its z is V's
+  size_t vt, vt_exp, ut, ut_exp, row, offset, sums_a, sums_b, total;
 };
 GradLayout grad_layout(const LowRankPlan& p) {
   const LowRankArgs& l = p.l;
   GradLayout w;
   w.fused = lowrank_fused_layout(l, p.K);
-  w.zt_ld = w.fused.zt_ld;
   size_t o = w.fused.total;
   auto take = [&](size_t bytes) { const size_t at = o; o = align256(o + bytes); return at; };
-  w.u = take((size_t)l.M * (size_t)l.R * 4);
-  w.ut = take((size_t)l.M * (size_t)w.zt_ld * 2);
+  const size_t part = (size_t)l.M * (size_t)w.fused.z_ld * 2, groups = (size_t)((l.R + 63) / 64);
+  const size_t exps = l.dtype == MM_F16 ? groups * (size_t)l.M * 4 : 0;
+  w.vt = take(2 * part);
+  w.vt_exp = take(exps);
+  w.ut = take(2 * part);
+  w.ut_exp = take(exps);
   w.row = take((size_t)l.M * 4);
   w.offset = take((size_t)(l.G + 1) * 4);
   w.sums_a = take((size_t)lowrank_max_parts(l) * (size_t)p.K * (size_t)l.R * 4);
@@ -348,16 +350,16 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
     z = reinterpret_cast<float*>(ws + w.z);
     const FusedTables slots = lowrank_fused_tables(w, ws);
     const LowRankShrink q = {X->data, X->strides[0], p.K, A->data, A->strides[0], A->strides[1], A->strides[2], z,
-                             ws + w.zt};
-    s = launch_lowrank_shrink_tiles(l, &q, 1, w.zt_ld, &slots, nullptr, st);
-    const LowRankFused u = {g, &w, ws, z, ws + w.zt, B->data, B->strides[0], B->strides[1], B->strides[2]};
-    if (s == MM_OK) s = launch_lowrank_finish(l, &u, nullptr, nullptr, 0, w.zt_ld, st);
+                             slots.wide, nullptr, nullptr};
+    s = launch_lowrank_shrink_tiles(l, &q, 1, w.z_ld, &slots, nullptr, st);
+    const LowRankFused u = {g, &w, ws, z, B->data, B->strides[0], B->strides[1], B->strides[2]};
+    if (s == MM_OK) s = launch_lowrank_finish(l, &u, nullptr, nullptr, 0, w.z_ld, st);
     return finish(s, MM_PATH_TENSOR);
   }
   if ((s = launch_lowrank_shrink(l, X->data, X->strides[0], X->strides[1], p.K, A->data, A->strides[0], A->strides[1],
                                  A->strides[2], z, st)) != MM_OK)
     return s;
-  if ((s = launch_lowrank_expand(l, z, B->data, B->strides[0], B->strides[1], B->strides[2], p.N, Y->data, st)) !=
+  if ((s = launch_lowrank_expand(l, z, l.R, B->data, B->strides[0], B->strides[1], B->strides[2], p.N, Y->data, st)) !=
       MM_OK)
     return s;
   return add_projection(g, st);
@@ -402,32 +404,35 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
     const GradLayout w = grad_layout(p);
     char* ws = static_cast<char*>(workspace);
     float* zv = reinterpret_cast<float*>(ws + w.fused.z);
-    void* vt = ws + w.fused.zt;
+    int32_t* v_exp = reinterpret_cast<int32_t*>(ws + w.vt_exp);
+    int32_t* u_exp = reinterpret_cast<int32_t*>(ws + w.ut_exp);
+    const int64_t z_ld = w.fused.z_ld;
     const AdapterRows t = {reinterpret_cast<int32_t*>(ws + w.row), reinterpret_cast<int32_t*>(ws + w.offset)};
     const FusedTables slots = lowrank_fused_tables(w.fused, ws);
     LowRankShrink q[2];
     int factors = 0;
     if (dX || dA)
-      q[factors++] = {dY->data, dY->strides[0], N, B->data, B->strides[0], B->strides[2], B->strides[1], zv, vt};
+      q[factors++] = {dY->data, dY->strides[0], N, B->data, B->strides[0], B->strides[2], B->strides[1],
+                      dX ? zv : nullptr, dX ? slots.wide : nullptr, dA ? ws + w.vt : nullptr, v_exp};
     if (dB)
-      q[factors++] = {X->data, X->strides[0], K, A->data, A->strides[0], A->strides[1], A->strides[2],
-                      reinterpret_cast<float*>(ws + w.u), ws + w.ut};
-    if (factors) s = launch_lowrank_shrink_tiles(l, q, factors, w.zt_ld, dX ? &slots : nullptr, dA || dB ? &t : nullptr, st);
+      q[factors++] = {X->data, X->strides[0], K, A->data, A->strides[0], A->strides[1], A->strides[2], nullptr, nullptr,
+                      ws + w.ut, u_exp};
+    if (factors) s = launch_lowrank_shrink_tiles(l, q, factors, z_ld, dX ? &slots : nullptr, dA || dB ? &t : nullptr, st);
     LowRankOuter o[2];
     int problems = 0;
     if (dA)
-      o[problems++] = {X->data, X->strides[0], K, vt, dA->data, l.R, 1, reinterpret_cast<float*>(ws + w.sums_a)};
+      o[problems++] = {X->data, X->strides[0], K, ws + w.vt, v_exp, dA->data, l.R, 1, reinterpret_cast<float*>(ws + w.sums_a)};
     if (dB)
-      o[problems++] = {dY->data, dY->strides[0], N, ws + w.ut, dB->data, 1, N, reinterpret_cast<float*>(ws + w.sums_b)};
+      o[problems++] = {dY->data, dY->strides[0], N, ws + w.ut, u_exp, dB->data, 1, N, reinterpret_cast<float*>(ws + w.sums_b)};
     const GemmArgs g = projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1], W->strides[0], K,
                                   dX ? dX->data : nullptr);
     const bool fuse = dX && fused_pays(l, g);
-    const LowRankFused u = {g, &w.fused, ws, zv, vt, A->data, A->strides[0], A->strides[2], A->strides[1]};
+    const LowRankFused u = {g, &w.fused, ws, zv, A->data, A->strides[0], A->strides[2], A->strides[1]};
     if (s == MM_OK && (problems || fuse))
-      s = finish(launch_lowrank_finish(l, fuse ? &u : nullptr, &t, o, problems, w.zt_ld, st),
+      s = finish(launch_lowrank_finish(l, fuse ? &u : nullptr, &t, o, problems, z_ld, st),
                  fuse ? MM_PATH_TENSOR : MM_PATH_SIMT);
     if (s == MM_OK && dX && !fuse) {
-      s = launch_lowrank_expand(l, zv, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
+      s = launch_lowrank_expand(l, zv, z_ld, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
       if (s == MM_OK) s = add_projection(g, st);
     }
     return s;
@@ -443,7 +448,7 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
   if (s == MM_OK && dB)
     s = launch_lowrank_outer(l, dY->data, dY->strides[0], dY->strides[1], N, u, dB->data, l.R * N, 1, N, st);
   if (s == MM_OK && dX && l.M > 0 && K > 0) {
-    s = launch_lowrank_expand(l, v, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
+    s = launch_lowrank_expand(l, v, l.R, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
     if (s == MM_OK)
       s = add_projection(projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1],
                                     W->strides[0], K, dX->data), st);

@@ -112,9 +112,9 @@ mm_status launch_simt_moe(const MoeArgs& args, float* h, unsigned* status, cudaS
 mm_status launch_lowrank_shrink(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
                                 const void* a, int64_t a_gs, int64_t a_cs, int64_t a_rs, float* z,
                                 cudaStream_t stream);
-// y[m, n] = sum_r z[m, r] b[g, r, n], rounded to T (dense rows of N).
-mm_status launch_lowrank_expand(const LowRankArgs& l, const float* z, const void* b, int64_t b_gs, int64_t b_rs,
-                                int64_t b_ns, int64_t N, void* y, cudaStream_t stream);
+// y[m, n] = sum_r z[m, r] b[g, r, n], rounded to T (dense rows of N; rows of z z_ld apart).
+mm_status launch_lowrank_expand(const LowRankArgs& l, const float* z, int64_t z_ld, const void* b, int64_t b_gs,
+                                int64_t b_rs, int64_t b_ns, int64_t N, void* y, cudaStream_t stream);
 // out[g, c, r] = sum over the rows m of adapter g of x[m, c] z[m, r] (element strides of out given).
 mm_status launch_lowrank_outer(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
                                const float* z, void* out, int64_t o_gs, int64_t o_cs, int64_t o_rs,

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(256)
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-    expand_kernel(const LowRankArgs l, const float* z, const T* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
+    expand_kernel(const LowRankArgs l, const float* z, int64_t z_ld, const T* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
                   int64_t N, T* y) {
   pdl_begin();
   const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256)
     float v = 0.f;
     if (g >= 0) {
       const T* bg = b + g * b_gs + n * b_ns;
-      for (int64_t r = 0; r < l.R; ++r) v = __fmaf_rn(z[m * l.R + r], to_f32(bg[r * b_rs]), v);
+      for (int64_t r = 0; r < l.R; ++r) v = __fmaf_rn(z[m * z_ld + r], to_f32(bg[r * b_rs]), v);
     }
     y[m * N + n] = from_f32<T>(v);
   }
@@ -335,10 +335,10 @@ mm_status shrink_typed(const LowRankArgs& l, const void* x, int64_t x_rs, int64_
 }
 
 template <typename T>
-mm_status expand_typed(const LowRankArgs& l, const float* z, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
+mm_status expand_typed(const LowRankArgs& l, const float* z, int64_t z_ld, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
                        int64_t N, void* y, cudaStream_t stream) {
   const dim3 grid((unsigned)((N + 255) / 256), rows_y(l.M));
-  return launch_pdl(expand_kernel<T>, grid, dim3(256), 0, stream, l, z, static_cast<const T*>(b), b_gs, b_rs, b_ns, N,
+  return launch_pdl(expand_kernel<T>, grid, dim3(256), 0, stream, l, z, z_ld, static_cast<const T*>(b), b_gs, b_rs, b_ns, N,
                     static_cast<T*>(y)) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
@@ -411,10 +411,10 @@ mm_status launch_lowrank_shrink(const LowRankArgs& l, const void* x, int64_t x_r
   QG_BY_TYPE(shrink_typed, x, x_rs, x_cs, C, a, a_gs, a_cs, a_rs, z, stream)
 }
 
-mm_status launch_lowrank_expand(const LowRankArgs& l, const float* z, const void* b, int64_t b_gs, int64_t b_rs,
-                                int64_t b_ns, int64_t N, void* y, cudaStream_t stream) {
+mm_status launch_lowrank_expand(const LowRankArgs& l, const float* z, int64_t z_ld, const void* b, int64_t b_gs,
+                                int64_t b_rs, int64_t b_ns, int64_t N, void* y, cudaStream_t stream) {
   if (l.M == 0 || N == 0) return MM_OK;
-  QG_BY_TYPE(expand_typed, z, b, b_gs, b_rs, b_ns, N, y, stream)
+  QG_BY_TYPE(expand_typed, z, z_ld, b, b_gs, b_rs, b_ns, N, y, stream)
 }
 
 mm_status launch_lowrank_outer(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,

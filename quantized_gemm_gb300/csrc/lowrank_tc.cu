@@ -12,9 +12,10 @@
 // and the preparation of the fused product Y[m] = X[m] W + z[m] b[g], in which
 // the tcgen05 kernel (tc_gemm.cu, kLowRank) lets each row tile go on, after
 // the k-blocks of X W, with one set of k-blocks per adapter that the tile's
-// rows name: the rows' z (zeros for the other adapters' rows) times that
-// adapter.  The low-rank part then costs ceil(R / 64) k-blocks per adapter and
-// tile on top of K / 64, and Y is written once.  A zero times an infinity or
+// rows name: the rows' z, in two parts (lowrank_two_parts), zeros for the other
+// adapters' rows, times that adapter.  The low-rank part then costs ceil(R / 32)
+// k-blocks per adapter and tile (one part: ceil(R / 64)) on top of K / 64, and Y
+// is written once.  A zero times an infinity or
 // a NaN is not zero, so the adapters that the kernel reads are copies with
 // their non-finite values set to 0.  What those values add to their own rows,
 // and the whole low-rank part of the rows of any adapter past a tile's list
@@ -23,7 +24,7 @@
 //
 // 8192 x 4096 x 14336 with 12 adapters of rank 16 in runs: the product takes
 // 540 us (1.79 PFLOP/s; 40 to 50 adapters over its 32 row tiles of 64 k-blocks
-// make 2 % more of them) and the call 0.60 ms, against 1.99 ms with the
+// make 2 % more of them) and the call 0.57 to 0.60 ms, against 1.99 ms with the
 // low-rank part expanded first and added through C.
 #include <cstring>
 
@@ -73,6 +74,10 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int vali
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid) : "memory");
 }
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  const __half2 c = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&c);
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -109,8 +114,8 @@ __device__ __forceinline__ void load_block(uint32_t dst, int pitch, const T* src
 // alignment allows.  Two blocks per SM (up to 16 ranks) keep 64 KB of x in
 // flight.  The tile is multiplied once per adapter that its rows name (rows of
 // a request are neighbours, so one or two); each pass keeps its own adapter's
-// rows.  zt is z rounded to T: it is the operand of the products that follow,
-// and the one rounding that they add to their sums.
+// rows.  Their z goes out in fp32 (the fused product's operands are made of it)
+// and, for the adapters' gradients, as two T values (zt).
 //
 // 8192 rows of 4096, rank 16: 21 us for one factor (67 MB, 3.2 TB/s), 36 us for
 // a gradient's two (134 MB, 3.7 TB/s); bound by latency: 256 or 512 blocks of
@@ -145,10 +150,27 @@ struct ShrinkArgs {
   int64_t C;
   const void* a; int64_t a_gs, a_ld;
   int per;                                     // elements per copy of the adapter
-  float* z;
-  void* zt; int64_t zt_ld;
+  float* z; int64_t z_ld;
+  uint8_t* wide;
+  void* zt; int32_t* zt_exp;
   unsigned long long timeout_ns, teardown_ns;
 };
+
+// v as two T values.
+template <typename T>
+__device__ __forceinline__ void split(float v, float lo_scale, T& hi, T& lo) {
+  hi = from_f32<T>(v);
+  const float back = to_f32(hi);
+  lo = from_f32<T>(fabsf(back) < INFINITY ? (v - back) * lo_scale : 0.f);
+}
+
+// 2^k, |k| <= 126; v 2^k, |k| <= 250, by two factors.
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + k) << 23); }
+__device__ __forceinline__ float times_pow2(float v, int k) { return v * pow2(k / 2) * pow2(k - k / 2); }
+
+// Exponents of f16 rows whose values are all 0 (they scale nothing), or all 0
+// or not finite (they must not be scaled to 0).
+constexpr int kExpZero = -1000, kExpAny = 1000;
 
 // NT: 8-rank tiles that the accumulators hold.
 template <typename T, bool CK, int NT>
@@ -188,14 +210,9 @@ __device__ void shrink_tile(const CUtensorMap* tmX, const LowRankArgs& l, const 
     else if (g != -1) atomicOr(l.status, kStatusIndexRange);
   }
   unsigned left = __ballot_sync(0xffffffffu, g_lane >= 0);
-  const unsigned none = part == 0 ? ~left : 0u;
   T* zt = static_cast<T*>(p.zt);
-  for (int i = tid; i < rows * nt * 8; i += kShThreads) {   // rows without adapter
-    const int r = i / (nt * 8), c = i - r * (nt * 8);
-    if (!((none >> r) & 1u)) continue;
-    if (c < rc) p.z[(m0 + r) * l.R + r0 + c] = 0.f;
-    if (r0 + c < p.zt_ld) zt[(m0 + r) * p.zt_ld + r0 + c] = from_f32<T>(0.f);
-  }
+  __shared__ unsigned row_max[kShRows];                   // largest finite |z| of a row, as bits
+  __shared__ int row_wide[kShRows];
   uint32_t done = 0, issued = 0;       // this warp's k-blocks over all passes: stage = count % stages
   uint32_t istage = 0, dstage = 0, dphase = 0;
   bool ok = true;
@@ -284,19 +301,49 @@ __device__ void shrink_tile(const CUtensorMap* tmX, const LowRankArgs& l, const 
         q[0] = acc[h][j][0]; q[1] = acc[h][j][1];
         q[8 * red_pitch] = acc[h][j][2]; q[8 * red_pitch + 1] = acc[h][j][3];
       }
+    if (tid < kShRows) {
+      row_max[tid] = 0u;
+      row_wide[tid] = 0;
+    }
     ok = __syncthreads_and(ok);
     const float scale = l.scales ? l.scales[g * l.scales_s] : 1.f;
-    for (int i = tid; i < rows * nt * 8; i += kShThreads) {
-      const int r = i / (nt * 8), c = i - r * (nt * 8);
-      if (!((sel >> r) & 1u)) continue;
+    constexpr bool kScaled = std::is_same<T, __half>::value;
+    auto value = [&](int r, int c) {
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < kShWarps; ++w) v += red[(w * kShRows + r) * red_pitch + c];
-      v = c < rc ? v * scale : 0.f;
-      if (c < rc) p.z[(m0 + r) * l.R + r0 + c] = v;
-      if (r0 + c < p.zt_ld) zt[(m0 + r) * p.zt_ld + r0 + c] = from_f32<T>(v);
+      return c < rc ? v * scale : 0.f;
+    };
+    auto put = [&](int r, int c, float v) {
+      T hi, lo;
+      split<T>(v, 1.f, hi, lo);
+      T* q = zt + (m0 + r) * 2 * p.z_ld + r0 + c;
+      q[0] = hi;
+      q[p.z_ld] = lo;
+    };
+    for (int i = tid; i < rows * nt * 8; i += kShThreads) {
+      const int r = i / (nt * 8), c = i - r * (nt * 8);
+      if (!((sel >> r) & 1u)) continue;
+      const float v = value(r, c);
+      if (p.z) p.z[(m0 + r) * p.z_ld + r0 + c] = v;
+      if (!(fabsf(to_f32(from_f32<T>(v))) < INFINITY)) row_wide[r] = 1;
+      if (!zt) continue;
+      if constexpr (!kScaled) put(r, c, v);
+      else if (fabsf(v) < INFINITY) atomicMax(row_max + r, __float_as_uint(fabsf(v)));
     }
     __syncthreads();
+    if (kScaled && zt) {
+      auto exponent = [&](int r) {                        // -141 to 113
+        return row_max[r] ? (int)(row_max[r] >> 23) - (127 + 14) : row_wide[r] ? kExpAny : kExpZero;
+      };
+      for (int i = tid; i < rows * nt * 8; i += kShThreads) {
+        const int r = i / (nt * 8), c = i - r * (nt * 8);
+        if ((sel >> r) & 1u) put(r, c, times_pow2(value(r, c), max(-150, min(150, -exponent(r)))));
+      }
+      if (tid < rows && ((sel >> tid) & 1u)) p.zt_exp[(int64_t)blockIdx.y * l.M + m0 + tid] = exponent(tid);
+      __syncthreads();
+    }
+    if (p.wide && tid < rows && ((sel >> tid) & 1u)) p.wide[(int64_t)blockIdx.y * l.M + m0 + tid] = (uint8_t)row_wide[tid];
   }
   // After a wait that ran out: let the copies still in flight land.
   for (; done != issued; ++done) {
@@ -430,18 +477,20 @@ __global__ void __launch_bounds__(kShThreads, NT <= 4 ? 2 : 1)
 // ring.  An adapter of one chunk is written at once; the others' chunks are
 // added, in order, by outer_sum.
 //
-// dA and dB of 8192 rows, 4096 + 4096 columns, rank 16 (134 MB): 36 us (3.7
-// TB/s), issue slots 43 % busy: the row gathering and the fragments' loads per
-// 8 KB of x cost more than its two MMAs a warp.  A row's 256 bytes as one bulk
-// copy took 85 us.
+// z comes in two parts, which meet the same fragments of x in one accumulator.
+//
+// dA and dB of 8192 rows, 4096 + 4096 columns, rank 16 (134 MB): bf16 36 us (3.7
+// TB/s), f16 39 us (its rows' scales), 31 us with z rounded once; the row
+// gathering and the fragments' loads per 8 KB of x cost more than its four MMAs
+// a warp.  A row's 256 bytes as one bulk copy took 85 us.
 constexpr int kOutC = 128, kOutRows = 32, kOutStages = 3, kOutThreads = 256;
-constexpr int kOutXPitch = kOutC * 2 + 16, kOutZPitch = 64 * 2 + 16;
+constexpr int kOutXPitch = kOutC * 2 + 16, kOutZPitch = 2 * 64 * 2 + 16;    // z: 64 ranks' hi, then their lo
 constexpr int kOutStage = kOutRows * (kOutXPitch + kOutZPitch);
 
 template <typename T>
 struct OuterProblem {
   const T* x; int64_t x_rs, C;
-  const T* zt;
+  const T* zt; const int32_t* zt_exp;
   T* out; int64_t o_cs, o_rs;      // out [G, C, R] in the order of these strides
   float* part;
 };
@@ -449,11 +498,14 @@ struct OuterProblem {
 // Block bx: 128 columns of the first problem's x (below blocks0) or the second's.
 template <typename T>
 __device__ void outer_tile(const LowRankArgs& l, const AdapterRows& t, const OuterProblem<T>& p0, const OuterProblem<T>& p1,
-                           const int blocks0, const int64_t zt_ld, const int bx, uint8_t* sm) {
+                           const int blocks0, const int64_t z_ld, const int bx, uint8_t* sm) {
   __shared__ int32_t rows[kChunkRows];
+  __shared__ __align__(4) __half factor[kChunkRows];   // f16: what brings a row's z to the chunk's scale
+  __shared__ int chunk_exp;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = (int)l.G;
   const OuterProblem<T>& p = bx < blocks0 ? p0 : p1;
   const int64_t C = p.C;
+  if (tid == 0) chunk_exp = 2 * kExpZero;
   __shared__ int found;                             // the adapter with first_chunk(g) <= chunk < first_chunk(g + 1)
   for (int h = tid; h < G; h += kOutThreads)
     if (first_chunk(__ldcg(t.offset + h), h) <= (int)blockIdx.y && (int)blockIdx.y < first_chunk(__ldcg(t.offset + h + 1), h + 1))
@@ -465,32 +517,45 @@ __device__ void outer_tile(const LowRankArgs& l, const AdapterRows& t, const Out
   const int first = begin + chunk * kChunkRows;
   const int n = min(kChunkRows, end - first);
   if (n <= 0) return;
-  for (int i = tid; i < n; i += kOutThreads) rows[i] = __ldcg(t.row + first + i);
+  // f16: row i's z is held divided by 2^e; the sum is taken divided by 2^E, E the
+  // chunk's largest e, so a row's z comes in times 2^(e - E), exactly but for the
+  // bits that leave f16 at the low end (2^-40 of the largest).  A row whose
+  // largest z is less than 2^-24 of the chunk's adds nothing.
+  constexpr bool kScaled = std::is_same<T, __half>::value;
+  static_assert(kChunkRows == 2 * kOutThreads, "two rows a thread");
+  int e[2] = {kExpZero, kExpZero};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = tid + q * kOutThreads;
+    if (i >= n) continue;
+    const int m = __ldcg(t.row + first + i);
+    rows[i] = m;
+    if constexpr (kScaled) e[q] = __ldcg(p.zt_exp + (int64_t)blockIdx.z * l.M + m);
+  }
   __syncthreads();
   const int64_t c0 = (int64_t)(bx < blocks0 ? bx : bx - blocks0) * kOutC;
   const int cn = (int)min((int64_t)kOutC, C - c0);
   const int r0 = blockIdx.z * 64, rc = (int)min((int64_t)64, l.R - r0), nt = (rc + 7) / 8;
   const uint32_t ring = shared_u32(sm);
   const int steps = (n + kOutRows - 1) / kOutRows;
-  // A thread's pieces: 16 bytes of x in rows tid / 16 and 16 more, 16 bytes of z in row tid / 8.
-  const int xr = tid >> 4, zr = tid >> 3;
+  // A thread's pieces: 16 bytes of x and of z (lanes 8 to 15 of 16: its lo) in rows tid / 16 and 16 more.
+  const int xr = tid >> 4;
   const int x_ok = max(0, min(8, cn - (tid & 15) * 8)) * 2;
   const bool z_in = (tid & 7) < nt;
   const T* xc = p.x + c0 + (x_ok ? (tid & 15) * 8 : 0);
-  const T* zc = p.zt + r0 + (z_in ? (tid & 7) * 8 : 0);
+  const T* zc = p.zt + r0 + (z_in ? ((tid >> 3) & 1) * z_ld + (tid & 7) * 8 : 0);
   const uint32_t xd = ring + (uint32_t)(xr * kOutXPitch + (tid & 15) * 16);
-  const uint32_t zd = ring + (uint32_t)(kOutRows * kOutXPitch + zr * kOutZPitch + (tid & 7) * 16);
+  const uint32_t zd = ring + (uint32_t)(kOutRows * kOutXPitch + xr * kOutZPitch + (tid & 15) * 16);
   auto load = [&](int i, uint32_t st) {
     const int at = i * kOutRows;
-    if (at + kOutRows <= n) {
-      cp_async<16>(xd + st, xc + (int64_t)rows[at + xr] * p.x_rs, x_ok);
-      cp_async<16>(xd + st + 16 * kOutXPitch, xc + (int64_t)rows[at + xr + 16] * p.x_rs, x_ok);
-      if (z_in) cp_async<16>(zd + st, zc + (int64_t)rows[at + zr] * zt_ld, 16);
-    } else {                                        // rows past the end: zeros
-      const int a = at + xr, b = a + 16, z = at + zr;
-      cp_async<16>(xd + st, xc + (int64_t)rows[min(a, n - 1)] * p.x_rs, a < n ? x_ok : 0);
-      cp_async<16>(xd + st + 16 * kOutXPitch, xc + (int64_t)rows[min(b, n - 1)] * p.x_rs, b < n ? x_ok : 0);
-      if (z_in) cp_async<16>(zd + st, zc + (int64_t)rows[min(z, n - 1)] * zt_ld, z < n ? 16 : 0);
+    const bool all = at + kOutRows <= n;            // rows past the end: zeros
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      const int i = at + xr + h;
+      const bool in = all || i < n;
+      const int64_t m = rows[all ? i : min(i, n - 1)];
+      cp_async<16>(xd + st + h * kOutXPitch, xc + m * p.x_rs, in ? x_ok : 0);
+      if (z_in) cp_async<16>(zd + st + h * kOutZPitch, zc + m * 2 * z_ld, in ? 16 : 0);
     }
   };
   float acc[8][4];
@@ -502,6 +567,17 @@ __device__ void outer_tile(const LowRankArgs& l, const AdapterRows& t, const Out
   for (int i = 0; i < kOutStages - 1; ++i) {
     if (i < steps) load(i, (uint32_t)(i * kOutStage));
     cp_commit();
+  }
+  int E = 0;
+  if constexpr (kScaled) {                          // here the first copies are under way
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (e[q] != kExpAny && e[q] != kExpZero) atomicMax(&chunk_exp, e[q]);
+    __syncthreads();
+    E = chunk_exp > kExpZero ? chunk_exp : 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      factor[tid + q * kOutThreads] = __float2half_rn(e[q] == kExpAny ? 1.f : pow2(max(e[q] - E, -30)));
   }
   uint32_t cur = 0, nxt = (kOutStages - 1) * kOutStage;      // byte offsets of stages i and i + kOutStages - 1
   for (int i = 0; i < steps; ++i) {
@@ -517,12 +593,24 @@ __device__ void outer_tile(const LowRankArgs& l, const AdapterRows& t, const Out
       uint32_t fa[4];
       ldsm_x4_t(fa, s + (uint32_t)((k * 16 + (lane & 7) + ((lane >> 4) & 1) * 8) * kOutXPitch + warp * 32 +
                                    ((lane >> 3) & 1) * 16));
+      uint32_t f0 = 0, f1 = 0;                      // of this lane's rows of z: 2 (lane % 4), the next, and 8 more
+      if constexpr (kScaled) {
+        const uint32_t* f = reinterpret_cast<const uint32_t*>(factor + i * kOutRows + k * 16) + (lane & 3);
+        f0 = f[0];
+        f1 = f[4];
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j >= nt) break;
-        uint32_t fb[2];
-        ldsm_x2_t(fb, s + (uint32_t)(kOutRows * kOutXPitch + (k * 16 + (lane & 15)) * kOutZPitch + j * 16));
-        mma16816<T>(acc[j], fa, fb);
+        uint32_t fb[4];                             // hi's fragment, then lo's
+        ldsm_x4_t(fb, s + (uint32_t)(kOutRows * kOutXPitch + (k * 16 + (lane & 15)) * kOutZPitch + j * 16 + (lane >> 4) * 128));
+        if constexpr (kScaled) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) fb[h] = mul_half2(fb[h], h & 1 ? f1 : f0);
+        }
+        const uint32_t hi[2] = {fb[0], fb[1]}, lo[2] = {fb[2], fb[3]};
+        mma16816<T>(acc[j], fa, hi);
+        mma16816<T>(acc[j], fa, lo);
       }
     }
   }
@@ -537,8 +625,9 @@ __device__ void outer_tile(const LowRankArgs& l, const AdapterRows& t, const Out
       const int64_t c = c0 + warp * 16 + (lane >> 2) + (e >> 1) * 8;
       const int r = r0 + j * 8 + (lane & 3) * 2 + (e & 1);
       if (c >= C || r >= l.R) continue;
-      if (whole) out[c * p.o_cs + r * p.o_rs] = from_f32<T>(acc[j][e]);
-      else mine[c * p.o_cs + r * p.o_rs] = acc[j][e];
+      const float v = kScaled ? times_pow2(acc[j][e], E) : acc[j][e];
+      if (whole) out[c * p.o_cs + r * p.o_rs] = from_f32<T>(v);
+      else mine[c * p.o_cs + r * p.o_rs] = v;
     }
   }
 }
@@ -583,20 +672,23 @@ template <typename T>
 struct PlaceArgs {
   int blocks;                    // 0: nothing to place
   int tile_rows, tiles, per_tile, parts;
-  const T* zt; int64_t zt_ld;
+  const float* z; int64_t z_ld;
+  int two;                       // lowrank_two_parts: hi in columns [0, z_ld), lo in the next z_ld
   T* factors; int64_t f_ld;
   const T* b; int64_t b_gs, b_rs, b_ns, N;
-  T* copy; int64_t c_ld;
+  T* copy; int64_t c_ld, k_rows;
   int pieces, vec;
 };
 
 template <typename T>
 __device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const PlaceArgs<T>& p, const int bx) {
   const int tile_rows = p.tile_rows, tiles = p.tiles, per_tile = p.per_tile, parts = p.parts, pieces = p.pieces, vec = p.vec;
-  const T *zt = p.zt, *b = p.b;
+  const T* b = p.b;
   T *factors = p.factors, *copy = p.copy;
-  const int64_t zt_ld = p.zt_ld, f_ld = p.f_ld, b_gs = p.b_gs, b_rs = p.b_rs, b_ns = p.b_ns, N = p.N, c_ld = p.c_ld;
+  const int64_t z_ld = p.z_ld, f_ld = p.f_ld, b_gs = p.b_gs, b_rs = p.b_rs, b_ns = p.b_ns, N = p.N, c_ld = p.c_ld;
   const int tid = threadIdx.x;
+  constexpr bool kF16 = std::is_same<T, __half>::value;
+  constexpr float kLoScale = kF16 ? kF16LoScale : 1.f;
   if (bx < tiles * parts) {
     __shared__ uint32_t named[kSlots / 32];
     __shared__ signed char entry[256];
@@ -607,7 +699,12 @@ __device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const 
     if (tid < tile_rows && m < l.M) {
       const int64_t g = load_index(l.idx, m * l.idx_s, l.ind64);
       has = g >= 0 && g < l.G;
-      if (has) slot = __ldcg(t.slot_of + g);
+      if (has) {
+        slot = __ldcg(t.slot_of + g);
+        // a factor with values that T cannot hold: the fix takes the row in fp32
+        for (int64_t q = 0; q < (l.R + 63) / 64; ++q)
+          if (__ldcg(t.wide + q * l.M + m)) slot = -1;
+      }
     }
     if (tid < kSlots / 32) named[tid] = 0u;
     __syncthreads();
@@ -634,24 +731,46 @@ __device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const 
       if (has && mine < 0) atomicOr(t.head + 1, 1);
     }
     __syncthreads();
-    const int pieces_row = (int)(f_ld / 8), total = n * tile_rows * pieces_row;
+    const int pieces_row = (int)(f_ld / 8), total = n * tile_rows * pieces_row, part_cols = (int)z_ld;
     constexpr int kAhead = 4;                             // reads in flight before the first write
+    const float* z0 = p.z + (int64_t)tile * tile_rows * z_ld;
     for (int i0 = part * 256 + tid; i0 < total; i0 += 256 * parts * kAhead) {
-      uint4 v[kAhead];
+      float4 v[kAhead][2];
+      int from[kAhead];                                   // 0: zeros, 1: hi, 2: lo
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         const int i = i0 + q * 256 * parts;
-        const int row = i / pieces_row, c = (i - row * pieces_row) * 8;     // row of the tile's n blocks
-        const int r = row % tile_rows, j = row / tile_rows;
-        v[q] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < total && entry[r] == j && c < zt_ld)
-          v[q] = __ldcg(reinterpret_cast<const uint4*>(zt + ((int64_t)tile * tile_rows + r) * zt_ld + c));
+        const int row = i / pieces_row, r = row % tile_rows, j = row / tile_rows;     // row of the tile's n blocks
+        int c = (i - row * pieces_row) * 8;
+        from[q] = 1;
+        if (p.two && c >= part_cols) {
+          c -= part_cols;
+          from[q] = 2;
+        }
+        if (i >= total || entry[r] != j || c >= part_cols) {
+          from[q] = 0;
+          continue;
+        }
+        const float4* src = reinterpret_cast<const float4*>(z0 + (int64_t)r * z_ld + c);
+        v[q][0] = __ldcg(src);
+        v[q][1] = __ldcg(src + 1);
       }
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         const int i = i0 + q * 256 * parts;
-        if (i < total)
-          *reinterpret_cast<uint4*>(factors + (int64_t)tile * per_tile * tile_rows * f_ld + (int64_t)i * 8) = v[q];
+        if (i >= total) break;
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        if (from[q]) {
+          const float* s = reinterpret_cast<const float*>(v[q]);
+          T* e = reinterpret_cast<T*>(&o);
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            T hi, lo;
+            split<T>(s[h], kLoScale, hi, lo);
+            e[h] = from[q] == 2 ? lo : hi;
+          }
+        }
+        *reinterpret_cast<uint4*>(factors + (int64_t)tile * per_tile * tile_rows * f_ld + (int64_t)i * 8) = o;
       }
     }
     return;
@@ -659,9 +778,13 @@ __device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const 
   const int rest = bx - tiles * parts;
   const int piece = rest % pieces, slot = rest / pieces;
   if (slot >= __ldcg(t.head)) return;
-  constexpr uint16_t kExp = std::is_same<T, __half>::value ? 0x7C00 : 0x7F80;
+  constexpr uint16_t kExp = kF16 ? 0x7C00 : 0x7F80;
   const uint16_t* src = reinterpret_cast<const uint16_t*>(b) + (int64_t)__ldcg(t.adapter_of + slot) * b_gs;
-  uint16_t* dst = reinterpret_cast<uint16_t*>(copy) + (int64_t)slot * l.R * c_ld;
+  uint16_t* dst = reinterpret_cast<uint16_t*>(copy) + (int64_t)slot * p.k_rows * c_ld;
+  const int64_t ranks = p.two ? z_ld : l.R;                // rows of a part: zeros past R
+  auto second = [&](uint16_t v) {                          // what lo's columns multiply
+    return kF16 ? __half_as_ushort(__float2half_rn(__half2float(__ushort_as_half(v)) * (1.f / kLoScale))) : v;
+  };
   bool bad = false;
   auto finite = [&](uint16_t v) {
     const bool f = (v & kExp) != kExp;
@@ -671,16 +794,27 @@ __device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const 
   constexpr int kAhead = 8;
   if (vec == 1) {                                          // n contiguous: 8 columns of every other rank
     const int64_t n = ((int64_t)piece * 128 + (tid & 127)) * 8;
-    for (int64_t r0 = tid >> 7; n < N && r0 < l.R; r0 += 2 * kAhead) {
+    const int R = (int)l.R, last = (int)ranks;
+    src += n;
+    dst += n;
+    for (int r0 = tid >> 7; n < N && r0 < last; r0 += 2 * kAhead) {
       uint4 u[kAhead];
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) u[q] = *reinterpret_cast<const uint4*>(src + min(r0 + 2 * q, l.R - 1) * b_rs + n);
+      for (int q = 0; q < kAhead; ++q) u[q] = *reinterpret_cast<const uint4*>(src + min(r0 + 2 * q, R - 1) * b_rs);
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
+        const int r = r0 + 2 * q;
+        if (r >= last) break;
         uint16_t* e = reinterpret_cast<uint16_t*>(&u[q]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = finite(e[j]);
-        if (r0 + 2 * q < l.R) *reinterpret_cast<uint4*>(dst + (r0 + 2 * q) * c_ld + n) = u[q];
+        for (int j = 0; j < 8; ++j) e[j] = r < R ? finite(e[j]) : (uint16_t)0;
+        uint16_t* to = dst + r * c_ld;
+        *reinterpret_cast<uint4*>(to) = u[q];
+        if (p.two) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = second(e[j]);
+          *reinterpret_cast<uint4*>(to + z_ld * c_ld) = u[q];
+        }
       }
     }
   } else {                                                 // 4 columns, 8 ranks of each at a time
@@ -707,7 +841,11 @@ __device__ void lowrank_place(const LowRankArgs& l, const FusedTables& t, const 
         const uint16_t* e = reinterpret_cast<const uint16_t*>(&u[q]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (n < c_ld && r0 + j < l.R) dst[(r0 + j) * c_ld + n] = finite(e[j]);
+          if (n < c_ld && r0 + j < ranks) {
+            const uint16_t v = finite(e[j]);
+            dst[(r0 + j) * c_ld + n] = v;
+            if (p.two) dst[(z_ld + r0 + j) * c_ld + n] = second(v);
+          }
       }
     }
   }
@@ -725,7 +863,7 @@ constexpr int kFixColumns = 8, kFixRows = 152;   // its blocks: 256 columns at a
 template <typename T>
 struct FixArgs {
   int blocks;                    // 0: nothing to fix
-  const float* z;
+  const float* z; int64_t z_ld;
   const T* b; int64_t b_gs, b_rs, b_ns, N;
   T* y;
 };
@@ -748,7 +886,7 @@ __device__ void lowrank_fix(const LowRankArgs& l, const FusedTables& t, const Fi
       for (int64_t r = 0; r < l.R; ++r) {
         const T q = bn[r * p.b_rs];
         const bool bad = (*reinterpret_cast<const uint16_t*>(&q) & kExp) == kExp;
-        if (all || bad) v = __fmaf_rn(p.z[m * l.R + r], to_f32(q), v);
+        if (all || bad) v = __fmaf_rn(p.z[m * p.z_ld + r], to_f32(q), v);
       }
       p.y[m * p.N + n] = from_f32<T>(v);
     }
@@ -763,13 +901,13 @@ template <typename T>
 __global__ void __launch_bounds__(256, 3)
     lowrank_middle_kernel(const LowRankArgs l, const FusedTables f, const __grid_constant__ PlaceArgs<T> place,
                           const AdapterRows t, const __grid_constant__ OuterProblem<T> p0,
-                          const __grid_constant__ OuterProblem<T> p1, const int blocks0, const int64_t zt_ld) {
+                          const __grid_constant__ OuterProblem<T> p1, const int blocks0, const int64_t z_ld) {
   pdl_begin();
   extern __shared__ __align__(16) uint8_t sm[];
   if ((int)blockIdx.x < place.blocks) {
     if (blockIdx.y == 0 && blockIdx.z == 0) lowrank_place<T>(l, f, place, blockIdx.x);
   } else {
-    outer_tile<T>(l, t, p0, p1, blocks0, zt_ld, (int)blockIdx.x - place.blocks, sm);
+    outer_tile<T>(l, t, p0, p1, blocks0, z_ld, (int)blockIdx.x - place.blocks, sm);
   }
 }
 
@@ -806,7 +944,7 @@ bool shrink_map(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t C, Op
 }
 
 template <typename T>
-mm_status shrink_launch(const LowRankArgs& l, const LowRankShrink* q, int problems, int64_t zt_ld,
+mm_status shrink_launch(const LowRankArgs& l, const LowRankShrink* q, int problems, int64_t z_ld,
                         const FusedTables* slots, const AdapterRows* sort, cudaStream_t stream) {
   TcParams limits;                      // the pipelines' wait limits
   init_params(&limits);
@@ -824,7 +962,7 @@ mm_status shrink_launch(const LowRankArgs& l, const LowRankShrink* q, int proble
     a.per = 8;
     while (a.per > 1 && (reinterpret_cast<uintptr_t>(a.a) % (a.per * 2) || (l.G > 1 && a.a_gs % a.per) || a.a_ld % a.per))
       a.per >>= 1;
-    a.z = s.z; a.zt = s.zt; a.zt_ld = zt_ld;
+    a.z = s.z; a.z_ld = z_ld; a.wide = s.wide; a.zt = s.zt; a.zt_exp = s.zt_exp;
     a.timeout_ns = limits.timeout_ns; a.teardown_ns = limits.teardown_ns;
     if (!shrink_map(l, s.x, s.x_rs, s.C, &map[i])) return MM_ERR_UNSUPPORTED;
     const int need = shrink_smem(a.ck, rc);
@@ -857,18 +995,22 @@ bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t
          shrink_map(l, x, x_rs, C, &map);
 }
 
-mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const LowRankShrink* p, int problems, int64_t zt_ld,
+mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const LowRankShrink* p, int problems, int64_t z_ld,
                                       const FusedTables* slots, const AdapterRows* sort, cudaStream_t stream) {
-  return l.dtype == MM_F16 ? shrink_launch<__half>(l, p, problems, zt_ld, slots, sort, stream)
-                           : shrink_launch<__nv_bfloat16>(l, p, problems, zt_ld, slots, sort, stream);
+  return l.dtype == MM_F16 ? shrink_launch<__half>(l, p, problems, z_ld, slots, sort, stream)
+                           : shrink_launch<__nv_bfloat16>(l, p, problems, z_ld, slots, sort, stream);
 }
 
 namespace {
 
+int64_t factor_columns(const LowRankArgs& l) {
+  const int64_t z_ld = (l.R + 7) / 8 * 8;
+  return ((lowrank_two_parts(l) ? 2 * z_ld : l.R) + 63) / 64 * 64;
+}
 // Adapters that a row tile can list: all of them up to kExtPerTile, fewer
 // (16 at least) where the factors' blocks would take more than 256 MB.
 int64_t per_tile(const LowRankArgs& l) {
-  const int64_t bytes = (l.M + 255) / 256 * 256 * ((l.R + 63) / 64 * 64) * 2;
+  const int64_t bytes = (l.M + 255) / 256 * 256 * factor_columns(l) * 2;
   int64_t n = kExtPerTile;
   while (n > 16 && n * bytes > (256ll << 20)) n /= 2;
   const int64_t most = l.G < l.M ? l.G : l.M;
@@ -884,12 +1026,13 @@ FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N) {
   const int64_t rows = (l.M + 255) / 256 * 256, tiles = rows / 128;
   w.slots = l.G < l.M ? l.G : l.M;
   if (w.slots > kSlots) w.slots = kSlots;
-  w.zt_ld = (l.R + 7) / 8 * 8;
-  w.f_ld = (l.R + 63) / 64 * 64;
+  w.two = lowrank_two_parts(l);
+  w.z_ld = (l.R + 7) / 8 * 8;
+  w.k_rows = w.two ? 2 * w.z_ld : l.R;
+  w.f_ld = factor_columns(l);
   w.per_tile = per_tile(l);
   w.c_ld = (N + 7) / 8 * 8;
-  w.z = take((size_t)l.M * (size_t)l.R * 4);
-  w.zt = take((size_t)l.M * (size_t)w.zt_ld * 2);
+  w.z = take((size_t)l.M * (size_t)w.z_ld * 4);
   w.head = take(8);
   w.slot_of = take((size_t)l.G * 4);
   w.adapter_of = take(kSlots * 4);
@@ -898,8 +1041,9 @@ FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N) {
   w.ext_count = take((size_t)tiles * 4);
   w.ext_slot = take((size_t)tiles * (size_t)w.per_tile * 4);
   w.row_c = take((size_t)l.M * 4);
+  w.wide = take((size_t)l.M * (size_t)((l.R + 63) / 64));
   w.factors = take((size_t)rows * (size_t)w.per_tile * (size_t)w.f_ld * 2);
-  w.copy = take((size_t)w.slots * (size_t)l.R * (size_t)w.c_ld * 2);
+  w.copy = take((size_t)w.slots * (size_t)w.k_rows * (size_t)w.c_ld * 2);
   w.total = o;
   return w;
 }
@@ -919,6 +1063,7 @@ FusedTables lowrank_fused_tables(const FusedLayout& w, char* ws) {
   t.ext_count = reinterpret_cast<int32_t*>(ws + w.ext_count);
   t.ext_slot = reinterpret_cast<int32_t*>(ws + w.ext_slot);
   t.row_c = reinterpret_cast<int32_t*>(ws + w.row_c);
+  t.wide = reinterpret_cast<uint8_t*>(ws + w.wide);
   return t;
 }
 
@@ -926,7 +1071,7 @@ namespace {
 
 template <typename T>
 mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const AdapterRows* t, const LowRankOuter* o,
-                       int problems, int64_t zt_ld, cudaStream_t stream) {
+                       int problems, int64_t z_ld, cudaStream_t stream) {
   FusedTables f = {};
   PlaceArgs<T> place = {};
   FixArgs<T> fix = {};
@@ -936,7 +1081,7 @@ mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const Adapte
     f = lowrank_fused_tables(w, u->ws);
     e.tile_rows = tc_lowrank_tile_rows(u->product);
     e.factors = u->ws + w.factors; e.factor_ld = w.f_ld; e.per_tile = w.per_tile;
-    e.adapters = u->ws + w.copy; e.slots = w.slots; e.R = l.R; e.adapter_ld = w.c_ld;
+    e.adapters = u->ws + w.copy; e.slots = w.slots; e.k_rows = w.k_rows; e.adapter_ld = w.c_ld;
     e.count = f.ext_count; e.slot = f.ext_slot;
     e.head = f.head; e.row_c = f.row_c;
     const int64_t N = u->product.N, tiles = (l.M + e.tile_rows - 1) / e.tile_rows, pieces = (w.c_ld + 1023) / 1024;
@@ -948,7 +1093,7 @@ mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const Adapte
     const bool base = (l.G == 1 || u->b_gs % 8 == 0) && reinterpret_cast<uintptr_t>(u->b) % 16 == 0;
     place.blocks = (int)blocks;
     place.tile_rows = e.tile_rows; place.tiles = (int)tiles; place.per_tile = (int)w.per_tile; place.parts = (int)parts;
-    place.zt = static_cast<const T*>(u->zt); place.zt_ld = w.zt_ld;
+    place.z = u->z; place.z_ld = w.z_ld; place.two = w.two; place.k_rows = w.k_rows;
     place.factors = reinterpret_cast<T*>(u->ws + w.factors); place.f_ld = w.f_ld;
     place.b = static_cast<const T*>(u->b);
     place.b_gs = u->b_gs; place.b_rs = u->b_rs; place.b_ns = u->b_ns; place.N = N;
@@ -957,23 +1102,26 @@ mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const Adapte
     place.vec = base && u->b_ns == 1 && u->b_rs % 8 == 0 && N % 8 == 0     ? 1
                 : base && u->b_rs == 1 && u->b_ns % 8 == 0 && l.R % 8 == 0 ? 2 : 0;
     fix.blocks = kFixColumns * kFixRows;
-    fix.z = u->z;
+    fix.z = u->z; fix.z_ld = w.z_ld;
     fix.b = place.b; fix.b_gs = u->b_gs; fix.b_rs = u->b_rs; fix.b_ns = u->b_ns; fix.N = N;
     fix.y = static_cast<T*>(const_cast<void*>(u->product.y.ptr));
   }
   OuterProblem<T> p[2] = {};
   int64_t blocks[2] = {0, 0}, most = 0;
   for (int i = 0; i < problems; ++i) {
-    p[i] = {static_cast<const T*>(o[i].x), o[i].x_rs, o[i].C, static_cast<const T*>(o[i].zt), static_cast<T*>(o[i].out),
-            o[i].o_cs, o[i].o_rs, o[i].part};
+    p[i] = {static_cast<const T*>(o[i].x), o[i].x_rs, o[i].C, static_cast<const T*>(o[i].zt), o[i].zt_exp,
+            static_cast<T*>(o[i].out), o[i].o_cs, o[i].o_rs, o[i].part};
     blocks[i] = (o[i].C + kOutC - 1) / kOutC;
     if (o[i].C > most) most = o[i].C;
   }
   const AdapterRows rows = t ? *t : AdapterRows{};
   const dim3 middle((unsigned)(place.blocks + blocks[0] + blocks[1]), problems ? (unsigned)lowrank_max_chunks(l) : 1u,
                     problems ? (unsigned)((l.R + 63) / 64) : 1u);
+  if (cudaFuncSetAttribute(lowrank_middle_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutStages * kOutStage) !=
+      cudaSuccess)
+    return MM_ERR_CUDA;
   if (launch_pdl(lowrank_middle_kernel<T>, middle, dim3(256), problems ? (size_t)(kOutStages * kOutStage) : 0, stream, l, f,
-                 place, rows, p[0], p[1], (int)blocks[0], zt_ld) != cudaSuccess)
+                 place, rows, p[0], p[1], (int)blocks[0], z_ld) != cudaSuccess)
     return MM_ERR_CUDA;
   const int64_t per = (most * l.R + 1023) / 1024, sum_blocks = per < 64 ? per : 64;
   const int64_t last = fix.blocks + problems * l.G * sum_blocks;
@@ -986,9 +1134,9 @@ mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const Adapte
 }  // namespace
 
 mm_status launch_lowrank_finish(const LowRankArgs& l, const LowRankFused* fused, const AdapterRows* rows,
-                                const LowRankOuter* outer, int problems, int64_t zt_ld, cudaStream_t stream) {
-  return l.dtype == MM_F16 ? finish_typed<__half>(l, fused, rows, outer, problems, zt_ld, stream)
-                           : finish_typed<__nv_bfloat16>(l, fused, rows, outer, problems, zt_ld, stream);
+                                const LowRankOuter* outer, int problems, int64_t z_ld, cudaStream_t stream) {
+  return l.dtype == MM_F16 ? finish_typed<__half>(l, fused, rows, outer, problems, z_ld, stream)
+                           : finish_typed<__nv_bfloat16>(l, fused, rows, outer, problems, z_ld, stream);
 }
 
 }  // namespace qg

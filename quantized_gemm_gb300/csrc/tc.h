@@ -29,8 +29,8 @@ struct LowRankExt {
   int tile_rows;                 // tc_lowrank_tile_rows
   const void* factors;           // [row tiles * per_tile * tile_rows, factor_ld], factor_ld a multiple of 64
   int64_t factor_ld, per_tile;   // per_tile: adapters that a tile can list
-  const void* adapters;          // [slots, R, adapter_ld], finite, adapter_ld a multiple of 8
-  int64_t slots, R, adapter_ld;
+  const void* adapters;          // [slots, k_rows, adapter_ld], finite, adapter_ld a multiple of 8
+  int64_t slots, k_rows, adapter_ld;
   const int32_t* count;
   const int32_t* slot;
   const int32_t* head;           // [1]: whether any row's Y holds a part to add

@@ -1885,8 +1885,8 @@ mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* st
   BatchMap slots = g.bm;
   slots.nb = 1;
   slots.shape[0] = slots.count = e.slots;
-  const int64_t ss[kMaxBatchDims] = {e.R * e.adapter_ld, 0, 0, 0, 0, 0};
-  if (!plan_operand(e.adapters, g.dtype, g.N, e.R, 1, e.adapter_ld, slots, ss, BN, &w) || !w.mn_major)
+  const int64_t ss[kMaxBatchDims] = {e.k_rows * e.adapter_ld, 0, 0, 0, 0, 0};
+  if (!plan_operand(e.adapters, g.dtype, g.N, e.k_rows, 1, e.adapter_ld, slots, ss, BN, &w) || !w.mn_major)
     return MM_ERR_UNSUPPORTED;
   p.idesc = make_idesc(p.out_f16, a.mn_major, b.mn_major, pair);
   p.idesc_ext = make_idesc(p.out_f16, 0, 1, pair);
@@ -1898,7 +1898,7 @@ mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* st
   p.beta = 1.f;
   p.c_cs = 1;
   p.c_vec = p.y_vec;
-  p.ext_kb = (int)((e.R + BK - 1) / BK);
+  p.ext_kb = (int)((e.k_rows + BK - 1) / BK);
   return launch_tc(kLowRank, pair, a, b, p, stream, &z, &w);
 }
 

@@ -229,3 +229,56 @@ def test_projection_adds_what_the_expansion_has_just_written(M, K, N, dtype):
     assert differ.item() == 0
     args = [to_np(t) for t in (inputs[3], W, A, B, idx, scales)]
     assert_within(fresh[3], select.lowrank_matmul(*args), select.lowrank_matmul_bound(*args, u=U[dtype]))
+
+
+
+@pytest.mark.parametrize("M", [40, 200, 300, 700])
+def test_lowrank_factors_past_f16s_range(M):
+    """X A above f16's largest value, B small: Y lies well inside the range, whichever kernel the row count selects."""
+    X, W, A, B, idx, scales, _ = _lowrank_inputs(M, 256, 264, 16, 4, F16, 201)
+    X, A, B = X * 64, A * 600, (B * 2.0 ** -10).to(F16)
+    args = [to_np(t) for t in (X, W, A, B, idx, scales)]
+    z = np.concatenate([args[5][g] * (args[0][args[4] == g] @ args[2][g]) for g in range(4)])
+    assert (np.abs(z).max(axis=1) > 65504).any() and (np.abs(z).max(axis=1) < 65504).any()
+    assert_within(qg.mm_lowrank_matmul(X, W, A, B, idx, scales), select.lowrank_matmul(*args),
+                  select.lowrank_matmul_bound(*args, u=U[F16]))
+
+
+@pytest.mark.parametrize("M,R,runs", [(300, 16, 0), (700, 40, 1), (1100, 8, 1)])
+@pytest.mark.parametrize("big", ["V", "U"])
+def test_lowrank_gradients_of_factors_at_both_ends_of_f16s_range(M, R, runs, big):
+    """V = s dY B^T above f16's largest value beside U = s X A below its smallest, and the reverse."""
+    X, W, A, B, idx, scales, dY = _lowrank_inputs(M, 256, 264, R, 4, F16, 211, runs)
+    if big == "V":           # dX and dA inside the range through small A and X, dB through a large dY
+        dY, B, X, A, scales = dY * 4096, B * 16, X * 2.0 ** -12, A * 2.0 ** -10, scales * 2.0 ** -2
+    else:                    # a large U with a small dY, and V below 2^-24
+        dY, B, X, A = dY * 2.0 ** -12, (B * 2.0 ** -14).to(F16), X * 4096, A * 64
+    W = (W * 2.0 ** -4).to(F16)
+    args = [to_np(t) for t in (dY, X, W, A, B, idx, scales)]
+    V = np.concatenate([args[6][g] * (args[0][args[5] == g] @ args[4][g].T) for g in range(4)])
+    Uf = np.concatenate([args[6][g] * (args[1][args[5] == g] @ args[3][g]) for g in range(4)])
+    large, small = (V, Uf) if big == "V" else (Uf, V)
+    assert np.abs(large).max() > 65504 and _rms(small) < 2.0 ** -17
+    got = qg.mm_lowrank_matmul_grad(dY, X, W, A, B, idx, scales)
+    for name, g, want, bound in zip(("dX", "dA", "dB"), got, select.lowrank_matmul_grad(*args),
+                                    select.lowrank_matmul_grad_bound(*args, u=U[F16])):
+        assert_within(g, want, bound, name)
+        # in the mean: the output's own rounding and 5 % of it; where V is past the range, dX takes that part of itself
+        # as one value of the type, an error of the same size
+        most = 1.5 if (name, big) == ("dX", "V") else 1.05
+        assert _rms(to_np(g) - want) <= most * _rms(_rounded(want, F16) - want) + 2.0 ** -19 * _rms(want), name
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("M,K,N,R,G,runs", [(700, 256, 264, 16, 4, 1), (1040, 264, 520, 12, 3, 0), (600, 512, 256, 32, 2, 1)])
+def test_lowrank_error_in_the_mean_is_one_rounding_of_the_output(M, K, N, R, G, runs, dtype):
+    """Many rows: the factors are not rounded to the tensors' type on their way into the products.  (One rounding of a
+    factor adds an error of the size of the output's: sqrt(2) of it in the mean for dA and dB.)"""
+    X, W, A, B, idx, scales, dY = _lowrank_inputs(M, K, N, R, G, dtype, M + R, runs)
+    B = B * 4                                                   # the low-rank part dominates Y and dX
+    args = [to_np(t) for t in (X, W, A, B, idx, scales)]
+    Y, want = to_np(qg.mm_lowrank_matmul(X, W, A, B, idx, scales)), select.lowrank_matmul(*args)
+    assert _rms(Y - want) <= 1.05 * _rms(_rounded(want, dtype) - want)
+    got = qg.mm_lowrank_matmul_grad(dY, X, W, A, B, idx, scales)
+    for name, g, want in zip(("dX", "dA", "dB"), got, select.lowrank_matmul_grad(to_np(dY), *args)):
+        assert _rms(to_np(g) - want) <= 1.05 * _rms(_rounded(want, dtype) - want), name
