@@ -495,10 +495,11 @@ struct OuterProblem {
   float* part;
 };
 
-// Block bx: 128 columns of the first problem's x (below blocks0) or the second's.
+// Block bx: 128 columns of the first problem's x (below blocks0) or the second's;
+// chunk number `number`, ranks from 64 `group`.
 template <typename T>
 __device__ void outer_tile(const LowRankArgs& l, const AdapterRows& t, const OuterProblem<T>& p0, const OuterProblem<T>& p1,
-                           const int blocks0, const int64_t z_ld, const int bx, uint8_t* sm) {
+                           const int blocks0, const int64_t z_ld, const int bx, const int number, const int group, uint8_t* sm) {
   __shared__ int32_t rows[kChunkRows];
   __shared__ __align__(4) __half factor[kChunkRows];   // f16: what brings a row's z to the chunk's scale
   __shared__ int chunk_exp;
@@ -508,12 +509,12 @@ __device__ void outer_tile(const LowRankArgs& l, const AdapterRows& t, const Out
   if (tid == 0) chunk_exp = 2 * kExpZero;
   __shared__ int found;                             // the adapter with first_chunk(g) <= chunk < first_chunk(g + 1)
   for (int h = tid; h < G; h += kOutThreads)
-    if (first_chunk(__ldcg(t.offset + h), h) <= (int)blockIdx.y && (int)blockIdx.y < first_chunk(__ldcg(t.offset + h + 1), h + 1))
+    if (first_chunk(__ldcg(t.offset + h), h) <= number && number < first_chunk(__ldcg(t.offset + h + 1), h + 1))
       found = h;
   __syncthreads();
-  if ((int)blockIdx.y >= first_chunk(__ldcg(t.offset + G), G)) return;
+  if (number >= first_chunk(__ldcg(t.offset + G), G)) return;
   const int g = found, begin = __ldcg(t.offset + g), end = __ldcg(t.offset + g + 1);
-  const int chunk = (int)blockIdx.y - first_chunk(begin, g);          // of this adapter
+  const int chunk = number - first_chunk(begin, g);          // of this adapter
   const int first = begin + chunk * kChunkRows;
   const int n = min(kChunkRows, end - first);
   if (n <= 0) return;
@@ -530,12 +531,12 @@ __device__ void outer_tile(const LowRankArgs& l, const AdapterRows& t, const Out
     if (i >= n) continue;
     const int m = __ldcg(t.row + first + i);
     rows[i] = m;
-    if constexpr (kScaled) e[q] = __ldcg(p.zt_exp + (int64_t)blockIdx.z * l.M + m);
+    if constexpr (kScaled) e[q] = __ldcg(p.zt_exp + (int64_t)group * l.M + m);
   }
   __syncthreads();
   const int64_t c0 = (int64_t)(bx < blocks0 ? bx : bx - blocks0) * kOutC;
   const int cn = (int)min((int64_t)kOutC, C - c0);
-  const int r0 = blockIdx.z * 64, rc = (int)min((int64_t)64, l.R - r0), nt = (rc + 7) / 8;
+  const int r0 = group * 64, rc = (int)min((int64_t)64, l.R - r0), nt = (rc + 7) / 8;
   const uint32_t ring = shared_u32(sm);
   const int steps = (n + kOutRows - 1) / kOutRows;
   // A thread's pieces: 16 bytes of x and of z (lanes 8 to 15 of 16: its lo) in rows tid / 16 and 16 more.
@@ -895,19 +896,22 @@ __device__ void lowrank_fix(const LowRankArgs& l, const FusedTables& t, const Fi
 
 // ------------------------------------------------------------------ kernels of several steps
 
-// After the factors: the fused product's operands (first blocks; 7 us alone)
-// and the adapters' gradients, which do not depend on each other.
+// After the factors: the fused product's operands (first blocks; 9 us alone)
+// and the adapters' gradients (the others: columns, then chunks, then groups of
+// ranks), which do not depend on each other.
 template <typename T>
 __global__ void __launch_bounds__(256, 3)
     lowrank_middle_kernel(const LowRankArgs l, const FusedTables f, const __grid_constant__ PlaceArgs<T> place,
                           const AdapterRows t, const __grid_constant__ OuterProblem<T> p0,
-                          const __grid_constant__ OuterProblem<T> p1, const int blocks0, const int64_t z_ld) {
+                          const __grid_constant__ OuterProblem<T> p1, const int blocks0, const int columns,
+                          const int chunks, const int64_t z_ld) {
   pdl_begin();
   extern __shared__ __align__(16) uint8_t sm[];
   if ((int)blockIdx.x < place.blocks) {
-    if (blockIdx.y == 0 && blockIdx.z == 0) lowrank_place<T>(l, f, place, blockIdx.x);
+    lowrank_place<T>(l, f, place, blockIdx.x);
   } else {
-    outer_tile<T>(l, t, p0, p1, blocks0, z_ld, (int)blockIdx.x - place.blocks, sm);
+    const int b = (int)blockIdx.x - place.blocks, rest = b / columns;
+    outer_tile<T>(l, t, p0, p1, blocks0, z_ld, b % columns, rest % chunks, rest / chunks, sm);
   }
 }
 
@@ -1115,13 +1119,15 @@ mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const Adapte
     if (o[i].C > most) most = o[i].C;
   }
   const AdapterRows rows = t ? *t : AdapterRows{};
-  const dim3 middle((unsigned)(place.blocks + blocks[0] + blocks[1]), problems ? (unsigned)lowrank_max_chunks(l) : 1u,
-                    problems ? (unsigned)((l.R + 63) / 64) : 1u);
+  const int64_t columns = blocks[0] + blocks[1], chunks = lowrank_max_chunks(l);
+  const int64_t middle = place.blocks + columns * chunks * ((l.R + 63) / 64);
+  if (middle > 0x7fffffffLL) return MM_ERR_UNSUPPORTED;     // the operands would not fit the memory
   if (cudaFuncSetAttribute(lowrank_middle_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutStages * kOutStage) !=
       cudaSuccess)
     return MM_ERR_CUDA;
-  if (launch_pdl(lowrank_middle_kernel<T>, middle, dim3(256), problems ? (size_t)(kOutStages * kOutStage) : 0, stream, l, f,
-                 place, rows, p[0], p[1], (int)blocks[0], z_ld) != cudaSuccess)
+  if (launch_pdl(lowrank_middle_kernel<T>, dim3((unsigned)middle), dim3(256), problems ? (size_t)(kOutStages * kOutStage) : 0, stream, l, f,
+                 place, rows, p[0], p[1], (int)blocks[0], (int)(columns > 0 ? columns : 1), (int)chunks, z_ld) !=
+      cudaSuccess)
     return MM_ERR_CUDA;
   const int64_t per = (most * l.R + 1023) / 1024, sum_blocks = per < 64 ? per : 64;
   const int64_t last = fix.blocks + problems * l.G * sum_blocks;

@@ -13,7 +13,7 @@ import torch
 import quantized_gemm_gb300 as qg
 from helpers import rand_tensor, to_np
 from oracle import select
-from test_gpu_select import (U, _check_route, _logits, _lowrank_inputs, _moe_inputs, assert_within,  # noqa: F401
+from test_gpu_select import (U, _check_lowrank_grad, _check_route, _logits, _lowrank_inputs, _moe_inputs, assert_within,  # noqa: F401
                              clean_status, tensor_path)
 
 pytestmark = pytest.mark.gpu
@@ -282,3 +282,14 @@ def test_lowrank_error_in_the_mean_is_one_rounding_of_the_output(M, K, N, R, G, 
     got = qg.mm_lowrank_matmul_grad(dY, X, W, A, B, idx, scales)
     for name, g, want in zip(("dX", "dA", "dB"), got, select.lowrank_matmul_grad(to_np(dY), *args)):
         assert _rms(to_np(g) - want) <= 1.05 * _rms(_rounded(want, dtype) - want), name
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("M,K,N,R,G", [(300, 136, 264, 200, 3), (2000, 72, 136, 72, 600), (1100, 264, 72, 8, 1024)])
+def test_lowrank_gradients_of_many_adapters_and_ranks(M, K, N, R, G, dtype):
+    """Several groups of 64 ranks, more adapters than rows have, all three gradients and each pair."""
+    X, W, A, B, idx, scales, dY = _lowrank_inputs(M, K, N, R, G, dtype, M + R)
+    full = _check_lowrank_grad(dY, X, W, A, B, idx, scales)
+    for need in ((True, True, False), (True, False, True), (False, True, True)):
+        for f, p in zip(full, qg.mm_lowrank_matmul_grad(dY, X, W, A, B, idx, scales, need=need)):
+            assert p is None or torch.equal(f, p)
