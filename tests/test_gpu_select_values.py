@@ -293,3 +293,20 @@ def test_lowrank_gradients_of_many_adapters_and_ranks(M, K, N, R, G, dtype):
     for need in ((True, True, False), (True, False, True), (False, True, True)):
         for f, p in zip(full, qg.mm_lowrank_matmul_grad(dY, X, W, A, B, idx, scales, need=need)):
             assert p is None or torch.equal(f, p)
+
+
+@pytest.mark.parametrize("R", [16, 72])
+def test_lowrank_gradients_of_rows_of_very_different_size_f16(R):
+    """Rows of one adapter whose factors lie up to 2^20 apart, in no order: each row's part of the sum to its own scale."""
+    M, K, N, G = 900, 136, 72, 2
+    X, W, A, B, idx, scales, dY = _lowrank_inputs(M, K, N, R, G, F16, 241)
+    rng = np.random.default_rng(5)
+    size = torch.from_numpy(2.0 ** rng.integers(-10, 11, size=(M, 1))).to(DEV)
+    X, dY = (X * size).to(F16), (dY / size).to(F16)             # U as large as X, V as small as dY
+    W = (W * 2.0 ** -8).to(F16)
+    args = [to_np(t) for t in (dY, X, W, A, B, idx, scales)]
+    got = qg.mm_lowrank_matmul_grad(dY, X, W, A, B, idx, scales)
+    for name, g, want, bound in zip(("dX", "dA", "dB"), got, select.lowrank_matmul_grad(*args),
+                                    select.lowrank_matmul_grad_bound(*args, u=U[F16])):
+        assert_within(g, want, bound, name)
+        assert _rms(to_np(g) - want) <= 1.05 * _rms(_rounded(want, F16) - want) + 2.0 ** -19 * _rms(want), name
