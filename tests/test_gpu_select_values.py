@@ -310,3 +310,34 @@ def test_lowrank_gradients_of_rows_of_very_different_size_f16(R):
                                     select.lowrank_matmul_grad_bound(*args, u=U[F16])):
         assert_within(g, want, bound, name)
         assert _rms(to_np(g) - want) <= 1.05 * _rms(_rounded(want, F16) - want) + 2.0 ** -19 * _rms(want), name
+
+
+def _constant(name):
+    import os
+    import re
+
+    with open(os.path.join(os.path.dirname(qg.__file__), "csrc", "lowrank.cuh")) as f:
+        return int(re.search(r"constexpr int %s = (\d+);" % name, f.read()).group(1))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("M,K,N,R,G", [(3400, 48, 136, 1, 200), (4200, 40, 72, 2500, 100)])
+def test_lowrank_rows_past_the_slots_or_the_list_are_rounded_once(M, K, N, R, G, dtype):
+    """Rows of more adapters than the product holds copies of, or than a row tile lists: the projection's sum is not
+    rounded before the low-rank part joins it."""
+    X, W, A, B, idx, scales, _ = _lowrank_inputs(M, K, N, R, G, dtype, M)
+    args = [to_np(t) for t in (X, W, A, B, idx, scales)]
+    slots, per_tile = _constant("kSlots"), _constant("kSlots")
+    while per_tile > 16 and per_tile * ((M + 255) // 256 * 256 * ((R + 63) // 64 * 64) * 2) > 256 << 20:
+        per_tile //= 2
+    per_tile = min(per_tile, G)
+    used = np.unique(args[4][args[4] >= 0])
+    named = max(len(np.unique(args[4][t:t + 256][args[4][t:t + 256] >= 0])) for t in range(0, M, 256))
+    assert len(used) > slots or named > per_tile
+    assert G < (M + 15) // 16                                   # not the few-row kernels
+    want = select.lowrank_matmul(*args)
+    base, zero = np.abs(args[0]) @ np.abs(args[1]), np.zeros_like(args[1])
+    low = select.lowrank_matmul(np.abs(args[0]), zero, np.abs(args[2]), np.abs(args[3]), args[4], args[5])
+    u = U[dtype]                     # Y's rounding, and one or two of the low-rank part
+    assert_within(qg.mm_lowrank_matmul(X, W, A, B, idx, scales), want,
+                  u * np.abs(want) + 2.01 * u * low + (2 * K + R) * EPS32 * (base + low) + 2.0 ** -24)
