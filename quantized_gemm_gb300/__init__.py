@@ -167,6 +167,21 @@ def _stream(t, stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, like, stream):
+    """Memory for a call on ``stream`` (None: the current one), of that stream's own: what torch hands out on the current
+    stream may still be in use by work queued there, which another stream does not wait for.  The current stream may
+    then use it until it is freed, too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    current = torch.cuda.current_stream(like.device)
+    if stream == current:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(current)
+    return t
+
+
 def _check(status, where):
     if status != 0:
         raise MMError(status, where)
@@ -179,7 +194,7 @@ def _out_shape(fn, *args):
     return tuple(shape[i] for i in range(nd.value))
 
 
-def _workspace(nbytes, device, given=None):
+def _workspace(nbytes, like, stream, given=None):
     """(tensor, size) of a workspace of at least ``nbytes``: ``given`` when it is large enough."""
     if nbytes == 0:
         return None, 0
@@ -187,8 +202,7 @@ def _workspace(nbytes, device, given=None):
         if given.numel() * given.element_size() < nbytes:
             raise ValueError("workspace of %d bytes is smaller than the %d required" % (given.numel(), nbytes))
         return given, given.numel() * given.element_size()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return ws, nbytes
+    return _empty(nbytes, torch.uint8, like, stream), nbytes
 
 
 def mm_qlinear_matmul_workspace_size(a, b):
@@ -254,8 +268,7 @@ def mm_matmul(A, B, out=None, stream=None):
     lib = _lib()
     dA, dB = _desc(A), _desc(B)
     # A given output is checked by the library itself (MM_ERR_SHAPE).
-    Y = out if out is not None else torch.empty(_out_shape(lib.mm_matmul_output_shape, _ref(dA), _ref(dB)),
-                                                dtype=A.dtype, device=A.device)
+    Y = out if out is not None else _empty(_out_shape(lib.mm_matmul_output_shape, _ref(dA), _ref(dB)), A.dtype, A, stream)
     _check(lib.mm_matmul(_ref(dA), _ref(dB), _ref(_desc(Y)), _stream(A, stream)), "mm_matmul")
     return Y
 
@@ -264,9 +277,8 @@ def mm_gemm(A, B, C=None, alpha=1.0, beta=1.0, transA=0, transB=0, out=None, str
     """Y = alpha * A' @ B' + beta * C (Gemm, opset 13)."""
     lib = _lib()
     dA, dB = _desc(A), _desc(B)
-    Y = out if out is not None else torch.empty(
-        _out_shape(lib.mm_gemm_output_shape, _ref(dA), _ref(dB), int(transA), int(transB)), dtype=A.dtype,
-        device=A.device)
+    Y = out if out is not None else _empty(
+        _out_shape(lib.mm_gemm_output_shape, _ref(dA), _ref(dB), int(transA), int(transB)), A.dtype, A, stream)
     _check(lib.mm_gemm(_ref(dA), _ref(dB), _ref(_desc(C)), float(alpha), float(beta), int(transA), int(transB),
                        _ref(_desc(Y)), _stream(A, stream)), "mm_gemm")
     return Y
@@ -277,12 +289,12 @@ def mm_qlinear_matmul(a, a_scale, a_zero_point, b, b_scale, b_zero_point, y_scal
     """Quantized matmul of int8/uint8 tensors (QLinearMatMul, opset 10); y has y_zero_point's type."""
     lib = _lib()
     da, db = _desc(a), _desc(b)
-    y = out if out is not None else torch.empty(_out_shape(lib.mm_matmul_output_shape, _ref(da), _ref(db)),
-                                                dtype=y_zero_point.dtype, device=a.device)
+    y = out if out is not None else _empty(_out_shape(lib.mm_matmul_output_shape, _ref(da), _ref(db)),
+                                           y_zero_point.dtype, a, stream)
     nbytes = ctypes.c_size_t()
     _check(lib.mm_qlinear_matmul_workspace_size(_ref(da), _ref(db), ctypes.byref(nbytes)),
            "mm_qlinear_matmul_workspace_size")
-    ws, wsb = _workspace(nbytes.value, a.device, workspace)
+    ws, wsb = _workspace(nbytes.value, a, stream, workspace)
     _check(lib.mm_qlinear_matmul(_ref(da), _ref(_desc(a_scale)), _ref(_desc(a_zero_point)), _ref(db),
                                  _ref(_desc(b_scale)), _ref(_desc(b_zero_point)), _ref(_desc(y_scale)),
                                  _ref(_desc(y_zero_point)), _ref(_desc(y)),
@@ -296,11 +308,11 @@ def mm_grouped_matmul(input, weights, group_indices, bias=None, out=None, stream
     lib = _lib()
     dx, dw, dg = _desc(input), _desc(weights), _desc(group_indices)
     M, S, N = input.shape[0], group_indices.shape[1], weights.shape[2]
-    y = torch.empty((M, S, N), dtype=input.dtype, device=input.device) if out is None else out
+    y = _empty((M, S, N), input.dtype, input, stream) if out is None else out
     nbytes = ctypes.c_size_t()
     _check(lib.mm_grouped_matmul_workspace_size(_ref(dx), _ref(dw), _ref(dg), ctypes.byref(nbytes)),
            "mm_grouped_matmul_workspace_size")
-    ws, wsb = _workspace(nbytes.value, input.device, workspace)
+    ws, wsb = _workspace(nbytes.value, input, stream, workspace)
     _check(lib.mm_grouped_matmul(_ref(dx), _ref(dw), _ref(dg), _ref(_desc(bias)), _ref(_desc(y)),
                                  None if ws is None else ws.data_ptr(), wsb, _stream(input, stream)),
            "mm_grouped_matmul")
@@ -332,10 +344,10 @@ def mm_grouped_matmul_qweights(input, weights_q, w_scale, w_zero_point, block_si
     lib = _lib()
     M, S = input.shape[0], group_indices.shape[1]
     N = weights_q.shape[2] * (2 if packed4 is not None else 1)
-    y = torch.empty((M, S, N), dtype=input.dtype, device=input.device) if out is None else out
+    y = _empty((M, S, N), input.dtype, input, stream) if out is None else out
     ws, wsb = _workspace(mm_grouped_matmul_qweights_workspace_size(input, weights_q, w_scale, w_zero_point,
                                                                    block_size, group_indices, packed4),
-                         input.device, workspace)
+                         input, stream, workspace)
     _check(lib.mm_grouped_matmul_qweights(_ref(_desc(input)), _ref(_qdesc(weights_q, packed4)), _ref(_desc(w_scale)),
                                           _ref(_qdesc(w_zero_point, packed4)), int(block_size),
                                           _ref(_desc(group_indices)),
@@ -353,20 +365,12 @@ def mm_grouped_matmul_noalloc(input, weights, group_indices, bias=None, out=None
     allocation by the library).  ``out`` must be given by such callers; when
     it is None this binding allocates it with torch for convenience.
     """
-    y = torch.empty((input.shape[0], group_indices.shape[1], weights.shape[2]), dtype=input.dtype,
-                    device=input.device) if out is None else out
+    y = _empty((input.shape[0], group_indices.shape[1], weights.shape[2]), input.dtype, input,
+               stream) if out is None else out
     _check(_lib().mm_grouped_matmul_noalloc(_ref(_desc(input)), _ref(_desc(weights)), _ref(_desc(group_indices)),
                                             _ref(_desc(bias)), _ref(_desc(y)), _stream(input, stream)),
            "mm_grouped_matmul_noalloc")
     return y
-
-
-def _used_on(stream, *tensors):
-    """Tells torch's allocator that ``stream`` uses the tensors, which come from the current stream's memory and may be
-    freed before the work on ``stream`` has run."""
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
 
 
 # The calls below take a few microseconds on the device for small sizes, as
@@ -379,28 +383,24 @@ def mm_route_topk(logits, k, normalize=1, indices=None, weights=None, stream=Non
     the lowest index; weights are the softmax over all experts, divided by the picks' sum when ``normalize``."""
     lib = _LIB or _lib()
     if indices is None:
-        indices = torch.empty((logits.shape[0], k), dtype=torch.int32, device=logits.device)
+        indices = _empty((logits.shape[0], k), torch.int32, logits, stream)
     if weights is None:
-        weights = torch.empty((logits.shape[0], k), dtype=torch.float32, device=logits.device)
+        weights = _empty((logits.shape[0], k), torch.float32, logits, stream)
     status = lib.mm_route_topk(_ref(_desc(logits)), int(normalize), _ref(_desc(indices)), _ref(_desc(weights)),
                                _stream(logits, stream))
     if status:
         raise MMError(status, "mm_route_topk")
-    if stream is not None:
-        _used_on(stream, indices, weights)
     return indices, weights
 
 
 def mm_route_topk_grad(logits, indices, grad_weights, normalize=1, out=None, stream=None):
     """Gradient of mm_route_topk's weights with respect to the logits (in the logits' type)."""
     lib = _LIB or _lib()
-    y = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if out is None else out
+    y = _empty(logits.shape, logits.dtype, logits, stream) if out is None else out
     status = lib.mm_route_topk_grad(_ref(_desc(logits)), _ref(_desc(indices)), _ref(_desc(grad_weights)),
                                     int(normalize), _ref(_desc(y)), _stream(logits, stream))
     if status:
         raise MMError(status, "mm_route_topk_grad")
-    if stream is not None:
-        _used_on(stream, y)
     return y
 
 
@@ -413,11 +413,11 @@ def _sized(fn, *descs):
     return nbytes.value
 
 
-def _given_or_sized(workspace, device, fn, *descs):
+def _given_or_sized(workspace, like, stream, fn, *descs):
     """(tensor, size) of the workspace: the caller's (the library checks its size), or one of the size ``fn`` names."""
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
-    return _workspace(_sized(fn, *descs), device)
+    return _workspace(_sized(fn, *descs), like, stream)
 
 
 def mm_moe_layer_workspace_size(x, w_gate, w_up, w_down, expert_indices):
@@ -435,15 +435,13 @@ def mm_moe_layer(x, w_gate, w_up, w_down, expert_indices, expert_weights=None, a
         raise ValueError("activation must be one of %s" % ", ".join(sorted(_ACTIVATIONS)))
     lib = _LIB or _lib()
     dx, dg, du, dd, di = _desc(x), _desc(w_gate), _desc(w_up), _desc(w_down), _desc(expert_indices)
-    y = torch.empty((x.shape[0], w_down.shape[2]), dtype=x.dtype, device=x.device) if out is None else out
-    ws, wsb = _given_or_sized(workspace, x.device, lib.mm_moe_layer_workspace_size, dx, dg, du, dd, di)
+    y = _empty((x.shape[0], w_down.shape[2]), x.dtype, x, stream) if out is None else out
+    ws, wsb = _given_or_sized(workspace, x, stream, lib.mm_moe_layer_workspace_size, dx, dg, du, dd, di)
     status = lib.mm_moe_layer(_ref(dx), _ref(dg), _ref(du), _ref(dd), _ref(di),
                               _ref(_desc(expert_weights)), act, _ref(_desc(y)),
                               None if ws is None else ws.data_ptr(), wsb, _stream(x, stream))
     if status:
         raise MMError(status, "mm_moe_layer")
-    if stream is not None:
-        _used_on(stream, y, ws)
     return y
 
 
@@ -456,15 +454,13 @@ def mm_lowrank_matmul(X, W, A, B, adapter_indices, scales=None, out=None, stream
     g = adapter_indices[m] (-1: no adapter)."""
     lib = _LIB or _lib()
     dX, dW, dA, dB = _desc(X), _desc(W), _desc(A), _desc(B)
-    y = torch.empty((X.shape[0], W.shape[1]), dtype=X.dtype, device=X.device) if out is None else out
-    ws, wsb = _given_or_sized(workspace, X.device, lib.mm_lowrank_matmul_workspace_size, dX, dW, dA, dB)
+    y = _empty((X.shape[0], W.shape[1]), X.dtype, X, stream) if out is None else out
+    ws, wsb = _given_or_sized(workspace, X, stream, lib.mm_lowrank_matmul_workspace_size, dX, dW, dA, dB)
     status = lib.mm_lowrank_matmul(_ref(dX), _ref(dW), _ref(dA), _ref(dB), _ref(_desc(adapter_indices)),
                                    _ref(_desc(scales)), _ref(_desc(y)),
                                    None if ws is None else ws.data_ptr(), wsb, _stream(X, stream))
     if status:
         raise MMError(status, "mm_lowrank_matmul")
-    if stream is not None:
-        _used_on(stream, y, ws)
     return y
 
 
@@ -478,17 +474,15 @@ def mm_lowrank_matmul_grad(dY, X, W, A, B, adapter_indices, scales=None, need=(T
     others' place)."""
     lib = _LIB or _lib()
     d = [_desc(t) for t in (X, W, A, B)]
-    dX = torch.empty(X.shape, dtype=X.dtype, device=X.device) if need[0] else None
-    dA = torch.empty(A.shape, dtype=A.dtype, device=X.device) if need[1] else None
-    dB = torch.empty(B.shape, dtype=B.dtype, device=X.device) if need[2] else None
-    ws, wsb = _given_or_sized(workspace, X.device, lib.mm_lowrank_matmul_grad_workspace_size, *d)
+    dX = _empty(X.shape, X.dtype, X, stream) if need[0] else None
+    dA = _empty(A.shape, A.dtype, X, stream) if need[1] else None
+    dB = _empty(B.shape, B.dtype, X, stream) if need[2] else None
+    ws, wsb = _given_or_sized(workspace, X, stream, lib.mm_lowrank_matmul_grad_workspace_size, *d)
     status = lib.mm_lowrank_matmul_grad(_ref(_desc(dY)), *[_ref(t) for t in d], _ref(_desc(adapter_indices)),
                                         _ref(_desc(scales)), _ref(_desc(dX)), _ref(_desc(dA)), _ref(_desc(dB)),
                                         None if ws is None else ws.data_ptr(), wsb, _stream(X, stream))
     if status:
         raise MMError(status, "mm_lowrank_matmul_grad")
-    if stream is not None:
-        _used_on(stream, dX, dA, dB, ws)
     return dX, dA, dB
 
 

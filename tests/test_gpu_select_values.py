@@ -341,3 +341,51 @@ def test_lowrank_rows_past_the_slots_or_the_list_are_rounded_once(M, K, N, R, G,
     u = U[dtype]                     # Y's rounding, and one or two of the low-rank part
     assert_within(qg.mm_lowrank_matmul(X, W, A, B, idx, scales), want,
                   u * np.abs(want) + 2.01 * u * low + (2 * K + R) * EPS32 * (base + low) + 2.0 ** -24)
+
+
+# ------------------------------------------------------------------ streams
+
+
+@pytest.mark.parametrize("call", ["matmul", "gemm", "qlinear", "grouped", "qweights", "noalloc", "route", "route_grad", "moe",
+                                  "lowrank", "lowrank_grad"])
+def test_outputs_of_a_call_on_another_stream_are_not_memory_still_in_use(call):
+    """Memory freed on the current stream is handed out again at once, ordered by that stream alone: a call on another
+    stream that took it would write while the current stream's work still does."""
+    x, wg, wu, wd, idx, w = _moe_inputs(64, 4, 2, 256, 256, 256, BF16, 221)
+    *lr, dY = _lowrank_inputs(64, 256, 256, 16, 4, BF16, 222)
+    q8 = torch.randint(-100, 100, (64, 256), dtype=torch.int8, device=DEV)
+    sc, zp = torch.tensor(0.02, device=DEV), torch.tensor(3, dtype=torch.int8, device=DEV)
+    wq = torch.randint(-100, 100, (4, 256, 256), dtype=torch.int8, device=DEV)
+    ws = torch.rand((4, 1, 256), device=DEV).to(BF16)
+    ri, rw = qg.mm_route_topk(x, 4)
+    calls = {"matmul": lambda s: qg.mm_matmul(x, wg[0], stream=s),
+             "gemm": lambda s: qg.mm_gemm(x, wg[0], stream=s),
+             "qlinear": lambda s: qg.mm_qlinear_matmul(q8, sc, zp, q8.t(), sc, zp, sc, zp, stream=s),
+             "grouped": lambda s: qg.mm_grouped_matmul(x, wg, idx, stream=s),
+             "qweights": lambda s: qg.mm_grouped_matmul_qweights(x, wq, ws, None, 0, idx, stream=s),
+             "noalloc": lambda s: qg.mm_grouped_matmul_noalloc(x, wg, idx, stream=s),
+             "route": lambda s: qg.mm_route_topk(x, 4, stream=s),
+             "route_grad": lambda s: qg.mm_route_topk_grad(x, ri, rw, stream=s),
+             "moe": lambda s: qg.mm_moe_layer(x, wg, wu, wd, idx, w, stream=s),
+             "lowrank": lambda s: qg.mm_lowrank_matmul(*lr, stream=s),
+             "lowrank_grad": lambda s: qg.mm_lowrank_matmul_grad(dY, *lr, stream=s)}
+
+    def run(stream):
+        got = calls[call](stream)
+        return list(got) if isinstance(got, tuple) else [got]
+
+    want = run(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    sizes = sorted({t.numel() * t.element_size() for t in want} | {1 << n for n in range(9, 25)})
+    junk = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(4)]
+    torch.cuda._sleep(100_000_000)
+    for t in junk:
+        t.fill_(0xFF)                                    # still to run when the call below is made
+    del junk, t
+    got = run(side)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    for t in got:                                        # and the outputs are good for the current stream's work
+        t.add_(1)
