@@ -352,11 +352,12 @@ mm_status mm_moe_layer(const mm_tensor* x, const mm_tensor* w_gate, const mm_ten
  * Inputs take any strides (W, A and B may be transposed views).  An index of
  * -1 is a row without adapter; any other index outside [0,G) counts as -1 and
  * is recorded as MM_ERR_INDEX_RANGE.
- * Every sum is fp32; Y is rounded to T.  For few rows, and for a row whose
- * factor scales[g] X A exceeds T's range, the low-rank part of Y is rounded to T
- * once before the projection joins it.  For many rows on the tensor cores the
- * factor is held as two T values instead (16 bits of it for bf16; for f16 22, or
- * an absolute 2^-32 where that is more), or for bf16 above rank 32 as one.
+ * Every sum is fp32; Y is rounded to T.  For up to 64 rows the low-rank part of
+ * Y joins the projection in fp32.  For many rows on the tensor cores the factor
+ * scales[g] X A is held as two T values (16 bits of it for bf16; for f16 22, or an
+ * absolute 2^-32 where that is more), or for bf16 above rank 32 as one.  In
+ * between, on the CUDA cores, and for a row whose factor exceeds T's range, the
+ * low-rank part is rounded to T once before the projection joins it.
  * Workspace: mm_lowrank_matmul_workspace_size() bytes. */
 mm_status mm_lowrank_matmul_workspace_size(const mm_tensor* X, const mm_tensor* W, const mm_tensor* A,
                                            const mm_tensor* B, size_t* bytes);

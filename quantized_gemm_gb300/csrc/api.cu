@@ -202,16 +202,31 @@ mm_status finish(mm_status s, int path) {
 // products take one pass of the CUDA-core tiles.
 static bool few_row_pays(const GemmArgs& g) { return (double)g.N * (double)g.K * (double)g.bm.count >= 131072.0; }
 
-mm_status run_dense(const GemmArgs& g, bool pays, cudaStream_t st) {
+int dense_path(const GemmArgs& g, bool pays, bool* c_f32) {
   const int pol = g_policy.load();
+  int path;
+  bool few = false;
   if (pol == MM_PATH_VECTOR || (pol == MM_PATH_AUTO && vec_gemm_preferred(g) && few_row_pays(g))) {
-    if (!vec_gemm_supported(g)) return MM_ERR_UNSUPPORTED;
-    return finish(launch_vec_gemm(g, st), MM_PATH_VECTOR);
+    path = vec_gemm_supported(g) ? MM_PATH_VECTOR : -1;
+  } else {
+    few = c_f32 && tc_gemm_few_rows(g);
+    path = choose(few || tc_gemm_supported(g), pays);
   }
-  const int path = choose(tc_gemm_supported(g), pays);
-  if (path < 0) return MM_ERR_UNSUPPORTED;
-  if (path == MM_PATH_TENSOR) return finish(launch_tc_gemm(g, device_status_ptr(), st), MM_PATH_TENSOR);
-  return finish(launch_simt_gemm(g, st), MM_PATH_SIMT);
+  if (c_f32) *c_f32 = g.dtype != MM_F32 && (path != MM_PATH_TENSOR || few);
+  return path;
+}
+
+mm_status run_dense_on(int path, const GemmArgs& g, cudaStream_t st) {
+  switch (path) {
+    case MM_PATH_VECTOR: return finish(launch_vec_gemm(g, st), MM_PATH_VECTOR);
+    case MM_PATH_TENSOR: return finish(launch_tc_gemm(g, device_status_ptr(), st), MM_PATH_TENSOR);
+    case MM_PATH_SIMT: return finish(launch_simt_gemm(g, st), MM_PATH_SIMT);
+    default: return MM_ERR_UNSUPPORTED;
+  }
+}
+
+mm_status run_dense(const GemmArgs& g, bool pays, cudaStream_t st) {
+  return run_dense_on(dense_path(g, pays, nullptr), g, st);
 }
 
 }  // namespace qg

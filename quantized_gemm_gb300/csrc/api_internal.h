@@ -28,7 +28,11 @@ bool tensor_pays(int64_t M, int64_t N, int64_t K, int64_t batch);
 bool tensor_pays_dense(int dtype, int64_t M, int64_t N, int64_t K, int64_t batch);
 // Records the path of a successful call.
 mm_status finish(mm_status s, int path);
-// MatMul and Gemm after validation.
+// MatMul and Gemm after validation: the path that a product takes (an mm_path
+// value, -1: none) and, where asked for, whether its kernel takes C in fp32
+// (GemmArgs::c_f32); the product on that path; both.
+int dense_path(const GemmArgs& g, bool pays, bool* c_f32);
+mm_status run_dense_on(int path, const GemmArgs& g, cudaStream_t st);
 mm_status run_dense(const GemmArgs& g, bool pays, cudaStream_t st);
 
 }  // namespace qg

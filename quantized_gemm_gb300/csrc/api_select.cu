@@ -260,15 +260,22 @@ bool many_rows(const LowRankArgs& l) {
          lowrank_sort_supported(l);
 }
 
-// What a call asks for, whichever of its kernels then runs.
-size_t lowrank_bytes(const LowRankPlan& p) {
+// What a call asks for, whichever of its kernels then runs: the factors and what
+// belongs to them, then (few rows) the low-rank part in fp32.
+size_t lowrank_base_bytes(const LowRankPlan& p) {
   const size_t few = factor_bytes(p.l), many = many_rows(p.l) ? lowrank_fused_layout(p.l, p.N).total : 0;
   return few > many ? few : many;
 }
-size_t lowrank_grad_bytes(const LowRankPlan& p) {
+size_t lowrank_grad_base_bytes(const LowRankPlan& p) {
   const size_t few = 2 * factor_bytes(p.l), many = many_rows(p.l) ? grad_layout(p).total : 0;
   return few > many ? few : many;
 }
+bool float_part(const LowRankArgs& l) { return l.dtype != MM_F32 && l.M <= kFloatPartRows; }
+size_t part_bytes(const LowRankArgs& l, int64_t N) {
+  return float_part(l) ? align256((size_t)l.M * (size_t)N * sizeof(float)) : 0;
+}
+size_t lowrank_bytes(const LowRankPlan& p) { return lowrank_base_bytes(p) + part_bytes(p.l, p.N); }
+size_t lowrank_grad_bytes(const LowRankPlan& p) { return lowrank_grad_base_bytes(p) + part_bytes(p.l, p.K); }
 
 // Y = x w for dense Y [M, N].
 GemmArgs projection(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t K, const void* w,
@@ -285,15 +292,33 @@ GemmArgs projection(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x
   return g;
 }
 
-// Y += x w where Y already holds the low-rank part.
-mm_status add_projection(GemmArgs g, cudaStream_t st) {
-  // Every kernel of the dense product reads an element of C in the thread
-  // that then writes that element of Y (or before its tile's store).
-  g.c = g.y;
+// Y = x w plus the low-rank part, which an expansion puts at part() before: an
+// fp32 array of the workspace (few rows) or Y itself.
+struct Projection {
+  GemmArgs g;
+  int path;
+  bool f32;
+  void* part() const { return const_cast<void*>(g.c.ptr); }
+  mm_status run(cudaStream_t st) const { return run_dense_on(path, g, st); }
+};
+Projection plan_projection(const LowRankArgs& l, const GemmArgs& g, char* float_array) {
+  Projection p;
   // A long sum over k leaves the CUDA-core tiles waiting even where the work is
   // small: 4 rows of 512 x 512 take 17 us there and 8 us on the tensor cores.
   const bool long_k = g.dtype != MM_F32 && g.K >= 256;
-  return run_dense(g, long_k || tensor_pays_dense(g.dtype, g.M, g.N, g.K, 1), st);
+  p.g = g;
+  // Every kernel of the dense product reads an element of C in the thread
+  // that then writes that element of Y (or before its tile's store).
+  p.g.c = g.y;
+  p.f32 = false;
+  p.path = dense_path(p.g, long_k || tensor_pays_dense(g.dtype, g.M, g.N, g.K, 1), float_part(l) ? &p.f32 : nullptr);
+  if (p.f32) {
+    p.g.c.ptr = float_array;
+    p.g.c.rs = 2 * g.N;
+    p.g.c.cs = 2;
+    p.g.c_f32 = 1;
+  }
+  return p;
 }
 
 // Whether a 16-bit product may take the fused kernel (the dense products' rules).
@@ -332,15 +357,19 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
   float* z = static_cast<float*>(workspace);
   const GemmArgs g = projection(l, X->data, X->strides[0], X->strides[1], p.K, W->data, W->strides[0], W->strides[1], p.N,
                                 Y->data);
-  const LowRankFew f = {X->data, X->strides[0], X->strides[1], p.K, A->data, A->strides[0], A->strides[1], A->strides[2],
-                        B->data, B->strides[0], B->strides[1], B->strides[2], p.N, Y->data};
+  char* float_array = static_cast<char*>(workspace) + lowrank_base_bytes(p);
+  LowRankFew f = {X->data, X->strides[0], X->strides[1], p.K, A->data, A->strides[0], A->strides[1], A->strides[2],
+                  B->data, B->strides[0], B->strides[1], B->strides[2], p.N, nullptr, 0};
   if (path_policy() != MM_PATH_SIMT && lowrank_few_supported(l, f)) {
+    Projection late = plan_projection(l, g, float_array);
+    if (late.path < 0) return MM_ERR_UNSUPPORTED;
+    f.y = late.part();
+    f.y_f32 = late.f32;
     if ((s = launch_lowrank_few(l, f, z, st)) != MM_OK) return s;
     // The expansion lets the product start while it runs; the first of the two
     // launches waited for all earlier work, X and W included.
-    GemmArgs late = g;
-    late.c_late = 1;
-    return add_projection(late, st);
+    late.g.c_late = 1;
+    return late.run(st);
   }
   if (many_rows(l) && p.K >= 1 &&
       lowrank_shrink_tiles_supported(l, X->data, X->strides[0], X->strides[1], p.K, A->strides[1], A->strides[2]) &&
@@ -359,10 +388,11 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
   if ((s = launch_lowrank_shrink(l, X->data, X->strides[0], X->strides[1], p.K, A->data, A->strides[0], A->strides[1],
                                  A->strides[2], z, st)) != MM_OK)
     return s;
-  if ((s = launch_lowrank_expand(l, z, l.R, B->data, B->strides[0], B->strides[1], B->strides[2], p.N, Y->data, st)) !=
-      MM_OK)
+  const Projection rest = plan_projection(l, g, float_array);
+  if ((s = launch_lowrank_expand(l, z, l.R, B->data, B->strides[0], B->strides[1], B->strides[2], p.N, rest.part(),
+                                 rest.f32, st)) != MM_OK)
     return s;
-  return add_projection(g, st);
+  return rest.run(st);
 }
 
 mm_status mm_lowrank_matmul_grad_workspace_size(const mm_tensor* X, const mm_tensor* W, const mm_tensor* A,
@@ -397,6 +427,7 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* v = static_cast<float*>(workspace);
   float* u = reinterpret_cast<float*>(static_cast<char*>(workspace) + factor_bytes(l));
+  char* float_array = static_cast<char*>(workspace) + lowrank_grad_base_bytes(p);
   s = finish(MM_OK, MM_PATH_NONE);
   if (many_rows(l) && K >= 1 && N >= 1 &&
       lowrank_shrink_tiles_supported(l, dY->data, dY->strides[0], dY->strides[1], N, B->strides[2], B->strides[1]) &&
@@ -432,8 +463,10 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
       s = finish(launch_lowrank_finish(l, fuse ? &u : nullptr, &t, o, problems, z_ld, st),
                  fuse ? MM_PATH_TENSOR : MM_PATH_SIMT);
     if (s == MM_OK && dX && !fuse) {
-      s = launch_lowrank_expand(l, zv, z_ld, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
-      if (s == MM_OK) s = add_projection(g, st);
+      const Projection rest = plan_projection(l, g, float_array);
+      s = launch_lowrank_expand(l, zv, z_ld, A->data, A->strides[0], A->strides[2], A->strides[1], K, rest.part(), rest.f32,
+                                st);
+      if (s == MM_OK) s = rest.run(st);
     }
     return s;
   }
@@ -448,10 +481,10 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
   if (s == MM_OK && dB)
     s = launch_lowrank_outer(l, dY->data, dY->strides[0], dY->strides[1], N, u, dB->data, l.R * N, 1, N, st);
   if (s == MM_OK && dX && l.M > 0 && K > 0) {
-    s = launch_lowrank_expand(l, v, l.R, A->data, A->strides[0], A->strides[2], A->strides[1], K, dX->data, st);
-    if (s == MM_OK)
-      s = add_projection(projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1],
-                                    W->strides[0], K, dX->data), st);
+    const Projection rest = plan_projection(l, projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data,
+                                                          W->strides[1], W->strides[0], K, dX->data), float_array);
+    s = launch_lowrank_expand(l, v, l.R, A->data, A->strides[0], A->strides[2], A->strides[1], K, rest.part(), rest.f32, st);
+    if (s == MM_OK) s = rest.run(st);
   }
   return s;
 }

@@ -23,6 +23,9 @@ struct GemmArgs {
   // were complete before that launch began: a few-row kernel may then read A
   // and B at once and wait for the previous launch only before its epilogue.
   int c_late;
+  // 16-bit types: C holds fp32 values (c.rs, c.cs and the batch strides count
+  // 16-bit units all the same).  Not every kernel takes it (dense_path).
+  int c_f32;
   // Integer types with a non-integral alpha or beta: y = trunc(alpha*acc + beta*c)
   // evaluated in fp64 (each product, then the sum, rounded once), saturated to T.
   int int_float;
@@ -112,9 +115,9 @@ mm_status launch_simt_moe(const MoeArgs& args, float* h, unsigned* status, cudaS
 mm_status launch_lowrank_shrink(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
                                 const void* a, int64_t a_gs, int64_t a_cs, int64_t a_rs, float* z,
                                 cudaStream_t stream);
-// y[m, n] = sum_r z[m, r] b[g, r, n], rounded to T (dense rows of N; rows of z z_ld apart).
+// y[m, n] = sum_r z[m, r] b[g, r, n] (dense rows of N; rows of z z_ld apart), rounded to T or fp32 (y_f32).
 mm_status launch_lowrank_expand(const LowRankArgs& l, const float* z, int64_t z_ld, const void* b, int64_t b_gs,
-                                int64_t b_rs, int64_t b_ns, int64_t N, void* y, cudaStream_t stream);
+                                int64_t b_rs, int64_t b_ns, int64_t N, void* y, int y_f32, cudaStream_t stream);
 // out[g, c, r] = sum over the rows m of adapter g of x[m, c] z[m, r] (element strides of out given).
 mm_status launch_lowrank_outer(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
                                const float* z, void* out, int64_t o_gs, int64_t o_cs, int64_t o_rs,
@@ -144,8 +147,15 @@ struct LowRankFew {
   const void* a; int64_t a_gs, a_cs, a_rs;     // [G, C, R]
   const void* b; int64_t b_gs, b_rs, b_ns;     // [G, R, N]
   int64_t N;
-  void* y;                                     // dense [M, N]
+  void* y;                                     // dense [M, N]: T, or fp32
+  int y_f32;
 };
+// Up to kFloatPartRows rows (those of the few-row products, which take C in
+// fp32) the low-rank part joins the projection unrounded, from an fp32 [M, N]
+// array; above, that array would outweigh the adapters, and the part is rounded
+// to T in Y.  Rounded and not: one row of 4096 x 4096, rank 16, 11.2 and 11.5 us;
+// 61 rows of 4096 x 14336, rank 32, 42.9 and 42.4 us.
+constexpr int64_t kFloatPartRows = 64;
 bool lowrank_few_supported(const LowRankArgs& l, const LowRankFew& f);
 size_t lowrank_few_bytes(const LowRankArgs& l);
 mm_status launch_lowrank_few(const LowRankArgs& l, const LowRankFew& f, float* zp, cudaStream_t stream);

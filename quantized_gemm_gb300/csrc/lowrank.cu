@@ -6,7 +6,8 @@
 //   expand   y[m, n]      = sum_r z[m, r] b[g, r, n]
 //   outer    out[g, c, r] = sum over the rows m of adapter g of x[m, c] z[m, r]
 //
-// z stays fp32; every sum is fp32 in a fixed order.
+// z stays fp32; every sum is fp32 in a fixed order.  The expansion's y is T in Y
+// itself or, for few rows, an fp32 array (kFloatPartRows, kernels.h).
 #include "kernels.h"
 
 namespace qg {
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(256)
 template <typename T>
 __global__ void __launch_bounds__(256)
     expand_kernel(const LowRankArgs l, const float* z, int64_t z_ld, const T* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
-                  int64_t N, T* y) {
+                  int64_t N, T* y, int y_f32) {
   pdl_begin();
   const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (n >= N) return;
@@ -78,7 +79,8 @@ __global__ void __launch_bounds__(256)
       const T* bg = b + g * b_gs + n * b_ns;
       for (int64_t r = 0; r < l.R; ++r) v = __fmaf_rn(z[m * z_ld + r], to_f32(bg[r * b_rs]), v);
     }
-    y[m * N + n] = from_f32<T>(v);
+    if (y_f32) reinterpret_cast<float*>(y)[m * N + n] = v;
+    else y[m * N + n] = from_f32<T>(v);
   }
 }
 
@@ -220,7 +222,7 @@ constexpr int kExpandMaxR = 1024;
 template <typename T, bool NC>
 __global__ void __launch_bounds__(kFewThreads)
     expand_rows_kernel(const LowRankArgs l, const float* zp, const T* b, int64_t b_gs, int64_t b_ld, int64_t N, T* y,
-                       int yvec) {
+                       int yvec, int y_f32) {
   pdl_trigger();
   __shared__ float zs[kExpandMaxR];
   const int64_t m = blockIdx.y;
@@ -261,6 +263,12 @@ __global__ void __launch_bounds__(kFewThreads)
         for (int j = 0; j < 8; ++j) acc[j] = __fmaf_rn(zs[r0 + i], f[j], acc[j]);
       }
     }
+    if (y_f32) {                                               // N is a multiple of 8
+      float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(y) + m * N + n8);
+      to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      return;
+    }
     uint4 o;
     T* e = reinterpret_cast<T*>(&o);
 #pragma unroll
@@ -286,7 +294,8 @@ __global__ void __launch_bounds__(kFewThreads)
           for (int j = 0; j < 8; ++j) acc = __fmaf_rn(zs[r0 + j], f[j], acc);
         }
       }
-      yr[n] = from_f32<T>(acc);
+      if (y_f32) reinterpret_cast<float*>(y)[m * N + n] = acc;
+      else yr[n] = from_f32<T>(acc);
     }
   }
 }
@@ -336,10 +345,10 @@ mm_status shrink_typed(const LowRankArgs& l, const void* x, int64_t x_rs, int64_
 
 template <typename T>
 mm_status expand_typed(const LowRankArgs& l, const float* z, int64_t z_ld, const void* b, int64_t b_gs, int64_t b_rs, int64_t b_ns,
-                       int64_t N, void* y, cudaStream_t stream) {
+                       int64_t N, void* y, int y_f32, cudaStream_t stream) {
   const dim3 grid((unsigned)((N + 255) / 256), rows_y(l.M));
   return launch_pdl(expand_kernel<T>, grid, dim3(256), 0, stream, l, z, z_ld, static_cast<const T*>(b), b_gs, b_rs, b_ns, N,
-                    static_cast<T*>(y)) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+                    static_cast<T*>(y), y_f32) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
 template <typename T>
@@ -369,10 +378,10 @@ mm_status few_typed(const LowRankArgs& l, const LowRankFew& f, float* zp, cudaSt
   const int yvec = f.N % 8 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
   if (f.b_ns == 1)
     e = launch_pdl(expand_rows_kernel<T, true>, ge, dim3(kFewThreads), 0, stream, l, (const float*)zp, b, f.b_gs, f.b_rs,
-                   f.N, y, yvec);
+                   f.N, y, yvec, f.y_f32);
   else
     e = launch_pdl(expand_rows_kernel<T, false>, ge, dim3(kFewThreads), 0, stream, l, (const float*)zp, b, f.b_gs, f.b_ns,
-                   f.N, y, yvec);
+                   f.N, y, yvec, f.y_f32);
   return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
@@ -412,9 +421,9 @@ mm_status launch_lowrank_shrink(const LowRankArgs& l, const void* x, int64_t x_r
 }
 
 mm_status launch_lowrank_expand(const LowRankArgs& l, const float* z, int64_t z_ld, const void* b, int64_t b_gs,
-                                int64_t b_rs, int64_t b_ns, int64_t N, void* y, cudaStream_t stream) {
+                                int64_t b_rs, int64_t b_ns, int64_t N, void* y, int y_f32, cudaStream_t stream) {
   if (l.M == 0 || N == 0) return MM_OK;
-  QG_BY_TYPE(expand_typed, z, z_ld, b, b_gs, b_rs, b_ns, N, y, stream)
+  QG_BY_TYPE(expand_typed, z, z_ld, b, b_gs, b_rs, b_ns, N, y, y_f32, stream)
 }
 
 mm_status launch_lowrank_outer(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,

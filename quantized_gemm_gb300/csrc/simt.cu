@@ -80,7 +80,7 @@ template <typename T> struct Epi {
   using acc = typename Arith<T>::acc;
   static __device__ __forceinline__ acc apply(const GemmArgs& p, acc v, const T* c) {
     acc r = (acc)p.alpha * v;
-    if (c) r = __fmaf_rn(p.beta, Arith<T>::load(c), r);
+    if (c) r = __fmaf_rn(p.beta, sizeof(T) == 2 && p.c_f32 ? *reinterpret_cast<const float*>(c) : Arith<T>::load(c), r);
     return r;
   }
 };

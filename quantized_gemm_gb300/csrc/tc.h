@@ -11,6 +11,8 @@ namespace qg {
 void tc_set_wait_limit_ns(unsigned long long ns);
 
 bool tc_gemm_supported(const GemmArgs& g);
+// Whether launch_tc_gemm takes the few-row configuration (which takes a c_f32 call).
+bool tc_gemm_few_rows(const GemmArgs& g);
 mm_status launch_tc_gemm(const GemmArgs& g, unsigned* status, cudaStream_t stream);
 
 bool tc_qlinear_supported(const QLinearArgs& q);

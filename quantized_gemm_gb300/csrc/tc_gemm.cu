@@ -1248,9 +1248,20 @@ __device__ void run_skinny_reduce(const TcParams& p, uint32_t part) {
       v[4] += f1.x; v[5] += f1.y; v[6] += f1.z; v[7] += f1.w;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = p.alpha * v[j];
-      if (cbase && n + j < p.N) v[j] = __fmaf_rn(p.beta, unpack16(cbase[m * p.c_rs + (n + j) * p.c_cs], p.out_f16), v[j]);
+    for (int j = 0; j < 8; ++j) v[j] = p.alpha * v[j];
+    if (p.c_f32 && p.c_vec && n + 8 <= p.N) {
+      const float4* c = reinterpret_cast<const float4*>(cbase + m * p.c_rs + n * p.c_cs);
+      const float4 c0 = c[0], c1 = c[1];
+      const float cv[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(p.beta, cv[j], v[j]);
+    } else if (cbase) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint16_t* c = cbase + m * p.c_rs + (n + j) * p.c_cs;
+        if (n + j < p.N)
+          v[j] = __fmaf_rn(p.beta, p.c_f32 ? *reinterpret_cast<const float*>(c) : unpack16(*c, p.out_f16), v[j]);
+      }
     }
     uint16_t* yrow = ybase + m * p.y_rs;
     const uint4 w = make_uint4(pack2(v[0], v[1], p.out_f16), pack2(v[2], v[3], p.out_f16),
@@ -1790,6 +1801,23 @@ bool tc_gemm_supported(const GemmArgs& g) {
   return plan_dense(g, false, &a, &b);
 }
 
+// A few rows (at most 64, K-major A) against fewer 256-column tiles than
+// SMs: the few-row configuration splits each tile's k-blocks over a cluster
+// so that every SM streams B'.
+static bool plan_few_rows(const GemmArgs& g, OperandPlan* a, OperandPlan* b) {
+  if (g.dtype == MM_F32 || g.M > BM / 2 || ((g.N + BN - 1) / BN) * g.bm.count >= sm_count()) return false;
+  const int64_t vec = 8;
+  const int64_t a_rs = (g.M == 1 && g.a.cs == 1) ? (g.K + vec - 1) / vec * vec : g.a.rs;
+  return g.N >= 2 && g.y.cs == 1 &&
+         plan_operand(g.a.ptr, g.dtype, g.M, g.K, a_rs, g.a.cs, g.bm, g.a.bstride, BM / 2, a) && !a->mn_major &&
+         plan_operand(g.b.ptr, g.dtype, g.N, g.K, g.b.cs, g.b.rs, g.bm, g.b.bstride, BN, b);
+}
+
+bool tc_gemm_few_rows(const GemmArgs& g) {
+  OperandPlan a, b;
+  return plan_few_rows(g, &a, &b);
+}
+
 mm_status launch_tc_gemm(const GemmArgs& g, unsigned* status, cudaStream_t stream) {
   if (!status) return MM_ERR_UNSUPPORTED;
   TcParams p;
@@ -1814,21 +1842,16 @@ mm_status launch_tc_gemm(const GemmArgs& g, unsigned* status, cudaStream_t strea
     for (int d = 0; d < g.bm.nb; ++d) p.c_vec = p.c_vec && (g.c.bstride[d] % vec == 0);
   }
   p.status = status;
-  // A few rows (at most 64, K-major A) against fewer 256-column tiles than
-  // SMs: the few-row configuration splits each tile's k-blocks over a cluster
-  // so that every SM streams B'.
-  if (!p.out_f32 && g.M <= BM / 2 && ((g.N + BN - 1) / BN) * g.bm.count < sm_count()) {
-    OperandPlan a, b;
-    const int64_t vec = 8;
-    const int64_t a_rs = (g.M == 1 && g.a.cs == 1) ? (g.K + vec - 1) / vec * vec : g.a.rs;
-    if (g.N >= 2 && g.y.cs == 1 &&
-        plan_operand(g.a.ptr, g.dtype, g.M, g.K, a_rs, g.a.cs, g.bm, g.a.bstride, BM / 2, &a) && !a.mn_major &&
-        plan_operand(g.b.ptr, g.dtype, g.N, g.K, g.b.cs, g.b.rs, g.bm, g.b.bstride, BN, &b)) {
-      p.idesc = make_idesc_mn(p.out_f16, 0, b.mn_major, BM, BN);
-      p.c_late = g.c_late;
-      return launch_tc(kSkinny, false, a, b, p, stream);
-    }
+  OperandPlan few_a, few_b;
+  if (plan_few_rows(g, &few_a, &few_b)) {
+    p.idesc = make_idesc_mn(p.out_f16, 0, few_b.mn_major, BM, BN);
+    p.c_late = g.c_late;
+    p.c_f32 = g.c_f32;
+    if (g.c_f32)                            // 16-byte pieces of its rows
+      p.c_vec = g.c.cs == 2 && g.c.rs % 8 == 0 && g.bm.nb == 0 && reinterpret_cast<uintptr_t>(g.c.ptr) % 16 == 0;
+    return launch_tc(kSkinny, false, few_a, few_b, p, stream);
   }
+  if (g.c_f32) return MM_ERR_UNSUPPORTED;
   // CTA pairs (256-row tiles) for long-K products with more than one row tile;
   // one CTA per tile otherwise, or if no pair can be placed.
   for (int attempt = use_pair(g.M, g.K) ? 0 : 1; attempt < 2; ++attempt) {

@@ -343,6 +343,36 @@ def test_lowrank_rows_past_the_slots_or_the_list_are_rounded_once(M, K, N, R, G,
                   u * np.abs(want) + 2.01 * u * low + (2 * K + R) * EPS32 * (base + low) + 2.0 ** -24)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("layout", ["rows", "columns", "odd"])
+@pytest.mark.parametrize("M", [1, 2, 4, 7, 33, 64])
+def test_lowrank_error_of_few_rows_in_the_mean_is_one_rounding_of_the_output(M, layout, dtype):
+    """Up to 64 rows: the low-rank part is not rounded on its way to the projection (rounded, and as large as the whole,
+    it would add an error of the size of the output's own rounding)."""
+    K, N = (512, 1032) if layout != "odd" else (509, 1031)
+    X, W, A, B, idx, scales, dY = _lowrank_inputs(M, K, N, 16, 6, dtype, 251 + M)
+    B, idx = B * 4, idx.clamp(min=0)
+    if layout == "columns":
+        W, A, B = W.t().contiguous().t(), *(t.transpose(1, 2).contiguous().transpose(1, 2) for t in (A, B))
+    args = [to_np(t) for t in (X, W, A, B, idx, scales)]
+    Y, want = to_np(qg.mm_lowrank_matmul(X, W, A, B, idx, scales)), select.lowrank_matmul(*args)
+    assert _rms(Y - want) <= 1.05 * _rms(_rounded(want, dtype) - want)
+    dX, want = qg.mm_lowrank_matmul_grad(dY, X, W, A, B, idx, scales)[0], select.lowrank_matmul_grad(to_np(dY), *args)[0]
+    assert _rms(to_np(dX) - want) <= 1.05 * _rms(_rounded(want, dtype) - want)
+
+
+@pytest.mark.parametrize("M", [1, 3, 40])
+def test_lowrank_part_past_f16s_range_that_the_projection_brings_back(M):
+    """The low-rank part alone is above f16's largest value, Y = X W plus it is not."""
+    K, N, R = 64, 264, 8
+    X, W, A, B = (torch.zeros(s, dtype=F16, device=DEV) for s in ((M, K), (K, N), (1, K, R), (1, R, N)))
+    X[:, 0], W[0], A[0, 0, 0], B[0, 0] = 256.0, -160.0, 1.0, 300.0          # -40960 and 76800
+    X[:, 1], W[1] = 1.0, torch.arange(N, device=DEV).to(F16)
+    idx = torch.zeros(M, dtype=torch.int32, device=DEV)
+    want = select.lowrank_matmul(*[to_np(t) for t in (X, W, A, B)], np.zeros(M, int))
+    assert (to_np(qg.mm_lowrank_matmul(X, W, A, B, idx)) == _rounded(want, F16)).all()
+
+
 # ------------------------------------------------------------------ streams
 
 
