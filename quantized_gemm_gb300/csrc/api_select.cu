@@ -322,8 +322,8 @@ Projection plan_projection(const LowRankArgs& l, const GemmArgs& g, char* float_
 }
 
 // Whether a 16-bit product may take the fused kernel (the dense products' rules).
-bool fused_pays(const LowRankArgs& l, const GemmArgs& g) {
-  return choose(true, tensor_pays_dense(g.dtype, g.M, g.N, g.K, 1)) == MM_PATH_TENSOR && lowrank_fused_supported(l, g);
+bool fused_pays(const LowRankArgs& l, const GemmArgs& g, LowRankProduct* plan) {
+  return choose(true, tensor_pays_dense(g.dtype, g.M, g.N, g.K, 1)) == MM_PATH_TENSOR && lowrank_fused_supported(l, g, plan);
 }
 
 }  // namespace
@@ -371,17 +371,19 @@ mm_status mm_lowrank_matmul(const mm_tensor* X, const mm_tensor* W, const mm_ten
     late.g.c_late = 1;
     return late.run(st);
   }
+  OperandPlan x_map;
+  LowRankProduct product;
   if (many_rows(l) && p.K >= 1 &&
-      lowrank_shrink_tiles_supported(l, X->data, X->strides[0], X->strides[1], p.K, A->strides[1], A->strides[2]) &&
-      fused_pays(l, g)) {
+      lowrank_shrink_tiles_supported(l, X->data, X->strides[0], X->strides[1], p.K, A->strides[1], A->strides[2], &x_map) &&
+      fused_pays(l, g, &product)) {
     const FusedLayout w = lowrank_fused_layout(l, p.N);
     char* ws = static_cast<char*>(workspace);
     z = reinterpret_cast<float*>(ws + w.z);
     const FusedTables slots = lowrank_fused_tables(w, ws);
-    const LowRankShrink q = {X->data, X->strides[0], p.K, A->data, A->strides[0], A->strides[1], A->strides[2], z,
+    const LowRankShrink q = {&x_map, p.K, A->data, A->strides[0], A->strides[1], A->strides[2], z,
                              slots.wide, nullptr, nullptr};
     s = launch_lowrank_shrink_tiles(l, &q, 1, w.z_ld, &slots, nullptr, st);
-    const LowRankFused u = {g, &w, ws, z, B->data, B->strides[0], B->strides[1], B->strides[2]};
+    const LowRankFused u = {g, &product, &w, ws, z, B->data, B->strides[0], B->strides[1], B->strides[2]};
     if (s == MM_OK) s = launch_lowrank_finish(l, &u, nullptr, nullptr, 0, w.z_ld, st);
     return finish(s, MM_PATH_TENSOR);
   }
@@ -429,9 +431,11 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
   float* u = reinterpret_cast<float*>(static_cast<char*>(workspace) + factor_bytes(l));
   char* float_array = static_cast<char*>(workspace) + lowrank_grad_base_bytes(p);
   s = finish(MM_OK, MM_PATH_NONE);
+  OperandPlan dy_map, x_map;
   if (many_rows(l) && K >= 1 && N >= 1 &&
-      lowrank_shrink_tiles_supported(l, dY->data, dY->strides[0], dY->strides[1], N, B->strides[2], B->strides[1]) &&
-      lowrank_shrink_tiles_supported(l, X->data, X->strides[0], X->strides[1], K, A->strides[1], A->strides[2])) {
+      lowrank_shrink_tiles_supported(l, dY->data, dY->strides[0], dY->strides[1], N, B->strides[2], B->strides[1],
+                                     &dy_map) &&
+      lowrank_shrink_tiles_supported(l, X->data, X->strides[0], X->strides[1], K, A->strides[1], A->strides[2], &x_map)) {
     const GradLayout w = grad_layout(p);
     char* ws = static_cast<char*>(workspace);
     float* zv = reinterpret_cast<float*>(ws + w.fused.z);
@@ -443,10 +447,10 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
     LowRankShrink q[2];
     int factors = 0;
     if (dX || dA)
-      q[factors++] = {dY->data, dY->strides[0], N, B->data, B->strides[0], B->strides[2], B->strides[1],
+      q[factors++] = {&dy_map, N, B->data, B->strides[0], B->strides[2], B->strides[1],
                       dX ? zv : nullptr, dX ? slots.wide : nullptr, dA ? ws + w.vt : nullptr, v_exp};
     if (dB)
-      q[factors++] = {X->data, X->strides[0], K, A->data, A->strides[0], A->strides[1], A->strides[2], nullptr, nullptr,
+      q[factors++] = {&x_map, K, A->data, A->strides[0], A->strides[1], A->strides[2], nullptr, nullptr,
                       ws + w.ut, u_exp};
     if (factors) s = launch_lowrank_shrink_tiles(l, q, factors, z_ld, dX ? &slots : nullptr, dA || dB ? &t : nullptr, st);
     LowRankOuter o[2];
@@ -457,8 +461,9 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
       o[problems++] = {dY->data, dY->strides[0], N, ws + w.ut, u_exp, dB->data, 1, N, reinterpret_cast<float*>(ws + w.sums_b)};
     const GemmArgs g = projection(l, dY->data, dY->strides[0], dY->strides[1], N, W->data, W->strides[1], W->strides[0], K,
                                   dX ? dX->data : nullptr);
-    const bool fuse = dX && fused_pays(l, g);
-    const LowRankFused u = {g, &w.fused, ws, zv, A->data, A->strides[0], A->strides[2], A->strides[1]};
+    LowRankProduct product;
+    const bool fuse = dX && fused_pays(l, g, &product);
+    const LowRankFused u = {g, &product, &w.fused, ws, zv, A->data, A->strides[0], A->strides[2], A->strides[1]};
     if (s == MM_OK && (problems || fuse))
       s = finish(launch_lowrank_finish(l, fuse ? &u : nullptr, &t, o, problems, z_ld, st),
                  fuse ? MM_PATH_TENSOR : MM_PATH_SIMT);

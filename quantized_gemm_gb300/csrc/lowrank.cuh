@@ -72,7 +72,7 @@ struct FusedLayout {
 };
 FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N);
 FusedTables lowrank_fused_tables(const FusedLayout& w, char* ws);
-bool lowrank_fused_supported(const LowRankArgs& l, const GemmArgs& g);
+bool lowrank_fused_supported(const LowRankArgs& l, const GemmArgs& g, LowRankProduct* plan);
 
 // One or two factors, scaled, each as z [M, z_ld] (fp32, zeros past R; for the
 // fused product, with its `wide`) and as zt [M, 2, z_ld] (hi and lo, zeros past
@@ -80,10 +80,11 @@ bool lowrank_fused_supported(const LowRankArgs& l, const GemmArgs& g);
 // by 2^e, e = zt_exp[rank / 64, row], so that its largest value is in [2^14,
 // 2^15).  Rows without adapter are not written.  The same launch makes the
 // fused product's slots and the sorted rows where asked for.
+// `map` receives x's tensor map.
 bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
-                                    int64_t a_cs, int64_t a_rs);
+                                    int64_t a_cs, int64_t a_rs, OperandPlan* map);
 struct LowRankShrink {
-  const void* x; int64_t x_rs, C;
+  const OperandPlan* map; int64_t C;
   const void* a; int64_t a_gs, a_cs, a_rs;
   float* z;
   uint8_t* wide;
@@ -98,6 +99,7 @@ mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const LowRankShrink*
 // aligned rows) and zt; part holds lowrank_max_parts * C * R floats.
 struct LowRankFused {
   GemmArgs product;
+  const LowRankProduct* plan;
   const FusedLayout* layout;
   char* ws;
   const float* z;

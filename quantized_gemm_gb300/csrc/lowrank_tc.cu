@@ -957,7 +957,6 @@ mm_status shrink_launch(const LowRankArgs& l, const LowRankShrink* q, int proble
   TcParams limits;                      // the pipelines' wait limits
   init_params(&limits);
   ShrinkArgs p[2];
-  OperandPlan map[2];
   const int rc = (int)(l.R < 64 ? l.R : 64);
   int smem = 0;
   for (int i = 0; i < 2; ++i) {
@@ -972,7 +971,6 @@ mm_status shrink_launch(const LowRankArgs& l, const LowRankShrink* q, int proble
       a.per >>= 1;
     a.z = s.z; a.z_ld = z_ld; a.wide = s.wide; a.zt = s.zt; a.zt_exp = s.zt_exp;
     a.timeout_ns = limits.timeout_ns; a.teardown_ns = limits.teardown_ns;
-    if (!shrink_map(l, s.x, s.x_rs, s.C, &map[i])) return MM_ERR_UNSUPPORTED;
     const int need = shrink_smem(a.ck, rc);
     if (smem < need) smem = need;
   }
@@ -989,18 +987,17 @@ mm_status shrink_launch(const LowRankArgs& l, const LowRankShrink* q, int proble
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024) != cudaSuccess)
     return MM_ERR_CUDA;
   return launch_pdl(kernel, dim3((unsigned)blocks, (unsigned)ranks), dim3(kShThreads), (size_t)smem, stream,
-                    map[0].map, map[1].map, l, p[0], p[1], (int)tiles, problems, (int)parts, slots ? *slots : FusedTables{},
+                    q[0].map->map, q[problems - 1].map->map, l, p[0], p[1], (int)tiles, problems, (int)parts, slots ? *slots : FusedTables{},
                     sort ? *sort : AdapterRows{}) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
 }  // namespace
 
 bool lowrank_shrink_tiles_supported(const LowRankArgs& l, const void* x, int64_t x_rs, int64_t x_cs, int64_t C,
-                                    int64_t a_cs, int64_t a_rs) {
-  OperandPlan map;
+                                    int64_t a_cs, int64_t a_rs, OperandPlan* map) {
   return (l.dtype == MM_BF16 || l.dtype == MM_F16) && l.M >= 1 && l.R >= 1 && l.G >= 1 && l.G <= 0x7fffffffLL && C >= 1 &&
          l.M <= 0x7fffffffLL && l.R <= 64 * 65535LL && rows16(x, x_rs, x_cs, l.M) && (a_rs == 1 || a_cs == 1) &&
-         shrink_map(l, x, x_rs, C, &map);
+         shrink_map(l, x, x_rs, C, map);
 }
 
 mm_status launch_lowrank_shrink_tiles(const LowRankArgs& l, const LowRankShrink* p, int problems, int64_t z_ld,
@@ -1056,9 +1053,9 @@ FusedLayout lowrank_fused_layout(const LowRankArgs& l, int64_t N) {
   return w;
 }
 
-bool lowrank_fused_supported(const LowRankArgs& l, const GemmArgs& g) {
+bool lowrank_fused_supported(const LowRankArgs& l, const GemmArgs& g, LowRankProduct* plan) {
   return (l.dtype == MM_BF16 || l.dtype == MM_F16) && l.M >= 1 && l.R >= 1 && l.R <= 4096 && l.G >= 1 && l.G <= 65536 &&
-         l.M * per_tile(l) < (1ll << 30) && tc_lowrank_tile_rows(g) != 0;
+         l.M * per_tile(l) < (1ll << 30) && tc_lowrank_plan(g, plan);
 }
 
 FusedTables lowrank_fused_tables(const FusedLayout& w, char* ws) {
@@ -1087,12 +1084,12 @@ mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const Adapte
   if (u) {
     const FusedLayout& w = *u->layout;
     f = lowrank_fused_tables(w, u->ws);
-    e.tile_rows = tc_lowrank_tile_rows(u->product);
+    const int tile_rows = u->plan->tile_rows;
     e.factors = u->ws + w.factors; e.factor_ld = w.f_ld; e.per_tile = w.per_tile;
     e.adapters = u->ws + w.copy; e.slots = w.slots; e.k_rows = w.k_rows; e.adapter_ld = w.c_ld;
     e.count = f.ext_count; e.slot = f.ext_slot;
     e.head = f.head; e.row_c = f.row_c;
-    const int64_t N = u->product.N, tiles = (l.M + e.tile_rows - 1) / e.tile_rows, pieces = (w.c_ld + 1023) / 1024;
+    const int64_t N = u->product.N, tiles = (l.M + tile_rows - 1) / tile_rows, pieces = (w.c_ld + 1023) / 1024;
     int64_t parts = 152 / tiles;      // blocks that write one tile's factors: about one per SM in all
     parts = parts < 4 ? 4 : parts > 32 ? 32 : parts;
     const int64_t blocks = tiles * parts + w.slots * pieces;
@@ -1100,7 +1097,7 @@ mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const Adapte
     // 16-byte reads of b along n (1) or along the ranks (2)
     const bool base = (l.G == 1 || u->b_gs % 8 == 0) && reinterpret_cast<uintptr_t>(u->b) % 16 == 0;
     place.blocks = (int)blocks;
-    place.tile_rows = e.tile_rows; place.tiles = (int)tiles; place.per_tile = (int)w.per_tile; place.parts = (int)parts;
+    place.tile_rows = tile_rows; place.tiles = (int)tiles; place.per_tile = (int)w.per_tile; place.parts = (int)parts;
     place.z = u->z; place.z_ld = w.z_ld; place.two = w.two; place.k_rows = w.k_rows;
     place.factors = reinterpret_cast<T*>(u->ws + w.factors); place.f_ld = w.f_ld;
     place.b = static_cast<const T*>(u->b);
@@ -1140,7 +1137,7 @@ mm_status finish_typed(const LowRankArgs& l, const LowRankFused* u, const Adapte
   if (launch_pdl(lowrank_sums_kernel<T>, dim3((unsigned)last), dim3(256), 0, stream, l, f, fix, rows, p[0], p[1],
                  (int)(sum_blocks > 0 ? sum_blocks : 1)) != cudaSuccess)
     return MM_ERR_CUDA;
-  return u ? launch_tc_lowrank(u->product, e, l.status, stream) : MM_OK;
+  return u ? launch_tc_lowrank(u->product, *u->plan, e, l.status, stream) : MM_OK;
 }
 
 }  // namespace

@@ -28,7 +28,6 @@ mm_status launch_tc_grouped(const GroupedArgs& g, void* workspace, unsigned* sta
 // Y = A B (16-bit, no batch) plus, per row tile, the products of the rows'
 // factors with their adapters (device tables as TcParams describes them).
 struct LowRankExt {
-  int tile_rows;                 // tc_lowrank_tile_rows
   const void* factors;           // [row tiles * per_tile * tile_rows, factor_ld], factor_ld a multiple of 64
   int64_t factor_ld, per_tile;   // per_tile: adapters that a tile can list
   const void* adapters;          // [slots, k_rows, adapter_ld], finite, adapter_ld a multiple of 8
@@ -38,8 +37,12 @@ struct LowRankExt {
   const int32_t* head;           // [1]: whether any row's Y holds a part to add
   const int32_t* row_c;          // [M] (read when it does): rows whose Y does
 };
-int tc_lowrank_tile_rows(const GemmArgs& g);
-mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* status, cudaStream_t stream);
+// The product's row tiles (256 rows: CTA pairs, 128: single CTAs) and operands,
+// planned once per call; false where it does not fit the kernel.
+struct LowRankProduct;
+bool tc_lowrank_plan(const GemmArgs& g, LowRankProduct* plan);
+mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankProduct& plan, const LowRankExt& e, unsigned* status,
+                            cudaStream_t stream);
 
 // The mixture-of-experts layer for a few tokens (moe_tc.cu): every matrix with
 // 16-byte aligned rows along a unit-stride matrix dimension, w_gate and w_up

@@ -1875,19 +1875,18 @@ mm_status launch_tc_gemm(const GemmArgs& g, unsigned* status, cudaStream_t strea
 
 // ------------------------------------------------------------------ dense product with per-row adapters
 
-// Rows of the row tiles (256: CTA pairs, 128: single CTAs), 0 where the
-// product does not fit the kernel.
-int tc_lowrank_tile_rows(const GemmArgs& g) {
-  OperandPlan a, b;
-  if (g.dtype == MM_F32 || g.bm.nb != 0) return 0;
+bool tc_lowrank_plan(const GemmArgs& g, LowRankProduct* plan) {
+  if (g.dtype == MM_F32 || g.bm.nb != 0) return false;
   const bool pair = use_pair(g.M, g.K) && max_pair_clusters<kLowRank>() > 0;
-  if (!plan_dense(g, pair, &a, &b)) return 0;
-  return pair ? 2 * BM : BM;
+  plan->tile_rows = pair ? 2 * BM : BM;
+  return plan_dense(g, pair, &plan->a, &plan->b);
 }
 
-mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* status, cudaStream_t stream) {
+mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankProduct& plan, const LowRankExt& e, unsigned* status,
+                            cudaStream_t stream) {
   if (!status) return MM_ERR_CUDA;
-  const bool pair = e.tile_rows == 2 * BM;
+  const bool pair = plan.tile_rows == 2 * BM;
+  const OperandPlan &a = plan.a, &b = plan.b;
   TcParams p;
   init_params(&p);
   p.M = g.M; p.N = g.N; p.K = g.K;
@@ -1897,12 +1896,11 @@ mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankExt& e, unsigned* st
   p.y_rs = g.y.rs;
   p.y_vec = (reinterpret_cast<uintptr_t>(g.y.ptr) % 16 == 0) && (g.y.rs % 8 == 0);
   p.status = status;
-  OperandPlan a, b, z, w;
-  if (!plan_dense(g, pair, &a, &b)) return MM_ERR_UNSUPPORTED;
+  OperandPlan z, w;
   BatchMap one = g.bm;
   const int64_t none[kMaxBatchDims] = {};
-  const int64_t tiles = (g.M + e.tile_rows - 1) / e.tile_rows;
-  if (!plan_operand(e.factors, g.dtype, tiles * e.per_tile * e.tile_rows, e.factor_ld, e.factor_ld, 1, one, none, BM, &z) ||
+  const int64_t tiles = (g.M + plan.tile_rows - 1) / plan.tile_rows;
+  if (!plan_operand(e.factors, g.dtype, tiles * e.per_tile * plan.tile_rows, e.factor_ld, e.factor_ld, 1, one, none, BM, &z) ||
       z.mn_major)
     return MM_ERR_UNSUPPORTED;
   BatchMap slots = g.bm;

@@ -105,6 +105,11 @@ struct OperandPlan {
   int64_t bc[kMaxBatchDims];
 };
 
+struct LowRankProduct {
+  int tile_rows;
+  OperandPlan a, b;
+};
+
 bool plan_operand(const void* ptr, int dtype, int64_t mn_len, int64_t k_len, int64_t mn_stride, int64_t k_stride,
                   const BatchMap& bm, const int64_t* bstride, int box_mn, OperandPlan* out, int box_batch = 1);
 // A plain (unswizzled) 3-D tensor map over elements of elem_bytes bytes:
