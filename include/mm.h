@@ -294,8 +294,9 @@ mm_status mm_grouped_matmul_noalloc(const mm_tensor* input, const mm_tensor* wei
  * part in the softmax; a row with fewer than k others gets index -1 and
  * weight 0 in the remaining places.  A maximum of +inf takes the limit: the
  * +inf logits share the row equally.
- *   indices: dense [T,k] MM_I32 (as mm_grouped_matmul and mm_moe_layer take
- *   them); weights: dense [T,k] MM_F32.  1 <= k <= min(G, 32) (else
+ *   indices: dense [T,k] MM_I32, as mm_moe_layer takes them (mm_grouped_matmul
+ *   takes them too where no pick is missing: it records a -1 as
+ *   MM_ERR_INDEX_RANGE); weights: dense [T,k] MM_F32, rounded quotients.  1 <= k <= min(G, 32) (else
  *   MM_ERR_SHAPE) and G <= 1024 (else MM_ERR_UNSUPPORTED). */
 mm_status mm_route_topk(const mm_tensor* logits, int32_t normalize, const mm_tensor* indices,
                         const mm_tensor* weights, void* stream);

@@ -419,3 +419,21 @@ def test_outputs_of_a_call_on_another_stream_are_not_memory_still_in_use(call):
         assert torch.equal(a, b)
     for t in got:                                        # and the outputs are good for the current stream's work
         t.add_(1)
+
+
+# ------------------------------------------------------------------ the profiles' command
+
+
+@pytest.mark.parametrize("workload", ["operator_route_decode", "operator_moe_small_g8", "operator_lowrank_grad_ragged"])
+def test_the_profiles_command_runs(workload):
+    import json
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "bench.py"), "--profile-workload", workload, "--steps", "2",
+                        "--warmup", "3"], capture_output=True, text=True, cwd=root)
+    assert r.returncode == 0, r.stderr
+    line = json.loads(r.stdout.strip().splitlines()[-1])
+    assert line["profile_workload"] == workload and line["status"] == "MM_OK"
