@@ -384,6 +384,8 @@ def mm_route_topk(logits, k, normalize=1, indices=None, weights=None, stream=Non
     lib = _LIB or _lib()
     if indices is None:
         indices = _empty((logits.shape[0], k), torch.int32, logits, stream)
+    elif indices.shape[-1] != k:
+        raise ValueError("indices for %d picks, k is %d" % (indices.shape[-1], k))
     if weights is None:
         weights = _empty((logits.shape[0], k), torch.float32, logits, stream)
     status = lib.mm_route_topk(_ref(_desc(logits)), int(normalize), _ref(_desc(indices)), _ref(_desc(weights)),
