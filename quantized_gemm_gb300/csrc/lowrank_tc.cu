@@ -616,6 +616,8 @@ __device__ void outer_tile(const LowRankArgs& l, const AdapterRows& t, const Out
     }
   }
   const bool whole = end - begin <= kChunkRows;
+  static_assert(kOutC == 128 && kOutThreads == 256, "a thread's 8 x 4 values are bits of `again`");
+  uint32_t again = 0u;
   float* mine = p.part + (int64_t)(first_part(begin) + chunk) * C * l.R;
   T* out = p.out + (int64_t)g * C * l.R;
 #pragma unroll
@@ -627,9 +629,33 @@ __device__ void outer_tile(const LowRankArgs& l, const AdapterRows& t, const Out
       const int r = r0 + j * 8 + (lane & 3) * 2 + (e & 1);
       if (c >= C || r >= l.R) continue;
       const float v = kScaled ? times_pow2(acc[j][e], E) : acc[j][e];
+      if (isnan(v)) again |= 1u << (j * 4 + e);
       if (whole) out[c * p.o_cs + r * p.o_rs] = from_f32<T>(v);
       else mine[c * p.o_cs + r * p.o_rs] = v;
     }
+  }
+  // An infinite x makes hi's product infinite and lo's infinite of either sign
+  // or, where lo is 0, NaN: such a value once more, from the sum of the parts.
+  // Only NaN results come here.
+#pragma unroll 1
+  for (; again; again &= again - 1) {
+    const int at = __ffs(again) - 1, j = at >> 2, e = at & 3;
+    const int64_t c = c0 + warp * 16 + (lane >> 2) + (e >> 1) * 8;
+    const int r = r0 + j * 8 + (lane & 3) * 2 + (e & 1);
+    float v = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int64_t m = rows[i];
+      const T* zr = p.zt + m * 2 * z_ld + r;
+      float z = to_f32(zr[0]) + to_f32(zr[z_ld]);
+      if constexpr (kScaled) {
+        const int k = __ldcg(p.zt_exp + (int64_t)group * l.M + m);
+        if (k != kExpAny && k != kExpZero) z = times_pow2(z, k);
+      }
+      v = __fmaf_rn(to_f32(p.x[m * p.x_rs + c]), z, v);
+    }
+    if (whole) out[c * p.o_cs + r * p.o_rs] = from_f32<T>(v);
+    else mine[c * p.o_cs + r * p.o_rs] = v;
   }
 }
 

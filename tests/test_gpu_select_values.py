@@ -373,6 +373,35 @@ def test_lowrank_part_past_f16s_range_that_the_projection_brings_back(M):
     assert (to_np(qg.mm_lowrank_matmul(X, W, A, B, idx)) == _rounded(want, F16)).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("R,chunks", [(1, 1), (8, 1), (16, 3), (72, 1)])
+def test_lowrank_gradients_of_infinite_inputs(R, chunks, dtype):
+    """Infinite values of X or dY give dA and dB the infinity or NaN of the formula, whatever parts the factors are held
+    in, and leave the other adapters', columns' and rows' values alone."""
+    M, K, N, G = 300 + 1100 * (chunks - 1), 136, 264, 4
+    X, W, A, B, _, scales, dY = _lowrank_inputs(M, K, N, R, G, dtype, 261)
+    idx = torch.arange(M, device=DEV) % (G + 1) - 1 if chunks == 1 else torch.where(torch.arange(M, device=DEV) < 4, 1, 0)
+    A, B = torch.where(A == 0, 1, A), torch.where(B == 0, 1, B)
+    X[dY.abs().amin(dim=1) == 0], dY[dY == 0] = 1, 1
+    inf = float("inf")
+    for m, c, v in ((6, 3, inf), (6, 9, -inf), (7, 70, inf), (11, 70, -inf), (2, 5, inf)):
+        X[m, c] = v                                             # adapter m % 5 - 1, or chunks' adapter 0
+    for m, c, v in ((8, 100, inf), (13, 100, inf), (18, 101, -inf), (3, 7, -inf)):
+        dY[m, c] = v
+    args = [to_np(t) for t in (dY, X, W, A, B, idx, scales)]
+    got = qg.mm_lowrank_matmul_grad(dY, X, W, A, B, idx, scales)
+    with np.errstate(invalid="ignore"):
+        wants = select.lowrank_matmul_grad(*args)
+    zero = [np.where(np.isfinite(a), a, 0.0) for a in args[:2]] + args[2:]
+    bounds = select.lowrank_matmul_grad_bound(*zero, u=U[dtype])
+    for name, g, want, bound in zip(("dX", "dA", "dB"), got, wants, bounds):
+        g, ok = to_np(g), np.isfinite(want)
+        assert not ok.all(), name
+        assert (np.isnan(g) == np.isnan(want)).all(), name
+        assert (np.isposinf(g) == np.isposinf(want)).all() and (np.isneginf(g) == np.isneginf(want)).all(), name
+        assert (np.abs(np.where(ok, g - np.where(ok, want, 0), 0)) <= bound).all(), name
+
+
 # ------------------------------------------------------------------ streams
 
 
