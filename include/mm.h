@@ -141,7 +141,8 @@ mm_status mm_set_wait_limit_ns(uint64_t ns);
  * never uses plain TF32: small or strided f32 products use FFMA, large ones
  * with a unit-stride matrix dimension per operand use three tf32 tensor-core
  * products (each operand split into tf32 high and low parts; relative error
- * about 3 * 2^-22 per product, within the fp32 bound).  K = 0 gives zeros. */
+ * about 3 * 2^-22 per product, within the fp32 bound; an infinite operand gives
+ * NaN there).  K = 0 gives zeros. */
 mm_status mm_matmul_output_shape(const mm_tensor* A, const mm_tensor* B,
                                  int32_t* out_ndim, int64_t* out_shape /* [MM_MAX_DIMS] */);
 mm_status mm_matmul(const mm_tensor* A, const mm_tensor* B, const mm_tensor* Y, void* stream);
@@ -328,7 +329,9 @@ mm_status mm_route_topk_grad(const mm_tensor* logits, const mm_tensor* indices, 
  * An index of -1 is no pick (mm_route_topk writes it); a token without any
  * pick gets zeros.  Any other index outside [0,G) counts as -1 and is
  * recorded as MM_ERR_INDEX_RANGE.  A token's result depends on its own picks
- * alone, whatever the other tokens or the unpicked experts hold.
+ * alone, whatever the other tokens or the unpicked experts hold.  A token may
+ * name an expert more than once; on the tensor cores that expert's output then
+ * counts once, with the sum of the weights.
  * The layer reads each picked expert's weights once per 128 tokens: it is
  * meant for few tokens; for many, mm_grouped_matmul is the better product.
  * Workspace: mm_moe_layer_workspace_size() bytes. */
