@@ -505,16 +505,17 @@ __device__ __forceinline__ float unpack16(uint16_t x, int f16) {
   return f16 ? __half2float(__ushort_as_half(x)) : __bfloat162float(__ushort_as_bfloat16(x));
 }
 
-// v[j] += beta * C[n + j] for the 32 columns starting at n.  Plain loads, not
-// those of the read-only cache: C may be Y, written by the launch before while
-// this grid waited for it, and then by this grid (kLowRank, and the product
-// beside adapters).
+// v[j] += beta * C[n + j] for the 32 columns starting at n.  The read-only cache
+// is for a C that nothing writes while this grid lives.  Where C is Y (c_live:
+// kLowRank, and the product beside adapters) the launch before has written it
+// while this grid waited, and this grid does: loads from the L2.  (Plain loads
+// for both cost the batched product without C 3 %: 0.400 against 0.385 ms.)
 __device__ __forceinline__ void add_c32(const TcParams& p, const uint16_t* crow, int64_t n, float (&v)[32]) {
   if (p.c_vec && n + 32 <= p.N) {
     const uint4* src = reinterpret_cast<const uint4*>(crow + n);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint4 u = src[q];
+      const uint4 u = p.c_live ? __ldcg(src + q) : __ldg(src + q);
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -1852,6 +1853,7 @@ mm_status launch_tc_gemm(const GemmArgs& g, unsigned* status, cudaStream_t strea
     return launch_tc(kSkinny, false, few_a, few_b, p, stream);
   }
   if (g.c_f32) return MM_ERR_UNSUPPORTED;
+  p.c_live = g.c.ptr == g.y.ptr;
   // CTA pairs (256-row tiles) for long-K products with more than one row tile;
   // one CTA per tile otherwise, or if no pair can be placed.
   for (int attempt = use_pair(g.M, g.K) ? 0 : 1; attempt < 2; ++attempt) {
@@ -1919,6 +1921,7 @@ mm_status launch_tc_lowrank(const GemmArgs& g, const LowRankProduct& plan, const
   p.beta = 1.f;
   p.c_cs = 1;
   p.c_vec = p.y_vec;
+  p.c_live = 1;
   p.ext_kb = (int)((e.k_rows + BK - 1) / BK);
   return launch_tc(kLowRank, pair, a, b, p, stream, &z, &w);
 }

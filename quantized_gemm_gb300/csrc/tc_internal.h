@@ -62,7 +62,7 @@ struct TcParams {
   const void* c;
   int64_t c_bstride[kMaxBatchDims];
   int64_t c_rs, c_cs, c_gs;                    // c_gs: grouped bias row stride per group
-  int c_vec;
+  int c_vec, c_live;                           // c_live: C is Y
   int c_late, c_f32;                           // kSkinny: GemmArgs::c_late, c_f32
   // QLinear epilogue: zero-point correction from the operand sums, then requantisation
   VecView sa, sb, za, zb;
