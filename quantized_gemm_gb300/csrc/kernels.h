@@ -129,7 +129,7 @@ mm_status launch_lowrank_outer(const LowRankArgs& l, const void* x, int64_t x_rs
 // one pass per adapter and row tile; these read each row's own adapter and do
 // not care.  us for rows in random order and in runs, N = K = 4096, rank 16:
 //      M     G    many-row         here
-//    256     8    48   47         42   42
+//    256     8    48   47         40   40
 //    512     8    49   46         52   52
 //    512    32    76   54         52   52
 //   1024    16    73   48         73   73

@@ -95,9 +95,9 @@ __global__ void __launch_bounds__(256)
 // once for four neighbouring rows was slower below 512 rows, and above for
 // rows of different adapters.)
 //
-// 61 rows of 4096 x 14336, rank 32, 48 adapters: 43 us for the three launches,
-// 159 MB (3.7 TB/s): shrink about 10, the expansion 10 under the projection's
-// 29.  One row of 4096 x 4096, rank 16: 11 us (3.0 TB/s), most of it the three
+// 61 rows of 4096 x 14336, rank 32, 48 adapters: 42 us for the three launches,
+// 159 MB (3.8 TB/s): shrink about 11, the expansion 9 under the projection's
+// 27.  One row of 4096 x 4096, rank 16: 12 us (2.9 TB/s), most of it the three
 // launches' latency.
 
 constexpr int kSplit = 8;

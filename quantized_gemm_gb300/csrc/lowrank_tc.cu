@@ -117,8 +117,8 @@ __device__ __forceinline__ void load_block(uint32_t dst, int pitch, const T* src
 // rows.  Their z goes out in fp32 (the fused product's operands are made of it)
 // and, for the adapters' gradients, as two T values (zt).
 //
-// 8192 rows of 4096, rank 16: 21 us for one factor (67 MB, 3.2 TB/s), 36 us for
-// a gradient's two (134 MB, 3.7 TB/s); bound by latency: 256 or 512 blocks of
+// 8192 rows of 4096, rank 16: 18 us for one factor (67 MB, 3.7 TB/s), 32 us for
+// a gradient's two (134 MB, 4.2 TB/s); bound by latency: 256 or 512 blocks of
 // some 12 us on 304 places, and half as many bytes again of adapters out of the
 // L2.  With one block for both adapters of a tile 27 and 41 us; x staged
 // behind block barriers 43 us for one, x straight into the MMA's registers 43
@@ -479,8 +479,8 @@ __global__ void __launch_bounds__(kShThreads, NT <= 4 ? 2 : 1)
 //
 // z comes in two parts, which meet the same fragments of x in one accumulator.
 //
-// dA and dB of 8192 rows, 4096 + 4096 columns, rank 16 (134 MB): bf16 36 us (3.7
-// TB/s), f16 39 us (its rows' scales), 31 us with z rounded once; the row
+// dA and dB of 8192 rows, 4096 + 4096 columns, rank 16 (134 MB): bf16 36 to 39 us
+// (3.7 TB/s), f16 39 us (its rows' scales), 31 us with z rounded once; the row
 // gathering and the fragments' loads per 8 KB of x cost more than its four MMAs
 // a warp.  A row's 256 bytes as one bulk copy took 85 us.
 constexpr int kOutC = 128, kOutRows = 32, kOutStages = 3, kOutThreads = 256;
@@ -946,7 +946,7 @@ __global__ void __launch_bounds__(256, 3)
 }
 
 // After those, and before the fused product: the fix (first blocks; 4 us, its
-// launch, when there is nothing to fix) and the chunks' sums (9 us).
+// launch, when there is nothing to fix) and the chunks' sums (8 us).
 template <typename T>
 __global__ void __launch_bounds__(256)
     lowrank_sums_kernel(const LowRankArgs l, const FusedTables f, const __grid_constant__ FixArgs<T> fix,
