@@ -1,9 +1,11 @@
 /*
  * mm.h -- C ABI of the GB300 (sm_103a) library for the ONNX matrix-product
- * operator family (MatMul, Gemm, QLinearMatMul and GroupedMatMul) and for the
- * language-model operators whose products select their weights per row:
- * top-k routing, the mixture-of-experts layer for a few tokens, and per-row
- * low-rank adapters beside a shared projection.
+ * operator family (MatMul, Gemm, QLinearMatMul and GroupedMatMul), for the
+ * language-model operators whose products select their weights per row
+ * (top-k routing with its balance loss, the mixture-of-experts layer for a few
+ * tokens, and per-row low-rank adapters beside a shared projection), for 8-bit
+ * products with scales per token and channel, and for the orthogonalised update
+ * of stacked weights.
  *
  * Every entry point takes plain pointers and sizes; no C++ or framework type
  * crosses this boundary.  All computation runs in this library's own CUDA
@@ -23,8 +25,8 @@
  * Streams.  `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *   stream).  Calls are asynchronous: the return value reports host-side
  *   validation and launch errors only.  mm_matmul, mm_gemm, mm_qlinear_matmul,
- *   mm_grouped_matmul, and the routing, expert-layer and low-rank calls
- *   enqueue only kernels and asynchronous memsets, so
+ *   mm_grouped_matmul, and the routing, expert-layer, low-rank, 8-bit and
+ *   orthogonalising calls enqueue only kernels and asynchronous memsets, so
  *   once one call has run on the device (it caches per-device properties)
  *   they can be captured in a CUDA graph and replayed.  Device-side conditions (an out-of-range
  *   group index, a pipeline wait that timed out) are recorded in a per-device
@@ -34,8 +36,9 @@
  *   complete (and its memory to be visible) before its first global-memory
  *   access, so stream order is kept for any work before or after a call.
  * Memory.  The library never allocates device memory.  Operators whose fast
- *   path needs scratch space (QLinearMatMul, GroupedMatMul, the
- *   mixture-of-experts layer and the low-rank adapters) take a
+ *   path needs scratch space (QLinearMatMul, GroupedMatMul, the balance loss, the
+ *   mixture-of-experts layer, the low-rank adapters, the 8-bit product and the
+ *   orthogonalised update) take a
  *   caller-provided workspace whose size is given by the matching
  *   *_workspace_size function; the workspace must be 256-byte aligned.
  * Threads.  Entry points may be called from several host threads; calls that
@@ -312,6 +315,32 @@ mm_status mm_route_topk(const mm_tensor* logits, int32_t normalize, const mm_ten
 mm_status mm_route_topk_grad(const mm_tensor* logits, const mm_tensor* indices, const mm_tensor* grad_weights,
                              int32_t normalize, const mm_tensor* grad_logits, void* stream);
 
+/* The balance loss of a router and the picks per expert.  With p the softmax
+ * of a row's logits over the experts that can be picked (-inf and NaN cannot,
+ * +inf takes the limit, as in mm_route_topk), c[g] the number of times that
+ * indices names expert g, C their sum, T' the rows with an expert that can be
+ * picked (a padded row is one of -inf alone) and P[g] = sum_t p[t,g] / T':
+ *   loss = G sum_g (c[g] / C) P[g]         (1 where either is uniform)
+ * logits [T,G] (bf16, f16 or f32), indices [T,k] (MM_I32 or MM_I64, any
+ * strides; -1 is no pick, any other index outside [0,G) is left out and recorded
+ * as MM_ERR_INDEX_RANGE); loss dense [1] MM_F32; counts dense [G+1] MM_I32, c[g]
+ * and in its last place T'; mean_probs dense [G] MM_F32, P.  C = 0 or T' = 0 give
+ * a loss of 0.  exp is off by 2 ulp and 2^-23 |l - max|; sums are fp32, in an order that
+ * depends on the sizes alone.  G <= 1024, T k < 2^31 (else MM_ERR_UNSUPPORTED).
+ * Workspace: mm_route_balance_workspace_size() bytes. */
+mm_status mm_route_balance_workspace_size(const mm_tensor* logits, const mm_tensor* indices, size_t* bytes);
+mm_status mm_route_balance(const mm_tensor* logits, const mm_tensor* indices, const mm_tensor* loss,
+                           const mm_tensor* counts, const mm_tensor* mean_probs, void* workspace,
+                           size_t workspace_bytes, void* stream);
+/* The loss's gradient with respect to the logits (the counts are constants):
+ *   dl[t,j] = grad_loss (G / T') p[t,j] (c[j] / C - sum_g (c[g] / C) p[t,g]) + base[t,j]
+ * counts [G+1] MM_I32 as mm_route_balance leaves them (or their sums over several
+ * ranks), grad_loss one MM_F32 on the device, base [T,G] another gradient of the
+ * logits (NULL = 0) in their type, such as mm_route_topk_grad's; the sum is
+ * rounded once to that type.  A logit that takes no part gets base alone. */
+mm_status mm_route_balance_grad(const mm_tensor* logits, const mm_tensor* counts, const mm_tensor* grad_loss,
+                                const mm_tensor* base /* NULL = 0 */, const mm_tensor* grad_logits, void* stream);
+
 /* ---------------------------------------------------------------- mixture-of-experts layer, few tokens
  * The whole expert layer for the tokens of a decode step:
  *   h[t,s,:] = act(x[t,:] @ w_gate[e]) * (x[t,:] @ w_up[e]),  e = expert_indices[t,s],
@@ -384,6 +413,50 @@ mm_status mm_lowrank_matmul_grad(const mm_tensor* dY, const mm_tensor* X, const 
                                  const mm_tensor* B, const mm_tensor* adapter_indices,
                                  const mm_tensor* scales /* NULL = 1 */, const mm_tensor* dX, const mm_tensor* dA,
                                  const mm_tensor* dB, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- products in 8 bits, scaled per token and channel
+ * The rows of x [M,K] (bf16, f16 or f32, any strides) as int8 with one scale
+ * each: with s[m] = max_k |x[m,k]| / 127 and q[m,k] = round(x[m,k] / s[m]), each
+ * one rounded fp32 operation, ties to even, x ~ q s.  A row of zeros gets s = 0;
+ * a scale that underflows to 0 gives q = 0; where a subnormal scale was rounded
+ * down, q is clamped to [-127, 127].  A row that holds an infinity or NaN gets
+ * the scale NaN and q = 0, so that its products are NaN.
+ * q dense [M,K] MM_I8, scales dense [M] MM_F32.  Activations are quantised per
+ * token with x as it is, weights [K,N] per output channel as their transpose
+ * [N,K], which leaves them in the layout that mm_int8_matmul reads fastest. */
+mm_status mm_quantize_rows(const mm_tensor* x, const mm_tensor* q, const mm_tensor* scales, void* stream);
+/* The product of int8 operands with a scale per row of A (token) and per column
+ * of B (output channel):
+ *   Y[m,n] = T((acc * a_scale[m]) * b_scale[n] + bias[n]),  acc = sum_k A[m,k] B[k,n],
+ * each step rounded in fp32, then once to T.  A [M,K] and B [K,N] MM_I8 with any
+ * strides, a_scale [M] and b_scale [N] MM_F32, bias NULL or [N] of type T, Y
+ * dense [M,N], T one of bf16, f16, f32.  acc is the exact integer while the
+ * partial sums stay below 2^24 in magnitude (any K up to 1024), and an fp32 sum of exact products
+ * where they do not.  K = 0 gives the bias.
+ * The fastest layout has B's columns contiguous along k and 16-byte aligned (a
+ * transposed [N,K] tensor, K a multiple of 16), rows of A likewise.
+ * Workspace: mm_int8_matmul_workspace_size() bytes for an output of out_dtype. */
+mm_status mm_int8_matmul_workspace_size(const mm_tensor* A, const mm_tensor* B, int32_t out_dtype, size_t* bytes);
+mm_status mm_int8_matmul(const mm_tensor* A, const mm_tensor* B, const mm_tensor* a_scale, const mm_tensor* b_scale,
+                         const mm_tensor* bias /* NULL = 0 */, const mm_tensor* Y, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- orthogonalised update
+ * The update of an optimiser that orthogonalises its momentum (Newton-Schulz
+ * iteration).  For each matrix of X [..., M, N] (bf16, f16 or f32, any strides):
+ *   X_0 = X / (|X|_F + eps),
+ *   X_{i+1} = a X_i + (b A + c A A) X_i,  A = X_i X_i^T   (M <= N; else on the other side),
+ *   Y = scale X_steps                                     (dense, X's type),
+ * with coefficients [steps][3] = a, b, c of each step, host memory, read before
+ * the call returns.  0 <= steps <= MM_ORTHO_MAX_STEPS, eps >= 0, all finite (else
+ * MM_ERR_INVALID_ARG).  A matrix of zeros gives zeros for eps > 0 and NaN for eps =
+ * 0; one that holds an infinity or NaN gives NaN, and touches no other.
+ * The norm covers fp32's whole range.  X_i is held in fp32 between the steps.
+ * Workspace: mm_orthogonalize_workspace_size() bytes. */
+#define MM_ORTHO_MAX_STEPS 64
+mm_status mm_orthogonalize_workspace_size(const mm_tensor* X, size_t* bytes);
+mm_status mm_orthogonalize(const mm_tensor* X, int32_t steps, const float* coefficients, float eps, float scale,
+                           const mm_tensor* Y, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- memory-stream measurement
  * Not an operator (the pages have no counterpart): the streaming kernels that

@@ -24,6 +24,8 @@ Each module cites the page and section it follows:
 * ``grouped_matmul``  -- GroupedMatMul - 29 (onnx.ai)
 * ``dequantize_linear`` -- GroupedMatMul - 29, Summary: weight-only quantized
   experts (DequantizeLinear of the weights, then GroupedMatMul)
+* ``layer``           -- 8-bit products with their quantisation, the router's balance
+  loss and the orthogonalised update (formulas in ``include/mm.h``)
 * ``select``          -- top-k routing, the mixture-of-experts layer and per-row
   low-rank adapters, with gradients (formulas in ``include/mm.h``)
 

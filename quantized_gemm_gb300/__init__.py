@@ -26,6 +26,9 @@ __all__ = [
     "mm_route_topk", "mm_route_topk_grad", "mm_moe_layer", "mm_moe_layer_workspace_size",
     "mm_lowrank_matmul", "mm_lowrank_matmul_workspace_size", "mm_lowrank_matmul_grad",
     "mm_lowrank_matmul_grad_workspace_size",
+    "mm_route_balance", "mm_route_balance_workspace_size", "mm_route_balance_grad",
+    "mm_quantize_rows", "mm_int8_matmul", "mm_int8_matmul_workspace_size",
+    "mm_orthogonalize", "mm_orthogonalize_workspace_size",
 ]
 
 MM_MAX_DIMS = 8
@@ -100,6 +103,14 @@ def _lib():
             "mm_lowrank_matmul_workspace_size": ([T, T, T, T, ctypes.POINTER(SZ)], I32),
             "mm_lowrank_matmul": ([T, T, T, T, T, T, T, P, SZ, P], I32),
             "mm_lowrank_matmul_grad_workspace_size": ([T, T, T, T, ctypes.POINTER(SZ)], I32),
+            "mm_route_balance_workspace_size": ([T, T, ctypes.POINTER(SZ)], I32),
+            "mm_route_balance": ([T, T, T, T, T, P, SZ, P], I32),
+            "mm_route_balance_grad": ([T, T, T, T, T, P], I32),
+            "mm_quantize_rows": ([T, T, T, P], I32),
+            "mm_int8_matmul_workspace_size": ([T, T, I32, ctypes.POINTER(SZ)], I32),
+            "mm_int8_matmul": ([T, T, T, T, T, T, P, SZ, P], I32),
+            "mm_orthogonalize_workspace_size": ([T, ctypes.POINTER(SZ)], I32),
+            "mm_orthogonalize": ([T, I32, ctypes.POINTER(F), F, F, T, P, SZ, P], I32),
             "mm_lowrank_matmul_grad": ([T, T, T, T, T, T, T, T, T, T, P, SZ, P], I32),
         }
         for name, (args, res) in sigs.items():
@@ -406,6 +417,43 @@ def mm_route_topk_grad(logits, indices, grad_weights, normalize=1, out=None, str
     return y
 
 
+def mm_route_balance_workspace_size(logits, indices):
+    return _sized(_lib().mm_route_balance_workspace_size, _desc(logits), _desc(indices))
+
+
+def mm_route_balance(logits, indices, loss=None, counts=None, mean_probs=None, stream=None, workspace=None):
+    """The router's balance loss: (loss fp32 [1], counts int32 [G + 1], mean_probs fp32 [G]) with loss = G * sum_g
+    (counts[g] / all picks) * mean_probs[g]; the last place of counts holds the rows that take part (a row of -inf
+    alone is padding)."""
+    lib = _LIB or _lib()
+    G = logits.shape[1]
+    dl, di = _desc(logits), _desc(indices)
+    if loss is None:
+        loss = _empty((1,), torch.float32, logits, stream)
+    if counts is None:
+        counts = _empty((G + 1,), torch.int32, logits, stream)
+    if mean_probs is None:
+        mean_probs = _empty((G,), torch.float32, logits, stream)
+    ws, wsb = _given_or_sized(workspace, logits, stream, lib.mm_route_balance_workspace_size, dl, di)
+    status = lib.mm_route_balance(_ref(dl), _ref(di), _ref(_desc(loss)), _ref(_desc(counts)), _ref(_desc(mean_probs)),
+                                  None if ws is None else ws.data_ptr(), wsb, _stream(logits, stream))
+    if status:
+        raise MMError(status, "mm_route_balance")
+    return loss, counts, mean_probs
+
+
+def mm_route_balance_grad(logits, counts, grad_loss, base=None, out=None, stream=None):
+    """Gradient of mm_route_balance's loss with respect to the logits, times grad_loss (one fp32 value on the device),
+    plus ``base``, another gradient of the logits."""
+    lib = _LIB or _lib()
+    y = _empty(logits.shape, logits.dtype, logits, stream) if out is None else out
+    status = lib.mm_route_balance_grad(_ref(_desc(logits)), _ref(_desc(counts)), _ref(_desc(grad_loss)),
+                                       _ref(_desc(base)), _ref(_desc(y)), _stream(logits, stream))
+    if status:
+        raise MMError(status, "mm_route_balance_grad")
+    return y
+
+
 _ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
 
 
@@ -486,6 +534,83 @@ def mm_lowrank_matmul_grad(dY, X, W, A, B, adapter_indices, scales=None, need=(T
     if status:
         raise MMError(status, "mm_lowrank_matmul_grad")
     return dX, dA, dB
+
+
+def mm_quantize_rows(x, out=None, scales=None, stream=None):
+    """Rows of x [M, K] as int8 with a scale each: (q int8 [M, K], scales fp32 [M]), x ~ q * scales[:, None].  For
+    weights [K, N] pass their transpose: a scale per output channel."""
+    lib = _LIB or _lib()
+    q = _empty(x.shape, torch.int8, x, stream) if out is None else out
+    if scales is None:
+        scales = _empty(x.shape[:1], torch.float32, x, stream)
+    status = lib.mm_quantize_rows(_ref(_desc(x)), _ref(_desc(q)), _ref(_desc(scales)), _stream(x, stream))
+    if status:
+        raise MMError(status, "mm_quantize_rows")
+    return q, scales
+
+
+def _float_type(dtype):
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise TypeError("unsupported dtype %s" % dtype)
+    return dt
+
+
+def mm_int8_matmul_workspace_size(A, B, dtype=torch.bfloat16):
+    nbytes = ctypes.c_size_t()
+    _check(_lib().mm_int8_matmul_workspace_size(_ref(_desc(A)), _ref(_desc(B)), _float_type(dtype), ctypes.byref(nbytes)),
+           "mm_int8_matmul_workspace_size")
+    return nbytes.value
+
+
+def mm_int8_matmul(A, B, a_scale, b_scale, bias=None, dtype=torch.bfloat16, out=None, stream=None, workspace=None):
+    """Product of int8 tensors scaled per row of A and per column of B: Y[m, n] = sum_k A[m, k] B[k, n] * a_scale[m] *
+    b_scale[n] + bias[n], in ``dtype`` (or the type of ``out``).  Weights quantised as [N, K] rows are passed transposed."""
+    lib = _LIB or _lib()
+    dA, dB = _desc(A), _desc(B)
+    y = _empty((A.shape[0], B.shape[1]), dtype, A, stream) if out is None else out
+    dY = _desc(y)
+    if workspace is None:
+        nbytes = ctypes.c_size_t()
+        _check(lib.mm_int8_matmul_workspace_size(_ref(dA), _ref(dB), dY.dtype, ctypes.byref(nbytes)),
+               "mm_int8_matmul_workspace_size")
+        ws, wsb = _workspace(nbytes.value, A, stream)
+    else:
+        ws, wsb = workspace, workspace.numel() * workspace.element_size()
+    status = lib.mm_int8_matmul(_ref(dA), _ref(dB), _ref(_desc(a_scale)), _ref(_desc(b_scale)), _ref(_desc(bias)),
+                                _ref(dY), None if ws is None else ws.data_ptr(), wsb, _stream(A, stream))
+    if status:
+        raise MMError(status, "mm_int8_matmul")
+    return y
+
+
+def mm_orthogonalize_workspace_size(X):
+    return _sized(_lib().mm_orthogonalize_workspace_size, _desc(X))
+
+
+def mm_orthogonalize(X, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=1.0, out=None, stream=None,
+                     workspace=None):
+    """Each matrix of X [..., M, N] divided by its Frobenius norm (plus eps) and driven towards the nearest orthogonal
+    one by ``steps`` of X = a X + (b X X^T + c (X X^T)^2) X, times ``scale``.  ``coefficients`` is one (a, b, c) for all
+    steps, or a sequence of them, one a step."""
+    lib = _LIB or _lib()
+    steps = int(steps)
+    if steps and isinstance(coefficients[0], (tuple, list)):
+        if len(coefficients) != steps:
+            raise ValueError("coefficients for %d steps, steps is %d" % (len(coefficients), steps))
+        flat = [v for step in coefficients for v in step]
+    else:
+        flat = list(coefficients) * steps
+    if len(flat) != 3 * steps:
+        raise ValueError("three coefficients a step")
+    dX = _desc(X)
+    y = _empty(X.shape, X.dtype, X, stream) if out is None else out
+    ws, wsb = _given_or_sized(workspace, X, stream, lib.mm_orthogonalize_workspace_size, dX)
+    status = lib.mm_orthogonalize(_ref(dX), steps, (ctypes.c_float * max(1, len(flat)))(*flat), eps, scale,
+                                  _ref(_desc(y)), None if ws is None else ws.data_ptr(), wsb, _stream(X, stream))
+    if status:
+        raise MMError(status, "mm_orthogonalize")
+    return y
 
 
 def mm_get_device_status(stream=None, device=None):

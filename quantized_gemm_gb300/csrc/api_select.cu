@@ -1,6 +1,6 @@
 // C-ABI entry points of the operators whose products select their weights per
-// row: top-k routing, the mixture-of-experts layer and the low-rank adapters
-// (include/mm.h).  Validation, workspace layout and dispatch only.
+// row: top-k routing with its balance loss, the mixture-of-experts layer and the
+// low-rank adapters (include/mm.h).  Validation, workspace layout and dispatch only.
 #include <cstring>
 
 #include "api_internal.h"
@@ -87,6 +87,72 @@ mm_status mm_route_topk_grad(const mm_tensor* logits, const mm_tensor* indices, 
   unsigned* status = device_status_ptr();
   if (!status) return MM_ERR_CUDA;
   return finish(launch_route_topk_grad(a, status, static_cast<cudaStream_t>(stream)), MM_PATH_SIMT);
+}
+
+// ------------------------------------------------------------------ the router's balance loss
+
+mm_status mm_route_balance_workspace_size(const mm_tensor* logits, const mm_tensor* indices, size_t* bytes) {
+  if (!bytes) return MM_ERR_INVALID_ARG;
+  mm_status s;
+  if ((s = check_tensor(logits)) != MM_OK || (s = check_tensor(indices)) != MM_OK) return s;
+  if (!is_float16_32(logits->dtype) || !is_index(indices->dtype)) return MM_ERR_DTYPE;
+  if (logits->ndim != 2 || indices->ndim != 2 || indices->shape[0] != logits->shape[0]) return MM_ERR_SHAPE;
+  if (logits->shape[1] < 1 || indices->shape[1] < 1) return MM_ERR_SHAPE;
+  if (logits->shape[1] > kRouteMaxExperts || logits->shape[0] >= (1ll << 31) / indices->shape[1]) return MM_ERR_UNSUPPORTED;
+  *bytes = balance_workspace_bytes(logits->shape[0], logits->shape[1]);
+  return MM_OK;
+}
+
+mm_status mm_route_balance(const mm_tensor* logits, const mm_tensor* indices, const mm_tensor* loss,
+                           const mm_tensor* counts, const mm_tensor* mean_probs, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  mm_status s;
+  size_t need;
+  if ((s = mm_route_balance_workspace_size(logits, indices, &need)) != MM_OK) return s;
+  BalanceArgs a;
+  memset(&a, 0, sizeof(a));
+  a.dtype = logits->dtype; a.ind64 = indices->dtype == MM_I64;
+  a.rows = logits->shape[0]; a.G = logits->shape[1]; a.k = indices->shape[1];
+  const int64_t one[1] = {1}, gs[1] = {a.G}, gs1[1] = {a.G + 1};
+  if ((s = check_output(loss, MM_F32, 1, one)) != MM_OK || (s = check_output(counts, MM_I32, 1, gs1)) != MM_OK ||
+      (s = check_output(mean_probs, MM_F32, 1, gs)) != MM_OK)
+    return s;
+  a.logits = logits->data; a.l_rs = logits->strides[0]; a.l_cs = a.G == 1 ? 1 : logits->strides[1];
+  a.indices = indices->data; a.i_rs = indices->strides[0]; a.i_cs = indices->strides[1];
+  a.loss = static_cast<float*>(loss->data);
+  a.counts = static_cast<int32_t*>(counts->data);
+  a.mean = static_cast<float*>(mean_probs->data);
+  if (!workspace_ok(workspace, workspace_bytes, need)) return MM_ERR_WORKSPACE;
+  unsigned* status = device_status_ptr();
+  if (!status) return MM_ERR_CUDA;
+  return finish(launch_balance(a, workspace, status, static_cast<cudaStream_t>(stream)), MM_PATH_SIMT);
+}
+
+mm_status mm_route_balance_grad(const mm_tensor* logits, const mm_tensor* counts, const mm_tensor* grad_loss,
+                                const mm_tensor* base, const mm_tensor* grad_logits, void* stream) {
+  mm_status s;
+  if ((s = check_tensor(logits)) != MM_OK || (s = check_tensor(counts)) != MM_OK || (s = check_tensor(grad_loss)) != MM_OK)
+    return s;
+  if (base && (s = check_tensor(base)) != MM_OK) return s;
+  if (!is_float16_32(logits->dtype) || counts->dtype != MM_I32 || grad_loss->dtype != MM_F32 ||
+      (base && base->dtype != logits->dtype))
+    return MM_ERR_DTYPE;
+  if (logits->ndim != 2 || logits->shape[1] < 1) return MM_ERR_SHAPE;
+  BalanceGradArgs a;
+  memset(&a, 0, sizeof(a));
+  a.dtype = logits->dtype;
+  a.rows = logits->shape[0]; a.G = logits->shape[1];
+  if (!has_shape(counts, {a.G + 1}) || numel(grad_loss) != 1 || (base && !has_shape(base, {a.rows, a.G})))
+    return MM_ERR_SHAPE;
+  if ((s = check_output(grad_logits, a.dtype, 2, logits->shape)) != MM_OK) return s;
+  if (a.G > kRouteMaxExperts) return MM_ERR_UNSUPPORTED;
+  if (a.rows == 0) return finish(MM_OK, MM_PATH_NONE);
+  a.logits = logits->data; a.l_rs = logits->strides[0]; a.l_cs = a.G == 1 ? 1 : logits->strides[1];
+  a.counts = static_cast<const int32_t*>(counts->data); a.counts_s = counts->strides[0];
+  a.dloss = static_cast<const float*>(grad_loss->data);
+  if (base) { a.base = base->data; a.b_rs = base->strides[0]; a.b_cs = a.G == 1 ? 1 : base->strides[1]; }
+  a.out = grad_logits->data;
+  return finish(launch_balance_grad(a, static_cast<cudaStream_t>(stream)), MM_PATH_SIMT);
 }
 
 }  // extern "C"

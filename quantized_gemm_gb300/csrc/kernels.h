@@ -81,6 +81,66 @@ struct RouteArgs {
 };
 constexpr int64_t kRouteMaxExperts = 1024, kRouteMaxPicks = 32;
 
+// The router's balance loss (mm_route_balance) and its gradient.
+struct BalanceArgs {
+  int dtype;                 // T of logits
+  int ind64;
+  int64_t rows, G, k;
+  const void* logits;  int64_t l_rs, l_cs;
+  const void* indices; int64_t i_rs, i_cs;
+  float* loss;               // [1]
+  int32_t* counts;           // [G + 1]: picks per expert, rows that take part
+  float* mean;               // [G]
+};
+struct BalanceGradArgs {
+  int dtype;
+  int64_t rows, G;
+  const void* logits; int64_t l_rs, l_cs;
+  const int32_t* counts; int64_t counts_s;
+  const float* dloss;        // [1]
+  const void* base; int64_t b_rs, b_cs;        // T, null = none
+  void* out;                 // dense T
+};
+
+// Rows to int8 with a scale each (mm_quantize_rows).
+struct QuantizeArgs {
+  int dtype;                 // of x
+  int64_t M, K;
+  const void* x; int64_t x_rs, x_cs;
+  int8_t* q;                 // dense [M, K]
+  float* scales;             // [M]
+};
+
+// 8-bit product with scales (mm_int8_matmul).
+struct Int8Args {
+  int out_dtype;             // of y and bias
+  int64_t M, N, K;
+  const int8_t* a; int64_t a_rs, a_cs;
+  const int8_t* b; int64_t b_ks, b_ns;
+  const float* sa; int64_t sa_s;
+  const float* sb; int64_t sb_s;
+  const void* bias; int64_t bias_s;            // null = none
+  void* y;                   // dense [M, N]
+};
+constexpr int kInt8FewRows = 8, kInt8FewCols = 2;
+// An operand's f16 copy: dst[r, c] = src[r * rs + c * cs], rows of `ld` values.
+struct Int8Copy {
+  const int8_t* src; int64_t rs, cs, rows, cols, ld;
+  __half* dst;
+};
+
+// Orthogonalised update (mm_orthogonalize).
+struct OrthoArgs {
+  int dtype;
+  int64_t M, N;
+  BatchMap bm;
+  MatView x;                 // any strides
+  void* out;                 // dense
+  int steps;
+  const float* coef;         // host, [steps][3]
+  float eps, scale;
+};
+
 // Mixture-of-experts layer (mm_moe_layer).
 struct MoeArgs {
   int dtype;                 // T
@@ -107,6 +167,24 @@ struct LowRankArgs {
 
 mm_status launch_route_topk(const RouteArgs& args, cudaStream_t stream);
 mm_status launch_route_topk_grad(const RouteArgs& args, unsigned* status, cudaStream_t stream);
+
+// Partial sums of every block, then one cluster that adds them.
+int64_t balance_partial_blocks(int64_t rows);
+size_t balance_workspace_bytes(int64_t rows, int64_t G);
+mm_status launch_balance(const BalanceArgs& args, void* workspace, unsigned* status, cudaStream_t stream);
+mm_status launch_balance_grad(const BalanceGradArgs& args, cudaStream_t stream);
+
+mm_status launch_quantize_rows(const QuantizeArgs& args, cudaStream_t stream);
+// Few rows against columns of B contiguous along k (16-byte aligned); every
+// stride; the operands' f16 copies for the tensor cores.
+bool int8_few_supported(const Int8Args& args);
+mm_status launch_int8_few(const Int8Args& args, cudaStream_t stream);
+mm_status launch_int8_any(const Int8Args& args, cudaStream_t stream);
+mm_status launch_int8_copies(const Int8Copy& A, const Int8Copy& B, cudaStream_t stream);
+
+// The norm, the division and the chain of products.
+size_t ortho_workspace_bytes(const OrthoArgs& args);
+mm_status launch_ortho(const OrthoArgs& args, void* workspace, cudaStream_t stream);
 
 // h[t * S + s, f] (f32) and then the weighted sum over s, on the CUDA cores.
 mm_status launch_simt_moe(const MoeArgs& args, float* h, unsigned* status, cudaStream_t stream);

@@ -1,0 +1,329 @@
+// The orthogonalised update (mm_orthogonalize): a matrix is divided by its
+// Frobenius norm and driven towards the nearest orthogonal one by the odd
+// polynomial X <- a X + (b A + c A A) X, A = X X^T (Newton-Schulz), on the side
+// with fewer rows (A = X^T X and X <- a X + X (b A + c A A) for a tall matrix).
+//
+// This file holds the norm, the division and the chain of products.
+#include <cmath>
+#include <cstring>
+
+#include "api_internal.h"
+#include "kernels.h"
+#include "tc.h"
+
+namespace qg {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------ norm and division
+//
+// Both kernels walk a matrix in pieces of 16 bytes (VEC: rows contiguous, a
+// whole number of aligned pieces) or elements; block (b, c) takes share c of
+// matrix b.  Bound: memory, each reads X once.
+
+struct NormArgs {
+  int64_t M, N, count;               // matrices
+  BatchMap bm;
+  MatView x;
+  int chunks;                        // shares of a matrix
+  FastDiv fd_row;                    // pieces (or elements) of a row
+  double* part;                      // [count][chunks] sums of squares
+  float eps;
+  float* s;                          // [count][M][ld], the divided matrix
+  int64_t ld;
+};
+
+// Sums of squares over the whole range of fp32: values of 2^50 and more, and of
+// less than 2^-60, are squared after a shift by 2^-80 and 2^80.
+struct Squares {
+  float mid = 0.f, big = 0.f, small = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float ax = fabsf(x);
+    if (ax < 1.1258999e+15f && (ax >= 8.6736174e-19f || ax == 0.f)) {
+      mid = fmaf(x, x, mid);
+    } else if (ax < 1.f) {
+      const float y = x * 1.2089258e+24f;
+      small = fmaf(y, y, small);
+    } else {                         // infinities and NaN too
+      const float y = x * 8.2718061e-25f;
+      big = fmaf(y, y, big);
+    }
+  }
+  __device__ __forceinline__ double total() const {
+    return (double)mid + (double)big * 1.4615016373309029e+48 + (double)small * 6.8422776578360209e-49;   // 2^160, 2^-160
+  }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void walk_share(const NormArgs& a, int64_t b, int chunk, int64_t& first, int64_t& last) {
+  constexpr int E = VEC ? 16 / (int)sizeof(T) : 1;
+  const int64_t pieces = a.M * (a.N / E);
+  first = pieces * chunk / a.chunks;
+  last = pieces * (chunk + 1) / a.chunks;
+}
+
+template <typename T, bool VEC, typename F>
+__device__ __forceinline__ void walk(const NormArgs& a, F&& f) {
+  constexpr int E = VEC ? 16 / (int)sizeof(T) : 1;
+  const int64_t b = blockIdx.x / a.chunks;
+  const int chunk = (int)(blockIdx.x - b * a.chunks);
+  int64_t first, last;
+  walk_share<T, VEC>(a, b, chunk, first, last);
+  const T* x = static_cast<const T*>(a.x.ptr) + batch_offset(a.bm, a.x.bstride, b);
+  const uint32_t per_row = a.fd_row.d;
+#pragma unroll 4
+  for (int64_t i = first + threadIdx.x; i < last; i += kThreads) {
+    const uint32_t r = i < (1ll << 32) ? fast_div((uint32_t)i, a.fd_row) : (uint32_t)(i / per_row);
+    const int64_t c = (i - (int64_t)r * per_row) * E;
+    T e[E];
+    if constexpr (VEC) *reinterpret_cast<uint4*>(e) = __ldg(reinterpret_cast<const uint4*>(x + r * a.x.rs + c));
+    else e[0] = x[r * a.x.rs + c * a.x.cs];
+    f(b, r, c, e);
+  }
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs a) {
+  pdl_begin();
+  __shared__ double part[kThreads / 32];
+  Squares q;
+  walk<T, VEC>(a, [&](int64_t, uint32_t, int64_t, const auto& e) {
+#pragma unroll
+    for (const T& v : e) q.add(to_f32(v));
+  });
+  double v = q.total();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    v = 0.;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) v += part[w];
+    a.part[blockIdx.x] = v;
+  }
+}
+
+// |X|_F + eps from the shares' sums, as d = m 2^k: fp32 division where the whole
+// is in fp32's middle range (k = 0), m in [1, 2) otherwise.
+struct Divisor {
+  float m;
+  int k;
+  __device__ __forceinline__ float divide(float x) const {
+    return k == 0 ? __fdiv_rn(x, m) : __fdiv_rn(scalbnf(x, -k), m);
+  }
+};
+__device__ __forceinline__ Divisor load_divisor(const NormArgs& a, int64_t b) {
+  __shared__ double total;
+  if (threadIdx.x < 32) {
+    double v = 0.;
+    for (int c = threadIdx.x; c < a.chunks; c += 32) v += a.part[b * a.chunks + c];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (threadIdx.x == 0) total = sqrt(v) + (double)a.eps;
+  }
+  __syncthreads();
+  Divisor d;
+  const double t = total;
+  if (!(t < 1e30) || !(t > 1e-30)) {
+    if (t > 0. && t < 1e300) {
+      int k;
+      const double f = frexp(t, &k);
+      d.m = (float)(2. * f);
+      d.k = k - 1;
+    } else {                        // zero, infinite, NaN
+      d.m = (float)t;
+      d.k = 0;
+    }
+  } else {
+    d.m = (float)t;
+    d.k = 0;
+  }
+  return d;
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) divide_kernel(const NormArgs a) {
+  pdl_begin();
+  const Divisor d = load_divisor(a, blockIdx.x / a.chunks);
+  walk<T, VEC>(a, [&](int64_t b, uint32_t r, int64_t c, const auto& e) {
+    constexpr int E = sizeof(e) / sizeof(T);
+    float* dst = a.s + (b * a.M + r) * a.ld + c;
+    float v[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] = d.divide(to_f32(e[j]));
+    if constexpr (E >= 4) {          // ld is a multiple of 4, c of E
+#pragma unroll
+      for (int j = 0; j < E; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) dst[j] = v[j];
+    }
+  });
+}
+
+// out = T(scale * S): S [count][M][ld], out dense.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) round_kernel(const float* s, int64_t rows, int64_t N, int64_t ld,
+                                                         float scale, T* out) {
+  pdl_begin();
+  const int64_t n = rows * N, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+    const int64_t r = i / N;
+    out[i] = from_f32<T>(scale * s[r * ld + (i - r * N)]);
+  }
+}
+
+int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Shares per matrix: four blocks per SM over all matrices, at least 4096 elements each.
+int norm_chunks(int64_t M, int64_t N, int64_t count) {
+  const int64_t want = (4 * (int64_t)sm_count_public() + count - 1) / count;
+  const int64_t most = (M * N + 4095) / 4096;
+  const int64_t n = want < most ? want : most;
+  return (int)(n < 1 ? 1 : n);
+}
+
+template <typename T>
+mm_status run_norm(const OrthoArgs& o, NormArgs a, cudaStream_t stream) {
+  constexpr int E = 16 / (int)sizeof(T);
+  bool vec = o.x.cs == 1 && o.N % E == 0 && (o.x.rs % E == 0 || o.M == 1) && (reinterpret_cast<uintptr_t>(o.x.ptr) & 15) == 0;
+  for (int d = 0; d < o.bm.nb; ++d) vec = vec && (o.x.bstride[d] % E == 0 || o.bm.shape[d] == 1);
+  a.fd_row = make_fastdiv((uint32_t)(vec ? o.N / E : o.N));
+  const int64_t blocks = o.bm.count * a.chunks;
+  if (blocks >= (1ll << 31)) return MM_ERR_UNSUPPORTED;
+  const dim3 g((unsigned)blocks), t(kThreads);
+  cudaError_t e = vec ? launch_pdl(norm_kernel<T, true>, g, t, 0, stream, a)
+                      : launch_pdl(norm_kernel<T, false>, g, t, 0, stream, a);
+  if (e == cudaSuccess)
+    e = vec ? launch_pdl(divide_kernel<T, true>, g, t, 0, stream, a) : launch_pdl(divide_kernel<T, false>, g, t, 0, stream, a);
+  return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+}
+
+template <typename T>
+mm_status run_round(const OrthoArgs& o, const float* s, int64_t ld, cudaStream_t stream) {
+  const int64_t rows = o.bm.count * o.M, want = (rows * o.N + 4 * kThreads - 1) / (4 * kThreads);
+  const int64_t most = 8 * (int64_t)sm_count_public();
+  return launch_pdl(round_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(kThreads), 0, stream, s, rows,
+                    o.N, ld, o.scale, static_cast<T*>(o.out)) == cudaSuccess
+             ? MM_OK
+             : MM_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ the chain in fp32
+
+struct FloatPlan {
+  int64_t m, ld, ldm;               // the smaller side; row pitches of X and of A, B
+  int chunks;
+  size_t part, s[2], a, b, bytes;   // offsets in the workspace
+};
+FloatPlan plan_float(const OrthoArgs& o) {
+  FloatPlan p;
+  p.m = o.M < o.N ? o.M : o.N;
+  p.ld = round_up(o.N, 4);
+  p.ldm = round_up(p.m, 4);
+  p.chunks = norm_chunks(o.M, o.N, o.bm.count);
+  const size_t x = align256((size_t)o.bm.count * o.M * p.ld * 4), sq = align256((size_t)o.bm.count * p.m * p.ldm * 4);
+  p.part = 0;
+  p.s[0] = align256((size_t)o.bm.count * p.chunks * 8);
+  p.s[1] = p.s[0] + x;
+  p.a = p.s[1] + x;
+  p.b = p.a + sq;
+  p.bytes = p.b + sq;
+  return p;
+}
+
+// A batch of `count` products C = alpha A B + beta C0 of matrices `*_step` apart.
+GemmArgs batched(int dtype, int64_t count, int64_t M, int64_t N, int64_t K) {
+  GemmArgs g;
+  memset(&g, 0, sizeof(g));
+  g.dtype = dtype;
+  g.M = M; g.N = N; g.K = K;
+  g.bm.nb = 1;
+  for (int d = 0; d < kMaxBatchDims; ++d) g.bm.shape[d] = 1;
+  g.bm.shape[0] = g.bm.count = count;
+  g.alpha = 1.f;
+  return g;
+}
+MatView view(const void* p, int64_t step, int64_t rs, int64_t cs) {
+  MatView v;
+  memset(&v, 0, sizeof(v));
+  v.ptr = p;
+  v.bstride[0] = step;
+  v.rs = rs;
+  v.cs = cs;
+  return v;
+}
+
+// The products of the chain go by the policy as MatMul's do, without the few-row kernels.
+mm_status product(const GemmArgs& g, cudaStream_t st) {
+  const int path = choose(tc_gemm_supported(g), tensor_pays_dense(g.dtype, g.M, g.N, g.K, g.bm.count));
+  return run_dense_on(path, g, st);
+}
+
+mm_status run_float(const OrthoArgs& o, void* ws, cudaStream_t st) {
+  const FloatPlan p = plan_float(o);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  NormArgs n;
+  memset(&n, 0, sizeof(n));
+  n.M = o.M; n.N = o.N; n.count = o.bm.count;
+  n.bm = o.bm; n.x = o.x;
+  n.chunks = p.chunks;
+  n.part = reinterpret_cast<double*>(w + p.part);
+  n.eps = o.eps;
+  n.s = reinterpret_cast<float*>(w + p.s[0]);
+  n.ld = p.ld;
+  mm_status s = o.dtype == MM_F32    ? run_norm<float>(o, n, st)
+                : o.dtype == MM_BF16 ? run_norm<__nv_bfloat16>(o, n, st)
+                                     : run_norm<__half>(o, n, st);
+  const bool tall = o.M > o.N;
+  const int64_t xs = o.M * p.ld, as = p.m * p.ldm;
+  float *A = reinterpret_cast<float*>(w + p.a), *B = reinterpret_cast<float*>(w + p.b);
+  int cur = 0;
+  for (int i = 0; i < o.steps && s == MM_OK; ++i) {
+    const float *X = reinterpret_cast<float*>(w + p.s[cur]), *k = o.coef + 3 * i;
+    GemmArgs g = batched(MM_F32, o.bm.count, p.m, p.m, tall ? o.M : o.N);
+    g.a = tall ? view(X, xs, 1, p.ld) : view(X, xs, p.ld, 1);
+    g.b = tall ? view(X, xs, p.ld, 1) : view(X, xs, 1, p.ld);
+    g.y = view(A, as, p.ldm, 1);
+    if ((s = product(g, st)) != MM_OK) return s;
+    g = batched(MM_F32, o.bm.count, p.m, p.m, p.m);
+    g.a = g.b = g.c = view(A, as, p.ldm, 1);
+    g.y = view(B, as, p.ldm, 1);
+    g.alpha = k[2];
+    g.beta = k[1];
+    if ((s = product(g, st)) != MM_OK) return s;
+    g = batched(MM_F32, o.bm.count, o.M, o.N, p.m);
+    g.a = tall ? view(X, xs, p.ld, 1) : view(B, as, p.ldm, 1);
+    g.b = tall ? view(B, as, p.ldm, 1) : view(X, xs, p.ld, 1);
+    g.c = view(X, xs, p.ld, 1);
+    g.beta = k[0];
+    cur ^= 1;
+    if (i + 1 == o.steps && o.dtype == MM_F32) {        // straight into the output
+      g.alpha = o.scale;
+      g.beta = k[0] * o.scale;
+      g.y = view(o.out, o.M * o.N, o.N, 1);
+      return product(g, st);
+    }
+    g.y = view(w + p.s[cur], xs, p.ld, 1);
+    s = product(g, st);
+  }
+  if (s != MM_OK) return s;
+  const float* X = reinterpret_cast<float*>(w + p.s[cur]);
+  return o.dtype == MM_F32    ? run_round<float>(o, X, p.ld, st)
+         : o.dtype == MM_BF16 ? run_round<__nv_bfloat16>(o, X, p.ld, st)
+                              : run_round<__half>(o, X, p.ld, st);
+}
+
+}  // namespace
+
+size_t ortho_workspace_bytes(const OrthoArgs& o) { return plan_float(o).bytes; }
+
+mm_status launch_ortho(const OrthoArgs& o, void* workspace, cudaStream_t stream) {
+  return run_float(o, workspace, stream);
+}
+
+}  // namespace qg

@@ -19,6 +19,11 @@ bool tc_qlinear_supported(const QLinearArgs& q);
 size_t tc_qlinear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t a_count, int64_t b_count);
 mm_status launch_tc_qlinear(const QLinearArgs& q, void* workspace, unsigned* status, cudaStream_t stream);
 
+// Y = (A B) scaled per row and per column plus a bias, of f16 copies a (rows
+// lda apart, K-major) and b (K-major [N, ldb], or with b_mn [K, ldb]).
+mm_status launch_tc_int8(const Int8Args& q, const void* a, int64_t lda, const void* b, int64_t ldb, int b_mn,
+                         unsigned* status, cudaStream_t stream);
+
 bool tc_grouped_supported(const GroupedArgs& g);
 size_t tc_grouped_workspace_bytes(const GroupedArgs& g);
 // GroupedArgs with wq != 0 take the fused-dequantisation kernel (CTA pairs):

@@ -48,6 +48,8 @@
 //   kTF32     fp32 MatMul / Gemm as three tf32 products of split operands.
 //   kLowRank  kDense whose tiles go on with the k-blocks of their rows'
 //             low-rank adapters (see lowrank_tc.cu).
+//   kInt8     kDense over f16 copies of int8 operands; epilogue
+//             y = (acc * a_scale[m]) * b_scale[n] + bias[n], rounded once.
 //   kSkinny   kDense for at most 64 rows of A': 256-column tiles whose
 //             k-blocks are split over the CTAs of a cluster (non-persistent,
 //             one tile per cluster), so that B' streams through every SM with
@@ -527,6 +529,47 @@ __device__ __forceinline__ void add_c32(const TcParams& p, const uint16_t* crow,
 #pragma unroll
     for (int j = 0; j < 32; ++j)
       if (n + j < p.N) v[j] = __fmaf_rn(p.beta, unpack16(crow[(n + j) * p.c_cs], p.out_f16), v[j]);
+  }
+}
+
+// v[j] = v[j] * b_scale[n + j] + bias[n + j] (kInt8; each step rounded).  The
+// addresses are the same in every lane.
+__device__ __forceinline__ void scale_columns32(const TcParams& p, int64_t n, float (&v)[32]) {
+  const float* s = static_cast<const float*>(p.sb.ptr) + n * p.sb.vs;
+  if (p.s_vec && n + 32 <= p.N) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(s) + q);
+      v[4 * q] = __fmul_rn(v[4 * q], f.x);
+      v[4 * q + 1] = __fmul_rn(v[4 * q + 1], f.y);
+      v[4 * q + 2] = __fmul_rn(v[4 * q + 2], f.z);
+      v[4 * q + 3] = __fmul_rn(v[4 * q + 3], f.w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (n + j < p.N) v[j] = __fmul_rn(v[j], __ldg(s + j * p.sb.vs));
+  }
+  if (!p.c) return;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (n + j < p.N) {
+      const int64_t off = (n + j) * p.c_cs;
+      const float c = p.out_f32 ? __ldg(static_cast<const float*>(p.c) + off)
+                                : unpack16(__ldg(static_cast<const uint16_t*>(p.c) + off), p.out_f16);
+      v[j] = __fadd_rn(v[j], c);
+    }
+}
+// 32 fp32 values of a row from column n on (128 bytes where the row allows vectors).
+__device__ __forceinline__ void store_f32_32(const TcParams& p, float* yf, int64_t n, const float (&v)[32]) {
+  if (p.y_vec && n + 32 <= p.N) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      *reinterpret_cast<float4*>(yf + n + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (n + j < p.N) yf[n + j] = v[j];
   }
 }
 
@@ -1060,7 +1103,11 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
         } else if (p.c && rok)
           crow = static_cast<const uint16_t*>(p.c) + batch_off(p, p.c_bstride, ti.batch) + m * p.c_rs;
       }
-      if constexpr (MODE == kDense || MODE == kSkinny) {
+      float row_scale = 0.f;
+      if constexpr (MODE == kInt8) {
+        if (rok) row_scale = __ldg(static_cast<const float*>(p.sa.ptr) + (ti.m0 + roff + rl) * p.sa.vs);
+      }
+      if constexpr (MODE == kDense || MODE == kSkinny || MODE == kInt8) {
         if (p.y_tma) {
           // The warp's 32 rows x 64 columns: into registers, release the
           // accumulator, then alpha/beta/C and the rounding to 16 bits.
@@ -1082,9 +1129,15 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float v[32];
+            if constexpr (MODE == kInt8) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(r[h][j]);
-            if (crow) add_c32(p, crow, ncol + 32 * h, v);
+              for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(__uint_as_float(r[h][j]), row_scale);
+              scale_columns32(p, ncol + 32 * h, v);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(r[h][j]);
+              if (crow) add_c32(p, crow, ncol + 32 * h, v);
+            }
             if (lane == 0) bulk_wait_read_all();
             __syncwarp();
 #pragma unroll
@@ -1140,23 +1193,24 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
                 v[j] = p.alpha * __uint_as_float(r[h][j]);
                 if (cf && n + j < p.N) v[j] = __fmaf_rn(p.beta, cf[(n + j) * p.c_cs], v[j]);
               }
-              if (p.y_vec && n + 32 <= p.N) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  *reinterpret_cast<float4*>(yf + n + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2],
-                                                                           v[4 * q + 3]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (n + j < p.N) yf[n + j] = v[j];
-              }
+              store_f32_32(p, yf, n, v);
             }
             continue;
           }
           float v[32];
+          if constexpr (MODE == kInt8) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(r[h][j]);
-          if (crow) add_c32(p, crow, n, v);
+            for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(__uint_as_float(r[h][j]), row_scale);
+            scale_columns32(p, n, v);
+            if (p.out_f32) {
+              if (rok) store_f32_32(p, static_cast<float*>(p.y) + (ti.m0 + roff + rl) * p.y_rs, n, v);
+              continue;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(r[h][j]);
+            if (crow) add_c32(p, crow, n, v);
+          }
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], p.out_f16);
@@ -1344,7 +1398,7 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
   // the previous kernel on the stream is finishing: the set-up above overlaps
   // its tail, and nothing below touches global memory before it completes.
   if (MODE != kSkinny || !p.c_late) pdl_wait();
-  if constexpr (MODE == kDense || MODE == kTF32) pdl_trigger();
+  if constexpr (MODE == kDense || MODE == kTF32 || MODE == kInt8) pdl_trigger();
   const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
 
   if (warp == 0) {
@@ -1604,7 +1658,7 @@ mm_status launch_kernel(const OperandPlan& a, const OperandPlan& b, const CUtens
                         const TcParams& p_in, int64_t work, cudaStream_t stream) {
   constexpr int kSmem = Cfg<MODE, PAIR>::kSmem, kThreadsM = Cfg<MODE, PAIR>::kThreads;
   TcParams p = p_in;
-  if (MODE != kDense) p.y_tma = 0;
+  if (MODE != kDense && MODE != kInt8) p.y_tma = 0;
   if (cudaFuncSetAttribute(tc_gemm_kernel<MODE, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
       cudaSuccess)
     return MM_ERR_CUDA;
@@ -1708,6 +1762,9 @@ mm_status launch_tc(int mode, bool pair, const OperandPlan& a, const OperandPlan
     case kTF32:
       return pair ? launch_kernel<kTF32, true>(a, b, ms, mz, p, work, stream)
                   : launch_kernel<kTF32, false>(a, b, ms, mz, p, work, stream);
+    case kInt8:
+      return pair ? launch_kernel<kInt8, true>(a, b, ms, mz, p, work, stream)
+                  : launch_kernel<kInt8, false>(a, b, ms, mz, p, work, stream);
     case kGroupedQ:  // CTA pairs only
       if (!pair || !s) return MM_ERR_UNSUPPORTED;
       return launch_kernel<kGroupedQ, true>(a, b, ms, mz, p, work, stream);
@@ -1870,6 +1927,53 @@ mm_status launch_tc_gemm(const GemmArgs& g, unsigned* status, cudaStream_t strea
     plan_output(g, &p, &ymap);
     const mm_status st = launch_tc(p.out_f32 ? kTF32 : kDense, pair, a, b, p, stream,
                                    p.pair_tail ? &a_tail : nullptr, p.y_tma ? &ymap : nullptr);
+    if (st != MM_ERR_UNSUPPORTED || !pair) return st;
+  }
+  return MM_ERR_UNSUPPORTED;
+}
+
+// ------------------------------------------------------------------ 8-bit product
+
+mm_status launch_tc_int8(const Int8Args& q, const void* a, int64_t lda, const void* b, int64_t ldb, int b_mn,
+                         unsigned* status, cudaStream_t stream) {
+  if (!status) return MM_ERR_CUDA;
+  GemmArgs g;
+  memset(&g, 0, sizeof(g));
+  g.M = q.M; g.N = q.N; g.K = q.K;
+  g.bm.count = 1;
+  for (int d = 0; d < kMaxBatchDims; ++d) g.bm.shape[d] = 1;
+  g.a.ptr = a; g.a.rs = lda; g.a.cs = 1;
+  g.b.ptr = b; g.b.rs = b_mn ? ldb : 1; g.b.cs = b_mn ? 1 : ldb;
+  g.y.ptr = q.y; g.y.rs = q.N; g.y.cs = 1;
+  TcParams p;
+  init_params(&p);
+  p.M = g.M; p.N = g.N; p.K = g.K;
+  p.bm = g.bm;
+  p.out_f16 = q.out_dtype == MM_F16;
+  p.out_f32 = q.out_dtype == MM_F32;
+  p.y = q.y;
+  p.y_rs = q.N;
+  p.y_vec = (reinterpret_cast<uintptr_t>(q.y) % 16 == 0) && (q.N % (p.out_f32 ? 4 : 8) == 0);
+  p.sa.ptr = q.sa; p.sa.vs = q.sa_s;
+  p.sb.ptr = q.sb; p.sb.vs = q.sb_s;
+  p.s_vec = q.sb_s == 1 && (reinterpret_cast<uintptr_t>(q.sb) & 15) == 0;
+  p.c = q.bias;
+  p.c_cs = q.bias_s;
+  p.status = status;
+  OperandPlan ymap;
+  g.dtype = q.out_dtype;
+  plan_output(g, &p, &ymap);
+  g.dtype = MM_F16;
+  for (int attempt = use_pair(g.M, g.K) ? 0 : 1; attempt < 2; ++attempt) {
+    const bool pair = attempt == 0;
+    OperandPlan pa, pb, tail;
+    if (!plan_operand(a, MM_F16, g.M, g.K, lda, 1, g.bm, g.a.bstride, BM, &pa) ||
+        !plan_operand(b, MM_F16, g.N, g.K, g.b.cs, g.b.rs, g.bm, g.b.bstride, pair ? BN / 2 : BN, &pb))
+      return MM_ERR_UNSUPPORTED;
+    p.idesc = make_idesc(1, 0, pb.mn_major, pair);
+    p.pair_tail = pair && plan_operand(a, MM_F16, g.M, g.K, lda, 1, g.bm, g.a.bstride, BM / 2, &tail);
+    if (p.pair_tail) p.idesc_tail = make_idesc_rows(1, 0, pb.mn_major, BM);
+    const mm_status st = launch_tc(kInt8, pair, pa, pb, p, stream, p.pair_tail ? &tail : nullptr, p.y_tma ? &ymap : nullptr);
     if (st != MM_ERR_UNSUPPORTED || !pair) return st;
   }
   return MM_ERR_UNSUPPORTED;

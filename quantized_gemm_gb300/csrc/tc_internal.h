@@ -25,7 +25,9 @@ constexpr int kTileK = 64;    // one 128-byte swizzle row of 16-bit elements
 // kLowRank: a dense product whose row tiles go on, after the k-blocks of A B,
 // with k-blocks of other operands (the rows' low-rank factors times their
 // adapters), accumulated on top.
-enum TcMode { kDense = 0, kGrouped = 1, kQLinear = 2, kGroupedQ = 3, kTF32 = 4, kSkinny = 5, kLowRank = 6 };
+// kInt8: a dense product of f16 copies of int8 operands whose epilogue
+// multiplies by a scale per row and per column and adds a bias.
+enum TcMode { kDense = 0, kGrouped = 1, kQLinear = 2, kGroupedQ = 3, kTF32 = 4, kSkinny = 5, kLowRank = 6, kInt8 = 7 };
 
 struct TcParams {
   int64_t M, N, K;
@@ -69,6 +71,7 @@ struct TcParams {
   const void* ys;
   const void* yz;
   int sa_f16, sb_f16, ys_f16, y_signed;
+  int s_vec;                                   // kInt8 (sa, sb fp32, c its bias): sb allows 16-byte reads
   int a_signed, b_signed;                      // uint8 operands were shifted by -128
   const int32_t* q_rs;                         // [a matrices, M] row sums of a'
   const int32_t* q_cs;                         // [b matrices, N] column sums of b'
