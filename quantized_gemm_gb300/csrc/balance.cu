@@ -9,14 +9,19 @@
 // A logit of -inf or NaN takes no part (p = 0); a maximum of +inf takes the
 // limit, as in mm_route_topk.
 //
-// Both directions read the logits once and are bound by memory.  A row belongs
-// to LPR neighbouring lanes, lane i holding columns [i*V, i*V + V); a lane keeps
-// the same columns for every row of its warp, so the column sums (forward) and
-// the shares c/C (gradient) stay in its registers.  kRows rows are loaded before
-// any is used.  Column sums leave a block through shared memory, one partial
-// per block, and a second launch, one cluster, adds the partials in a fixed
-// order; picks are integers, counted with shared-memory atomics, whose order
-// does not matter.
+// Both directions read the logits once.  A row belongs to LPR neighbouring lanes,
+// which hold its 16-byte pieces in turn (piece q of lane i is the row's piece
+// q * LPR + i), so that a warp reads 32 / LPR rows at once, each in whole
+// sectors, and a sum over a row takes log2(LPR) shuffles for all of them.  A lane
+// keeps the same columns for every row, so the column sums (forward) and the
+// shares c / C (gradient) stay in its registers.  With 65536 rows of 256 bf16
+// logits a row over all 32 lanes, with a branch per logit, took 30 us forward and
+// 59 us backward (276 instructions a row); see the kernels for today's.  Column
+// sums leave a block through shared memory, one partial per block, and a second
+// launch, one cluster, adds the partials in a fixed order; picks are integers,
+// counted with shared-memory atomics, whose order does not matter.
+#include <type_traits>
+
 #include "kernels.h"
 #include "tc_ptx.cuh"
 
@@ -25,13 +30,19 @@ namespace qg {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kRows = 4;
 constexpr int kFinalBlocks = 8;      // the cluster of the second launch
 
-// exp(l - top), with the limit for an infinite top.  The difference is rounded
-// once and the function is off by 2 ulp and by |l - top| 2^-23: 3e-6 where the
-// result still matters (l - top > -20).
-__device__ __forceinline__ float share_of(float l, float top) { return l == top ? 1.f : __expf(l - top); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 
 template <int LPR>
 __device__ __forceinline__ float lanes_max(float v) {
@@ -46,60 +57,172 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// V neighbouring values of a row as loaded: raw 16-byte pieces where the row
-// allows it, otherwise one element at a time (`fill` past the end).
-template <typename T, int V>
-struct Piece {
-  static constexpr int kPer = 16 / sizeof(T), kVecs = V / kPer;
-  static_assert(V % kPer == 0, "whole 16-byte pieces");
-  uint4 u[kVecs];
-  __device__ __forceinline__ void load(const T* row, int64_t cs, int c0, int n, bool vec, float fill) {
-    if (vec && c0 + V <= n) {
-#pragma unroll
-      for (int q = 0; q < kVecs; ++q) u[q] = __ldg(reinterpret_cast<const uint4*>(row + c0) + q);
-    } else {
-      T* e = reinterpret_cast<T*>(u);
-#pragma unroll
-      for (int j = 0; j < V; ++j) e[j] = c0 + j < n ? row[(c0 + j) * cs] : from_f32<T>(fill);
-    }
+// A 16-byte piece as pairs of floats, NaN turned into -inf (the maximum with -inf
+// drops NaN), and back with one rounding.
+template <typename T> struct Pairs;
+template <> struct Pairs<float> {
+  static constexpr int kElems = 4;
+  static __device__ __forceinline__ uint4 clean(uint4 u) {
+    const auto f = [](uint32_t w) { return __float_as_uint(fmaxf(__uint_as_float(w), -INFINITY)); };
+    return make_uint4(f(u.x), f(u.y), f(u.z), f(u.w));
   }
-  __device__ __forceinline__ float at(int j) const { return to_f32(reinterpret_cast<const T*>(u)[j]); }
+  static __device__ __forceinline__ float max(uint4 u) {
+    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+  }
+  static __device__ __forceinline__ void split(uint4 u, float2 (&x)[2]) {
+    x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+    x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  static __device__ __forceinline__ uint4 join(const float2 (&x)[2]) {
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
+  }
+};
+template <typename H2>
+struct Pairs16 {
+  static constexpr int kElems = 8;
+  static __device__ __forceinline__ H2 as(uint32_t w) { return *reinterpret_cast<const H2*>(&w); }
+  static __device__ __forceinline__ uint32_t bits(H2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+};
+template <> struct Pairs<__nv_bfloat16> : Pairs16<__nv_bfloat162> {
+  static __device__ __forceinline__ uint4 clean(uint4 u) {
+    const __nv_bfloat162 low = as(0xFF80FF80u);
+    return make_uint4(bits(__hmax2(as(u.x), low)), bits(__hmax2(as(u.y), low)), bits(__hmax2(as(u.z), low)),
+                      bits(__hmax2(as(u.w), low)));
+  }
+  static __device__ __forceinline__ float max(uint4 u) {
+    const __nv_bfloat162 m = __hmax2(__hmax2(as(u.x), as(u.y)), __hmax2(as(u.z), as(u.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ void split(uint4 u, float2 (&x)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint4 join(const float2 (&x)[4]) {
+    return make_uint4(bits(__float22bfloat162_rn(x[0])), bits(__float22bfloat162_rn(x[1])),
+                      bits(__float22bfloat162_rn(x[2])), bits(__float22bfloat162_rn(x[3])));
+  }
+};
+template <> struct Pairs<__half> : Pairs16<__half2> {
+  static __device__ __forceinline__ uint4 clean(uint4 u) {
+    const __half2 low = as(0xFC00FC00u);
+    return make_uint4(bits(__hmax2(as(u.x), low)), bits(__hmax2(as(u.y), low)), bits(__hmax2(as(u.z), low)),
+                      bits(__hmax2(as(u.w), low)));
+  }
+  static __device__ __forceinline__ float max(uint4 u) {
+    const __half2 m = __hmax2(__hmax2(as(u.x), as(u.y)), __hmax2(as(u.z), as(u.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ void split(uint4 u, float2 (&x)[4]) {
+    x[0] = __half22float2(as(u.x)); x[1] = __half22float2(as(u.y));
+    x[2] = __half22float2(as(u.z)); x[3] = __half22float2(as(u.w));
+  }
+  static __device__ __forceinline__ uint4 join(const float2 (&x)[4]) {
+    return make_uint4(bits(__float22half2_rn(x[0])), bits(__float22half2_rn(x[1])), bits(__float22half2_rn(x[2])),
+                      bits(__float22half2_rn(x[3])));
+  }
 };
 
-// e[j] = exp(l[j] - top) and 1 / sum; false for a row without any expert.
-template <typename T, int LPR, int V>
-__device__ __forceinline__ bool softmax_row(const Piece<T, V>& l, float (&e)[V], float* inv) {
-  float top = -INFINITY;
+// A lane's NP pieces of a row.  `vec`: 16-byte reads; elements past G are `fill`.
+template <typename T, int LPR, int NP>
+struct Row {
+  static constexpr int E = Pairs<T>::kElems;
+  uint4 u[NP];
+  __device__ __forceinline__ void load(const T* row, int64_t cs, int lane, int G, bool vec, float fill) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) top = fmaxf(top, l.at(j));       // fmaxf drops NaN
-  top = lanes_max<LPR>(top);
-  float sum = 0.f;
+    for (int q = 0; q < NP; ++q) {
+      const int c0 = (q * LPR + lane) * E;
+      if (vec && c0 + E <= G) {
+        u[q] = __ldg(reinterpret_cast<const uint4*>(row + c0));
+      } else {
+        T e[E];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const float x = l.at(j);
-    e[j] = x > -INFINITY ? share_of(x, top) : 0.f;             // false for NaN
-    sum += e[j];
+        for (int j = 0; j < E; ++j) e[j] = c0 + j < G ? row[(c0 + j) * cs] : from_f32<T>(fill);
+        u[q] = *reinterpret_cast<const uint4*>(e);
+      }
+    }
   }
-  sum = lanes_sum<LPR>(sum);
-  *inv = sum > 0.f ? 1.f / sum : 0.f;
-  return sum > 0.f;
+};
+
+// e = exp(l - max) of a row's logits, in pairs; returns 1 / sum, or 0 for a row
+// without an expert that can be picked.  The difference is rounded once and the
+// function is off by 2 ulp and by |l - max| 2^-23.  A maximum of +inf takes the
+// limit: 1 for the logits that reach it.
+template <typename T, int LPR, int NP>
+__device__ __forceinline__ float softmax_row(const Row<T, LPR, NP>& r, float2 (&e)[NP][Pairs<T>::kElems / 2]) {
+  constexpr int H = Pairs<T>::kElems / 2;
+  float top = -INFINITY;
+  uint4 c[NP];
+#pragma unroll
+  for (int q = 0; q < NP; ++q) {
+    c[q] = Pairs<T>::clean(r.u[q]);
+    top = fmaxf(top, Pairs<T>::max(c[q]));
+  }
+  top = lanes_max<LPR>(top);
+  const float base = top > -INFINITY ? top : 0.f;      // nothing to pick: exp(-inf - 0) = 0
+  float2 sum = twice(0.f);
+#pragma unroll
+  for (int q = 0; q < NP; ++q) {
+    float2 x[H];
+    Pairs<T>::split(c[q], x);
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+      const float2 d = mul2(add2(x[j], twice(-base)), twice(1.44269504f));
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[q][j].x) : "f"(d.x));
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[q][j].y) : "f"(d.y));
+      sum = add2(sum, e[q][j]);
+    }
+  }
+  if (base == INFINITY) {                              // rare: inf - inf above
+    sum = twice(0.f);
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+      float2 x[H];
+      Pairs<T>::split(c[q], x);
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        e[q][j] = make_float2(x[j].x == INFINITY ? 1.f : 0.f, x[j].y == INFINITY ? 1.f : 0.f);
+        sum = add2(sum, e[q][j]);
+      }
+    }
+  }
+  const float s = lanes_sum<LPR>(sum.x + sum.y);
+  return s > 0.f ? __fdividef(1.f, s) : 0.f;           // 1 <= s <= G
 }
+
+// Rows in flight per lane group, by the columns a lane holds.
+template <typename T, int NP> constexpr int kFlight = NP * Pairs<T>::kElems >= 32 ? 1 : NP * Pairs<T>::kElems >= 16 ? 2 : 4;
 
 // Partials of a block: psum [G] f32, then picks [G] i32, then rows that take
 // part and picks in all.
-template <typename T, int LPR, int V>
-__global__ void __launch_bounds__(kThreads) balance_partial_kernel(const BalanceArgs a, const int vec, float* psum,
-                                                                   int32_t* cnt, unsigned* status) {
+template <typename T, int LPR, int NP>
+__global__ void __launch_bounds__(kThreads, 2) balance_partial_kernel(const BalanceArgs a, const int vec, float* psum,
+                                                                      int32_t* cnt, unsigned* status) {
   pdl_wait();
   extern __shared__ float sh[];                                // [kWarps][G] column sums, then [G + 2] counts
   int32_t* hist = reinterpret_cast<int32_t*>(sh + kWarps * a.G);
+  constexpr int E = Pairs<T>::kElems, H = E / 2, R = kFlight<T, NP>;
   const int G = (int)a.G, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < G + 2; i += kThreads) hist[i] = 0;
   __syncthreads();
-  // picks
+  constexpr int kPerWarp = 32 / LPR;
+  const int sub = lane / LPR, l = lane % LPR;
+  const T* logits = static_cast<const T*>(a.logits);
+  const int64_t step = (int64_t)gridDim.x * kWarps * kPerWarp;
+  int64_t r0 = ((int64_t)blockIdx.x * kWarps + warp) * kPerWarp;
+  Row<T, LPR, NP> row[R];
+  const auto load = [&]() {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const int64_t r = r0 + q * step + sub;
+      row[q].load(logits + (r < a.rows ? r : 0) * a.l_rs, a.l_cs, l, G, vec, -INFINITY);
+    }
+  };
+  if (r0 < a.rows) load();                                     // the first rows arrive while the picks are counted
   int mine = 0;
   bool bad = false;
   const int64_t picks = a.rows * a.k;
+#pragma unroll 4
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < picks; i += (int64_t)gridDim.x * kThreads) {
     const int64_t off = a.i_cs == 1 && a.i_rs == a.k ? i : (i / a.k) * a.i_rs + (i % a.k) * a.i_cs;
     const int64_t g = load_index(a.indices, off, a.ind64);
@@ -112,30 +235,27 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const Balance
   }
   if (bad) atomicOr(status, kStatusIndexRange);
   // column sums
-  constexpr int kPerWarp = 32 / LPR;
-  const int sub = lane / LPR, l = lane % LPR, c0 = l * V;
-  const T* logits = static_cast<const T*>(a.logits);
-  float acc[V];
+  float2 acc[NP][H];
 #pragma unroll
-  for (int j = 0; j < V; ++j) acc[j] = 0.f;
+  for (int q = 0; q < NP; ++q)
+#pragma unroll
+    for (int j = 0; j < H; ++j) acc[q][j] = twice(0.f);
   int alive = 0;
-  const int64_t step = (int64_t)gridDim.x * kWarps * kPerWarp;
-  for (int64_t r0 = ((int64_t)blockIdx.x * kWarps + warp) * kPerWarp; r0 < a.rows; r0 += step * kRows) {
-    Piece<T, V> p[kRows];
+  while (r0 < a.rows) {
 #pragma unroll
-    for (int q = 0; q < kRows; ++q) {
-      const int64_t r = r0 + q * step + sub;
-      p[q].load(logits + (r < a.rows ? r : 0) * a.l_rs, a.l_cs, c0, G, vec, -INFINITY);
+    for (int q = 0; q < R; ++q) {
+      float2 e[NP][H];
+      const bool live = r0 + q * step + sub < a.rows;
+      const float inv = softmax_row<T, LPR, NP>(row[q], e);
+      const float2 w = twice(live ? inv : 0.f);
+      alive += live && inv > 0.f && l == 0;
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int j = 0; j < H; ++j) acc[p][j] = ptx::fma2_rn(e[p][j], w, acc[p][j]);
     }
-#pragma unroll
-    for (int q = 0; q < kRows; ++q) {
-      float e[V], inv;
-      const bool any = softmax_row<T, LPR, V>(p[q], e, &inv);
-      if (r0 + q * step + sub >= a.rows) continue;
-      if (any && l == 0) ++alive;
-#pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] = fmaf(e[j], inv, acc[j]);
-    }
+    r0 += step * R;
+    if (r0 < a.rows) load();
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -147,11 +267,18 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const Balance
     atomicAdd(hist + G + 1, mine);
   }
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
+  for (int p = 0; p < NP; ++p)
 #pragma unroll
-    for (int o = LPR; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);   // the warp's row groups
-    if (sub == 0 && c0 + j < G) sh[warp * G + c0 + j] = acc[j];
-  }
+    for (int j = 0; j < H; ++j) {
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1) {                     // the warp's row groups
+        acc[p][j].x += __shfl_xor_sync(0xffffffffu, acc[p][j].x, o);
+        acc[p][j].y += __shfl_xor_sync(0xffffffffu, acc[p][j].y, o);
+      }
+      const int c = (p * LPR + l) * E + 2 * j;
+      if (sub == 0 && c < G) sh[warp * G + c] = acc[p][j].x;
+      if (sub == 0 && c + 1 < G) sh[warp * G + c + 1] = acc[p][j].y;
+    }
   __syncthreads();
   for (int c = threadIdx.x; c < G; c += kThreads) {
     float s = 0.f;
@@ -196,7 +323,7 @@ __global__ void __launch_bounds__(1024) __cluster_dims__(kFinalBlocks, 1, 1)
     float s = 0.f;
     int n = 0;
     if (c0 + lane < G) {
-#pragma unroll 4
+#pragma unroll 10
       for (int b = warp; b < nb; b += 32) {
         s += __ldg(psum + (int64_t)b * G + c0 + lane);
         n += __ldg(cnt + (int64_t)b * (G + 2) + c0 + lane);
@@ -241,72 +368,88 @@ __global__ void __launch_bounds__(1024) __cluster_dims__(kFinalBlocks, 1, 1)
   ptx::cluster_sync();       // no block leaves before its part has been read
 }
 
-template <typename T, int LPR, int V>
-__global__ void __launch_bounds__(kThreads) balance_grad_kernel(const BalanceGradArgs a, const int vec, const int bvec,
-                                                                const int ovec) {
+template <typename T, int LPR, int NP, bool BASE>
+__global__ void __launch_bounds__(kThreads, 2) balance_grad_kernel(const BalanceGradArgs a, const int vec, const int bvec,
+                                                                   const int ovec) {
   pdl_begin();
-  constexpr int kPerWarp = 32 / LPR, kGradRows = V >= 16 ? 2 : kRows;
+  constexpr int E = Pairs<T>::kElems, H = E / 2, R = kFlight<T, NP>;
+  constexpr int kPerWarp = 32 / LPR;
   const int G = (int)a.G, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = lane / LPR, l = lane % LPR, c0 = l * V;
+  const int sub = lane / LPR, l = lane % LPR;
+  const T* logits = static_cast<const T*>(a.logits);
+  const T* base = static_cast<const T*>(a.base);
+  T* out = static_cast<T*>(a.out);
+  const int64_t step = (int64_t)gridDim.x * kWarps * kPerWarp;
+  int64_t r0 = ((int64_t)blockIdx.x * kWarps + warp) * kPerWarp;
+  Row<T, LPR, NP> row[R], add[R];
+  const auto load = [&]() {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const int64_t r = r0 + q * step + sub, rr = r < a.rows ? r : 0;
+      row[q].load(logits + rr * a.l_rs, a.l_cs, l, G, vec, -INFINITY);
+      if (BASE) add[q].load(base + rr * a.b_rs, a.b_cs, l, G, bvec, 0.f);
+    }
+  };
+  if (r0 < a.rows) load();
   // The shares c / C of this lane's columns; a row's lanes hold all of them.
-  float share[V];
+  float2 share[NP][H];
   int total = 0;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int n = c0 + j < G ? __ldg(a.counts + (c0 + j) * a.counts_s) : 0;
-    total += n;
-    share[j] = (float)n;
-  }
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+      const int c = (p * LPR + l) * E + 2 * j;
+      const int n0 = c < G ? __ldg(a.counts + c * a.counts_s) : 0, n1 = c + 1 < G ? __ldg(a.counts + (c + 1) * a.counts_s) : 0;
+      total += n0 + n1;
+      share[p][j] = make_float2((float)n0, (float)n1);
+    }
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const int rows_in = __ldg(a.counts + G * a.counts_s);
   const float scale = total > 0 ? 1.f / (float)total : 0.f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) share[j] *= scale;
+  for (int p = 0; p < NP; ++p)
+#pragma unroll
+    for (int j = 0; j < H; ++j) share[p][j] = mul2(share[p][j], twice(scale));
   const float coef = rows_in > 0 ? __ldg(a.dloss) * ((float)G / (float)rows_in) : 0.f;
-  const T* logits = static_cast<const T*>(a.logits);
-  const T* base = static_cast<const T*>(a.base);
-  T* out = static_cast<T*>(a.out);
-  const int64_t step = (int64_t)gridDim.x * kWarps * kPerWarp;
-  for (int64_t r0 = ((int64_t)blockIdx.x * kWarps + warp) * kPerWarp; r0 < a.rows; r0 += step * kGradRows) {
-    Piece<T, V> p[kGradRows], pb[kGradRows];
+  while (r0 < a.rows) {
 #pragma unroll
-    for (int q = 0; q < kGradRows; ++q) {
-      const int64_t r = r0 + q * step + sub, rr = r < a.rows ? r : 0;
-      p[q].load(logits + rr * a.l_rs, a.l_cs, c0, G, vec, -INFINITY);
-      if (base) pb[q].load(base + rr * a.b_rs, a.b_cs, c0, G, bvec, 0.f);
-    }
-#pragma unroll
-    for (int q = 0; q < kGradRows; ++q) {
+    for (int q = 0; q < R; ++q) {
       const int64_t r = r0 + q * step + sub;
-      float e[V], inv;
-      softmax_row<T, LPR, V>(p[q], e, &inv);
-      float dot = 0.f;
+      float2 e[NP][H];
+      const float inv = softmax_row<T, LPR, NP>(row[q], e);
+      float2 dots = twice(0.f);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        e[j] *= inv;
-        dot = fmaf(share[j], e[j], dot);
-      }
-      dot = lanes_sum<LPR>(dot);
-      if (r >= a.rows) continue;
-      Piece<T, V> o;
-      T* oe = reinterpret_cast<T*>(o.u);
+      for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        // a column that takes no part has a gradient of zero, whatever dloss is
-        const float d = e[j] > 0.f ? coef * e[j] * (share[j] - dot) : 0.f;
-        oe[j] = from_f32<T>(base ? pb[q].at(j) + d : d);
-      }
-      T* dst = out + r * (int64_t)G + c0;
-      if (ovec && c0 + V <= G) {
+        for (int j = 0; j < H; ++j) dots = ptx::fma2_rn(share[p][j], e[p][j], dots);
+      const float dot = lanes_sum<LPR>(dots.x + dots.y) * inv;
+      const float2 w = twice(inv * coef), nd = twice(-dot);
+      T* dst = out + r * (int64_t)G;
 #pragma unroll
-        for (int v = 0; v < Piece<T, V>::kVecs; ++v) reinterpret_cast<uint4*>(dst)[v] = o.u[v];
-      } else {
+      for (int p = 0; p < NP; ++p) {
+        float2 v[H];
+        if (BASE) Pairs<T>::split(add[q].u[p], v);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (c0 + j < G) dst[j] = oe[j];
+        for (int j = 0; j < H; ++j) {
+          const float2 k = mul2(e[p][j], w), d = add2(share[p][j], nd);
+          v[j] = BASE ? ptx::fma2_rn(k, d, v[j]) : mul2(k, d);
+        }
+        const uint4 o = Pairs<T>::join(v);
+        const int c0 = (p * LPR + l) * E;
+        if (r < a.rows) {
+          if (ovec && c0 + E <= G) {
+            *reinterpret_cast<uint4*>(dst + c0) = o;
+          } else {
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+              if (c0 + j < G) dst[c0 + j] = reinterpret_cast<const T*>(&o)[j];
+          }
+        }
       }
     }
+    r0 += step * R;
+    if (r0 < a.rows) load();
   }
 }
 
@@ -315,18 +458,21 @@ int vec_ok(const void* p, int64_t rs, int64_t cs) {
   return cs == 1 && (rs * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 }
 
-// Lanes per row and values per lane for G experts: whole 16-byte pieces, a full
-// warp from 16 lanes on.
+// Lanes per row and 16-byte pieces per lane for G experts: 8 lanes with up to 16
+// columns each, then more lanes; 32 columns a lane (from 513 experts on) leave
+// registers for one row at a time.
 template <typename T, typename F>
 mm_status by_width(int64_t G, F&& f) {
-  constexpr int P = 16 / sizeof(T);
-  if (G <= 4 * P) return f(std::integral_constant<int, 4>(), std::integral_constant<int, P>());
-  if (G <= 8 * P) return f(std::integral_constant<int, 8>(), std::integral_constant<int, P>());
-  if (G <= 16 * P) return f(std::integral_constant<int, 16>(), std::integral_constant<int, P>());
-  if (G <= 32 * P) return f(std::integral_constant<int, 32>(), std::integral_constant<int, P>());
-  if (G <= 64 * P) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2 * P>());
-  if (G <= 128 * P) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 4 * P>());
-  return f(std::integral_constant<int, 32>(), std::integral_constant<int, 32>());
+  constexpr int kSixteen = 16 / Pairs<T>::kElems;      // pieces of 16 columns
+#define QG_WIDTH(LPR, NP) \
+  if (G <= LPR * NP * Pairs<T>::kElems) return f(std::integral_constant<int, LPR>(), std::integral_constant<int, NP>())
+  QG_WIDTH(8, kSixteen / 2);
+  QG_WIDTH(8, kSixteen);
+  QG_WIDTH(16, kSixteen);
+  QG_WIDTH(32, kSixteen);
+  QG_WIDTH(32, 2 * kSixteen);
+#undef QG_WIDTH
+  return MM_ERR_UNSUPPORTED;
 }
 
 // Blocks for `rows` rows: enough for one round of kRows rows a warp, at most `per_sm` per SM.
@@ -335,7 +481,7 @@ int64_t row_blocks(int64_t rows, int rows_per_block, int per_sm) {
   return want < 1 ? 1 : want < most ? want : most;
 }
 
-constexpr int kPartialPerSm = 3;
+constexpr int kPartialPerSm = 2, kGradPerSm = 4;
 
 template <typename T>
 mm_status run_partial(const BalanceArgs& a, void* ws, unsigned* status, cudaStream_t stream) {
@@ -344,7 +490,7 @@ mm_status run_partial(const BalanceArgs& a, void* ws, unsigned* status, cudaStre
   int32_t* cnt = reinterpret_cast<int32_t*>(psum + nb * a.G);
   const size_t smem = (size_t)(kWarps * a.G + a.G + 2) * 4;
   return by_width<T>(a.G, [&](auto lpr, auto v) {
-    return launch_pdl(balance_partial_kernel<T, lpr(), v()>, dim3((unsigned)nb), dim3(kThreads), smem, stream, a,
+    return launch_pdl(balance_partial_kernel<T, decltype(lpr)::value, decltype(v)::value>, dim3((unsigned)nb), dim3(kThreads), smem, stream, a,
                       vec_ok<T>(a.logits, a.l_rs, a.l_cs), psum, cnt, status) == cudaSuccess
                ? MM_OK
                : MM_ERR_CUDA;
@@ -354,20 +500,21 @@ mm_status run_partial(const BalanceArgs& a, void* ws, unsigned* status, cudaStre
 template <typename T>
 mm_status run_grad(const BalanceGradArgs& a, cudaStream_t stream) {
   return by_width<T>(a.G, [&](auto lpr, auto v) {
-    const int64_t nb = row_blocks(a.rows, kWarps * (32 / lpr()), 6);
-    return launch_pdl(balance_grad_kernel<T, lpr(), v()>, dim3((unsigned)nb), dim3(kThreads), 0, stream, a,
-                      vec_ok<T>(a.logits, a.l_rs, a.l_cs), a.base ? vec_ok<T>(a.base, a.b_rs, a.b_cs) : 0,
-                      vec_ok<T>(a.out, a.G, 1)) == cudaSuccess
-               ? MM_OK
-               : MM_ERR_CUDA;
+    constexpr int L = decltype(lpr)::value, P = decltype(v)::value;
+    const dim3 grid((unsigned)row_blocks(a.rows, kWarps * (32 / L), kGradPerSm));
+    const int lv = vec_ok<T>(a.logits, a.l_rs, a.l_cs), ov = vec_ok<T>(a.out, a.G, 1);
+    const cudaError_t e =
+        a.base ? launch_pdl(balance_grad_kernel<T, L, P, true>, grid, dim3(kThreads), 0, stream, a, lv,
+                            vec_ok<T>(a.base, a.b_rs, a.b_cs), ov)
+               : launch_pdl(balance_grad_kernel<T, L, P, false>, grid, dim3(kThreads), 0, stream, a, lv, 0, ov);
+    return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
   });
 }
 
 }  // namespace
 
-// A block takes 32 rows at least (a warp's kRows rows each), so that a few rows
-// leave few partials to add.
-int64_t balance_partial_blocks(int64_t rows) { return row_blocks(rows, kWarps * kRows, kPartialPerSm); }
+// A block takes 32 rows at least, so that a few rows leave few partials to add.
+int64_t balance_partial_blocks(int64_t rows) { return row_blocks(rows, 32, kPartialPerSm); }
 
 size_t balance_workspace_bytes(int64_t rows, int64_t G) {
   return (size_t)balance_partial_blocks(rows) * (size_t)(2 * G + 2) * 4;
