@@ -31,8 +31,10 @@ struct NormArgs {
   FastDiv fd_row;                    // pieces (or elements) of a row
   double* part;                      // [count][chunks] sums of squares
   float eps;
-  float* s;                          // [count][M][ld], the divided matrix
-  int64_t ld;
+  float* s;                          // [count][M][ld], the divided matrix,
+  __half* h;                         // or that times `up` as f16 [count][M][ld] and, `rest` further, what that leaves
+  int64_t ld, rest;
+  float up;
 };
 
 // Sums of squares over the whole range of fp32: values of 2^50 and more, and of
@@ -144,16 +146,37 @@ __device__ __forceinline__ Divisor load_divisor(const NormArgs& a, int64_t b) {
   return d;
 }
 
-template <typename T, bool VEC>
+// HALVES: the state in two f16 parts.
+template <typename T, bool VEC, bool HALVES>
 __global__ void __launch_bounds__(kThreads) divide_kernel(const NormArgs a) {
   pdl_begin();
   const Divisor d = load_divisor(a, blockIdx.x / a.chunks);
   walk<T, VEC>(a, [&](int64_t b, uint32_t r, int64_t c, const auto& e) {
     constexpr int E = sizeof(e) / sizeof(T);
-    float* dst = a.s + (b * a.M + r) * a.ld + c;
     float v[E];
 #pragma unroll
     for (int j = 0; j < E; ++j) v[j] = d.divide(to_f32(e[j]));
+    if constexpr (HALVES) {
+      __half* hi = a.h + (b * a.M + r) * a.ld + c;
+      __half h[E], l[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        h[j] = __float2half_rn(a.up * v[j]);
+        l[j] = __float2half_rn(a.up * v[j] - __half2float(h[j]));
+      }
+      if constexpr (E == 8) {        // ld is a multiple of 8
+        *reinterpret_cast<uint4*>(hi) = *reinterpret_cast<const uint4*>(h);
+        *reinterpret_cast<uint4*>(hi + a.rest) = *reinterpret_cast<const uint4*>(l);
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          hi[j] = h[j];
+          hi[a.rest + j] = l[j];
+        }
+      }
+      return;
+    }
+    float* dst = a.s + (b * a.M + r) * a.ld + c;
     if constexpr (E >= 4) {          // ld is a multiple of 4, c of E
 #pragma unroll
       for (int j = 0; j < E; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
@@ -198,8 +221,16 @@ mm_status run_norm(const OrthoArgs& o, NormArgs a, cudaStream_t stream) {
   const dim3 g((unsigned)blocks), t(kThreads);
   cudaError_t e = vec ? launch_pdl(norm_kernel<T, true>, g, t, 0, stream, a)
                       : launch_pdl(norm_kernel<T, false>, g, t, 0, stream, a);
-  if (e == cudaSuccess)
-    e = vec ? launch_pdl(divide_kernel<T, true>, g, t, 0, stream, a) : launch_pdl(divide_kernel<T, false>, g, t, 0, stream, a);
+  if (e == cudaSuccess) {
+    if (a.h) {
+      if constexpr (sizeof(T) == 2)
+        e = vec ? launch_pdl(divide_kernel<T, true, true>, g, t, 0, stream, a)
+                : launch_pdl(divide_kernel<T, false, true>, g, t, 0, stream, a);
+    } else {
+      e = vec ? launch_pdl(divide_kernel<T, true, false>, g, t, 0, stream, a)
+              : launch_pdl(divide_kernel<T, false, false>, g, t, 0, stream, a);
+    }
+  }
   return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
@@ -264,21 +295,29 @@ mm_status product(const GemmArgs& g, cudaStream_t st) {
   return run_dense_on(path, g, st);
 }
 
-mm_status run_float(const OrthoArgs& o, void* ws, cudaStream_t st) {
-  const FloatPlan p = plan_float(o);
-  uint8_t* w = static_cast<uint8_t*>(ws);
+NormArgs norm_args(const OrthoArgs& o, int chunks, void* part, int64_t ld) {
   NormArgs n;
   memset(&n, 0, sizeof(n));
   n.M = o.M; n.N = o.N; n.count = o.bm.count;
   n.bm = o.bm; n.x = o.x;
-  n.chunks = p.chunks;
-  n.part = reinterpret_cast<double*>(w + p.part);
+  n.chunks = chunks;
+  n.part = static_cast<double*>(part);
   n.eps = o.eps;
+  n.ld = ld;
+  return n;
+}
+mm_status divide(const OrthoArgs& o, const NormArgs& n, cudaStream_t st) {
+  return o.dtype == MM_F32    ? run_norm<float>(o, n, st)
+         : o.dtype == MM_BF16 ? run_norm<__nv_bfloat16>(o, n, st)
+                              : run_norm<__half>(o, n, st);
+}
+
+mm_status run_float(const OrthoArgs& o, void* ws, cudaStream_t st) {
+  const FloatPlan p = plan_float(o);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  NormArgs n = norm_args(o, p.chunks, w + p.part, p.ld);
   n.s = reinterpret_cast<float*>(w + p.s[0]);
-  n.ld = p.ld;
-  mm_status s = o.dtype == MM_F32    ? run_norm<float>(o, n, st)
-                : o.dtype == MM_BF16 ? run_norm<__nv_bfloat16>(o, n, st)
-                                     : run_norm<__half>(o, n, st);
+  mm_status s = divide(o, n, st);
   const bool tall = o.M > o.N;
   const int64_t xs = o.M * p.ld, as = p.m * p.ldm;
   float *A = reinterpret_cast<float*>(w + p.a), *B = reinterpret_cast<float*>(w + p.b);
@@ -318,11 +357,165 @@ mm_status run_float(const OrthoArgs& o, void* ws, cudaStream_t st) {
                               : run_round<__half>(o, X, p.ld, st);
 }
 
+// ------------------------------------------------------------------ the chain of 16-bit matrices
+//
+// The products' operands are f16 (11 bits; X, A and B each rounded once a step),
+// their sums fp32.  What is rounded to 11 bits only enters the correction (b A + c A A) X;
+// a X itself comes from the state, which is held as two f16 parts (22 bits), since
+// the iteration magnifies small singular values by a in every step and the state's
+// rounding with them: with the state rounded to 11 bits the result was off by 4e-2
+// for matrices with a few strong directions, so it is off by 1.7e-3 (one rounding of
+// a bf16 output) for those and 2.2e-3 for random ones.  Each array has a power of
+// two of its own, the largest that cannot overflow: the singular values start at
+// 1 at most and the polynomial's maximum bounds every later step's, so that f16's
+// range is used from the top (a value below 2^-29 of the bound loses digits of its
+// high part, below 2^-39 the pair has none).
+// A and B are symmetric: only the lower triangle's tiles are computed.
+
+double power_below(double x) {
+  if (!(x > 0.)) return 1.;
+  int e = (int)std::floor(std::log2(x));
+  e = e < -60 ? -60 : e > 30 ? 30 : e;
+  return std::ldexp(1., e);
+}
+// The largest |f| of f(s) = s (a + b s^2 + c s^4) on [0, u], and of b l + c l^2 on [0, u^2].
+double odd_bound(double a, double b, double c, double u) {
+  const auto f = [&](double s) { return std::fabs(s * (a + s * s * (b + s * s * c))); };
+  double most = f(u);
+  const double qa = 5. * c, qb = 3. * b, disc = qb * qb - 4. * qa * a;
+  if (disc >= 0.) {
+    for (int sign = -1; sign <= 1; sign += 2) {
+      const double t = qa != 0. ? (-qb + sign * std::sqrt(disc)) / (2. * qa) : qb != 0. ? -a / qb : -1.;
+      if (t > 0. && t < u * u) most = std::fmax(most, f(std::sqrt(t)));
+    }
+  }
+  return most;
+}
+double even_bound(double b, double c, double u) {
+  const auto f = [&](double l) { return std::fabs(l * (b + l * c)); };
+  double most = f(u * u);
+  const double l = c != 0. ? -b / (2. * c) : -1.;
+  if (l > 0. && l < u * u) most = std::fmax(most, f(l));
+  return most;
+}
+
+struct HalfScales { double x, a, b; };       // powers of two of X, A, B in a step
+constexpr double kHalfTop = 32768.;
+constexpr double kSlack = 1.02;              // what the roundings may add to a bound
+// False where the bounds leave the range that the scales cover.
+bool half_scales(const OrthoArgs& o, HalfScales (&k)[MM_ORTHO_MAX_STEPS + 1]) {
+  double u = kSlack;
+  for (int i = 0; i <= o.steps; ++i) {
+    if (!(u < 1e6)) return false;
+    k[i].x = power_below(kHalfTop / u);
+    if (i == o.steps) break;
+    const float* c = o.coef + 3 * i;
+    k[i].a = power_below(kHalfTop / (u * u));
+    k[i].b = power_below(kHalfTop / (kSlack * even_bound(c[1], c[2], u)));
+    u = kSlack * odd_bound(c[0], c[1], c[2], u);
+  }
+  return true;
+}
+
+struct HalfPlan {
+  int64_t m, ld, ldm;
+  int chunks;
+  size_t part, x[2], a, b, bytes;
+};
+HalfPlan plan_half(const OrthoArgs& o) {
+  HalfPlan p;
+  p.m = o.M < o.N ? o.M : o.N;
+  p.ld = round_up(o.N, 8);
+  p.ldm = round_up(p.m, 8);
+  p.chunks = norm_chunks(o.M, o.N, o.bm.count);
+  const size_t x = align256((size_t)o.bm.count * o.M * p.ld * 4), sq = align256((size_t)o.bm.count * p.m * p.ldm * 2);
+  p.part = 0;
+  p.x[0] = align256((size_t)o.bm.count * p.chunks * 8);
+  p.x[1] = p.x[0] + x;
+  p.a = p.x[1] + x;
+  p.b = p.a + sq;
+  p.bytes = p.b + sq;
+  return p;
+}
+
+// 16-bit matrices whose Gram product is worth the tensor cores.
+bool half_chain(const OrthoArgs& o) {
+  const int64_t m = o.M < o.N ? o.M : o.N, n = o.M < o.N ? o.N : o.M;
+  return o.dtype != MM_F32 && choose(m > 1, tensor_pays(m, m, n, o.bm.count)) == MM_PATH_TENSOR;
+}
+
+mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream_t st) {
+  unsigned* status = device_status_ptr();
+  if (!status) return MM_ERR_CUDA;
+  const HalfPlan p = plan_half(o);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const int64_t xs = o.M * p.ld, rest = o.bm.count * xs, as = p.m * p.ldm;
+  NormArgs n = norm_args(o, p.chunks, w + p.part, p.ld);
+  n.h = reinterpret_cast<__half*>(w + p.x[0]);
+  n.rest = rest;
+  n.up = (float)k[0].x;
+  mm_status s = divide(o, n, st);
+  const bool tall = o.M > o.N;
+  void *A = w + p.a, *B = w + p.b;
+  for (int i = 0; i < o.steps && s == MM_OK; ++i) {
+    const void* X = w + p.x[i & 1];
+    const double a = o.coef[3 * i], b = o.coef[3 * i + 1], c = o.coef[3 * i + 2];
+    OrthoProduct g;
+    memset(&g, 0, sizeof(g));
+    g.sym = 1;
+    g.y_dtype = MM_F16;
+    g.M = g.N = p.m;
+    g.K = tall ? o.M : o.N;
+    g.count = o.bm.count;
+    g.a = g.b = X;
+    g.a_step = g.b_step = xs;
+    g.a_rs = g.b_cs = tall ? 1 : p.ld;
+    g.a_cs = g.b_rs = tall ? p.ld : 1;
+    g.y = A; g.y_rs = p.ldm; g.y_step = as;
+    g.alpha = (float)(k[i].a / (k[i].x * k[i].x));
+    if ((s = launch_tc_ortho(g, status, st)) != MM_OK) return s;
+    g.K = p.m;
+    g.a = g.b = g.c = A;
+    g.a_step = g.b_step = g.c_step = as;
+    g.a_rs = g.b_cs = g.c_rs = p.ldm;
+    g.a_cs = g.b_rs = 1;
+    g.y = B;
+    g.alpha = (float)(k[i].b * c / (k[i].a * k[i].a));
+    g.beta = (float)(k[i].b * b / k[i].a);
+    if ((s = launch_tc_ortho(g, status, st)) != MM_OK) return s;
+    memset(&g, 0, sizeof(g));
+    g.M = o.M; g.N = o.N; g.K = p.m;
+    g.count = o.bm.count;
+    g.a = tall ? X : B; g.a_step = tall ? xs : as; g.a_rs = tall ? p.ld : p.ldm; g.a_cs = 1;
+    g.b = tall ? B : X; g.b_step = tall ? as : xs; g.b_rs = tall ? p.ldm : p.ld; g.b_cs = 1;
+    g.c = X; g.c_rs = p.ld; g.c_step = xs; g.c_lo = rest;
+    const bool last = i + 1 == o.steps;
+    const double up = last ? (double)o.scale : k[i + 1].x;
+    g.alpha = (float)(up / (k[i].b * k[i].x));
+    g.beta = (float)(up * a / k[i].x);
+    g.y_dtype = last ? o.dtype : MM_F16;
+    g.y = last ? o.out : w + p.x[(i + 1) & 1];
+    g.y_rs = last ? o.N : p.ld;
+    g.y_step = last ? o.M * o.N : xs;
+    g.y_lo = last ? 0 : 1;
+    s = launch_tc_ortho(g, status, st);
+  }
+  return finish(s, MM_PATH_TENSOR);
+}
+
 }  // namespace
 
-size_t ortho_workspace_bytes(const OrthoArgs& o) { return plan_float(o).bytes; }
+size_t ortho_workspace_bytes(const OrthoArgs& o) {
+  // The coefficients are not known yet: room for either chain of 16-bit matrices.
+  const size_t f = plan_float(o).bytes;
+  if (!half_chain(o)) return f;
+  const size_t h = plan_half(o).bytes;
+  return h > f ? h : f;
+}
 
 mm_status launch_ortho(const OrthoArgs& o, void* workspace, cudaStream_t stream) {
+  HalfScales k[MM_ORTHO_MAX_STEPS + 1];
+  if (o.steps > 0 && half_chain(o) && half_scales(o, k)) return run_half(o, k, workspace, stream);
   return run_float(o, workspace, stream);
 }
 

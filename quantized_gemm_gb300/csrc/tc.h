@@ -24,6 +24,21 @@ mm_status launch_tc_qlinear(const QLinearArgs& q, void* workspace, unsigned* sta
 mm_status launch_tc_int8(const Int8Args& q, const void* a, int64_t lda, const void* b, int64_t ldb, int b_mn,
                          unsigned* status, cudaStream_t stream);
 
+// A product of the orthogonalised update's chain, over `count` matrices of f16
+// operands: sym != 0, Y = f16(alpha A B + beta C), symmetric (C optional); else
+// the state's step alpha A B + beta (C + its rest c_lo further), out as f16 and
+// the rest y_lo matrices further, or with y_lo = 0 rounded to y_dtype.
+struct OrthoProduct {
+  int sym, y_dtype;
+  int64_t M, N, K, count;
+  const void* a; int64_t a_rs, a_cs, a_step;
+  const void* b; int64_t b_rs, b_cs, b_step;
+  const void* c; int64_t c_rs, c_step, c_lo;
+  void* y; int64_t y_rs, y_step, y_lo;
+  float alpha, beta;
+};
+mm_status launch_tc_ortho(const OrthoProduct& g, unsigned* status, cudaStream_t stream);
+
 bool tc_grouped_supported(const GroupedArgs& g);
 size_t tc_grouped_workspace_bytes(const GroupedArgs& g);
 // GroupedArgs with wq != 0 take the fused-dequantisation kernel (CTA pairs):

@@ -50,6 +50,8 @@
 //             low-rank adapters (see lowrank_tc.cu).
 //   kInt8     kDense over f16 copies of int8 operands; epilogue
 //             y = (acc * a_scale[m]) * b_scale[n] + bias[n], rounded once.
+//   kSym      kDense with a symmetric result: the lower triangle's tiles only.
+//   kState    kDense plus a state held in two f16 parts.
 //   kSkinny   kDense for at most 64 rows of A': 256-column tiles whose
 //             k-blocks are split over the CTAs of a cluster (non-persistent,
 //             one tile per cluster), so that B' streams through every SM with
@@ -204,6 +206,26 @@ __device__ __forceinline__ bool get_tile(const TcParams& p, int64_t t, int64_t t
   const uint32_t tt = (uint32_t)t;
   const uint32_t b = fast_div(tt, p.fd_per_batch);
   const uint32_t r = tt - b * p.fd_per_batch.d;
+  if (MODE == kSym) {
+    // Row by row of the lower triangle.  256-row tiles: row i has i + 1 tiles;
+    // 128-row tiles: rows 2a and 2a + 1 have a + 1 each (see sym_tiles).
+    constexpr uint32_t kHalf = Geo<MODE, PAIR>::kTileRows == BN ? 1 : 2;   // row tiles per square of 256
+    const uint32_t q = kHalf == 1 ? r : r >> 1;                            // a (a + 1) / 2 tiles (pairs of them) before row a
+    uint32_t i = (uint32_t)((sqrtf(8.f * (float)q + 1.f) - 1.f) * 0.5f);
+    while ((i + 1) * (i + 2) / 2 <= q) ++i;
+    while (i * (i + 1) / 2 > q) --i;
+    uint32_t w = r - kHalf * (i * (i + 1) / 2), mtile = i * kHalf;
+    if (w > i) { w -= i + 1; ++mtile; }
+    ti.batch = b;
+    ti.g = 0;
+    ti.m0 = (int64_t)mtile * Geo<MODE, PAIR>::kTileRows;
+    ti.n0 = (int64_t)w * BN;
+    ti.a_row = (int32_t)ti.m0;
+    ti.a_b = (int32_t)batch_off(p, p.a_bc, b);
+    ti.b_b = (int32_t)batch_off(p, p.b_bc, b);
+    ti.rows = (int32_t)min((int64_t)Geo<MODE, PAIR>::kTileRows, p.M - ti.m0);
+    return true;
+  }
   const uint32_t gband = fast_div(r, p.fd_band);
   const uint32_t w = r - gband * p.fd_band.d;
   uint32_t mtile, ntile;
@@ -529,6 +551,24 @@ __device__ __forceinline__ void add_c32(const TcParams& p, const uint16_t* crow,
 #pragma unroll
     for (int j = 0; j < 32; ++j)
       if (n + j < p.N) v[j] = __fmaf_rn(p.beta, unpack16(crow[(n + j) * p.c_cs], p.out_f16), v[j]);
+  }
+}
+
+// v[j] += beta * (C[n + j] + the rest of it), kState: f16 rows of whole 16-byte
+// pieces (values past N are read from the rows' padding and not stored).
+__device__ __forceinline__ void add_state32(const TcParams& p, const uint16_t* crow, int64_t n, float (&v)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (n + 8 * q >= p.c_rs) break;
+    const uint4 hi = __ldg(reinterpret_cast<const uint4*>(crow + n) + q), lo = __ldg(reinterpret_cast<const uint4*>(crow + p.c_lo + n) + q);
+    const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hw[e]));
+      const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&lw[e]));
+      v[q * 8 + 2 * e] = __fmaf_rn(p.beta, h.x + l.x, v[q * 8 + 2 * e]);
+      v[q * 8 + 2 * e + 1] = __fmaf_rn(p.beta, h.y + l.y, v[q * 8 + 2 * e + 1]);
+    }
   }
 }
 
@@ -1107,7 +1147,7 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
       if constexpr (MODE == kInt8) {
         if (rok) row_scale = __ldg(static_cast<const float*>(p.sa.ptr) + (ti.m0 + roff + rl) * p.sa.vs);
       }
-      if constexpr (MODE == kDense || MODE == kSkinny || MODE == kInt8) {
+      if constexpr (MODE == kDense || MODE == kSkinny || MODE == kInt8 || MODE == kSym || MODE == kState) {
         if (p.y_tma) {
           // The warp's 32 rows x 64 columns: into registers, release the
           // accumulator, then alpha/beta/C and the rounding to 16 bits.
@@ -1136,7 +1176,10 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(r[h][j]);
-              if (crow) add_c32(p, crow, ncol + 32 * h, v);
+              if (crow) {
+                if constexpr (MODE == kState) add_state32(p, crow, ncol + 32 * h, v);
+                else add_c32(p, crow, ncol + 32 * h, v);
+              }
             }
             if (lane == 0) bulk_wait_read_all();
             __syncwarp();
@@ -1151,6 +1194,45 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
             if (lane == 0 && rbase < rows_t) {
               tma_store_3d(tmY, sbox, (int32_t)(ncol + 32 * h), yrow0, yb);
               bulk_commit();
+            }
+            if constexpr (MODE == kSym) {
+              // The box transposed, where it falls into a tile that is not computed.
+              constexpr int TR = Geo<MODE, PAIR>::kTileRows;
+              const int32_t c0 = (int32_t)(ncol + 32 * h);
+              if (rbase < rows_t && (yrow0 / BN) * BN > (c0 / TR) * TR + TR - 1) {
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)      // row j of the box takes this lane's column j
+                  sts16(sbox + (uint32_t)j * 64 + ((((uint32_t)lane >> 3) ^ (((uint32_t)j >> 1) & 3u)) << 4) + ((uint32_t)lane & 7u) * 2,
+                        __half_as_ushort(__float2half_rn(v[j])));
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0 && c0 < p.N) {
+                  tma_store_3d(tmY, sbox, yrow0, c0, yb);
+                  bulk_commit();
+                }
+              }
+            }
+            if constexpr (MODE == kState) {
+              // The rest of each value after its f16 rounding, y_lo matrices further.
+              if (p.y_lo != 0) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  sts128(sbox + (uint32_t)lane * 64 + (((uint32_t)q ^ ((uint32_t)(lane >> 1) & 3u)) << 4),
+                         make_uint4(pack2(v[8 * q], v[8 * q + 1], 1), pack2(v[8 * q + 2], v[8 * q + 3], 1),
+                                    pack2(v[8 * q + 4], v[8 * q + 5], 1), pack2(v[8 * q + 6], v[8 * q + 7], 1)));
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0 && rbase < rows_t) {
+                  tma_store_3d(tmY, sbox, (int32_t)(ncol + 32 * h), yrow0, yb + (int32_t)p.y_lo);
+                  bulk_commit();
+                }
+              }
             }
           }
           continue;
@@ -1209,7 +1291,10 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(r[h][j]);
-            if (crow) add_c32(p, crow, n, v);
+            if (crow) {
+              if constexpr (MODE == kState) add_state32(p, crow, n, v);
+              else add_c32(p, crow, n, v);
+            }
           }
           uint32_t w[16];
 #pragma unroll
@@ -1398,7 +1483,7 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
   // the previous kernel on the stream is finishing: the set-up above overlaps
   // its tail, and nothing below touches global memory before it completes.
   if (MODE != kSkinny || !p.c_late) pdl_wait();
-  if constexpr (MODE == kDense || MODE == kTF32 || MODE == kInt8) pdl_trigger();
+  if constexpr (MODE == kDense || MODE == kTF32 || MODE == kInt8 || MODE == kSym || MODE == kState) pdl_trigger();
   const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
 
   if (warp == 0) {
@@ -1658,7 +1743,7 @@ mm_status launch_kernel(const OperandPlan& a, const OperandPlan& b, const CUtens
                         const TcParams& p_in, int64_t work, cudaStream_t stream) {
   constexpr int kSmem = Cfg<MODE, PAIR>::kSmem, kThreadsM = Cfg<MODE, PAIR>::kThreads;
   TcParams p = p_in;
-  if (MODE != kDense && MODE != kInt8) p.y_tma = 0;
+  if (MODE != kDense && MODE != kInt8 && MODE != kSym && MODE != kState) p.y_tma = 0;
   if (cudaFuncSetAttribute(tc_gemm_kernel<MODE, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
       cudaSuccess)
     return MM_ERR_CUDA;
@@ -1707,6 +1792,14 @@ mm_status launch_kernel(const OperandPlan& a, const OperandPlan& b, const CUtens
                                                                                                       : MM_ERR_CUDA;
 }
 
+// Tiles of mt row tiles (256 rows in a pair, 128 else) that touch the lower
+// triangle of a symmetric product with 256-column tiles.
+int64_t sym_tiles(int64_t mt, bool pair) {
+  if (pair) return mt * (mt + 1) / 2;
+  const int64_t a = mt / 2;
+  return a * (a + 1) + (mt & 1 ? a + 1 : 0);
+}
+
 }  // namespace
 
 mm_status launch_tc(int mode, bool pair, const OperandPlan& a, const OperandPlan& b, TcParams& p,
@@ -1722,9 +1815,10 @@ mm_status launch_tc(int mode, bool pair, const OperandPlan& a, const OperandPlan
     const int64_t cols = BN;
     p.mt = (p.M + rows - 1) / rows;
     p.nt = (p.N + cols - 1) / cols;
-    p.tiles = p.mt * p.nt * p.bm.count;
+    const int64_t per_matrix = mode == kSym ? sym_tiles(p.mt, pair) : p.mt * p.nt;
+    p.tiles = per_matrix * p.bm.count;
     if (p.tiles >= (1ll << 31) || p.mt * p.nt >= (1ll << 31)) return MM_ERR_UNSUPPORTED;
-    const uint32_t per_batch = (uint32_t)(p.mt * p.nt);
+    const uint32_t per_batch = (uint32_t)per_matrix;
     const uint32_t bands = (uint32_t)((p.mt + kGroupM - 1) / kGroupM);
     p.fd_per_batch = make_fastdiv(per_batch);
     p.fd_band = make_fastdiv((uint32_t)(kGroupM * p.nt));
@@ -1765,6 +1859,12 @@ mm_status launch_tc(int mode, bool pair, const OperandPlan& a, const OperandPlan
     case kInt8:
       return pair ? launch_kernel<kInt8, true>(a, b, ms, mz, p, work, stream)
                   : launch_kernel<kInt8, false>(a, b, ms, mz, p, work, stream);
+    case kSym:
+      return pair ? launch_kernel<kSym, true>(a, b, ms, mz, p, work, stream)
+                  : launch_kernel<kSym, false>(a, b, ms, mz, p, work, stream);
+    case kState:
+      return pair ? launch_kernel<kState, true>(a, b, ms, mz, p, work, stream)
+                  : launch_kernel<kState, false>(a, b, ms, mz, p, work, stream);
     case kGroupedQ:  // CTA pairs only
       if (!pair || !s) return MM_ERR_UNSUPPORTED;
       return launch_kernel<kGroupedQ, true>(a, b, ms, mz, p, work, stream);
@@ -1974,6 +2074,62 @@ mm_status launch_tc_int8(const Int8Args& q, const void* a, int64_t lda, const vo
     p.pair_tail = pair && plan_operand(a, MM_F16, g.M, g.K, lda, 1, g.bm, g.a.bstride, BM / 2, &tail);
     if (p.pair_tail) p.idesc_tail = make_idesc_rows(1, 0, pb.mn_major, BM);
     const mm_status st = launch_tc(kInt8, pair, pa, pb, p, stream, p.pair_tail ? &tail : nullptr, p.y_tma ? &ymap : nullptr);
+    if (st != MM_ERR_UNSUPPORTED || !pair) return st;
+  }
+  return MM_ERR_UNSUPPORTED;
+}
+
+// ------------------------------------------------------------------ the orthogonalised update's products
+
+mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t stream) {
+  if (!status) return MM_ERR_CUDA;
+  GemmArgs g;
+  memset(&g, 0, sizeof(g));
+  g.dtype = o.y_dtype;
+  g.M = o.M; g.N = o.N; g.K = o.K;
+  g.bm.nb = 1;
+  for (int d = 0; d < kMaxBatchDims; ++d) g.bm.shape[d] = 1;
+  g.bm.shape[0] = g.bm.count = o.count;
+  g.y.ptr = o.y; g.y.rs = o.y_rs; g.y.cs = 1; g.y.bstride[0] = o.y_step;
+  TcParams p;
+  init_params(&p);
+  p.M = g.M; p.N = g.N; p.K = g.K;
+  p.bm = g.bm;
+  p.out_f16 = o.y_dtype == MM_F16;
+  p.y = o.y;
+  p.y_rs = o.y_rs;
+  p.y_bstride[0] = o.y_step;
+  p.y_vec = (reinterpret_cast<uintptr_t>(o.y) & 15) == 0 && o.y_rs % 8 == 0 && (o.y_step % 8 == 0 || o.count == 1);
+  p.alpha = o.alpha;
+  p.beta = o.beta;
+  if (o.c) {
+    p.c = o.c;
+    p.c_rs = o.c_rs; p.c_cs = 1; p.c_vec = 1;
+    p.c_bstride[0] = o.c_step;
+    p.c_lo = o.c_lo;
+  }
+  p.status = status;
+  OperandPlan ymap;
+  // The rests lie behind all the high parts: the map spans both.
+  GemmArgs ym = g;
+  if (o.y_lo) {
+    ym.bm.shape[0] = ym.bm.count = 2 * o.count;
+    p.y_lo = o.count;
+  }
+  plan_output(ym, &p, &ymap);
+  if ((o.sym || o.y_lo) && !p.y_tma) return MM_ERR_UNSUPPORTED;
+  const int mode = o.sym ? kSym : kState;
+  const int64_t as[kMaxBatchDims] = {o.a_step}, bs[kMaxBatchDims] = {o.b_step};
+  for (int attempt = use_pair(g.M, g.K) ? 0 : 1; attempt < 2; ++attempt) {
+    const bool pair = attempt == 0;
+    OperandPlan a, b, tail;
+    if (!plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, g.bm, as, BM, &a) ||
+        !plan_operand(o.b, MM_F16, g.N, g.K, o.b_cs, o.b_rs, g.bm, bs, pair ? BN / 2 : BN, &b))
+      return MM_ERR_UNSUPPORTED;
+    p.idesc = make_idesc(1, a.mn_major, b.mn_major, pair);
+    p.pair_tail = pair && !a.mn_major && plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, g.bm, as, BM / 2, &tail);
+    if (p.pair_tail) p.idesc_tail = make_idesc_rows(1, 0, b.mn_major, BM);
+    const mm_status st = launch_tc(mode, pair, a, b, p, stream, p.pair_tail ? &tail : nullptr, p.y_tma ? &ymap : nullptr);
     if (st != MM_ERR_UNSUPPORTED || !pair) return st;
   }
   return MM_ERR_UNSUPPORTED;

@@ -27,7 +27,12 @@ constexpr int kTileK = 64;    // one 128-byte swizzle row of 16-bit elements
 // adapters), accumulated on top.
 // kInt8: a dense product of f16 copies of int8 operands whose epilogue
 // multiplies by a scale per row and per column and adds a bias.
-enum TcMode { kDense = 0, kGrouped = 1, kQLinear = 2, kGroupedQ = 3, kTF32 = 4, kSkinny = 5, kLowRank = 6, kInt8 = 7 };
+// kSym: a dense f16 product whose result is symmetric (M = N): only the tiles
+// that touch the lower triangle are computed, and their 32 x 32 boxes are also
+// stored transposed where the tile on the other side was left out.
+// kState: a dense f16 product plus beta times a state held as two f16 values
+// (high part and rest); the sum goes out as such a pair, or rounded to T.
+enum TcMode { kDense = 0, kGrouped = 1, kQLinear = 2, kGroupedQ = 3, kTF32 = 4, kSkinny = 5, kLowRank = 6, kInt8 = 7, kSym = 8, kState = 9 };
 
 struct TcParams {
   int64_t M, N, K;
@@ -65,6 +70,7 @@ struct TcParams {
   int64_t c_bstride[kMaxBatchDims];
   int64_t c_rs, c_cs, c_gs;                    // c_gs: grouped bias row stride per group
   int c_vec, c_live;                           // c_live: C is Y
+  int64_t c_lo, y_lo;                          // kState: from the high part to the rest (elements; batch coordinates, 0: Y is T)
   int c_late, c_f32;                           // kSkinny: GemmArgs::c_late, c_f32
   // QLinear epilogue: zero-point correction from the operand sums, then requantisation
   VecView sa, sb, za, zb;

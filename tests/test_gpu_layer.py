@@ -312,9 +312,9 @@ def test_orthogonalize(shape, dtype):
 @pytest.mark.parametrize("shape", [(3, 20, 33), (2, 2, 70, 30), (5, 130, 64), (1, 1, 8), (40, 17, 17), (3, 136, 264)])
 def test_orthogonalize_stacks(shape, dtype):
     X = rand_tensor(shape, dtype, sum(shape), DEV)
-    Y = _check_ortho(X, scale=0.7)
-    flat = X.reshape((-1,) + shape[-2:])
-    assert torch.equal(Y.reshape(flat.shape)[0], qg.mm_orthogonalize(flat[:1].contiguous(), scale=0.7)[0])
+    _check_ortho(X, scale=0.7)
+    # alone, a matrix may take other kernels (the choice goes by the work of the stack): the same bound, not the same bits
+    _check_ortho(X.reshape((-1,) + shape[-2:])[:1], scale=0.7)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
