@@ -31,8 +31,8 @@ struct NormArgs {
   FastDiv fd_row;                    // pieces (or elements) of a row
   double* part;                      // [count][chunks] sums of squares
   float eps;
-  float* s;                          // [count][M][ld], the divided matrix,
-  __half* h;                         // or that times `up` as f16 [count][M][ld] and, `rest` further, what that leaves
+  float* s;                          // [count][M][ld], the divided matrix, and
+  __half* h;                         // that times `up` as f16 [count][M][ld] and, `rest` further, what that leaves (NULL: not wanted)
   int64_t ld, rest;
   float up;
 };
@@ -146,43 +146,44 @@ __device__ __forceinline__ Divisor load_divisor(const NormArgs& a, int64_t b) {
   return d;
 }
 
-// HALVES: the state in two f16 parts.
-template <typename T, bool VEC, bool HALVES>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) divide_kernel(const NormArgs a) {
   pdl_begin();
   const Divisor d = load_divisor(a, blockIdx.x / a.chunks);
   walk<T, VEC>(a, [&](int64_t b, uint32_t r, int64_t c, const auto& e) {
     constexpr int E = sizeof(e) / sizeof(T);
+    const int64_t at = (b * a.M + r) * a.ld + c;          // ld is a multiple of 8, c of E
     float v[E];
 #pragma unroll
     for (int j = 0; j < E; ++j) v[j] = d.divide(to_f32(e[j]));
-    if constexpr (HALVES) {
-      __half* hi = a.h + (b * a.M + r) * a.ld + c;
-      __half h[E], l[E];
+    if (a.h) {
+      __align__(16) __half h[E], l[E];
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         h[j] = __float2half_rn(a.up * v[j]);
         l[j] = __float2half_rn(a.up * v[j] - __half2float(h[j]));
       }
-      if constexpr (E == 8) {        // ld is a multiple of 8
-        *reinterpret_cast<uint4*>(hi) = *reinterpret_cast<const uint4*>(h);
-        *reinterpret_cast<uint4*>(hi + a.rest) = *reinterpret_cast<const uint4*>(l);
+      if constexpr (E == 8) {
+        *reinterpret_cast<uint4*>(a.h + at) = *reinterpret_cast<const uint4*>(h);
+        *reinterpret_cast<uint4*>(a.h + a.rest + at) = *reinterpret_cast<const uint4*>(l);
+      } else if constexpr (E == 4) {
+        *reinterpret_cast<uint2*>(a.h + at) = *reinterpret_cast<const uint2*>(h);
+        *reinterpret_cast<uint2*>(a.h + a.rest + at) = *reinterpret_cast<const uint2*>(l);
       } else {
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-          hi[j] = h[j];
-          hi[a.rest + j] = l[j];
+          a.h[at + j] = h[j];
+          a.h[a.rest + at + j] = l[j];
         }
       }
-      return;
     }
-    float* dst = a.s + (b * a.M + r) * a.ld + c;
-    if constexpr (E >= 4) {          // ld is a multiple of 4, c of E
+    if (!a.s) return;
+    if constexpr (E >= 4) {
 #pragma unroll
-      for (int j = 0; j < E; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      for (int j = 0; j < E; j += 4) *reinterpret_cast<float4*>(a.s + at + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j) dst[j] = v[j];
+      for (int j = 0; j < E; ++j) a.s[at + j] = v[j];
     }
   });
 }
@@ -221,16 +222,8 @@ mm_status run_norm(const OrthoArgs& o, NormArgs a, cudaStream_t stream) {
   const dim3 g((unsigned)blocks), t(kThreads);
   cudaError_t e = vec ? launch_pdl(norm_kernel<T, true>, g, t, 0, stream, a)
                       : launch_pdl(norm_kernel<T, false>, g, t, 0, stream, a);
-  if (e == cudaSuccess) {
-    if (a.h) {
-      if constexpr (sizeof(T) == 2)
-        e = vec ? launch_pdl(divide_kernel<T, true, true>, g, t, 0, stream, a)
-                : launch_pdl(divide_kernel<T, false, true>, g, t, 0, stream, a);
-    } else {
-      e = vec ? launch_pdl(divide_kernel<T, true, false>, g, t, 0, stream, a)
-              : launch_pdl(divide_kernel<T, false, false>, g, t, 0, stream, a);
-    }
-  }
+  if (e == cudaSuccess)
+    e = vec ? launch_pdl(divide_kernel<T, true>, g, t, 0, stream, a) : launch_pdl(divide_kernel<T, false>, g, t, 0, stream, a);
   return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
@@ -254,7 +247,7 @@ struct FloatPlan {
 FloatPlan plan_float(const OrthoArgs& o) {
   FloatPlan p;
   p.m = o.M < o.N ? o.M : o.N;
-  p.ld = round_up(o.N, 4);
+  p.ld = round_up(o.N, 8);
   p.ldm = round_up(p.m, 4);
   p.chunks = norm_chunks(o.M, o.N, o.bm.count);
   const size_t x = align256((size_t)o.bm.count * o.M * p.ld * 4), sq = align256((size_t)o.bm.count * p.m * p.ldm * 4);
@@ -357,7 +350,7 @@ mm_status run_float(const OrthoArgs& o, void* ws, cudaStream_t st) {
                               : run_round<__half>(o, X, p.ld, st);
 }
 
-// ------------------------------------------------------------------ the chain of 16-bit matrices
+// ------------------------------------------------------------------ the chain on the tensor cores
 //
 // The products' operands are f16 (11 bits; X, A and B each rounded once a step),
 // their sums fp32.  What is rounded to 11 bits only enters the correction (b A + c A A) X;
@@ -371,6 +364,11 @@ mm_status run_float(const OrthoArgs& o, void* ws, cudaStream_t st) {
 // range is used from the top (a value below 2^-29 of the bound loses digits of its
 // high part, below 2^-39 the pair has none).
 // A and B are symmetric: only the lower triangle's tiles are computed.
+//
+// fp32 matrices take the same chain with every operand split into two f16 values
+// (22 bits) and three products each, and a state in fp32 beside them.  (Three tf32
+// products of fp32 operands took 1.49 ms for 2048 x 2048 and were off by 1.8e-5:
+// their additions truncate, 3 K / 8 times a sum; see kSymF.)
 
 double power_below(double x) {
   if (!(x > 0.)) return 1.;
@@ -420,7 +418,7 @@ bool half_scales(const OrthoArgs& o, HalfScales (&k)[MM_ORTHO_MAX_STEPS + 1]) {
 struct HalfPlan {
   int64_t m, ld, ldm;
   int chunks;
-  size_t part, x[2], a, b, bytes;
+  size_t part, x[2], a, b, s, bytes;
 };
 HalfPlan plan_half(const OrthoArgs& o) {
   HalfPlan p;
@@ -428,20 +426,21 @@ HalfPlan plan_half(const OrthoArgs& o) {
   p.ld = round_up(o.N, 8);
   p.ldm = round_up(p.m, 8);
   p.chunks = norm_chunks(o.M, o.N, o.bm.count);
-  const size_t x = align256((size_t)o.bm.count * o.M * p.ld * 4), sq = align256((size_t)o.bm.count * p.m * p.ldm * 2);
+  const size_t x = align256((size_t)o.bm.count * o.M * p.ld * 4), sq = align256((size_t)o.bm.count * p.m * p.ldm * (o.dtype == MM_F32 ? 4 : 2));
   p.part = 0;
   p.x[0] = align256((size_t)o.bm.count * p.chunks * 8);
   p.x[1] = p.x[0] + x;
   p.a = p.x[1] + x;
   p.b = p.a + sq;
-  p.bytes = p.b + sq;
+  p.s = p.b + sq;
+  p.bytes = p.s + (o.dtype == MM_F32 ? x : 0);
   return p;
 }
 
-// 16-bit matrices whose Gram product is worth the tensor cores.
+// Matrices whose Gram product is worth the tensor cores.
 bool half_chain(const OrthoArgs& o) {
   const int64_t m = o.M < o.N ? o.M : o.N, n = o.M < o.N ? o.N : o.M;
-  return o.dtype != MM_F32 && choose(m > 1, tensor_pays(m, m, n, o.bm.count)) == MM_PATH_TENSOR;
+  return choose(m > 1, tensor_pays(m, m, n, o.bm.count)) == MM_PATH_TENSOR;
 }
 
 mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream_t st) {
@@ -454,6 +453,9 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
   n.h = reinterpret_cast<__half*>(w + p.x[0]);
   n.rest = rest;
   n.up = (float)k[0].x;
+  const bool split = o.dtype == MM_F32;
+  float* S = split ? reinterpret_cast<float*>(w + p.s) : nullptr;
+  n.s = S;
   mm_status s = divide(o, n, st);
   const bool tall = o.M > o.N;
   void *A = w + p.a, *B = w + p.b;
@@ -463,7 +465,9 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
     OrthoProduct g;
     memset(&g, 0, sizeof(g));
     g.sym = 1;
+    g.split = split;
     g.y_dtype = MM_F16;
+    g.y_lo = split;
     g.M = g.N = p.m;
     g.K = tall ? o.M : o.N;
     g.count = o.bm.count;
@@ -477,6 +481,7 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
     g.K = p.m;
     g.a = g.b = g.c = A;
     g.a_step = g.b_step = g.c_step = as;
+    g.c_lo = split ? o.bm.count * as : 0;
     g.a_rs = g.b_cs = g.c_rs = p.ldm;
     g.a_cs = g.b_rs = 1;
     g.y = B;
@@ -488,11 +493,20 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
     g.count = o.bm.count;
     g.a = tall ? X : B; g.a_step = tall ? xs : as; g.a_rs = tall ? p.ld : p.ldm; g.a_cs = 1;
     g.b = tall ? B : X; g.b_step = tall ? as : xs; g.b_rs = tall ? p.ldm : p.ld; g.b_cs = 1;
-    g.c = X; g.c_rs = p.ld; g.c_step = xs; g.c_lo = rest;
     const bool last = i + 1 == o.steps;
-    const double up = last ? (double)o.scale : k[i + 1].x;
-    g.alpha = (float)(up / (k[i].b * k[i].x));
-    g.beta = (float)(up * a / k[i].x);
+    if (split) {                            // the fp32 state holds X itself
+      const double up = last ? (double)o.scale : 1.;
+      g.split = 1;
+      g.s32 = S; g.s_rs = p.ld; g.s_step = xs;
+      g.up = (float)k[i + 1].x;
+      g.alpha = (float)(up / (k[i].b * k[i].x));
+      g.beta = (float)(up * a);
+    } else {
+      const double up = last ? (double)o.scale : k[i + 1].x;
+      g.c = X; g.c_rs = p.ld; g.c_step = xs; g.c_lo = rest;
+      g.alpha = (float)(up / (k[i].b * k[i].x));
+      g.beta = (float)(up * a / k[i].x);
+    }
     g.y_dtype = last ? o.dtype : MM_F16;
     g.y = last ? o.out : w + p.x[(i + 1) & 1];
     g.y_rs = last ? o.N : p.ld;

@@ -52,6 +52,7 @@
 //             y = (acc * a_scale[m]) * b_scale[n] + bias[n], rounded once.
 //   kSym      kDense with a symmetric result: the lower triangle's tiles only.
 //   kState    kDense plus a state held in two f16 parts.
+//   kSymF, kStateF  the same for fp32: three f16 products of split operands.
 //   kSkinny   kDense for at most 64 rows of A': 256-column tiles whose
 //             k-blocks are split over the CTAs of a cluster (non-persistent,
 //             one tile per cluster), so that B' streams through every SM with
@@ -83,6 +84,8 @@ constexpr int kEpiWarp0 = 2;                     // warps 2.. run the epilogue
 // 4 stages.  CTA pair (cta_group::2, a 256 x 256 tile per pair): each CTA holds
 // its 128 rows of A and half (128) of the tile's B columns, 32 KB per stage,
 // 6 stages.
+__host__ __device__ constexpr bool is_split(int mode) { return mode == kSymF || mode == kStateF; }
+
 template <int MODE, bool PAIR>
 struct Geo {
   // kSkinny: 64-row A boxes; the M = 128 MMA's rows 64..127 read the
@@ -92,12 +95,12 @@ struct Geo {
   static constexpr int kABytes = (MODE == kSkinny ? BM / 2 : BM) * BK * 2;   // rows x 128 bytes
   static constexpr int kBBytes = kBRows * BK * 2;
   // kTF32: each stage holds the loaded (then high) parts of A and B followed
-  // by their low parts at kLoOff.
-  static constexpr int kLoOff = MODE == kTF32 ? kABytes + kBBytes : 0;
-  static constexpr int kStageBytes = (kABytes + kBBytes) * (MODE == kTF32 ? 2 : 1);
+  // by their low parts at kLoOff; split operands likewise.
+  static constexpr int kLoOff = MODE == kTF32 || is_split(MODE) ? kABytes + kBBytes : 0;
+  static constexpr int kStageBytes = (kABytes + kBBytes) * (kLoOff ? 2 : 1);
   // kGroupedQ gives one stage's worth of shared memory to its int8 staging ring.
   static constexpr int kStages =
-      MODE == kTF32 ? (PAIR ? 3 : 2) : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
+      kLoOff ? (PAIR ? 3 : 2) : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
   static constexpr int kTileRows = PAIR ? 2 * BM : BM;  // output rows per (pair) tile
   static constexpr int kRingBytes = kStages * kStageBytes;
 };
@@ -131,7 +134,7 @@ constexpr int kStageWords = 32 * 16;             // float per-warp output stagin
 // warps of 128 columns plus 4 converter warps (14 warps: 128 registers).
 template <int MODE, bool PAIR>
 struct Cfg {
-  static constexpr int kEpiWarps = (MODE == kGroupedQ || MODE == kTF32) ? 8 : 16;
+  static constexpr int kEpiWarps = (MODE == kGroupedQ || MODE == kTF32 || is_split(MODE)) ? 8 : 16;
   static constexpr int kConv = (MODE == kGroupedQ || MODE == kTF32) ? kConvWarps : 0;
   static constexpr int kConvWarp0 = kEpiWarp0 + kEpiWarps;
   static constexpr int kThreads = (kEpiWarp0 + kEpiWarps + kConv) * 32;
@@ -206,7 +209,7 @@ __device__ __forceinline__ bool get_tile(const TcParams& p, int64_t t, int64_t t
   const uint32_t tt = (uint32_t)t;
   const uint32_t b = fast_div(tt, p.fd_per_batch);
   const uint32_t r = tt - b * p.fd_per_batch.d;
-  if (MODE == kSym) {
+  if (MODE == kSym || MODE == kSymF) {
     // Row by row of the lower triangle.  256-row tiles: row i has i + 1 tiles;
     // 128-row tiles: rows 2a and 2a + 1 have a + 1 each (see sym_tiles).
     constexpr uint32_t kHalf = Geo<MODE, PAIR>::kTileRows == BN ? 1 : 2;   // row tiles per square of 256
@@ -376,6 +379,30 @@ __device__ void run_producer(const CUtensorMap* tmA, const CUtensorMap* tmB, con
 #pragma unroll
           for (int j = 0; j < G::kBRows / 64; ++j) tma_load_3d(sb + j * 8192, tmZ, bc + 64 * j, r0, slot, full);
         }
+      } else if constexpr (is_split(MODE)) {
+        const uint32_t bar = PAIR ? mapa_shared(full, 0) : full;
+        if (rank == 0) mbar_arrive_expect_tx(full, (PAIR ? 2 : 1) * G::kStageBytes);
+        const auto load = [&](uint32_t dst, const CUtensorMap* tm, int32_t c0, int32_t c1, int32_t c2) {
+          if constexpr (PAIR) tma_load_3d_pair(dst, tm, c0, c1, c2, bar);
+          else tma_load_3d(dst, tm, c0, c1, c2, bar);
+        };
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t a = sa + half * G::kLoOff, b = sb + half * G::kLoOff;
+          const int32_t ab = ti.a_b + (half ? (int32_t)p.a_lo : 0), bb = ti.b_b + (half ? (int32_t)p.b_lo : 0);
+          if (!p.a_mn) {
+            load(a, tmA, k0, ar, ab);
+          } else {
+            load(a, tmA, ar, k0, ab);
+            load(a + 8192, tmA, ar + 64, k0, ab);
+          }
+          if (!p.b_mn) {
+            load(b, tmB, k0, bc, bb);
+          } else {
+#pragma unroll
+            for (int j = 0; j < G::kBRows / 64; ++j) load(b + j * 8192, tmB, bc + 64 * j, k0, bb);
+          }
+        }
       } else if (PAIR) {
         const uint32_t bar = mapa_shared(full, 0);
         // A tail tile (at most 128 rows) takes 64 rows of A per CTA.
@@ -492,6 +519,20 @@ __device__ void run_mma(const TcParams& p, uint32_t sbase, uint32_t tmem, uint32
               tc_mma_tf32(d, adl, bd, p.idesc, acc);
               tc_mma_tf32(d, ad, bdl, p.idesc, 1u);
               tc_mma_tf32(d, ad, bd, p.idesc, 1u);
+            }
+          } else if constexpr (is_split(MODE)) {
+            // hi*lo and lo*hi, then hi*hi
+            const uint32_t al = sa + G::kLoOff, bl = sb + G::kLoOff;
+            const uint64_t adl = amn ? smem_desc_sw128(al + k * 2048, 8192, 1024) : smem_desc_sw128(al + k * 32, 16, 1024);
+            const uint64_t bdl = bmn ? smem_desc_sw128(bl + k * 2048, 8192, 1024) : smem_desc_sw128(bl + k * 32, 16, 1024);
+            if (PAIR) {
+              tc_mma_f16_pair(d, ad, bdl, idesc, acc);
+              tc_mma_f16_pair(d, adl, bd, idesc, 1u);
+              tc_mma_f16_pair(d, ad, bd, idesc, 1u);
+            } else {
+              tc_mma_f16(d, ad, bdl, idesc, acc);
+              tc_mma_f16(d, adl, bd, idesc, 1u);
+              tc_mma_f16(d, ad, bd, idesc, 1u);
             }
           } else if (PAIR) {
             tc_mma_f16_pair(d, ad, bd, idesc, acc);
@@ -1325,6 +1366,141 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
   }
 }
 
+// ------------------------------------------------------------------ split epilogue (kSymF, kStateF)
+
+// 32 values per lane (a row's, from column c0 on) to the 32 x 32 box at (row0, c0)
+// of Y's tensor map as f16, with `turn` also transposed to (c0, row0); then the
+// rest of each value as f16 `lo` batches further.
+__device__ __forceinline__ void store_pair_box(const CUtensorMap* tmY, uint32_t sbox, int lane, float (&v)[32],
+                                               int32_t row0, int32_t c0, int32_t batch, int32_t lo, bool turn) {
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      sts128(sbox + (uint32_t)lane * 64 + (((uint32_t)q ^ ((uint32_t)(lane >> 1) & 3u)) << 4),
+             make_uint4(pack2(v[8 * q], v[8 * q + 1], 1), pack2(v[8 * q + 2], v[8 * q + 3], 1),
+                        pack2(v[8 * q + 4], v[8 * q + 5], 1), pack2(v[8 * q + 6], v[8 * q + 7], 1)));
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(tmY, sbox, c0, row0, batch);
+      bulk_commit();
+    }
+    if (turn) {
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        sts16(sbox + (uint32_t)j * 64 + ((((uint32_t)lane >> 3) ^ (((uint32_t)j >> 1) & 3u)) << 4) + ((uint32_t)lane & 7u) * 2,
+              __half_as_ushort(__float2half_rn(v[j])));
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(tmY, sbox, row0, c0, batch);
+        bulk_commit();
+      }
+    }
+    batch += lo;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
+  }
+}
+
+// 8 warps of 128 columns: every segment's accumulator is added to fp32 sums in
+// registers, then alpha, the state or C, and the stores.
+template <int MODE, bool PAIR>
+__device__ void run_split_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t tmem, uint32_t accf0,
+                                   uint32_t acce0, volatile int* abort, uint32_t* stage) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kCols = Cfg<MODE, PAIR>::kCols, kChunks = kCols / 32;
+  const int quad = warp & 3, slice = (warp - kEpiWarp0) >> 2;
+  const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
+  const int64_t row_off = PAIR ? (int64_t)rank * BM : 0;
+  const uint32_t rel0 = PAIR ? mapa_shared(acce0, 0) : acce0, tlane = (uint32_t)(quad * 32) << 16;
+  const uint32_t sbox = smem_u32(stage);
+  const int64_t total = total_tiles<MODE>(p);
+  const int nseg = (p.num_kb + p.kb_per_seg - 1) / p.kb_per_seg;
+  uint32_t seg = 0;
+  Tile ti;
+  int gh = 0;
+  for (int64_t t = first_tile<MODE, PAIR>(p); get_tile<MODE, PAIR>(p, t, total, ti, gh); t += tile_step<MODE, PAIR>(p)) {
+    float acc[kChunks][32];
+    for (int s = 0; s < nseg; ++s, ++seg) {
+      const uint32_t buf = seg & 1, aph = (seg >> 1) & 1;
+      const bool ok = PAIR ? mbar_wait_cluster(accf0 + 8 * buf, aph, abort, p.status, p.timeout_ns)
+                           : mbar_wait(accf0 + 8 * buf, aph, abort, p.status, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      tc_fence_after();
+      const uint32_t taddr = tmem + tlane + buf * BN + slice * kCols;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t r[32];
+        tmem_ld32(taddr + c * 32, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[c][j] = s == 0 ? __uint_as_float(r[j]) : acc[c][j] + __uint_as_float(r[j]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_cluster(rel0 + 8 * buf);
+        else mbar_arrive(acce0 + 8 * buf);
+      }
+    }
+    const int rows_t = PAIR ? max(0, min(BM, ti.rows - (int)row_off)) : ti.rows;
+    const int rl = quad * 32 + lane;
+    const bool rok = rl < rows_t;
+    const int64_t m = ti.m0 + row_off + rl;
+    const int32_t row0 = (int32_t)(ti.m0 + row_off + quad * 32), yb = (int32_t)batch_off(p, p.y_bc, ti.batch);
+    const uint16_t* crow =
+        p.c && rok ? static_cast<const uint16_t*>(p.c) + batch_off(p, p.c_bstride, ti.batch) + m * p.c_rs : nullptr;
+    float* srow = MODE == kStateF && rok ? p.s32 + ti.batch * p.s_step + m * p.s_rs : nullptr;
+#pragma unroll
+    for (int h = 0; h < kChunks; ++h) {
+      const int64_t n = ti.n0 + slice * kCols + 32 * h;
+      if (n >= p.N) break;
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = p.alpha * acc[h][j];
+      if (crow) add_state32(p, crow, n, v);
+      if constexpr (MODE == kStateF) {
+        if (srow) {                          // s_rs is a multiple of 4; the padding past N is never stored from
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            if (n + 4 * q >= p.s_rs) break;
+            const float4 f = *reinterpret_cast<const float4*>(srow + n + 4 * q);
+            v[4 * q] = __fmaf_rn(p.beta, f.x, v[4 * q]);
+            v[4 * q + 1] = __fmaf_rn(p.beta, f.y, v[4 * q + 1]);
+            v[4 * q + 2] = __fmaf_rn(p.beta, f.z, v[4 * q + 2]);
+            v[4 * q + 3] = __fmaf_rn(p.beta, f.w, v[4 * q + 3]);
+          }
+        }
+        if (p.y_lo == 0) {                   // the result
+          if (rok) store_f32_32(p, static_cast<float*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + m * p.y_rs, n, v);
+          continue;
+        }
+        if (srow) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            if (n + 4 * q >= p.s_rs) break;
+            *reinterpret_cast<float4*>(srow + n + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= p.up;
+      }
+      if (quad * 32 < rows_t) {
+        // kSymF: also transposed, where that falls into a tile that is not computed (as kSym)
+        constexpr int TR = Geo<MODE, PAIR>::kTileRows;
+        store_pair_box(tmY, sbox, lane, v, row0, (int32_t)n, yb, (int32_t)p.y_lo,
+                       MODE == kSymF && (row0 / BN) * BN > ((int32_t)n / TR) * TR + TR - 1);
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ few-row epilogue (kSkinny)
 
 // Each CTA of a cluster has accumulated its share of the tile's k-blocks in
@@ -1483,7 +1659,9 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
   // the previous kernel on the stream is finishing: the set-up above overlaps
   // its tail, and nothing below touches global memory before it completes.
   if (MODE != kSkinny || !p.c_late) pdl_wait();
-  if constexpr (MODE == kDense || MODE == kTF32 || MODE == kInt8 || MODE == kSym || MODE == kState) pdl_trigger();
+  if constexpr (MODE == kDense || MODE == kTF32 || MODE == kInt8 || MODE == kSym || MODE == kState ||
+                is_split(MODE))
+    pdl_trigger();
   const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
 
   if (warp == 0) {
@@ -1498,6 +1676,7 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
     uint32_t* stage = reinterpret_cast<uint32_t*>(smem_raw + (sbase - raw) + G::kRingBytes) +
                       (warp - kEpiWarp0) * Cfg<MODE, PAIR>::kWarpWords;
     if constexpr (MODE == kSkinny) run_skinny_partial<MODE, PAIR>(p, tmem, accf0, abort, sbase);
+    else if constexpr (is_split(MODE)) run_split_epilogue<MODE, PAIR>(p, &tmZ, tmem, accf0, acce0, abort, stage);
     else run_epilogue<MODE, PAIR>(p, &tmZ, tmem, accf0, acce0, abort, stage);
     // Every tensor store has read its box before the CTA can exit.
     if (p.y_tma && lane == 0) bulk_wait_all();
@@ -1743,7 +1922,7 @@ mm_status launch_kernel(const OperandPlan& a, const OperandPlan& b, const CUtens
                         const TcParams& p_in, int64_t work, cudaStream_t stream) {
   constexpr int kSmem = Cfg<MODE, PAIR>::kSmem, kThreadsM = Cfg<MODE, PAIR>::kThreads;
   TcParams p = p_in;
-  if (MODE != kDense && MODE != kInt8 && MODE != kSym && MODE != kState) p.y_tma = 0;
+  if (MODE != kDense && MODE != kInt8 && MODE != kSym && MODE != kState && !is_split(MODE)) p.y_tma = 0;
   if (cudaFuncSetAttribute(tc_gemm_kernel<MODE, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
       cudaSuccess)
     return MM_ERR_CUDA;
@@ -1815,7 +1994,7 @@ mm_status launch_tc(int mode, bool pair, const OperandPlan& a, const OperandPlan
     const int64_t cols = BN;
     p.mt = (p.M + rows - 1) / rows;
     p.nt = (p.N + cols - 1) / cols;
-    const int64_t per_matrix = mode == kSym ? sym_tiles(p.mt, pair) : p.mt * p.nt;
+    const int64_t per_matrix = mode == kSym || mode == kSymF ? sym_tiles(p.mt, pair) : p.mt * p.nt;
     p.tiles = per_matrix * p.bm.count;
     if (p.tiles >= (1ll << 31) || p.mt * p.nt >= (1ll << 31)) return MM_ERR_UNSUPPORTED;
     const uint32_t per_batch = (uint32_t)per_matrix;
@@ -1865,6 +2044,12 @@ mm_status launch_tc(int mode, bool pair, const OperandPlan& a, const OperandPlan
     case kState:
       return pair ? launch_kernel<kState, true>(a, b, ms, mz, p, work, stream)
                   : launch_kernel<kState, false>(a, b, ms, mz, p, work, stream);
+    case kSymF:
+      return pair ? launch_kernel<kSymF, true>(a, b, ms, mz, p, work, stream)
+                  : launch_kernel<kSymF, false>(a, b, ms, mz, p, work, stream);
+    case kStateF:
+      return pair ? launch_kernel<kStateF, true>(a, b, ms, mz, p, work, stream)
+                  : launch_kernel<kStateF, false>(a, b, ms, mz, p, work, stream);
     case kGroupedQ:  // CTA pairs only
       if (!pair || !s) return MM_ERR_UNSUPPORTED;
       return launch_kernel<kGroupedQ, true>(a, b, ms, mz, p, work, stream);
@@ -2085,7 +2270,8 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
   if (!status) return MM_ERR_CUDA;
   GemmArgs g;
   memset(&g, 0, sizeof(g));
-  g.dtype = o.y_dtype;
+  const bool f32_out = o.y_dtype == MM_F32;
+  g.dtype = f32_out ? MM_F16 : o.y_dtype;
   g.M = o.M; g.N = o.N; g.K = o.K;
   g.bm.nb = 1;
   for (int d = 0; d < kMaxBatchDims; ++d) g.bm.shape[d] = 1;
@@ -2099,7 +2285,8 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
   p.y = o.y;
   p.y_rs = o.y_rs;
   p.y_bstride[0] = o.y_step;
-  p.y_vec = (reinterpret_cast<uintptr_t>(o.y) & 15) == 0 && o.y_rs % 8 == 0 && (o.y_step % 8 == 0 || o.count == 1);
+  const int64_t vec = f32_out ? 4 : 8;
+  p.y_vec = (reinterpret_cast<uintptr_t>(o.y) & 15) == 0 && o.y_rs % vec == 0 && (o.y_step % vec == 0 || o.count == 1);
   p.alpha = o.alpha;
   p.beta = o.beta;
   if (o.c) {
@@ -2116,18 +2303,27 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
     ym.bm.shape[0] = ym.bm.count = 2 * o.count;
     p.y_lo = o.count;
   }
-  plan_output(ym, &p, &ymap);
+  if (!f32_out) plan_output(ym, &p, &ymap);
   if ((o.sym || o.y_lo) && !p.y_tma) return MM_ERR_UNSUPPORTED;
-  const int mode = o.sym ? kSym : kState;
+  const int mode = o.split ? (o.sym ? kSymF : kStateF) : o.sym ? kSym : kState;
+  BatchMap om = g.bm;                          // the operands' maps span the rests too
+  if (o.split) {
+    p.kb_per_seg = kSplitSegment / BK;
+    om.shape[0] = om.count = 2 * o.count;
+    p.a_lo = p.b_lo = o.count;
+    p.s32 = o.s32;
+    p.s_rs = o.s_rs; p.s_step = o.s_step;
+    p.up = o.up;
+  }
   const int64_t as[kMaxBatchDims] = {o.a_step}, bs[kMaxBatchDims] = {o.b_step};
   for (int attempt = use_pair(g.M, g.K) ? 0 : 1; attempt < 2; ++attempt) {
     const bool pair = attempt == 0;
     OperandPlan a, b, tail;
-    if (!plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, g.bm, as, BM, &a) ||
-        !plan_operand(o.b, MM_F16, g.N, g.K, o.b_cs, o.b_rs, g.bm, bs, pair ? BN / 2 : BN, &b))
+    if (!plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, om, as, BM, &a) ||
+        !plan_operand(o.b, MM_F16, g.N, g.K, o.b_cs, o.b_rs, om, bs, pair ? BN / 2 : BN, &b))
       return MM_ERR_UNSUPPORTED;
     p.idesc = make_idesc(1, a.mn_major, b.mn_major, pair);
-    p.pair_tail = pair && !a.mn_major && plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, g.bm, as, BM / 2, &tail);
+    p.pair_tail = pair && !o.split && !a.mn_major && plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, g.bm, as, BM / 2, &tail);
     if (p.pair_tail) p.idesc_tail = make_idesc_rows(1, 0, b.mn_major, BM);
     const mm_status st = launch_tc(mode, pair, a, b, p, stream, p.pair_tail ? &tail : nullptr, p.y_tma ? &ymap : nullptr);
     if (st != MM_ERR_UNSUPPORTED || !pair) return st;

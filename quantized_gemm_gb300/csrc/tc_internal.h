@@ -32,7 +32,9 @@ constexpr int kTileK = 64;    // one 128-byte swizzle row of 16-bit elements
 // stored transposed where the tile on the other side was left out.
 // kState: a dense f16 product plus beta times a state held as two f16 values
 // (high part and rest); the sum goes out as such a pair, or rounded to T.
-enum TcMode { kDense = 0, kGrouped = 1, kQLinear = 2, kGroupedQ = 3, kTF32 = 4, kSkinny = 5, kLowRank = 6, kInt8 = 7, kSym = 8, kState = 9 };
+enum TcMode { kDense = 0, kGrouped = 1, kQLinear = 2, kGroupedQ = 3, kTF32 = 4, kSkinny = 5, kLowRank = 6, kInt8 = 7, kSym = 8, kState = 9,
+              kSymF = 10, kStateF = 11 };
+constexpr int kSplitSegment = 256;
 
 struct TcParams {
   int64_t M, N, K;
@@ -71,6 +73,12 @@ struct TcParams {
   int64_t c_rs, c_cs, c_gs;                    // c_gs: grouped bias row stride per group
   int c_vec, c_live;                           // c_live: C is Y
   int64_t c_lo, y_lo;                          // kState: from the high part to the rest (elements; batch coordinates, 0: Y is T)
+  // kSymF, kStateF: batch coordinates from the operands' high parts to their
+  // rests; kStateF: the fp32 state, read and (where Y is not the result) written.
+  int64_t a_lo, b_lo;
+  float* s32;
+  int64_t s_rs, s_step;
+  float up;                                    // Y's pair is `up` times the new state
   int c_late, c_f32;                           // kSkinny: GemmArgs::c_late, c_f32
   // QLinear epilogue: zero-point correction from the operand sums, then requantisation
   VecView sa, sb, za, zb;
