@@ -439,7 +439,7 @@ __device__ __forceinline__ void half4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 __global__ void __launch_bounds__(256) int8_copy_kernel(const Int8Copy A, const Int8Copy B, const int64_t blocks_a) {
-  pdl_wait();
+  pdl_begin();               // the product may start: it waits for this grid where it reads a copy
   const bool first = (int64_t)blockIdx.x < blocks_a;
   const Int8Copy& c = first ? A : B;
   const int64_t per_row = (c.ld + 15) / 16;

@@ -1,0 +1,396 @@
+// The 8-bit product for a few tokens up to a few hundred (mm_int8_matmul): the
+// weights stream once, as int8, and are the MMA's 128-row operand.
+//
+// There is no 8-bit integer tensor instruction on sm_103a, so int8 values are
+// multiplied as f16, which holds them exactly.  A CTA owns 128 output channels
+// and NT tokens (a multiple of 16, up to 256):
+//   warp 0       streams [128 channels x 128 k] tiles of int8 weights by TMA into a
+//                ring, before the launch in front of this one has ended (that one
+//                only copies the tokens to f16);
+//   warp 2       streams the tokens' f16 tiles [NT x 128 k] once it has;
+//   warps 4-19   turn weight bytes into f16 pairs (flip the sign bit, put the byte
+//                into the mantissa of 1024, subtract 1152: 1.25 instructions a value)
+//                and store them to tensor memory, where the MMA takes its first
+//                operand from (a thread owns a channel, that is a lane): the weights
+//                pass through shared memory once, as bytes, which leaves its
+//                bandwidth to the stream; two groups of 8 warps take turns;
+//   warp 1       issues the MMAs, D[channel, token] in fp32.
+// K is split over the CTAs of a cluster where there are fewer tiles than SMs; the
+// partial sums meet in a fixed order through distributed shared memory, a token's
+// 128 channels in neighbouring lanes, and the epilogue scales and stores them in
+// rows.  Bound: memory (one byte per weight) up to about 100 tokens, then the MMAs.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
+#include "tc.h"
+#include "tc_internal.h"
+#include "tc_ptx.cuh"
+
+namespace qg {
+
+using namespace ptx;
+
+namespace {
+
+constexpr int kRows = 128;                       // channels of a CTA
+constexpr int kDepth = 128;                      // k of a stage
+constexpr int kWBytes = kRows * kDepth;
+constexpr int kAStages = 4, kACols = kDepth / 2; // operand stages in tensor memory, columns each
+constexpr int kConvWarp0 = 4, kConvWarps = 16;
+constexpr int kThreads = (kConvWarp0 + kConvWarps) * 32;
+constexpr int kCtrl = 512;
+
+template <int NT>
+struct Cfg {
+  static constexpr int kXBytes = NT * kDepth * 2;
+  static constexpr int kXStages = NT <= 64 ? 4 : NT <= 128 ? 3 : 2;
+  static constexpr int kWStages = NT <= 128 ? 7 : 5;
+  static constexpr int kXOff = kWStages * kWBytes;
+  static constexpr int kRing = kXOff + kXStages * kXBytes;
+  static constexpr int kSmem = kRing + kCtrl + 1024;
+  static_assert(kSmem <= 232448, "shared memory per block");
+  static_assert(NT * kRows * 4 <= kRing, "the partial sums take the ring's place");
+  static_assert(NT + kAStages * kACols <= 512, "tensor memory");
+};
+
+struct StreamArgs {
+  Int8Args q;
+  int num_kb, split, mtiles;
+  int y_vec;                                     // rows of Y allow stores of four values
+  uint32_t idesc;
+  unsigned* status;
+  unsigned long long timeout_ns, teardown_ns;
+};
+
+// D[tmem] (+)= A[tmem] * B[smem], f16 operands, fp32 accumulator.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 32 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Four int8 values as two f16 pairs, exactly.
+__device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t l = __byte_perm(u, 0x64u, 0x4140u), h = __byte_perm(u, 0x64u, 0x4342u);
+  const uint32_t c = 0x64806480u;                // 1152 twice
+  const __half2 dl = __hsub2(*reinterpret_cast<const __half2*>(&l), *reinterpret_cast<const __half2*>(&c));
+  const __half2 dh = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&c));
+  lo = *reinterpret_cast<const uint32_t*>(&dl);
+  hi = *reinterpret_cast<const uint32_t*>(&dh);
+}
+
+template <typename O>
+__device__ __forceinline__ float bias_of(const Int8Args& q, int64_t n) {
+  return q.bias ? to_f32(static_cast<const O*>(q.bias)[n * q.bias_s]) : 0.f;
+}
+
+template <typename O, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                       const StreamArgs p) {
+  using C = Cfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  const uint32_t ctrl = sbase + C::kRing;
+  const uint32_t wfull = ctrl, wempty = wfull + 8 * C::kWStages, xfull = wempty + 8 * C::kWStages,
+                 xempty = xfull + 8 * C::kXStages, afull = xempty + 8 * C::kXStages, aempty = afull + 8 * kAStages,
+                 accf = aempty + 8 * kAStages;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + C::kRing + kCtrl - 16);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kRing + kCtrl - 8);
+  static_assert(16 * C::kWStages + 16 * C::kXStages + 16 * kAStages + 8 <= kCtrl - 16, "control block");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kWStages; ++s) {
+      mbar_init(wfull + 8 * s, 1);
+      mbar_init(wempty + 8 * s, kConvWarps / 2);
+    }
+    for (int s = 0; s < C::kXStages; ++s) {
+      mbar_init(xfull + 8 * s, 1);
+      mbar_init(xempty + 8 * s, 1);
+    }
+    for (int s = 0; s < kAStages; ++s) {
+      mbar_init(afull + 8 * s, kConvWarps / 2);
+      mbar_init(aempty + 8 * s, 1);
+    }
+    mbar_init(accf, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot, tmem_a = tmem + NT;
+
+  const int rank = (int)(blockIdx.x % (unsigned)p.split), tile = (int)(blockIdx.x / (unsigned)p.split);
+  const int64_t n0 = (int64_t)(tile / p.mtiles) * kRows, m0 = (int64_t)(tile % p.mtiles) * NT;
+  const int kb0 = (int)((int64_t)rank * p.num_kb / p.split), kb1 = (int)((int64_t)(rank + 1) * p.num_kb / p.split);
+  const int nkb = kb1 - kb0;
+
+  if (warp == 0) {
+    // The weights were complete before the launch in front of this one (the copy
+    // of the tokens, which lets this grid start only after its own wait).
+    if (lane == 0) {
+      prefetch_tmap(&tmW);
+      int i = 0;
+      for (; i < nkb; ++i) {
+        const int s = i % C::kWStages, ph = (i / C::kWStages) & 1;
+        if (!mbar_wait(wempty + 8 * s, ph ^ 1, abort, p.status, p.timeout_ns)) break;
+        mbar_arrive_expect_tx(wfull + 8 * s, kWBytes);
+        tma_load_3d(sbase + s * kWBytes, &tmW, (kb0 + i) * kDepth, (int32_t)n0, 0, wfull + 8 * s);
+      }
+      for (int j = i > C::kWStages ? i - C::kWStages : 0; j < i; ++j)      // every copy lands before the CTA can end
+        mbar_wait_teardown(wfull + 8 * (j % C::kWStages), (j / C::kWStages) & 1, p.teardown_ns);
+    }
+  } else if (warp == 2) {
+    if (lane == 0) {
+      prefetch_tmap(&tmX);
+      pdl_wait();
+      int i = 0;
+      for (; i < nkb; ++i) {
+        const int s = i % C::kXStages, ph = (i / C::kXStages) & 1;
+        if (!mbar_wait(xempty + 8 * s, ph ^ 1, abort, p.status, p.timeout_ns)) break;
+        mbar_arrive_expect_tx(xfull + 8 * s, C::kXBytes);
+        const uint32_t dst = sbase + C::kXOff + s * C::kXBytes;
+        tma_load_3d(dst, &tmX, (kb0 + i) * kDepth, (int32_t)m0, 0, xfull + 8 * s);
+        tma_load_3d(dst + C::kXBytes / 2, &tmX, (kb0 + i) * kDepth + 64, (int32_t)m0, 0, xfull + 8 * s);
+      }
+      for (int j = i > C::kXStages ? i - C::kXStages : 0; j < i; ++j)
+        mbar_wait_teardown(xfull + 8 * (j % C::kXStages), (j / C::kXStages) & 1, p.teardown_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int i = 0; i < nkb; ++i) {
+        const int xs = i % C::kXStages, as = i % kAStages;
+        if (!mbar_wait(xfull + 8 * xs, (i / C::kXStages) & 1, abort, p.status, p.timeout_ns)) break;
+        if (!mbar_wait(afull + 8 * as, (i / kAStages) & 1, abort, p.status, p.timeout_ns)) break;
+        tc_fence_after();
+        const uint32_t x = sbase + C::kXOff + xs * C::kXBytes;
+#pragma unroll
+        for (int k = 0; k < kDepth / 16; ++k)
+          mma_ts(tmem, tmem_a + as * kACols + k * 8,
+                 smem_desc_sw128(x + (k >> 2) * (C::kXBytes / 2) + (k & 3) * 32, 16, 1024), p.idesc, i > 0 || k > 0);
+        tc_commit(aempty + 8 * as);
+        tc_commit(xempty + 8 * xs);
+      }
+      tc_commit(accf);
+      mbar_wait_teardown(accf, 0, p.teardown_ns);
+    }
+  } else if (warp >= kConvWarp0) {
+    const int cw = warp - kConvWarp0, quad = warp & 3, half = (cw >> 2) & 1, group = cw >> 3;
+    const int row = quad * 32 + lane;
+    for (int i = group; i < nkb; i += 2) {
+      const int ws = i % C::kWStages, as = i % kAStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(wfull + 8 * ws, (i / C::kWStages) & 1, abort, p.status, p.timeout_ns))) break;
+      uint4 u[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        u[c] = lds128(sbase + ws * kWBytes + row * kDepth + (((half * 4 + c) ^ (row & 7)) << 4));
+      uint32_t r[32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        halves(u[c].x, r[8 * c], r[8 * c + 1]);
+        halves(u[c].y, r[8 * c + 2], r[8 * c + 3]);
+        halves(u[c].z, r[8 * c + 4], r[8 * c + 5]);
+        halves(u[c].w, r[8 * c + 6], r[8 * c + 7]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(wempty + 8 * ws);
+      if (!__all_sync(0xffffffffu, mbar_wait(aempty + 8 * as, ((i / kAStages) & 1) ^ 1, abort, p.status, p.timeout_ns))) break;
+      tc_fence_after();
+      tmem_st32(tmem_a + as * kACols + half * 32 + ((uint32_t)(quad * 32) << 16), r);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(afull + 8 * as);
+    }
+    // This CTA's sums, [token][channel], into the drained ring.
+    if (__all_sync(0xffffffffu, mbar_wait(accf, 0, abort, p.status, p.timeout_ns))) {
+      tc_fence_after();
+      float* part = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+      for (int c = (cw >> 2) * 16; c < NT; c += 64) {
+        uint32_t r[16];
+        tmem_ld16(tmem + c + ((uint32_t)(quad * 32) << 16), r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * kRows + row] = __uint_as_float(r[j]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (p.split > 1) cluster_sync();
+  pdl_wait();
+  if (warp >= kConvWarp0 && !*abort) {
+    // Tokens [rank * NT / split, ...), a warp per token, four channels a lane.
+    const int per = NT / p.split, cw = warp - kConvWarp0;
+    const int64_t n = n0 + lane * 4;
+    float sb[4], bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool in = n + j < p.q.N;
+      sb[j] = in ? __ldg(p.q.sb + (n + j) * p.q.sb_s) : 0.f;
+      bias[j] = in ? bias_of<O>(p.q, n + j) : 0.f;
+    }
+    for (int t = cw; t < per; t += kConvWarps) {
+      const int tok = rank * per + t;
+      const int64_t m = m0 + tok;
+      if (m >= p.q.M) break;
+      const uint32_t src = sbase + (uint32_t)(tok * kRows + lane * 4) * 4;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int rk = 0; rk < p.split; ++rk) {
+        const float4 f = p.split > 1 ? lds128_cluster(mapa_shared(src, (uint32_t)rk))
+                                     : *reinterpret_cast<const float4*>(smem + (src - sbase));
+        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+      }
+      const float sa = __ldg(p.q.sa + m * p.q.sa_s);
+      O o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = from_f32<O>(__fadd_rn(__fmul_rn(__fmul_rn(v[j], sa), sb[j]), bias[j]));
+      O* y = static_cast<O*>(p.q.y) + m * p.q.N + n;
+      if (p.y_vec && n + 4 <= p.q.N) {
+        if constexpr (sizeof(O) == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(o);
+        else *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(o);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j < p.q.N) y[j] = o[j];
+      }
+    }
+  }
+  if (p.split > 1) cluster_sync();               // no CTA leaves while its sums are read
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The weights [N, K] int8 as [128 channels x 128 k] tiles, 128-byte swizzled.
+bool weight_map(const Int8Args& q, CUtensorMap* map) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  if (!encode) return false;
+  const int64_t pitch = q.N == 1 ? (q.K + 15) / 16 * 16 : q.b_ns;
+  const cuuint64_t dims[3] = {(cuuint64_t)q.K, (cuuint64_t)q.N, 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)pitch * (cuuint64_t)q.N};
+  if (strides[0] >= (1ull << 40) || strides[1] >= (1ull << 40)) return false;
+  const cuuint32_t box[3] = {kDepth, kRows, 1}, estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(q.b), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename O, int NT>
+mm_status launch(const StreamArgs& p_in, const CUtensorMap& w, const CUtensorMap& x, cudaStream_t stream) {
+  StreamArgs p = p_in;
+  p.mtiles = (int)((p.q.M + NT - 1) / NT);
+  const int64_t tiles = (p.q.N + kRows - 1) / kRows * p.mtiles;
+  // K over a cluster: the largest power of two up to 8 that keeps the CTAs within
+  // the SMs and gives each at least two stages.
+  int split = 8;
+  while (split > 1 && (tiles * split > sm_count_public() || p.num_kb < 2 * split)) split >>= 1;
+  p.split = split;
+  if (tiles * split > 0x7fffffffLL) return MM_ERR_UNSUPPORTED;
+  p.idesc = make_idesc_mn(1, 0, 0, kRows, NT);
+  const auto kernel = int8_stream_kernel<O, NT>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::kSmem) != cudaSuccess)
+    return MM_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<NT>::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, w, x, p) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+}
+
+template <typename O>
+mm_status launch_typed(const StreamArgs& p, int nt, const CUtensorMap& w, const CUtensorMap& x, cudaStream_t stream) {
+  switch (nt) {
+    case 16: return launch<O, 16>(p, w, x, stream);
+    case 32: return launch<O, 32>(p, w, x, stream);
+    case 64: return launch<O, 64>(p, w, x, stream);
+    case 128: return launch<O, 128>(p, w, x, stream);
+    default: return launch<O, 256>(p, w, x, stream);
+  }
+}
+
+}  // namespace
+
+// B's columns contiguous along k, 16-byte aligned.
+bool int8_stream_supported(const Int8Args& q) {
+  return q.K >= 1 && q.b_ks == 1 && (q.N == 1 || (q.b_ns % 16 == 0 && q.b_ns > 0)) &&
+         (reinterpret_cast<uintptr_t>(q.b) & 15) == 0;
+}
+
+mm_status launch_int8_stream(const Int8Args& q, const void* x, int64_t ldx, unsigned* status, cudaStream_t stream) {
+  if (!status) return MM_ERR_CUDA;
+  int nt = 16;
+  while (nt < 256 && nt < q.M) nt *= 2;
+  StreamArgs p;
+  memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.num_kb = (int)((q.K + kDepth - 1) / kDepth);
+  const int size = q.out_dtype == MM_F32 ? 4 : 2;
+  p.y_vec = q.N % 4 == 0 && (reinterpret_cast<uintptr_t>(q.y) & (size * 4 - 1)) == 0;
+  p.status = status;
+  TcParams limits;
+  init_params(&limits);
+  p.timeout_ns = limits.timeout_ns;
+  p.teardown_ns = limits.teardown_ns;
+  CUtensorMap w;
+  OperandPlan xp;
+  BatchMap one;
+  memset(&one, 0, sizeof(one));
+  one.count = 1;
+  for (int d = 0; d < kMaxBatchDims; ++d) one.shape[d] = 1;
+  const int64_t none[kMaxBatchDims] = {};
+  if (!weight_map(q, &w) || !plan_operand(x, MM_F16, q.M, q.K, ldx, 1, one, none, nt, &xp)) return MM_ERR_UNSUPPORTED;
+  switch (q.out_dtype) {
+    case MM_F32: return launch_typed<float>(p, nt, w, xp.map, stream);
+    case MM_BF16: return launch_typed<__nv_bfloat16>(p, nt, w, xp.map, stream);
+    default: return launch_typed<__half>(p, nt, w, xp.map, stream);
+  }
+}
+
+}  // namespace qg
