@@ -45,6 +45,7 @@ constexpr int kCtrl = 512;
 template <int NT>
 struct Cfg {
   static constexpr int kXBytes = NT * kDepth * 2;
+  static constexpr int kAccs = NT <= 64 ? 4 : NT <= 128 ? 2 : 1;   // accumulators that take the k steps in turn
   static constexpr int kXStages = NT <= 64 ? 4 : NT <= 128 ? 3 : 2;
   static constexpr int kWStages = NT <= 128 ? 7 : 5;
   static constexpr int kXOff = kWStages * kWBytes;
@@ -52,7 +53,7 @@ struct Cfg {
   static constexpr int kSmem = kRing + kCtrl + 1024;
   static_assert(kSmem <= 232448, "shared memory per block");
   static_assert(NT * kRows * 4 <= kRing, "the partial sums take the ring's place");
-  static_assert(NT + kAStages * kACols <= 512, "tensor memory");
+  static_assert(NT * kAccs + kAStages * kACols <= 512, "tensor memory");
 };
 
 struct StreamArgs {
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *slot, tmem_a = tmem + NT;
+  const uint32_t tmem = *slot, tmem_a = tmem + NT * C::kAccs;
 
   const int rank = (int)(blockIdx.x % (unsigned)p.split), tile = (int)(blockIdx.x / (unsigned)p.split);
   const int64_t n0 = (int64_t)(tile / p.mtiles) * kRows, m0 = (int64_t)(tile % p.mtiles) * NT;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // The weights were complete before the launch in front of this one (the copy
     // of the tokens, which lets this grid start only after its own wait).
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tmap(&tmW);
       int i = 0;
       for (; i < nkb; ++i) {
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_teardown(wfull + 8 * (j % C::kWStages), (j / C::kWStages) & 1, p.teardown_ns);
     }
   } else if (warp == 2) {
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tmap(&tmX);
       pdl_wait();
       int i = 0;
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_teardown(xfull + 8 * (j % C::kXStages), (j / C::kXStages) & 1, p.teardown_ns);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       for (int i = 0; i < nkb; ++i) {
         const int xs = i % C::kXStages, as = i % kAStages;
         if (!mbar_wait(xfull + 8 * xs, (i / C::kXStages) & 1, abort, p.status, p.timeout_ns)) break;
@@ -192,8 +193,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t x = sbase + C::kXOff + xs * C::kXBytes;
 #pragma unroll
         for (int k = 0; k < kDepth / 16; ++k)
-          mma_ts(tmem, tmem_a + as * kACols + k * 8,
-                 smem_desc_sw128(x + (k >> 2) * (C::kXBytes / 2) + (k & 3) * 32, 16, 1024), p.idesc, i > 0 || k > 0);
+          mma_ts(tmem + k % C::kAccs * NT, tmem_a + as * kACols + k * 8,
+                 smem_desc_sw128(x + (k >> 2) * (C::kXBytes / 2) + (k & 3) * 32, 16, 1024), p.idesc,
+                 i > 0 || k >= C::kAccs);
         tc_commit(aempty + 8 * as);
         tc_commit(xempty + 8 * xs);
       }
@@ -234,11 +236,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* part = reinterpret_cast<float*>(smem);
 #pragma unroll 1
       for (int c = (cw >> 2) * 16; c < NT; c += 64) {
-        uint32_t r[16];
-        tmem_ld16(tmem + c + ((uint32_t)(quad * 32) << 16), r);
+        uint32_t r[C::kAccs][16];
+#pragma unroll
+        for (int a = 0; a < C::kAccs; ++a) tmem_ld16(tmem + a * NT + c + ((uint32_t)(quad * 32) << 16), r[a]);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * kRows + row] = __uint_as_float(r[j]);
+        for (int j = 0; j < 16; ++j) {
+          float v = __uint_as_float(r[0][j]);
+#pragma unroll
+          for (int a = 1; a < C::kAccs; ++a) v += __uint_as_float(r[a][j]);
+          part[(c + j) * kRows + row] = v;
+        }
       }
     }
   }
