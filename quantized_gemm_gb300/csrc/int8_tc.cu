@@ -2,9 +2,9 @@
 // weights stream once, as int8, and are the MMA's 128-row operand.
 //
 // There is no 8-bit integer tensor instruction on sm_103a, so int8 values are
-// multiplied as f16, which holds them exactly.  A CTA owns 128 output channels
-// and NT tokens (a multiple of 16, up to 256):
-//   warp 0       streams [128 channels x 128 k] tiles of int8 weights by TMA into a
+// multiplied as f16, which holds them exactly.  A CTA owns `rows` output channels
+// (64 to 128, chosen so that the CTAs fill the SMs) and NT tokens (16 to 256):
+//   warp 0       streams [rows channels x 128 k] tiles of int8 weights by TMA into a
 //                ring, before the launch in front of this one has ended (that one
 //                only copies the tokens to f16);
 //   warp 2       streams the tokens' f16 tiles [NT x 128 k] once it has;
@@ -15,13 +15,14 @@
 //                pass through shared memory once, as bytes, which leaves its
 //                bandwidth to the stream; two groups of 8 warps take turns;
 //   warp 1       issues the MMAs, D[channel, token] in fp32.
-// K is split over the CTAs of a cluster where there are fewer tiles than SMs; the
+// K is split over the CTAs of a cluster where that fills the SMs better; the
 // partial sums meet in a fixed order through distributed shared memory, a token's
-// 128 channels in neighbouring lanes, and the epilogue scales and stores them in
+// channels in neighbouring lanes, and the epilogue scales and stores them in
 // rows.  Bound: memory (one byte per weight) up to about 100 tokens, then the MMAs.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "tc.h"
@@ -34,7 +35,7 @@ using namespace ptx;
 
 namespace {
 
-constexpr int kRows = 128;                       // channels of a CTA
+constexpr int kRows = 128;                       // channels of a CTA at most: the MMA's rows
 constexpr int kDepth = 128;                      // k of a stage
 constexpr int kWBytes = kRows * kDepth;
 constexpr int kAStages = 4, kACols = kDepth / 2; // operand stages in tensor memory, columns each
@@ -50,7 +51,8 @@ struct Cfg {
   static constexpr int kWStages = NT <= 128 ? 7 : 5;
   static constexpr int kXOff = kWStages * kWBytes;
   static constexpr int kRing = kXOff + kXStages * kXBytes;
-  static constexpr int kSmem = kRing + kCtrl + 1024;
+  static constexpr int kParam = (2 * kRows + NT) * 4;              // scales and bias of the channels, scales of the tokens
+  static constexpr int kSmem = kRing + kCtrl + kParam + 1024;
   static_assert(kSmem <= 232448, "shared memory per block");
   static_assert(NT * kRows * 4 <= kRing, "the partial sums take the ring's place");
   static_assert(NT * kAccs + kAStages * kACols <= 512, "tensor memory");
@@ -58,7 +60,7 @@ struct Cfg {
 
 struct StreamArgs {
   Int8Args q;
-  int num_kb, split, mtiles;
+  int num_kb, split, mtiles, rows;
   int y_vec;                                     // rows of Y allow stores of four values
   uint32_t idesc;
   unsigned* status;
@@ -100,6 +102,13 @@ __device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 template <typename O>
+__device__ __forceinline__ uint32_t pair_bits(O a, O b) {
+  uint16_t x, y;
+  memcpy(&x, &a, 2);
+  memcpy(&y, &b, 2);
+  return (uint32_t)x | (uint32_t)y << 16;
+}
+template <typename O>
 __device__ __forceinline__ float bias_of(const Int8Args& q, int64_t n) {
   return q.bias ? to_f32(static_cast<const O*>(q.bias)[n * q.bias_s]) : 0.f;
 }
@@ -138,6 +147,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     fence_mbar_init();
   }
+  const int rank = (int)(blockIdx.x % (unsigned)p.split), tile = (int)(blockIdx.x / (unsigned)p.split);
+  const int64_t n0 = (int64_t)(tile / p.mtiles) * p.rows, m0 = (int64_t)(tile % p.mtiles) * NT;
+  const int kb0 = (int)((int64_t)rank * p.num_kb / p.split), kb1 = (int)((int64_t)(rank + 1) * p.num_kb / p.split);
+  const int nkb = kb1 - kb0;
+  // The weights were complete before the launch in front of this one (the copy of
+  // the tokens, which lets this grid start only after its own wait): the ring is
+  // filled at once.
+  const auto load_weights = [&](int i) {
+    const int s = i % C::kWStages;
+    mbar_arrive_expect_tx(wfull + 8 * s, p.rows * kDepth);
+    tma_load_3d(sbase + s * kWBytes, &tmW, (kb0 + i) * kDepth, (int32_t)n0, 0, wfull + 8 * s);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < nkb && i < C::kWStages; ++i) load_weights(i);
   if (warp == 1) {
     tmem_alloc(smem_u32(slot), 512);
     tmem_relinquish();
@@ -147,22 +170,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *slot, tmem_a = tmem + NT * C::kAccs;
 
-  const int rank = (int)(blockIdx.x % (unsigned)p.split), tile = (int)(blockIdx.x / (unsigned)p.split);
-  const int64_t n0 = (int64_t)(tile / p.mtiles) * kRows, m0 = (int64_t)(tile % p.mtiles) * NT;
-  const int kb0 = (int)((int64_t)rank * p.num_kb / p.split), kb1 = (int)((int64_t)(rank + 1) * p.num_kb / p.split);
-  const int nkb = kb1 - kb0;
-
+  const int per = NT / p.split, cw = warp - kConvWarp0;
+  constexpr int kMine = (NT + kConvWarps - 1) / kConvWarps;      // tokens of a warp at most
+  float* param = reinterpret_cast<float*>(smem + C::kRing + kCtrl);
   if (warp == 0) {
-    // The weights were complete before the launch in front of this one (the copy
-    // of the tokens, which lets this grid start only after its own wait).
     if (elect_one()) {
-      prefetch_tmap(&tmW);
-      int i = 0;
+      int i = min(nkb, C::kWStages);
       for (; i < nkb; ++i) {
-        const int s = i % C::kWStages, ph = (i / C::kWStages) & 1;
-        if (!mbar_wait(wempty + 8 * s, ph ^ 1, abort, p.status, p.timeout_ns)) break;
-        mbar_arrive_expect_tx(wfull + 8 * s, kWBytes);
-        tma_load_3d(sbase + s * kWBytes, &tmW, (kb0 + i) * kDepth, (int32_t)n0, 0, wfull + 8 * s);
+        if (!mbar_wait(wempty + 8 * (i % C::kWStages), ((i / C::kWStages) & 1) ^ 1, abort, p.status, p.timeout_ns)) break;
+        load_weights(i);
       }
       for (int j = i > C::kWStages ? i - C::kWStages : 0; j < i; ++j)      // every copy lands before the CTA can end
         mbar_wait_teardown(wfull + 8 * (j % C::kWStages), (j / C::kWStages) & 1, p.teardown_ns);
@@ -202,8 +218,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_commit(accf);
       mbar_wait_teardown(accf, 0, p.teardown_ns);
     }
+  } else if (warp == 3) {
+    // For the epilogue (inputs, complete like the weights).
+    for (int j = lane; j < kRows; j += 32) {
+      const bool in = j < p.rows && n0 + j < p.q.N;
+      param[j] = in ? __ldg(p.q.sb + (n0 + j) * p.q.sb_s) : 0.f;
+      param[kRows + j] = in ? bias_of<O>(p.q, n0 + j) : 0.f;
+    }
+    for (int j = lane; j < NT; j += 32) param[2 * kRows + j] = m0 + j < p.q.M ? __ldg(p.q.sa + (m0 + j) * p.q.sa_s) : 0.f;
   } else if (warp >= kConvWarp0) {
-    const int cw = warp - kConvWarp0, quad = warp & 3, half = (cw >> 2) & 1, group = cw >> 3;
+    const int quad = warp & 3, half = (cw >> 2) & 1, group = cw >> 3;
     const int row = quad * 32 + lane;
     for (int i = group; i < nkb; i += 2) {
       const int ws = i % C::kWStages, as = i % kAStages;
@@ -256,38 +280,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   if (warp >= kConvWarp0 && !*abort) {
     // Tokens [rank * NT / split, ...), a warp per token, four channels a lane.
-    const int per = NT / p.split, cw = warp - kConvWarp0;
-    const int64_t n = n0 + lane * 4;
-    float sb[4], bias[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool in = n + j < p.q.N;
-      sb[j] = in ? __ldg(p.q.sb + (n + j) * p.q.sb_s) : 0.f;
-      bias[j] = in ? bias_of<O>(p.q, n + j) : 0.f;
-    }
-    for (int t = cw; t < per; t += kConvWarps) {
-      const int tok = rank * per + t;
+    const int64_t nl = n0 + lane * 4;
+    const float4 s4 = *reinterpret_cast<const float4*>(param + lane * 4);
+    const float4 b4 = *reinterpret_cast<const float4*>(param + kRows + lane * 4);
+    const float sb[4] = {s4.x, s4.y, s4.z, s4.w}, bias[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll 4
+    for (int t = 0; t < kMine; ++t) {
+      const int tok = rank * per + cw + t * kConvWarps;
       const int64_t m = m0 + tok;
-      if (m >= p.q.M) break;
+      if (cw + t * kConvWarps >= per || m >= p.q.M) break;
       const uint32_t src = sbase + (uint32_t)(tok * kRows + lane * 4) * 4;
+      const float sa = param[2 * kRows + tok];
       float v[4] = {0.f, 0.f, 0.f, 0.f};
       for (int rk = 0; rk < p.split; ++rk) {
         const float4 f = p.split > 1 ? lds128_cluster(mapa_shared(src, (uint32_t)rk))
                                      : *reinterpret_cast<const float4*>(smem + (src - sbase));
         v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
       }
-      const float sa = __ldg(p.q.sa + m * p.q.sa_s);
       O o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = from_f32<O>(__fadd_rn(__fmul_rn(__fmul_rn(v[j], sa), sb[j]), bias[j]));
-      O* y = static_cast<O*>(p.q.y) + m * p.q.N + n;
-      if (p.y_vec && n + 4 <= p.q.N) {
-        if constexpr (sizeof(O) == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(o);
-        else *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(o);
+      O* y = static_cast<O*>(p.q.y) + m * p.q.N + nl;
+      if (lane * 4 >= p.rows) continue;                // rows is a multiple of 4
+      if (p.y_vec && nl + 4 <= p.q.N) {
+        if constexpr (sizeof(O) == 4) *reinterpret_cast<float4*>(y) = make_float4(o[0], o[1], o[2], o[3]);
+        else *reinterpret_cast<uint2*>(y) = make_uint2(pair_bits(o[0], o[1]), pair_bits(o[2], o[3]));
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (n + j < p.q.N) y[j] = o[j];
+          if (nl + j < p.q.N) y[j] = o[j];
       }
     }
   }
@@ -299,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The weights [N, K] int8 as [128 channels x 128 k] tiles, 128-byte swizzled.
-bool weight_map(const Int8Args& q, CUtensorMap* map) {
+// The weights [N, K] int8 as [rows channels x 128 k] tiles, 128-byte swizzled.
+bool weight_map(const Int8Args& q, int rows, CUtensorMap* map) {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult r;
@@ -314,27 +335,86 @@ bool weight_map(const Int8Args& q, CUtensorMap* map) {
   const cuuint64_t dims[3] = {(cuuint64_t)q.K, (cuuint64_t)q.N, 1};
   const cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)pitch * (cuuint64_t)q.N};
   if (strides[0] >= (1ull << 40) || strides[1] >= (1ull << 40)) return false;
-  const cuuint32_t box[3] = {kDepth, kRows, 1}, estr[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {kDepth, (cuuint32_t)rows, 1}, estr[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(q.b), dims, strides, box, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of `split` CTAs, one CTA an SM, that are resident at once (the SMs of a
+// GPC that a cluster does not fill stay idle): 36 of 4 on 152 SMs.
 template <typename O, int NT>
-mm_status launch(const StreamArgs& p_in, const CUtensorMap& w, const CUtensorMap& x, cudaStream_t stream) {
+int resident_clusters(int split) {
+  static std::atomic<int> cache[128][4];         // value + 1 once known
+  int dev = 0, at = 0;
+  cudaGetDevice(&dev);
+  if (split == 1 || dev < 0 || dev >= 128) return sm_count_public() / split;
+  while ((1 << at) < split) ++at;
+  const int known = cache[dev][at].load(std::memory_order_relaxed);
+  if (known > 0) return known - 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(sm_count_public() / split * split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<NT>::kSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, int8_stream_kernel<O, NT>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  cache[dev][at].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// Channels per CTA and CTAs per cluster.  A CTA's stage takes the longer of its
+// bytes (about 25 a cycle and SM, all SMs streaming) and its 8 MMAs (NT / 2 cycles
+// each); starting, handing over the sums and storing take about 6000 cycles more,
+// for every round of resident clusters.  The pair with the least cycles is taken,
+// the larger tile among equals: N = 14336 has 112 tiles of 128 channels but 150 of
+// 96, which keep 150 of 152 SMs at work.
+template <typename O, int NT>
+void plan_tiles(const Int8Args& q, int num_kb, int* rows, int* split) {
+  const int64_t mtiles = (q.M + NT - 1) / NT;
+  double best = 0.;
+  *rows = kRows;
+  *split = 1;
+  for (int s = 1; s <= 8 && (s == 1 || num_kb >= 2 * s); s *= 2) {
+    const int64_t room = resident_clusters<O, NT>(s);
+    if (room < 1) continue;
+    for (int r = kRows; r >= 64; r -= 8) {
+      const int64_t rounds = ((q.N + r - 1) / r * mtiles + room - 1) / room;
+      const double bytes = r * kDepth / 25., mma = 4. * NT;
+      const double cycles = (double)rounds * (((num_kb + s - 1) / s) * (bytes > mma ? bytes : mma) + 6000.);
+      if (best == 0. || cycles < best) {
+        best = cycles;
+        *rows = r;
+        *split = s;
+      }
+    }
+  }
+}
+
+template <typename O, int NT>
+mm_status launch(const StreamArgs& p_in, const CUtensorMap& x, cudaStream_t stream) {
   StreamArgs p = p_in;
   p.mtiles = (int)((p.q.M + NT - 1) / NT);
-  const int64_t tiles = (p.q.N + kRows - 1) / kRows * p.mtiles;
-  // K over a cluster: the largest power of two up to 8 that keeps the CTAs within
-  // the SMs and gives each at least two stages.
-  int split = 8;
-  while (split > 1 && (tiles * split > sm_count_public() || p.num_kb < 2 * split)) split >>= 1;
-  p.split = split;
+  if (cudaFuncSetAttribute(int8_stream_kernel<O, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::kSmem) !=
+      cudaSuccess)
+    return MM_ERR_CUDA;
+  plan_tiles<O, NT>(p.q, p.num_kb, &p.rows, &p.split);
+  const int split = p.split;
+  const int64_t tiles = (p.q.N + p.rows - 1) / p.rows * p.mtiles;
   if (tiles * split > 0x7fffffffLL) return MM_ERR_UNSUPPORTED;
+  CUtensorMap w;
+  if (!weight_map(p.q, p.rows, &w)) return MM_ERR_UNSUPPORTED;
   p.idesc = make_idesc_mn(1, 0, 0, kRows, NT);
   const auto kernel = int8_stream_kernel<O, NT>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::kSmem) != cudaSuccess)
-    return MM_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -353,13 +433,13 @@ mm_status launch(const StreamArgs& p_in, const CUtensorMap& w, const CUtensorMap
 }
 
 template <typename O>
-mm_status launch_typed(const StreamArgs& p, int nt, const CUtensorMap& w, const CUtensorMap& x, cudaStream_t stream) {
+mm_status launch_typed(const StreamArgs& p, int nt, const CUtensorMap& x, cudaStream_t stream) {
   switch (nt) {
-    case 16: return launch<O, 16>(p, w, x, stream);
-    case 32: return launch<O, 32>(p, w, x, stream);
-    case 64: return launch<O, 64>(p, w, x, stream);
-    case 128: return launch<O, 128>(p, w, x, stream);
-    default: return launch<O, 256>(p, w, x, stream);
+    case 16: return launch<O, 16>(p, x, stream);
+    case 32: return launch<O, 32>(p, x, stream);
+    case 64: return launch<O, 64>(p, x, stream);
+    case 128: return launch<O, 128>(p, x, stream);
+    default: return launch<O, 256>(p, x, stream);
   }
 }
 
@@ -386,18 +466,17 @@ mm_status launch_int8_stream(const Int8Args& q, const void* x, int64_t ldx, unsi
   init_params(&limits);
   p.timeout_ns = limits.timeout_ns;
   p.teardown_ns = limits.teardown_ns;
-  CUtensorMap w;
   OperandPlan xp;
   BatchMap one;
   memset(&one, 0, sizeof(one));
   one.count = 1;
   for (int d = 0; d < kMaxBatchDims; ++d) one.shape[d] = 1;
   const int64_t none[kMaxBatchDims] = {};
-  if (!weight_map(q, &w) || !plan_operand(x, MM_F16, q.M, q.K, ldx, 1, one, none, nt, &xp)) return MM_ERR_UNSUPPORTED;
+  if (!plan_operand(x, MM_F16, q.M, q.K, ldx, 1, one, none, nt, &xp)) return MM_ERR_UNSUPPORTED;
   switch (q.out_dtype) {
-    case MM_F32: return launch_typed<float>(p, nt, w, xp.map, stream);
-    case MM_BF16: return launch_typed<__nv_bfloat16>(p, nt, w, xp.map, stream);
-    default: return launch_typed<__half>(p, nt, w, xp.map, stream);
+    case MM_F32: return launch_typed<float>(p, nt, xp.map, stream);
+    case MM_BF16: return launch_typed<__nv_bfloat16>(p, nt, xp.map, stream);
+    default: return launch_typed<__half>(p, nt, xp.map, stream);
   }
 }
 

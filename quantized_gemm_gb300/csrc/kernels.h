@@ -123,7 +123,7 @@ struct Int8Args {
   void* y;                   // dense [M, N]
 };
 constexpr int kInt8FewRows = 8, kInt8FewCols = 2;
-constexpr int64_t kInt8StreamRows = 256;     // rows that stream the weights as bytes (int8_tc.cu)
+constexpr int64_t kInt8StreamRows = 4096;     // rows that stream the weights as bytes (int8_tc.cu)
 // An operand's f16 copy: dst[r, c] = src[r * rs + c * cs], rows of `ld` values.
 struct Int8Copy {
   const int8_t* src; int64_t rs, cs, rows, cols, ld;
