@@ -69,7 +69,7 @@ mm_status plan_int8(const mm_tensor* A, const mm_tensor* B, int32_t out_dtype, I
 // The tensor cores' f16 copies: A [M, lda]; B as it lies, [N, ldb] or (columns
 // contiguous) [K, ldb].
 struct Int8Plan {
-  int path, stream;          // stream: B is read as it lies
+  int path, stream, as_is;   // stream: B in bytes, K-major, as it lies or as a copy [N, ldb]
   int64_t lda, ldb;
   int b_mn;
   size_t a, b, bytes;
@@ -85,9 +85,12 @@ Int8Plan int8_path(const Int8Args& a) {
   p.path = choose(a.K > 0, tensor_pays(a.M, a.N, a.K, 1));
   if (p.path != MM_PATH_TENSOR) return p;
   p.lda = (a.K + 7) / 8 * 8;
-  if (a.M <= kInt8StreamRows && int8_stream_supported(a)) {
+  if (int8_stream_pays(a)) {
     p.stream = 1;
-    p.bytes = align256((size_t)a.M * (size_t)p.lda * 2);
+    p.as_is = int8_stream_supported(a);
+    p.ldb = (a.K + 15) / 16 * 16;
+    p.b = align256((size_t)a.M * (size_t)p.lda * 2);
+    p.bytes = p.b + (p.as_is ? 0 : align256((size_t)a.N * (size_t)p.ldb));
     return p;
   }
   p.b_mn = a.b_ns == 1 && a.b_ks != 1;
@@ -139,19 +142,26 @@ mm_status mm_int8_matmul(const mm_tensor* A, const mm_tensor* B, const mm_tensor
   if (!status) return MM_ERR_CUDA;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   Int8Copy ca, cb;
+  memset(&ca, 0, sizeof(ca));
   memset(&cb, 0, sizeof(cb));
   ca.src = a.a; ca.rs = a.a_rs; ca.cs = a.a_cs; ca.rows = a.M; ca.cols = a.K; ca.ld = p.lda;
-  ca.dst = reinterpret_cast<__half*>(w + p.a);
-  if (p.stream) {
-    cb.rows = cb.cols = cb.ld = 0;
-    if ((s = launch_int8_copies(ca, cb, st)) != MM_OK) return s;
-    return finish(launch_int8_stream(a, ca.dst, p.lda, status, st), MM_PATH_TENSOR);
+  ca.dst = w + p.a;
+  if (!p.as_is) {
+    cb.src = a.b; cb.ld = p.ldb;
+    cb.rs = p.b_mn ? a.b_ks : a.b_ns; cb.cs = p.b_mn ? a.b_ns : a.b_ks;
+    cb.rows = p.b_mn ? a.K : a.N; cb.cols = p.b_mn ? a.N : a.K;
+    cb.dst = w + p.b;
+    cb.bytes = p.stream;
   }
-  cb.src = a.b; cb.ld = p.ldb;
-  cb.rs = p.b_mn ? a.b_ks : a.b_ns; cb.cs = p.b_mn ? a.b_ns : a.b_ks;
-  cb.rows = p.b_mn ? a.K : a.N; cb.cols = p.b_mn ? a.N : a.K;
-  cb.dst = reinterpret_cast<__half*>(w + p.b);
   if ((s = launch_int8_copies(ca, cb, st)) != MM_OK) return s;
+  if (p.stream) {
+    if (!p.as_is) {
+      a.b = static_cast<const int8_t*>(cb.dst);
+      a.b_ks = 1;
+      a.b_ns = p.ldb;
+    }
+    return finish(launch_int8_stream(a, ca.dst, p.lda, !p.as_is, status, st), MM_PATH_TENSOR);
+  }
   return finish(launch_tc_int8(a, ca.dst, p.lda, cb.dst, p.ldb, p.b_mn, status, st), MM_PATH_TENSOR);
 }
 

@@ -421,11 +421,13 @@ mm_status run_any(const Int8Args& a, cudaStream_t stream) {
   return MM_OK;
 }
 
-// ------------------------------------------------------------------ f16 copies
+// ------------------------------------------------------------------ copies of operands
 //
-// int8 values are exact in f16.  A row of the copy is `ld` values (a multiple of
+// int8 values are exact in f16.  A row of an f16 copy is `ld` values (a multiple of
 // 8, zeros past `cols`); 16 values a thread.  Bound: memory, 1 byte read and 2
-// written per value.
+// written per value.  A copy in bytes puts rows next to each other that are not
+// contiguous or not aligned: tiles of 64 rows x 128 columns through shared memory,
+// read along whichever side neighbours lie on.
 
 // The bytes of w (two at a time) as f16 pairs: 1024 + (byte ^ 0x80) by placing the
 // byte in the mantissa of 1024, minus 1024 + 128.
@@ -438,10 +440,33 @@ __device__ __forceinline__ void half4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   hi = *reinterpret_cast<const uint32_t*>(&dh);
 }
 
+constexpr int kCopyRows = 64, kCopyCols = 128;
+__device__ void copy_bytes(const Int8Copy& c, int64_t block) {
+  __shared__ int8_t tile[kCopyRows][kCopyCols + 4];
+  const int64_t across = (c.ld + kCopyCols - 1) / kCopyCols;
+  const int64_t r0 = block / across * kCopyRows, c0 = block % across * kCopyCols;
+  const bool along = c.cs <= c.rs;                       // a row's elements are neighbours
+#pragma unroll 16
+  for (int i = 0; i < kCopyRows * kCopyCols / 256; ++i) {
+    const int e = threadIdx.x + 256 * i;
+    const int r = along ? e / kCopyCols : e % kCopyRows, k = along ? e % kCopyCols : e / kCopyRows;
+    tile[r][k] = r0 + r < c.rows && c0 + k < c.cols ? __ldg(c.src + (r0 + r) * c.rs + (c0 + k) * c.cs) : (int8_t)0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kCopyRows * kCopyCols / 16 / 256; ++i) {
+    const int e = threadIdx.x + 256 * i, r = e / (kCopyCols / 16), k = e % (kCopyCols / 16) * 16;
+    if (r0 + r >= c.rows || c0 + k >= c.ld) continue;    // ld is a multiple of 16
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&tile[r][k]);
+    *reinterpret_cast<uint4*>(static_cast<int8_t*>(c.dst) + (r0 + r) * c.ld + c0 + k) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 __global__ void __launch_bounds__(256) int8_copy_kernel(const Int8Copy A, const Int8Copy B, const int64_t blocks_a) {
   pdl_begin();               // the product may start: it waits for this grid where it reads a copy
   const bool first = (int64_t)blockIdx.x < blocks_a;
   const Int8Copy& c = first ? A : B;
+  if (c.bytes) return copy_bytes(c, (int64_t)blockIdx.x - (first ? 0 : blocks_a));
   const int64_t per_row = (c.ld + 15) / 16;
   const int64_t e = ((int64_t)blockIdx.x - (first ? 0 : blocks_a)) * 256 + threadIdx.x;
   if (e >= per_row * c.rows) return;
@@ -462,7 +487,7 @@ __global__ void __launch_bounds__(256) int8_copy_kernel(const Int8Copy A, const 
   half4(u.y, o[0].z, o[0].w);
   half4(u.z, o[1].x, o[1].y);
   half4(u.w, o[1].z, o[1].w);
-  uint4* dst = reinterpret_cast<uint4*>(c.dst + r * c.ld + c0);
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(c.dst) + r * c.ld + c0);
   dst[0] = o[0];
   if (c0 + 8 < c.ld) dst[1] = o[1];
 }
@@ -500,7 +525,10 @@ mm_status launch_int8_any(const Int8Args& a, cudaStream_t stream) {
 }
 
 mm_status launch_int8_copies(const Int8Copy& A, const Int8Copy& B, cudaStream_t stream) {
-  const auto blocks = [](const Int8Copy& c) { return ((c.ld + 15) / 16 * c.rows + 255) / 256; };
+  const auto blocks = [](const Int8Copy& c) {
+    return c.bytes ? (c.rows + kCopyRows - 1) / kCopyRows * ((c.ld + kCopyCols - 1) / kCopyCols)
+                   : ((c.ld + 15) / 16 * c.rows + 255) / 256;
+  };
   const int64_t na = blocks(A), nb = blocks(B);
   if (na + nb >= (1ll << 31)) return MM_ERR_UNSUPPORTED;
   return launch_pdl(int8_copy_kernel, dim3((unsigned)(na + nb)), dim3(256), 0, stream, A, B, na) == cudaSuccess

@@ -61,6 +61,7 @@ struct Cfg {
 struct StreamArgs {
   Int8Args q;
   int num_kb, split, mtiles, rows;
+  int w_late;                                    // the launch in front of this one writes the weights
   int y_vec;                                     // rows of Y allow stores of four values
   uint32_t idesc;
   unsigned* status;
@@ -151,16 +152,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t n0 = (int64_t)(tile / p.mtiles) * p.rows, m0 = (int64_t)(tile % p.mtiles) * NT;
   const int kb0 = (int)((int64_t)rank * p.num_kb / p.split), kb1 = (int)((int64_t)(rank + 1) * p.num_kb / p.split);
   const int nkb = kb1 - kb0;
-  // The weights were complete before the launch in front of this one (the copy of
-  // the tokens, which lets this grid start only after its own wait): the ring is
-  // filled at once.
+  // Unless they are a copy too, the weights were complete before the launch in
+  // front of this one (the copy of the tokens, which lets this grid start only
+  // after its own wait): the ring is filled at once.
   const auto load_weights = [&](int i) {
     const int s = i % C::kWStages;
     mbar_arrive_expect_tx(wfull + 8 * s, p.rows * kDepth);
     tma_load_3d(sbase + s * kWBytes, &tmW, (kb0 + i) * kDepth, (int32_t)n0, 0, wfull + 8 * s);
   };
-  if (threadIdx.x == 0)
+  if (threadIdx.x == 0) {
+    if (p.w_late) pdl_wait();
     for (int i = 0; i < nkb && i < C::kWStages; ++i) load_weights(i);
+  }
   if (warp == 1) {
     tmem_alloc(smem_u32(slot), 512);
     tmem_relinquish();
@@ -343,7 +346,6 @@ bool weight_map(const Int8Args& q, int rows, CUtensorMap* map) {
 
 // Clusters of `split` CTAs, one CTA an SM, that are resident at once (the SMs of a
 // GPC that a cluster does not fill stay idle): 36 of 4 on 152 SMs.
-template <typename O, int NT>
 int resident_clusters(int split) {
   static std::atomic<int> cache[128][4];         // value + 1 once known
   int dev = 0, at = 0;
@@ -352,6 +354,7 @@ int resident_clusters(int split) {
   while ((1 << at) < split) ++at;
   const int known = cache[dev][at].load(std::memory_order_relaxed);
   if (known > 0) return known - 1;
+  const auto kernel = int8_stream_kernel<float, 256>;      // any: all leave room for one CTA an SM
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -360,11 +363,12 @@ int resident_clusters(int split) {
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(sm_count_public() / split * split));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<NT>::kSmem;
+  cfg.dynamicSmemBytes = Cfg<256>::kSmem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, int8_stream_kernel<O, NT>, &cfg) != cudaSuccess) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<256>::kSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -372,32 +376,39 @@ int resident_clusters(int split) {
   return n;
 }
 
-// Channels per CTA and CTAs per cluster.  A CTA's stage takes the longer of its
-// bytes (about 25 a cycle and SM, all SMs streaming) and its 8 MMAs (NT / 2 cycles
-// each); starting, handing over the sums and storing take about 6000 cycles more,
-// for every round of resident clusters.  The pair with the least cycles is taken,
-// the larger tile among equals: N = 14336 has 112 tiles of 128 channels but 150 of
-// 96, which keep 150 of 152 SMs at work.
-template <typename O, int NT>
-void plan_tiles(const Int8Args& q, int num_kb, int* rows, int* split) {
-  const int64_t mtiles = (q.M + NT - 1) / NT;
-  double best = 0.;
-  *rows = kRows;
-  *split = 1;
-  for (int s = 1; s <= 8 && (s == 1 || num_kb >= 2 * s); s *= 2) {
-    const int64_t room = resident_clusters<O, NT>(s);
-    if (room < 1) continue;
-    for (int r = kRows; r >= 64; r -= 8) {
-      const int64_t rounds = ((q.N + r - 1) / r * mtiles + room - 1) / room;
-      const double bytes = r * kDepth / 25., mma = 4. * NT;
-      const double cycles = (double)rounds * (((num_kb + s - 1) / s) * (bytes > mma ? bytes : mma) + 6000.);
-      if (best == 0. || cycles < best) {
-        best = cycles;
-        *rows = r;
-        *split = s;
+// Tokens and channels per CTA and CTAs per cluster.  A CTA's stage takes the
+// longer of its bytes (about 25 a cycle and SM, all SMs streaming) and its 8 MMAs
+// (NT / 2 cycles each); starting, handing over the sums and storing take about 6000
+// cycles more, for every round of resident clusters.  The least cycles win, the
+// larger tile among equals: N = 14336 has 112 tiles of 128 channels but 150 of 96,
+// which keep 150 of 152 SMs at work; 1027 tokens are 5 tiles of 256 or 9 of 128.
+struct TilePlan {
+  int nt, rows, split;
+  int64_t rounds;
+};
+TilePlan plan_tiles(const Int8Args& q) {
+  const int num_kb = (int)((q.K + kDepth - 1) / kDepth);
+  int first = 16;
+  while (first < 256 && first < q.M) first *= 2;
+  TilePlan best = {first, kRows, 1, 1};
+  double least = 0.;
+  for (int nt = first; nt >= 128 || nt == first; nt /= 2) {
+    const int64_t mtiles = (q.M + nt - 1) / nt;
+    for (int s = 1; s <= 8 && (s == 1 || num_kb >= 2 * s); s *= 2) {
+      const int64_t room = resident_clusters(s);
+      if (room < 1) continue;
+      for (int r = kRows; r >= 64; r -= 8) {
+        const int64_t rounds = ((q.N + r - 1) / r * mtiles + room - 1) / room;
+        const double bytes = r * kDepth / 25., mma = 4. * nt;
+        const double cycles = (double)rounds * (((num_kb + s - 1) / s) * (bytes > mma ? bytes : mma) + 6000.);
+        if (least == 0. || cycles < least) {
+          least = cycles;
+          best = {nt, r, s, rounds};
+        }
       }
     }
   }
+  return best;
 }
 
 template <typename O, int NT>
@@ -407,7 +418,6 @@ mm_status launch(const StreamArgs& p_in, const CUtensorMap& x, cudaStream_t stre
   if (cudaFuncSetAttribute(int8_stream_kernel<O, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::kSmem) !=
       cudaSuccess)
     return MM_ERR_CUDA;
-  plan_tiles<O, NT>(p.q, p.num_kb, &p.rows, &p.split);
   const int split = p.split;
   const int64_t tiles = (p.q.N + p.rows - 1) / p.rows * p.mtiles;
   if (tiles * split > 0x7fffffffLL) return MM_ERR_UNSUPPORTED;
@@ -451,13 +461,30 @@ bool int8_stream_supported(const Int8Args& q) {
          (reinterpret_cast<uintptr_t>(q.b) & 15) == 0;
 }
 
-mm_status launch_int8_stream(const Int8Args& q, const void* x, int64_t ldx, unsigned* status, cudaStream_t stream) {
+// One round of CTAs, or so few rows that the f16 copies of the weights (3 bytes
+// moved for each) and a last round of half-empty tiles cost the dense product more.
+// us here and there, M = 300, 1024, 2048:
+//   4096 x 14336   60  81    94 100   181 159
+//   4096 x  4096   22  34    33  37    64  59
+//   2048 x  2048   12  19    17  20    22  22
+//   1024 x  1024   10  12    11  13    13  15
+//   8192 x  1024   22  49    25  52    40  56     (K = 8192)
+//    512 x  8192   11  12    22  16    41  23     (K = 512)
+bool int8_stream_pays(const Int8Args& q) {
+  return q.M <= 256 || (q.M <= 1024 && q.K >= 2048) || (q.M <= 2048 && plan_tiles(q).rounds == 1);
+}
+
+mm_status launch_int8_stream(const Int8Args& q, const void* x, int64_t ldx, int w_late, unsigned* status,
+                             cudaStream_t stream) {
   if (!status) return MM_ERR_CUDA;
-  int nt = 16;
-  while (nt < 256 && nt < q.M) nt *= 2;
   StreamArgs p;
   memset(&p, 0, sizeof(p));
   p.q = q;
+  p.w_late = w_late;
+  const TilePlan t = plan_tiles(q);
+  const int nt = t.nt;
+  p.rows = t.rows;
+  p.split = t.split;
   p.num_kb = (int)((q.K + kDepth - 1) / kDepth);
   const int size = q.out_dtype == MM_F32 ? 4 : 2;
   p.y_vec = q.N % 4 == 0 && (reinterpret_cast<uintptr_t>(q.y) & (size * 4 - 1)) == 0;

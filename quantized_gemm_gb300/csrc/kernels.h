@@ -123,11 +123,12 @@ struct Int8Args {
   void* y;                   // dense [M, N]
 };
 constexpr int kInt8FewRows = 8, kInt8FewCols = 2;
-constexpr int64_t kInt8StreamRows = 4096;     // rows that stream the weights as bytes (int8_tc.cu)
-// An operand's f16 copy: dst[r, c] = src[r * rs + c * cs], rows of `ld` values.
+// An operand's copy, f16 or (bytes) int8: dst[r, c] = src[r * rs + c * cs], rows of
+// `ld` values.
 struct Int8Copy {
   const int8_t* src; int64_t rs, cs, rows, cols, ld;
-  __half* dst;
+  void* dst;
+  int bytes;
 };
 
 // Orthogonalised update (mm_orthogonalize).
@@ -177,7 +178,7 @@ mm_status launch_balance_grad(const BalanceGradArgs& args, cudaStream_t stream);
 
 mm_status launch_quantize_rows(const QuantizeArgs& args, cudaStream_t stream);
 // Few rows against columns of B contiguous along k (16-byte aligned); every
-// stride; the operands' f16 copies for the tensor cores.
+// stride; the operands' copies for the tensor cores (A f16, B either).
 bool int8_few_supported(const Int8Args& args);
 mm_status launch_int8_few(const Int8Args& args, cudaStream_t stream);
 mm_status launch_int8_any(const Int8Args& args, cudaStream_t stream);

@@ -24,10 +24,13 @@ mm_status launch_tc_qlinear(const QLinearArgs& q, void* workspace, unsigned* sta
 mm_status launch_tc_int8(const Int8Args& q, const void* a, int64_t lda, const void* b, int64_t ldb, int b_mn,
                          unsigned* status, cudaStream_t stream);
 
-// The same for up to a few hundred rows, of a's f16 copy (rows ldx apart) and
-// the int8 weights as they lie (columns contiguous along k, 16-byte aligned).
+// The same for fewer rows, of a's f16 copy (rows ldx apart) and int8 weights whose
+// columns are contiguous along k and 16-byte aligned, as they lie or as a copy that
+// the launch before makes (w_late).
 bool int8_stream_supported(const Int8Args& q);
-mm_status launch_int8_stream(const Int8Args& q, const void* x, int64_t ldx, unsigned* status, cudaStream_t stream);
+bool int8_stream_pays(const Int8Args& q);
+mm_status launch_int8_stream(const Int8Args& q, const void* x, int64_t ldx, int w_late, unsigned* status,
+                             cudaStream_t stream);
 
 // A product of the orthogonalised update's chain, over `count` matrices of f16
 // operands: sym != 0, Y = f16(alpha A B + beta C), symmetric (C optional); else
