@@ -93,7 +93,7 @@ Int8Plan int8_path(const Int8Args& a) {
     p.bytes = p.b + (p.as_is ? 0 : align256((size_t)a.N * (size_t)p.ldb));
     return p;
   }
-  p.b_mn = a.b_ns == 1 && a.b_ks != 1;
+  p.b_mn = a.b_ns == 1 && a.b_ks != 1;      // (only the dense product's copy keeps that order)
   p.ldb = ((p.b_mn ? a.N : a.K) + 7) / 8 * 8;
   p.a = 0;
   p.b = align256((size_t)a.M * (size_t)p.lda * 2);

@@ -424,10 +424,27 @@ mm_status run_any(const Int8Args& a, cudaStream_t stream) {
 // ------------------------------------------------------------------ copies of operands
 //
 // int8 values are exact in f16.  A row of an f16 copy is `ld` values (a multiple of
-// 8, zeros past `cols`); 16 values a thread.  Bound: memory, 1 byte read and 2
-// written per value.  A copy in bytes puts rows next to each other that are not
-// contiguous or not aligned: tiles of 64 rows x 128 columns through shared memory,
-// read along whichever side neighbours lie on.
+// 8, zeros past `cols`), of a copy in bytes a multiple of 16; 16 values a thread.
+// Bound: memory, 1 byte read and 2 or 1 written per value.  Sources of any
+// alignment are read in aligned words (each holds a byte that is wanted) and
+// shifted; one whose rows are neighbours (rs = 1) is turned in tiles of 128 x 128
+// through shared memory.  (Byte by byte, 4096 x 14336 took 160 us.)
+
+// 4 bytes, and 16, at any address.
+__device__ __forceinline__ uint32_t bytes4(const int8_t* p) {
+  const uint32_t sh = ((uint32_t)reinterpret_cast<uintptr_t>(p) & 3u) * 8;
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
+  return sh ? __funnelshift_r(__ldg(w), __ldg(w + 1), sh) : __ldg(w);
+}
+__device__ __forceinline__ uint4 bytes16(const int8_t* p) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  if ((at & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t sh = ((uint32_t)at & 3u) * 8;
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
+  const uint32_t w0 = __ldg(w), w1 = __ldg(w + 1), w2 = __ldg(w + 2), w3 = __ldg(w + 3), w4 = sh ? __ldg(w + 4) : 0u;
+  return make_uint4(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh), __funnelshift_r(w2, w3, sh),
+                    __funnelshift_r(w3, w4, sh));
+}
 
 // The bytes of w (two at a time) as f16 pairs: 1024 + (byte ^ 0x80) by placing the
 // byte in the mantissa of 1024, minus 1024 + 128.
@@ -440,47 +457,76 @@ __device__ __forceinline__ void half4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   hi = *reinterpret_cast<const uint32_t*>(&dh);
 }
 
-constexpr int kCopyRows = 64, kCopyCols = 128;
-__device__ void copy_bytes(const Int8Copy& c, int64_t block) {
-  __shared__ int8_t tile[kCopyRows][kCopyCols + 4];
-  const int64_t across = (c.ld + kCopyCols - 1) / kCopyCols;
-  const int64_t r0 = block / across * kCopyRows, c0 = block % across * kCopyCols;
-  const bool along = c.cs <= c.rs;                       // a row's elements are neighbours
-#pragma unroll 16
-  for (int i = 0; i < kCopyRows * kCopyCols / 256; ++i) {
-    const int e = threadIdx.x + 256 * i;
-    const int r = along ? e / kCopyCols : e % kCopyRows, k = along ? e % kCopyCols : e / kCopyRows;
-    tile[r][k] = r0 + r < c.rows && c0 + k < c.cols ? __ldg(c.src + (r0 + r) * c.rs + (c0 + k) * c.cs) : (int8_t)0;
+// A copy in bytes of a source whose rows are neighbours (rs = 1): 4 x 4 bytes a step.
+constexpr int kTile = 128;
+__device__ void turn_bytes(const Int8Copy& c, int64_t block) {
+  __shared__ uint32_t tile[kTile][kTile / 4 + 1];      // [row][4 columns], words XORed with row / 32: no bank conflicts
+  const int64_t across = (c.ld + kTile - 1) / kTile;
+  const int64_t r0 = block / across * kTile, c0 = block % across * kTile;
+  const int g = threadIdx.x & 31;
+  const int64_t r = r0 + 4 * g;
+#pragma unroll
+  for (int i = 0; i < kTile / 32; ++i) {
+    const int kq = (threadIdx.x >> 5) + 8 * i;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t k = c0 + 4 * kq + j;
+      w[j] = 0;
+      if (k < c.cols) {
+        const int8_t* p = c.src + k * c.cs + r;
+        if (r + 4 <= c.rows) {
+          w[j] = bytes4(p);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (r + e < c.rows) w[j] |= (uint32_t)(uint8_t)__ldg(p + e) << (8 * e);
+        }
+      }
+    }
+    const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+    const uint32_t d = __byte_perm(w[0], w[1], 0x7362), e = __byte_perm(w[2], w[3], 0x7362);
+    const int at = kq ^ (g >> 3);
+    tile[4 * g][at] = __byte_perm(a, b, 0x5410);
+    tile[4 * g + 1][at] = __byte_perm(a, b, 0x7632);
+    tile[4 * g + 2][at] = __byte_perm(d, e, 0x5410);
+    tile[4 * g + 3][at] = __byte_perm(d, e, 0x7632);
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kCopyRows * kCopyCols / 16 / 256; ++i) {
-    const int e = threadIdx.x + 256 * i, r = e / (kCopyCols / 16), k = e % (kCopyCols / 16) * 16;
-    if (r0 + r >= c.rows || c0 + k >= c.ld) continue;    // ld is a multiple of 16
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&tile[r][k]);
-    *reinterpret_cast<uint4*>(static_cast<int8_t*>(c.dst) + (r0 + r) * c.ld + c0 + k) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < kTile * kTile / 16 / 256; ++i) {
+    const int e = threadIdx.x + 256 * i, row = e / (kTile / 16), q = e % (kTile / 16) * 4, x = row >> 5;
+    if (r0 + row >= c.rows || c0 + 4 * q >= c.ld) continue;
+    const uint32_t* t = tile[row];
+    *reinterpret_cast<uint4*>(static_cast<int8_t*>(c.dst) + (r0 + row) * c.ld + c0 + 4 * q) =
+        make_uint4(t[q ^ x], t[(q + 1) ^ x], t[(q + 2) ^ x], t[(q + 3) ^ x]);
   }
 }
+__host__ __device__ __forceinline__ bool turned(const Int8Copy& c) { return c.bytes && c.rs == 1 && c.cs != 1; }
 
 __global__ void __launch_bounds__(256) int8_copy_kernel(const Int8Copy A, const Int8Copy B, const int64_t blocks_a) {
   pdl_begin();               // the product may start: it waits for this grid where it reads a copy
   const bool first = (int64_t)blockIdx.x < blocks_a;
   const Int8Copy& c = first ? A : B;
-  if (c.bytes) return copy_bytes(c, (int64_t)blockIdx.x - (first ? 0 : blocks_a));
+  if (turned(c)) return turn_bytes(c, (int64_t)blockIdx.x - (first ? 0 : blocks_a));
   const int64_t per_row = (c.ld + 15) / 16;
   const int64_t e = ((int64_t)blockIdx.x - (first ? 0 : blocks_a)) * 256 + threadIdx.x;
   if (e >= per_row * c.rows) return;
-  const int64_t r = e / per_row, c0 = (e - r * per_row) * 16;
+  const int64_t r = e < (1ll << 32) ? (int64_t)((uint32_t)e / (uint32_t)per_row) : e / per_row, c0 = (e - r * per_row) * 16;
   const int8_t* src = c.src + r * c.rs + c0 * c.cs;
   uint4 u;
-  if (c.cs == 1 && c0 + 16 <= c.cols && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-    u = __ldg(reinterpret_cast<const uint4*>(src));
+  if (c.cs == 1 && c0 + 16 <= c.cols) {
+    u = bytes16(src);
   } else {
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 16; ++j)
       if (c0 + j < c.cols) w[j >> 2] |= (uint32_t)(uint8_t)__ldg(src + j * c.cs) << (8 * (j & 3));
     u = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (c.bytes) {
+    *reinterpret_cast<uint4*>(static_cast<int8_t*>(c.dst) + r * c.ld + c0) = u;
+    return;
   }
   uint4 o[2];
   half4(u.x, o[0].x, o[0].y);
@@ -526,8 +572,8 @@ mm_status launch_int8_any(const Int8Args& a, cudaStream_t stream) {
 
 mm_status launch_int8_copies(const Int8Copy& A, const Int8Copy& B, cudaStream_t stream) {
   const auto blocks = [](const Int8Copy& c) {
-    return c.bytes ? (c.rows + kCopyRows - 1) / kCopyRows * ((c.ld + kCopyCols - 1) / kCopyCols)
-                   : ((c.ld + 15) / 16 * c.rows + 255) / 256;
+    return turned(c) ? (c.rows + kTile - 1) / kTile * ((c.ld + kTile - 1) / kTile)
+                     : ((c.ld + 15) / 16 * c.rows + 255) / 256;
   };
   const int64_t na = blocks(A), nb = blocks(B);
   if (na + nb >= (1ll << 31)) return MM_ERR_UNSUPPORTED;

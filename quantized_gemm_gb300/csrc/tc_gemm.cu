@@ -641,6 +641,54 @@ __device__ __forceinline__ void scale_columns32(const TcParams& p, int64_t n, fl
       v[j] = __fadd_rn(v[j], c);
     }
 }
+// A warp's 32 x 32 block (a row per lane) to a dense Y whose rows are not 16-byte
+// aligned, or that is fp32: through the warp's 2 KB slice, so that the lanes store
+// neighbouring columns.  y0: Y at the block's first row and column; `rows` and
+// `cols` of it are stored.
+__device__ __forceinline__ void store_block16(uint32_t* stg, int lane, const uint32_t (&w)[16], uint16_t* y0, int64_t rs,
+                                              int rows, int cols) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint4*>(stg + lane * 16 + ((q ^ ((lane >> 1) & 3)) * 4)) =
+        make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  __syncwarp();
+  const uint16_t* e = reinterpret_cast<const uint16_t*>(stg);
+#pragma unroll 8
+  for (int r = 0; r < rows; ++r) {
+    const uint16_t v = e[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)];
+    if (lane < cols) y0[r * rs + lane] = v;
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void store_block32(uint32_t* stg, int lane, const float (&v)[32], float* y0, int64_t rs,
+                                              int rows, int cols, int vec) {
+  const float* e = reinterpret_cast<const float*>(stg);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4*>(stg + lane * 16 + ((q ^ ((lane >> 1) & 3)) * 4)) =
+          make_float4(v[16 * h + 4 * q], v[16 * h + 4 * q + 1], v[16 * h + 4 * q + 2], v[16 * h + 4 * q + 3]);
+    __syncwarp();
+    if (vec && 16 * h + 16 <= cols) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), q = lane & 3;
+        if (r < rows)
+          *reinterpret_cast<float4*>(y0 + r * rs + 16 * h + 4 * q) =
+              *reinterpret_cast<const float4*>(e + r * 16 + ((q ^ ((r >> 1) & 3)) << 2));
+      }
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int r = i * 2 + (lane >> 4), c = lane & 15;
+        if (r < rows && 16 * h + c < cols) y0[r * rs + 16 * h + c] = e[r * 16 + (((c >> 2) ^ ((r >> 1) & 3)) << 2) + (c & 3)];
+      }
+    }
+    __syncwarp();
+  }
+}
+
 // 32 fp32 values of a row from column n on (128 bytes where the row allows vectors).
 __device__ __forceinline__ void store_f32_32(const TcParams& p, float* yf, int64_t n, const float (&v)[32]) {
   if (p.y_vec && n + 32 <= p.N) {
@@ -1326,7 +1374,8 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
             for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(__uint_as_float(r[h][j]), row_scale);
             scale_columns32(p, n, v);
             if (p.out_f32) {
-              if (rok) store_f32_32(p, static_cast<float*>(p.y) + (ti.m0 + roff + rl) * p.y_rs, n, v);
+              store_block32(stg, lane, v, static_cast<float*>(p.y) + (ti.m0 + roff + rbase) * p.y_rs + n, p.y_rs,
+                            min(32, rows_t - rbase), (int)min((int64_t)32, p.N - n), p.y_vec);
               continue;
             }
           } else {
@@ -1340,6 +1389,12 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], p.out_f16);
+          if constexpr (MODE == kInt8 || MODE == kState) {
+            store_block16(stg, lane, w,
+                          static_cast<uint16_t*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + (ti.m0 + roff + rbase) * p.y_rs + n,
+                          p.y_rs, min(32, rows_t - rbase), (int)min((int64_t)32, p.N - n));
+            continue;
+          }
           if (p.y_vec && n + 32 <= p.N) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -1478,7 +1533,8 @@ __device__ void run_split_epilogue(const TcParams& p, const CUtensorMap* tmY, ui
           }
         }
         if (p.y_lo == 0) {                   // the result
-          if (rok) store_f32_32(p, static_cast<float*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + m * p.y_rs, n, v);
+          store_block32(stage, lane, v, static_cast<float*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + row0 * p.y_rs + n,
+                        p.y_rs, min(32, rows_t - quad * 32), (int)min((int64_t)32, p.N - n), p.y_vec);
           continue;
         }
         if (srow) {
