@@ -184,7 +184,9 @@ mm_status launch_int8_few(const Int8Args& args, cudaStream_t stream);
 mm_status launch_int8_any(const Int8Args& args, cudaStream_t stream);
 mm_status launch_int8_copies(const Int8Copy& A, const Int8Copy& B, cudaStream_t stream);
 
-// The norm, the division and the chain of products.
+// The norm, the division and the chain of products; or, up to kOrthoSmallWork =
+// m m n matrices (m the smaller side) that fit a cluster's shared memory, one launch.
+constexpr double kOrthoSmallWork = 1.5e8;
 size_t ortho_workspace_bytes(const OrthoArgs& args);
 mm_status launch_ortho(const OrthoArgs& args, void* workspace, cudaStream_t stream);
 

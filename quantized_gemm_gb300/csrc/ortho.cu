@@ -9,6 +9,7 @@
 
 #include "api_internal.h"
 #include "kernels.h"
+#include "ortho.cuh"
 #include "tc.h"
 
 namespace qg {
@@ -35,27 +36,6 @@ struct NormArgs {
   __half* h;                         // that times `up` as f16 [count][M][ld] and, `rest` further, what that leaves (NULL: not wanted)
   int64_t ld, rest;
   float up;
-};
-
-// Sums of squares over the whole range of fp32: values of 2^50 and more, and of
-// less than 2^-60, are squared after a shift by 2^-80 and 2^80.
-struct Squares {
-  float mid = 0.f, big = 0.f, small = 0.f;
-  __device__ __forceinline__ void add(float x) {
-    const float ax = fabsf(x);
-    if (ax < 1.1258999e+15f && (ax >= 8.6736174e-19f || ax == 0.f)) {
-      mid = fmaf(x, x, mid);
-    } else if (ax < 1.f) {
-      const float y = x * 1.2089258e+24f;
-      small = fmaf(y, y, small);
-    } else {                         // infinities and NaN too
-      const float y = x * 8.2718061e-25f;
-      big = fmaf(y, y, big);
-    }
-  }
-  __device__ __forceinline__ double total() const {
-    return (double)mid + (double)big * 1.4615016373309029e+48 + (double)small * 6.8422776578360209e-49;   // 2^160, 2^-160
-  }
 };
 
 template <typename T, bool VEC>
@@ -108,15 +88,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs a) {
   }
 }
 
-// |X|_F + eps from the shares' sums, as d = m 2^k: fp32 division where the whole
-// is in fp32's middle range (k = 0), m in [1, 2) otherwise.
-struct Divisor {
-  float m;
-  int k;
-  __device__ __forceinline__ float divide(float x) const {
-    return k == 0 ? __fdiv_rn(x, m) : __fdiv_rn(scalbnf(x, -k), m);
-  }
-};
+// |X|_F + eps from the shares' sums.
 __device__ __forceinline__ Divisor load_divisor(const NormArgs& a, int64_t b) {
   __shared__ double total;
   if (threadIdx.x < 32) {
@@ -127,23 +99,7 @@ __device__ __forceinline__ Divisor load_divisor(const NormArgs& a, int64_t b) {
     if (threadIdx.x == 0) total = sqrt(v) + (double)a.eps;
   }
   __syncthreads();
-  Divisor d;
-  const double t = total;
-  if (!(t < 1e30) || !(t > 1e-30)) {
-    if (t > 0. && t < 1e300) {
-      int k;
-      const double f = frexp(t, &k);
-      d.m = (float)(2. * f);
-      d.k = k - 1;
-    } else {                        // zero, infinite, NaN
-      d.m = (float)t;
-      d.k = 0;
-    }
-  } else {
-    d.m = (float)t;
-    d.k = 0;
-  }
-  return d;
+  return Divisor(total);
 }
 
 template <typename T, bool VEC>
@@ -517,10 +473,13 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
   return finish(s, MM_PATH_TENSOR);
 }
 
+bool ortho_small(const OrthoArgs& o) { return path_policy() != MM_PATH_TENSOR && ortho_small_pays(o); }
+
 }  // namespace
 
 size_t ortho_workspace_bytes(const OrthoArgs& o) {
   // The coefficients are not known yet: room for either chain of 16-bit matrices.
+  if (ortho_small(o)) return 0;
   const size_t f = plan_float(o).bytes;
   if (!half_chain(o)) return f;
   const size_t h = plan_half(o).bytes;
@@ -528,6 +487,7 @@ size_t ortho_workspace_bytes(const OrthoArgs& o) {
 }
 
 mm_status launch_ortho(const OrthoArgs& o, void* workspace, cudaStream_t stream) {
+  if (ortho_small(o)) return finish(launch_ortho_small(o, stream), MM_PATH_SIMT);
   HalfScales k[MM_ORTHO_MAX_STEPS + 1];
   if (o.steps > 0 && half_chain(o) && half_scales(o, k)) return run_half(o, k, workspace, stream);
   return run_float(o, workspace, stream);

@@ -1,0 +1,53 @@
+// What the two forms of the orthogonalised update share: the norm over fp32's
+// whole range and the division by it.
+#pragma once
+
+#include "kernels.h"
+
+namespace qg {
+
+// Sums of squares over the whole range of fp32: values of 2^50 and more, and of
+// less than 2^-60, are squared after a shift by 2^-80 and 2^80.
+struct Squares {
+  float mid = 0.f, big = 0.f, small = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float ax = fabsf(x);
+    if (ax < 1.1258999e+15f && (ax >= 8.6736174e-19f || ax == 0.f)) {
+      mid = fmaf(x, x, mid);
+    } else if (ax < 1.f) {
+      const float y = x * 1.2089258e+24f;
+      small = fmaf(y, y, small);
+    } else {                         // infinities and NaN too
+      const float y = x * 8.2718061e-25f;
+      big = fmaf(y, y, big);
+    }
+  }
+  __device__ __forceinline__ double total() const {
+    return (double)mid + (double)big * 1.4615016373309029e+48 + (double)small * 6.8422776578360209e-49;   // 2^160, 2^-160
+  }
+};
+
+// d = |X|_F + eps as m 2^k: fp32 division where it is in fp32's middle range (k =
+// 0), m in [1, 2) otherwise.
+struct Divisor {
+  float m;
+  int k;
+  __device__ __forceinline__ explicit Divisor(double t) {
+    m = (float)t;
+    k = 0;
+    if ((!(t < 1e30) || !(t > 1e-30)) && t > 0. && t < 1e300) {      // not zero, infinite or NaN
+      const double f = frexp(t, &k);
+      m = (float)(2. * f);
+      --k;
+    }
+  }
+  __device__ __forceinline__ float divide(float x) const {
+    return k == 0 ? __fdiv_rn(x, m) : __fdiv_rn(scalbnf(x, -k), m);
+  }
+};
+
+// Small matrices, one cluster each (ortho_small.cu).
+bool ortho_small_pays(const OrthoArgs& args);
+mm_status launch_ortho_small(const OrthoArgs& args, cudaStream_t stream);
+
+}  // namespace qg

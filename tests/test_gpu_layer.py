@@ -308,6 +308,43 @@ def test_orthogonalize(shape, dtype):
     _check_ortho(rand_tensor(shape, dtype, sum(shape), DEV))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("shape", [(2, 2), (16, 16), (61, 100), (100, 61), (64, 64), (65, 300), (300, 65), (130, 136), (256, 256), (257, 600),
+                                   (385, 129), (520, 264), (3, 20, 33), (5, 130, 64), (3, 136, 264), (2, 300, 1100)])
+def test_orthogonalize_on_the_tensor_cores(shape, dtype):
+    """The chain of products for sizes that a cluster would take; tiles that end inside, and on both sides of the diagonal."""
+    qg.mm_set_path_policy(qg.MM_PATH_TENSOR)
+    try:
+        _check_ortho(rand_tensor(shape, dtype, sum(shape) + 1, DEV), scale=1.5)
+        assert qg.mm_last_path() == qg.MM_PATH_TENSOR
+        _check_ortho(rand_tensor(shape, dtype, sum(shape) + 2, DEV), steps=1)
+    finally:
+        qg.mm_set_path_policy(qg.MM_PATH_AUTO)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(300, 520), (2, 260, 200), (129, 1300)])
+def test_orthogonalize_on_the_cuda_cores(shape, dtype):
+    """The chain in fp32: larger than a cluster's shared memory, and coefficients that leave the f16 operands' range."""
+    X = rand_tensor(shape, dtype, 9, DEV)
+    qg.mm_set_path_policy(qg.MM_PATH_SIMT)
+    try:
+        _check_ortho(X)
+        assert qg.mm_last_path() == qg.MM_PATH_SIMT
+    finally:
+        qg.mm_set_path_policy(qg.MM_PATH_AUTO)
+    _check_ortho(X, 5, (40.0, 0.0, 0.0))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("shape", [(8, 16), (31, 31), (32, 5000), (33, 1000), (1000, 33), (64, 4000), (65, 999), (128, 1024), (1024, 127),
+                                   (90, 11, 7), (200, 40, 64), (30, 128, 130)])
+def test_orthogonalize_in_a_cluster(shape, dtype):
+    """Slabs of every size, stacks with fewer CTAs a matrix."""
+    _check_ortho(rand_tensor(shape, dtype, sum(shape) + 3, DEV), scale=0.3)
+    assert qg.mm_last_path() == qg.MM_PATH_SIMT
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("shape", [(3, 20, 33), (2, 2, 70, 30), (5, 130, 64), (1, 1, 8), (40, 17, 17), (3, 136, 264)])
 def test_orthogonalize_stacks(shape, dtype):
@@ -465,10 +502,11 @@ def test_graphs_replay_on_new_values():
 
 def test_given_workspaces_and_outputs():
     """A workspace full of garbage gives the same results, and one byte too few is refused."""
+    assert qg.mm_orthogonalize_workspace_size(torch.empty((60, 80), device=DEV)) == 0
     l, idx = _balance_inputs(300, 40, 2, F32, 91, 0)
     A, B, sa, sb, _ = _int8_inputs(300, 512, 264, F32, 92)
     X = rand_tensor((300, 264), BF16, 93, DEV)
-    R = rand_tensor((200, 264), F32, 94, DEV)
+    R = rand_tensor((400, 264), F32, 94, DEV)
     for size, call in ((qg.mm_route_balance_workspace_size(l, idx), lambda w: qg.mm_route_balance(l, idx, workspace=w)),
                        (qg.mm_int8_matmul_workspace_size(A, B.t(), F32), lambda w: qg.mm_int8_matmul(A, B.t(), sa, sb, dtype=F32, workspace=w)),
                        (qg.mm_orthogonalize_workspace_size(X), lambda w: qg.mm_orthogonalize(X, workspace=w)),
