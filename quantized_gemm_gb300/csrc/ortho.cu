@@ -75,13 +75,11 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs a) {
 #pragma unroll
     for (const T& v : e) q.add(to_f32(v));
   });
-  double v = q.total();
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  q.join_warp();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = q.total();
   __syncthreads();
   if (threadIdx.x == 0) {
-    v = 0.;
+    double v = 0.;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) v += part[w];
     a.part[blockIdx.x] = v;
@@ -90,16 +88,16 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs a) {
 
 // |X|_F + eps from the shares' sums.
 __device__ __forceinline__ Divisor load_divisor(const NormArgs& a, int64_t b) {
-  __shared__ double total;
+  __shared__ Divisor d;
   if (threadIdx.x < 32) {
     double v = 0.;
     for (int c = threadIdx.x; c < a.chunks; c += 32) v += a.part[b * a.chunks + c];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (threadIdx.x == 0) total = sqrt(v) + (double)a.eps;
+    if (threadIdx.x == 0) d = Divisor(sqrt(v) + (double)a.eps);
   }
   __syncthreads();
-  return Divisor(total);
+  return d;
 }
 
 template <typename T, bool VEC>

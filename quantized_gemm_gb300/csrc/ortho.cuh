@@ -22,6 +22,16 @@ struct Squares {
       big = fmaf(y, y, big);
     }
   }
+  // Over a warp, in fp32; the sums then meet in fp64, which one lane of each warp
+  // does (fp64 runs at 1/64 of fp32's rate here).
+  __device__ __forceinline__ void join_warp() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      mid += __shfl_xor_sync(0xffffffffu, mid, o);
+      big += __shfl_xor_sync(0xffffffffu, big, o);
+      small += __shfl_xor_sync(0xffffffffu, small, o);
+    }
+  }
   __device__ __forceinline__ double total() const {
     return (double)mid + (double)big * 1.4615016373309029e+48 + (double)small * 6.8422776578360209e-49;   // 2^160, 2^-160
   }
@@ -32,6 +42,7 @@ struct Squares {
 struct Divisor {
   float m;
   int k;
+  Divisor() = default;
   __device__ __forceinline__ explicit Divisor(double t) {
     m = (float)t;
     k = 0;
