@@ -85,6 +85,7 @@ constexpr int kEpiWarp0 = 2;                     // warps 2.. run the epilogue
 // its 128 rows of A and half (128) of the tile's B columns, 32 KB per stage,
 // 6 stages.
 __host__ __device__ constexpr bool is_split(int mode) { return mode == kSymF || mode == kStateF; }
+__host__ __device__ constexpr bool is_ortho(int mode) { return mode == kSym || mode == kState; }
 
 template <int MODE, bool PAIR>
 struct Geo {
@@ -100,7 +101,7 @@ struct Geo {
   static constexpr int kStageBytes = (kABytes + kBBytes) * (kLoOff ? 2 : 1);
   // kGroupedQ gives one stage's worth of shared memory to its int8 staging ring.
   static constexpr int kStages =
-      kLoOff ? (PAIR ? 3 : 2) : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
+      kLoOff ? (PAIR ? 3 : 2) : is_ortho(MODE) ? (PAIR ? 5 : 3) : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
   static constexpr int kTileRows = PAIR ? 2 * BM : BM;  // output rows per (pair) tile
   static constexpr int kRingBytes = kStages * kStageBytes;
 };
@@ -125,6 +126,7 @@ constexpr int64_t kPairMinK = 1024;              // CTA pairs for K >= this
 constexpr uint32_t kTmemCols = 512;
 constexpr int kCtrlBytes = 256;                  // mbarriers, TMEM slot, abort flag
 constexpr int kStageWords = 32 * 16;             // float per-warp output staging: 32 rows x 64 bytes
+constexpr int kBoxBytes = 32 * 128;              // kSym, kState: a warp's 32 rows x 64 columns, and the rest of them
 
 // Shape of the CTA: 16 epilogue warps of 64 columns each, enough warps to hide
 // the epilogue's latency (short-K float products, the QLinear requantisation).
@@ -134,12 +136,12 @@ constexpr int kStageWords = 32 * 16;             // float per-warp output stagin
 // warps of 128 columns plus 4 converter warps (14 warps: 128 registers).
 template <int MODE, bool PAIR>
 struct Cfg {
-  static constexpr int kEpiWarps = (MODE == kGroupedQ || MODE == kTF32 || is_split(MODE)) ? 8 : 16;
+  static constexpr int kEpiWarps = (MODE == kGroupedQ || MODE == kTF32 || is_split(MODE) || is_ortho(MODE)) ? 8 : 16;
   static constexpr int kConv = (MODE == kGroupedQ || MODE == kTF32) ? kConvWarps : 0;
   static constexpr int kConvWarp0 = kEpiWarp0 + kEpiWarps;
   static constexpr int kThreads = (kEpiWarp0 + kEpiWarps + kConv) * 32;
   static constexpr int kCols = kTileN / (kEpiWarps / 4);      // columns per epilogue warp
-  static constexpr int kWarpWords = MODE == kQLinear ? 3 * kCols : (MODE == kTF32 || MODE == kSkinny) ? 0 : kStageWords;
+  static constexpr int kWarpWords = is_ortho(MODE) ? 2 * kBoxBytes / 4 : MODE == kQLinear ? 3 * kCols : (MODE == kTF32 || MODE == kSkinny) ? 0 : kStageWords;
   static constexpr int kEpiBytes = kEpiWarps * kWarpWords * 4;
   // kGroupedQ staging ring, after the epilogue's slices (1024-byte aligned)
   static constexpr int kQOff = (Geo<MODE, PAIR>::kRingBytes + kCtrlBytes + kEpiBytes + 1023) / 1024 * 1024;
@@ -148,7 +150,7 @@ struct Cfg {
                                1024;
   static_assert(kSmem <= 232448, "shared memory per block");
   static_assert(16 * Geo<MODE, PAIR>::kStages + 48 +
-                        (MODE == kGroupedQ ? 16 * kQStages : MODE == kTF32 ? 8 * Geo<MODE, PAIR>::kStages : 0) <=
+                        (MODE == kGroupedQ ? 16 * kQStages : MODE == kTF32 ? 8 * Geo<MODE, PAIR>::kStages : is_ortho(MODE) ? 64 : 0) <=
                     kSignalOff,
                 "control block");
   static_assert(MODE != kGroupedQ || PAIR, "the fused dequantisation runs on CTA pairs");
@@ -1236,7 +1238,7 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
       if constexpr (MODE == kInt8) {
         if (rok) row_scale = __ldg(static_cast<const float*>(p.sa.ptr) + (ti.m0 + roff + rl) * p.sa.vs);
       }
-      if constexpr (MODE == kDense || MODE == kSkinny || MODE == kInt8 || MODE == kSym || MODE == kState) {
+      if constexpr (MODE == kDense || MODE == kSkinny || MODE == kInt8) {
         if (p.y_tma) {
           // The warp's 32 rows x 64 columns: into registers, release the
           // accumulator, then alpha/beta/C and the rounding to 16 bits.
@@ -1265,10 +1267,7 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(r[h][j]);
-              if (crow) {
-                if constexpr (MODE == kState) add_state32(p, crow, ncol + 32 * h, v);
-                else add_c32(p, crow, ncol + 32 * h, v);
-              }
+              if (crow) add_c32(p, crow, ncol + 32 * h, v);
             }
             if (lane == 0) bulk_wait_read_all();
             __syncwarp();
@@ -1283,45 +1282,6 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
             if (lane == 0 && rbase < rows_t) {
               tma_store_3d(tmY, sbox, (int32_t)(ncol + 32 * h), yrow0, yb);
               bulk_commit();
-            }
-            if constexpr (MODE == kSym) {
-              // The box transposed, where it falls into a tile that is not computed.
-              constexpr int TR = Geo<MODE, PAIR>::kTileRows;
-              const int32_t c0 = (int32_t)(ncol + 32 * h);
-              if (rbase < rows_t && (yrow0 / BN) * BN > (c0 / TR) * TR + TR - 1) {
-                if (lane == 0) bulk_wait_read_all();
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 32; ++j)      // row j of the box takes this lane's column j
-                  sts16(sbox + (uint32_t)j * 64 + ((((uint32_t)lane >> 3) ^ (((uint32_t)j >> 1) & 3u)) << 4) + ((uint32_t)lane & 7u) * 2,
-                        __half_as_ushort(__float2half_rn(v[j])));
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0 && c0 < p.N) {
-                  tma_store_3d(tmY, sbox, yrow0, c0, yb);
-                  bulk_commit();
-                }
-              }
-            }
-            if constexpr (MODE == kState) {
-              // The rest of each value after its f16 rounding, y_lo matrices further.
-              if (p.y_lo != 0) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
-                if (lane == 0) bulk_wait_read_all();
-                __syncwarp();
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  sts128(sbox + (uint32_t)lane * 64 + (((uint32_t)q ^ ((uint32_t)(lane >> 1) & 3u)) << 4),
-                         make_uint4(pack2(v[8 * q], v[8 * q + 1], 1), pack2(v[8 * q + 2], v[8 * q + 3], 1),
-                                    pack2(v[8 * q + 4], v[8 * q + 5], 1), pack2(v[8 * q + 6], v[8 * q + 7], 1)));
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0 && rbase < rows_t) {
-                  tma_store_3d(tmY, sbox, (int32_t)(ncol + 32 * h), yrow0, yb + (int32_t)p.y_lo);
-                  bulk_commit();
-                }
-              }
             }
           }
           continue;
@@ -1381,15 +1341,12 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(r[h][j]);
-            if (crow) {
-              if constexpr (MODE == kState) add_state32(p, crow, n, v);
-              else add_c32(p, crow, n, v);
-            }
+            if (crow) add_c32(p, crow, n, v);
           }
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], p.out_f16);
-          if constexpr (MODE == kInt8 || MODE == kState) {
+          if constexpr (MODE == kInt8) {
             store_block16(stg, lane, w,
                           static_cast<uint16_t*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + (ti.m0 + roff + rbase) * p.y_rs + n,
                           p.y_rs, min(32, rows_t - rbase), (int)min((int64_t)32, p.N - n));
@@ -1423,58 +1380,70 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
 
 // ------------------------------------------------------------------ split epilogue (kSymF, kStateF)
 
-// 32 values per lane (a row's, from column c0 on) to the 32 x 32 box at (row0, c0)
-// of Y's tensor map as f16, with `turn` also transposed to (c0, row0); then the
-// rest of each value as f16 `lo` batches further.
-__device__ __forceinline__ void store_pair_box(const CUtensorMap* tmY, uint32_t sbox, int lane, float (&v)[32],
-                                               int32_t row0, int32_t c0, int32_t batch, int32_t lo, bool turn) {
+// Rows of 32 16-bit values in a warp's slice (64 bytes each, 16-byte pieces XORed by
+// row pair): `slots` of them, written by lanes as rows (put_row) or, one value of
+// each lane a row, as columns (put_column), leave as whole 16-byte pieces, 8 rows a
+// store.  dst: the first row's place; `rows` rows and `pieces` pieces of each are stored.
+__device__ __forceinline__ void put_row(uint32_t* stg, int lane, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint4*>(stg + lane * 16 + ((q ^ ((lane >> 1) & 3)) * 4)) =
+        make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+}
+__device__ __forceinline__ void put_column(uint32_t* stg, int lane, int row, uint16_t v) {
+  reinterpret_cast<uint16_t*>(stg)[row * 32 + (((lane >> 3) ^ ((row >> 1) & 3)) << 3) + (lane & 7)] = v;
+}
+template <int SLOTS>
+__device__ __forceinline__ void store_slots(const uint32_t* stg, int lane, uint16_t* dst, int64_t rs, int rows, int pieces) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < SLOTS / 8; ++i) {
+    const int r = i * 8 + (lane >> 2), q = lane & 3;
+    if (r < rows && q < pieces)
+      *reinterpret_cast<uint4*>(dst + r * rs + 8 * q) =
+          *reinterpret_cast<const uint4*>(stg + r * 16 + ((q ^ ((r >> 1) & 3)) * 4));
+  }
+  __syncwarp();
+}
+
+// A warp's 32 x 32 block of Y (a row per lane, the first row0, from column n on) as
+// f16, with `turn` also transposed, then the rest of each value `lo` elements further.
+__device__ __forceinline__ void store_pair(const TcParams& p, uint32_t* stg, int lane, uint16_t* y, int64_t lo, float (&v)[32],
+                                           int row0, int64_t n, int rows, bool turn) {
+  const int pieces = (int)min((int64_t)4, (p.y_rs - n) / 8), turned = (int)min((int64_t)4, (p.y_rs - row0) / 8);
+  const int cols = (int)min((int64_t)32, p.N - n);
 #pragma unroll 1
-  for (int part = 0; part < 2; ++part) {
-    if (lane == 0) bulk_wait_read_all();
-    __syncwarp();
+  for (int part = 0; part < 2; ++part, y += lo) {
+    uint32_t w[16];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      sts128(sbox + (uint32_t)lane * 64 + (((uint32_t)q ^ ((uint32_t)(lane >> 1) & 3u)) << 4),
-             make_uint4(pack2(v[8 * q], v[8 * q + 1], 1), pack2(v[8 * q + 2], v[8 * q + 3], 1),
-                        pack2(v[8 * q + 4], v[8 * q + 5], 1), pack2(v[8 * q + 6], v[8 * q + 7], 1)));
-    fence_proxy_async_shared();
-    __syncwarp();
-    if (lane == 0) {
-      tma_store_3d(tmY, sbox, c0, row0, batch);
-      bulk_commit();
-    }
+    for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], 1);
+    put_row(stg, lane, w);
+    store_slots<32>(stg, lane, y + row0 * p.y_rs + n, p.y_rs, rows, pieces);
     if (turn) {
-      if (lane == 0) bulk_wait_read_all();
-      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        sts16(sbox + (uint32_t)j * 64 + ((((uint32_t)lane >> 3) ^ (((uint32_t)j >> 1) & 3u)) << 4) + ((uint32_t)lane & 7u) * 2,
-              __half_as_ushort(__float2half_rn(v[j])));
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_3d(tmY, sbox, row0, c0, batch);
-        bulk_commit();
-      }
+      for (int j = 0; j < 32; ++j) put_column(stg, lane, j, (uint16_t)(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]));
+      store_slots<32>(stg, lane, y + n * p.y_rs + row0, p.y_rs, cols, turned);
     }
-    batch += lo;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
+    for (int j = 0; j < 16; ++j) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      v[2 * j] -= f.x;
+      v[2 * j + 1] -= f.y;
+    }
   }
 }
 
 // 8 warps of 128 columns: every segment's accumulator is added to fp32 sums in
 // registers, then alpha, the state or C, and the stores.
 template <int MODE, bool PAIR>
-__device__ void run_split_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t tmem, uint32_t accf0,
-                                   uint32_t acce0, volatile int* abort, uint32_t* stage) {
+__device__ void run_split_epilogue(const TcParams& p, uint32_t tmem, uint32_t accf0, uint32_t acce0,
+                                   volatile int* abort, uint32_t* stage) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kCols = Cfg<MODE, PAIR>::kCols, kChunks = kCols / 32;
   const int quad = warp & 3, slice = (warp - kEpiWarp0) >> 2;
   const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
   const int64_t row_off = PAIR ? (int64_t)rank * BM : 0;
   const uint32_t rel0 = PAIR ? mapa_shared(acce0, 0) : acce0, tlane = (uint32_t)(quad * 32) << 16;
-  const uint32_t sbox = smem_u32(stage);
   const int64_t total = total_tiles<MODE>(p);
   const int nseg = (p.num_kb + p.kb_per_seg - 1) / p.kb_per_seg;
   uint32_t seg = 0;
@@ -1508,7 +1477,7 @@ __device__ void run_split_epilogue(const TcParams& p, const CUtensorMap* tmY, ui
     const int rl = quad * 32 + lane;
     const bool rok = rl < rows_t;
     const int64_t m = ti.m0 + row_off + rl;
-    const int32_t row0 = (int32_t)(ti.m0 + row_off + quad * 32), yb = (int32_t)batch_off(p, p.y_bc, ti.batch);
+    const int32_t row0 = (int32_t)(ti.m0 + row_off + quad * 32);
     const uint16_t* crow =
         p.c && rok ? static_cast<const uint16_t*>(p.c) + batch_off(p, p.c_bstride, ti.batch) + m * p.c_rs : nullptr;
     float* srow = MODE == kStateF && rok ? p.s32 + ti.batch * p.s_step + m * p.s_rs : nullptr;
@@ -1547,13 +1516,177 @@ __device__ void run_split_epilogue(const TcParams& p, const CUtensorMap* tmY, ui
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] *= p.up;
       }
-      if (quad * 32 < rows_t) {
-        // kSymF: also transposed, where that falls into a tile that is not computed (as kSym)
-        constexpr int TR = Geo<MODE, PAIR>::kTileRows;
-        store_pair_box(tmY, sbox, lane, v, row0, (int32_t)n, yb, (int32_t)p.y_lo,
-                       MODE == kSymF && (row0 / BN) * BN > ((int32_t)n / TR) * TR + TR - 1);
-      }
+      // kSymF: also transposed, where that falls into a tile that is not computed.
+      constexpr int TR = Geo<MODE, PAIR>::kTileRows;
+      if (quad * 32 < rows_t)
+        store_pair(p, stage, lane, static_cast<uint16_t*>(p.y) + batch_off(p, p.y_bstride, ti.batch),
+                   p.y_lo * p.y_bstride[0], v, row0, n, min(32, rows_t - quad * 32),
+                   MODE == kSymF && (row0 / BN) * BN > ((int32_t)n / TR) * TR + TR - 1);
     }
+  }
+}
+
+// ------------------------------------------------------------------ epilogue of kSym and kState
+
+// 8 warps of 128 columns.  C (and, for kState, its rest) arrives by TMA as 32 x 64
+// boxes, 128-byte swizzled, in the warp's two slots, the next box while the
+// accumulators of a tile are awaited or the box before is on its way out; the
+// results replace it in place and leave by TMA, a row of a box being 128 bytes.
+// (With 64-byte rows and C read from memory row by row the copy engine and the load
+// pipe held a tile for 16 us: 222 us a step of 32 x 2048 x 1024 instead of 130.)
+template <int MODE, bool PAIR>
+__device__ void run_ortho_epilogue(const TcParams& p, const CUtensorMap* tmC, const CUtensorMap* tmY, uint32_t tmem,
+                                   uint32_t accf0, uint32_t acce0, uint32_t cbar, volatile int* abort, uint32_t* stage) {
+  constexpr int kCols = Cfg<MODE, PAIR>::kCols, TR = Geo<MODE, PAIR>::kTileRows;
+  static_assert(kCols == 128, "two boxes a tile");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = warp & 3, slice = (warp - kEpiWarp0) >> 2;
+  const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
+  const int row_off = PAIR ? (int)rank * BM : 0;
+  const uint32_t rel0 = PAIR ? mapa_shared(acce0, 0) : acce0, tlane = (uint32_t)(quad * 32) << 16;
+  const uint32_t hi = smem_u32(stage), lo = hi + kBoxBytes, mine = (uint32_t)lane * 128;
+  const int64_t total = total_tiles<MODE>(p);
+  const bool has_c = p.c != nullptr;
+  const auto fetch = [&](const Tile& ti, int h) {
+    if (!has_c) return;
+    if (lane == 0) bulk_wait_read_all();                 // the slots' last stores have read them
+    __syncwarp();
+    fence_proxy_async_shared();
+    if (lane == 0) {
+      const int32_t c0 = (int32_t)ti.n0 + slice * kCols + 64 * h, r0 = (int32_t)ti.m0 + row_off + quad * 32;
+      mbar_arrive_expect_tx(cbar, MODE == kState ? 2 * kBoxBytes : kBoxBytes);
+      tma_load_3d(hi, tmC, c0, r0, (int32_t)ti.batch, cbar);
+      if (MODE == kState) tma_load_3d(lo, tmC, c0, r0, (int32_t)(ti.batch + p.c_lo), cbar);
+    }
+  };
+  uint32_t seg = 0, cphase = 0;
+  Tile ti, next;
+  int gh = 0;
+  int64_t t = first_tile<MODE, PAIR>(p);
+  bool have = get_tile<MODE, PAIR>(p, t, total, ti, gh);
+  if (have) fetch(ti, 0);
+  while (have) {
+    t += tile_step<MODE, PAIR>(p);
+    const bool more = get_tile<MODE, PAIR>(p, t, total, next, gh);
+    const uint32_t buf = seg & 1, aph = (seg >> 1) & 1;
+    ++seg;
+    const bool ok = PAIR ? mbar_wait_cluster(accf0 + 8 * buf, aph, abort, p.status, p.timeout_ns)
+                         : mbar_wait(accf0 + 8 * buf, aph, abort, p.status, p.timeout_ns);
+    if (!__all_sync(0xffffffffu, ok)) {
+      if (has_c) mbar_wait_teardown(cbar, cphase, p.teardown_ns);      // the box in flight lands
+      return;
+    }
+    tc_fence_after();
+    const int rows_t = PAIR ? max(0, min(BM, ti.rows - row_off)) : ti.rows;
+    const int32_t row0 = (int32_t)ti.m0 + row_off + quad * 32;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r[2][32];
+      const uint32_t taddr = tmem + tlane + buf * BN + slice * kCols + 64 * h;
+      tmem_ld32(taddr, r[0]);
+      tmem_ld32(taddr + 32, r[1]);
+      tmem_ld_wait();
+      if (h == 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) mbar_arrive_cluster(rel0 + 8 * buf);
+          else mbar_arrive(acce0 + 8 * buf);
+        }
+      }
+      if (has_c) {
+        if (!__all_sync(0xffffffffu, mbar_wait(cbar, cphase, abort, p.status, p.timeout_ns))) {
+          mbar_wait_teardown(cbar, cphase, p.teardown_ns);
+          return;
+        }
+        cphase ^= 1;
+      }
+      // This lane's row: 8 pieces of 8 columns.
+      uint32_t w[32], rest[32];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t at = mine + (((uint32_t)q ^ ((uint32_t)lane & 7u)) << 4);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = p.alpha * __uint_as_float(r[q >> 2][(q & 3) * 8 + e]);
+        if (has_c) {
+          const uint4 a = lds128(hi + at);
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+          float2 c[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[e] = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
+          if constexpr (MODE == kState) {
+            const uint4 b = lds128(lo + at);
+            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&bw[e]));
+              c[e].x += l.x;
+              c[e].y += l.y;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __fmaf_rn(p.beta, c[e].x, v[2 * e]);
+            v[2 * e + 1] = __fmaf_rn(p.beta, c[e].y, v[2 * e + 1]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[4 * q + e] = pack2(v[2 * e], v[2 * e + 1], p.out_f16);
+          if constexpr (MODE == kState) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[4 * q + e]));
+            rest[4 * q + e] = pack2(v[2 * e] - f.x, v[2 * e + 1] - f.y, 1);
+          }
+        }
+      }
+      const int32_t c0 = (int32_t)ti.n0 + slice * kCols + 64 * h;
+      const bool live = quad * 32 < rows_t && c0 < p.N;
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();                                      // every lane has read its row of C
+      if (p.y_tma) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t at = mine + (((uint32_t)q ^ ((uint32_t)lane & 7u)) << 4);
+          sts128(hi + at, make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
+          if (MODE == kState && p.y_lo != 0)
+            sts128(lo + at, make_uint4(rest[4 * q], rest[4 * q + 1], rest[4 * q + 2], rest[4 * q + 3]));
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0 && live) {
+          tma_store_3d(tmY, hi, c0, row0, (int32_t)ti.batch);
+          if (MODE == kState && p.y_lo != 0) tma_store_3d(tmY, lo, c0, row0, (int32_t)(ti.batch + p.y_lo));
+          bulk_commit();
+        }
+      } else if (live) {                                 // the result, in rows that TMA does not take
+        uint16_t* y0 = static_cast<uint16_t*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + (int64_t)row0 * p.y_rs + c0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t half[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) half[e] = w[16 * q + e];
+          if (c0 + 32 * q < p.N)
+            store_block16(stage, lane, half, y0 + 32 * q, p.y_rs, min(32, rows_t - quad * 32),
+                          (int)min((int64_t)32, p.N - c0 - 32 * q));
+        }
+      }
+      if constexpr (MODE == kSym) {
+        // Transposed, where that falls into a tile that is not computed, through the
+        // slot that kState has its rests in.
+        if (live && (row0 / BN) * BN > (c0 / TR) * TR + TR - 1) {
+          uint32_t* turn = stage + kBoxBytes / 4;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) put_column(turn, lane, j, (uint16_t)(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]));
+          store_slots<64>(turn, lane, static_cast<uint16_t*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + c0 * p.y_rs + row0,
+                          p.y_rs, (int)min((int64_t)64, p.N - c0), (int)min((int64_t)4, (p.y_rs - row0) / 8));
+        }
+      }
+      if (h == 0) fetch(ti, 1);
+      else if (more) fetch(next, 0);
+    }
+    ti = next;
+    have = more;
   }
 }
 
@@ -1682,6 +1815,8 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
     }
     if (MODE == kTF32)
       for (int s = 0; s < S; ++s) mbar_init(qfull0 + 8 * s, 1);
+    if (is_ortho(MODE))                       // a barrier for each epilogue warp's boxes of C
+      for (int w = 0; w < Cfg<MODE, PAIR>::kEpiWarps; ++w) mbar_init(cbase + 16 * S + 48 + 8 * w, 1);
     if (MODE == kGroupedQ)
       for (int s = 0; s < kQStages; ++s) {
         mbar_init(qfull0 + 8 * s, 1);
@@ -1715,8 +1850,7 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
   // the previous kernel on the stream is finishing: the set-up above overlaps
   // its tail, and nothing below touches global memory before it completes.
   if (MODE != kSkinny || !p.c_late) pdl_wait();
-  if constexpr (MODE == kDense || MODE == kTF32 || MODE == kInt8 || MODE == kSym || MODE == kState ||
-                is_split(MODE))
+  if constexpr (MODE == kDense || MODE == kTF32 || MODE == kInt8 || is_ortho(MODE) || is_split(MODE))
     pdl_trigger();
   const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
 
@@ -1732,7 +1866,9 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
     uint32_t* stage = reinterpret_cast<uint32_t*>(smem_raw + (sbase - raw) + G::kRingBytes) +
                       (warp - kEpiWarp0) * Cfg<MODE, PAIR>::kWarpWords;
     if constexpr (MODE == kSkinny) run_skinny_partial<MODE, PAIR>(p, tmem, accf0, abort, sbase);
-    else if constexpr (is_split(MODE)) run_split_epilogue<MODE, PAIR>(p, &tmZ, tmem, accf0, acce0, abort, stage);
+    else if constexpr (is_split(MODE)) run_split_epilogue<MODE, PAIR>(p, tmem, accf0, acce0, abort, stage);
+    else if constexpr (is_ortho(MODE))
+      run_ortho_epilogue<MODE, PAIR>(p, &tmS, &tmZ, tmem, accf0, acce0, cbase + 16 * S + 48 + 8 * (warp - kEpiWarp0), abort, stage);
     else run_epilogue<MODE, PAIR>(p, &tmZ, tmem, accf0, acce0, abort, stage);
     // Every tensor store has read its box before the CTA can exit.
     if (p.y_tma && lane == 0) bulk_wait_all();
@@ -1978,7 +2114,7 @@ mm_status launch_kernel(const OperandPlan& a, const OperandPlan& b, const CUtens
                         const TcParams& p_in, int64_t work, cudaStream_t stream) {
   constexpr int kSmem = Cfg<MODE, PAIR>::kSmem, kThreadsM = Cfg<MODE, PAIR>::kThreads;
   TcParams p = p_in;
-  if (MODE != kDense && MODE != kInt8 && MODE != kSym && MODE != kState && !is_split(MODE)) p.y_tma = 0;
+  if (MODE != kDense && MODE != kInt8 && !is_ortho(MODE)) p.y_tma = 0;
   if (cudaFuncSetAttribute(tc_gemm_kernel<MODE, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
       cudaSuccess)
     return MM_ERR_CUDA;
@@ -2322,6 +2458,25 @@ mm_status launch_tc_int8(const Int8Args& q, const void* a, int64_t lda, const vo
 
 // ------------------------------------------------------------------ the orthogonalised update's products
 
+// [count][M][N] 16-bit values, rows ld and matrices `step` apart, in boxes of 32
+// rows and 64 columns, 128-byte swizzled.
+static bool plan_boxes64(const void* ptr, int dtype, int64_t M, int64_t N, int64_t ld, int64_t step, int64_t count,
+                         OperandPlan* out) {
+  auto encode = encode_fn();
+  if (!encode || (reinterpret_cast<uintptr_t>(ptr) & 15) || ld % 8 || (count > 1 && step % 8)) return false;
+  if (M > 0x7fffffffLL || N > 0x7fffffffLL || count > 0x7fffffffLL) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)count};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)((count > 1 ? step : M * ld) * 2)};
+  if (strides[0] >= (1ull << 40) || strides[1] >= (1ull << 40)) return false;
+  const cuuint32_t box[3] = {64u, 32u, 1u}, estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = dtype == MM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  out->mn_major = 0;
+  for (int d = 0; d < kMaxBatchDims; ++d) out->bc[d] = 0;
+  return encode(&out->map, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t stream) {
   if (!status) return MM_ERR_CUDA;
   GemmArgs g;
@@ -2352,17 +2507,10 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
     p.c_lo = o.c_lo;
   }
   p.status = status;
-  OperandPlan ymap;
-  // The rests lie behind all the high parts: the map spans both.
-  GemmArgs ym = g;
-  if (o.y_lo) {
-    ym.bm.shape[0] = ym.bm.count = 2 * o.count;
-    p.y_lo = o.count;
-  }
-  if (!f32_out) plan_output(ym, &p, &ymap);
-  if ((o.sym || o.y_lo) && !p.y_tma) return MM_ERR_UNSUPPORTED;
   const int mode = o.split ? (o.sym ? kSymF : kStateF) : o.sym ? kSym : kState;
+  p.y_lo = o.y_lo ? o.count : 0;
   BatchMap om = g.bm;                          // the operands' maps span the rests too
+  OperandPlan cmap, ymap;
   if (o.split) {
     p.kb_per_seg = kSplitSegment / BK;
     om.shape[0] = om.count = 2 * o.count;
@@ -2370,18 +2518,23 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
     p.s32 = o.s32;
     p.s_rs = o.s_rs; p.s_step = o.s_step;
     p.up = o.up;
+  } else {
+    p.c_lo = o.sym ? 0 : o.count;
+    p.y_tma = plan_boxes64(o.y, o.y_dtype, g.M, g.N, o.y_rs, o.y_step, o.y_lo ? 2 * o.count : o.count, &ymap);
+    if ((o.sym || o.y_lo) && !p.y_tma) return MM_ERR_UNSUPPORTED;
+    if (o.c && !plan_boxes64(o.c, MM_F16, g.M, g.N, o.c_rs, o.c_step, o.sym ? o.count : 2 * o.count, &cmap))
+      return MM_ERR_UNSUPPORTED;
   }
   const int64_t as[kMaxBatchDims] = {o.a_step}, bs[kMaxBatchDims] = {o.b_step};
   for (int attempt = use_pair(g.M, g.K) ? 0 : 1; attempt < 2; ++attempt) {
     const bool pair = attempt == 0;
-    OperandPlan a, b, tail;
+    OperandPlan a, b;
     if (!plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, om, as, BM, &a) ||
         !plan_operand(o.b, MM_F16, g.N, g.K, o.b_cs, o.b_rs, om, bs, pair ? BN / 2 : BN, &b))
       return MM_ERR_UNSUPPORTED;
     p.idesc = make_idesc(1, a.mn_major, b.mn_major, pair);
-    p.pair_tail = pair && !o.split && !a.mn_major && plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, g.bm, as, BM / 2, &tail);
-    if (p.pair_tail) p.idesc_tail = make_idesc_rows(1, 0, b.mn_major, BM);
-    const mm_status st = launch_tc(mode, pair, a, b, p, stream, p.pair_tail ? &tail : nullptr, p.y_tma ? &ymap : nullptr);
+    // C's map takes the place of the tail map: these products have no tail tiles.
+    const mm_status st = launch_tc(mode, pair, a, b, p, stream, !o.split && o.c ? &cmap : &a, p.y_tma ? &ymap : nullptr);
     if (st != MM_ERR_UNSUPPORTED || !pair) return st;
   }
   return MM_ERR_UNSUPPORTED;
