@@ -91,8 +91,10 @@ template <int MODE, bool PAIR>
 struct Geo {
   // kSkinny: 64-row A boxes; the M = 128 MMA's rows 64..127 read the
   // stage's B bytes and are never stored.
-  static constexpr int kTileN = BN;
-  static constexpr int kBRows = PAIR ? BN / 2 : kTileN;  // B columns (rows of B') held by one CTA
+  // Split operands: 128 columns, so that the running sums of an epilogue thread are
+  // 64 (128 of them spilled: three warps share a sub-partition's registers).
+  static constexpr int kTileN = is_split(MODE) ? BN / 2 : BN;
+  static constexpr int kBRows = PAIR ? kTileN / 2 : kTileN;  // B columns (rows of B') held by one CTA
   static constexpr int kABytes = (MODE == kSkinny ? BM / 2 : BM) * BK * 2;   // rows x 128 bytes
   static constexpr int kBBytes = kBRows * BK * 2;
   // kTF32: each stage holds the loaded (then high) parts of A and B followed
@@ -101,7 +103,7 @@ struct Geo {
   static constexpr int kStageBytes = (kABytes + kBBytes) * (kLoOff ? 2 : 1);
   // kGroupedQ gives one stage's worth of shared memory to its int8 staging ring.
   static constexpr int kStages =
-      kLoOff ? (PAIR ? 3 : 2) : is_ortho(MODE) ? (PAIR ? 5 : 3) : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
+      is_split(MODE) ? (PAIR ? 4 : 3) : kLoOff ? (PAIR ? 3 : 2) : is_ortho(MODE) ? (PAIR ? 5 : 3) : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
   static constexpr int kTileRows = PAIR ? 2 * BM : BM;  // output rows per (pair) tile
   static constexpr int kRingBytes = kStages * kStageBytes;
 };
@@ -140,7 +142,7 @@ struct Cfg {
   static constexpr int kConv = (MODE == kGroupedQ || MODE == kTF32) ? kConvWarps : 0;
   static constexpr int kConvWarp0 = kEpiWarp0 + kEpiWarps;
   static constexpr int kThreads = (kEpiWarp0 + kEpiWarps + kConv) * 32;
-  static constexpr int kCols = kTileN / (kEpiWarps / 4);      // columns per epilogue warp
+  static constexpr int kCols = Geo<MODE, PAIR>::kTileN / (kEpiWarps / 4);      // columns per epilogue warp
   static constexpr int kWarpWords = is_ortho(MODE) ? 2 * kBoxBytes / 4 : MODE == kQLinear ? 3 * kCols : (MODE == kTF32 || MODE == kSkinny) ? 0 : kStageWords;
   static constexpr int kEpiBytes = kEpiWarps * kWarpWords * 4;
   // kGroupedQ staging ring, after the epilogue's slices (1024-byte aligned)
@@ -212,19 +214,21 @@ __device__ __forceinline__ bool get_tile(const TcParams& p, int64_t t, int64_t t
   const uint32_t b = fast_div(tt, p.fd_per_batch);
   const uint32_t r = tt - b * p.fd_per_batch.d;
   if (MODE == kSym || MODE == kSymF) {
-    // Row by row of the lower triangle.  256-row tiles: row i has i + 1 tiles;
-    // 128-row tiles: rows 2a and 2a + 1 have a + 1 each (see sym_tiles).
-    constexpr uint32_t kHalf = Geo<MODE, PAIR>::kTileRows == BN ? 1 : 2;   // row tiles per square of 256
-    const uint32_t q = kHalf == 1 ? r : r >> 1;                            // a (a + 1) / 2 tiles (pairs of them) before row a
+    // Row by row of the lower triangle (see sym_tiles): where a tile is as wide as it
+    // is high, row i has i + 1 tiles; half as wide, 2 (i + 1); twice as wide, rows 2i
+    // and 2i + 1 have i + 1 each.
+    constexpr uint32_t TR = Geo<MODE, PAIR>::kTileRows, TN = Geo<MODE, PAIR>::kTileN;
+    constexpr uint32_t kHigh = TN > TR ? TN / TR : 1, kWide = TR > TN ? TR / TN : 1;
+    const uint32_t q = r / (kHigh * kWide);              // of the squares of max(TR, TN)
     uint32_t i = (uint32_t)((sqrtf(8.f * (float)q + 1.f) - 1.f) * 0.5f);
     while ((i + 1) * (i + 2) / 2 <= q) ++i;
     while (i * (i + 1) / 2 > q) --i;
-    uint32_t w = r - kHalf * (i * (i + 1) / 2), mtile = i * kHalf;
-    if (w > i) { w -= i + 1; ++mtile; }
+    uint32_t w = r - kHigh * kWide * (i * (i + 1) / 2), mtile = i * kHigh;
+    if (kHigh > 1 && w > i) { w -= i + 1; ++mtile; }
     ti.batch = b;
     ti.g = 0;
     ti.m0 = (int64_t)mtile * Geo<MODE, PAIR>::kTileRows;
-    ti.n0 = (int64_t)w * BN;
+    ti.n0 = (int64_t)w * TN;
     ti.a_row = (int32_t)ti.m0;
     ti.a_b = (int32_t)batch_off(p, p.a_bc, b);
     ti.b_b = (int32_t)batch_off(p, p.b_bc, b);
@@ -1433,7 +1437,7 @@ __device__ __forceinline__ void store_pair(const TcParams& p, uint32_t* stg, int
   }
 }
 
-// 8 warps of 128 columns: every segment's accumulator is added to fp32 sums in
+// 8 warps of 64 columns: every segment's accumulator is added to fp32 sums in
 // registers, then alpha, the state or C, and the stores.
 template <int MODE, bool PAIR>
 __device__ void run_split_epilogue(const TcParams& p, uint32_t tmem, uint32_t accf0, uint32_t acce0,
@@ -1517,11 +1521,11 @@ __device__ void run_split_epilogue(const TcParams& p, uint32_t tmem, uint32_t ac
         for (int j = 0; j < 32; ++j) v[j] *= p.up;
       }
       // kSymF: also transposed, where that falls into a tile that is not computed.
-      constexpr int TR = Geo<MODE, PAIR>::kTileRows;
+      constexpr int TR = Geo<MODE, PAIR>::kTileRows, TN = Geo<MODE, PAIR>::kTileN;
       if (quad * 32 < rows_t)
         store_pair(p, stage, lane, static_cast<uint16_t*>(p.y) + batch_off(p, p.y_bstride, ti.batch),
                    p.y_lo * p.y_bstride[0], v, row0, n, min(32, rows_t - quad * 32),
-                   MODE == kSymF && (row0 / BN) * BN > ((int32_t)n / TR) * TR + TR - 1);
+                   MODE == kSymF && (row0 / TN) * TN > ((int32_t)n / TR) * TR + TR - 1);
     }
   }
 }
@@ -2163,10 +2167,11 @@ mm_status launch_kernel(const OperandPlan& a, const OperandPlan& b, const CUtens
                                                                                                       : MM_ERR_CUDA;
 }
 
-// Tiles of mt row tiles (256 rows in a pair, 128 else) that touch the lower
-// triangle of a symmetric product with 256-column tiles.
-int64_t sym_tiles(int64_t mt, bool pair) {
-  if (pair) return mt * (mt + 1) / 2;
+// Tiles of a symmetric product that touch its lower triangle, of mt row tiles (256
+// rows in a pair, 128 else); columns: 256, or 128 for split operands.
+int64_t sym_tiles(int64_t mt, bool pair, int cols) {
+  const int rows = pair ? 2 * BM : BM;
+  if (cols <= rows) return rows / cols * (mt * (mt + 1) / 2);
   const int64_t a = mt / 2;
   return a * (a + 1) + (mt & 1 ? a + 1 : 0);
 }
@@ -2183,10 +2188,10 @@ mm_status launch_tc(int mode, bool pair, const OperandPlan& a, const OperandPlan
   int64_t work = 0;
   if (!is_grouped(mode)) {
     const int64_t rows = pair ? 2 * BM : BM;
-    const int64_t cols = BN;
+    const int64_t cols = is_split(mode) ? BN / 2 : BN;
     p.mt = (p.M + rows - 1) / rows;
     p.nt = (p.N + cols - 1) / cols;
-    const int64_t per_matrix = mode == kSym || mode == kSymF ? sym_tiles(p.mt, pair) : p.mt * p.nt;
+    const int64_t per_matrix = mode == kSym || mode == kSymF ? sym_tiles(p.mt, pair, (int)cols) : p.mt * p.nt;
     p.tiles = per_matrix * p.bm.count;
     if (p.tiles >= (1ll << 31) || p.mt * p.nt >= (1ll << 31)) return MM_ERR_UNSUPPORTED;
     const uint32_t per_batch = (uint32_t)per_matrix;
@@ -2530,9 +2535,9 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
     const bool pair = attempt == 0;
     OperandPlan a, b;
     if (!plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, om, as, BM, &a) ||
-        !plan_operand(o.b, MM_F16, g.N, g.K, o.b_cs, o.b_rs, om, bs, pair ? BN / 2 : BN, &b))
+        !plan_operand(o.b, MM_F16, g.N, g.K, o.b_cs, o.b_rs, om, bs, (o.split ? BN / 2 : BN) / (pair ? 2 : 1), &b))
       return MM_ERR_UNSUPPORTED;
-    p.idesc = make_idesc(1, a.mn_major, b.mn_major, pair);
+    p.idesc = make_idesc_mn(1, a.mn_major, b.mn_major, pair ? 2 * BM : BM, o.split ? BN / 2 : BN);
     // C's map takes the place of the tail map: these products have no tail tiles.
     const mm_status st = launch_tc(mode, pair, a, b, p, stream, !o.split && o.c ? &cmap : &a, p.y_tma ? &ymap : nullptr);
     if (st != MM_ERR_UNSUPPORTED || !pair) return st;
