@@ -72,8 +72,11 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs a) {
   __shared__ double part[kThreads / 32];
   Squares q;
   walk<T, VEC>(a, [&](int64_t, uint32_t, int64_t, const auto& e) {
+    constexpr int E = sizeof(e) / sizeof(T);
+    float v[E];
 #pragma unroll
-    for (const T& v : e) q.add(to_f32(v));
+    for (int j = 0; j < E; ++j) v[j] = to_f32(e[j]);
+    q.add(v);
   });
   q.join_warp();
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = q.total();
@@ -170,7 +173,13 @@ mm_status run_norm(const OrthoArgs& o, NormArgs a, cudaStream_t stream) {
   constexpr int E = 16 / (int)sizeof(T);
   bool vec = o.x.cs == 1 && o.N % E == 0 && (o.x.rs % E == 0 || o.M == 1) && (reinterpret_cast<uintptr_t>(o.x.ptr) & 15) == 0;
   for (int d = 0; d < o.bm.nb; ++d) vec = vec && (o.x.bstride[d] % E == 0 || o.bm.shape[d] == 1);
-  a.fd_row = make_fastdiv((uint32_t)(vec ? o.N / E : o.N));
+  // Rows that follow one another without a gap, here and in the copy, are one row.
+  if (vec && a.ld == o.N && (o.x.rs == o.N || o.M == 1) && o.M * o.N < (1ll << 31)) {
+    a.N = o.M * o.N;
+    a.ld = a.N;
+    a.M = 1;
+  }
+  a.fd_row = make_fastdiv((uint32_t)(vec ? a.N / E : a.N));
   const int64_t blocks = o.bm.count * a.chunks;
   if (blocks >= (1ll << 31)) return MM_ERR_UNSUPPORTED;
   const dim3 g((unsigned)blocks), t(kThreads);

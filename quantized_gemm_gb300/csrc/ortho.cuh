@@ -22,6 +22,25 @@ struct Squares {
       big = fmaf(y, y, big);
     }
   }
+  // A group of values: where the largest lies in [2^-30, 2^50) all squares add up as
+  // they are (one below 2^-60 is lost, which is nothing beside the largest's).
+  template <int E>
+  __device__ __forceinline__ void add(const float (&x)[E]) {
+    float top = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      top = fmaxf(top, fabsf(x[j]));
+      nan |= x[j] != x[j];
+    }
+    if (top < 1.1258999e+15f && top >= 9.3132257e-10f && !nan) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) mid = fmaf(x[j], x[j], mid);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) add(x[j]);
+    }
+  }
   // Over a warp, in fp32; the sums then meet in fp64, which one lane of each warp
   // does (fp64 runs at 1/64 of fp32's rate here).
   __device__ __forceinline__ void join_warp() {
@@ -37,10 +56,11 @@ struct Squares {
   }
 };
 
-// d = |X|_F + eps as m 2^k: fp32 division where it is in fp32's middle range (k =
-// 0), m in [1, 2) otherwise.
+// d = |X|_F + eps as m 2^k: a product with the rounded 1 / d where that is in
+// fp32's middle range (k = 0; its rounding scales the whole matrix by 1 + 2^-24 at
+// most), a division by m in [1, 2) otherwise.
 struct Divisor {
-  float m;
+  float m, r;
   int k;
   Divisor() = default;
   __device__ __forceinline__ explicit Divisor(double t) {
@@ -51,9 +71,12 @@ struct Divisor {
       m = (float)(2. * f);
       --k;
     }
+    r = __frcp_rn(m);
+    if (k == 0 && !(r < 3e38f && r > 1e-37f)) k = kAlways;      // a zero, infinite or NaN divisor divides
   }
+  static constexpr int kAlways = 1 << 20;
   __device__ __forceinline__ float divide(float x) const {
-    return k == 0 ? __fdiv_rn(x, m) : __fdiv_rn(scalbnf(x, -k), m);
+    return k == 0 ? x * r : __fdiv_rn(k == kAlways ? x : scalbnf(x, -k), m);
   }
 };
 

@@ -1858,11 +1858,13 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
     pdl_trigger();
   const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
 
+  // (elect_one: fewer cycles an instruction, and the compiler's to know.)
+  constexpr bool kElect = is_ortho(MODE) || is_split(MODE) || MODE == kInt8;
   if (warp == 0) {
-    if (lane == 0)
+    if (kElect ? elect_one() : lane == 0)
       run_producer<MODE, PAIR>(&tmA, &tmB, &tmS, &tmZ, p, sbase, full0, empty0, qbase, qfull0, qempty0, abort);
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (kElect ? elect_one() : lane == 0) {
       if (rank == 0) run_mma<MODE, PAIR>(p, sbase, tmem, full0, empty0, accf0, acce0, drain, abort);
       else mbar_wait_teardown(drain, 0, p.teardown_ns);   // the leader's last commit reaches this CTA too
     }
