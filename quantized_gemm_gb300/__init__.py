@@ -55,6 +55,14 @@ class MMTensor(ctypes.Structure):
                 ("shape", ctypes.c_int64 * MM_MAX_DIMS), ("strides", ctypes.c_int64 * MM_MAX_DIMS)]
 
 
+class _Descriptor:
+    """Argument type of a descriptor: its packed bytes as they are (see _packed), a pointer to an MMTensor, or None."""
+
+    @classmethod
+    def from_param(cls, d):
+        return d if d is None or isinstance(d, bytes) else ctypes.POINTER(MMTensor).from_param(d)
+
+
 class MMError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -75,6 +83,7 @@ def _lib():
         lib = ctypes.CDLL(path)
         P, I32, I64, F, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
         T = ctypes.POINTER(MMTensor)
+        D = _Descriptor                # an MMTensor's bytes, or a pointer to one
         sigs = {
             "mm_status_string": ([I32], ctypes.c_char_p),
             "mm_version": ([], ctypes.c_char_p),
@@ -103,14 +112,14 @@ def _lib():
             "mm_lowrank_matmul_workspace_size": ([T, T, T, T, ctypes.POINTER(SZ)], I32),
             "mm_lowrank_matmul": ([T, T, T, T, T, T, T, P, SZ, P], I32),
             "mm_lowrank_matmul_grad_workspace_size": ([T, T, T, T, ctypes.POINTER(SZ)], I32),
-            "mm_route_balance_workspace_size": ([T, T, ctypes.POINTER(SZ)], I32),
-            "mm_route_balance": ([T, T, T, T, T, P, SZ, P], I32),
-            "mm_route_balance_grad": ([T, T, T, T, T, P], I32),
-            "mm_quantize_rows": ([T, T, T, P], I32),
-            "mm_int8_matmul_workspace_size": ([T, T, I32, ctypes.POINTER(SZ)], I32),
-            "mm_int8_matmul": ([T, T, T, T, T, T, P, SZ, P], I32),
-            "mm_orthogonalize_workspace_size": ([T, ctypes.POINTER(SZ)], I32),
-            "mm_orthogonalize": ([T, I32, ctypes.POINTER(F), F, F, T, P, SZ, P], I32),
+            "mm_route_balance_workspace_size": ([D, D, ctypes.POINTER(SZ)], I32),
+            "mm_route_balance": ([D, D, D, D, D, P, SZ, P], I32),
+            "mm_route_balance_grad": ([D, D, D, D, D, P], I32),
+            "mm_quantize_rows": ([D, D, D, P], I32),
+            "mm_int8_matmul_workspace_size": ([D, D, I32, ctypes.POINTER(SZ)], I32),
+            "mm_int8_matmul": ([D, D, D, D, D, D, P, SZ, P], I32),
+            "mm_orthogonalize_workspace_size": ([D, ctypes.POINTER(SZ)], I32),
+            "mm_orthogonalize": ([D, I32, ctypes.POINTER(F), F, F, D, P, SZ, P], I32),
             "mm_lowrank_matmul_grad": ([T, T, T, T, T, T, T, T, T, T, P, SZ, P], I32),
         }
         for name, (args, res) in sigs.items():
@@ -142,6 +151,19 @@ def _desc(t):
     if nd > MM_MAX_DIMS:
         raise ValueError("at most %d dimensions" % MM_MAX_DIMS)
     return _TENSOR_OF(_PACK[nd](t.data_ptr() if t.numel() > 0 else 0, dt, nd, *t.shape, *t.stride()))
+
+
+def _packed(t):
+    """The same as bytes, which ctypes passes on without building a structure."""
+    if t is None:
+        return None
+    nd = t.dim()
+    if nd > MM_MAX_DIMS:
+        raise ValueError("at most %d dimensions" % MM_MAX_DIMS)
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError("unsupported dtype %s" % t.dtype)
+    return _PACK[nd](t.data_ptr(), dt, nd, *t.shape, *t.stride())
 
 
 def _desc4(t, kind):
@@ -176,6 +198,13 @@ def _stream(t, stream):
             return ctypes.c_void_p(_RAW_STREAM(t.get_device()))
         stream = torch.cuda.current_stream(t.device)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _handle(t, stream):
+    """The stream's handle as a number."""
+    if stream is None and _RAW_STREAM is not None and t.is_cuda:
+        return _RAW_STREAM(t.get_device())
+    return _stream(t, stream).value
 
 
 def _empty(shape, dtype, like, stream):
@@ -418,7 +447,23 @@ def mm_route_topk_grad(logits, indices, grad_weights, normalize=1, out=None, str
 
 
 def mm_route_balance_workspace_size(logits, indices):
-    return _sized(_lib().mm_route_balance_workspace_size, _desc(logits), _desc(indices))
+    return _room(_lib().mm_route_balance_workspace_size, _packed(logits), _packed(indices))
+
+
+def _room(fn, *args):
+    """Bytes of workspace that ``fn`` names."""
+    nbytes = ctypes.c_size_t()
+    _check(fn(*args, ctypes.byref(nbytes)), fn.__name__)
+    return nbytes.value
+
+
+def _work(workspace, like, stream, fn, *args):
+    """(tensor, address, size) of the workspace: the caller's (the library checks its size), or one of the size ``fn``
+    names; the tensor keeps the memory until the call has been made."""
+    if workspace is None:
+        workspace, nbytes = _workspace(_room(fn, *args), like, stream)
+        return workspace, None if workspace is None else workspace.data_ptr(), nbytes
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def mm_route_balance(logits, indices, loss=None, counts=None, mean_probs=None, stream=None, workspace=None):
@@ -427,16 +472,16 @@ def mm_route_balance(logits, indices, loss=None, counts=None, mean_probs=None, s
     alone is padding)."""
     lib = _LIB or _lib()
     G = logits.shape[1]
-    dl, di = _desc(logits), _desc(indices)
+    dl, di = _packed(logits), _packed(indices)
     if loss is None:
         loss = _empty((1,), torch.float32, logits, stream)
     if counts is None:
         counts = _empty((G + 1,), torch.int32, logits, stream)
     if mean_probs is None:
         mean_probs = _empty((G,), torch.float32, logits, stream)
-    ws, wsb = _given_or_sized(workspace, logits, stream, lib.mm_route_balance_workspace_size, dl, di)
-    status = lib.mm_route_balance(_ref(dl), _ref(di), _ref(_desc(loss)), _ref(_desc(counts)), _ref(_desc(mean_probs)),
-                                  None if ws is None else ws.data_ptr(), wsb, _stream(logits, stream))
+    ws, at, nbytes = _work(workspace, logits, stream, lib.mm_route_balance_workspace_size, dl, di)
+    status = lib.mm_route_balance(dl, di, _packed(loss), _packed(counts), _packed(mean_probs), at, nbytes,
+                                  _handle(logits, stream))
     if status:
         raise MMError(status, "mm_route_balance")
     return loss, counts, mean_probs
@@ -447,8 +492,8 @@ def mm_route_balance_grad(logits, counts, grad_loss, base=None, out=None, stream
     plus ``base``, another gradient of the logits."""
     lib = _LIB or _lib()
     y = _empty(logits.shape, logits.dtype, logits, stream) if out is None else out
-    status = lib.mm_route_balance_grad(_ref(_desc(logits)), _ref(_desc(counts)), _ref(_desc(grad_loss)),
-                                       _ref(_desc(base)), _ref(_desc(y)), _stream(logits, stream))
+    status = lib.mm_route_balance_grad(_packed(logits), _packed(counts), _packed(grad_loss), _packed(base), _packed(y),
+                                       _handle(logits, stream))
     if status:
         raise MMError(status, "mm_route_balance_grad")
     return y
@@ -543,13 +588,13 @@ def mm_quantize_rows(x, out=None, scales=None, stream=None):
     q = _empty(x.shape, torch.int8, x, stream) if out is None else out
     if scales is None:
         scales = _empty(x.shape[:1], torch.float32, x, stream)
-    status = lib.mm_quantize_rows(_ref(_desc(x)), _ref(_desc(q)), _ref(_desc(scales)), _stream(x, stream))
+    status = lib.mm_quantize_rows(_packed(x), _packed(q), _packed(scales), _handle(x, stream))
     if status:
         raise MMError(status, "mm_quantize_rows")
     return q, scales
 
 
-def _float_type(dtype):
+def _type_of(dtype):
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise TypeError("unsupported dtype %s" % dtype)
@@ -557,35 +602,25 @@ def _float_type(dtype):
 
 
 def mm_int8_matmul_workspace_size(A, B, dtype=torch.bfloat16):
-    nbytes = ctypes.c_size_t()
-    _check(_lib().mm_int8_matmul_workspace_size(_ref(_desc(A)), _ref(_desc(B)), _float_type(dtype), ctypes.byref(nbytes)),
-           "mm_int8_matmul_workspace_size")
-    return nbytes.value
+    return _room(_lib().mm_int8_matmul_workspace_size, _packed(A), _packed(B), _type_of(dtype))
 
 
 def mm_int8_matmul(A, B, a_scale, b_scale, bias=None, dtype=torch.bfloat16, out=None, stream=None, workspace=None):
     """Product of int8 tensors scaled per row of A and per column of B: Y[m, n] = sum_k A[m, k] B[k, n] * a_scale[m] *
     b_scale[n] + bias[n], in ``dtype`` (or the type of ``out``).  Weights quantised as [N, K] rows are passed transposed."""
     lib = _LIB or _lib()
-    dA, dB = _desc(A), _desc(B)
+    dA, dB = _packed(A), _packed(B)
     y = _empty((A.shape[0], B.shape[1]), dtype, A, stream) if out is None else out
-    dY = _desc(y)
-    if workspace is None:
-        nbytes = ctypes.c_size_t()
-        _check(lib.mm_int8_matmul_workspace_size(_ref(dA), _ref(dB), dY.dtype, ctypes.byref(nbytes)),
-               "mm_int8_matmul_workspace_size")
-        ws, wsb = _workspace(nbytes.value, A, stream)
-    else:
-        ws, wsb = workspace, workspace.numel() * workspace.element_size()
-    status = lib.mm_int8_matmul(_ref(dA), _ref(dB), _ref(_desc(a_scale)), _ref(_desc(b_scale)), _ref(_desc(bias)),
-                                _ref(dY), None if ws is None else ws.data_ptr(), wsb, _stream(A, stream))
+    ws, at, nbytes = _work(workspace, A, stream, lib.mm_int8_matmul_workspace_size, dA, dB, _type_of(y.dtype))
+    status = lib.mm_int8_matmul(dA, dB, _packed(a_scale), _packed(b_scale), _packed(bias), _packed(y), at, nbytes,
+                                _handle(A, stream))
     if status:
         raise MMError(status, "mm_int8_matmul")
     return y
 
 
 def mm_orthogonalize_workspace_size(X):
-    return _sized(_lib().mm_orthogonalize_workspace_size, _desc(X))
+    return _room(_lib().mm_orthogonalize_workspace_size, _packed(X))
 
 
 def mm_orthogonalize(X, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=1.0, out=None, stream=None,
@@ -601,13 +636,13 @@ def mm_orthogonalize(X, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-
         flat = [v for step in coefficients for v in step]
     else:
         flat = list(coefficients) * steps
-    if len(flat) != 3 * steps:
+    if len(flat) != 3 * max(0, steps):
         raise ValueError("three coefficients a step")
-    dX = _desc(X)
+    dX = _packed(X)
     y = _empty(X.shape, X.dtype, X, stream) if out is None else out
-    ws, wsb = _given_or_sized(workspace, X, stream, lib.mm_orthogonalize_workspace_size, dX)
-    status = lib.mm_orthogonalize(_ref(dX), steps, (ctypes.c_float * max(1, len(flat)))(*flat), eps, scale,
-                                  _ref(_desc(y)), None if ws is None else ws.data_ptr(), wsb, _stream(X, stream))
+    ws, at, nbytes = _work(workspace, X, stream, lib.mm_orthogonalize_workspace_size, dX)
+    status = lib.mm_orthogonalize(dX, steps, (ctypes.c_float * max(1, len(flat)))(*flat), eps, scale, _packed(y), at,
+                                  nbytes, _handle(X, stream))
     if status:
         raise MMError(status, "mm_orthogonalize")
     return y

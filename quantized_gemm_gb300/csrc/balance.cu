@@ -14,12 +14,15 @@
 // q * LPR + i), so that a warp reads 32 / LPR rows at once, each in whole
 // sectors, and a sum over a row takes log2(LPR) shuffles for all of them.  A lane
 // keeps the same columns for every row, so the column sums (forward) and the
-// shares c / C (gradient) stay in its registers.  With 65536 rows of 256 bf16
-// logits a row over all 32 lanes, with a branch per logit, took 30 us forward and
-// 59 us backward (276 instructions a row); see the kernels for today's.  Column
-// sums leave a block through shared memory, one partial per block, and a second
-// launch, one cluster, adds the partials in a fixed order; picks are integers,
-// counted with shared-memory atomics, whose order does not matter.
+// shares c / C (gradient) stay in its registers.  Each lane copies the pieces of
+// rows to come into its own places in shared memory (cp.async, kAhead rows).  65536
+// rows of 256 bf16 logits, forward and backward (101 MB, 15 us of memory): 95 us with
+// a row over all 32 lanes and a branch per logit (276 instructions a row), 43 with
+// two rows loaded into registers at a time, 40 so; what is left is the arithmetic
+// (107 instructions a row forward) and three launches.  Column sums leave a block
+// through shared memory, one partial per block, and a second launch, one cluster,
+// adds the partials in a fixed order; picks are integers, counted with shared-memory
+// atomics, whose order does not matter.
 #include <type_traits>
 
 #include "kernels.h"
@@ -190,35 +193,77 @@ __device__ __forceinline__ float softmax_row(const Row<T, LPR, NP>& r, float2 (&
   return s > 0.f ? __fdividef(1.f, s) : 0.f;           // 1 <= s <= G
 }
 
-// Rows in flight per lane group, by the columns a lane holds.
-template <typename T, int NP> constexpr int kFlight = NP * Pairs<T>::kElems >= 32 ? 1 : NP * Pairs<T>::kElems >= 16 ? 2 : 4;
+// A lane's queue of row pieces: kAhead rows are on their way while one is worked on.
+// ASYNC (rows of whole aligned pieces): through the lane's own places in shared
+// memory; otherwise each row is loaded when its turn comes.
+template <int NP> constexpr int kAhead = NP <= 2 ? 6 : NP <= 4 ? 3 : 2;     // 48 to 64 KB a block
+template <typename T, int LPR, int NP, bool ASYNC>
+struct Queue {
+  const T* base;
+  int64_t rs, cs, rows;
+  int lane, G;
+  float fill;
+  uint32_t place;                                // this lane's first place
+  static constexpr int kBytes = kThreads * NP * 16 * kAhead<NP>;     // of a block
+  __device__ __forceinline__ Queue(const void* p, int64_t rs_, int64_t cs_, int64_t rows_, int lane_, int G_, float fill_, uint8_t* sm)
+      : base(static_cast<const T*>(p)), rs(rs_), cs(cs_), rows(rows_), lane(lane_), G(G_), fill(fill_),
+        place(ptx::smem_u32(sm) + threadIdx.x * 16) {}
+  __device__ __forceinline__ uint32_t at(int slot, int q) const { return place + (uint32_t)((slot * NP + q) * kThreads * 16); }
+  __device__ __forceinline__ void issue(int64_t r, int slot) const {
+    if (ASYNC) {
+      if (r < rows) {
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+          const int c0 = (q * LPR + lane) * Pairs<T>::kElems;
+          if (c0 < G)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(slot, q)), "l"(base + r * rs + c0) : "memory");
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void take(int64_t r, int slot, Row<T, LPR, NP>& row) const {
+    if (ASYNC) {
+#pragma unroll
+      for (int q = 0; q < NP; ++q) {
+        const int c0 = (q * LPR + lane) * Pairs<T>::kElems;
+        T e[Pairs<T>::kElems];
+#pragma unroll
+        for (int j = 0; j < Pairs<T>::kElems; ++j) e[j] = from_f32<T>(fill);
+        row.u[q] = c0 < G && r < rows ? ptx::lds128(at(slot, q)) : *reinterpret_cast<const uint4*>(e);
+      }
+    } else {
+      row.load(base + (r < rows ? r : 0) * rs, cs, lane, G, false, fill);
+    }
+  }
+};
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int NP>
+__device__ __forceinline__ void async_wait_oldest() { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead<NP> - 1) : "memory"); }
 
 // Partials of a block: psum [G] f32, then picks [G] i32, then rows that take
 // part and picks in all.
-template <typename T, int LPR, int NP>
-__global__ void __launch_bounds__(kThreads, 2) balance_partial_kernel(const BalanceArgs a, const int vec, float* psum,
-                                                                      int32_t* cnt, unsigned* status) {
+template <typename T, int LPR, int NP, bool ASYNC>
+__global__ void __launch_bounds__(kThreads, 2) balance_partial_kernel(const BalanceArgs a, float* psum, int32_t* cnt,
+                                                                      unsigned* status) {
   pdl_wait();
-  extern __shared__ float sh[];                                // [kWarps][G] column sums, then [G + 2] counts
+  extern __shared__ __align__(16) uint8_t raw[];               // the queue, then [kWarps][G] column sums, [G + 2] counts
+  using Q = Queue<T, LPR, NP, ASYNC>;
+  float* sh = reinterpret_cast<float*>(raw + (ASYNC ? Q::kBytes : 0));
   int32_t* hist = reinterpret_cast<int32_t*>(sh + kWarps * a.G);
-  constexpr int E = Pairs<T>::kElems, H = E / 2, R = kFlight<T, NP>;
+  constexpr int E = Pairs<T>::kElems, H = E / 2;
   const int G = (int)a.G, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < G + 2; i += kThreads) hist[i] = 0;
   __syncthreads();
   constexpr int kPerWarp = 32 / LPR;
   const int sub = lane / LPR, l = lane % LPR;
-  const T* logits = static_cast<const T*>(a.logits);
   const int64_t step = (int64_t)gridDim.x * kWarps * kPerWarp;
-  int64_t r0 = ((int64_t)blockIdx.x * kWarps + warp) * kPerWarp;
-  Row<T, LPR, NP> row[R];
-  const auto load = [&]() {
+  int64_t r = ((int64_t)blockIdx.x * kWarps + warp) * kPerWarp + sub;
+  const Q queue(a.logits, a.l_rs, a.l_cs, a.rows, l, G, -INFINITY, raw);
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const int64_t r = r0 + q * step + sub;
-      row[q].load(logits + (r < a.rows ? r : 0) * a.l_rs, a.l_cs, l, G, vec, -INFINITY);
-    }
-  };
-  if (r0 < a.rows) load();                                     // the first rows arrive while the picks are counted
+  for (int k = 0; k < kAhead<NP>; ++k) {                           // the first rows arrive while the picks are counted
+    queue.issue(r + k * step, k);
+    async_commit();
+  }
   int mine = 0;
   bool bad = false;
   const int64_t picks = a.rows * a.k;
@@ -241,21 +286,23 @@ __global__ void __launch_bounds__(kThreads, 2) balance_partial_kernel(const Bala
 #pragma unroll
     for (int j = 0; j < H; ++j) acc[q][j] = twice(0.f);
   int alive = 0;
-  while (r0 < a.rows) {
+  int slot = 0;
+  for (; r - sub < a.rows; r += step) {
+    Row<T, LPR, NP> row;
+    async_wait_oldest<NP>();
+    queue.take(r, slot, row);
+    float2 e[NP][H];
+    const bool live = r < a.rows;
+    const float inv = softmax_row<T, LPR, NP>(row, e);
+    const float2 w = twice(live ? inv : 0.f);
+    alive += live && inv > 0.f && l == 0;
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      float2 e[NP][H];
-      const bool live = r0 + q * step + sub < a.rows;
-      const float inv = softmax_row<T, LPR, NP>(row[q], e);
-      const float2 w = twice(live ? inv : 0.f);
-      alive += live && inv > 0.f && l == 0;
+    for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int p = 0; p < NP; ++p)
-#pragma unroll
-        for (int j = 0; j < H; ++j) acc[p][j] = ptx::fma2_rn(e[p][j], w, acc[p][j]);
-    }
-    r0 += step * R;
-    if (r0 < a.rows) load();
+      for (int j = 0; j < H; ++j) acc[p][j] = ptx::fma2_rn(e[p][j], w, acc[p][j]);
+    queue.issue(r + kAhead<NP> * step, slot);                      // the place has been read
+    async_commit();
+    if (++slot == kAhead<NP>) slot = 0;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -368,29 +415,26 @@ __global__ void __launch_bounds__(1024) __cluster_dims__(kFinalBlocks, 1, 1)
   ptx::cluster_sync();       // no block leaves before its part has been read
 }
 
-template <typename T, int LPR, int NP, bool BASE>
-__global__ void __launch_bounds__(kThreads, 2) balance_grad_kernel(const BalanceGradArgs a, const int vec, const int bvec,
-                                                                   const int ovec) {
+template <typename T, int LPR, int NP, bool BASE, bool ASYNC>
+__global__ void __launch_bounds__(kThreads, 2) balance_grad_kernel(const BalanceGradArgs a, const int ovec) {
   pdl_begin();
-  constexpr int E = Pairs<T>::kElems, H = E / 2, R = kFlight<T, NP>;
+  extern __shared__ __align__(16) uint8_t raw[];               // the queues
+  constexpr int E = Pairs<T>::kElems, H = E / 2;
   constexpr int kPerWarp = 32 / LPR;
   const int G = (int)a.G, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / LPR, l = lane % LPR;
-  const T* logits = static_cast<const T*>(a.logits);
-  const T* base = static_cast<const T*>(a.base);
   T* out = static_cast<T*>(a.out);
   const int64_t step = (int64_t)gridDim.x * kWarps * kPerWarp;
-  int64_t r0 = ((int64_t)blockIdx.x * kWarps + warp) * kPerWarp;
-  Row<T, LPR, NP> row[R], add[R];
-  const auto load = [&]() {
+  int64_t r = ((int64_t)blockIdx.x * kWarps + warp) * kPerWarp + sub;
+  using Q = Queue<T, LPR, NP, ASYNC>;
+  const Q queue(a.logits, a.l_rs, a.l_cs, a.rows, l, G, -INFINITY, raw);
+  const Q add(a.base, a.b_rs, a.b_cs, a.rows, l, G, 0.f, raw + (ASYNC ? Q::kBytes : 0));
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const int64_t r = r0 + q * step + sub, rr = r < a.rows ? r : 0;
-      row[q].load(logits + rr * a.l_rs, a.l_cs, l, G, vec, -INFINITY);
-      if (BASE) add[q].load(base + rr * a.b_rs, a.b_cs, l, G, bvec, 0.f);
-    }
-  };
-  if (r0 < a.rows) load();
+  for (int k = 0; k < kAhead<NP>; ++k) {
+    queue.issue(r + k * step, k);
+    if (BASE) add.issue(r + k * step, k);
+    async_commit();
+  }
   // The shares c / C of this lane's columns; a row's lanes hold all of them.
   float2 share[NP][H];
   int total = 0;
@@ -412,44 +456,47 @@ __global__ void __launch_bounds__(kThreads, 2) balance_grad_kernel(const Balance
 #pragma unroll
     for (int j = 0; j < H; ++j) share[p][j] = mul2(share[p][j], twice(scale));
   const float coef = rows_in > 0 ? __ldg(a.dloss) * ((float)G / (float)rows_in) : 0.f;
-  while (r0 < a.rows) {
+  int slot = 0;
+  for (; r - sub < a.rows; r += step) {
+    Row<T, LPR, NP> row, other;
+    async_wait_oldest<NP>();
+    queue.take(r, slot, row);
+    if (BASE) add.take(r, slot, other);
+    float2 e[NP][H];
+    const float inv = softmax_row<T, LPR, NP>(row, e);
+    float2 dots = twice(0.f);
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const int64_t r = r0 + q * step + sub;
-      float2 e[NP][H];
-      const float inv = softmax_row<T, LPR, NP>(row[q], e);
-      float2 dots = twice(0.f);
+    for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int p = 0; p < NP; ++p)
+      for (int j = 0; j < H; ++j) dots = ptx::fma2_rn(share[p][j], e[p][j], dots);
+    const float dot = lanes_sum<LPR>(dots.x + dots.y) * inv;
+    const float2 w = twice(inv * coef), nd = twice(-dot);
+    T* dst = out + r * (int64_t)G;
 #pragma unroll
-        for (int j = 0; j < H; ++j) dots = ptx::fma2_rn(share[p][j], e[p][j], dots);
-      const float dot = lanes_sum<LPR>(dots.x + dots.y) * inv;
-      const float2 w = twice(inv * coef), nd = twice(-dot);
-      T* dst = out + r * (int64_t)G;
+    for (int p = 0; p < NP; ++p) {
+      float2 v[H];
+      if (BASE) Pairs<T>::split(other.u[p], v);
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        float2 v[H];
-        if (BASE) Pairs<T>::split(add[q].u[p], v);
+      for (int j = 0; j < H; ++j) {
+        const float2 k = mul2(e[p][j], w), d = add2(share[p][j], nd);
+        v[j] = BASE ? ptx::fma2_rn(k, d, v[j]) : mul2(k, d);
+      }
+      const uint4 o = Pairs<T>::join(v);
+      const int c0 = (p * LPR + l) * E;
+      if (r < a.rows) {
+        if (ovec && c0 + E <= G) {
+          *reinterpret_cast<uint4*>(dst + c0) = o;
+        } else {
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
-          const float2 k = mul2(e[p][j], w), d = add2(share[p][j], nd);
-          v[j] = BASE ? ptx::fma2_rn(k, d, v[j]) : mul2(k, d);
-        }
-        const uint4 o = Pairs<T>::join(v);
-        const int c0 = (p * LPR + l) * E;
-        if (r < a.rows) {
-          if (ovec && c0 + E <= G) {
-            *reinterpret_cast<uint4*>(dst + c0) = o;
-          } else {
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-              if (c0 + j < G) dst[c0 + j] = reinterpret_cast<const T*>(&o)[j];
-          }
+          for (int j = 0; j < E; ++j)
+            if (c0 + j < G) dst[c0 + j] = reinterpret_cast<const T*>(&o)[j];
         }
       }
     }
-    r0 += step * R;
-    if (r0 < a.rows) load();
+    queue.issue(r + kAhead<NP> * step, slot);                      // the places have been read
+    if (BASE) add.issue(r + kAhead<NP> * step, slot);
+    async_commit();
+    if (++slot == kAhead<NP>) slot = 0;
   }
 }
 
@@ -481,33 +528,45 @@ int64_t row_blocks(int64_t rows, int rows_per_block, int per_sm) {
   return want < 1 ? 1 : want < most ? want : most;
 }
 
-constexpr int kPartialPerSm = 2, kGradPerSm = 4;
+constexpr int kPartialPerSm = 2, kGradPerSm = 2;
+
+template <typename T, typename K, typename... A>
+mm_status launch_queued(K kernel, int64_t blocks, size_t smem, cudaStream_t stream, A... args) {
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return MM_ERR_CUDA;
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), smem, stream, args...) == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+}
 
 template <typename T>
 mm_status run_partial(const BalanceArgs& a, void* ws, unsigned* status, cudaStream_t stream) {
   const int64_t nb = balance_partial_blocks(a.rows);
   float* psum = static_cast<float*>(ws);
   int32_t* cnt = reinterpret_cast<int32_t*>(psum + nb * a.G);
-  const size_t smem = (size_t)(kWarps * a.G + a.G + 2) * 4;
+  const size_t sums = (size_t)(kWarps * a.G + a.G + 2) * 4;
+  const bool async = vec_ok<T>(a.logits, a.l_rs, a.l_cs) && a.G % Pairs<T>::kElems == 0;
   return by_width<T>(a.G, [&](auto lpr, auto v) {
-    return launch_pdl(balance_partial_kernel<T, decltype(lpr)::value, decltype(v)::value>, dim3((unsigned)nb), dim3(kThreads), smem, stream, a,
-                      vec_ok<T>(a.logits, a.l_rs, a.l_cs), psum, cnt, status) == cudaSuccess
-               ? MM_OK
-               : MM_ERR_CUDA;
+    constexpr int L = decltype(lpr)::value, P = decltype(v)::value;
+    return async ? launch_queued<T>(balance_partial_kernel<T, L, P, true>, nb, sums + Queue<T, L, P, true>::kBytes, stream, a,
+                                    psum, cnt, status)
+                 : launch_queued<T>(balance_partial_kernel<T, L, P, false>, nb, sums, stream, a, psum, cnt, status);
   });
 }
 
 template <typename T>
 mm_status run_grad(const BalanceGradArgs& a, cudaStream_t stream) {
+  const int ov = vec_ok<T>(a.out, a.G, 1);
+  const bool async = vec_ok<T>(a.logits, a.l_rs, a.l_cs) && a.G % Pairs<T>::kElems == 0 &&
+                     (!a.base || vec_ok<T>(a.base, a.b_rs, a.b_cs));
   return by_width<T>(a.G, [&](auto lpr, auto v) {
     constexpr int L = decltype(lpr)::value, P = decltype(v)::value;
-    const dim3 grid((unsigned)row_blocks(a.rows, kWarps * (32 / L), kGradPerSm));
-    const int lv = vec_ok<T>(a.logits, a.l_rs, a.l_cs), ov = vec_ok<T>(a.out, a.G, 1);
-    const cudaError_t e =
-        a.base ? launch_pdl(balance_grad_kernel<T, L, P, true>, grid, dim3(kThreads), 0, stream, a, lv,
-                            vec_ok<T>(a.base, a.b_rs, a.b_cs), ov)
-               : launch_pdl(balance_grad_kernel<T, L, P, false>, grid, dim3(kThreads), 0, stream, a, lv, 0, ov);
-    return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+    const int64_t nb = row_blocks(a.rows, kWarps * (32 / L), kGradPerSm);
+    const size_t q = async ? Queue<T, L, P, true>::kBytes : 0;
+    if (a.base)
+      return async ? launch_queued<T>(balance_grad_kernel<T, L, P, true, true>, nb, 2 * q, stream, a, ov)
+                   : launch_queued<T>(balance_grad_kernel<T, L, P, true, false>, nb, 0, stream, a, ov);
+    return async ? launch_queued<T>(balance_grad_kernel<T, L, P, false, true>, nb, q, stream, a, ov)
+                 : launch_queued<T>(balance_grad_kernel<T, L, P, false, false>, nb, 0, stream, a, ov);
   });
 }
 
