@@ -927,19 +927,21 @@ def run_profile_workload(args):
         step = lambda: qg.mm_grouped_matmul(d["input"], d["weights"], d["group_indices"], d["bias"], out=yo,
                                             workspace=ws)
     elif name.startswith("operator_"):
-        # operator_moe_one_token: that case of perf/operators.py; a _gN suffix: N
+        # operator_moe_one_token: that case of perf/operators.py or of perf/more_operators.py; a _gN suffix: N
         # experts or adapters (a smaller case of the same kernels, for captures of
         # more than the duration)
         sys.path.insert(0, os.path.join(ROOT, "perf"))
+        import more_operators
         import operators
-        operators.own = True
         case, _, groups = name[len("operator_"):].partition("_g")
         case, groups = (case, groups) if groups.isdigit() else (name[len("operator_"):], "")
-        found = [c for c in operators.listed() if c["name"] == case]
+        found = [(m, c) for m in (operators, more_operators) for c in m.listed() if c["name"] == case]
         if not found:
             raise SystemExit("unknown workload " + name)
-        state = operators.prepare(dict(found[0], **({"G": int(groups)} if groups else {})), 1)
-        step = lambda: operators.run(state)
+        module, found = found[0]
+        module.own = True
+        state = module.prepare(dict(found, **({"G": int(groups)} if groups else {})), 1)
+        step = lambda: module.run(state)
     else:
         raise SystemExit("unknown workload " + name)
     stream = torch.cuda.current_stream(dev)
@@ -960,7 +962,8 @@ def main():
                     help="run only this workload (gemm_bf16, matmul_f32, gemm_f64_simt, gemm_i32_simt, "
                          "gemm_bf16_skinny_mR[_tensor], matmul_bf16_bcast[_bN], qlinear_s8 or a "
                          "QLinear variant, "
-                         "grouped_bf16[_gG][_nN], operator_CASE[_gG] for a case of perf/operators.py)")
+                         "grouped_bf16[_gG][_nN], operator_CASE[_gG] for a case of perf/operators.py or "
+                         "perf/more_operators.py)")
     args = ap.parse_args()
     if args.warmup < 3:
         args.warmup = 3

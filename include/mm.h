@@ -34,7 +34,8 @@
  *   with programmatic stream serialization: it may be scheduled while the
  *   previous kernel on the stream is finishing, and waits for that kernel to
  *   complete (and its memory to be visible) before its first global-memory
- *   access, so stream order is kept for any work before or after a call.
+ *   access (a call's later kernels may read its inputs once its first kernel has
+ *   waited), so stream order is kept for any work before or after a call.
  * Memory.  The library never allocates device memory.  Operators whose fast
  *   path needs scratch space (QLinearMatMul, GroupedMatMul, the balance loss, the
  *   mixture-of-experts layer, the low-rank adapters, the 8-bit product and the
@@ -335,9 +336,10 @@ mm_status mm_route_balance(const mm_tensor* logits, const mm_tensor* indices, co
 /* The loss's gradient with respect to the logits (the counts are constants):
  *   dl[t,j] = grad_loss (G / T') p[t,j] (c[j] / C - sum_g (c[g] / C) p[t,g]) + base[t,j]
  * counts [G+1] MM_I32 as mm_route_balance leaves them (or their sums over several
- * ranks), grad_loss one MM_F32 on the device, base [T,G] another gradient of the
+ * ranks, all picks below 2^31), grad_loss one MM_F32 on the device, base [T,G] another gradient of the
  * logits (NULL = 0) in their type, such as mm_route_topk_grad's; the sum is
- * rounded once to that type.  A logit that takes no part gets base alone. */
+ * rounded once to that type.  A logit that takes no part gets base alone where
+ * grad_loss is finite, and NaN where it is not. */
 mm_status mm_route_balance_grad(const mm_tensor* logits, const mm_tensor* counts, const mm_tensor* grad_loss,
                                 const mm_tensor* base /* NULL = 0 */, const mm_tensor* grad_logits, void* stream);
 
@@ -431,8 +433,9 @@ mm_status mm_quantize_rows(const mm_tensor* x, const mm_tensor* q, const mm_tens
  * each step rounded in fp32, then once to T.  A [M,K] and B [K,N] MM_I8 with any
  * strides, a_scale [M] and b_scale [N] MM_F32, bias NULL or [N] of type T, Y
  * dense [M,N], T one of bf16, f16, f32.  acc is the exact integer while the
- * partial sums stay below 2^24 in magnitude (any K up to 1024), and an fp32 sum of exact products
- * where they do not.  K = 0 gives the bias.
+ * partial sums stay below 2^24 in magnitude (any K up to 1024).  Where they do not
+ * it is a sum of exact products in fp32 whose additions may truncate: off by at most
+ * (K / 16 + 1) 2^-23 sum_k |A[m,k] B[k,n]|.  K = 0 gives the bias.
  * The fastest layout has B's columns contiguous along k and 16-byte aligned (a
  * transposed [N,K] tensor, K a multiple of 16), rows of A likewise.
  * Workspace: mm_int8_matmul_workspace_size() bytes for an output of out_dtype. */
@@ -451,7 +454,10 @@ mm_status mm_int8_matmul(const mm_tensor* A, const mm_tensor* B, const mm_tensor
  * the call returns.  0 <= steps <= MM_ORTHO_MAX_STEPS, eps >= 0, all finite (else
  * MM_ERR_INVALID_ARG).  A matrix of zeros gives zeros for eps > 0 and NaN for eps =
  * 0; one that holds an infinity or NaN gives NaN, and touches no other.
- * The norm covers fp32's whole range.  X_i is held in fp32 between the steps.
+ * The norm covers fp32's whole range.  Between the steps X_i is fp32, or 22 bits in
+ * two f16 values where a stack of 16-bit matrices runs on the tensor cores; there
+ * the operands of the products are f16 values for 16-bit types (11 bits, scaled so
+ * that none leaves the type's range) and pairs of them, 22 bits, for f32.
  * Workspace: mm_orthogonalize_workspace_size() bytes. */
 #define MM_ORTHO_MAX_STEPS 64
 mm_status mm_orthogonalize_workspace_size(const mm_tensor* X, size_t* bytes);

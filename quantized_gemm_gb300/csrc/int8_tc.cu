@@ -455,9 +455,9 @@ mm_status launch_typed(const StreamArgs& p, int nt, const CUtensorMap& x, cudaSt
 
 }  // namespace
 
-// B's columns contiguous along k, 16-byte aligned.
+// B's columns contiguous along k, 16-byte aligned, none inside another (others are copied).
 bool int8_stream_supported(const Int8Args& q) {
-  return q.K >= 1 && q.b_ks == 1 && (q.N == 1 || (q.b_ns % 16 == 0 && q.b_ns > 0)) &&
+  return q.K >= 1 && q.b_ks == 1 && (q.N == 1 || (q.b_ns % 16 == 0 && q.b_ns >= q.K)) &&
          (reinterpret_cast<uintptr_t>(q.b) & 15) == 0;
 }
 

@@ -184,8 +184,13 @@ mm_status launch_int8_few(const Int8Args& args, cudaStream_t stream);
 mm_status launch_int8_any(const Int8Args& args, cudaStream_t stream);
 mm_status launch_int8_copies(const Int8Copy& A, const Int8Copy& B, cudaStream_t stream);
 
-// The norm, the division and the chain of products; or, up to kOrthoSmallWork =
-// m m n matrices (m the smaller side) that fit a cluster's shared memory, one launch.
+// The norm, the division and the chain of products; or one launch, for matrices that
+// fit a cluster's shared memory: stacks of up to kOrthoSmallWork = m m n matrices (m
+// the smaller side), and any of m <= 32, of which a tile of the chain would use an
+// eighth at most.  us in one launch and in the chain, f32 and bf16:
+//   64 x 1000        63 286   65 147      32 of 64 x 512   62 230   65 136
+//   128 x 1000      184 378  190 188      8 of 128 x 512  135 291  140 159
+//   64 x 4000       167 512  180 211      200 of 32 x 32   25 199   26 155
 constexpr double kOrthoSmallWork = 1.5e8;
 size_t ortho_workspace_bytes(const OrthoArgs& args);
 mm_status launch_ortho(const OrthoArgs& args, void* workspace, cudaStream_t stream);

@@ -308,9 +308,10 @@ mm_status run_float(const OrthoArgs& o, void* ws, cudaStream_t st) {
   }
   if (s != MM_OK) return s;
   const float* X = reinterpret_cast<float*>(w + p.s[cur]);
-  return o.dtype == MM_F32    ? run_round<float>(o, X, p.ld, st)
-         : o.dtype == MM_BF16 ? run_round<__nv_bfloat16>(o, X, p.ld, st)
-                              : run_round<__half>(o, X, p.ld, st);
+  s = o.dtype == MM_F32    ? run_round<float>(o, X, p.ld, st)
+      : o.dtype == MM_BF16 ? run_round<__nv_bfloat16>(o, X, p.ld, st)
+                           : run_round<__half>(o, X, p.ld, st);
+  return o.steps == 0 ? finish(s, MM_PATH_SIMT) : s;     // (the products have said theirs)
 }
 
 // ------------------------------------------------------------------ the chain on the tensor cores
@@ -334,10 +335,9 @@ mm_status run_float(const OrthoArgs& o, void* ws, cudaStream_t st) {
 // their additions truncate, 3 K / 8 times a sum; see kSymF.)
 
 double power_below(double x) {
-  if (!(x > 0.)) return 1.;
-  int e = (int)std::floor(std::log2(x));
-  e = e < -60 ? -60 : e > 30 ? 30 : e;
-  return std::ldexp(1., e);
+  if (x > 0x1p30) return 0x1p30;         // infinite where the array is zeros
+  if (!(x > 0x1p-60)) return 0x1p-60;    // (the bounds are then out of range)
+  return std::ldexp(1., (int)std::floor(std::log2(x)));
 }
 // The largest |f| of f(s) = s (a + b s^2 + c s^4) on [0, u], and of b l + c l^2 on [0, u^2].
 double odd_bound(double a, double b, double c, double u) {

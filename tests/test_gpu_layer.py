@@ -136,6 +136,14 @@ def test_int8_strided_views(path):
     _check_int8(A[:45], B[:200].t(), sa[::2], sb[::2], bias[1::2], F32)
 
 
+def test_int8_columns_that_overlap(path):
+    """Weights whose columns lie 16 bytes apart and are 64 long: windows over one array."""
+    A, B, sa, sb, bias = _int8_inputs(300, 64, 264, BF16, 12)
+    windows = B.reshape(-1).as_strided((64, 264), (1, 16))
+    for M in (5, 40, 300):
+        _check_int8(A[:M], windows, sa[:M], sb, bias, BF16)
+
+
 def test_int8_rows_depend_on_themselves_alone(path):
     """A row of NaN scale (quantised from an infinity) is NaN, and the others are what they were."""
     A, B, sa, sb, bias = _int8_inputs(70, 256, 264, BF16, 21)
@@ -370,6 +378,35 @@ def test_orthogonalize_other_coefficients(dtype):
     _check_ortho(X, 1, (0.0, 0.0, 0.0))
     _check_ortho(X, 2, (10.0, -20.0, 15.0))
     _check_ortho(X, 8, (1.5, -0.5, 0.0))
+    L = rand_tensor((300, 520), dtype, 10, DEV)          # the chain of products
+    for coefficients, steps in (((0.0, 0.0, 0.0), 2), ((2.0, 0.0, 0.0), 2), ((0.0, 1.0, 0.0), 1), ((1.5, -0.5, 0.0), 6), (MUON, 0)):
+        _check_ortho(L, steps, coefficients, scale=-0.5)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_orthogonalize_more_matrices_than_a_grid_axis_holds(dtype):
+    X = rand_tensor((66000, 40, 48), dtype, 13, DEV)
+    for which in (qg.MM_PATH_AUTO, qg.MM_PATH_SIMT, qg.MM_PATH_TENSOR):
+        qg.mm_set_path_policy(which)
+        try:
+            Y = qg.mm_orthogonalize(X)
+        finally:
+            qg.mm_set_path_policy(qg.MM_PATH_AUTO)
+        for i in (0, 65535, 65536, 65999):
+            want = layer.orthogonalize(to_np(X[i]), [MUON] * 5, 1e-7)
+            bound = layer.orthogonalize_bound(to_np(X[i]), [MUON] * 5, 1e-7, 1.0, _operand(dtype), U[dtype])
+            assert np.linalg.norm(to_np(Y[i]) - want) <= bound
+
+
+def test_orthogonalize_many_tiny_matrices():
+    X = rand_tensor((3000, 6, 7), BF16, 12, DEV)
+    Y = qg.mm_orthogonalize(X)
+    assert qg.mm_last_path() == qg.MM_PATH_SIMT
+    pick = [0, 1, 1499, 2999]
+    for i in pick:
+        want = layer.orthogonalize(to_np(X[i]), [MUON] * 5, 1e-7)
+        bound = layer.orthogonalize_bound(to_np(X[i]), [MUON] * 5, 1e-7, 1.0, U[F32], U[BF16])
+        assert np.linalg.norm(to_np(Y[i]) - want) <= bound
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -521,7 +558,99 @@ def test_given_workspaces_and_outputs():
     assert qg.mm_orthogonalize(X, out=out) is out and torch.equal(out, qg.mm_orthogonalize(X))
 
 
+# ------------------------------------------------------------------ offsets past 32 bits
+
+
+def test_large_quantisation_and_product():
+    """2.2e9 values in, 2.2e9 products out; the last rows against the oracle."""
+    x = torch.zeros((17000, 131072), dtype=BF16, device=DEV)
+    x[-3:] = rand_tensor((3, 131072), BF16, 5, DEV)
+    q, s = qg.mm_quantize_rows(x)
+    wq, ws = layer.quantize_rows(to_np(x[-3:]))
+    np.testing.assert_array_equal(q[-3:].cpu().numpy(), wq)
+    np.testing.assert_array_equal(s[-3:].cpu().numpy(), ws)
+    assert not q[:-3].any()
+    del x
+    # the long array as weights of 17000 channels, and as tokens
+    A, B = q[-300:, :64].contiguous(), q[:, :64]
+    sa = torch.ones(300, device=DEV)
+    for M in (3, 40, 300):
+        Y = qg.mm_int8_matmul(A[-M:], B.t(), sa[-M:], s)
+        want = A[-M:].double() @ B[-3:].double().t() * s[-3:].double()
+        assert float((Y[:, -3:].double() - want).abs().max()) <= U[BF16] * 1.01 * float(want.abs().max()) + 1e-12
+    C = torch.randint(-128, 128, (131072, 64), dtype=torch.int8, device=DEV)
+    Y = qg.mm_int8_matmul(q[:, :64], C.t(), s, torch.ones(131072, device=DEV))
+    want = q[-3:, :64].double() @ C.double().t() * s[-3:, None].double()
+    assert float(((Y[-3:].double() - want).abs() - U[BF16] * 1.01 * want.abs()).max()) <= 1e-12
+    assert not Y[:-3].any()
+
+
+def test_large_balance():
+    T, G = 2200000, 1024
+    l = torch.zeros((T, G), dtype=BF16, device=DEV)
+    l[-1] = rand_tensor((G,), BF16, 6, DEV)
+    idx = (torch.arange(T, device=DEV, dtype=torch.int32) % G)[:, None].contiguous()
+    loss, counts, mean = qg.mm_route_balance(l, idx)
+    assert torch.equal(counts[:G].long(), torch.bincount(idx[:, 0].long(), minlength=G)) and int(counts[G]) == T
+    # each block adds T / 304 equal terms in fp32 to a lane's sum, off by half an ulp each
+    assert float((mean * G - 1).abs().max()) < T / 304 * 2.0 ** -24 + 1e-5 and abs(float(loss) - 1) < 1e-3
+    g = qg.mm_route_balance_grad(l, counts, torch.full((1,), float(T), device=DEV), base=l)
+    p, share = torch.softmax(l[-1].double(), 0), counts[:G].double() / T
+    want = G * p * (share - (p * share).sum()) + l[-1].double()
+    assert float((g[-1].double() - want).abs().max()) < U[BF16] * float(want.abs().max()) + 1e-3 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_large_stack(dtype):
+    X = torch.zeros((9000, 240, 1024), dtype=dtype, device=DEV)
+    X[-1] = rand_tensor((240, 1024), dtype, 7, DEV)
+    Y = qg.mm_orthogonalize(X)
+    want = layer.orthogonalize(to_np(X[-1]), [MUON] * 5, 1e-7)
+    bound = layer.orthogonalize_bound(to_np(X[-1]), [MUON] * 5, 1e-7, 1.0, _operand(dtype), U[dtype])
+    assert np.linalg.norm(to_np(Y[-1]) - want) <= bound
+    assert not Y[:-1].any()
+
+
 # ------------------------------------------------------------------ together
+
+
+def test_the_example_trains_and_serves():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, root)
+    from examples import train_and_serve
+    block = train_and_serve.ExpertLayer(hidden=128, ffn=136, experts=6, picks=2)
+    x = rand_tensor((40, 128), F32, 111, DEV)
+    logits, idx, weights = block.route(x)
+    assert np.array_equal(to_np(idx), select.route_topk(to_np(logits), 2, 1)[0])
+    dw = rand_tensor((40, 2), F32, 112, DEV) / 40
+    loss, counts, dlogits = block.router_gradient(logits, idx, dw, balance=0.05)
+    l64 = to_np(logits)
+    want = select.route_topk_grad(l64, to_np(idx), to_np(dw)) + layer.route_balance_grad(l64, to_np(counts), 0.05)
+    assert abs(float(loss) - layer.route_balance(l64, to_np(idx))[0]) < 1e-5
+    assert_within(dlogits, want, 1e-5 * np.abs(want) + 1e-8, "router gradient")
+    # against a difference of the two losses' sum
+    def total(l):
+        _, w = select.route_topk(l, 2, 1)
+        return (w * to_np(dw)).sum() + 0.05 * layer.route_balance(l, to_np(idx))[0]
+    for t, j in ((0, 1), (7, 3), (39, 5)):
+        d = np.zeros_like(l64)
+        d[t, j] = 1e-5
+        assert abs((total(l64 + d) - total(l64 - d)) / 2e-5 - want[t, j]) < 1e-6
+    before = block.experts.clone()
+    block.update(x, dlogits, rand_tensor(block.experts.shape, BF16, 113, DEV), rate=0.02)
+    assert not torch.equal(before, block.experts) and torch.isfinite(block.experts.float()).all()
+    served = block.serve()
+    y = served(x.to(BF16), 3)
+    q, s = layer.quantize_rows(to_np(x.to(BF16)))
+    wq, ws = layer.quantize_rows(to_np(block.experts[3]).T)
+    want = layer.int8_matmul(q, wq.T, s.astype(np.float64), ws.astype(np.float64))
+    assert_within(y, want, layer.int8_matmul_bound(q, wq.T, s.astype(np.float64), ws.astype(np.float64), u=U[BF16]), "served")
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "train_and_serve.py"), "--steps", "2"],
+                       capture_output=True, text=True)
+    assert r.returncode == 0 and "us a step" in r.stdout, r.stderr
 
 
 def test_a_training_step_and_its_8_bit_layer():
