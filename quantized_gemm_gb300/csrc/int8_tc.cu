@@ -19,6 +19,9 @@
 // partial sums meet in a fixed order through distributed shared memory, a token's
 // channels in neighbouring lanes, and the epilogue scales and stores them in
 // rows.  Bound: memory (one byte per weight) up to about 100 tokens, then the MMAs.
+// 61 tokens by 4096 x 14336 (59 MB): 17.7 us with the tokens' copy; what is left
+// above the stream's 9 are that launch, the hand-over of the first tiles and the
+// split's last sums.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -86,6 +86,7 @@ constexpr int kEpiWarp0 = 2;                     // warps 2.. run the epilogue
 // 6 stages.
 __host__ __device__ constexpr bool is_split(int mode) { return mode == kSymF || mode == kStateF; }
 __host__ __device__ constexpr bool is_ortho(int mode) { return mode == kSym || mode == kState; }
+__host__ __device__ constexpr bool has_boxes(int mode) { return is_ortho(mode) || is_split(mode); }
 
 template <int MODE, bool PAIR>
 struct Geo {
@@ -103,7 +104,7 @@ struct Geo {
   static constexpr int kStageBytes = (kABytes + kBBytes) * (kLoOff ? 2 : 1);
   // kGroupedQ gives one stage's worth of shared memory to its int8 staging ring.
   static constexpr int kStages =
-      is_split(MODE) ? (PAIR ? 4 : 3) : kLoOff ? (PAIR ? 3 : 2) : is_ortho(MODE) ? (PAIR ? 5 : 3) : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
+      is_split(MODE) ? (PAIR ? 3 : 2) : kLoOff ? (PAIR ? 3 : 2) : is_ortho(MODE) ? (PAIR ? 5 : 3) : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
   static constexpr int kTileRows = PAIR ? 2 * BM : BM;  // output rows per (pair) tile
   static constexpr int kRingBytes = kStages * kStageBytes;
 };
@@ -143,7 +144,7 @@ struct Cfg {
   static constexpr int kConvWarp0 = kEpiWarp0 + kEpiWarps;
   static constexpr int kThreads = (kEpiWarp0 + kEpiWarps + kConv) * 32;
   static constexpr int kCols = Geo<MODE, PAIR>::kTileN / (kEpiWarps / 4);      // columns per epilogue warp
-  static constexpr int kWarpWords = is_ortho(MODE) ? 2 * kBoxBytes / 4 : MODE == kQLinear ? 3 * kCols : (MODE == kTF32 || MODE == kSkinny) ? 0 : kStageWords;
+  static constexpr int kWarpWords = has_boxes(MODE) ? 2 * kBoxBytes / 4 : MODE == kQLinear ? 3 * kCols : (MODE == kTF32 || MODE == kSkinny) ? 0 : kStageWords;
   static constexpr int kEpiBytes = kEpiWarps * kWarpWords * 4;
   // kGroupedQ staging ring, after the epilogue's slices (1024-byte aligned)
   static constexpr int kQOff = (Geo<MODE, PAIR>::kRingBytes + kCtrlBytes + kEpiBytes + 1023) / 1024 * 1024;
@@ -152,7 +153,7 @@ struct Cfg {
                                1024;
   static_assert(kSmem <= 232448, "shared memory per block");
   static_assert(16 * Geo<MODE, PAIR>::kStages + 48 +
-                        (MODE == kGroupedQ ? 16 * kQStages : MODE == kTF32 ? 8 * Geo<MODE, PAIR>::kStages : is_ortho(MODE) ? 64 : 0) <=
+                        (MODE == kGroupedQ ? 16 * kQStages : MODE == kTF32 ? 8 * Geo<MODE, PAIR>::kStages : has_boxes(MODE) ? 64 : 0) <=
                     kSignalOff,
                 "control block");
   static_assert(MODE != kGroupedQ || PAIR, "the fused dequantisation runs on CTA pairs");
@@ -598,24 +599,6 @@ __device__ __forceinline__ void add_c32(const TcParams& p, const uint16_t* crow,
 #pragma unroll
     for (int j = 0; j < 32; ++j)
       if (n + j < p.N) v[j] = __fmaf_rn(p.beta, unpack16(crow[(n + j) * p.c_cs], p.out_f16), v[j]);
-  }
-}
-
-// v[j] += beta * (C[n + j] + the rest of it), kState: f16 rows of whole 16-byte
-// pieces (values past N are read from the rows' padding and not stored).
-__device__ __forceinline__ void add_state32(const TcParams& p, const uint16_t* crow, int64_t n, float (&v)[32]) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (n + 8 * q >= p.c_rs) break;
-    const uint4 hi = __ldg(reinterpret_cast<const uint4*>(crow + n) + q), lo = __ldg(reinterpret_cast<const uint4*>(crow + p.c_lo + n) + q);
-    const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hw[e]));
-      const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&lw[e]));
-      v[q * 8 + 2 * e] = __fmaf_rn(p.beta, h.x + l.x, v[q * 8 + 2 * e]);
-      v[q * 8 + 2 * e + 1] = __fmaf_rn(p.beta, h.y + l.y, v[q * 8 + 2 * e + 1]);
-    }
   }
 }
 
@@ -1384,16 +1367,10 @@ __device__ void run_epilogue(const TcParams& p, const CUtensorMap* tmY, uint32_t
 
 // ------------------------------------------------------------------ split epilogue (kSymF, kStateF)
 
-// Rows of 32 16-bit values in a warp's slice (64 bytes each, 16-byte pieces XORed by
-// row pair): `slots` of them, written by lanes as rows (put_row) or, one value of
-// each lane a row, as columns (put_column), leave as whole 16-byte pieces, 8 rows a
-// store.  dst: the first row's place; `rows` rows and `pieces` pieces of each are stored.
-__device__ __forceinline__ void put_row(uint32_t* stg, int lane, const uint32_t (&w)[16]) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    *reinterpret_cast<uint4*>(stg + lane * 16 + ((q ^ ((lane >> 1) & 3)) * 4)) =
-        make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-}
+// Rows of 32 16-bit values in a warp's slice (64 bytes each, 16-byte pieces XORED by
+// row pair): `slots` of them, written by lanes as columns (one value of each lane a
+// row), leave as whole 16-byte pieces, 8 rows a store.  dst: the first row's place;
+// `rows` rows and `pieces` pieces of each are stored.
 __device__ __forceinline__ void put_column(uint32_t* stg, int lane, int row, uint16_t v) {
   reinterpret_cast<uint16_t*>(stg)[row * 32 + (((lane >> 3) ^ ((row >> 1) & 3)) << 3) + (lane & 7)] = v;
 }
@@ -1410,65 +1387,67 @@ __device__ __forceinline__ void store_slots(const uint32_t* stg, int lane, uint1
   __syncwarp();
 }
 
-// A warp's 32 x 32 block of Y (a row per lane, the first row0, from column n on) as
-// f16, with `turn` also transposed, then the rest of each value `lo` elements further.
-__device__ __forceinline__ void store_pair(const TcParams& p, uint32_t* stg, int lane, uint16_t* y, int64_t lo, float (&v)[32],
-                                           int row0, int64_t n, int rows, bool turn) {
-  const int pieces = (int)min((int64_t)4, (p.y_rs - n) / 8), turned = (int)min((int64_t)4, (p.y_rs - row0) / 8);
-  const int cols = (int)min((int64_t)32, p.N - n);
-#pragma unroll 1
-  for (int part = 0; part < 2; ++part, y += lo) {
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], 1);
-    put_row(stg, lane, w);
-    store_slots<32>(stg, lane, y + row0 * p.y_rs + n, p.y_rs, rows, pieces);
-    if (turn) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) put_column(stg, lane, j, (uint16_t)(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]));
-      store_slots<32>(stg, lane, y + n * p.y_rs + row0, p.y_rs, cols, turned);
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-      v[2 * j] -= f.x;
-      v[2 * j + 1] -= f.y;
-    }
-  }
-}
-
-// 8 warps of 64 columns: every segment's accumulator is added to fp32 sums in
-// registers, then alpha, the state or C, and the stores.
+// 8 warps of 64 columns.  What is added to the product (kStateF: the fp32 state as
+// two boxes of 32 x 32; kSymF: C as 32 x 64 boxes of its high parts and rests)
+// arrives by TMA in the warp's two slots while the product is computed.  Every
+// segment's accumulator is added to fp32 sums in registers; the new state, then Y's
+// high parts and rests, take the slots' places and leave by TMA.  (Rows read and
+// written by their lanes, 16 bytes a lane and row: 28 and 58 us a launch at 2048.)
 template <int MODE, bool PAIR>
-__device__ void run_split_epilogue(const TcParams& p, uint32_t tmem, uint32_t accf0, uint32_t acce0,
-                                   volatile int* abort, uint32_t* stage) {
+__device__ void run_split_epilogue(const TcParams& p, const CUtensorMap* tmC, const CUtensorMap* tmY, uint32_t tmem,
+                                   uint32_t accf0, uint32_t acce0, uint32_t cbar, volatile int* abort, uint32_t* stage) {
+  constexpr int kCols = Cfg<MODE, PAIR>::kCols, TR = Geo<MODE, PAIR>::kTileRows, TN = Geo<MODE, PAIR>::kTileN;
+  static_assert(kCols == 64, "one pair of boxes a tile");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kCols = Cfg<MODE, PAIR>::kCols, kChunks = kCols / 32;
   const int quad = warp & 3, slice = (warp - kEpiWarp0) >> 2;
   const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
-  const int64_t row_off = PAIR ? (int64_t)rank * BM : 0;
+  const int row_off = PAIR ? (int)rank * BM : 0;
   const uint32_t rel0 = PAIR ? mapa_shared(acce0, 0) : acce0, tlane = (uint32_t)(quad * 32) << 16;
+  const uint32_t slot0 = smem_u32(stage), slot1 = slot0 + kBoxBytes, mine = (uint32_t)lane * 128;
+  const auto piece = [&](int q) { return mine + (((uint32_t)(q & 7) ^ ((uint32_t)lane & 7u)) << 4); };
   const int64_t total = total_tiles<MODE>(p);
   const int nseg = (p.num_kb + p.kb_per_seg - 1) / p.kb_per_seg;
-  uint32_t seg = 0;
-  Tile ti;
+  const bool has_c = MODE == kStateF || p.c != nullptr;
+  const auto fetch = [&](const Tile& ti) {
+    if (!has_c) return;
+    if (lane == 0) bulk_wait_read_all();                 // the slots' last stores have read them
+    __syncwarp();
+    fence_proxy_async_shared();
+    if (lane == 0) {
+      const int32_t c0 = (int32_t)ti.n0 + slice * kCols, r0 = (int32_t)ti.m0 + row_off + quad * 32;
+      mbar_arrive_expect_tx(cbar, 2 * kBoxBytes);
+      tma_load_3d(slot0, tmC, c0, r0, (int32_t)ti.batch, cbar);
+      if (MODE == kStateF) tma_load_3d(slot1, tmC, c0 + 32, r0, (int32_t)ti.batch, cbar);
+      else tma_load_3d(slot1, tmC, c0, r0, (int32_t)(ti.batch + p.c_lo), cbar);
+    }
+  };
+  uint32_t seg = 0, cphase = 0;
+  Tile ti, next;
   int gh = 0;
-  for (int64_t t = first_tile<MODE, PAIR>(p); get_tile<MODE, PAIR>(p, t, total, ti, gh); t += tile_step<MODE, PAIR>(p)) {
-    float acc[kChunks][32];
+  int64_t t = first_tile<MODE, PAIR>(p);
+  bool have = get_tile<MODE, PAIR>(p, t, total, ti, gh);
+  if (have) fetch(ti);
+  while (have) {
+    t += tile_step<MODE, PAIR>(p);
+    const bool more = get_tile<MODE, PAIR>(p, t, total, next, gh);
+    float acc[kCols];
     for (int s = 0; s < nseg; ++s, ++seg) {
       const uint32_t buf = seg & 1, aph = (seg >> 1) & 1;
       const bool ok = PAIR ? mbar_wait_cluster(accf0 + 8 * buf, aph, abort, p.status, p.timeout_ns)
                            : mbar_wait(accf0 + 8 * buf, aph, abort, p.status, p.timeout_ns);
-      if (!__all_sync(0xffffffffu, ok)) return;
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (has_c) mbar_wait_teardown(cbar, cphase, p.teardown_ns);      // the boxes in flight land
+        return;
+      }
       tc_fence_after();
       const uint32_t taddr = tmem + tlane + buf * BN + slice * kCols;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
+      for (int c = 0; c < kCols; c += 32) {
         uint32_t r[32];
-        tmem_ld32(taddr + c * 32, r);
+        tmem_ld32(taddr + c, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) acc[c][j] = s == 0 ? __uint_as_float(r[j]) : acc[c][j] + __uint_as_float(r[j]);
+        for (int j = 0; j < 32; ++j) acc[c + j] = s == 0 ? __uint_as_float(r[j]) : acc[c + j] + __uint_as_float(r[j]);
       }
       tc_fence_before();
       __syncwarp();
@@ -1477,56 +1456,115 @@ __device__ void run_split_epilogue(const TcParams& p, uint32_t tmem, uint32_t ac
         else mbar_arrive(acce0 + 8 * buf);
       }
     }
-    const int rows_t = PAIR ? max(0, min(BM, ti.rows - (int)row_off)) : ti.rows;
-    const int rl = quad * 32 + lane;
-    const bool rok = rl < rows_t;
-    const int64_t m = ti.m0 + row_off + rl;
-    const int32_t row0 = (int32_t)(ti.m0 + row_off + quad * 32);
-    const uint16_t* crow =
-        p.c && rok ? static_cast<const uint16_t*>(p.c) + batch_off(p, p.c_bstride, ti.batch) + m * p.c_rs : nullptr;
-    float* srow = MODE == kStateF && rok ? p.s32 + ti.batch * p.s_step + m * p.s_rs : nullptr;
 #pragma unroll
-    for (int h = 0; h < kChunks; ++h) {
-      const int64_t n = ti.n0 + slice * kCols + 32 * h;
-      if (n >= p.N) break;
-      float v[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = p.alpha * acc[h][j];
-      if (crow) add_state32(p, crow, n, v);
-      if constexpr (MODE == kStateF) {
-        if (srow) {                          // s_rs is a multiple of 4; the padding past N is never stored from
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            if (n + 4 * q >= p.s_rs) break;
-            const float4 f = *reinterpret_cast<const float4*>(srow + n + 4 * q);
-            v[4 * q] = __fmaf_rn(p.beta, f.x, v[4 * q]);
-            v[4 * q + 1] = __fmaf_rn(p.beta, f.y, v[4 * q + 1]);
-            v[4 * q + 2] = __fmaf_rn(p.beta, f.z, v[4 * q + 2]);
-            v[4 * q + 3] = __fmaf_rn(p.beta, f.w, v[4 * q + 3]);
-          }
-        }
-        if (p.y_lo == 0) {                   // the result
-          store_block32(stage, lane, v, static_cast<float*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + row0 * p.y_rs + n,
-                        p.y_rs, min(32, rows_t - quad * 32), (int)min((int64_t)32, p.N - n), p.y_vec);
-          continue;
-        }
-        if (srow) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            if (n + 4 * q >= p.s_rs) break;
-            *reinterpret_cast<float4*>(srow + n + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= p.up;
+    for (int j = 0; j < kCols; ++j) acc[j] *= p.alpha;
+    if (has_c) {
+      if (!__all_sync(0xffffffffu, mbar_wait(cbar, cphase, abort, p.status, p.timeout_ns))) {
+        mbar_wait_teardown(cbar, cphase, p.teardown_ns);
+        return;
       }
-      // kSymF: also transposed, where that falls into a tile that is not computed.
-      constexpr int TR = Geo<MODE, PAIR>::kTileRows, TN = Geo<MODE, PAIR>::kTileN;
-      if (quad * 32 < rows_t)
-        store_pair(p, stage, lane, static_cast<uint16_t*>(p.y) + batch_off(p, p.y_bstride, ti.batch),
-                   p.y_lo * p.y_bstride[0], v, row0, n, min(32, rows_t - quad * 32),
-                   MODE == kSymF && (row0 / TN) * TN > ((int32_t)n / TR) * TR + TR - 1);
+      cphase ^= 1;
+      if constexpr (MODE == kStateF) {
+#pragma unroll
+        for (int q = 0; q < kCols / 4; ++q) {
+          const uint32_t at = (q < 8 ? slot0 : slot1) + piece(q);
+          const uint4 u = lds128(at);
+          acc[4 * q] = __fmaf_rn(p.beta, __uint_as_float(u.x), acc[4 * q]);
+          acc[4 * q + 1] = __fmaf_rn(p.beta, __uint_as_float(u.y), acc[4 * q + 1]);
+          acc[4 * q + 2] = __fmaf_rn(p.beta, __uint_as_float(u.z), acc[4 * q + 2]);
+          acc[4 * q + 3] = __fmaf_rn(p.beta, __uint_as_float(u.w), acc[4 * q + 3]);
+          sts128(at, make_uint4(__float_as_uint(acc[4 * q]), __float_as_uint(acc[4 * q + 1]),
+                                __float_as_uint(acc[4 * q + 2]), __float_as_uint(acc[4 * q + 3])));
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < kCols / 8; ++q) {
+          const uint4 a = lds128(slot0 + piece(q)), b = lds128(slot1 + piece(q));
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
+            const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&bw[e]));
+            acc[8 * q + 2 * e] = __fmaf_rn(p.beta, h.x + l.x, acc[8 * q + 2 * e]);
+            acc[8 * q + 2 * e + 1] = __fmaf_rn(p.beta, h.y + l.y, acc[8 * q + 2 * e + 1]);
+          }
+        }
+      }
     }
+    const int rows_t = PAIR ? max(0, min(BM, ti.rows - row_off)) : ti.rows;
+    const int32_t c0 = (int32_t)ti.n0 + slice * kCols, row0 = (int32_t)ti.m0 + row_off + quad * 32;
+    const bool live = quad * 32 < rows_t && c0 < p.N;
+    bool result = false;
+    if constexpr (MODE == kStateF) {
+      result = p.y_lo == 0;
+      if (!result || p.y_tma) {                          // the slots hold the new state, or the result
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0 && live) {
+          const CUtensorMap* to = result ? tmY : tmC;
+          tma_store_3d(to, slot0, c0, row0, (int32_t)ti.batch);
+          if (c0 + 32 < p.N) tma_store_3d(to, slot1, c0 + 32, row0, (int32_t)ti.batch);
+          bulk_commit();
+        }
+      } else {
+        __syncwarp();                                    // every lane has read its row
+        if (live) {
+          float* y0 = static_cast<float*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + (int64_t)row0 * p.y_rs + c0;
+#pragma unroll
+          for (int h = 0; h < kCols; h += 32) {
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = acc[h + j];
+            if (c0 + h < p.N)
+              store_block32(stage, lane, v, y0 + h, p.y_rs, min(32, rows_t - quad * 32), (int)min((int64_t)32, p.N - c0 - h), 0);
+          }
+        }
+      }
+    }
+    if (!result) {
+      uint32_t w[kCols / 2], rest[kCols / 2];
+#pragma unroll
+      for (int j = 0; j < kCols / 2; ++j) {
+        const float x = MODE == kStateF ? acc[2 * j] * p.up : acc[2 * j], y = MODE == kStateF ? acc[2 * j + 1] * p.up : acc[2 * j + 1];
+        w[j] = pack2(x, y, 1);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        rest[j] = pack2(x - f.x, y - f.y, 1);
+      }
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kCols / 8; ++q) {
+        sts128(slot0 + piece(q), make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
+        sts128(slot1 + piece(q), make_uint4(rest[4 * q], rest[4 * q + 1], rest[4 * q + 2], rest[4 * q + 3]));
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0 && live) {
+        tma_store_3d(tmY, slot0, c0, row0, (int32_t)ti.batch);
+        tma_store_3d(tmY, slot1, c0, row0, (int32_t)(ti.batch + p.y_lo));
+        bulk_commit();
+      }
+      if constexpr (MODE == kSymF) {
+        // Also transposed, where that falls into a tile that is not computed.
+        if (live && (row0 / TN) * TN > (c0 / TR) * TR + TR - 1) {
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+          uint32_t* turn = stage + kBoxBytes / 4;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            put_column(stage, lane, j, (uint16_t)(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]));
+            put_column(turn, lane, j, (uint16_t)(j & 1 ? rest[j >> 1] >> 16 : rest[j >> 1]));
+          }
+          uint16_t* y0 = static_cast<uint16_t*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + c0 * p.y_rs + row0;
+          const int cols = (int)min((int64_t)kCols, p.N - c0), pieces = (int)min((int64_t)4, (p.y_rs - row0) / 8);
+          store_slots<64>(stage, lane, y0, p.y_rs, cols, pieces);
+          store_slots<64>(turn, lane, y0 + p.y_lo * p.y_bstride[0], p.y_rs, cols, pieces);
+        }
+      }
+    }
+    if (more) fetch(next);
+    ti = next;
+    have = more;
   }
 }
 
@@ -1819,7 +1857,7 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
     }
     if (MODE == kTF32)
       for (int s = 0; s < S; ++s) mbar_init(qfull0 + 8 * s, 1);
-    if (is_ortho(MODE))                       // a barrier for each epilogue warp's boxes of C
+    if (has_boxes(MODE))                      // a barrier for each epilogue warp's boxes of C
       for (int w = 0; w < Cfg<MODE, PAIR>::kEpiWarps; ++w) mbar_init(cbase + 16 * S + 48 + 8 * w, 1);
     if (MODE == kGroupedQ)
       for (int s = 0; s < kQStages; ++s) {
@@ -1854,12 +1892,12 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
   // the previous kernel on the stream is finishing: the set-up above overlaps
   // its tail, and nothing below touches global memory before it completes.
   if (MODE != kSkinny || !p.c_late) pdl_wait();
-  if constexpr (MODE == kDense || MODE == kTF32 || MODE == kInt8 || is_ortho(MODE) || is_split(MODE))
+  if constexpr (MODE == kDense || MODE == kTF32 || MODE == kInt8 || has_boxes(MODE))
     pdl_trigger();
   const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
 
   // (elect_one: fewer cycles an instruction, and the compiler's to know.)
-  constexpr bool kElect = is_ortho(MODE) || is_split(MODE) || MODE == kInt8;
+  constexpr bool kElect = has_boxes(MODE) || MODE == kInt8;
   if (warp == 0) {
     if (kElect ? elect_one() : lane == 0)
       run_producer<MODE, PAIR>(&tmA, &tmB, &tmS, &tmZ, p, sbase, full0, empty0, qbase, qfull0, qempty0, abort);
@@ -1872,12 +1910,13 @@ __global__ void __launch_bounds__(Cfg<MODE, PAIR>::kThreads, 1)
     uint32_t* stage = reinterpret_cast<uint32_t*>(smem_raw + (sbase - raw) + G::kRingBytes) +
                       (warp - kEpiWarp0) * Cfg<MODE, PAIR>::kWarpWords;
     if constexpr (MODE == kSkinny) run_skinny_partial<MODE, PAIR>(p, tmem, accf0, abort, sbase);
-    else if constexpr (is_split(MODE)) run_split_epilogue<MODE, PAIR>(p, tmem, accf0, acce0, abort, stage);
+    else if constexpr (is_split(MODE)) 
+      run_split_epilogue<MODE, PAIR>(p, &tmS, &tmZ, tmem, accf0, acce0, cbase + 16 * S + 48 + 8 * (warp - kEpiWarp0), abort, stage);
     else if constexpr (is_ortho(MODE))
       run_ortho_epilogue<MODE, PAIR>(p, &tmS, &tmZ, tmem, accf0, acce0, cbase + 16 * S + 48 + 8 * (warp - kEpiWarp0), abort, stage);
     else run_epilogue<MODE, PAIR>(p, &tmZ, tmem, accf0, acce0, abort, stage);
     // Every tensor store has read its box before the CTA can exit.
-    if (p.y_tma && lane == 0) bulk_wait_all();
+    if ((p.y_tma || MODE == kStateF) && lane == 0) bulk_wait_all();
   } else if (MODE == kGroupedQ) {
     if (p.w4) run_convert<MODE, PAIR, true>(p, smem_raw, sbase, full0, qbase, qfull0, qempty0, cbase, abort);
     else run_convert<MODE, PAIR, false>(p, smem_raw, sbase, full0, qbase, qfull0, qempty0, cbase, abort);
@@ -2120,7 +2159,7 @@ mm_status launch_kernel(const OperandPlan& a, const OperandPlan& b, const CUtens
                         const TcParams& p_in, int64_t work, cudaStream_t stream) {
   constexpr int kSmem = Cfg<MODE, PAIR>::kSmem, kThreadsM = Cfg<MODE, PAIR>::kThreads;
   TcParams p = p_in;
-  if (MODE != kDense && MODE != kInt8 && !is_ortho(MODE)) p.y_tma = 0;
+  if (MODE != kDense && MODE != kInt8 && !has_boxes(MODE)) p.y_tma = 0;
   if (cudaFuncSetAttribute(tc_gemm_kernel<MODE, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
       cudaSuccess)
     return MM_ERR_CUDA;
@@ -2467,16 +2506,19 @@ mm_status launch_tc_int8(const Int8Args& q, const void* a, int64_t lda, const vo
 
 // [count][M][N] 16-bit values, rows ld and matrices `step` apart, in boxes of 32
 // rows and 64 columns, 128-byte swizzled.
-static bool plan_boxes64(const void* ptr, int dtype, int64_t M, int64_t N, int64_t ld, int64_t step, int64_t count,
+static bool plan_boxes(const void* ptr, int dtype, int64_t M, int64_t N, int64_t ld, int64_t step, int64_t count,
                          OperandPlan* out) {
   auto encode = encode_fn();
-  if (!encode || (reinterpret_cast<uintptr_t>(ptr) & 15) || ld % 8 || (count > 1 && step % 8)) return false;
+  const int size = dtype == MM_F32 ? 4 : 2, vec = 16 / size;
+  if (!encode || (reinterpret_cast<uintptr_t>(ptr) & 15) || ld % vec || (count > 1 && step % vec)) return false;
   if (M > 0x7fffffffLL || N > 0x7fffffffLL || count > 0x7fffffffLL) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)count};
-  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)((count > 1 ? step : M * ld) * 2)};
+  const cuuint64_t strides[2] = {(cuuint64_t)(ld * size), (cuuint64_t)((count > 1 ? step : M * ld) * size)};
   if (strides[0] >= (1ull << 40) || strides[1] >= (1ull << 40)) return false;
-  const cuuint32_t box[3] = {64u, 32u, 1u}, estr[3] = {1, 1, 1};
-  const CUtensorMapDataType dt = dtype == MM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint32_t box[3] = {128u / size, 32u, 1u}, estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = dtype == MM_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : dtype == MM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   out->mn_major = 0;
   for (int d = 0; d < kMaxBatchDims; ++d) out->bc[d] = 0;
   return encode(&out->map, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -2522,18 +2564,21 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
     p.kb_per_seg = kSplitSegment / BK;
     om.shape[0] = om.count = 2 * o.count;
     p.a_lo = p.b_lo = o.count;
-    p.s32 = o.s32;
-    p.s_rs = o.s_rs; p.s_step = o.s_step;
     p.up = o.up;
-  } else {
-    p.c_lo = o.sym ? 0 : o.count;
-    p.y_tma = plan_boxes64(o.y, o.y_dtype, g.M, g.N, o.y_rs, o.y_step, o.y_lo ? 2 * o.count : o.count, &ymap);
-    if ((o.sym || o.y_lo) && !p.y_tma) return MM_ERR_UNSUPPORTED;
-    if (o.c && !plan_boxes64(o.c, MM_F16, g.M, g.N, o.c_rs, o.c_step, o.sym ? o.count : 2 * o.count, &cmap))
-      return MM_ERR_UNSUPPORTED;
   }
+  p.c_lo = o.sym && !o.split ? 0 : o.count;
+  p.y_tma = plan_boxes(o.y, o.y_dtype, g.M, g.N, o.y_rs, o.y_step, o.y_lo ? 2 * o.count : o.count, &ymap);
+  if ((o.sym || o.y_lo) && !p.y_tma) return MM_ERR_UNSUPPORTED;
+  // C as it is held, or kStateF's state.
+  const bool have_c = o.s32 || o.c;
+  if (have_c && !(o.s32 ? plan_boxes(o.s32, MM_F32, g.M, g.N, o.s_rs, o.s_step, o.count, &cmap)
+                        : plan_boxes(o.c, MM_F16, g.M, g.N, o.c_rs, o.c_step, p.c_lo ? 2 * o.count : o.count, &cmap)))
+    return MM_ERR_UNSUPPORTED;
   const int64_t as[kMaxBatchDims] = {o.a_step}, bs[kMaxBatchDims] = {o.b_step};
-  for (int attempt = use_pair(g.M, g.K) ? 0 : 1; attempt < 2; ++attempt) {
+  // Pairs of CTAs read a third less per tile.  Split operands always (48 KB a k-block
+  // and CTA against 64); 16-bit ones from K = 512 on (us in pairs and singly: 1000 x
+  // 2500 291 318, 8 of 512 x 1000 200 208, 512 x 512 155 151, 256 x 256 125 113).
+  for (int attempt = use_pair(g.M, o.split || g.K > 512 ? kPairMinK : g.K) ? 0 : 1; attempt < 2; ++attempt) {
     const bool pair = attempt == 0;
     OperandPlan a, b;
     if (!plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, om, as, BM, &a) ||
@@ -2541,7 +2586,7 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
       return MM_ERR_UNSUPPORTED;
     p.idesc = make_idesc_mn(1, a.mn_major, b.mn_major, pair ? 2 * BM : BM, o.split ? BN / 2 : BN);
     // C's map takes the place of the tail map: these products have no tail tiles.
-    const mm_status st = launch_tc(mode, pair, a, b, p, stream, !o.split && o.c ? &cmap : &a, p.y_tma ? &ymap : nullptr);
+    const mm_status st = launch_tc(mode, pair, a, b, p, stream, have_c ? &cmap : &a, p.y_tma ? &ymap : nullptr);
     if (st != MM_ERR_UNSUPPORTED || !pair) return st;
   }
   return MM_ERR_UNSUPPORTED;

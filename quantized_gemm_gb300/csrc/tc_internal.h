@@ -72,12 +72,8 @@ struct TcParams {
   int64_t c_bstride[kMaxBatchDims];
   int64_t c_rs, c_cs, c_gs;                    // c_gs: grouped bias row stride per group
   int c_vec, c_live;                           // c_live: C is Y
-  int64_t c_lo, y_lo;                          // kState: from the high part to the rest (elements; batch coordinates, 0: Y is T)
-  // kSymF, kStateF: batch coordinates from the operands' high parts to their
-  // rests; kStateF: the fp32 state, read and (where Y is not the result) written.
-  int64_t a_lo, b_lo;
-  float* s32;
-  int64_t s_rs, s_step;
+  int64_t c_lo, y_lo;                          // kSym to kStateF: from the high part to the rest (batch coordinates; 0: none)
+  int64_t a_lo, b_lo;                          // kSymF, kStateF: batch coordinates from the operands' high parts to their rests
   float up;                                    // Y's pair is `up` times the new state
   int c_late, c_f32;                           // kSkinny: GemmArgs::c_late, c_f32
   // QLinear epilogue: zero-point correction from the operand sums, then requantisation
