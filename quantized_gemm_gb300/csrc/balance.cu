@@ -18,7 +18,7 @@
 // rows to come into its own places in shared memory (cp.async, kAhead rows).  65536
 // rows of 256 bf16 logits, forward and backward (101 MB, 15 us of memory): 95 us with
 // a row over all 32 lanes and a branch per logit (276 instructions a row), 43 with
-// two rows loaded into registers at a time, 40 so; what is left is the arithmetic
+// two rows loaded into registers at a time, 37 so; what is left is the arithmetic
 // (107 instructions a row forward) and three launches.  Column sums leave a block
 // through shared memory, one partial per block, and a second launch, one cluster,
 // adds the partials in a fixed order; picks are integers, counted with shared-memory
@@ -245,7 +245,7 @@ __device__ __forceinline__ void async_wait_oldest() { asm volatile("cp.async.wai
 template <typename T, int LPR, int NP, bool ASYNC>
 __global__ void __launch_bounds__(kThreads, 2) balance_partial_kernel(const BalanceArgs a, float* psum, int32_t* cnt,
                                                                       unsigned* status) {
-  pdl_wait();
+  pdl_begin();
   extern __shared__ __align__(16) uint8_t raw[];               // the queue, then [kWarps][G] column sums, [G + 2] counts
   using Q = Queue<T, LPR, NP, ASYNC>;
   float* sh = reinterpret_cast<float*>(raw + (ASYNC ? Q::kBytes : 0));
@@ -341,17 +341,34 @@ __global__ void __launch_bounds__(kThreads, 2) balance_partial_kernel(const Bala
 __global__ void __launch_bounds__(1024) __cluster_dims__(kFinalBlocks, 1, 1)
     balance_final_kernel(const int G, const int nb, const float* psum, const int32_t* cnt, float* loss, int32_t* counts,
                          float* mean) {
-  pdl_wait();
+  pdl_begin();
   __shared__ float part[32];
   __shared__ int tot[2][32];
   __shared__ float mine;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = (int)ptx::cluster_ctarank();
+  // 32 neighbouring columns at a time: lane = column for the reads, warps share the blocks.
+  __shared__ float ps[32][33];
+  __shared__ int cs[32][33];
+  float s;
+  int n;
+  const auto add_up = [&](int c0) {
+    s = 0.f;
+    n = 0;
+    if (c0 + lane < G) {
+#pragma unroll 10
+      for (int b = warp; b < nb; b += 32) {
+        s += __ldg(psum + (int64_t)b * G + c0 + lane);
+        n += __ldg(cnt + (int64_t)b * (G + 2) + c0 + lane);
+      }
+    }
+  };
   // Rows and picks in all: every block adds them for itself.
   int rows = 0, picks = 0;
   for (int b = threadIdx.x; b < nb; b += 1024) {
     rows += __ldg(cnt + (int64_t)b * (G + 2) + G);
     picks += __ldg(cnt + (int64_t)b * (G + 2) + G + 1);
   }
+  add_up(rank * 32);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     rows += __shfl_xor_sync(0xffffffffu, rows, o);
@@ -362,20 +379,9 @@ __global__ void __launch_bounds__(1024) __cluster_dims__(kFinalBlocks, 1, 1)
   rows = __reduce_add_sync(0xffffffffu, tot[0][lane]);
   picks = __reduce_add_sync(0xffffffffu, tot[1][lane]);
   const float inv_rows = rows > 0 ? 1.f / (float)rows : 0.f, inv_picks = picks > 0 ? 1.f / (float)picks : 0.f;
-  // 32 neighbouring columns at a time: lane = column for the reads, warps share the blocks.
-  __shared__ float ps[32][33];
-  __shared__ int cs[32][33];
   float lsum = 0.f;
   for (int c0 = rank * 32; c0 < G; c0 += kFinalBlocks * 32) {
-    float s = 0.f;
-    int n = 0;
-    if (c0 + lane < G) {
-#pragma unroll 10
-      for (int b = warp; b < nb; b += 32) {
-        s += __ldg(psum + (int64_t)b * G + c0 + lane);
-        n += __ldg(cnt + (int64_t)b * (G + 2) + c0 + lane);
-      }
-    }
+    if (c0 != rank * 32) add_up(c0);
     __syncthreads();
     ps[lane][warp] = s;
     cs[lane][warp] = n;
