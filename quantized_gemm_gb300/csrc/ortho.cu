@@ -55,13 +55,35 @@ __device__ __forceinline__ void walk(const NormArgs& a, F&& f) {
   walk_share<T, VEC>(a, b, chunk, first, last);
   const T* x = static_cast<const T*>(a.x.ptr) + batch_offset(a.bm, a.x.bstride, b);
   const uint32_t per_row = a.fd_row.d;
-#pragma unroll 4
-  for (int64_t i = first + threadIdx.x; i < last; i += kThreads) {
-    const uint32_t r = i < (1ll << 32) ? fast_div((uint32_t)i, a.fd_row) : (uint32_t)(i / per_row);
-    const int64_t c = (i - (int64_t)r * per_row) * E;
-    T e[E];
+  const auto place = [&](int64_t i, uint32_t& r, int64_t& c) {
+    r = i < (1ll << 32) ? fast_div((uint32_t)i, a.fd_row) : (uint32_t)(i / per_row);
+    c = (i - (int64_t)r * per_row) * E;
+  };
+  const auto load = [&](uint32_t r, int64_t c, T (&e)[E]) {
     if constexpr (VEC) *reinterpret_cast<uint4*>(e) = __ldg(reinterpret_cast<const uint4*>(x + r * a.x.rs + c));
     else e[0] = x[r * a.x.rs + c * a.x.cs];
+  };
+  // (Loads that the calls of f stand between are not moved together by the compiler.)
+  constexpr int kTogether = 4;
+  int64_t i = first + threadIdx.x;
+  for (; i + (kTogether - 1) * kThreads < last; i += kTogether * kThreads) {
+    uint32_t r[kTogether];
+    int64_t c[kTogether];
+    __align__(16) T e[kTogether][E];
+#pragma unroll
+    for (int q = 0; q < kTogether; ++q) {
+      place(i + q * kThreads, r[q], c[q]);
+      load(r[q], c[q], e[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < kTogether; ++q) f(b, r[q], c[q], e[q]);
+  }
+  for (; i < last; i += kThreads) {
+    uint32_t r;
+    int64_t c;
+    __align__(16) T e[E];
+    place(i, r, c);
+    load(r, c, e);
     f(b, r, c, e);
   }
 }
