@@ -454,10 +454,10 @@ mm_status mm_int8_matmul(const mm_tensor* A, const mm_tensor* B, const mm_tensor
  * the call returns.  0 <= steps <= MM_ORTHO_MAX_STEPS, eps >= 0, all finite (else
  * MM_ERR_INVALID_ARG).  A matrix of zeros gives zeros for eps > 0 and NaN for eps =
  * 0; one that holds an infinity or NaN gives NaN, and touches no other.
- * The norm covers fp32's whole range.  Between the steps X_i is fp32, or 22 bits in
- * two f16 values where a stack of 16-bit matrices runs on the tensor cores; there
- * the operands of the products are f16 values for 16-bit types (11 bits, scaled so
- * that none leaves the type's range) and pairs of them, 22 bits, for f32.
+ * The norm covers fp32's whole range.  Between the steps X_i is fp32, and on the
+ * tensor cores the products' operands are pairs of f16 values (22 bits, scaled so
+ * that none leaves the type's range); for bf16 matrices with both sides above 512 the
+ * operands are one f16 value (11 bits) and X_i two.
  * Workspace: mm_orthogonalize_workspace_size() bytes. */
 #define MM_ORTHO_MAX_STEPS 64
 mm_status mm_orthogonalize_workspace_size(const mm_tensor* X, size_t* bytes);

@@ -185,15 +185,13 @@ mm_status launch_int8_any(const Int8Args& args, cudaStream_t stream);
 mm_status launch_int8_copies(const Int8Copy& A, const Int8Copy& B, cudaStream_t stream);
 
 // The norm, the division and the chain of products; or one launch, for matrices that
-// fit a cluster's shared memory.  m is the smaller side: any stack of m <= 32, of
-// which a tile of the chain would use an eighth at most, and of m <= 64 for fp32,
-// whose products are three; else up to kOrthoSmallWork = m m n matrices.  us in one
-// launch and in the chain, f32 and bf16:
-//   64 x 1000        62 177   67 120      300 of 64 x 64     110 209   114 140
-//   128 x 1000      183 237  189 137      300 of 64 x 256    209 295   226 159
-//   64 x 4000       163 300  180 192      8 of 128 x 512     135 189   137 113
-//   200 of 32 x 32   25 137   26 134      100 of 128 x 128   267 189   273 111
-//   500 of 32 x 512 200 640  214 331      400 of 32 x 2000   718 1869  912 831
+// fit a cluster's shared memory: with m the smaller side, any stack of m <= 64, of
+// which a tile of the chain would use a quarter at most, and up to kOrthoSmallWork =
+// m m n matrices above.  us in one launch and in the chain:
+//   64 x 1000        62 177      300 of 64 x 64     110 209    128 x 1000       183 237
+//   64 x 4000       163 300      300 of 64 x 256    209 295    8 of 128 x 512   135 189
+//   200 of 32 x 32   25 137      1000 of 64 x 64    379 590    30 of 128 x 256  139 180
+//   500 of 32 x 512 200 640      256 of 64 x 512    344 437    100 of 128 x 128 267 189
 constexpr double kOrthoSmallWork = 1.5e8;
 size_t ortho_workspace_bytes(const OrthoArgs& args);
 mm_status launch_ortho(const OrthoArgs& args, void* workspace, cudaStream_t stream);

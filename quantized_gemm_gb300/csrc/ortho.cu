@@ -351,10 +351,14 @@ mm_status run_float(const OrthoArgs& o, void* ws, cudaStream_t st) {
 // high part, below 2^-39 the pair has none).
 // A and B are symmetric: only the lower triangle's tiles are computed.
 //
-// fp32 matrices take the same chain with every operand split into two f16 values
-// (22 bits) and three products each, and a state in fp32 beside them.  (Three tf32
-// products of fp32 operands took 1.49 ms for 2048 x 2048 and were off by 1.8e-5:
-// their additions truncate, 3 K / 8 times a sum; see kSymF.)
+// fp32 and f16 matrices, and bf16 ones up to kHalfSide, take the same chain with
+// every operand split into two f16 values (22 bits) and three products each, and a
+// state in fp32 beside them.  (Three tf32 products of fp32 operands took 1.49 ms for
+// 2048 x 2048 and were off by 1.8e-5: their additions truncate, 3 K / 8 times a sum;
+// see kSymF.)  An f16 result would be off by 2.1e-3 with 11-bit operands, ten times
+// its own rounding; a bf16 one is off by 1.2 to 1.4 times its rounding from 512 rows
+// on, by up to 1.6 times below, where the launches cost more than the products
+// (us for 512 x 512, 256 x 256, 8 of 512 x 1000: 148 113 204, split 178 126 267).
 
 double power_below(double x) {
   if (x > 0x1p30) return 0x1p30;         // infinite where the array is zeros
@@ -400,6 +404,9 @@ bool half_scales(const OrthoArgs& o, HalfScales (&k)[MM_ORTHO_MAX_STEPS + 1]) {
   return true;
 }
 
+constexpr int64_t kHalfSide = 512;
+bool split_operands(const OrthoArgs& o) { return o.dtype != MM_BF16 || o.M <= kHalfSide || o.N <= kHalfSide; }
+
 struct HalfPlan {
   int64_t m, ld, ldm;
   int chunks;
@@ -411,14 +418,14 @@ HalfPlan plan_half(const OrthoArgs& o) {
   p.ld = round_up(o.N, 8);
   p.ldm = round_up(p.m, 8);
   p.chunks = norm_chunks(o.M, o.N, o.bm.count);
-  const size_t x = align256((size_t)o.bm.count * o.M * p.ld * 4), sq = align256((size_t)o.bm.count * p.m * p.ldm * (o.dtype == MM_F32 ? 4 : 2));
+  const size_t x = align256((size_t)o.bm.count * o.M * p.ld * 4), sq = align256((size_t)o.bm.count * p.m * p.ldm * (split_operands(o) ? 4 : 2));
   p.part = 0;
   p.x[0] = align256((size_t)o.bm.count * p.chunks * 8);
   p.x[1] = p.x[0] + x;
   p.a = p.x[1] + x;
   p.b = p.a + sq;
   p.s = p.b + sq;
-  p.bytes = p.s + (o.dtype == MM_F32 ? x : 0);
+  p.bytes = p.s + (split_operands(o) ? x : 0);
   return p;
 }
 
@@ -438,7 +445,7 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
   n.h = reinterpret_cast<__half*>(w + p.x[0]);
   n.rest = rest;
   n.up = (float)k[0].x;
-  const bool split = o.dtype == MM_F32;
+  const bool split = split_operands(o);
   float* S = split ? reinterpret_cast<float*>(w + p.s) : nullptr;
   n.s = S;
   mm_status s = divide(o, n, st);

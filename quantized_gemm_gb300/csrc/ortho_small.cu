@@ -370,7 +370,7 @@ cudaError_t by_side(const SmallArgs& a, int cluster, int64_t count, size_t smem,
 bool ortho_small_pays(const OrthoArgs& o) {
   const int64_t m = o.M < o.N ? o.M : o.N, n = o.M < o.N ? o.N : o.M;
   return small_cluster(o) > 0 && o.bm.count < (1ll << 27) &&
-         (m <= (o.dtype == MM_F32 ? 64 : 32) || (double)m * (double)m * (double)n * (double)o.bm.count <= kOrthoSmallWork);
+         (m <= 64 || (double)m * (double)m * (double)n * (double)o.bm.count <= kOrthoSmallWork);
 }
 
 mm_status launch_ortho_small(const OrthoArgs& o, cudaStream_t stream) {

@@ -44,9 +44,9 @@ struct OrthoProduct {
   const void* c; int64_t c_rs, c_step, c_lo;
   void* y; int64_t y_rs, y_step, y_lo;
   float alpha, beta;
-  // fp32: the operands are pairs (their rests count matrices further); the
+  // split: the operands are pairs (their rests count matrices further); the
   // state s32 is fp32 and takes C's place, holds the result times 1 / up, and
-  // Y is the pair of `up` times it, or with y_lo = 0 the fp32 result.
+  // Y is the pair of `up` times it, or with y_lo = 0 the result in y_dtype.
   int split;
   float* s32; int64_t s_rs, s_step;
   float up;

@@ -52,7 +52,7 @@
 //             y = (acc * a_scale[m]) * b_scale[n] + bias[n], rounded once.
 //   kSym      kDense with a symmetric result: the lower triangle's tiles only.
 //   kState    kDense plus a state held in two f16 parts.
-//   kSymF, kStateF  the same for fp32: three f16 products of split operands.
+//   kSymF, kStateF  the same with three f16 products of split operands and a state in fp32.
 //   kSkinny   kDense for at most 64 rows of A': 256-column tiles whose
 //             k-blocks are split over the CTAs of a cluster (non-persistent,
 //             one tile per cluster), so that B' streams through every SM with
@@ -104,7 +104,7 @@ struct Geo {
   static constexpr int kStageBytes = (kABytes + kBBytes) * (kLoOff ? 2 : 1);
   // kGroupedQ gives one stage's worth of shared memory to its int8 staging ring.
   static constexpr int kStages =
-      is_split(MODE) ? (PAIR ? 3 : 2) : kLoOff ? (PAIR ? 3 : 2) : is_ortho(MODE) ? (PAIR ? 5 : 3) : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
+      is_split(MODE) ? (PAIR ? 3 : 2) : kLoOff ? (PAIR ? 3 : 2) : is_ortho(MODE) ? 5 : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
   static constexpr int kTileRows = PAIR ? 2 * BM : BM;  // output rows per (pair) tile
   static constexpr int kRingBytes = kStages * kStageBytes;
 };
@@ -214,21 +214,18 @@ __device__ __forceinline__ bool get_tile(const TcParams& p, int64_t t, int64_t t
   const uint32_t tt = (uint32_t)t;
   const uint32_t b = fast_div(tt, p.fd_per_batch);
   const uint32_t r = tt - b * p.fd_per_batch.d;
-  if (MODE == kSym || MODE == kSymF) {
-    // Row by row of the lower triangle (see sym_tiles): where a tile is as wide as it
-    // is high, row i has i + 1 tiles; half as wide, 2 (i + 1); twice as wide, rows 2i
-    // and 2i + 1 have i + 1 each.
-    constexpr uint32_t TR = Geo<MODE, PAIR>::kTileRows, TN = Geo<MODE, PAIR>::kTileN;
-    constexpr uint32_t kHigh = TN > TR ? TN / TR : 1, kWide = TR > TN ? TR / TN : 1;
-    const uint32_t q = r / (kHigh * kWide);              // of the squares of max(TR, TN)
+  if constexpr (MODE == kSym || MODE == kSymF) {
+    // Row by row of the lower triangle (see sym_tiles): row i has i + 1 tiles that are
+    // as wide as high, 2 (i + 1) that are half as wide.
+    constexpr uint32_t TR = Geo<MODE, PAIR>::kTileRows, TN = Geo<MODE, PAIR>::kTileN, kWide = TR / TN;
+    const uint32_t q = r / kWide;                        // of the squares
     uint32_t i = (uint32_t)((sqrtf(8.f * (float)q + 1.f) - 1.f) * 0.5f);
     while ((i + 1) * (i + 2) / 2 <= q) ++i;
     while (i * (i + 1) / 2 > q) --i;
-    uint32_t w = r - kHigh * kWide * (i * (i + 1) / 2), mtile = i * kHigh;
-    if (kHigh > 1 && w > i) { w -= i + 1; ++mtile; }
+    const uint32_t w = r - kWide * (i * (i + 1) / 2);
     ti.batch = b;
     ti.g = 0;
-    ti.m0 = (int64_t)mtile * Geo<MODE, PAIR>::kTileRows;
+    ti.m0 = (int64_t)i * TR;
     ti.n0 = (int64_t)w * TN;
     ti.a_row = (int32_t)ti.m0;
     ti.a_b = (int32_t)batch_off(p, p.a_bc, b);
@@ -1497,7 +1494,34 @@ __device__ void run_split_epilogue(const TcParams& p, const CUtensorMap* tmC, co
     bool result = false;
     if constexpr (MODE == kStateF) {
       result = p.y_lo == 0;
-      if (!result || p.y_tma) {                          // the slots hold the new state, or the result
+      if (result && !p.out_f32) {                        // rounded to 16 bits, in the first slot
+        uint32_t w[kCols / 2];
+#pragma unroll
+        for (int j = 0; j < kCols / 2; ++j) w[j] = pack2(acc[2 * j], acc[2 * j + 1], p.out_f16);
+        __syncwarp();
+        if (p.y_tma) {
+#pragma unroll
+          for (int q = 0; q < kCols / 8; ++q)
+            sts128(slot0 + piece(q), make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0 && live) {
+            tma_store_3d(tmY, slot0, c0, row0, (int32_t)ti.batch);
+            bulk_commit();
+          }
+        } else if (live) {
+          uint16_t* y0 = static_cast<uint16_t*>(p.y) + batch_off(p, p.y_bstride, ti.batch) + (int64_t)row0 * p.y_rs + c0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t half[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) half[e] = w[16 * h + e];
+            if (c0 + 32 * h < p.N)
+              store_block16(stage, lane, half, y0 + 32 * h, p.y_rs, min(32, rows_t - quad * 32),
+                            (int)min((int64_t)32, p.N - c0 - 32 * h));
+          }
+        }
+      } else if (!result || p.y_tma) {                   // the slots hold the new state, or the result
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0 && live) {
@@ -2208,14 +2232,9 @@ mm_status launch_kernel(const OperandPlan& a, const OperandPlan& b, const CUtens
                                                                                                       : MM_ERR_CUDA;
 }
 
-// Tiles of a symmetric product that touch its lower triangle, of mt row tiles (256
-// rows in a pair, 128 else); columns: 256, or 128 for split operands.
-int64_t sym_tiles(int64_t mt, bool pair, int cols) {
-  const int rows = pair ? 2 * BM : BM;
-  if (cols <= rows) return rows / cols * (mt * (mt + 1) / 2);
-  const int64_t a = mt / 2;
-  return a * (a + 1) + (mt & 1 ? a + 1 : 0);
-}
+// Tiles of a symmetric product that touch its lower triangle: mt row tiles of 256
+// rows in a pair, 128 else; 256 columns, or 128 for split operands.
+int64_t sym_tiles(int64_t mt, int64_t rows, int64_t cols) { return rows / cols * (mt * (mt + 1) / 2); }
 
 }  // namespace
 
@@ -2232,7 +2251,7 @@ mm_status launch_tc(int mode, bool pair, const OperandPlan& a, const OperandPlan
     const int64_t cols = is_split(mode) ? BN / 2 : BN;
     p.mt = (p.M + rows - 1) / rows;
     p.nt = (p.N + cols - 1) / cols;
-    const int64_t per_matrix = mode == kSym || mode == kSymF ? sym_tiles(p.mt, pair, (int)cols) : p.mt * p.nt;
+    const int64_t per_matrix = mode == kSym || mode == kSymF ? sym_tiles(p.mt, rows, cols) : p.mt * p.nt;
     p.tiles = per_matrix * p.bm.count;
     if (p.tiles >= (1ll << 31) || p.mt * p.nt >= (1ll << 31)) return MM_ERR_UNSUPPORTED;
     const uint32_t per_batch = (uint32_t)per_matrix;
@@ -2276,12 +2295,10 @@ mm_status launch_tc(int mode, bool pair, const OperandPlan& a, const OperandPlan
     case kInt8:
       return pair ? launch_kernel<kInt8, true>(a, b, ms, mz, p, work, stream)
                   : launch_kernel<kInt8, false>(a, b, ms, mz, p, work, stream);
-    case kSym:
-      return pair ? launch_kernel<kSym, true>(a, b, ms, mz, p, work, stream)
-                  : launch_kernel<kSym, false>(a, b, ms, mz, p, work, stream);
+    case kSym:       // larger matrices, in pairs only
+      return pair ? launch_kernel<kSym, true>(a, b, ms, mz, p, work, stream) : MM_ERR_UNSUPPORTED;
     case kState:
-      return pair ? launch_kernel<kState, true>(a, b, ms, mz, p, work, stream)
-                  : launch_kernel<kState, false>(a, b, ms, mz, p, work, stream);
+      return pair ? launch_kernel<kState, true>(a, b, ms, mz, p, work, stream) : MM_ERR_UNSUPPORTED;
     case kSymF:
       return pair ? launch_kernel<kSymF, true>(a, b, ms, mz, p, work, stream)
                   : launch_kernel<kSymF, false>(a, b, ms, mz, p, work, stream);
@@ -2542,6 +2559,7 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
   p.M = g.M; p.N = g.N; p.K = g.K;
   p.bm = g.bm;
   p.out_f16 = o.y_dtype == MM_F16;
+  p.out_f32 = f32_out;
   p.y = o.y;
   p.y_rs = o.y_rs;
   p.y_bstride[0] = o.y_step;
@@ -2575,21 +2593,16 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
                         : plan_boxes(o.c, MM_F16, g.M, g.N, o.c_rs, o.c_step, p.c_lo ? 2 * o.count : o.count, &cmap)))
     return MM_ERR_UNSUPPORTED;
   const int64_t as[kMaxBatchDims] = {o.a_step}, bs[kMaxBatchDims] = {o.b_step};
-  // Pairs of CTAs read a third less per tile.  Split operands always (48 KB a k-block
-  // and CTA against 64); 16-bit ones from K = 512 on (us in pairs and singly: 1000 x
-  // 2500 291 318, 8 of 512 x 1000 200 208, 512 x 512 155 151, 256 x 256 125 113).
-  for (int attempt = use_pair(g.M, o.split || g.K > 512 ? kPairMinK : g.K) ? 0 : 1; attempt < 2; ++attempt) {
-    const bool pair = attempt == 0;
-    OperandPlan a, b;
-    if (!plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, om, as, BM, &a) ||
-        !plan_operand(o.b, MM_F16, g.N, g.K, o.b_cs, o.b_rs, om, bs, (o.split ? BN / 2 : BN) / (pair ? 2 : 1), &b))
-      return MM_ERR_UNSUPPORTED;
-    p.idesc = make_idesc_mn(1, a.mn_major, b.mn_major, pair ? 2 * BM : BM, o.split ? BN / 2 : BN);
-    // C's map takes the place of the tail map: these products have no tail tiles.
-    const mm_status st = launch_tc(mode, pair, a, b, p, stream, have_c ? &cmap : &a, p.y_tma ? &ymap : nullptr);
-    if (st != MM_ERR_UNSUPPORTED || !pair) return st;
-  }
-  return MM_ERR_UNSUPPORTED;
+  // Pairs of CTAs read a third less per tile (a split k-block is 48 KB a CTA against 64).
+  const bool pair = g.M > BM;
+  OperandPlan a, b;
+  const int cols = o.split ? BN / 2 : BN;
+  if (!plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, om, as, BM, &a) ||
+      !plan_operand(o.b, MM_F16, g.N, g.K, o.b_cs, o.b_rs, om, bs, cols / (pair ? 2 : 1), &b))
+    return MM_ERR_UNSUPPORTED;
+  p.idesc = make_idesc_mn(1, a.mn_major, b.mn_major, pair ? 2 * BM : BM, cols);
+  // C's map takes the place of the tail map: these products have no tail tiles.
+  return launch_tc(mode, pair, a, b, p, stream, have_c ? &cmap : &a, p.y_tma ? &ymap : nullptr);
 }
 
 // ------------------------------------------------------------------ dense product with per-row adapters

@@ -290,8 +290,9 @@ def test_balance_results_repeat():
 # ------------------------------------------------------------------ orthogonalised update
 
 
-def _operand(dtype):
-    return 3 * 2.0 ** -22 if dtype == F32 else 2.0 ** -11
+def _operand(X):
+    """The products' operands: two f16 values, or one for larger bf16 matrices."""
+    return 2.0 ** -11 if X.dtype == BF16 and min(X.shape[-2:]) > 512 else 3 * 2.0 ** -22
 
 
 def _check_ortho(X, steps=5, coefficients=MUON, eps=1e-7, scale=1.0):
@@ -303,7 +304,7 @@ def _check_ortho(X, steps=5, coefficients=MUON, eps=1e-7, scale=1.0):
     assert np.isfinite(y).all()
     for a, b in zip(x, y):
         want = layer.orthogonalize(a, per, eps, scale)
-        bound = layer.orthogonalize_bound(a, per, eps, scale, _operand(X.dtype), U[X.dtype])
+        bound = layer.orthogonalize_bound(a, per, eps, scale, _operand(X), U[X.dtype])
         off = np.linalg.norm(b - want)
         assert off <= bound, "%g of the bound" % (off / bound)
     return Y
@@ -318,7 +319,8 @@ def test_orthogonalize(shape, dtype):
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("shape", [(2, 2), (16, 16), (61, 100), (100, 61), (64, 64), (65, 300), (300, 65), (130, 136), (256, 256), (257, 600),
-                                   (385, 129), (520, 264), (3, 20, 33), (5, 130, 64), (3, 136, 264), (2, 300, 1100)])
+                                   (385, 129), (520, 264), (3, 20, 33), (5, 130, 64), (3, 136, 264), (2, 300, 1100), (513, 513),
+                                   (520, 777), (1030, 523), (2, 516, 600)])
 def test_orthogonalize_on_the_tensor_cores(shape, dtype):
     """The chain of products for sizes that a cluster would take; tiles that end inside, and on both sides of the diagonal."""
     qg.mm_set_path_policy(qg.MM_PATH_TENSOR)
@@ -394,7 +396,7 @@ def test_orthogonalize_more_matrices_than_a_grid_axis_holds(dtype):
             qg.mm_set_path_policy(qg.MM_PATH_AUTO)
         for i in (0, 65535, 65536, 65999):
             want = layer.orthogonalize(to_np(X[i]), [MUON] * 5, 1e-7)
-            bound = layer.orthogonalize_bound(to_np(X[i]), [MUON] * 5, 1e-7, 1.0, _operand(dtype), U[dtype])
+            bound = layer.orthogonalize_bound(to_np(X[i]), [MUON] * 5, 1e-7, 1.0, _operand(X), U[dtype])
             assert np.linalg.norm(to_np(Y[i]) - want) <= bound
 
 
@@ -606,7 +608,7 @@ def test_large_stack(dtype):
     X[-1] = rand_tensor((240, 1024), dtype, 7, DEV)
     Y = qg.mm_orthogonalize(X)
     want = layer.orthogonalize(to_np(X[-1]), [MUON] * 5, 1e-7)
-    bound = layer.orthogonalize_bound(to_np(X[-1]), [MUON] * 5, 1e-7, 1.0, _operand(dtype), U[dtype])
+    bound = layer.orthogonalize_bound(to_np(X[-1]), [MUON] * 5, 1e-7, 1.0, _operand(X), U[dtype])
     assert np.linalg.norm(to_np(Y[-1]) - want) <= bound
     assert not Y[:-1].any()
 
