@@ -265,7 +265,7 @@ __device__ __forceinline__ float bias_at(const Int8Args& a, int64_t n) {
 // streams once.  A warp owns kCols columns; its lanes split k in 16-byte pieces,
 // hold kDeep pieces of each column in flight and multiply them with the rows of A
 // (from the L1) by dp4a, exactly: a lane adds fewer than 2^17 products of at most
-// 2^14 (K < 2^22), and the lanes' sums are added as floats.  Bound: memory; one row
+// 2^14, and the lanes' sums are added as floats.  Bound: memory; one row
 // by 4096 x 14336 (59 MB): 10.7 us, 5.5 TB/s.
 
 template <typename O, int M>
@@ -550,7 +550,8 @@ mm_status launch_quantize_rows(const QuantizeArgs& a, cudaStream_t stream) {
 }
 
 bool int8_few_supported(const Int8Args& a) {
-  return a.M <= kInt8FewRows && a.K % 16 == 0 && a.K >= 16 && a.K < (1 << 22) && a.a_cs == 1 && a.b_ks == 1 &&
+  // (8191 pieces a lane at most: 8192 products sums of -128 * -128 pass int32.)
+  return a.M <= kInt8FewRows && a.K % 16 == 0 && a.K >= 16 && a.K <= 8191 * 32 * 16 && a.a_cs == 1 && a.b_ks == 1 &&
          a.b_ns % 16 == 0 && (a.M == 1 || a.a_rs % 16 == 0) && (reinterpret_cast<uintptr_t>(a.a) & 15) == 0 &&
          (reinterpret_cast<uintptr_t>(a.b) & 15) == 0 && a.N < (1ll << 31);
 }

@@ -126,6 +126,18 @@ def test_int8_sums_at_their_largest(M, path):
         _check_int8(*(lambda A, B, *r: (A, B.t(), *r))(*_int8_inputs(M, K, 264, F32, 5, bias=False, full=True)), F32)
 
 
+@pytest.mark.parametrize("K", [8191 * 512, 8191 * 512 + 16, 8192 * 512 - 16, 8192 * 512])
+def test_int8_longest_sums_of_a_few_rows(K):
+    """Every product 2^14: the integer sums of the few-row form just fit, then other forms take over."""
+    A = torch.full((1, K), -128, dtype=torch.int8, device=DEV)
+    one = torch.ones(2, device=DEV)
+    Y = qg.mm_int8_matmul(A, A.expand(2, K).contiguous().t(), one[:1], one, dtype=F32)
+    # exact lanes and 31 fp32 additions, or the fp32 additions of the tensor cores
+    few = qg.mm_last_path() == qg.MM_PATH_VECTOR
+    assert few == (K <= 8191 * 512)
+    assert float((Y.double() / (2.0 ** 14 * K) - 1).abs().max()) <= (37 * 2.0 ** -24 if few else (K / 16 + 1) * 2.0 ** -23)
+
+
 def test_int8_strided_views(path):
     A, B, sa, sb, bias = _int8_inputs(90, 300, 400, F32, 11)
     for a in (A, A[::2], A[:, 5:], A[:, ::3], A.t().contiguous().t(), A[3:4].expand(20, 300), A[:1], A[5:7, 1:]):
