@@ -437,7 +437,8 @@ mm_status mm_quantize_rows(const mm_tensor* x, const mm_tensor* q, const mm_tens
  * it is a sum of exact products in fp32 whose additions may truncate: off by at most
  * (K / 16 + 1) 2^-23 sum_k |A[m,k] B[k,n]|.  K = 0 gives the bias.
  * The fastest layout has B's columns contiguous along k and 16-byte aligned (a
- * transposed [N,K] tensor, K a multiple of 16), rows of A likewise.
+ * transposed [N,K] tensor, K a multiple of 16), rows of A likewise; from 5 rows on
+ * other layouts cost a copy of the weights.
  * Workspace: mm_int8_matmul_workspace_size() bytes for an output of out_dtype. */
 mm_status mm_int8_matmul_workspace_size(const mm_tensor* A, const mm_tensor* B, int32_t out_dtype, size_t* bytes);
 mm_status mm_int8_matmul(const mm_tensor* A, const mm_tensor* B, const mm_tensor* a_scale, const mm_tensor* b_scale,

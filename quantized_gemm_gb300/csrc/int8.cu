@@ -1,7 +1,8 @@
 // Rows to int8 with a scale each (mm_quantize_rows), and the CUDA-core parts of
-// the 8-bit product (mm_int8_matmul): the form for a few rows, the form for every
-// stride, and the f16 copies that the dense tensor-core product multiplies.
-#include "kernels.h"
+// the 8-bit product (mm_int8_matmul): the form for a few aligned rows (others are
+// in int8_few.cu), the form for every stride, and the copies that the tensor-core
+// products multiply.
+#include "int8.cuh"
 #include "tc_ptx.cuh"
 
 namespace qg {
@@ -247,18 +248,6 @@ mm_status run_quantize(const QuantizeArgs& a, cudaStream_t stream) {
   return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
-// ------------------------------------------------------------------ the product's last step
-
-// y = T((acc * a_scale) * b_scale + bias), each step rounded in fp32.
-template <typename O>
-__device__ __forceinline__ O finish8(float acc, float sa, float sb, float bias) {
-  return from_f32<O>(__fadd_rn(__fmul_rn(__fmul_rn(acc, sa), sb), bias));
-}
-template <typename O>
-__device__ __forceinline__ float bias_at(const Int8Args& a, int64_t n) {
-  return a.bias ? to_f32(static_cast<const O*>(a.bias)[n * a.bias_s]) : 0.f;
-}
-
 // ------------------------------------------------------------------ a few rows
 //
 // Up to kInt8FewRows rows of A against B whose columns are contiguous along k: B
@@ -431,12 +420,7 @@ mm_status run_any(const Int8Args& a, cudaStream_t stream) {
 // shifted; one whose rows are neighbours (rs = 1) is turned in tiles of 128 x 128
 // through shared memory.  (Byte by byte, 4096 x 14336 took 160 us.)
 
-// 4 bytes, and 16, at any address.
-__device__ __forceinline__ uint32_t bytes4(const int8_t* p) {
-  const uint32_t sh = ((uint32_t)reinterpret_cast<uintptr_t>(p) & 3u) * 8;
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
-  return sh ? __funnelshift_r(__ldg(w), __ldg(w + 1), sh) : __ldg(w);
-}
+// 16 bytes at any address.
 __device__ __forceinline__ uint4 bytes16(const int8_t* p) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(p);
   if ((at & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(p));
@@ -549,14 +533,14 @@ mm_status launch_quantize_rows(const QuantizeArgs& a, cudaStream_t stream) {
   }
 }
 
-bool int8_few_supported(const Int8Args& a) {
+bool int8_few_aligned(const Int8Args& a) {
   // (8191 pieces a lane at most: 8192 products sums of -128 * -128 pass int32.)
-  return a.M <= kInt8FewRows && a.K % 16 == 0 && a.K >= 16 && a.K <= 8191 * 32 * 16 && a.a_cs == 1 && a.b_ks == 1 &&
+  return a.M <= kInt8FewRows && a.K % 16 == 0 && a.K >= 16 && a.K <= kInt8FewDepth && a.a_cs == 1 && a.b_ks == 1 &&
          a.b_ns % 16 == 0 && (a.M == 1 || a.a_rs % 16 == 0) && (reinterpret_cast<uintptr_t>(a.a) & 15) == 0 &&
          (reinterpret_cast<uintptr_t>(a.b) & 15) == 0 && a.N < (1ll << 31);
 }
 
-mm_status launch_int8_few(const Int8Args& a, cudaStream_t stream) {
+mm_status launch_int8_few_aligned(const Int8Args& a, cudaStream_t stream) {
   switch (a.out_dtype) {
     case MM_F32: return run_few<float>(a, stream);
     case MM_BF16: return run_few<__nv_bfloat16>(a, stream);

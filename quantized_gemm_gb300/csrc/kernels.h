@@ -122,7 +122,8 @@ struct Int8Args {
   const void* bias; int64_t bias_s;            // null = none
   void* y;                   // dense [M, N]
 };
-constexpr int kInt8FewRows = 8, kInt8FewCols = 2;
+constexpr int kInt8FewRows = 8, kInt8LooseRows = 4, kInt8FewCols = 2;
+constexpr int64_t kInt8FewDepth = 8191 * 32 * 16;      // K: a lane's share of int32 sums
 // An operand's copy, f16 or (bytes) int8: dst[r, c] = src[r * rs + c * cs], rows of
 // `ld` values.
 struct Int8Copy {
@@ -179,7 +180,9 @@ mm_status launch_balance_grad(const BalanceGradArgs& args, cudaStream_t stream);
 mm_status launch_quantize_rows(const QuantizeArgs& args, cudaStream_t stream);
 // Few rows against columns of B contiguous along k (16-byte aligned); every
 // stride; the operands' copies for the tensor cores (A f16, B either).
-bool int8_few_supported(const Int8Args& args);
+bool int8_few_aligned(const Int8Args& args);
+mm_status launch_int8_few_aligned(const Int8Args& args, cudaStream_t stream);
+bool int8_few_supported(const Int8Args& args);         // aligned or not
 mm_status launch_int8_few(const Int8Args& args, cudaStream_t stream);
 mm_status launch_int8_any(const Int8Args& args, cudaStream_t stream);
 mm_status launch_int8_copies(const Int8Copy& A, const Int8Copy& B, cudaStream_t stream);

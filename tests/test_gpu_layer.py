@@ -106,7 +106,12 @@ def _check_int8(A, B, sa, sb, bias, dtype, **kw):
     assert Y.dtype == dtype and Y.shape == (A.shape[0], B.shape[1])
     args = [to_np(t).astype(np.float64) if t is not None and t.is_floating_point() else None if t is None else to_np(t)
             for t in (A, B, sa, sb, bias)]
-    assert_within(Y, layer.int8_matmul(*args), layer.int8_matmul_bound(*args, u=U[dtype]), "int8")
+    want, bound = layer.int8_matmul(*args), layer.int8_matmul_bound(*args, u=U[dtype])
+    # What is more than half a step above the type's largest number is infinite (65504 and 65520 for f16).
+    top = torch.finfo(dtype).max * (1 + U[dtype] / 2)
+    past, fits, got = np.abs(want) - bound > top, np.abs(want) + bound < top, to_np(Y)
+    assert (got[past] == np.sign(want[past]) * np.inf).all()
+    assert_within(torch.from_numpy(got[fits]), want[fits], bound[fits], "int8")
     return Y
 
 
@@ -124,6 +129,34 @@ def test_int8(M, K, N, nk, dtype, path):
 def test_int8_sums_at_their_largest(M, path):
     for K in (1024, 9000):
         _check_int8(*(lambda A, B, *r: (A, B.t(), *r))(*_int8_inputs(M, K, 264, F32, 5, bias=False, full=True)), F32)
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8])
+@pytest.mark.parametrize("K", [1, 6, 127, 1023, 1024, 1029, 4099])
+@pytest.mark.parametrize("N", [1, 3, 130, 1157])
+def test_int8_a_few_rows_at_any_address(M, K, N):
+    """Weights as [N, K] and as [K, N], rows of every alignment."""
+    rng = np.random.default_rng(M * K + N)
+    for skip in range(4):
+        A = torch.from_numpy(rng.integers(-128, 128, (M, K + 7)).astype(np.int8)).to(DEV)[:, skip:skip + K]
+        kn = torch.from_numpy(rng.integers(-128, 128, (K, N + 9)).astype(np.int8)).to(DEV)[:, skip:skip + N]
+        nk = torch.from_numpy(rng.integers(-128, 128, (N, K + 5)).astype(np.int8)).to(DEV)[:, skip:skip + K]
+        sa, sb = torch.rand(M, device=DEV), torch.rand(N, device=DEV)
+        dtype = (BF16, F16, F32)[skip % 3]
+        bias = rand_tensor((N,), dtype, skip, DEV)
+        for B in (kn, nk.t(), kn.contiguous(), nk.contiguous().t()):
+            _check_int8(A, B, sa, sb, bias if skip & 1 else None, dtype)
+            assert M > 4 or qg.mm_last_path() == qg.MM_PATH_VECTOR
+
+
+@pytest.mark.parametrize("K", [(1 << 17) - 1, 1 << 17])
+def test_int8_longest_sums_of_a_few_rows_of_kn_weights(K):
+    A = torch.full((2, K), -128, dtype=torch.int8, device=DEV)
+    Y = qg.mm_int8_matmul(A, torch.full((K, 8), -128, dtype=torch.int8, device=DEV), torch.ones(2, device=DEV),
+                          torch.ones(8, device=DEV), dtype=F32)
+    few = qg.mm_last_path() == qg.MM_PATH_VECTOR
+    assert few == (K < 1 << 17)
+    assert float((Y.double() / (2.0 ** 14 * K) - 1).abs().max()) <= (2.0 ** -23 if few else (K / 16 + 1) * 2.0 ** -23)
 
 
 @pytest.mark.parametrize("K", [8191 * 512, 8191 * 512 + 16, 8192 * 512 - 16, 8192 * 512])
