@@ -407,6 +407,19 @@ bool half_scales(const OrthoArgs& o, HalfScales (&k)[MM_ORTHO_MAX_STEPS + 1]) {
 constexpr int64_t kHalfSide = 512;
 bool split_operands(const OrthoArgs& o) { return o.dtype != MM_BF16 || o.M <= kHalfSide || o.N <= kHalfSide; }
 
+// Products whose sum the tensor cores keep before it is added up in fp32.  Their
+// truncation shrinks every step by some 2^-25 an addition, which shows where a fp32
+// result is hardly blurred by small singular values: longer matrices, below 1024.
+// Error relative to fp32 sums' at 256, 128 and 64: 600 x 1000 1.9 and 1.1, 333 x 777 2.3
+// and 1.35, 1800 x 220 3.0, 1.8 and 1.2; 300 x 420 1.85, 512 x 512 0.9, 2048 x 2048 0.6
+// at 256.  A segment costs a hand-over: 8 of 512 x 1000 277 us at 256 and 297 at 128,
+// 2048 x 2048 490 and 610.
+int segment_of(const OrthoArgs& o) {
+  const int64_t m = o.M < o.N ? o.M : o.N, n = o.M < o.N ? o.N : o.M;
+  if (o.dtype != MM_F32 || m >= 1024 || 5 * n < 6 * m) return 256;
+  return n < 6 * m ? 128 : 64;
+}
+
 struct HalfPlan {
   int64_t m, ld, ldm;
   int chunks;
@@ -446,6 +459,7 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
   n.rest = rest;
   n.up = (float)k[0].x;
   const bool split = split_operands(o);
+  const int segment = segment_of(o);
   float* S = split ? reinterpret_cast<float*>(w + p.s) : nullptr;
   n.s = S;
   mm_status s = divide(o, n, st);
@@ -458,6 +472,7 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
     memset(&g, 0, sizeof(g));
     g.sym = 1;
     g.split = split;
+    g.segment = segment;
     g.y_dtype = MM_F16;
     g.y_lo = split;
     g.M = g.N = p.m;
@@ -489,6 +504,7 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
     if (split) {                            // the fp32 state holds X itself
       const double up = last ? (double)o.scale : 1.;
       g.split = 1;
+      g.segment = segment;
       g.s32 = S; g.s_rs = p.ld; g.s_step = xs;
       g.up = (float)k[i + 1].x;
       g.alpha = (float)(up / (k[i].b * k[i].x));

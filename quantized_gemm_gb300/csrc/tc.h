@@ -47,7 +47,8 @@ struct OrthoProduct {
   // split: the operands are pairs (their rests count matrices further); the
   // state s32 is fp32 and takes C's place, holds the result times 1 / up, and
   // Y is the pair of `up` times it, or with y_lo = 0 the result in y_dtype.
-  int split;
+  // Sums of `segment` products along K (a multiple of 64) are added up in fp32.
+  int split, segment;
   float* s32; int64_t s_rs, s_step;
   float up;
 };

@@ -525,18 +525,22 @@ __device__ void run_mma(const TcParams& p, uint32_t sbase, uint32_t tmem, uint32
               tc_mma_tf32(d, ad, bd, p.idesc, 1u);
             }
           } else if constexpr (is_split(MODE)) {
-            // hi*lo and lo*hi, then hi*hi
+            // hi*hi, and beside it hi*lo and lo*hi: the tensor cores truncate every
+            // addition at the size of the sum, so that the small products' additions
+            // cost the large sum nothing (a third of the additions).  The
+            // small sums run on over the tile's segments in both buffers.
+            const uint32_t d2 = d + G::kTileN, acc2 = acc | (kb0 >= 2 * p.kb_per_seg);
             const uint32_t al = sa + G::kLoOff, bl = sb + G::kLoOff;
             const uint64_t adl = amn ? smem_desc_sw128(al + k * 2048, 8192, 1024) : smem_desc_sw128(al + k * 32, 16, 1024);
             const uint64_t bdl = bmn ? smem_desc_sw128(bl + k * 2048, 8192, 1024) : smem_desc_sw128(bl + k * 32, 16, 1024);
             if (PAIR) {
-              tc_mma_f16_pair(d, ad, bdl, idesc, acc);
-              tc_mma_f16_pair(d, adl, bd, idesc, 1u);
-              tc_mma_f16_pair(d, ad, bd, idesc, 1u);
+              tc_mma_f16_pair(d2, ad, bdl, idesc, acc2);
+              tc_mma_f16_pair(d2, adl, bd, idesc, 1u);
+              tc_mma_f16_pair(d, ad, bd, idesc, acc);
             } else {
-              tc_mma_f16(d, ad, bdl, idesc, acc);
-              tc_mma_f16(d, adl, bd, idesc, 1u);
-              tc_mma_f16(d, ad, bd, idesc, 1u);
+              tc_mma_f16(d2, ad, bdl, idesc, acc2);
+              tc_mma_f16(d2, adl, bd, idesc, 1u);
+              tc_mma_f16(d, ad, bd, idesc, acc);
             }
           } else if (PAIR) {
             tc_mma_f16_pair(d, ad, bd, idesc, acc);
@@ -1446,6 +1450,12 @@ __device__ void run_split_epilogue(const TcParams& p, const CUtensorMap* tmC, co
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[c + j] = s == 0 ? __uint_as_float(r[j]) : acc[c + j] + __uint_as_float(r[j]);
+        if (s + 2 >= nseg) {                             // this buffer's sum of the small products
+          tmem_ld32(taddr + TN + c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[c + j] += __uint_as_float(r[j]);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -2580,7 +2590,7 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
   BatchMap om = g.bm;                          // the operands' maps span the rests too
   OperandPlan cmap, ymap;
   if (o.split) {
-    p.kb_per_seg = kSplitSegment / BK;
+    p.kb_per_seg = o.segment / BK;
     om.shape[0] = om.count = 2 * o.count;
     p.a_lo = p.b_lo = o.count;
     p.up = o.up;

@@ -34,7 +34,6 @@ constexpr int kTileK = 64;    // one 128-byte swizzle row of 16-bit elements
 // (high part and rest); the sum goes out as such a pair, or rounded to T.
 enum TcMode { kDense = 0, kGrouped = 1, kQLinear = 2, kGroupedQ = 3, kTF32 = 4, kSkinny = 5, kLowRank = 6, kInt8 = 7, kSym = 8, kState = 9,
               kSymF = 10, kStateF = 11 };
-constexpr int kSplitSegment = 256;
 
 struct TcParams {
   int64_t M, N, K;
