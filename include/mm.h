@@ -456,9 +456,9 @@ mm_status mm_int8_matmul(const mm_tensor* A, const mm_tensor* B, const mm_tensor
  * MM_ERR_INVALID_ARG).  A matrix of zeros gives zeros for eps > 0 and NaN for eps =
  * 0; one that holds an infinity or NaN gives NaN, and touches no other.
  * The norm covers fp32's whole range.  Between the steps X_i is fp32, and on the
- * tensor cores the products' operands are pairs of f16 values (22 bits, scaled so
- * that none leaves the type's range); for bf16 matrices with both sides above 512 the
- * operands are one f16 value (11 bits) and X_i two.
+ * tensor cores the products' operands are pairs of f16 values (22 bits), for bf16
+ * matrices with both sides above 512 one f16 value (11 bits), scaled so that none
+ * overflows; errors are relative to a matrix's norm, not to each value.
  * Workspace: mm_orthogonalize_workspace_size() bytes. */
 #define MM_ORTHO_MAX_STEPS 64
 mm_status mm_orthogonalize_workspace_size(const mm_tensor* X, size_t* bytes);

@@ -112,3 +112,49 @@ def orthogonalize_bound(X, coefficients, eps, scale=1.0, operand=EPS32, output=E
         X = a * X + B @ X
         err = slope * err + 1.1 * local + 4 * EPS32 * (abs(a) * nx + np.linalg.norm(X))
     return abs(scale) * (err * (1 + output) + (output + EPS32) * np.linalg.norm(X)) * 1.01 + 1e-30
+
+
+def _bits(x, bits):
+    """x rounded to `bits` significant bits, ties to even, no limit of range."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(np.ldexp(m, bits)), e - bits)
+
+
+def _truncated_product(A, B, group, segment, bits=24):
+    """A @ B as a sum of exact products of `group` terms, each addition cut towards zero to `bits` significant bits; every
+    `segment` terms the sum so far is added to an fp32 total."""
+    K = A.shape[1]
+    total = np.zeros((A.shape[0], B.shape[1]))
+    for s in range(0, K, segment):
+        acc = np.zeros_like(total)
+        for k in range(s, min(s + segment, K), group):
+            acc = acc + A[:, k:min(k + group, s + segment)] @ B[k:min(k + group, s + segment)]
+            acc = (acc.view(np.int64) & ~((1 << (53 - bits)) - 1)).view(np.float64)
+        total = _bits(total + acc, 24)
+    return total
+
+
+def orthogonalize_emulated(X, coefficients, eps, scale=1.0, parts=2, segment=64):
+    """The chain of orthogonalize with the roundings of the products on the tensor cores, before the rounding of the output:
+    operands of ``parts`` values of 11 bits (the product of two rests left out), truncating sums of 16 products, a state
+    of 24 bits.  Its distance from orthogonalize says how far roundings take a matrix, which the bound above only
+    limits from far away."""
+    tall = X.shape[0] > X.shape[1]
+    X = X.T if tall else X
+    X = _bits(X / (np.sqrt((X * X).sum()) + eps), 24)
+
+    def product(A, B):
+        ah, bh = _bits(A, 11), _bits(B, 11)
+        main = _truncated_product(ah, bh, 16, segment if parts == 2 else A.shape[1] + 16)
+        return main if parts == 1 else main + ah @ _bits(B - bh, 11) + _bits(A - ah, 11) @ bh
+
+    for a, b, c in coefficients:
+        A = _bits(product(X, X.T), 11 * parts)
+        B = _bits(b * A + c * product(A, A), 11 * parts)
+        X = _bits(a * X + product(B, X), 24)
+    return scale * (X.T if tall else X)
+
+
+def half_steps(x, u):
+    """Half a step of a type with unit roundoff u at each value of x: the most that rounding x can change it."""
+    return u * np.ldexp(1.0, np.frexp(x)[1] - 1) * (x != 0)

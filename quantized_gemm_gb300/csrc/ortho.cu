@@ -32,8 +32,8 @@ struct NormArgs {
   FastDiv fd_row;                    // pieces (or elements) of a row
   double* part;                      // [count][chunks] sums of squares
   float eps;
-  float* s;                          // [count][M][ld], the divided matrix, and
-  __half* h;                         // that times `up` as f16 [count][M][ld] and, `rest` further, what that leaves (NULL: not wanted)
+  float* s;                          // [count][M][ld], the divided matrix,
+  __half* h;                         // that times `up` as f16 [count][M][ld] (NULL: not wanted) and, `rest` further, what that leaves (0: not wanted)
   int64_t ld, rest;
   float up;
 };
@@ -144,19 +144,18 @@ __global__ void __launch_bounds__(kThreads) divide_kernel(const NormArgs a) {
       }
       if constexpr (E == 8) {
         *reinterpret_cast<uint4*>(a.h + at) = *reinterpret_cast<const uint4*>(h);
-        *reinterpret_cast<uint4*>(a.h + a.rest + at) = *reinterpret_cast<const uint4*>(l);
+        if (a.rest) *reinterpret_cast<uint4*>(a.h + a.rest + at) = *reinterpret_cast<const uint4*>(l);
       } else if constexpr (E == 4) {
         *reinterpret_cast<uint2*>(a.h + at) = *reinterpret_cast<const uint2*>(h);
-        *reinterpret_cast<uint2*>(a.h + a.rest + at) = *reinterpret_cast<const uint2*>(l);
+        if (a.rest) *reinterpret_cast<uint2*>(a.h + a.rest + at) = *reinterpret_cast<const uint2*>(l);
       } else {
 #pragma unroll
         for (int j = 0; j < E; ++j) {
           a.h[at + j] = h[j];
-          a.h[a.rest + at + j] = l[j];
+          if (a.rest) a.h[a.rest + at + j] = l[j];
         }
       }
     }
-    if (!a.s) return;
     if constexpr (E >= 4) {
 #pragma unroll
       for (int j = 0; j < E; j += 4) *reinterpret_cast<float4*>(a.s + at + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
@@ -340,20 +339,19 @@ mm_status run_float(const OrthoArgs& o, void* ws, cudaStream_t st) {
 //
 // The products' operands are f16 (11 bits; X, A and B each rounded once a step),
 // their sums fp32.  What is rounded to 11 bits only enters the correction (b A + c A A) X;
-// a X itself comes from the state, which is held as two f16 parts (22 bits), since
-// the iteration magnifies small singular values by a in every step and the state's
-// rounding with them: with the state rounded to 11 bits the result was off by 4e-2
-// for matrices with a few strong directions, so it is off by 1.7e-3 (one rounding of
-// a bf16 output) for those and 2.2e-3 for random ones.  Each array has a power of
-// two of its own, the largest that cannot overflow: the singular values start at
-// 1 at most and the polynomial's maximum bounds every later step's, so that f16's
-// range is used from the top (a value below 2^-29 of the bound loses digits of its
-// high part, below 2^-39 the pair has none).
+// a X itself comes from the state, which is fp32, since the iteration magnifies small
+// singular values by a in every step and the state's rounding with them (a state rounded
+// to 11 bits: off by 4e-2 for matrices with a few strong directions), and since X_0 is
+// as small as the norm is beside eps, matrix by matrix.  A value that is too small for
+// the operands (below 2^-39 of the array's bound) lacks its correction, which is as small
+// beside a X.  Each array has a power of two of its own, the largest that cannot
+// overflow: the singular values start at 1 at most and the polynomial's maximum bounds
+// every later step's, so that f16's range is used from the top.
 // A and B are symmetric: only the lower triangle's tiles are computed.
 //
 // fp32 and f16 matrices, and bf16 ones up to kHalfSide, take the same chain with
-// every operand split into two f16 values (22 bits) and three products each, and a
-// state in fp32 beside them.  (Three tf32 products of fp32 operands took 1.49 ms for
+// every operand split into two f16 values (22 bits) and three products each.
+// (Three tf32 products of fp32 operands took 1.49 ms for
 // 2048 x 2048 and were off by 1.8e-5: their additions truncate, 3 K / 8 times a sum;
 // see kSymF.)  An f16 result would be off by 2.1e-3 with 11-bit operands, ten times
 // its own rounding; a bf16 one is off by 1.2 to 1.4 times its rounding from 512 rows
@@ -431,14 +429,15 @@ HalfPlan plan_half(const OrthoArgs& o) {
   p.ld = round_up(o.N, 8);
   p.ldm = round_up(p.m, 8);
   p.chunks = norm_chunks(o.M, o.N, o.bm.count);
-  const size_t x = align256((size_t)o.bm.count * o.M * p.ld * 4), sq = align256((size_t)o.bm.count * p.m * p.ldm * (split_operands(o) ? 4 : 2));
+  const size_t size = split_operands(o) ? 4 : 2;       // of an operand's value
+  const size_t x = align256((size_t)o.bm.count * o.M * p.ld * size), sq = align256((size_t)o.bm.count * p.m * p.ldm * size);
   p.part = 0;
   p.x[0] = align256((size_t)o.bm.count * p.chunks * 8);
   p.x[1] = p.x[0] + x;
   p.a = p.x[1] + x;
   p.b = p.a + sq;
   p.s = p.b + sq;
-  p.bytes = p.s + (split_operands(o) ? x : 0);
+  p.bytes = p.s + align256((size_t)o.bm.count * o.M * p.ld * 4);
   return p;
 }
 
@@ -453,14 +452,14 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
   if (!status) return MM_ERR_CUDA;
   const HalfPlan p = plan_half(o);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const int64_t xs = o.M * p.ld, rest = o.bm.count * xs, as = p.m * p.ldm;
+  const int64_t xs = o.M * p.ld, as = p.m * p.ldm;
   NormArgs n = norm_args(o, p.chunks, w + p.part, p.ld);
   n.h = reinterpret_cast<__half*>(w + p.x[0]);
-  n.rest = rest;
-  n.up = (float)k[0].x;
   const bool split = split_operands(o);
   const int segment = segment_of(o);
-  float* S = split ? reinterpret_cast<float*>(w + p.s) : nullptr;
+  float* S = reinterpret_cast<float*>(w + p.s);
+  n.rest = split ? o.bm.count * xs : 0;
+  n.up = (float)k[0].x;
   n.s = S;
   mm_status s = divide(o, n, st);
   const bool tall = o.M > o.N;
@@ -474,7 +473,6 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
     g.split = split;
     g.segment = segment;
     g.y_dtype = MM_F16;
-    g.y_lo = split;
     g.M = g.N = p.m;
     g.K = tall ? o.M : o.N;
     g.count = o.bm.count;
@@ -488,7 +486,6 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
     g.K = p.m;
     g.a = g.b = g.c = A;
     g.a_step = g.b_step = g.c_step = as;
-    g.c_lo = split ? o.bm.count * as : 0;
     g.a_rs = g.b_cs = g.c_rs = p.ldm;
     g.a_cs = g.b_rs = 1;
     g.y = B;
@@ -501,25 +498,18 @@ mm_status run_half(const OrthoArgs& o, const HalfScales* k, void* ws, cudaStream
     g.a = tall ? X : B; g.a_step = tall ? xs : as; g.a_rs = tall ? p.ld : p.ldm; g.a_cs = 1;
     g.b = tall ? B : X; g.b_step = tall ? as : xs; g.b_rs = tall ? p.ldm : p.ld; g.b_cs = 1;
     const bool last = i + 1 == o.steps;
-    if (split) {                            // the fp32 state holds X itself
-      const double up = last ? (double)o.scale : 1.;
-      g.split = 1;
-      g.segment = segment;
-      g.s32 = S; g.s_rs = p.ld; g.s_step = xs;
-      g.up = (float)k[i + 1].x;
-      g.alpha = (float)(up / (k[i].b * k[i].x));
-      g.beta = (float)(up * a);
-    } else {
-      const double up = last ? (double)o.scale : k[i + 1].x;
-      g.c = X; g.c_rs = p.ld; g.c_step = xs; g.c_lo = rest;
-      g.alpha = (float)(up / (k[i].b * k[i].x));
-      g.beta = (float)(up * a / k[i].x);
-    }
+    const double up = last ? (double)o.scale : 1.;      // the state holds X itself
+    g.split = split;
+    g.segment = segment;
+    g.last = last;
+    g.s32 = S; g.s_rs = p.ld; g.s_step = xs;
+    g.up = (float)k[i + 1].x;
+    g.alpha = (float)(up / (k[i].b * k[i].x));
+    g.beta = (float)(up * a);
     g.y_dtype = last ? o.dtype : MM_F16;
     g.y = last ? o.out : w + p.x[(i + 1) & 1];
     g.y_rs = last ? o.N : p.ld;
     g.y_step = last ? o.M * o.N : xs;
-    g.y_lo = last ? 0 : 1;
     s = launch_tc_ortho(g, status, st);
   }
   return finish(s, MM_PATH_TENSOR);

@@ -34,23 +34,21 @@ mm_status launch_int8_stream(const Int8Args& q, const void* x, int64_t ldx, int 
 
 // A product of the orthogonalised update's chain, over `count` matrices of f16
 // operands: sym != 0, Y = f16(alpha A B + beta C), symmetric (C optional); else
-// the state's step alpha A B + beta (C + its rest c_lo further), out as f16 and
-// the rest y_lo matrices further, or with y_lo = 0 rounded to y_dtype.
+// the state's step S = alpha A B + beta S in fp32, in place, with Y = f16(up S);
+// the last step rounds its result to y_dtype instead and leaves S as it was.
 struct OrthoProduct {
-  int sym, y_dtype;
+  int sym, last, y_dtype;
   int64_t M, N, K, count;
   const void* a; int64_t a_rs, a_cs, a_step;
   const void* b; int64_t b_rs, b_cs, b_step;
-  const void* c; int64_t c_rs, c_step, c_lo;
-  void* y; int64_t y_rs, y_step, y_lo;
+  const void* c; int64_t c_rs, c_step;
+  void* y; int64_t y_rs, y_step;
   float alpha, beta;
-  // split: the operands are pairs (their rests count matrices further); the
-  // state s32 is fp32 and takes C's place, holds the result times 1 / up, and
-  // Y is the pair of `up` times it, or with y_lo = 0 the result in y_dtype.
-  // Sums of `segment` products along K (a multiple of 64) are added up in fp32.
-  int split, segment;
   float* s32; int64_t s_rs, s_step;
   float up;
+  // split: operands, C and f16 results are pairs, their rests count matrices further.
+  // Sums of `segment` products along K (a multiple of 64) are added up in fp32.
+  int split, segment;
 };
 mm_status launch_tc_ortho(const OrthoProduct& g, unsigned* status, cudaStream_t stream);
 

@@ -51,8 +51,8 @@
 //   kInt8     kDense over f16 copies of int8 operands; epilogue
 //             y = (acc * a_scale[m]) * b_scale[n] + bias[n], rounded once.
 //   kSym      kDense with a symmetric result: the lower triangle's tiles only.
-//   kState    kDense plus a state held in two f16 parts.
-//   kSymF, kStateF  the same with three f16 products of split operands and a state in fp32.
+//   kState    kDense plus a state in fp32.
+//   kSymF, kStateF  the same with three f16 products of split operands.
 //   kSkinny   kDense for at most 64 rows of A': 256-column tiles whose
 //             k-blocks are split over the CTAs of a cluster (non-persistent,
 //             one tile per cluster), so that B' streams through every SM with
@@ -104,7 +104,7 @@ struct Geo {
   static constexpr int kStageBytes = (kABytes + kBBytes) * (kLoOff ? 2 : 1);
   // kGroupedQ gives one stage's worth of shared memory to its int8 staging ring.
   static constexpr int kStages =
-      is_split(MODE) ? (PAIR ? 3 : 2) : kLoOff ? (PAIR ? 3 : 2) : is_ortho(MODE) ? 5 : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
+      kLoOff ? (PAIR ? 3 : 2) : is_ortho(MODE) ? 5 : PAIR ? (MODE == kGroupedQ ? 5 : 6) : MODE == kSkinny ? 5 : 4;
   static constexpr int kTileRows = PAIR ? 2 * BM : BM;  // output rows per (pair) tile
   static constexpr int kRingBytes = kStages * kStageBytes;
 };
@@ -129,7 +129,7 @@ constexpr int64_t kPairMinK = 1024;              // CTA pairs for K >= this
 constexpr uint32_t kTmemCols = 512;
 constexpr int kCtrlBytes = 256;                  // mbarriers, TMEM slot, abort flag
 constexpr int kStageWords = 32 * 16;             // float per-warp output staging: 32 rows x 64 bytes
-constexpr int kBoxBytes = 32 * 128;              // kSym, kState: a warp's 32 rows x 64 columns, and the rest of them
+constexpr int kBoxBytes = 32 * 128;              // kSym to kStateF: a warp's slots, 32 rows of 64 f16 or 32 fp32 values
 
 // Shape of the CTA: 16 epilogue warps of 64 columns each, enough warps to hide
 // the epilogue's latency (short-K float products, the QLinear requantisation).
@@ -1504,7 +1504,7 @@ __device__ void run_split_epilogue(const TcParams& p, const CUtensorMap* tmC, co
     const bool live = quad * 32 < rows_t && c0 < p.N;
     bool result = false;
     if constexpr (MODE == kStateF) {
-      result = p.y_lo == 0;
+      result = p.last;
       if (result && !p.out_f32) {                        // rounded to 16 bits, in the first slot
         uint32_t w[kCols / 2];
 #pragma unroll
@@ -1605,10 +1605,13 @@ __device__ void run_split_epilogue(const TcParams& p, const CUtensorMap* tmC, co
 
 // ------------------------------------------------------------------ epilogue of kSym and kState
 
-// 8 warps of 128 columns.  C (and, for kState, its rest) arrives by TMA as 32 x 64
-// boxes, 128-byte swizzled, in the warp's two slots, the next box while the
+// 8 warps of 128 columns.  kSym's C arrives by TMA as 32 x 64 boxes, kState's fp32
+// state as two of 32 x 32, 128-byte swizzled, in the warp's slots, the next while the
 // accumulators of a tile are awaited or the box before is on its way out; the
-// results replace it in place and leave by TMA, a row of a box being 128 bytes.
+// results replace it in place and leave by TMA, a row of a box being 128 bytes.  kState's
+// f16 values follow through the first slot once the state has left it (a third slot
+// for them, and a stage less: 1466 us for 32 x 2048 x 1024 instead of 1424; with the
+// state as two f16 values, without the fp32 range, 1245).
 // (With 64-byte rows and C read from memory row by row the copy engine and the load
 // pipe held a tile for 16 us: 222 us a step of 32 x 2048 x 1024 instead of 130.)
 template <int MODE, bool PAIR>
@@ -1621,9 +1624,10 @@ __device__ void run_ortho_epilogue(const TcParams& p, const CUtensorMap* tmC, co
   const uint32_t rank = PAIR ? (cluster_ctarank() & 1) : 0;
   const int row_off = PAIR ? (int)rank * BM : 0;
   const uint32_t rel0 = PAIR ? mapa_shared(acce0, 0) : acce0, tlane = (uint32_t)(quad * 32) << 16;
-  const uint32_t hi = smem_u32(stage), lo = hi + kBoxBytes, mine = (uint32_t)lane * 128;
+  const uint32_t slot0 = smem_u32(stage), slot1 = slot0 + kBoxBytes, mine = (uint32_t)lane * 128;
+  const auto piece = [&](int q) { return mine + (((uint32_t)(q & 7) ^ ((uint32_t)lane & 7u)) << 4); };
   const int64_t total = total_tiles<MODE>(p);
-  const bool has_c = p.c != nullptr;
+  const bool has_c = MODE == kState || p.c != nullptr;
   const auto fetch = [&](const Tile& ti, int h) {
     if (!has_c) return;
     if (lane == 0) bulk_wait_read_all();                 // the slots' last stores have read them
@@ -1632,8 +1636,8 @@ __device__ void run_ortho_epilogue(const TcParams& p, const CUtensorMap* tmC, co
     if (lane == 0) {
       const int32_t c0 = (int32_t)ti.n0 + slice * kCols + 64 * h, r0 = (int32_t)ti.m0 + row_off + quad * 32;
       mbar_arrive_expect_tx(cbar, MODE == kState ? 2 * kBoxBytes : kBoxBytes);
-      tma_load_3d(hi, tmC, c0, r0, (int32_t)ti.batch, cbar);
-      if (MODE == kState) tma_load_3d(lo, tmC, c0, r0, (int32_t)(ti.batch + p.c_lo), cbar);
+      tma_load_3d(slot0, tmC, c0, r0, (int32_t)ti.batch, cbar);
+      if (MODE == kState) tma_load_3d(slot1, tmC, c0 + 32, r0, (int32_t)ti.batch, cbar);
     }
   };
   uint32_t seg = 0, cphase = 0;
@@ -1678,62 +1682,65 @@ __device__ void run_ortho_epilogue(const TcParams& p, const CUtensorMap* tmC, co
         }
         cphase ^= 1;
       }
-      // This lane's row: 8 pieces of 8 columns.
-      uint32_t w[32], rest[32];
+      // This lane's row of 64 columns.
+      uint32_t w[32];
+      if constexpr (MODE == kState) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const uint32_t at = mine + (((uint32_t)q ^ ((uint32_t)lane & 7u)) << 4);
-        float v[8];
+        for (int q = 0; q < 16; ++q) {
+          const uint32_t at = (q < 8 ? slot0 : slot1) + piece(q);
+          const uint4 u = lds128(at);
+          const float s[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+          float v[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = p.alpha * __uint_as_float(r[q >> 2][(q & 3) * 8 + e]);
-        if (has_c) {
-          const uint4 a = lds128(hi + at);
-          const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-          float2 c[4];
+          for (int e = 0; e < 4; ++e) v[e] = __fmaf_rn(p.beta, s[e], p.alpha * __uint_as_float(r[q >> 3][(q & 7) * 4 + e]));
+          if (!p.last) {
+            sts128(at, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c[e] = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
-          if constexpr (MODE == kState) {
-            const uint4 b = lds128(lo + at);
-            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+            for (int e = 0; e < 4; ++e) v[e] *= p.up;
+          }
+          w[2 * q] = pack2(v[0], v[1], p.out_f16);
+          w[2 * q + 1] = pack2(v[2], v[3], p.out_f16);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = p.alpha * __uint_as_float(r[q >> 2][(q & 3) * 8 + e]);
+          if (has_c) {
+            const uint4 a = lds128(slot0 + piece(q));
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&bw[e]));
-              c[e].x += l.x;
-              c[e].y += l.y;
+              const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
+              v[2 * e] = __fmaf_rn(p.beta, c.x, v[2 * e]);
+              v[2 * e + 1] = __fmaf_rn(p.beta, c.y, v[2 * e + 1]);
             }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __fmaf_rn(p.beta, c[e].x, v[2 * e]);
-            v[2 * e + 1] = __fmaf_rn(p.beta, c[e].y, v[2 * e + 1]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[4 * q + e] = pack2(v[2 * e], v[2 * e + 1], p.out_f16);
-          if constexpr (MODE == kState) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[4 * q + e]));
-            rest[4 * q + e] = pack2(v[2 * e] - f.x, v[2 * e + 1] - f.y, 1);
-          }
+          for (int e = 0; e < 4; ++e) w[4 * q + e] = pack2(v[2 * e], v[2 * e + 1], 1);
         }
       }
       const int32_t c0 = (int32_t)ti.n0 + slice * kCols + 64 * h;
       const bool live = quad * 32 < rows_t && c0 < p.N;
+      if (MODE == kState && !p.last) {
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0 && live) {
+          tma_store_3d(tmC, slot0, c0, row0, (int32_t)ti.batch);
+          if (c0 + 32 < p.N) tma_store_3d(tmC, slot1, c0 + 32, row0, (int32_t)ti.batch);
+          bulk_commit();
+        }
+      }
       if (lane == 0) bulk_wait_read_all();
       __syncwarp();                                      // every lane has read its row of C
       if (p.y_tma) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t at = mine + (((uint32_t)q ^ ((uint32_t)lane & 7u)) << 4);
-          sts128(hi + at, make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
-          if (MODE == kState && p.y_lo != 0)
-            sts128(lo + at, make_uint4(rest[4 * q], rest[4 * q + 1], rest[4 * q + 2], rest[4 * q + 3]));
-        }
+        for (int q = 0; q < 8; ++q) sts128(slot0 + piece(q), make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0 && live) {
-          tma_store_3d(tmY, hi, c0, row0, (int32_t)ti.batch);
-          if (MODE == kState && p.y_lo != 0) tma_store_3d(tmY, lo, c0, row0, (int32_t)(ti.batch + p.y_lo));
+          tma_store_3d(tmY, slot0, c0, row0, (int32_t)ti.batch);
           bulk_commit();
         }
       } else if (live) {                                 // the result, in rows that TMA does not take
@@ -1750,7 +1757,7 @@ __device__ void run_ortho_epilogue(const TcParams& p, const CUtensorMap* tmC, co
       }
       if constexpr (MODE == kSym) {
         // Transposed, where that falls into a tile that is not computed, through the
-        // slot that kState has its rests in.
+        // second slot.
         if (live && (row0 / BN) * BN > (c0 / TR) * TR + TR - 1) {
           uint32_t* turn = stage + kBoxBytes / 4;
 #pragma unroll
@@ -2578,30 +2585,26 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
   p.y_vec = (reinterpret_cast<uintptr_t>(o.y) & 15) == 0 && o.y_rs % vec == 0 && (o.y_step % vec == 0 || o.count == 1);
   p.alpha = o.alpha;
   p.beta = o.beta;
-  if (o.c) {
-    p.c = o.c;
-    p.c_rs = o.c_rs; p.c_cs = 1; p.c_vec = 1;
-    p.c_bstride[0] = o.c_step;
-    p.c_lo = o.c_lo;
-  }
+  p.c = o.c;                                   // (kSym, kSymF: whether there is one)
   p.status = status;
   const int mode = o.split ? (o.sym ? kSymF : kStateF) : o.sym ? kSym : kState;
-  p.y_lo = o.y_lo ? o.count : 0;
+  p.last = o.last;
+  p.up = o.up;
+  const bool pairs = o.split && !o.last;
+  p.y_lo = pairs ? o.count : 0;
   BatchMap om = g.bm;                          // the operands' maps span the rests too
   OperandPlan cmap, ymap;
   if (o.split) {
     p.kb_per_seg = o.segment / BK;
     om.shape[0] = om.count = 2 * o.count;
-    p.a_lo = p.b_lo = o.count;
-    p.up = o.up;
+    p.a_lo = p.b_lo = p.c_lo = o.count;
   }
-  p.c_lo = o.sym && !o.split ? 0 : o.count;
-  p.y_tma = plan_boxes(o.y, o.y_dtype, g.M, g.N, o.y_rs, o.y_step, o.y_lo ? 2 * o.count : o.count, &ymap);
-  if ((o.sym || o.y_lo) && !p.y_tma) return MM_ERR_UNSUPPORTED;
-  // C as it is held, or kStateF's state.
+  p.y_tma = plan_boxes(o.y, o.y_dtype, g.M, g.N, o.y_rs, o.y_step, pairs ? 2 * o.count : o.count, &ymap);
+  if (!o.last && !p.y_tma) return MM_ERR_UNSUPPORTED;
+  // C, or the state.
   const bool have_c = o.s32 || o.c;
   if (have_c && !(o.s32 ? plan_boxes(o.s32, MM_F32, g.M, g.N, o.s_rs, o.s_step, o.count, &cmap)
-                        : plan_boxes(o.c, MM_F16, g.M, g.N, o.c_rs, o.c_step, p.c_lo ? 2 * o.count : o.count, &cmap)))
+                        : plan_boxes(o.c, MM_F16, g.M, g.N, o.c_rs, o.c_step, pairs ? 2 * o.count : o.count, &cmap)))
     return MM_ERR_UNSUPPORTED;
   const int64_t as[kMaxBatchDims] = {o.a_step}, bs[kMaxBatchDims] = {o.b_step};
   // Pairs of CTAs read a third less per tile (a split k-block is 48 KB a CTA against 64).

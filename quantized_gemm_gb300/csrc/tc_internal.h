@@ -30,8 +30,8 @@ constexpr int kTileK = 64;    // one 128-byte swizzle row of 16-bit elements
 // kSym: a dense f16 product whose result is symmetric (M = N): only the tiles
 // that touch the lower triangle are computed, and their 32 x 32 boxes are also
 // stored transposed where the tile on the other side was left out.
-// kState: a dense f16 product plus beta times a state held as two f16 values
-// (high part and rest); the sum goes out as such a pair, or rounded to T.
+// kState: a dense f16 product plus beta times a state in fp32; the sum takes the
+// state's place and goes out as f16, or goes out rounded to T (p.last).
 enum TcMode { kDense = 0, kGrouped = 1, kQLinear = 2, kGroupedQ = 3, kTF32 = 4, kSkinny = 5, kLowRank = 6, kInt8 = 7, kSym = 8, kState = 9,
               kSymF = 10, kStateF = 11 };
 
@@ -71,9 +71,10 @@ struct TcParams {
   int64_t c_bstride[kMaxBatchDims];
   int64_t c_rs, c_cs, c_gs;                    // c_gs: grouped bias row stride per group
   int c_vec, c_live;                           // c_live: C is Y
-  int64_t c_lo, y_lo;                          // kSym to kStateF: from the high part to the rest (batch coordinates; 0: none)
+  int64_t c_lo, y_lo;                          // kSymF, kStateF: from the high part to the rest (batch coordinates; 0: none)
+  int last;                                    // kState, kStateF: Y is the result, the state is not needed again
   int64_t a_lo, b_lo;                          // kSymF, kStateF: batch coordinates from the operands' high parts to their rests
-  float up;                                    // Y's pair is `up` times the new state
+  float up;                                    // Y (kStateF: its pair) is `up` times the new state
   int c_late, c_f32;                           // kSkinny: GemmArgs::c_late, c_f32
   // QLinear epilogue: zero-point correction from the operand sums, then requantisation
   VecView sa, sb, za, zb;

@@ -1,0 +1,74 @@
+"""The orthogonalised update over its range of values, against the formula in 64 bits.
+
+How far a result may be off is worked out for each matrix, not limited from far away: half a step of its type at every value
+(the output's rounding), plus what the stated roundings of operands, sums and state do to this matrix in an emulation on
+the CPU (oracle.layer.orthogonalize_emulated).  The kernels' roundings are others of the same size, so twice the emulated
+distance is allowed where the operands' 11 bits set it, and four times where the truncation of the tensor cores' sums does,
+whose spare bits are not documented.  Each 32 x 32 box is held to the same with a factor of 3 more for what it
+may stand out from the rest, so that a lost or misplaced box fails."""
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_gemm_gb300 as qg
+from helpers import rand_tensor, to_np
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+U = {BF16: 2.0 ** -8, F16: 2.0 ** -11, F32: 2.0 ** -24}
+MUON = (3.4445, -4.7750, 2.0315)
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    qg.mm_get_device_status()
+    yield
+    assert qg.mm_get_device_status() == "MM_OK"
+
+
+def _box_norms(x):
+    p = np.pad(x * x, [(0, -n % 32) for n in x.shape])
+    return np.sqrt(p.reshape(p.shape[0] // 32, 32, p.shape[1] // 32, 32).sum(axis=(1, 3)))
+
+
+def check(got, X, coefficients, eps=1e-7, scale=1.0):
+    """One matrix X (fp64 of the input's values) and its result."""
+    parts = 1 if got.dtype == BF16 and min(X.shape) > 512 else 2
+    y, u = to_np(got), U[got.dtype]
+    want = layer.orthogonalize(X, coefficients, eps, scale)
+    off = np.linalg.norm(layer.orthogonalize_emulated(X, coefficients, eps, scale, parts) - want)
+    off = (2 if parts == 1 else 4) * off + 8 * 2.0 ** -24 * np.linalg.norm(want)
+    assert np.isfinite(y).all()
+    err, bound = np.linalg.norm(y - want), np.linalg.norm(layer.half_steps(want, u)) + off
+    assert err <= bound, "off by %g of the bound, %g of the result" % (err / bound, err / np.linalg.norm(want))
+    share = np.sqrt(min(1.0, 1024 / want.size))
+    over = _box_norms(y - want) / (_box_norms(layer.half_steps(want, u)) + 3 * off * share + 1e-300)
+    worst = float(over.max())
+    assert worst <= 1.0, "box %s is off by %g of its bound" % (np.unravel_index(over.argmax(), over.shape), worst)
+
+
+def strong(shape, seed):
+    """A few directions far above the rest: the iteration magnifies what is small, and rounding of the state with it."""
+    g = torch.Generator().manual_seed(seed)
+    X = 0.02 * torch.randn(shape, generator=g)
+    for i in range(6):
+        X += 0.5 ** i * torch.randn(shape[:-1] + (1,), generator=g) @ torch.randn(shape[:-2] + (1,) + shape[-1:], generator=g)
+    return X
+
+
+# ------------------------------------------------------------------ norms far below eps
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("shape", [(520, 777), (600, 514), (40, 64), (200, 330)])
+def test_matrices_of_a_stack_whose_norms_are_far_apart(shape, dtype):
+    """Expert gradients that have died away: X / (norm + eps) is then far below 1, beside others that are 1."""
+    sizes = [1.0, 1e-7, 1e-13, 1e-14, 1e-15, 1e-16, 1e-20]
+    X = rand_tensor((len(sizes),) + shape, F32, 5, "cpu").double()
+    X = (X / X.pow(2).sum(dim=(1, 2), keepdim=True).sqrt() * torch.tensor(sizes, dtype=torch.float64)[:, None, None]).to(dtype)
+    got = qg.mm_orthogonalize(X.to(DEV))
+    for x, y in zip(to_np(X), got):
+        check(y, x, [MUON] * 5)
