@@ -459,6 +459,10 @@ mm_status mm_int8_matmul(const mm_tensor* A, const mm_tensor* B, const mm_tensor
  * tensor cores the products' operands are pairs of f16 values (22 bits), for bf16
  * matrices with both sides above 512 one f16 value (11 bits), scaled so that none
  * overflows; errors are relative to a matrix's norm, not to each value.
+ * Coefficients under which the singular values' bound (1 at first, with 2 % for
+ * roundings in every step) leaves 1e-6 to 1e6, or b A + c A A outweighs a by more
+ * than 2^12, take fp32 products instead, as mm_matmul's: a schedule that is steep
+ * just above 1 does so after a few steps, and is several times slower there.
  * Workspace: mm_orthogonalize_workspace_size() bytes. */
 #define MM_ORTHO_MAX_STEPS 64
 mm_status mm_orthogonalize_workspace_size(const mm_tensor* X, size_t* bytes);

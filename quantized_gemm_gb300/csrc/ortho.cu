@@ -359,8 +359,7 @@ mm_status run_float(const OrthoArgs& o, void* ws, cudaStream_t st) {
 // (us for 512 x 512, 256 x 256, 8 of 512 x 1000: 148 113 204, split 178 126 267).
 
 double power_below(double x) {
-  if (x > 0x1p30) return 0x1p30;         // infinite where the array is zeros
-  if (!(x > 0x1p-60)) return 0x1p-60;    // (the bounds are then out of range)
+  if (x > 0x1p60) return 0x1p60;         // infinite where the array is zeros
   return std::ldexp(1., (int)std::floor(std::log2(x)));
 }
 // The largest |f| of f(s) = s (a + b s^2 + c s^4) on [0, u], and of b l + c l^2 on [0, u^2].
@@ -387,18 +386,23 @@ double even_bound(double b, double c, double u) {
 struct HalfScales { double x, a, b; };       // powers of two of X, A, B in a step
 constexpr double kHalfTop = 32768.;
 constexpr double kSlack = 1.02;              // what the roundings may add to a bound
-// False where the bounds leave the range that the scales cover.
+// False where the bounds leave the range that the scales cover, and where a step's
+// product outweighs a X by so much that it counts for singular values whose squares are
+// lost in the operands: those below 2^-20 of the bound u are, and for s = 2^-20 u the
+// correction (b s^2 + c s^4) X is at most 2^-28 of a X under this limit.
 bool half_scales(const OrthoArgs& o, HalfScales (&k)[MM_ORTHO_MAX_STEPS + 1]) {
   double u = kSlack;
-  for (int i = 0; i <= o.steps; ++i) {
-    if (!(u < 1e6)) return false;
-    k[i].x = power_below(kHalfTop / u);
-    if (i == o.steps) break;
+  for (int i = 0; i < o.steps; ++i) {
     const float* c = o.coef + 3 * i;
-    k[i].a = power_below(kHalfTop / (u * u));
-    k[i].b = power_below(kHalfTop / (kSlack * even_bound(c[1], c[2], u)));
+    const double u2 = u * u, even = kSlack * even_bound(c[1], c[2], u);
+    if ((u != 0. && !(u > 1e-6 && u < 1e6)) || !(even < 1e18)) return false;
+    if (std::fabs(c[0]) < 0x1p-12 * (std::fabs(c[1]) + std::fabs(c[2]) * u2) * u2) return false;
+    k[i].x = power_below(kHalfTop / u);
+    k[i].a = power_below(kHalfTop / u2);
+    k[i].b = power_below(kHalfTop / even);
     u = kSlack * odd_bound(c[0], c[1], c[2], u);
   }
+  k[o.steps] = {1., 1., 1.};
   return true;
 }
 

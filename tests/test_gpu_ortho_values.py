@@ -34,13 +34,13 @@ def _box_norms(x):
     return np.sqrt(p.reshape(p.shape[0] // 32, 32, p.shape[1] // 32, 32).sum(axis=(1, 3)))
 
 
-def check(got, X, coefficients, eps=1e-7, scale=1.0):
-    """One matrix X (fp64 of the input's values) and its result."""
-    parts = 1 if got.dtype == BF16 and min(X.shape) > 512 else 2
+def check(got, X, coefficients, eps=1e-7, scale=1.0, form=None):
+    """One matrix X (fp64 of the input's values) and its result; ``form``: of the products, where it is not the usual one."""
+    form = form or ("single" if got.dtype == BF16 and min(X.shape) > 512 else "pairs")
     y, u = to_np(got), U[got.dtype]
     want = layer.orthogonalize(X, coefficients, eps, scale)
-    off = np.linalg.norm(layer.orthogonalize_emulated(X, coefficients, eps, scale, parts) - want)
-    off = (2 if parts == 1 else 4) * off + 8 * 2.0 ** -24 * np.linalg.norm(want)
+    off = np.linalg.norm(layer.orthogonalize_emulated(X, coefficients, eps, scale, form) - want)
+    off = (2 if form == "single" else 4) * off + 8 * 2.0 ** -24 * np.linalg.norm(want)
     assert np.isfinite(y).all()
     err, bound = np.linalg.norm(y - want), np.linalg.norm(layer.half_steps(want, u)) + off
     assert err <= bound, "off by %g of the bound, %g of the result" % (err / bound, err / np.linalg.norm(want))
@@ -72,3 +72,19 @@ def test_matrices_of_a_stack_whose_norms_are_far_apart(shape, dtype):
     got = qg.mm_orthogonalize(X.to(DEV))
     for x, y in zip(to_np(X), got):
         check(y, x, [MUON] * 5)
+
+
+# ------------------------------------------------------------------ coefficients
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("shape", [(520, 600), (200, 330), (40, 64)])
+@pytest.mark.parametrize("steps,coefficients", [(3, (0.0, 1.0, 0.0)), (2, (0.0, 0.0, 1.0)), (5, (1e-3, 0.0, 0.0)),
+                                                (4, (1e-4, 1e-5, 0.0)), (6, (0.02, 0.9, 0.0)), (2, (0.0, 0.0, 0.0))])
+def test_coefficients_that_shrink(shape, dtype, steps, coefficients):
+    """Singular values that end far below their bound, without a term a X to carry them or with a small one: the chain
+    of MatMul's products, in fp32."""
+    X = rand_tensor(shape, dtype, 21, DEV)
+    Y = qg.mm_orthogonalize(X, steps, coefficients)
+    fp32 = qg.mm_last_path() == qg.MM_PATH_TENSOR and coefficients[0] < 0.01 and any(coefficients)
+    check(Y, to_np(X), [coefficients] * steps, form="matmul" if fp32 else None)
