@@ -58,13 +58,14 @@ struct Squares {
 
 // d = |X|_F + eps as m 2^k: a product with the rounded 1 / d where that is in
 // fp32's middle range (k = 0; its rounding scales the whole matrix by 1 + 2^-24 at
-// most), a division by m in [1, 2) otherwise.
+// most), a division by m in [1, 2) otherwise.  An infinite d (only infinite values give
+// one) counts as NaN, so that the whole matrix becomes NaN, not only those values.
 struct Divisor {
   float m, r;
   int k;
   Divisor() = default;
   __device__ __forceinline__ explicit Divisor(double t) {
-    m = (float)t;
+    m = t < 1e300 ? (float)t : __uint_as_float(0x7FFFFFFFu);
     k = 0;
     if ((!(t < 1e30) || !(t > 1e-30)) && t > 0. && t < 1e300) {      // not zero, infinite or NaN
       const double f = frexp(t, &k);
@@ -72,7 +73,7 @@ struct Divisor {
       --k;
     }
     r = __frcp_rn(m);
-    if (k == 0 && !(r < 3e38f && r > 1e-37f)) k = kAlways;      // a zero, infinite or NaN divisor divides
+    if (k == 0 && !(r < 3e38f && r > 1e-37f)) k = kAlways;      // a zero or NaN divisor divides
   }
   static constexpr int kAlways = 1 << 20;
   __device__ __forceinline__ float divide(float x) const {

@@ -88,3 +88,18 @@ def test_coefficients_that_shrink(shape, dtype, steps, coefficients):
     Y = qg.mm_orthogonalize(X, steps, coefficients)
     fp32 = qg.mm_last_path() == qg.MM_PATH_TENSOR and coefficients[0] < 0.01 and any(coefficients)
     check(Y, to_np(X), [coefficients] * steps, form="matmul" if fp32 else None)
+
+
+# ------------------------------------------------------------------ infinities, outputs in place
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("shape", [(2, 520, 600), (2, 200, 330), (2, 40, 64)])
+@pytest.mark.parametrize("steps", [0, 1, 3])
+def test_an_infinity_makes_its_matrix_nan(shape, dtype, steps):
+    X = rand_tensor(shape, dtype, 23, DEV)
+    want = qg.mm_orthogonalize(X, steps)
+    X[1, 3, 5] = float("inf")
+    X[1, 7, 9] = float("-inf")
+    Y = qg.mm_orthogonalize(X, steps)
+    assert Y[1].isnan().all() and torch.equal(Y[0], want[0])
