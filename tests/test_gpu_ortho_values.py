@@ -90,7 +90,7 @@ def test_coefficients_that_shrink(shape, dtype, steps, coefficients):
     check(Y, to_np(X), [coefficients] * steps, form="matmul" if fp32 else None)
 
 
-# ------------------------------------------------------------------ infinities, outputs in place
+# ------------------------------------------------------------------ infinities
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
@@ -103,3 +103,53 @@ def test_an_infinity_makes_its_matrix_nan(shape, dtype, steps):
     X[1, 7, 9] = float("-inf")
     Y = qg.mm_orthogonalize(X, steps)
     assert Y[1].isnan().all() and torch.equal(Y[0], want[0])
+
+
+# ------------------------------------------------------------------ several steps
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("steps", [2, 5])
+@pytest.mark.parametrize("shape", [(513, 513), (520, 777), (1030, 523), (640, 900), (300, 520), (520, 264), (129, 1300), (61, 100), (100, 61),
+                                   (64, 64), (128, 256), (1000, 33)])
+def test_errors_are_those_of_the_stated_roundings(shape, steps, dtype):
+    """Row counts that end inside tiles of 128 and 256 rows, one launch and the chain of products, wide and tall."""
+    X = rand_tensor(shape, dtype, 25, DEV)
+    check(qg.mm_orthogonalize(X, steps, scale=1.5), to_np(X), [MUON] * steps, scale=1.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("shape", [(520, 777), (900, 513), (192, 320), (300, 140), (64, 200)])
+def test_strong_directions(shape, dtype):
+    """A state that lost its lower bits would show here first (4e-2 for one of 11 bits)."""
+    X = strong(shape, 4).to(dtype).to(DEV)
+    check(qg.mm_orthogonalize(X), to_np(X), [MUON] * 5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("shape", [(3, 640, 520), (2, 300, 264), (3, 2, 130, 200)])
+def test_stacks_of_unlike_matrices(shape, dtype):
+    """Random, strong and small matrices side by side: each is held to its own bound."""
+    X = rand_tensor(shape, F32, 27, "cpu").reshape((-1,) + shape[-2:])
+    X[0] = strong(shape[-2:], 5)
+    X[1] *= 2.0 ** -10
+    X = X.reshape(shape).to(dtype).to(DEV)
+    Y = qg.mm_orthogonalize(X, 3)
+    for x, y in zip(to_np(X).reshape((-1,) + shape[-2:]), Y.reshape((-1,) + shape[-2:])):
+        check(y, x, [MUON] * 3)
+
+
+STEEP = (8.287 / 1.01, -23.596 / 1.01 ** 3, 17.300 / 1.01 ** 5)
+THEN = (4.107 / 1.01, -2.948 / 1.01 ** 3, 0.545 / 1.01 ** 5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("shape", [(520, 777), (300, 520), (60, 200)])
+def test_coefficients_that_change_from_step_to_step(shape, dtype):
+    """A schedule that is steep just above 1; its bound leaves the f16 operands' range with five steps, not with two."""
+    for steps in (2, 5):
+        coefficients = [STEEP] + [THEN] * (steps - 1)
+        X = rand_tensor(shape, dtype, 26, DEV)
+        Y = qg.mm_orthogonalize(X, steps, coefficients)
+        fp32 = steps == 5 and qg.mm_last_path() == qg.MM_PATH_TENSOR
+        check(Y, to_np(X), coefficients, form="matmul" if fp32 else None)
