@@ -138,7 +138,7 @@ struct Row {
       if (vec && c0 + E <= G) {
         u[q] = __ldg(reinterpret_cast<const uint4*>(row + c0));
       } else {
-        T e[E];
+        __align__(16) T e[E];
 #pragma unroll
         for (int j = 0; j < E; ++j) e[j] = c0 + j < G ? row[(c0 + j) * cs] : from_f32<T>(fill);
         u[q] = *reinterpret_cast<const uint4*>(e);
@@ -226,7 +226,7 @@ struct Queue {
 #pragma unroll
       for (int q = 0; q < NP; ++q) {
         const int c0 = (q * LPR + lane) * Pairs<T>::kElems;
-        T e[Pairs<T>::kElems];
+        __align__(16) T e[Pairs<T>::kElems];
 #pragma unroll
         for (int j = 0; j < Pairs<T>::kElems; ++j) e[j] = from_f32<T>(fill);
         row.u[q] = c0 < G && r < rows ? ptx::lds128(at(slot, q)) : *reinterpret_cast<const uint4*>(e);

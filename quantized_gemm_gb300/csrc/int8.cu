@@ -348,7 +348,7 @@ mm_status run_few(const Int8Args& a, cudaStream_t stream) {
 template <typename O>
 __global__ void __launch_bounds__(256) int8_any_kernel(const Int8Args a) {
   pdl_begin();
-  __shared__ int8_t sA[32][36], sB[32][36];              // [row][k], [column][k]
+  __shared__ __align__(4) int8_t sA[32][36], sB[32][36];  // [row][k], [column][k]; read in words
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t m0 = (int64_t)blockIdx.y * 32, n0 = (int64_t)blockIdx.x * 32;
   const bool a_k = a.a_cs <= a.a_rs, b_k = a.b_ks <= a.b_ns;       // which way neighbours lie
