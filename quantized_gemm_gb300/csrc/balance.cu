@@ -126,23 +126,19 @@ template <> struct Pairs<__half> : Pairs16<__half2> {
   }
 };
 
-// A lane's NP pieces of a row.  `vec`: 16-byte reads; elements past G are `fill`.
+// A lane's NP pieces of a row, and their load element by element; past G they are `fill`.
 template <typename T, int LPR, int NP>
 struct Row {
   static constexpr int E = Pairs<T>::kElems;
   uint4 u[NP];
-  __device__ __forceinline__ void load(const T* row, int64_t cs, int lane, int G, bool vec, float fill) {
+  __device__ __forceinline__ void load(const T* row, int64_t cs, int lane, int G, float fill) {
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
       const int c0 = (q * LPR + lane) * E;
-      if (vec && c0 + E <= G) {
-        u[q] = __ldg(reinterpret_cast<const uint4*>(row + c0));
-      } else {
-        __align__(16) T e[E];
+      __align__(16) T e[E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) e[j] = c0 + j < G ? row[(c0 + j) * cs] : from_f32<T>(fill);
-        u[q] = *reinterpret_cast<const uint4*>(e);
-      }
+      for (int j = 0; j < E; ++j) e[j] = c0 + j < G ? row[(c0 + j) * cs] : from_f32<T>(fill);
+      u[q] = *reinterpret_cast<const uint4*>(e);
     }
   }
 };
@@ -232,7 +228,7 @@ struct Queue {
         row.u[q] = c0 < G && r < rows ? ptx::lds128(at(slot, q)) : *reinterpret_cast<const uint4*>(e);
       }
     } else {
-      row.load(base + (r < rows ? r : 0) * rs, cs, lane, G, false, fill);
+      row.load(base + (r < rows ? r : 0) * rs, cs, lane, G, fill);
     }
   }
 };

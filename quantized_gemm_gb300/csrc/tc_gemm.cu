@@ -2539,8 +2539,8 @@ mm_status launch_tc_int8(const Int8Args& q, const void* a, int64_t lda, const vo
 
 // ------------------------------------------------------------------ the orthogonalised update's products
 
-// [count][M][N] 16-bit values, rows ld and matrices `step` apart, in boxes of 32
-// rows and 64 columns, 128-byte swizzled.
+// [count][M][N], rows ld and matrices `step` apart, in boxes of 32 rows and 128 bytes
+// (64 or 32 columns), 128-byte swizzled.
 static bool plan_boxes(const void* ptr, int dtype, int64_t M, int64_t N, int64_t ld, int64_t step, int64_t count,
                          OperandPlan* out) {
   auto encode = encode_fn();
@@ -2563,26 +2563,17 @@ static bool plan_boxes(const void* ptr, int dtype, int64_t M, int64_t N, int64_t
 
 mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t stream) {
   if (!status) return MM_ERR_CUDA;
-  GemmArgs g;
-  memset(&g, 0, sizeof(g));
-  const bool f32_out = o.y_dtype == MM_F32;
-  g.dtype = f32_out ? MM_F16 : o.y_dtype;
-  g.M = o.M; g.N = o.N; g.K = o.K;
-  g.bm.nb = 1;
-  for (int d = 0; d < kMaxBatchDims; ++d) g.bm.shape[d] = 1;
-  g.bm.shape[0] = g.bm.count = o.count;
-  g.y.ptr = o.y; g.y.rs = o.y_rs; g.y.cs = 1; g.y.bstride[0] = o.y_step;
   TcParams p;
   init_params(&p);
-  p.M = g.M; p.N = g.N; p.K = g.K;
-  p.bm = g.bm;
+  p.M = o.M; p.N = o.N; p.K = o.K;
+  p.bm.nb = 1;
+  for (int d = 0; d < kMaxBatchDims; ++d) p.bm.shape[d] = 1;
+  p.bm.shape[0] = p.bm.count = o.count;
   p.out_f16 = o.y_dtype == MM_F16;
-  p.out_f32 = f32_out;
+  p.out_f32 = o.y_dtype == MM_F32;
   p.y = o.y;
   p.y_rs = o.y_rs;
   p.y_bstride[0] = o.y_step;
-  const int64_t vec = f32_out ? 4 : 8;
-  p.y_vec = (reinterpret_cast<uintptr_t>(o.y) & 15) == 0 && o.y_rs % vec == 0 && (o.y_step % vec == 0 || o.count == 1);
   p.alpha = o.alpha;
   p.beta = o.beta;
   p.c = o.c;                                   // (kSym, kSymF: whether there is one)
@@ -2592,27 +2583,27 @@ mm_status launch_tc_ortho(const OrthoProduct& o, unsigned* status, cudaStream_t 
   p.up = o.up;
   const bool pairs = o.split && !o.last;
   p.y_lo = pairs ? o.count : 0;
-  BatchMap om = g.bm;                          // the operands' maps span the rests too
+  BatchMap om = p.bm;                          // the operands' maps span the rests too
   OperandPlan cmap, ymap;
   if (o.split) {
     p.kb_per_seg = o.segment / BK;
     om.shape[0] = om.count = 2 * o.count;
     p.a_lo = p.b_lo = p.c_lo = o.count;
   }
-  p.y_tma = plan_boxes(o.y, o.y_dtype, g.M, g.N, o.y_rs, o.y_step, pairs ? 2 * o.count : o.count, &ymap);
+  p.y_tma = plan_boxes(o.y, o.y_dtype, o.M, o.N, o.y_rs, o.y_step, pairs ? 2 * o.count : o.count, &ymap);
   if (!o.last && !p.y_tma) return MM_ERR_UNSUPPORTED;
   // C, or the state.
   const bool have_c = o.s32 || o.c;
-  if (have_c && !(o.s32 ? plan_boxes(o.s32, MM_F32, g.M, g.N, o.s_rs, o.s_step, o.count, &cmap)
-                        : plan_boxes(o.c, MM_F16, g.M, g.N, o.c_rs, o.c_step, pairs ? 2 * o.count : o.count, &cmap)))
+  if (have_c && !(o.s32 ? plan_boxes(o.s32, MM_F32, o.M, o.N, o.s_rs, o.s_step, o.count, &cmap)
+                        : plan_boxes(o.c, MM_F16, o.M, o.N, o.c_rs, o.c_step, pairs ? 2 * o.count : o.count, &cmap)))
     return MM_ERR_UNSUPPORTED;
   const int64_t as[kMaxBatchDims] = {o.a_step}, bs[kMaxBatchDims] = {o.b_step};
   // Pairs of CTAs read a third less per tile (a split k-block is 48 KB a CTA against 64).
-  const bool pair = g.M > BM;
+  const bool pair = o.M > BM;
   OperandPlan a, b;
   const int cols = o.split ? BN / 2 : BN;
-  if (!plan_operand(o.a, MM_F16, g.M, g.K, o.a_rs, o.a_cs, om, as, BM, &a) ||
-      !plan_operand(o.b, MM_F16, g.N, g.K, o.b_cs, o.b_rs, om, bs, cols / (pair ? 2 : 1), &b))
+  if (!plan_operand(o.a, MM_F16, o.M, o.K, o.a_rs, o.a_cs, om, as, BM, &a) ||
+      !plan_operand(o.b, MM_F16, o.N, o.K, o.b_cs, o.b_rs, om, bs, cols / (pair ? 2 : 1), &b))
     return MM_ERR_UNSUPPORTED;
   p.idesc = make_idesc_mn(1, a.mn_major, b.mn_major, pair ? 2 * BM : BM, cols);
   // C's map takes the place of the tail map: these products have no tail tiles.

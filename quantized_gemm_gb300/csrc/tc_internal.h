@@ -28,7 +28,7 @@ constexpr int kTileK = 64;    // one 128-byte swizzle row of 16-bit elements
 // kInt8: a dense product of f16 copies of int8 operands whose epilogue
 // multiplies by a scale per row and per column and adds a bias.
 // kSym: a dense f16 product whose result is symmetric (M = N): only the tiles
-// that touch the lower triangle are computed, and their 32 x 32 boxes are also
+// that touch the lower triangle are computed, and their 32 x 64 boxes are also
 // stored transposed where the tile on the other side was left out.
 // kState: a dense f16 product plus beta times a state in fp32; the sum takes the
 // state's place and goes out as f16, or goes out rounded to T (p.last).
