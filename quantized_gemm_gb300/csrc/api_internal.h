@@ -6,6 +6,12 @@
 
 namespace qg {
 
+inline bool is_float16_32(int dt) { return dt == MM_BF16 || dt == MM_F16 || dt == MM_F32; }
+inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+inline bool workspace_ok(const void* ws, size_t have, size_t need) {
+  return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & 255) == 0);
+}
+
 // Device-side status word of the current device (NULL on failure).
 unsigned* device_status_ptr();
 

@@ -12,12 +12,7 @@ using namespace qg;
 
 namespace {
 
-bool is_float16_32(int dt) { return dt == MM_BF16 || dt == MM_F16 || dt == MM_F32; }
 bool is_vector(const mm_tensor* t, int64_t n) { return t->ndim == 1 && t->shape[0] == n; }
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-bool workspace_ok(const void* ws, size_t have, size_t need) {
-  return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & 255) == 0);
-}
 
 }  // namespace
 

@@ -13,7 +13,6 @@ using namespace qg;
 
 namespace {
 
-bool is_float16_32(int dt) { return dt == MM_BF16 || dt == MM_F16 || dt == MM_F32; }
 bool is_index(int dt) { return dt == MM_I32 || dt == MM_I64; }
 
 bool has_shape(const mm_tensor* t, std::initializer_list<int64_t> shape) {
@@ -24,11 +23,6 @@ bool has_shape(const mm_tensor* t, std::initializer_list<int64_t> shape) {
   return true;
 }
 
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-
-bool workspace_ok(const void* ws, size_t have, size_t need) {
-  return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & 255) == 0);
-}
 
 }  // namespace
 

@@ -431,17 +431,6 @@ __device__ __forceinline__ uint4 bytes16(const int8_t* p) {
                     __funnelshift_r(w3, w4, sh));
 }
 
-// The bytes of w (two at a time) as f16 pairs: 1024 + (byte ^ 0x80) by placing the
-// byte in the mantissa of 1024, minus 1024 + 128.
-__device__ __forceinline__ void half4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const __half2 c = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));    // 1152
-  const uint32_t l = __byte_perm(u, 0x64u, 0x4140u), h = __byte_perm(u, 0x64u, 0x4342u);
-  const __half2 dl = __hsub2(*reinterpret_cast<const __half2*>(&l), c), dh = __hsub2(*reinterpret_cast<const __half2*>(&h), c);
-  lo = *reinterpret_cast<const uint32_t*>(&dl);
-  hi = *reinterpret_cast<const uint32_t*>(&dh);
-}
-
 // A copy in bytes of a source whose rows are neighbours (rs = 1): 4 x 4 bytes a step.
 constexpr int kTile = 128;
 __device__ void turn_bytes(const Int8Copy& c, int64_t block) {
@@ -469,13 +458,10 @@ __device__ void turn_bytes(const Int8Copy& c, int64_t block) {
         }
       }
     }
-    const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
-    const uint32_t d = __byte_perm(w[0], w[1], 0x7362), e = __byte_perm(w[2], w[3], 0x7362);
-    const int at = kq ^ (g >> 3);
-    tile[4 * g][at] = __byte_perm(a, b, 0x5410);
-    tile[4 * g + 1][at] = __byte_perm(a, b, 0x7632);
-    tile[4 * g + 2][at] = __byte_perm(d, e, 0x5410);
-    tile[4 * g + 3][at] = __byte_perm(d, e, 0x7632);
+    uint32_t t[4];
+    turn4(w, t);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tile[4 * g + j][kq ^ (g >> 3)] = t[j];
   }
   __syncthreads();
 #pragma unroll
@@ -514,10 +500,10 @@ __global__ void __launch_bounds__(256) int8_copy_kernel(const Int8Copy A, const 
     return;
   }
   uint4 o[2];
-  half4(u.x, o[0].x, o[0].y);
-  half4(u.y, o[0].z, o[0].w);
-  half4(u.z, o[1].x, o[1].y);
-  half4(u.w, o[1].z, o[1].w);
+  halves(u.x, o[0].x, o[0].y);
+  halves(u.y, o[0].z, o[0].w);
+  halves(u.z, o[1].x, o[1].y);
+  halves(u.w, o[1].z, o[1].w);
   uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(c.dst) + r * c.ld + c0);
   dst[0] = o[0];
   if (c0 + 8 < c.ld) dst[1] = o[1];

@@ -161,10 +161,8 @@ __global__ void __launch_bounds__(kThreads, 4) int8_few_turned_kernel(const Int8
 #pragma unroll
       for (int u = 0; u < kFlight; ++u) {
         if (g0 + u * kWarps >= groups) break;
-        const uint32_t p = __byte_perm(w[u][0], w[u][1], 0x5140), q = __byte_perm(w[u][2], w[u][3], 0x5140);
-        const uint32_t s = __byte_perm(w[u][0], w[u][1], 0x7362), t = __byte_perm(w[u][2], w[u][3], 0x7362);
-        const uint32_t y[4] = {__byte_perm(p, q, 0x5410), __byte_perm(p, q, 0x7632), __byte_perm(s, t, 0x5410),
-                               __byte_perm(s, t, 0x7632)};
+        uint32_t y[4];
+        turn4(w[u], y);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
           const int x = sA[m][g0 + u * kWarps];

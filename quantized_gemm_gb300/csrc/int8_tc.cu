@@ -28,6 +28,7 @@
 #include <atomic>
 #include <cstring>
 
+#include "int8.cuh"
 #include "tc.h"
 #include "tc_internal.h"
 #include "tc_ptx.cuh"
@@ -94,17 +95,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Four int8 values as two f16 pairs, exactly.
-__device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const uint32_t l = __byte_perm(u, 0x64u, 0x4140u), h = __byte_perm(u, 0x64u, 0x4342u);
-  const uint32_t c = 0x64806480u;                // 1152 twice
-  const __half2 dl = __hsub2(*reinterpret_cast<const __half2*>(&l), *reinterpret_cast<const __half2*>(&c));
-  const __half2 dh = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&c));
-  lo = *reinterpret_cast<const uint32_t*>(&dl);
-  hi = *reinterpret_cast<const uint32_t*>(&dh);
-}
-
 template <typename O>
 __device__ __forceinline__ uint32_t pair_bits(O a, O b) {
   uint16_t x, y;
@@ -112,11 +102,6 @@ __device__ __forceinline__ uint32_t pair_bits(O a, O b) {
   memcpy(&y, &b, 2);
   return (uint32_t)x | (uint32_t)y << 16;
 }
-template <typename O>
-__device__ __forceinline__ float bias_of(const Int8Args& q, int64_t n) {
-  return q.bias ? to_f32(static_cast<const O*>(q.bias)[n * q.bias_s]) : 0.f;
-}
-
 template <typename O, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -229,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = lane; j < kRows; j += 32) {
       const bool in = j < p.rows && n0 + j < p.q.N;
       param[j] = in ? __ldg(p.q.sb + (n0 + j) * p.q.sb_s) : 0.f;
-      param[kRows + j] = in ? bias_of<O>(p.q, n0 + j) : 0.f;
+      param[kRows + j] = in ? bias_at<O>(p.q, n0 + j) : 0.f;
     }
     for (int j = lane; j < NT; j += 32) param[2 * kRows + j] = m0 + j < p.q.M ? __ldg(p.q.sa + (m0 + j) * p.q.sa_s) : 0.f;
   } else if (warp >= kConvWarp0) {
@@ -305,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       O o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = from_f32<O>(__fadd_rn(__fmul_rn(__fmul_rn(v[j], sa), sb[j]), bias[j]));
+      for (int j = 0; j < 4; ++j) o[j] = finish8<O>(v[j], sa, sb[j], bias[j]);
       O* y = static_cast<O*>(p.q.y) + m * p.q.N + nl;
       if (lane * 4 >= p.rows) continue;                // rows is a multiple of 4
       if (p.y_vec && nl + 4 <= p.q.N) {
@@ -328,14 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The weights [N, K] int8 as [rows channels x 128 k] tiles, 128-byte swizzled.
 bool weight_map(const Int8Args& q, int rows, CUtensorMap* map) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      ptr = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }();
+  const auto encode = encode_fn();
   if (!encode) return false;
   const int64_t pitch = q.N == 1 ? (q.K + 15) / 16 * 16 : q.b_ns;
   const cuuint64_t dims[3] = {(cuuint64_t)q.K, (cuuint64_t)q.N, 1};

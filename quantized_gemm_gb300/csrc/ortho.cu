@@ -179,8 +179,6 @@ __global__ void __launch_bounds__(kThreads) round_kernel(const float* s, int64_t
 }
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-
 // Shares per matrix: four blocks per SM over all matrices, at least 4096 elements each.
 int norm_chunks(int64_t M, int64_t N, int64_t count) {
   const int64_t want = (4 * (int64_t)sm_count_public() + count - 1) / count;

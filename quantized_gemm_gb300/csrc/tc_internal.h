@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "common.cuh"
 
@@ -111,6 +112,9 @@ struct TcParams {
   unsigned long long timeout_ns;    // limit of each pipeline wait
   unsigned long long teardown_ns;   // limit of the waits that let in-flight copies and MMAs land
 };
+
+// The driver's tensor-map encoder, looked up once (NULL: none).
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 struct OperandPlan {
   CUtensorMap map;
