@@ -156,9 +156,12 @@ __global__ void __launch_bounds__(kThreads) divide_kernel(const NormArgs a) {
         }
       }
     }
-    if constexpr (E >= 4) {
-#pragma unroll
-      for (int j = 0; j < E; j += 4) *reinterpret_cast<float4*>(a.s + at + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    if constexpr (E == 8) {                               // 32 bytes a lane: whole sectors
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a.s + at), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                   "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                   : "memory");
+    } else if constexpr (E == 4) {
+      *reinterpret_cast<float4*>(a.s + at) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
       for (int j = 0; j < E; ++j) a.s[at + j] = v[j];
