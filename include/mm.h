@@ -41,7 +41,10 @@
  *   mixture-of-experts layer, the low-rank adapters, the 8-bit product and the
  *   orthogonalised update) take a
  *   caller-provided workspace whose size is given by the matching
- *   *_workspace_size function; the workspace must be 256-byte aligned.
+ *   *_workspace_size function; the workspace must be 256-byte aligned.  The
+ *   size goes by the kernels that the call takes, and so by the tensors' strides
+ *   and the alignment of their addresses, by the current device and by the path
+ *   policy: ask with the tensors of the call.
  * Threads.  Entry points may be called from several host threads; calls that
  *   share a workspace must be ordered on one stream.
  */
@@ -98,7 +101,8 @@ typedef enum mm_path {
   MM_PATH_VECTOR = 4   /* MatMul/Gemm with 1 to 4 rows of A' (bf16/f16/f32) and B' either K-major (k
                           contiguous in A' and B', 16-byte aligned rows of A' and columns of B') or
                           MN-major (n contiguous, 16-byte aligned rows of B'): one pass over B' on the
-                          CUDA cores */
+                          CUDA cores; mm_int8_matmul with up to 8 rows of A (4 where rows and columns
+                          are not 16-byte aligned along k) */
 } mm_path;
 
 /* Human-readable name of a status code; never NULL. */

@@ -18,8 +18,8 @@
 // rows to come into its own places in shared memory (cp.async, kAhead rows).  65536
 // rows of 256 bf16 logits, forward and backward (101 MB, 15 us of memory): 95 us with
 // a row over all 32 lanes and a branch per logit (276 instructions a row), 43 with
-// two rows loaded into registers at a time, 37 so; what is left is the arithmetic
-// (107 instructions a row forward) and three launches.  Column sums leave a block
+// two rows loaded into registers at a time, 37 so; what is left is latency (issue slots
+// are half busy, with 107 instructions a row forward) and the second launch.  Column sums leave a block
 // through shared memory, one partial per block, and a second launch, one cluster,
 // adds the partials in a fixed order; picks are integers, counted with shared-memory
 // atomics, whose order does not matter.

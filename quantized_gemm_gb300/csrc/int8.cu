@@ -417,8 +417,10 @@ mm_status run_any(const Int8Args& a, cudaStream_t stream) {
 // 8, zeros past `cols`), of a copy in bytes a multiple of 16; 16 values a thread.
 // Bound: memory, 1 byte read and 2 or 1 written per value.  Sources of any
 // alignment are read in aligned words (each holds a byte that is wanted) and
-// shifted; one whose rows are neighbours (rs = 1) is turned in tiles of 128 x 128
-// through shared memory.  (Byte by byte, 4096 x 14336 took 160 us.)
+// shifted; a copy in bytes of one whose rows are neighbours (rs = 1) is turned in tiles
+// of 128 x 128 through shared memory.  (Byte by byte, 4096 x 14336 took 160 us.)  The f16
+// copy of such rows, tokens given as a transpose, is gathered byte by byte: 1024 x 4096
+// 16 us more than rows, 16384 x 4096 390.
 
 // 16 bytes at any address.
 __device__ __forceinline__ uint4 bytes16(const int8_t* p) {

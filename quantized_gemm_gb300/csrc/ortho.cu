@@ -412,11 +412,14 @@ bool split_operands(const OrthoArgs& o) { return o.dtype != MM_BF16 || o.M <= kH
 
 // Products whose sum the tensor cores keep before it is added up in fp32.  Their
 // truncation shrinks every step by some 2^-25 an addition, which shows where a fp32
-// result is hardly blurred by small singular values: longer matrices, below 1024.
+// result is hardly blurred by small singular values: longer matrices.  From 1024 rows on
+// fp32 sums are off by so much themselves that 256 is enough.
 // Error relative to fp32 sums' at 256, 128 and 64: 600 x 1000 1.9 and 1.1, 333 x 777 2.3
-// and 1.35, 1800 x 220 3.0, 1.8 and 1.2; 300 x 420 1.85, 512 x 512 0.9, 2048 x 2048 0.6
-// at 256.  A segment costs a hand-over: 8 of 512 x 1000 277 us at 256 and 297 at 128,
-// 2048 x 2048 490 and 610.
+// and 1.35, 1800 x 220 3.0, 1.8 and 1.2; 300 x 420 1.85, 512 x 512 0.9 at 256.  A segment
+// costs a hand-over: 8 of 512 x 1000 277 us at 256 and 297 at 128.  From 1024 on, at 256
+// and at what the rule below 1024 would take, with us: 1024 x 4096 1.14 435, 0.58 535;
+// 1024 x 8192 1.54 747, 0.49 1340; 1100 x 8000 0.81 842, 0.27 1490; 2048 x 6144 0.52 1139,
+// 0.30 1445; 9000 x 1500 0.48 1146, 0.21 2020; 2048 x 2048 0.58 511.
 int segment_of(const OrthoArgs& o) {
   const int64_t m = o.M < o.N ? o.M : o.N, n = o.M < o.N ? o.N : o.M;
   if (o.dtype != MM_F32 || m >= 1024 || 5 * n < 6 * m) return 256;
